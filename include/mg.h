@@ -313,6 +313,89 @@ mg_status mg_ffma_peak(double* tflops, double* flop_per_clk_per_sm, mg_stream_t 
 mg_status mg_softmax_ce_noalloc(int dtype, const void* logits, int rows, int cols, int label_kind,
                                 const void* labels, void* dlogits, float* loss, mg_stream_t stream);
 
+/* ---- language-model operators ---------------------------------------------
+ * Calls that need no plan, for the ends of a language model's training step
+ * and for serving; the layers `embedding` and `grouped linear` and
+ * mg_set_grad_clip use the same kernels inside a plan.
+ *
+ * Conventions: dtype 0 = fp32, 1 = bf16.  Matrices are dense and row-major.
+ * Pointers are caller-owned device memory of the current device, 16-byte
+ * aligned (ids, offsets and gradient lists: to their element); a pointer of another
+ * device or of pageable host memory is refused.  Everything is asynchronous on
+ * `stream`, allocates nothing (mg_grad_list_create excepted), reads no value
+ * back to the host, and can be captured into a CUDA graph.  A workspace is
+ * scratch of one call at a time: calls that may overlap on the GPU (other
+ * streams, other captured graphs) need one each.  Messages: mg_last_error(NULL).
+ *
+ * Embedding: out[i, :] = scale * table[ids[i], :], rounded once to out's type.
+ * id_kind 0 = int32, 1 = int64.  An id outside [0, vocab) -- padding -- reads
+ * nothing: its row of out is 0.  table [vocab, dim], ids [n], out [n, dim];
+ * n = 0 is allowed.
+ *
+ * Its gradient: dtable[v, :] = scale * sum over i with ids[i] == v of
+ * dout[i, :], fp32 sums in ascending i order (long runs in a fixed order of
+ * fixed windows), the same bits in every run.  All of dtable [vocab, dim]
+ * fp32 is written, zeros for ids that do not occur; ids outside [0, vocab)
+ * give nothing.  workspace: mg_embedding_workspace_bytes (0 for arguments the
+ * call would refuse); its contents before the call do not matter. */
+size_t mg_embedding_workspace_bytes(long long n, int vocab, int dim);
+mg_status mg_embedding_forward(int table_dtype, const void* table, int vocab, int dim, int id_kind,
+                               const void* ids, long long n, float scale, int out_dtype, void* out,
+                               mg_stream_t stream);
+mg_status mg_embedding_backward(int dtype, const void* dout, int vocab, int dim, int id_kind,
+                                const void* ids, long long n, float scale, float* dtable,
+                                void* workspace, size_t workspace_bytes, mg_stream_t stream);
+
+/* Matrix products grouped by expert.  The rows of x [rows, d_in] are ordered
+ * by group: group e has the rows offsets[e] .. offsets[e+1]-1, offsets
+ * [groups + 1] int32 in device memory, nondecreasing within [0, rows] (values
+ * that are not are clamped to that and never lead out of range).  Groups may
+ * be empty and of any size.  w [groups, d_in, d_out].
+ *   forward          y[r]  = x[r] w[e(r)]            [rows, d_out]
+ *   backward_input   dx[r] = dy[r] w[e(r)]^T         [rows, d_in]
+ *   backward_weight  dw[e] = x_e^T dy_e              [groups, d_in, d_out], fp32
+ * dtype is the type of x, w, y, dx, dy; sums are fp32.  Rows outside
+ * [offsets[0], offsets[groups]) are neither read nor written; dw of an empty
+ * group is 0.  groups at most 1024.  bf16 widths that are multiples of 8 run
+ * on the tensor cores, others and fp32 on the CUDA cores.
+ * workspace: mg_grouped_linear_workspace_bytes; zero it once before its first
+ * use (the calls leave its counters zero).  Its first int is set to 1 if a
+ * bounded device-side wait gave up, in which case that call's results are
+ * invalid. */
+size_t mg_grouped_linear_workspace_bytes(int rows, int groups, int d_in, int d_out);
+mg_status mg_grouped_linear_forward(int dtype, const void* x, const int* offsets, int rows, int groups,
+                                    int d_in, int d_out, const void* w, void* y, void* workspace,
+                                    size_t workspace_bytes, mg_stream_t stream);
+mg_status mg_grouped_linear_backward_input(int dtype, const void* dy, const int* offsets, int rows,
+                                           int groups, int d_in, int d_out, const void* w, void* dx,
+                                           void* workspace, size_t workspace_bytes,
+                                           mg_stream_t stream);
+mg_status mg_grouped_linear_backward_weight(int dtype, const void* x, const void* dy,
+                                            const int* offsets, int rows, int groups, int d_in,
+                                            int d_out, float* dw, void* workspace,
+                                            size_t workspace_bytes, mg_stream_t stream);
+
+/* Global gradient norm and clipping over many tensors.  A list holds n device
+ * tensors (counts[i] elements of dtypes[i] at grads[i]) and where their scaled
+ * values go: out[i], or in place where out is NULL or out[i] == grads[i].
+ * Memory that is written may not overlap any other tensor of the list
+ * (MG_ERR_INVALID_ARG).  counts[i] = 0 is allowed.  Creation copies the table
+ * to the device and allocates a few bytes per 16384 elements; the list is
+ * bound to the current device, and like a plan is used by one stream at a
+ * time.
+ * mg_grad_list_clip: stats[0] = norm = sqrt(sum of all squares), stats[1] =
+ * c = max_norm / norm if norm > max_norm, else 1 (fp32, device memory, 8-byte
+ * aligned), and out = c * grads.  With c = 1 an in-place list is left as it
+ * is.  A gradient that holds NaN or infinity gives such a norm and c = 1: the
+ * gradients keep their bits for the caller to find.  (Finite gradients whose
+ * norm is beyond fp32's range have stats[0] = infinity and are clipped.)
+ * max_norm >= 0; INFINITY only measures. */
+typedef struct mg_grad_list mg_grad_list;
+mg_status mg_grad_list_create(int n, const void* const* grads, void* const* out,
+                              const size_t* counts, const int* dtypes, mg_grad_list** list);
+void mg_grad_list_destroy(mg_grad_list* list);
+mg_status mg_grad_list_clip(mg_grad_list* list, float max_norm, float* stats, mg_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

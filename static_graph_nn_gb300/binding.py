@@ -76,6 +76,25 @@ _SIGS = {
                                         ctypes.POINTER(ctypes.c_double),
                                         ctypes.POINTER(ctypes.c_double),
                                         ctypes.POINTER(ctypes.c_double)]),
+    "mg_embedding_workspace_bytes": (ctypes.c_size_t, [ctypes.c_longlong, ctypes.c_int, ctypes.c_int]),
+    "mg_embedding_forward": (ctypes.c_int, [ctypes.c_int, _P, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                            _P, ctypes.c_longlong, ctypes.c_float, ctypes.c_int, _P,
+                                            _P]),
+    "mg_embedding_backward": (ctypes.c_int, [ctypes.c_int, _P, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                             _P, ctypes.c_longlong, ctypes.c_float, _P, _P,
+                                             ctypes.c_size_t, _P]),
+    "mg_grouped_linear_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int] * 4),
+    "mg_grouped_linear_forward": (ctypes.c_int, [ctypes.c_int, _P, _P] + [ctypes.c_int] * 4
+                                  + [_P, _P, _P, ctypes.c_size_t, _P]),
+    "mg_grouped_linear_backward_input": (ctypes.c_int, [ctypes.c_int, _P, _P] + [ctypes.c_int] * 4
+                                         + [_P, _P, _P, ctypes.c_size_t, _P]),
+    "mg_grouped_linear_backward_weight": (ctypes.c_int, [ctypes.c_int, _P, _P, _P] + [ctypes.c_int] * 4
+                                          + [_P, _P, ctypes.c_size_t, _P]),
+    "mg_grad_list_create": (ctypes.c_int, [ctypes.c_int, ctypes.POINTER(_P), ctypes.POINTER(_P),
+                                           ctypes.POINTER(ctypes.c_size_t),
+                                           ctypes.POINTER(ctypes.c_int), ctypes.POINTER(_P)]),
+    "mg_grad_list_destroy": (None, [_P]),
+    "mg_grad_list_clip": (ctypes.c_int, [_P, ctypes.c_float, _P, _P]),
 }
 
 _lib = None
@@ -279,3 +298,191 @@ def ffma_peak(stream=None) -> tuple[float, float]:
     if st != MG_OK:
         raise MGError(st, lib.mg_last_error(None).decode())
     return t.value, c.value
+
+
+# ---- language-model operators (no plan) ---------------------------------------
+# Tensors are dense torch tensors on the current device; shapes and types are
+# checked here and refused with an MGError before the library is called.
+
+_DTYPES = {"torch.float32": 0, "torch.bfloat16": 1}
+_ID_KINDS = {"torch.int32": 0, "torch.int64": 1}
+
+
+def _refuse(msg: str, status: int = MG_ERR_INVALID_ARG):
+    raise MGError(status, msg)
+
+
+def _code(t, name: str, table: dict = _DTYPES) -> int:
+    k = table.get(str(t.dtype))
+    if k is None:
+        _refuse(f"{name} must be one of {', '.join(sorted(table))}, not {t.dtype}")
+    return k
+
+
+def _dense(t, name: str, shape: tuple | None = None):
+    if not t.is_contiguous():
+        _refuse(f"{name} must be contiguous (strides {tuple(t.stride())})")
+    if not t.is_cuda:
+        _refuse(f"{name} must be a CUDA tensor")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        _refuse(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}", MG_ERR_SHAPE)
+
+
+def _status(st: int):
+    if st != MG_OK:
+        raise MGError(st, load().mg_last_error(None).decode())
+
+
+def embedding_workspace_bytes(n: int, vocab: int, dim: int) -> int:
+    """Bytes of workspace that embedding_backward needs for n ids."""
+    return load().mg_embedding_workspace_bytes(n, vocab, dim)
+
+
+def embedding_forward(table, ids, out, scale: float = 1.0, stream=None):
+    """out[i] = scale * table[ids[i]]; zeros for an id outside [0, vocab).
+
+    table [vocab, dim] and out [*ids.shape, dim] fp32 or bf16 (each its own
+    type), ids int32 or int64 of any shape."""
+    if table.dim() != 2:
+        _refuse("table must be [vocab, dim]", MG_ERR_SHAPE)
+    v, d = table.shape
+    _dense(table, "table")
+    _dense(ids, "ids")
+    _dense(out, "out", tuple(ids.shape) + (d,))
+    _status(load().mg_embedding_forward(_code(table, "table"), _ptr(table), v, d,
+                                        _code(ids, "ids", _ID_KINDS), _ptr(ids), ids.numel(), scale,
+                                        _code(out, "out"), _ptr(out), _stream(stream)))
+
+
+def embedding_backward(dout, ids, dtable, workspace, scale: float = 1.0, stream=None):
+    """dtable[v] = scale * sum of dout[i] over ids[i] == v; every row of dtable is
+    written.  dout [*ids.shape, dim] fp32 or bf16, dtable [vocab, dim] fp32,
+    workspace a byte tensor of embedding_workspace_bytes."""
+    if dtable.dim() != 2 or str(dtable.dtype) != "torch.float32":
+        _refuse("dtable must be [vocab, dim] float32", MG_ERR_SHAPE)
+    v, d = dtable.shape
+    _dense(dtable, "dtable")
+    _dense(ids, "ids")
+    _dense(dout, "dout", tuple(ids.shape) + (d,))
+    _dense(workspace, "workspace")
+    _status(load().mg_embedding_backward(_code(dout, "dout"), _ptr(dout), v, d,
+                                         _code(ids, "ids", _ID_KINDS), _ptr(ids), ids.numel(), scale,
+                                         _ptr(dtable), _ptr(workspace),
+                                         workspace.numel() * workspace.element_size(),
+                                         _stream(stream)))
+
+
+def grouped_linear_workspace_bytes(rows: int, groups: int, d_in: int, d_out: int) -> int:
+    """Bytes of workspace for the grouped products of these sizes (zero it once)."""
+    return load().mg_grouped_linear_workspace_bytes(rows, groups, d_in, d_out)
+
+
+def _grouped_args(rows_t, name, offsets, groups, workspace):
+    if rows_t.dim() != 2:
+        _refuse(f"{name} must be two-dimensional", MG_ERR_SHAPE)
+    _dense(rows_t, name)
+    if str(offsets.dtype) != "torch.int32":
+        _refuse("offsets must be int32")
+    _dense(offsets, "offsets", (groups + 1,))
+    _dense(workspace, "workspace")
+    return workspace.numel() * workspace.element_size()
+
+
+def _same_type(a, an, b, bn):
+    if a.dtype != b.dtype:
+        _refuse(f"{an} and {bn} must have one type, not {a.dtype} and {b.dtype}")
+
+
+def grouped_linear_forward(x, offsets, w, y, workspace, stream=None):
+    """y[r] = x[r] @ w[e] for the rows offsets[e] <= r < offsets[e + 1] of each
+    group e; other rows of y are left as they were.  x [rows, d_in], w [groups,
+    d_in, d_out], y [rows, d_out], all fp32 or all bf16; offsets int32 on the
+    device."""
+    if w.dim() != 3:
+        _refuse("w must be [groups, d_in, d_out]", MG_ERR_SHAPE)
+    e, k, n = w.shape
+    nb = _grouped_args(x, "x", offsets, e, workspace)
+    _dense(x, "x", (x.shape[0], k))
+    _dense(w, "w")
+    _dense(y, "y", (x.shape[0], n))
+    _same_type(x, "x", w, "w")
+    _same_type(x, "x", y, "y")
+    _status(load().mg_grouped_linear_forward(_code(x, "x"), _ptr(x), _ptr(offsets), x.shape[0], e, k, n,
+                                             _ptr(w), _ptr(y), _ptr(workspace), nb, _stream(stream)))
+
+
+def grouped_linear_backward_input(dy, offsets, w, dx, workspace, stream=None):
+    """dx[r] = dy[r] @ w[e].T; shapes and types as grouped_linear_forward's."""
+    if w.dim() != 3:
+        _refuse("w must be [groups, d_in, d_out]", MG_ERR_SHAPE)
+    e, k, n = w.shape
+    nb = _grouped_args(dy, "dy", offsets, e, workspace)
+    _dense(dy, "dy", (dy.shape[0], n))
+    _dense(w, "w")
+    _dense(dx, "dx", (dy.shape[0], k))
+    _same_type(dy, "dy", w, "w")
+    _same_type(dy, "dy", dx, "dx")
+    _status(load().mg_grouped_linear_backward_input(_code(dy, "dy"), _ptr(dy), _ptr(offsets),
+                                                    dy.shape[0], e, k, n, _ptr(w), _ptr(dx),
+                                                    _ptr(workspace), nb, _stream(stream)))
+
+
+def grouped_linear_backward_weight(x, dy, offsets, dw, workspace, stream=None):
+    """dw[e] = x_e.T @ dy_e (fp32; zeros for a group without rows)."""
+    if dw.dim() != 3 or str(dw.dtype) != "torch.float32":
+        _refuse("dw must be [groups, d_in, d_out] float32", MG_ERR_SHAPE)
+    e, k, n = dw.shape
+    nb = _grouped_args(x, "x", offsets, e, workspace)
+    _dense(x, "x", (x.shape[0], k))
+    _dense(dy, "dy", (x.shape[0], n))
+    _dense(dw, "dw")
+    _same_type(x, "x", dy, "dy")
+    _status(load().mg_grouped_linear_backward_weight(_code(x, "x"), _ptr(x), _ptr(dy), _ptr(offsets),
+                                                     x.shape[0], e, k, n, _ptr(dw), _ptr(workspace), nb,
+                                                     _stream(stream)))
+
+
+class GradList:
+    """Gradient tensors (fp32 or bf16, contiguous) whose global norm is taken and
+    that are scaled by it together, in place or into ``out``.  Keeps the tensors
+    alive; the table lives on the device until close()."""
+
+    def __init__(self, grads, out=None):
+        self.h = None
+        self.lib = load()
+        grads = list(grads)
+        out = None if out is None else list(out)
+        if out is not None and len(out) != len(grads):
+            _refuse(f"{len(grads)} gradients but {len(out)} outputs")
+        for i, g in enumerate(grads):
+            _dense(g, f"gradient {i}")
+            if out is not None:
+                _dense(out[i], f"output {i}", tuple(g.shape))
+                _same_type(g, f"gradient {i}", out[i], f"output {i}")
+        n = len(grads)
+        pg = (_P * max(1, n))(*[_ptr(g) for g in grads])
+        po = (_P * max(1, n))(*[_ptr(o) for o in out]) if out is not None else None
+        counts = (ctypes.c_size_t * max(1, n))(*[g.numel() for g in grads])
+        types = (ctypes.c_int * max(1, n))(*[_code(g, f"gradient {i}") for i, g in enumerate(grads)])
+        h = _P()
+        _status(self.lib.mg_grad_list_create(n, pg, po, counts, types, ctypes.byref(h)))
+        self.h, self.tensors = h, (grads, out)
+
+    def clip(self, max_norm: float, stats, stream=None):
+        """stats[0] = the norm, stats[1] = the factor (fp32 [2] on the device);
+        the gradients times the factor to their outputs."""
+        if str(stats.dtype) != "torch.float32":
+            _refuse("stats must be float32")
+        _dense(stats, "stats", (2,))
+        _status(self.lib.mg_grad_list_clip(self.h, max_norm, _ptr(stats), _stream(stream)))
+
+    def close(self):
+        if getattr(self, "h", None):
+            self.lib.mg_grad_list_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass

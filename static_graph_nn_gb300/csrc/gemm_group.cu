@@ -1,0 +1,234 @@
+// Matrix products grouped by expert (ragged row ranges), CUDA-core version and
+// the entry points.
+//
+//   forward  y_e  = x_e  W_e        x [rows, d_in], W [E, d_in, d_out]
+//   dX       dx_e = dy_e W_e^T
+//   dW       dW_e = x_e^T dy_e      fp32, 0 for a group without rows
+//
+// The group boundaries are device data: every block reads them into shared
+// memory and walks the same list of output tiles, so the host neither waits
+// for the router nor launches one product per expert.
+//
+// This file's kernel runs fp32 (FFMA only) and bf16 widths that TMA cannot
+// address (rows that are not multiples of 16 bytes).
+#include <cstdio>
+
+#include "../../include/mg.h"
+#include "common.cuh"
+#include "group_table.cuh"
+#include "kernels.h"
+#include "op_checks.h"
+
+namespace mg {
+namespace {
+
+constexpr int S_T = 64;    // output tile
+constexpr int S_K = 16;
+
+// One 64x64 output tile per step, 256 threads with 4x4 outputs each.
+template <typename T, int KIND>
+__global__ void __launch_bounds__(256) group_simt_kernel(const GroupArgs g) {
+  extern __shared__ int s_tab[];
+  __shared__ float As[S_K][S_T + 4], Bs[S_K][S_T + 4];
+  GroupTable t;
+  t.n = g.groups + (g.zero_rest ? 2 : 0);
+  t.lo = s_tab;
+  t.hi = s_tab + g.groups + 2;
+  t.cum = s_tab + 2 * (g.groups + 2);
+  if (threadIdx.x < 32) load_group_table(t, g.offsets, g.groups, g.rows, S_T);
+  __syncthreads();
+  const int K0 = KIND == GROUP_DX ? g.d_out : g.d_in;    // width of A's rows (FWD, DX)
+  const int N = KIND == GROUP_DX ? g.d_in : g.d_out;
+  const int tiles_n = (N + S_T - 1) / S_T;
+  const int tiles_k = (g.d_in + S_T - 1) / S_T;          // DW: row tiles of each dW[e]
+  const long long items = KIND == GROUP_DW ? (long long)g.groups * tiles_k * tiles_n
+                                           : (long long)t.cum[t.n - 1] * tiles_n;
+  const T* A = static_cast<const T*>(g.A);
+  const T* B = static_cast<const T*>(g.B);
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  int e = 0;
+  for (long long item = blockIdx.x; item < items; item += gridDim.x) {
+    const int mt = (int)(item / tiles_n), n0 = (int)(item % tiles_n) * S_T;
+    int m0, m_end, K;
+    long long krow0 = 0;
+    if (KIND == GROUP_DW) {
+      e = mt / tiles_k;
+      m0 = (mt % tiles_k) * S_T;
+      m_end = g.d_in;
+      krow0 = t.lo[e];
+      K = t.hi[e] - t.lo[e];
+    } else {
+      while (t.cum[e] <= mt) ++e;
+      m0 = t.lo[e] + (mt - (e ? t.cum[e - 1] : 0)) * S_T;
+      m_end = t.hi[e];
+      K = e < g.groups ? K0 : 0;
+    }
+    const T* W = KIND == GROUP_DW || e >= g.groups ? B : B + (size_t)e * g.d_in * g.d_out;
+    float acc[4][4] = {};
+    for (int k0 = 0; k0 < K; k0 += S_K) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int i = threadIdx.x + q * 256;
+        float a = 0.f, b = 0.f;
+        if (KIND == GROUP_DW) {
+          const int k = i / S_T, m = i % S_T;
+          if (k0 + k < K && m0 + m < m_end) a = ld_elem(A, (size_t)(krow0 + k0 + k) * g.d_in + m0 + m);
+          As[k][m] = a;
+          if (k0 + k < K && n0 + m < N) b = ld_elem(B, (size_t)(krow0 + k0 + k) * g.d_out + n0 + m);
+          Bs[k][m] = b;
+        } else {
+          const int k = i % S_K, m = i / S_K;
+          if (k0 + k < K && m0 + m < m_end) a = ld_elem(A, (size_t)(m0 + m) * K0 + k0 + k);
+          As[k][m] = a;
+          if (KIND == GROUP_FWD) {
+            const int kb = i / S_T, n = i % S_T;
+            if (k0 + kb < K && n0 + n < N) b = ld_elem(W, (size_t)(k0 + kb) * g.d_out + n0 + n);
+            Bs[kb][n] = b;
+          } else {
+            if (k0 + k < K && n0 + m < N) b = ld_elem(W, (size_t)(n0 + m) * g.d_out + k0 + k);
+            Bs[k][m] = b;
+          }
+        }
+      }
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < S_K; ++k) {
+        float a[4], b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          a[i] = As[k][ty * 4 + i];
+          b[i] = Bs[k][tx * 4 + i];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int m = m0 + ty * 4 + i;
+      if (m >= m_end) continue;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int n = n0 + tx * 4 + j;
+        if (n >= N) continue;
+        float x = acc[i][j];
+        if (KIND == GROUP_DW) {
+          static_cast<float*>(g.out)[((size_t)e * g.d_in + m) * g.d_out + n] = x;
+          continue;
+        }
+        const size_t o = (size_t)m * N + n;
+        auto round_t = [](float v) { return sizeof(T) == 2 ? __bfloat162float(__float2bfloat16_rn(v)) : v; };
+        if (g.act || g.resid || g.out_z) x = round_t(x);
+        if (g.out_z) st_elem(static_cast<T*>(g.out_z), o, x);
+        if (g.act) x = apply_act(g.act, x);
+        if (g.dact) x = round_t(x) * act_grad_from_saved(g.dact, ld_elem(static_cast<const T*>(g.saved), o));
+        if (g.resid) x += ld_elem(static_cast<const T*>(g.resid), o);
+        st_elem(static_cast<T*>(g.out), o, x);
+      }
+    }
+  }
+}
+
+template <typename T, int KIND>
+cudaError_t simt_launch(const GroupArgs& g, cudaStream_t s) {
+  const int N = KIND == GROUP_DX ? g.d_in : g.d_out;
+  const long long tiles_n = (N + S_T - 1) / S_T;
+  const long long tiles_m = KIND == GROUP_DW ? (long long)g.groups * ((g.d_in + S_T - 1) / S_T)
+                                             : (long long)g.rows / S_T + g.groups + 2;   // at most
+  const long long items = tiles_m * tiles_n;
+  const int slots = 8 * device_sms();
+  const int grid = (int)(items < slots ? items : slots);
+  const size_t smem = (size_t)kGroupTableInts(g.groups) * sizeof(int);
+  group_simt_kernel<T, KIND><<<grid, 256, smem, s>>>(g);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t group_ws_bytes(int rows, int groups, int d_in, int d_out) {
+  (void)rows; (void)groups; (void)d_in; (void)d_out;
+  return 256;
+}
+
+cudaError_t grouped_gemm(const GroupArgs& g, cudaStream_t s) {
+  if (g.rows == 0 && g.kind != GROUP_DW) return cudaSuccess;
+  if (g.type == DT_F32) {
+    if (g.kind == GROUP_FWD) return simt_launch<float, GROUP_FWD>(g, s);
+    if (g.kind == GROUP_DX) return simt_launch<float, GROUP_DX>(g, s);
+    return simt_launch<float, GROUP_DW>(g, s);
+  }
+  if (g.kind == GROUP_FWD) return simt_launch<bf16, GROUP_FWD>(g, s);
+  if (g.kind == GROUP_DX) return simt_launch<bf16, GROUP_DX>(g, s);
+  return simt_launch<bf16, GROUP_DW>(g, s);
+}
+
+}  // namespace mg
+
+// ============================================================================
+namespace {
+
+using mg::op_fail;
+
+mg_status grouped_call(const char* fn, mg::GroupKind kind, int dtype, const void* a, const void* b,
+                       const int* offsets, int rows, int groups, int d_in, int d_out, void* out, void* ws,
+                       size_t ws_bytes, mg_stream_t stream) {
+  if (dtype != 0 && dtype != 1) return op_fail(MG_ERR_INVALID_ARG, "%s: dtype must be 0 or 1", fn);
+  if (rows < 0 || groups < 1 || d_in < 1 || d_out < 1)
+    return op_fail(MG_ERR_SHAPE, "%s: bad sizes (rows %d, groups %d, d_in %d, d_out %d)", fn, rows, groups, d_in,
+                   d_out);
+  if (groups > mg::kMaxGroups)
+    return op_fail(MG_ERR_UNSUPPORTED, "%s: at most %d groups (got %d)", fn, mg::kMaxGroups, groups);
+  const bool rows_needed = rows > 0;
+  const bool dw = kind == mg::GROUP_DW;
+  if (!offsets || !ws || (rows_needed && !a) || (!b && (rows_needed || !dw)) || (!out && (rows_needed || dw)))
+    return op_fail(MG_ERR_INVALID_ARG, "%s: a pointer is NULL", fn);
+  const size_t need = mg::group_ws_bytes(rows, groups, d_in, d_out);
+  if (ws_bytes < need)
+    return op_fail(MG_ERR_INVALID_ARG, "%s: the workspace needs %zu bytes, %zu given", fn, need, ws_bytes);
+  mg_status st = mg::op_begin(fn, {{a, 16}, {b, 16}, {offsets, 4}, {out, 16}, {ws, 16}});
+  if (st != MG_OK) return st;
+  mg::GroupArgs g;
+  g.kind = kind;
+  g.type = (mg::DType)dtype;
+  g.rows = rows;
+  g.groups = groups;
+  g.d_in = d_in;
+  g.d_out = d_out;
+  g.offsets = offsets;
+  g.A = a;
+  g.B = b;
+  g.out = out;
+  g.ws = static_cast<int*>(ws);
+  return mg::op_end(fn, mg::grouped_gemm(g, (cudaStream_t)stream));
+}
+
+}  // namespace
+
+extern "C" size_t mg_grouped_linear_workspace_bytes(int rows, int groups, int d_in, int d_out) {
+  if (rows < 0 || groups < 1 || groups > mg::kMaxGroups || d_in < 1 || d_out < 1) return 0;
+  return mg::group_ws_bytes(rows, groups, d_in, d_out);
+}
+
+extern "C" mg_status mg_grouped_linear_forward(int dtype, const void* x, const int* offsets, int rows, int groups,
+                                               int d_in, int d_out, const void* w, void* y, void* ws,
+                                               size_t ws_bytes, mg_stream_t stream) {
+  return grouped_call("mg_grouped_linear_forward", mg::GROUP_FWD, dtype, x, w, offsets, rows, groups, d_in, d_out,
+                      y, ws, ws_bytes, stream);
+}
+
+extern "C" mg_status mg_grouped_linear_backward_input(int dtype, const void* dy, const int* offsets, int rows,
+                                                      int groups, int d_in, int d_out, const void* w, void* dx,
+                                                      void* ws, size_t ws_bytes, mg_stream_t stream) {
+  return grouped_call("mg_grouped_linear_backward_input", mg::GROUP_DX, dtype, dy, w, offsets, rows, groups, d_in,
+                      d_out, dx, ws, ws_bytes, stream);
+}
+
+extern "C" mg_status mg_grouped_linear_backward_weight(int dtype, const void* x, const void* dy, const int* offsets,
+                                                       int rows, int groups, int d_in, int d_out, float* dw,
+                                                       void* ws, size_t ws_bytes, mg_stream_t stream) {
+  return grouped_call("mg_grouped_linear_backward_weight", mg::GROUP_DW, dtype, x, dy, offsets, rows, groups, d_in,
+                      d_out, dw, ws, ws_bytes, stream);
+}

@@ -165,6 +165,45 @@ cudaError_t write_step_scalars(float* dst, float lr_bc1, float inv_sqrt_bc2, cud
 cudaError_t cast_shadow(const Chunk* chunks, int n_chunks, const float* p, void* shadow,
                         cudaStream_t s);
 
+// ---- embedding --------------------------------------------------------------
+// out[i] = scale * table[id_i], 0 for an id outside [0, V); id64: int64 ids.
+cudaError_t embedding_fwd(DType tt, const void* table, int V, int d, int id64, const void* ids,
+                          long long n, float scale, DType ot, void* out, cudaStream_t s);
+// The gradient in two parts, so that the sort of the ids (which needs nothing
+// of the backward pass) can run early: positions sorted by id in workspace
+// (embedding_ws_bytes), then every row of dtable written once.
+size_t embedding_ws_bytes(long long n, int V, int d);
+cudaError_t embedding_bwd_sort(int id64, const void* ids, long long n, int V, int d, void* workspace,
+                               cudaStream_t s);
+cudaError_t embedding_bwd_sum(DType t, const void* dout, long long n, int V, int d, float scale,
+                              float* dtable, void* workspace, cudaStream_t s);
+
+// ---- products grouped by expert ----------------------------------------------
+// Rows of the token operands ordered by group, offsets [groups + 1] in device
+// memory.  GROUP_FWD: out[r] = A[r] W[e]; GROUP_DX: out[r] = A[r] W[e]^T;
+// GROUP_DW: out[e] = A_e^T B_e (fp32).  W [groups, d_in, d_out].
+enum GroupKind { GROUP_FWD = 0, GROUP_DX = 1, GROUP_DW = 2 };
+struct GroupArgs {
+  int kind = GROUP_FWD;
+  DType type = DT_F32;
+  int rows = 0, groups = 0, d_in = 0, d_out = 0;
+  const int* offsets = nullptr;
+  const void* A = nullptr;     // x (FWD, DW) or dy (DX)
+  const void* B = nullptr;     // W (FWD, DX) or dy (DW)
+  void* out = nullptr;
+  // epilogue of FWD and DX, as GemmArgs': v (rounded to the type when act,
+  // resid or out_z is set); out_z = v; v = act(v); v *= act'(saved); v += resid
+  int act = 0;
+  void* out_z = nullptr;
+  const void* saved = nullptr; int dact = 0;
+  const void* resid = nullptr;
+  int zero_rest = 0;           // rows of no group are computed as if A were 0 there
+  int* ws = nullptr;           // group_ws_bytes; ws[0] is set to 1 on a timed-out wait
+};
+size_t group_ws_bytes(int rows, int groups, int d_in, int d_out);
+constexpr int kMaxGroups = 1024;
+cudaError_t grouped_gemm(const GroupArgs& g, cudaStream_t s);
+
 // ---- misc --------------------------------------------------------------------
 cudaError_t cast_to_f32(DType t, const void* src, float* dst, size_t n, cudaStream_t s);
 cudaError_t find_nonfinite(const float* data, size_t n, unsigned long long* first_bad,
