@@ -155,6 +155,7 @@ size_t group_ws_bytes(int rows, int groups, int d_in, int d_out) {
 
 cudaError_t grouped_gemm(const GroupArgs& g, cudaStream_t s) {
   if (g.rows == 0 && g.kind != GROUP_DW) return cudaSuccess;
+  if (grouped_tc_eligible(g)) return grouped_gemm_tc(g, s);
   if (g.type == DT_F32) {
     if (g.kind == GROUP_FWD) return simt_launch<float, GROUP_FWD>(g, s);
     if (g.kind == GROUP_DX) return simt_launch<float, GROUP_DX>(g, s);

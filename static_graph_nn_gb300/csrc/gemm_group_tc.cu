@@ -1,0 +1,480 @@
+// Matrix products grouped by expert on the tensor cores: 256x256 output tiles
+// on CTA pairs (tcgen05 cta_group::2, bf16 operands, fp32 accumulators in
+// TMEM), the arrangement of the dense SM-pair GEMM (gemm_tc2.cu) with a ragged
+// list of tiles.
+//
+//   forward  y_e  = x_e  W_e      A = x  K-major,  B = W_e N-major
+//   dX       dx_e = dy_e W_e^T    A = dy K-major,  B = W_e K-major
+//   dW       dW_e = x_e^T dy_e    A = x  M-major,  B = dy  N-major, fp32 out
+//
+// Bound by the tensor cores (2 T K N flops against x + W + y bytes) once the
+// groups have a few hundred rows.
+//
+// Ragged rows.  Every CTA reads the offsets into shared memory and walks the
+// same list of tiles (group by group, columns fastest), so one persistent
+// launch serves all groups.  A forward tile's last rows may belong to the next
+// group: they are computed into accumulator rows of their own and not stored.
+// W is addressed as a three-dimensional tensor, so a K block past its last row
+// reads zeros, not the next expert's weights.  In dW the groups' rows are the
+// K dimension, and the last 64-row block of a group may hold rows of the next
+// one: the producer warp loads that block on a barrier of its own, overwrites
+// the foreign rows with zeros in shared memory (both operands: a NaN there
+// would survive a zero factor), fences them to the async proxy and only then
+// reports the stage full.  One such block per group and tile; the MMAs of the
+// blocks before it run meanwhile.
+//
+// Warp roles and pipeline as in gemm_tc2.cu: warp 0 TMA producer, warp 1 MMA
+// issuer (leader CTA), warps 2-9 epilogue; six 32 KB stages per CTA; two
+// accumulators of 256 columns.  Every wait is bounded.
+#include <cuda.h>
+
+#include "common.cuh"
+#include "group_table.cuh"
+#include "kernels.h"
+#include "op_checks.h"
+#include "tc_common.cuh"
+#include "tc_epilogue.cuh"
+#include "tc_pair.cuh"
+
+namespace mg {
+namespace {
+
+using namespace tc;
+
+constexpr int G_BM = 128;          // rows per CTA (256 per pair)
+constexpr int G_BNH = 128;         // B columns per CTA (256 per pair)
+constexpr int G_BN = 256;
+constexpr int G_BK = 64;
+constexpr int G_STAGES = 6;
+constexpr int G_THREADS = 320;
+constexpr uint32_t G_A_BYTES = G_BM * G_BK * 2;
+constexpr uint32_t G_B_BYTES = G_BNH * G_BK * 2;
+constexpr int G_PANEL = 64 * G_BK * 2;   // one 64-column panel of a stage
+
+struct GroupTcParams {
+  GemmArgs g;              // the epilogue: N, leading dimensions, outputs
+  const int* offsets;
+  int rows, groups, zero_rest;
+  int d_in, d_out;
+  int tiles_n;             // 256-column tiles of an output row
+  int tiles_m;             // dW: 256-row tiles of one dW[e]
+  int k_blocks;            // forward, dX
+  int vec, vec32;
+  int* err;
+};
+
+// One output tile of the list.
+struct GroupTile {
+  int e, m0, m_end, n0;
+  int kb;        // K blocks (0: the result is zero)
+  int krow0;     // dW: first row of the group
+  int tail;      // dW: rows of the last K block that belong to the group, 0 if all 64 do
+};
+
+template <int KIND>
+__device__ __forceinline__ int tile_count(const GroupTcParams& P, const GroupTable& t) {
+  return KIND == GROUP_DW ? P.groups * P.tiles_m * P.tiles_n : t.cum[t.n - 1] * P.tiles_n;
+}
+
+// e: cursor kept between calls (items ascend).
+template <int KIND>
+__device__ __forceinline__ GroupTile tile_at(const GroupTcParams& P, const GroupTable& t, int item, int& e) {
+  GroupTile r;
+  if (KIND == GROUP_DW) {
+    const int per = P.tiles_m * P.tiles_n;
+    e = item / per;
+    const int q = item - e * per;
+    r.m0 = (q / P.tiles_n) * 2 * G_BM;
+    r.n0 = (q % P.tiles_n) * G_BN;
+    r.m_end = P.d_in;
+    r.krow0 = t.lo[e];
+    const int size = t.hi[e] - t.lo[e];
+    r.kb = (size + G_BK - 1) / G_BK;
+    r.tail = size % G_BK;
+  } else {
+    const int mt = item / P.tiles_n;
+    r.n0 = (item - mt * P.tiles_n) * G_BN;
+    while (t.cum[e] <= mt) ++e;
+    r.m0 = t.lo[e] + (mt - (e ? t.cum[e - 1] : 0)) * 2 * G_BM;
+    r.m_end = t.hi[e];
+    r.kb = e < P.groups ? P.k_blocks : 0;
+    r.krow0 = 0;
+    r.tail = 0;
+  }
+  r.e = e;
+  return r;
+}
+
+__device__ __forceinline__ void tma_load_3d_to_leader(void* dst, const CUtensorMap* map, uint32_t bar_cluster,
+                                                      int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+// Remote arrive that publishes this thread's earlier writes to the cluster.
+__device__ __forceinline__ void mbar_arrive_remote_release(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+template <int KIND, typename TO>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G_THREADS, 1)
+    group_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                      const GroupTcParams P) {
+  constexpr bool A_MN = KIND == GROUP_DW;
+  constexpr bool B_MN = KIND != GROUP_DX;
+  constexpr uint32_t TMEM_COLS = 2 * G_BN;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* sA = smem;
+  uint8_t* sB = smem + G_STAGES * G_A_BYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sB + G_STAGES * G_B_BYTES);
+  uint64_t* empty = full + G_STAGES;
+  uint64_t* tfull = empty + G_STAGES;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* tailbar = tempty + 2;      // this CTA's loads of a block that needs zeroing
+  uint64_t* fixbar = tailbar + 1;      // leader: the peer's block is zeroed
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(fixbar + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  GroupTable t;
+  t.n = P.groups + (P.zero_rest ? 2 : 0);
+  t.lo = reinterpret_cast<int*>(tmem_slot + 2);
+  t.hi = t.lo + P.groups + 2;
+  t.cum = t.hi + P.groups + 2;
+
+  const uint32_t rank = cluster_rank();
+  const bool leader = rank == 0;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < G_STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&tfull[a], 1);
+      mbar_init(&tempty[a], 2 * 256);
+    }
+    mbar_init(tailbar, 1);
+    mbar_init(fixbar, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"(TMEM_COLS));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  }
+  if (warp == 2) load_group_table(t, P.offsets, P.groups, P.rows, 2 * G_BM);
+  tc_fence_before();
+  cluster_sync();                      // barriers, tables and TMEM of both CTAs are ready
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const int n_items = tile_count<KIND>(P, t);
+
+  if (warp == 0) {
+    // ---------------- TMA producer (both CTAs; the whole warp, for the zeroing) ----------------
+    int stage = 0, e = 0;
+    uint32_t phase = 0, tail_phase = 0;
+    for (int item = pair; item < n_items; item += npairs) {
+      const GroupTile T = tile_at<KIND>(P, t, item, e);
+      const int plain = T.tail ? T.kb - 1 : T.kb;
+      const int m0 = T.m0 + (int)rank * G_BM, n0 = T.n0 + (int)rank * G_BNH;
+      int ok = 1;
+      if (lane == 0) {
+        int st = stage;
+        uint32_t ph = phase;
+        for (int kb = 0; kb < plain; ++kb) {
+          if (*abort_flag || !mbar_wait_cluster(&empty[st], ph ^ 1)) { ok = 0; break; }
+          if (leader) mbar_expect_tx(&full[st], 2 * (G_A_BYTES + G_B_BYTES));
+          const uint32_t fb = map_to(&full[st], 0);
+          const int k0 = kb * G_BK;
+          uint8_t* a = sA + st * G_A_BYTES;
+          uint8_t* b = sB + st * G_B_BYTES;
+          if (A_MN) {
+            tma_load_2d_to_leader(a, &tmA, fb, m0, T.krow0 + k0);
+            tma_load_2d_to_leader(a + G_PANEL, &tmA, fb, m0 + 64, T.krow0 + k0);
+          } else {
+            tma_load_2d_to_leader(a, &tmA, fb, k0, m0);
+          }
+          if (KIND == GROUP_DW) {
+            tma_load_2d_to_leader(b, &tmB, fb, n0, T.krow0 + k0);
+            tma_load_2d_to_leader(b + G_PANEL, &tmB, fb, n0 + 64, T.krow0 + k0);
+          } else if (B_MN) {
+            tma_load_3d_to_leader(b, &tmB, fb, n0, k0, T.e);
+            tma_load_3d_to_leader(b + G_PANEL, &tmB, fb, n0 + 64, k0, T.e);
+          } else {
+            tma_load_3d_to_leader(b, &tmB, fb, k0, n0, T.e);
+          }
+          if (++st == G_STAGES) { st = 0; ph ^= 1; }
+        }
+      }
+      const int adv = stage + plain;
+      stage = adv % G_STAGES;
+      phase ^= (uint32_t)(adv / G_STAGES) & 1u;
+      if (KIND == GROUP_DW && T.tail) {
+        uint8_t* a = sA + stage * G_A_BYTES;
+        uint8_t* b = sB + stage * G_B_BYTES;
+        if (lane == 0 && ok) {
+          ok = !*abort_flag && mbar_wait_cluster(&empty[stage], phase ^ 1);
+          if (ok) {
+            const int kr = T.krow0 + plain * G_BK;
+            mbar_expect_tx(tailbar, G_A_BYTES + G_B_BYTES);
+            tma_load_2d(a, &tmA, tailbar, m0, kr);
+            tma_load_2d(a + G_PANEL, &tmA, tailbar, m0 + 64, kr);
+            tma_load_2d(b, &tmB, tailbar, n0, kr);
+            tma_load_2d(b + G_PANEL, &tmB, tailbar, n0 + 64, kr);
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (ok) ok = mbar_wait(tailbar, tail_phase);
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok) {
+          // a K row is one 128-byte line of each panel, whatever the swizzle inside it
+          const int n16 = (G_BK - T.tail) * 8;
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            uint4* q = reinterpret_cast<uint4*>((p < 2 ? a + p * G_PANEL : b + (p - 2) * G_PANEL) + T.tail * 128);
+            for (int i = lane; i < n16; i += 32) q[i] = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) {
+            if (leader) {
+              ok = mbar_wait_cluster(fixbar, tail_phase);
+              if (ok) mbar_arrive(&full[stage]);
+            } else {
+              mbar_arrive_remote_release(map_to(fixbar, 0));
+            }
+          }
+        }
+        tail_phase ^= 1;
+        if (++stage == G_STAGES) { stage = 0; phase ^= 1; }
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) {
+        if (lane == 0) { *abort_flag = 1; atomicExch(P.err, 1); }
+        break;
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && leader) {
+      // ---------------- leader: MMA issuer for the pair ----------------
+      constexpr uint32_t idesc = instr_desc(2 * G_BM, G_BN, A_MN ? 1 : 0, B_MN ? 1 : 0);
+      int stage = 0, e = 0, it = 0;
+      uint32_t phase = 0;
+      for (int item = pair; item < n_items && !*abort_flag; item += npairs, ++it) {
+        const GroupTile T = tile_at<KIND>(P, t, item, e);
+        const int acc = it & 1;
+        const uint32_t use = (uint32_t)(it >> 1) & 1u;
+        if (!mbar_wait_cluster(&tempty[acc], use ^ 1)) { *abort_flag = 1; atomicExch(P.err, 1); break; }
+        tc_fence_after();
+        const uint32_t d = tmem_base + (uint32_t)(acc * G_BN);
+        bool ok = true;
+        for (int kb = 0; kb < T.kb; ++kb) {
+          if (!mbar_wait_cluster(&full[stage], phase)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t a = smem_u32(sA + stage * G_A_BYTES);
+          const uint32_t b = smem_u32(sB + stage * G_B_BYTES);
+#pragma unroll
+          for (int k = 0; k < G_BK / 16; ++k) {
+            const uint64_t ad = A_MN ? smem_desc(a + k * 2048, G_PANEL, 1024) : smem_desc(a + k * 32, 16, 1024);
+            const uint64_t bd = B_MN ? smem_desc(b + k * 2048, G_PANEL, 1024) : smem_desc(b + k * 32, 16, 1024);
+            mma_bf16_pair(d, ad, bd, idesc, (kb | k) ? 1u : 0u);
+          }
+          mma_commit_pair(&empty[stage]);
+          if (++stage == G_STAGES) { stage = 0; phase ^= 1; }
+        }
+        if (!ok) { *abort_flag = 1; atomicExch(P.err, 1); break; }
+        mma_commit_pair(&tfull[acc]);
+      }
+    }
+  } else {
+    // ---------------- epilogue (warps 2..9, both CTAs) ----------------
+    const int quarter = warp & 3;
+    const int half = (warp - 2) >> 2;
+    const int row_in_tile = quarter * 32 + lane;
+    const uint32_t leader_tempty[2] = {map_to(&tempty[0], 0), map_to(&tempty[1], 0)};
+    int e = 0, it = 0;
+    for (int item = pair; item < n_items; item += npairs, ++it) {
+      const GroupTile T = tile_at<KIND>(P, t, item, e);
+      const int acc = it & 1;
+      const uint32_t use = (uint32_t)(it >> 1) & 1u;
+      if (!mbar_wait(&tfull[acc], use)) { *abort_flag = 1; atomicExch(P.err, 1); break; }
+      if (*abort_flag) break;
+      tc_fence_after();
+      const int m = T.m0 + (int)rank * G_BM + row_in_tile;
+      const bool row_ok = m < T.m_end;
+      // dW[e] is rows e*d_in .. of one [groups * d_in, d_out] matrix
+      const int mo = KIND == GROUP_DW ? T.e * P.d_in + m : m;
+      const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * G_BN);
+#pragma unroll 1
+      for (int cp = 0; cp < 2; ++cp) {
+        const int c0 = half * (G_BN / 64) + 2 * cp;
+        uint32_t r0[32], r1[32];
+        tmem_ld32_async(taddr + c0 * 32, r0);
+        tmem_ld32_async(taddr + (c0 + 1) * 32, r1);
+        tmem_wait_regs(r0);
+        reg_fence(r1);
+        if (cp == 1) {
+          tc_fence_before();
+          mbar_arrive_remote(leader_tempty[acc]);
+        }
+        auto chunk = [&](int c, uint32_t (&r)[32]) {
+          const int n = T.n0 + c * 32;
+          if (!row_ok || n >= P.g.N) return;
+          float v[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = T.kb ? __uint_as_float(r[i]) : 0.0f;
+          epi32<TO>(P.g, P.vec != 0, P.vec32 != 0, mo, n, v);
+        };
+        chunk(c0, r0);
+        chunk(c0 + 1, r1);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();                      // no remote arrive or MMA still targets either CTA
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(TMEM_COLS));
+  }
+}
+
+// ---------------------------------------------------------------- host side
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn group_encode_fn() {
+  static EncodeTiledFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      return reinterpret_cast<EncodeTiledFn>(p);
+    return static_cast<EncodeTiledFn>(nullptr);
+  }();
+  return fn;
+}
+
+// bf16 [outer][rows][cols], dense; box box_cols x box_rows x 1, 128-byte
+// swizzle.  outer = 0: two-dimensional.
+bool group_map(CUtensorMap* map, const void* base, long long outer, long long rows, long long cols, int box_cols,
+               int box_rows) {
+  EncodeTiledFn fn = group_encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)outer};
+  cuuint64_t strides[2] = {(cuuint64_t)cols * 2, (cuuint64_t)cols * (cuuint64_t)rows * 2};
+  cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, outer ? 3 : 2, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+size_t group_pair_smem(int groups) {
+  return 1024 + (size_t)G_STAGES * (G_A_BYTES + G_B_BYTES) + (2 * G_STAGES + 6) * 8 + 8 +
+         (size_t)kGroupTableInts(groups) * 4;
+}
+
+template <int KIND, typename TO>
+cudaError_t launch_group_pair(const GroupArgs& g, cudaStream_t s) {
+  CUtensorMap ma, mb;
+  bool ok;
+  if (KIND == GROUP_DW) {
+    ok = group_map(&ma, g.A, 0, g.rows, g.d_in, 64, G_BK) && group_map(&mb, g.B, 0, g.rows, g.d_out, 64, G_BK);
+  } else {
+    const int k = KIND == GROUP_FWD ? g.d_in : g.d_out;
+    ok = group_map(&ma, g.A, 0, g.rows, k, G_BK, G_BM) &&
+         (KIND == GROUP_FWD ? group_map(&mb, g.B, g.groups, g.d_in, g.d_out, 64, G_BK)
+                            : group_map(&mb, g.B, g.groups, g.d_in, g.d_out, G_BK, G_BNH));
+  }
+  if (!ok) return cudaErrorInvalidValue;
+  GroupTcParams P;
+  const int N = KIND == GROUP_DX ? g.d_in : g.d_out;
+  P.g.N = N;
+  P.g.act = g.act;
+  P.g.out_z = g.out_z; P.g.ldz = N;
+  P.g.saved = g.saved; P.g.lds = N; P.g.dact = g.dact;
+  P.g.resid = g.resid; P.g.ldr = N;
+  P.g.aux_type = DT_BF16;
+  P.g.out = g.out; P.g.ldo = N;
+  P.g.out_type = sizeof(TO) == 4 ? DT_F32 : DT_BF16;
+  P.offsets = g.offsets;
+  P.rows = g.rows;
+  P.groups = g.groups;
+  P.zero_rest = g.zero_rest;
+  P.d_in = g.d_in;
+  P.d_out = g.d_out;
+  P.tiles_n = (N + G_BN - 1) / G_BN;
+  P.tiles_m = (g.d_in + 2 * G_BM - 1) / (2 * G_BM);
+  P.k_blocks = ((KIND == GROUP_FWD ? g.d_in : g.d_out) + G_BK - 1) / G_BK;
+  P.err = g.ws;
+  auto al = [](const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; };
+  P.vec = al(g.out, 16) && al(g.out_z, 16) && al(g.saved, 16) && al(g.resid, 16) && N % 8 == 0;
+  P.vec32 = al(g.out, 32) && al(g.out_z, 32) && al(g.saved, 32) && al(g.resid, 32) && N % 16 == 0;
+  auto kern = group_pair_kernel<KIND, TO>;
+  const size_t smem = group_pair_smem(g.groups);
+  static const cudaError_t attr = cudaFuncSetAttribute(
+      kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)group_pair_smem(kMaxGroups));
+  if (attr != cudaSuccess) return attr;
+  static const int slots = [&] {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * (device_sms() / 2));
+    cfg.blockDim = dim3(G_THREADS);
+    cfg.dynamicSmemBytes = group_pair_smem(kMaxGroups);
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = 2;
+    at.val.clusterDim.y = 1;
+    at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    int c = 0;
+    if (cudaOccupancyMaxActiveClusters(&c, kern, &cfg) != cudaSuccess || c <= 0) {
+      cudaGetLastError();
+      c = device_sms() / 2;
+    }
+    return c;
+  }();
+  // tiles at most: every group may end inside one
+  const long long items = KIND == GROUP_DW
+                              ? (long long)g.groups * P.tiles_m * P.tiles_n
+                              : ((long long)g.rows / (2 * G_BM) + g.groups + (g.zero_rest ? 2 : 0)) * P.tiles_n;
+  if (items > 0x7fffffff) return cudaErrorInvalidValue;
+  const int pairs = items < slots ? (int)items : slots;
+  kern<<<2 * pairs, G_THREADS, smem, s>>>(ma, mb, P);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+bool grouped_tc_eligible(const GroupArgs& g) {
+  auto al = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
+  // mo = e * d_in + m and the tile counts are 32-bit
+  if (g.type != DT_BF16 || g.rows == 0 || g.d_in % 8 || g.d_out % 8) return false;
+  if ((long long)g.groups * g.d_in > 0x7fff0000ll) return false;
+  const long long tiles_n = ((g.kind == GROUP_DX ? g.d_in : g.d_out) + G_BN - 1) / G_BN;
+  const long long tiles_m = g.kind == GROUP_DW ? (long long)g.groups * ((g.d_in + 255) / 256)
+                                               : g.rows / 256 + g.groups + 2ll;
+  if (tiles_m * tiles_n > 0x3fffffffll) return false;
+  return al(g.A) && al(g.B) && group_encode_fn() != nullptr;
+}
+
+cudaError_t grouped_gemm_tc(const GroupArgs& g, cudaStream_t s) {
+  if (g.kind == GROUP_FWD) return launch_group_pair<GROUP_FWD, bf16>(g, s);
+  if (g.kind == GROUP_DX) return launch_group_pair<GROUP_DX, bf16>(g, s);
+  return launch_group_pair<GROUP_DW, float>(g, s);
+}
+
+}  // namespace mg

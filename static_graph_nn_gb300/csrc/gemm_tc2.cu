@@ -28,6 +28,8 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "tc_common.cuh"
+#include "tc_epilogue.cuh"
+#include "tc_pair.cuh"
 
 namespace mg {
 namespace {
@@ -52,91 +54,6 @@ struct PairParams {
   int* err;
 };
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-
-// shared::cluster address of the same object in CTA `rank` of this cluster
-__device__ __forceinline__ uint32_t map_to(const void* p, uint32_t rank) {
-  uint32_t out;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(out) : "r"(smem_u32(p)), "r"(rank));
-  return out;
-}
-
-// Arrive on a barrier of another CTA of the cluster.  Default semantics
-// (release at CTA scope): it signals that this thread's TMEM reads are done
-// (tcgen05.wait::ld, then tcgen05.fence::before_thread_sync), and must not
-// wait for the thread's global stores to reach cluster scope -- nothing the
-// waiting MMA thread reads depends on them.  (With .release.cluster each
-// epilogue warp stalled on a memory barrier per tile, holding the
-// accumulator until its output stores were acknowledged.)
-__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-
-// TMA load into this CTA's shared memory whose completion is counted on the
-// leader CTA's barrier (cluster address bar_cluster).
-__device__ __forceinline__ void tma_load_2d_to_leader(void* dst, const CUtensorMap* map,
-                                                      uint32_t bar_cluster, int x, int y) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(x), "r"(y)
-      : "memory");
-}
-
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ void mma_bf16_pair(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
-                                              uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n.reg .pred p;\n"
-      "setp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(tmem_d),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate));
-}
-
-// Arrive on the barrier at this offset in both CTAs once the pair's MMAs issued
-// so far have completed.
-__device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
-      "[%0], %1;" ::"r"(smem_u32(bar)),
-      "h"((uint16_t)3)
-      : "memory");
-}
-
-template <typename TO>
-__device__ __forceinline__ float rv(float v) {
-  return sizeof(TO) == 2 ? __bfloat162float(__float2bfloat16_rn(v)) : v;
-}
-
-__device__ __forceinline__ void ld8f(const bf16* p, float* f) {
-  uint4 u = *reinterpret_cast<const uint4*>(p);
-  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float2 t = __bfloat1622float2(h[i]);
-    f[2 * i] = t.x;
-    f[2 * i + 1] = t.y;
-  }
-}
-
-__device__ __forceinline__ void st8f(bf16* p, const float* f) {
-  uint4 u;
-  uint32_t* w = reinterpret_cast<uint32_t*>(&u);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-    w[i] = *reinterpret_cast<uint32_t*>(&h);
-  }
-  *reinterpret_cast<uint4*>(p) = u;
-}
-
 // One split's partial sums of 32 columns of one row, added into the (zeroed)
 // fp32 output; plain weight-gradient outputs only.
 __device__ __forceinline__ void split_add32(const GemmArgs& g, bool vec, int m, int n0,
@@ -152,109 +69,6 @@ __device__ __forceinline__ void split_add32(const GemmArgs& g, bool vec, int m, 
 #pragma unroll
   for (int j = 0; j < 32; ++j)
     if (n0 + j < g.N) atomicAdd(out + j, v[j]);
-}
-
-// Epilogue of 32 columns of one row; identical arithmetic to gemm_tc.cu.  On
-// return v holds the values stored (before their rounding to TO) at the
-// columns below N.
-template <typename TO>
-__device__ __forceinline__ void epi32(const GemmArgs& g, bool vec, bool vec32, int m, int n0,
-                                      float (&v)[32]) {
-  if (vec && n0 + 32 <= g.N) {
-    if (g.bias) {
-      const float4* b4 = reinterpret_cast<const float4*>(g.bias + n0);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        float4 b = b4[q];
-        v[4 * q] += b.x; v[4 * q + 1] += b.y; v[4 * q + 2] += b.z; v[4 * q + 3] += b.w;
-      }
-    }
-    if (g.act || g.resid || g.out_z) {
-#pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] = rv<TO>(v[j]);
-    }
-    if (g.out_z) {
-      bf16* z = static_cast<bf16*>(g.out_z) + (size_t)m * g.ldz + n0;
-      if (vec32) {
-        st16bf(z, v);
-        st16bf(z + 16, v + 16);
-      } else {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) st8f(z + 8 * q, v + 8 * q);
-      }
-    }
-    if (g.act) {
-#pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] = apply_act(g.act, v[j]);
-    }
-    if (g.dact) {
-      const bf16* sv = static_cast<const bf16*>(g.saved) + (size_t)m * g.lds + n0;
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        float f[16];
-        if (vec32) {
-          ld16bf(sv + 16 * q, f);
-        } else {
-          ld8f(sv + 16 * q, f);
-          ld8f(sv + 16 * q + 8, f + 8);
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          v[16 * q + i] = rv<TO>(v[16 * q + i]) * act_grad_from_saved(g.dact, f[i]);
-      }
-    }
-    if (g.resid) {
-      const bf16* rp = static_cast<const bf16*>(g.resid) + (size_t)m * g.ldr + n0;
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        float f[16];
-        if (vec32) {
-          ld16bf(rp + 16 * q, f);
-        } else {
-          ld8f(rp + 16 * q, f);
-          ld8f(rp + 16 * q + 8, f + 8);
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[16 * q + i] += f[i];
-      }
-    }
-    TO* out = static_cast<TO*>(g.out) + (size_t)m * g.ldo + n0;
-    if (vec32) {
-      if (sizeof(TO) == 2) {
-        st16bf(reinterpret_cast<bf16*>(out), v);
-        st16bf(reinterpret_cast<bf16*>(out) + 16, v + 16);
-      } else {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) st8f32(reinterpret_cast<float*>(out) + 8 * q, v + 8 * q);
-      }
-    } else if (sizeof(TO) == 2) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) st8f(reinterpret_cast<bf16*>(out) + 8 * q, v + 8 * q);
-    } else {
-#pragma unroll
-      for (int q = 0; q < 8; ++q)
-        reinterpret_cast<float4*>(out)[q] = make_float4(v[q * 4], v[q * 4 + 1], v[q * 4 + 2], v[q * 4 + 3]);
-    }
-    return;
-  }
-  const size_t rz = (size_t)m * g.ldz, rs = (size_t)m * g.lds, rr = (size_t)m * g.ldr;
-#pragma unroll
-  for (int j = 0; j < 32; ++j) {
-    const int n = n0 + j;
-    if (n >= g.N) continue;
-    float x = v[j];
-    if (g.bias) x += g.bias[n];
-    if (g.act || g.resid || g.out_z) x = rv<TO>(x);
-    if (g.out_z) static_cast<bf16*>(g.out_z)[rz + n] = __float2bfloat16_rn(x);
-    if (g.act) x = apply_act(g.act, x);
-    if (g.dact) {
-      x = rv<TO>(x);
-      x *= act_grad_from_saved(g.dact, __bfloat162float(static_cast<const bf16*>(g.saved)[rs + n]));
-    }
-    if (g.resid) x += __bfloat162float(static_cast<const bf16*>(g.resid)[rr + n]);
-    st_elem(static_cast<TO*>(g.out), (size_t)m * g.ldo + n, x);
-    v[j] = x;
-  }
 }
 
 template <typename TO, bool A_MN, bool B_MN>

@@ -203,6 +203,9 @@ struct GroupArgs {
 size_t group_ws_bytes(int rows, int groups, int d_in, int d_out);
 constexpr int kMaxGroups = 1024;
 cudaError_t grouped_gemm(const GroupArgs& g, cudaStream_t s);
+// The tensor-core version: bf16, widths that are multiples of 8.
+bool grouped_tc_eligible(const GroupArgs& g);
+cudaError_t grouped_gemm_tc(const GroupArgs& g, cudaStream_t s);
 
 // ---- misc --------------------------------------------------------------------
 cudaError_t cast_to_f32(DType t, const void* src, float* dst, size_t n, cudaStream_t s);
