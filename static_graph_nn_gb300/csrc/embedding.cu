@@ -9,15 +9,23 @@
 //
 // The backward must write all V rows, and sums the rows of dout that share an
 // id.  Adding with atomics would need a zeroed table, a read-modify-write of
-// every touched row, and would change results from run to run.  Instead the
-// positions are sorted by id with a stable counting sort (positions of one id
-// stay ascending), which leaves each id's positions as one segment; then every
-// row of the table is written exactly once: zeros where the segment is empty,
-// else the fp32 sum in ascending position order.  Text has a few very frequent
-// ids; a segment longer than kHot entries is summed by many blocks, each over
-// one fixed window of the sorted order, and the last block to finish adds the
-// windows' partials in order.  The order of every addition is fixed by the ids
-// alone, so the result is the same in every run.
+// every touched row, and would change results from run to run.  Instead:
+//
+//   1. the positions are sorted by id with a stable counting sort (positions of
+//      one id stay ascending).  Up to 65536 ids one cluster of four CTAs sorts
+//      them in shared memory, exchanging counts and elements through DSMEM;
+//      meanwhile the other CTAs of the launch write the zero rows, each
+//      finding the ids of its own range of rows with one scan of the ids, so
+//      the sort's latency hides under bandwidth-bound stores;
+//   2. the sorted order is cut into equal windows, one thread group each, so
+//      that frequent ids cost no more than rare ones.  A group streams its
+//      window's rows of dout, eight in flight, and writes a row of the table
+//      whenever the id changes.  A sum that crosses windows leaves one partial
+//      per window; the group that arrives last adds them in window order.
+//
+// Every row of the table is written once, and the order of every addition is
+// fixed by the ids alone: the same bits in every run.  Bound by DRAM (V d fp32
+// written, n d read).
 #include <cstdio>
 
 #include "../../include/mg.h"
@@ -34,8 +42,12 @@ constexpr int kSortThreads = 256;
 constexpr int kSortItems = 16;                            // per thread
 constexpr int kSortTile = kSortThreads * kSortItems;      // 4096 keys per block
 constexpr int kWarps = kSortThreads / 32;
-constexpr int kWindowMin = 64;      // sorted entries per window of a hot segment
-constexpr int kMaxWindows = 2048;   // windows of any call: bounds a hot row's partials
+constexpr int kWindows = 512;       // windows a call is cut into (8 entries at least)
+constexpr int kCluster = 4;         // CTAs that sort together
+constexpr int kSmallThreads = 1024;
+constexpr int kSmallItems = 16;     // ids per thread at most
+constexpr long long kSmallMax = (long long)kCluster * kSmallThreads * kSmallItems;
+constexpr int kZeroRange = 65536;   // rows whose presence one block holds as bits
 
 // ---------------------------------------------------------------- forward
 
@@ -292,42 +304,222 @@ __global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(KeysIn in, u
   }
 }
 
-// start[v] = first sorted entry with key >= v, for v in [0, V]; also clears the
-// hot rows' arrival counters.  An entry fills the rows between its
-// predecessor's key and its own; long runs of absent ids are filled by the
-// whole block.
-__global__ void __launch_bounds__(256) sort_bounds_kernel(const uint32_t* key, uint32_t n, uint32_t V,
-                                                          uint32_t* start, uint32_t* arrivals,
-                                                          uint32_t n_arrivals) {
-  __shared__ uint32_t big_lo[256], big_hi[256], big_at[256];
-  __shared__ int nbig;
-  const uint32_t gtid = blockIdx.x * 256u + threadIdx.x;
-  for (uint32_t a = gtid; a < n_arrivals; a += gridDim.x * 256u) arrivals[a] = 0;
-  if (threadIdx.x == 0) nbig = 0;
-  __syncthreads();
-  const uint32_t i = gtid;
-  if (i <= n) {
-    const uint32_t lo = i == 0 ? 0 : key[i - 1] + 1;      // first row not yet filled
-    const uint32_t hi = i == n ? V : key[i];              // last row this entry fills
-    if (lo <= hi && hi - lo < 8) {
-      for (uint32_t v = lo; v <= hi && v <= V; ++v) start[v] = i;
-    } else if (lo <= hi) {
-      const int b = atomicAdd(&nbig, 1);
-      big_lo[b] = lo;
-      big_hi[b] = hi;
-      big_at[b] = i;
+// Segment bounds of every id that occurs, from the sorted keys; also clears the
+// arrival counters.
+__global__ void __launch_bounds__(256) sort_bounds_kernel(const uint32_t* key, uint32_t n, uint32_t V, uint2* seg,
+                                                          uint32_t* arrivals, uint32_t n_arrivals) {
+  const uint32_t i = blockIdx.x * 256u + threadIdx.x;
+  for (uint32_t a = i; a < n_arrivals; a += gridDim.x * 256u) arrivals[a] = 0;
+  if (i >= n) return;
+  const uint32_t k = key[i];
+  if (k >= V) return;
+  if (i == 0 || key[i - 1] != k) seg[k].x = i;
+  if (i + 1 == n || key[i + 1] != k) seg[k].y = i + 1;
+}
+
+// Zeros of one row; aligned 16-byte stores between a scalar head and tail.
+__device__ __forceinline__ void zero_row(float* row, int d, int lane) {
+  const int head = min(d, (int)((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / 4);
+  if (lane < head) row[lane] = 0.0f;
+  float4* body = reinterpret_cast<float4*>(row + head);
+  const int n4 = (d - head) / 4;
+  for (int i = lane; i < n4; i += 32) body[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int t = head + n4 * 4 + lane;
+  if (t < d) row[t] = 0.0f;
+}
+
+// Rows that no id names, after a sort that cleared seg: one warp per row.
+__global__ void __launch_bounds__(256) zero_rows_kernel(const uint2* seg, uint32_t V, int d, float* dtable) {
+  const int lane = threadIdx.x & 31;
+  for (uint32_t v = blockIdx.x * 8 + (threadIdx.x >> 5); v < V; v += gridDim.x * 8)
+    if (seg[v].y == 0) zero_row(dtable + (size_t)v * d, d, lane);
+}
+
+// ---- one launch for up to kSmallMax ids: the first cluster sorts, the others zero
+struct SmallArgs {
+  KeysIn in;
+  uint32_t n, V;
+  int d, digit_bits, passes;   // of the sort
+  uint32_t* key;
+  uint32_t* pos;
+  uint2* seg;
+  uint32_t* arrivals;
+  uint32_t n_arrivals;
+  float* dtable;
+};
+
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t cta) {
+  uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p)), out;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(out) : "r"(a), "r"(cta));
+  return out;
+}
+__device__ __forceinline__ uint32_t ld_cluster(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_cluster(uint32_t a, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+__device__ __forceinline__ void cluster_barrier() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
+template <int IPT>
+struct SmallSmem {
+  uint16_t cnt[32][kRadix];              // per warp and digit; then the exclusive prefix over warps
+  uint32_t tot[kRadix];                  // this CTA's digit counts, read by the cluster
+  uint32_t base[kRadix];                 // first place of this CTA's keys of a digit
+  uint32_t key[kSmallThreads * IPT];     // this CTA's part of the order, written by the cluster
+  uint32_t pos[kSmallThreads * IPT];
+  uint32_t wsum[32];
+};
+
+template <int IPT>
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSmallThreads, 1)
+    sort_small_kernel(const SmallArgs A) {
+  extern __shared__ __align__(16) uint8_t raw[];
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  if (blockIdx.x >= kCluster) {
+    // ---- zero rows of a contiguous range of the table
+    uint32_t* bits = reinterpret_cast<uint32_t*>(raw);
+    const uint32_t nz = gridDim.x - kCluster, z = blockIdx.x - kCluster;
+    const uint32_t lo = (uint32_t)((unsigned long long)A.V * z / nz);
+    const uint32_t hi = (uint32_t)((unsigned long long)A.V * (z + 1) / nz);
+    for (uint32_t r0 = lo; r0 < hi; r0 += kZeroRange) {
+      const uint32_t nr = min(hi - r0, (uint32_t)kZeroRange), nw = (nr + 31) / 32;
+      for (uint32_t i = tid; i < nw; i += kSmallThreads) bits[i] = 0;
+      __syncthreads();
+      for (uint32_t i0 = tid; i0 < A.n; i0 += 8 * kSmallThreads) {
+        uint32_t k[8];                        // eight loads in flight
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const uint32_t i = i0 + q * kSmallThreads;
+          k[q] = i < A.n ? A.in.k(i) - r0 : 0xffffffffu;    // below r0 wraps to a large value
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (k[q] < nr) atomicOr(&bits[k[q] >> 5], 1u << (k[q] & 31));
+      }
+      __syncthreads();
+      for (uint32_t r = w; r < nr; r += 32)
+        if (!(bits[r >> 5] >> (r & 31) & 1)) zero_row(A.dtable + (size_t)(r0 + r) * A.d, A.d, lane);
+      __syncthreads();
+    }
+    return;
+  }
+  SmallSmem<IPT>& S = *reinterpret_cast<SmallSmem<IPT>*>(raw);
+  const uint32_t cta = blockIdx.x;
+  constexpr uint32_t kChunk = kSmallThreads * IPT;
+  const int bins = 1 << A.digit_bits;
+  const uint32_t first = cta * kChunk + w * (32 * IPT) + lane;
+  for (uint32_t i = cta * kSmallThreads + tid; i < A.n_arrivals; i += kCluster * kSmallThreads) A.arrivals[i] = 0;
+  uint32_t k[IPT], p[IPT], rank[IPT];
+#pragma unroll
+  for (int j = 0; j < IPT; ++j) {
+    const uint32_t i = first + j * 32;
+    k[j] = i < A.n ? A.in.k(i) : 0;
+    p[j] = i;
+  }
+  for (int pass = 0; pass < A.passes; ++pass) {
+    const int shift = pass * A.digit_bits;
+    for (int i = lane; i < bins / 2; i += 32) reinterpret_cast<uint32_t*>(S.cnt[w])[i] = 0;
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < IPT; ++j) {
+      const bool ok = first + j * 32 < A.n;     // the places behind the last id stay behind it
+      const uint32_t dg = ok ? (k[j] >> shift) & (bins - 1) : kRadix + lane;
+      const uint32_t same = __match_any_sync(0xffffffffu, dg);
+      const uint32_t before = __popc(same & ((1u << lane) - 1));
+      uint32_t c = 0;
+      if (ok) c = S.cnt[w][dg];
+      __syncwarp();
+      if (ok && before == 0) S.cnt[w][dg] = (uint16_t)(c + __popc(same));
+      __syncwarp();
+      rank[j] = c + before;
+    }
+    __syncthreads();
+    if (tid < bins) {
+      uint32_t run = 0;
+#pragma unroll 8
+      for (int q = 0; q < 32; ++q) {
+        const uint32_t c = S.cnt[q][tid];
+        S.cnt[q][tid] = (uint16_t)run;
+        run += c;
+      }
+      S.tot[tid] = run;
+    }
+    cluster_barrier();                          // every CTA's counts are there
+    uint32_t all = 0, before = 0;
+    if (tid < bins) {
+#pragma unroll
+      for (uint32_t c = 0; c < kCluster; ++c) {
+        const uint32_t t = ld_cluster(cluster_addr(&S.tot[tid], c));
+        if (c < cta) before += t;
+        all += t;
+      }
+    }
+    uint32_t x = all;                           // exclusive scan over the digits
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) S.wsum[w] = x;
+    __syncthreads();
+    if (w == 0) {
+      uint32_t t = S.wsum[lane];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, t, o);
+        if (lane >= o) t += y;
+      }
+      S.wsum[lane] = t;
+    }
+    __syncthreads();
+    if (tid < bins) S.base[tid] = (w ? S.wsum[w - 1] : 0) + x - all + before;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < IPT; ++j) {
+      if (first + j * 32 >= A.n) continue;
+      const uint32_t dg = (k[j] >> shift) & (bins - 1);
+      const uint32_t o = S.base[dg] + S.cnt[w][dg] + rank[j];
+      const uint32_t c = o / kChunk, at = o % kChunk;
+      st_cluster(cluster_addr(&S.key[at], c), k[j]);
+      st_cluster(cluster_addr(&S.pos[at], c), p[j]);
+    }
+    cluster_barrier();                          // the order of this pass is complete
+#pragma unroll
+    for (int j = 0; j < IPT; ++j) {
+      const uint32_t i = w * (32 * IPT) + lane + j * 32;
+      k[j] = S.key[i];
+      p[j] = S.pos[i];
     }
   }
-  __syncthreads();
-  for (int b = 0; b < nbig; ++b)
-    for (uint32_t v = big_lo[b] + threadIdx.x; v <= big_hi[b]; v += 256) start[v] = big_at[b];
+#pragma unroll
+  for (int j = 0; j < IPT; ++j) {
+    const uint32_t i = first + j * 32;
+    if (i >= A.n) continue;
+    A.key[i] = k[j];
+    A.pos[i] = p[j];
+    if (k[j] >= A.V) continue;
+    const uint32_t at = i % kChunk;
+    const uint32_t prev = i == 0 ? 0xffffffffu
+                                 : at ? S.key[at - 1] : ld_cluster(cluster_addr(&S.key[kChunk - 1], cta - 1));
+    const uint32_t next = i + 1 == A.n ? 0xffffffffu
+                                       : at + 1 < kChunk ? S.key[at + 1] : ld_cluster(cluster_addr(&S.key[0], cta + 1));
+    if (prev != k[j]) A.seg[k[j]].x = i;
+    if (next != k[j]) A.seg[k[j]].y = i + 1;
+  }
+  cluster_barrier();                            // no CTA leaves while another reads its keys
 }
 
 // ---------------------------------------------------------------- sums
 struct SumArgs {
   const void* dout;
   float* dtable;
-  const uint32_t* start;
+  const uint2* seg;
   const uint32_t* key;
   const uint32_t* pos;
   float* part;            // [windows][2][d]
@@ -337,163 +529,293 @@ struct SumArgs {
   float scale;
   uint32_t window, n_windows;
   int col_tiles, tpr;
-  int hot_blocks;         // leading blocks: one (window, column tile) each
+  int v32;   // rows of dtable and part are 32-byte aligned
 };
 
-// Column layout of one thread: VEC: 8 consecutive columns; else 4 columns, tpr apart.
-template <typename T, bool VEC>
-struct Cols {
-  static constexpr int C = VEC ? 8 : 4;
-  static __device__ __forceinline__ int first(int tile, int lane, int tpr) {
-    return tile * tpr * C + (VEC ? lane * C : lane);
-  }
-  static __device__ __forceinline__ void add(const T* row, int c0, int d, int tpr, float* acc) {
-    float f[C];
-    get(row, c0, d, tpr, f);
-#pragma unroll
-    for (int i = 0; i < C; ++i) acc[i] += f[i];
-  }
-  static __device__ __forceinline__ void get(const T* row, int c0, int d, int tpr, float* f) {
-    if constexpr (VEC) {
-      if (c0 < d) {
-        Vec16<T>::load(row + c0, f);
-        if (sizeof(T) == 4) Vec16<T>::load(row + c0 + 4, f + 4);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < C; ++i) f[i] = c0 + i * tpr < d ? ld_elem(row, c0 + i * tpr) : 0.0f;
-    }
-  }
-  static __device__ __forceinline__ void put(float* row, int c0, int d, int tpr, const float* f) {
-    if constexpr (VEC) {
-      if (c0 < d) {
-        store_vec<8>(row + c0, f);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < C; ++i)
-        if (c0 + i * tpr < d) row[c0 + i * tpr] = f[i];
-    }
-  }
-};
+// One thread's columns of a row.  VEC: NCH chunks of 16 bytes, tpr chunks apart
+// (16 columns), each copied to a slot of shared memory that only this thread
+// reads (cp.async, no barrier); fp32 rows of any width: 8 columns, tpr apart, the
+// same way in 4-byte copies; bf16 rows of odd width: 4 columns through
+// registers.  Keys, addresses and comparisons are paid once per row and thread,
+// and eight columns a thread spent most of the kernel on them: 16384 bf16 rows
+// of 2048 took 41 us with 8 columns a thread, 33 with 16, and 24 with 32-byte
+// stores (two 16-byte ones write each sector in halves).  Rows are fetched in
+// batches of kBatch, two batches in flight.
+constexpr int kBatch = 4;
 
-// Sum of sorted entries [b, e) at this thread's columns, ascending, four rows
-// of dout in flight.
-template <typename T, bool VEC>
-__device__ __forceinline__ void sum_entries(const SumArgs& A, uint32_t b, uint32_t e, int c0, float* acc) {
-  using L = Cols<T, VEC>;
-  const T* dout = static_cast<const T*>(A.dout);
-#pragma unroll
-  for (int i = 0; i < L::C; ++i) acc[i] = 0.0f;
-  uint32_t j = b;
-  for (; j + 4 <= e; j += 4) {
-    float f[4][L::C];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) L::get(dout + (size_t)A.pos[j + q] * A.d, c0, A.d, A.tpr, f[q]);
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-#pragma unroll
-      for (int i = 0; i < L::C; ++i) acc[i] += f[q][i];
-  }
-  for (; j < e; ++j) L::add(dout + (size_t)A.pos[j] * A.d, c0, A.d, A.tpr, acc);
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(256) embed_sum_kernel(const SumArgs A) {
-  using L = Cols<T, VEC>;
-  const int lane = threadIdx.x % A.tpr, sub = threadIdx.x / A.tpr, rpb = 256 / A.tpr;
-  if ((int)blockIdx.x < A.hot_blocks) {
-    // ---- one window of the sorted order, for the hot segments it meets
-    __shared__ int last;
-    const uint32_t j = blockIdx.x / A.col_tiles;
-    const int tile = blockIdx.x % A.col_tiles;
-    const uint32_t wb = j * A.window, we = min(A.n, wb + A.window);
-    const uint32_t k0 = A.key[wb], k1 = A.key[we - 1];
-    for (int slot = 0; slot < 2; ++slot) {
-      const uint32_t k = slot ? k1 : k0;
-      if (k >= A.V || (slot && k1 == k0)) continue;
-      const uint32_t sb = A.start[k], se = A.start[k + 1];
-      if (se - sb <= 2 * A.window) continue;
-      const int c0 = L::first(tile, lane, A.tpr);
-      float acc[L::C];
-      if (sub == 0) {
-        sum_entries<T, VEC>(A, max(sb, wb), min(se, we), c0, acc);
-        L::put(A.part + ((size_t)j * 2 + slot) * A.d, c0, A.d, A.tpr, acc);
-      }
-      __threadfence();
-      __syncthreads();
-      const uint32_t w0 = sb / A.window, w1 = (se - 1) / A.window;
-      if (threadIdx.x == 0)
-        last = atomicAdd(&A.arrivals[(size_t)w0 * A.col_tiles + tile], 1u) == w1 - w0;
-      __syncthreads();
-      if (last && sub == 0) {
-        // every window's partial is there: add them in order
-        __threadfence();
+struct Fetch {   // VEC
+  static constexpr int E = 16 / sizeof(T), NCH = 16 / E, C = 16;
+  static constexpr int SMEM = 2 * kBatch * NCH * 256 * 16;
+  __device__ __forceinline__ void start(uint4* ring, int slot, const T* row, int lane, int d, int tpr) {
 #pragma unroll
-        for (int i = 0; i < L::C; ++i) acc[i] = 0.0f;
-        for (uint32_t w = w0; w <= w1; ++w) {
-          const int sl = (w == w0 && sb % A.window) ? 1 : 0;
-          const float* p = A.part + ((size_t)w * 2 + sl) * A.d;
-          float f[L::C];
-          if constexpr (VEC) {
-            if (c0 < A.d) {
-              const float4 a = __ldcg(reinterpret_cast<const float4*>(p + c0));
-              const float4 b = __ldcg(reinterpret_cast<const float4*>(p + c0) + 1);
-              f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-              f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < L::C; ++i) f[i] = c0 + i * A.tpr < A.d ? __ldcg(p + c0 + i * A.tpr) : 0.0f;
-          }
-#pragma unroll
-          for (int i = 0; i < L::C; ++i) acc[i] += f[i];
-        }
-#pragma unroll
-        for (int i = 0; i < L::C; ++i) acc[i] *= A.scale;
-        L::put(A.dtable + (size_t)k * A.d, c0, A.d, A.tpr, acc);
-      }
-      __syncthreads();
+    for (int i = 0; i < NCH; ++i) {
+      const int c = (lane + i * tpr) * E;
+      if (c < d)
+        cp_async16(static_cast<uint32_t>(__cvta_generic_to_shared(ring + (slot * NCH + i) * 256 + threadIdx.x)),
+                   row + c);
     }
-    return;
   }
-  // ---- rows of the table, each written once (hot rows by the blocks above)
-  const long long items = (long long)A.V * A.col_tiles;
-  const long long stride = (long long)(gridDim.x - A.hot_blocks) * rpb;
-  for (long long it = (long long)(blockIdx.x - A.hot_blocks) * rpb + sub; it < items; it += stride) {
-    const uint32_t v = (uint32_t)(it / A.col_tiles);
-    const int c0 = L::first((int)(it % A.col_tiles), lane, A.tpr);
-    const uint32_t b = A.start[v], e = A.start[v + 1];
-    if (e - b > 2 * A.window) continue;
-    float acc[L::C];
-    sum_entries<T, VEC>(A, b, e, c0, acc);
+  // columns beyond d add what their slot holds; they are not stored
+  __device__ __forceinline__ void add(const uint4* ring, int slot, float* acc) const {
 #pragma unroll
-    for (int i = 0; i < L::C; ++i) acc[i] *= A.scale;
-    L::put(A.dtable + (size_t)v * A.d, c0, A.d, A.tpr, acc);
+    for (int i = 0; i < NCH; ++i) {
+      const uint4 u = ring[(slot * NCH + i) * 256 + threadIdx.x];
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (E == 8) {
+          acc[i * 8 + 2 * q] += __uint_as_float(w[q] << 16);
+          acc[i * 8 + 2 * q + 1] += __uint_as_float(w[q] & 0xffff0000u);
+        } else {
+          acc[i * 4 + q] += __uint_as_float(w[q]);
+        }
+      }
+    }
+  }
+  static __device__ __forceinline__ void put(float* row, int lane, int d, int tpr, const float* f, float scale,
+                                             int v32) {
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+      const int c = (lane + i * tpr) * E;
+      if (c < d) {
+        float g[E];
+#pragma unroll
+        for (int q = 0; q < E; ++q) g[q] = f[i * E + q] * scale;
+        // 16-byte stores 32 bytes apart would be two half-written sectors a lane
+        if (E == 8 && v32) st8f32(row + c, g);
+        else store_vec<E>(row + c, g);
+      }
+    }
+  }
+  static __device__ __forceinline__ void get(const float* row, int lane, int d, int tpr, float* f) {
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+      const int c = (lane + i * tpr) * E;
+      if (c < d) {
+#pragma unroll
+        for (int q = 0; q < E / 4; ++q) {
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(row + c) + q);
+          f[i * E + 4 * q] = v.x; f[i * E + 4 * q + 1] = v.y; f[i * E + 4 * q + 2] = v.z; f[i * E + 4 * q + 3] = v.w;
+        }
+      }
+    }
+  }
+};
+template <>
+struct Fetch<float, false> {   // 4-byte copies, 8 columns
+  static constexpr int C = 8, SMEM = 2 * kBatch * C * 256 * 4;
+  __device__ __forceinline__ void start(uint4* ring, int slot, const float* row, int lane, int d, int tpr) {
+    const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + (slot * C * 256 + threadIdx.x) * 4;
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+      if (lane + i * tpr < d)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst + i * 1024), "l"(row + lane + i * tpr)
+                     : "memory");
+  }
+  __device__ __forceinline__ void add(const uint4* ring, int slot, float* acc) const {
+    const float* f = reinterpret_cast<const float*>(ring) + slot * C * 256 + threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < C; ++i) acc[i] += f[i * 256];
+  }
+  static __device__ __forceinline__ void put(float* row, int lane, int d, int tpr, const float* f, float scale, int) {
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+      if (lane + i * tpr < d) row[lane + i * tpr] = f[i] * scale;
+  }
+  static __device__ __forceinline__ void get(const float* row, int lane, int d, int tpr, float* f) {
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+      if (lane + i * tpr < d) f[i] = __ldcg(row + lane + i * tpr);
+  }
+};
+template <>
+struct Fetch<bf16, false> {
+  static constexpr int C = 4, SMEM = 0;
+  float f[2 * kBatch][C];
+  __device__ __forceinline__ void start(uint4*, int slot, const bf16* row, int lane, int d, int tpr) {
+#pragma unroll
+    for (int i = 0; i < C; ++i) f[slot][i] = lane + i * tpr < d ? ld_elem(row, lane + i * tpr) : 0.0f;
+  }
+  __device__ __forceinline__ void add(const uint4*, int slot, float* acc) const {
+#pragma unroll
+    for (int i = 0; i < C; ++i) acc[i] += f[slot][i];
+  }
+  static __device__ __forceinline__ void put(float* row, int lane, int d, int tpr, const float* f, float scale, int) {
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+      if (lane + i * tpr < d) row[lane + i * tpr] = f[i] * scale;
+  }
+  static __device__ __forceinline__ void get(const float* row, int lane, int d, int tpr, float* f) {
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+      if (lane + i * tpr < d) f[i] = __ldcg(row + lane + i * tpr);
+  }
+};
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256, 2) embed_sum_kernel(const SumArgs A) {
+  using L = Fetch<T, VEC>;
+  constexpr int C = L::C, B = kBatch, kAhead = 2;
+  extern __shared__ __align__(16) uint4 ring[];
+  __shared__ int last[2][256];
+  const int lane = threadIdx.x % A.tpr, sub = threadIdx.x / A.tpr, rpb = 256 / A.tpr;
+  const uint32_t items = A.n_windows * (uint32_t)A.col_tiles;
+  for (uint32_t base = blockIdx.x * rpb; base < items; base += gridDim.x * rpb) {
+    const uint32_t it = base + sub;
+    const uint32_t win = it / A.col_tiles;
+    const int tile = it % A.col_tiles;
+    // this tile's columns: pointers moved by c0, width d
+    const int c0 = tile * A.tpr * C, d = A.d - c0;
+    const T* dout = static_cast<const T*>(A.dout) + c0;
+    float* dtable = A.dtable + c0;
+    float* part = A.part + (size_t)win * 2 * A.d + c0;
+    uint32_t kfirst = A.V, klast = A.V;
+    uint2 sfirst = {0, 0}, slast = {0, 0};
+    bool left = false, right = false;
+    if (it < items) {
+      uint32_t wb = win * A.window, we = min(A.n, wb + A.window);
+      kfirst = A.key[wb];
+      klast = A.key[we - 1];
+      const uint32_t kprev = wb > 0 ? A.key[wb - 1] : 0xffffffffu, knext = we < A.n ? A.key[we] : 0xffffffffu;
+      left = kprev == kfirst && kfirst < A.V;       // the first sum began in an earlier window
+      right = knext == klast && klast < A.V;        // the last one goes on in a later one
+      if (left) sfirst = A.seg[kfirst];
+      if (right) slast = A.seg[klast];
+      // a segment of at most a window's length belongs to the window it begins
+      // in; only longer ones are cut
+      if (right && slast.y - slast.x <= A.window) {
+        right = false;
+        if (slast.x >= wb) we = slast.y;
+      }
+      if (left && sfirst.y - sfirst.x <= A.window) {
+        left = false;
+        wb = min(sfirst.y, we);
+      }
+      uint32_t cur = A.V;
+      bool from_left = left;
+      float acc[C];
+      L rows;
+      uint32_t kk[2][B];
+      // keys and fetches of the batch at j (a multiple of 4) into half h
+      auto fetch = [&](uint32_t j, int h) {
+        if (j < we) {
+          const uint4 k4 = __ldg(reinterpret_cast<const uint4*>(A.key + j));
+          const uint4 p4 = __ldg(reinterpret_cast<const uint4*>(A.pos + j));
+          const uint32_t kq[4] = {k4.x, k4.y, k4.z, k4.w}, pq[4] = {p4.x, p4.y, p4.z, p4.w};
+#pragma unroll
+          for (int q = 0; q < B; ++q) {
+            kk[h][q] = j + q >= wb && j + q < we ? kq[q] : A.V;
+            if (kk[h][q] < A.V) rows.start(ring, h * B + q, dout + (size_t)pq[q] * A.d, lane, d, A.tpr);
+          }
+        }
+        if (L::SMEM) asm volatile("cp.async.commit_group;" ::: "memory");
+      };
+      auto flush = [&] {
+        if (cur < A.V) {
+          if (from_left) L::put(part, lane, d, A.tpr, acc, 1.0f, A.v32);
+          else L::put(dtable + (size_t)cur * A.d, lane, d, A.tpr, acc, A.scale, A.v32);
+          from_left = false;
+        }
+      };
+      const uint32_t j0 = wb & ~3u;
+      fetch(j0, 0);
+      fetch(j0 + B, 1);
+      for (uint32_t j = j0; j < we; j += 2 * B) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (j + h * B >= we) break;
+          if (L::SMEM) asm volatile("cp.async.wait_group 1;" ::: "memory");   // all but the youngest batch
+#pragma unroll
+          for (int q = 0; q < B; ++q) {
+            const uint32_t k = kk[h][q];
+            if (k >= A.V) continue;      // outside the window, or padding (sorted behind every id)
+            if (k != cur) {
+              flush();
+#pragma unroll
+              for (int i = 0; i < C; ++i) acc[i] = 0.0f;
+              cur = k;
+            }
+            rows.add(ring, h * B + q, acc);
+          }
+          fetch(j + (2 + h) * B, h);
+        }
+      }
+      if (L::SMEM) asm volatile("cp.async.wait_group 0;" ::: "memory");
+      if (cur < A.V) {
+        if (right && !from_left) L::put(part + A.d, lane, d, A.tpr, acc, 1.0f, A.v32);
+        else flush();
+      }
+    }
+    // ---- sums that cross windows: slot 0 came from the left, slot 1 begins here
+    const bool has[2] = {left, right && !(left && klast == kfirst)};
+    if (!__syncthreads_or(has[0] || has[1])) continue;
+    __threadfence();
+    __syncthreads();
+    if (lane == 0) {
+#pragma unroll
+      for (int slot = 0; slot < 2; ++slot) {
+        int l = 0;
+        if (has[slot]) {
+          const uint2 s = slot ? slast : sfirst;
+          const uint32_t w0 = s.x / A.window, w1 = (s.y - 1) / A.window;
+          l = atomicAdd(&A.arrivals[(size_t)w0 * A.col_tiles + tile], 1u) == w1 - w0;
+        }
+        last[slot][sub] = l;
+      }
+    }
+    __syncthreads();
+    for (int slot = 0; slot < 2; ++slot) {
+      if (!last[slot][sub]) continue;
+      __threadfence();
+      const uint32_t k = slot ? klast : kfirst;
+      const uint2 s = slot ? slast : sfirst;
+      const uint32_t w0 = s.x / A.window, w1 = (s.y - 1) / A.window;
+      float acc[C];
+#pragma unroll
+      for (int i = 0; i < C; ++i) acc[i] = 0.0f;
+      for (uint32_t w = w0; w <= w1; w += kAhead) {
+        float f[kAhead][C];
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q)
+          if (w + q <= w1)
+            L::get(A.part + ((size_t)(w + q) * 2 + (w + q == w0 ? 1 : 0)) * A.d + c0, lane, d, A.tpr, f[q]);
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q) {
+          if (w + q > w1) continue;
+#pragma unroll
+          for (int i = 0; i < C; ++i) acc[i] += f[q][i];
+        }
+      }
+      L::put(dtable + (size_t)k * A.d, lane, d, A.tpr, acc, A.scale, A.v32);
+    }
+    __syncthreads();
   }
 }
 
 // ---------------------------------------------------------------- workspace
 struct Ws {
-  size_t key[2], pos[2], start, counts, arrivals, part, bytes;
+  size_t key[2], pos[2], seg, counts, arrivals, part, bytes;
   uint32_t window, n_windows, sort_blocks;
-  int tpr, col_tiles, passes;
+  int col_tiles, passes, digit_bits;
 };
 
 Ws ws_layout(long long n, int V, int d) {
   Ws w = {};
-  // d % 8 decides the column layout; both cover at most 256 threads a row
-  const bool vec = d % 8 == 0;
-  const int per = vec ? 8 : 4;
-  w.tpr = threads_per_row((d + per - 1) / per);
-  w.col_tiles = (d + w.tpr * per - 1) / (w.tpr * per);
-  long long win = (n + kMaxWindows - 1) / kMaxWindows;
-  w.window = (uint32_t)(win > kWindowMin ? win : kWindowMin);
+  w.col_tiles = (d + 1023) / 1024;    // at most: 256 threads of 4 columns or more
+  long long win = ((n + kWindows - 1) / kWindows + 7) / 8 * 8;
+  w.window = (uint32_t)(win > 8 ? win : 8);
   w.n_windows = (uint32_t)((n + w.window - 1) / w.window);
   w.sort_blocks = (uint32_t)((n + kSortTile - 1) / kSortTile);
-  int bits = 1;
-  while (((long long)V >> bits) != 0) ++bits;
-  w.passes = (bits + kRadixBits - 1) / kRadixBits;
+  int key_bits = 1;
+  while (((long long)V >> key_bits) != 0) ++key_bits;     // keys are 0 .. V
+  w.passes = (key_bits + kRadixBits - 1) / kRadixBits;
+  w.digit_bits = (key_bits + w.passes - 1) / w.passes;
+  if (w.digit_bits < 5) w.digit_bits = 5;
   size_t top = 0;
   auto take = [&](size_t bytes) {
     const size_t o = top;
@@ -504,7 +826,7 @@ Ws ws_layout(long long n, int V, int d) {
     w.key[i] = take((size_t)n * 4);
     w.pos[i] = take((size_t)n * 4);
   }
-  w.start = take(((size_t)V + 1) * 4);
+  w.seg = take((size_t)V * 8);
   w.counts = take((size_t)kRadix * w.sort_blocks * 4);
   w.arrivals = take((size_t)w.n_windows * w.col_tiles * 4);
   w.part = take((size_t)w.n_windows * 2 * d * 4);
@@ -529,16 +851,61 @@ cudaError_t embedding_fwd(DType tt, const void* table, int V, int d, int id64, c
 #undef MG_EMBED_FWD
 }
 
-cudaError_t embedding_bwd_sort(int id64, const void* ids, long long n, int V, int d, void* workspace,
+template <int IPT>
+static cudaError_t sort_small(const SmallArgs& A, cudaStream_t s) {
+  constexpr size_t smem = sizeof(SmallSmem<IPT>) > kZeroRange / 8 ? sizeof(SmallSmem<IPT>) : kZeroRange / 8;
+  static const cudaError_t attr =
+      cudaFuncSetAttribute(sort_small_kernel<IPT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (attr != cudaSuccess) return attr;
+  // clusters that run at once (a cluster's CTAs share a GPC, so some SMs may
+  // stay out): a later one would start when the first zeroing ones end
+  static const int slots = [&] {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kCluster * (device_sms() / kCluster));
+    cfg.blockDim = dim3(kSmallThreads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = kCluster;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    int c = 0;
+    if (cudaOccupancyMaxActiveClusters(&c, sort_small_kernel<IPT>, &cfg) != cudaSuccess || c < 2) {
+      cudaGetLastError();
+      c = 2;
+    }
+    return c;
+  }();
+  // a block's rows are worth its scan of the ids only if they are many
+  const long long most = slots - 1, rows = (long long)A.V * A.d / (kCluster * 65536);
+  const unsigned grid = kCluster + kCluster * (unsigned)(rows < 1 ? 1 : rows < most ? rows : most);
+  sort_small_kernel<IPT><<<grid, kSmallThreads, smem, s>>>(A);
+  return cudaGetLastError();
+}
+
+cudaError_t embedding_bwd_sort(int id64, const void* ids, long long n, int V, int d, float* dtable, void* workspace,
                                cudaStream_t s) {
   const Ws w = ws_layout(n, V, d);
   char* base = static_cast<char*>(workspace);
   auto u32 = [&](size_t off) { return reinterpret_cast<uint32_t*>(base + off); };
+  uint2* seg = reinterpret_cast<uint2*>(base + w.seg);
+  const uint32_t n_arrivals = w.n_windows * (uint32_t)w.col_tiles;
   KeysIn in{ids, id64, V, nullptr, nullptr};
-  for (int p = 0; p < w.passes && n > 0; ++p) {
+  if (n <= kSmallMax) {
+    SmallArgs A{in, (uint32_t)n, (uint32_t)V, d, w.digit_bits, w.passes, u32(w.key[0]), u32(w.pos[0]), seg,
+                u32(w.arrivals), n_arrivals, dtable};
+    const long long per_cluster = kCluster * kSmallThreads;
+    if (n <= per_cluster) return sort_small<1>(A, s);
+    if (n <= 2 * per_cluster) return sort_small<2>(A, s);
+    if (n <= 4 * per_cluster) return sort_small<4>(A, s);
+    return sort_small<kSmallItems>(A, s);
+  }
+  cudaError_t e = cudaMemsetAsync(seg, 0, (size_t)V * sizeof(uint2), s);
+  if (e != cudaSuccess) return e;
+  for (int p = 0; p < w.passes; ++p) {
     const int shift = p * kRadixBits;
-    // the last pass writes buffer 0
-    const int dst = (w.passes - 1 - p) & 1;
+    const int dst = (w.passes - 1 - p) & 1;   // the last pass writes buffer 0
     sort_count_kernel<<<w.sort_blocks, kSortThreads, 0, s>>>(in, (uint32_t)n, shift, u32(w.counts));
     sort_scan_kernel<<<1, 1024, 0, s>>>(u32(w.counts), (uint32_t)kRadix * w.sort_blocks);
     sort_scatter_kernel<<<w.sort_blocks, kSortThreads, 0, s>>>(in, (uint32_t)n, shift, u32(w.counts),
@@ -546,20 +913,32 @@ cudaError_t embedding_bwd_sort(int id64, const void* ids, long long n, int V, in
     in.key = u32(w.key[dst]);
     in.pos = u32(w.pos[dst]);
   }
-  const unsigned grid = (unsigned)((n + 1 + 255) / 256);
-  sort_bounds_kernel<<<grid, 256, 0, s>>>(u32(w.key[0]), (uint32_t)n, (uint32_t)V, u32(w.start),
-                                          u32(w.arrivals), w.n_windows * (uint32_t)w.col_tiles);
+  sort_bounds_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(u32(w.key[0]), (uint32_t)n, (uint32_t)V, seg,
+                                                                 u32(w.arrivals), n_arrivals);
+  const long long zblocks = ((long long)V + 7) / 8;
+  zero_rows_kernel<<<(unsigned)(zblocks < 152 * 8 ? zblocks : 152 * 8), 256, 0, s>>>(seg, (uint32_t)V, d, dtable);
+  return cudaGetLastError();
+}
+
+template <typename T, bool VEC>
+static cudaError_t sum_launch(const SumArgs& A, unsigned grid, cudaStream_t s) {
+  constexpr int smem = Fetch<T, VEC>::SMEM;
+  static const cudaError_t attr = cudaFuncSetAttribute(embed_sum_kernel<T, VEC>,
+                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (attr != cudaSuccess) return attr;
+  embed_sum_kernel<T, VEC><<<grid, 256, smem, s>>>(A);
   return cudaGetLastError();
 }
 
 cudaError_t embedding_bwd_sum(DType t, const void* dout, long long n, int V, int d, float scale, float* dtable,
                               void* workspace, cudaStream_t s) {
+  if (n == 0) return cudaSuccess;
   const Ws w = ws_layout(n, V, d);
   char* base = static_cast<char*>(workspace);
   SumArgs A;
   A.dout = dout;
   A.dtable = dtable;
-  A.start = reinterpret_cast<uint32_t*>(base + w.start);
+  A.seg = reinterpret_cast<uint2*>(base + w.seg);
   A.key = reinterpret_cast<uint32_t*>(base + w.key[0]);
   A.pos = reinterpret_cast<uint32_t*>(base + w.pos[0]);
   A.part = reinterpret_cast<float*>(base + w.part);
@@ -570,23 +949,17 @@ cudaError_t embedding_bwd_sum(DType t, const void* dout, long long n, int V, int
   A.scale = scale;
   A.window = w.window;
   A.n_windows = w.n_windows;
-  A.col_tiles = w.col_tiles;
-  A.tpr = w.tpr;
-  // a segment can be hot only if all tokens could fill one
-  A.hot_blocks = n > 2ll * w.window ? (int)w.n_windows * w.col_tiles : 0;
-  const int rpb = 256 / w.tpr;
-  const long long items = ((long long)V * w.col_tiles + rpb - 1) / rpb;
-  const long long rows_grid = items < 152 * 16 ? items : 152 * 16;
-  const unsigned grid = (unsigned)(rows_grid + A.hot_blocks);
+  // columns a thread: see Fetch; at most 256 threads (a block) a row
+  const int per = d % 8 == 0 ? 16 : t == DT_F32 ? 8 : 4;
+  A.tpr = threads_per_row((d + per - 1) / per);
+  A.col_tiles = (d + A.tpr * per - 1) / (A.tpr * per);
+  A.v32 = (reinterpret_cast<uintptr_t>(dtable) & 31) == 0 && (reinterpret_cast<uintptr_t>(A.part) & 31) == 0;
+  const int rpb = 256 / A.tpr;
+  const long long blocks = ((long long)w.n_windows * A.col_tiles + rpb - 1) / rpb;
+  const unsigned grid = (unsigned)(blocks < 152 * 16 ? blocks : 152 * 16);
   const bool vec = d % 8 == 0;
-  if (t == DT_F32) {
-    if (vec) embed_sum_kernel<float, true><<<grid, 256, 0, s>>>(A);
-    else embed_sum_kernel<float, false><<<grid, 256, 0, s>>>(A);
-  } else {
-    if (vec) embed_sum_kernel<bf16, true><<<grid, 256, 0, s>>>(A);
-    else embed_sum_kernel<bf16, false><<<grid, 256, 0, s>>>(A);
-  }
-  return cudaGetLastError();
+  if (t == DT_F32) return vec ? sum_launch<float, true>(A, grid, s) : sum_launch<float, false>(A, grid, s);
+  return vec ? sum_launch<bf16, true>(A, grid, s) : sum_launch<bf16, false>(A, grid, s);
 }
 
 }  // namespace mg
@@ -642,7 +1015,7 @@ extern "C" mg_status mg_embedding_backward(int dtype, const void* dout, int voca
   if (workspace_bytes < need)
     return op_fail(MG_ERR_INVALID_ARG, "%s: the workspace needs %zu bytes, %zu given", fn, need, workspace_bytes);
   if ((st = mg::op_begin(fn, {{dout, 16}, {ids, id_kind ? 8u : 4u}, {dtable, 16}, {workspace, 16}})) != MG_OK) return st;
-  cudaError_t e = mg::embedding_bwd_sort(id_kind, ids, n, vocab, dim, workspace, (cudaStream_t)stream);
+  cudaError_t e = mg::embedding_bwd_sort(id_kind, ids, n, vocab, dim, dtable, workspace, (cudaStream_t)stream);
   if (e == cudaSuccess)
     e = mg::embedding_bwd_sum((mg::DType)dtype, dout, n, vocab, dim, scale, dtable, workspace,
                               (cudaStream_t)stream);

@@ -169,12 +169,13 @@ cudaError_t cast_shadow(const Chunk* chunks, int n_chunks, const float* p, void*
 // out[i] = scale * table[id_i], 0 for an id outside [0, V); id64: int64 ids.
 cudaError_t embedding_fwd(DType tt, const void* table, int V, int d, int id64, const void* ids,
                           long long n, float scale, DType ot, void* out, cudaStream_t s);
-// The gradient in two parts, so that the sort of the ids (which needs nothing
-// of the backward pass) can run early: positions sorted by id in workspace
-// (embedding_ws_bytes), then every row of dtable written once.
+// The gradient in two parts, so that the first (which needs nothing of the
+// backward pass) can run early: positions sorted by id in workspace
+// (embedding_ws_bytes) and the rows of dtable that no id names zeroed; then the
+// rows of the ids that occur, each written once.
 size_t embedding_ws_bytes(long long n, int V, int d);
-cudaError_t embedding_bwd_sort(int id64, const void* ids, long long n, int V, int d, void* workspace,
-                               cudaStream_t s);
+cudaError_t embedding_bwd_sort(int id64, const void* ids, long long n, int V, int d, float* dtable,
+                               void* workspace, cudaStream_t s);
 cudaError_t embedding_bwd_sum(DType t, const void* dout, long long n, int V, int d, float scale,
                               float* dtable, void* workspace, cudaStream_t s);
 
