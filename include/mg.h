@@ -380,7 +380,7 @@ mg_status mg_grouped_linear_backward_weight(int dtype, const void* x, const void
  * values go: out[i], or in place where out is NULL or out[i] == grads[i].
  * Memory that is written may not overlap any other tensor of the list
  * (MG_ERR_INVALID_ARG).  counts[i] = 0 is allowed.  Creation copies the table
- * to the device and allocates a few bytes per 16384 elements; the list is
+ * to the device and allocates 32 bytes per 32 KB of gradients; the list is
  * bound to the current device, and like a plan is used by one stream at a
  * time.
  * mg_grad_list_clip: stats[0] = norm = sqrt(sum of all squares), stats[1] =
@@ -389,7 +389,8 @@ mg_status mg_grouped_linear_backward_weight(int dtype, const void* x, const void
  * is.  A gradient that holds NaN or infinity gives such a norm and c = 1: the
  * gradients keep their bits for the caller to find.  (Finite gradients whose
  * norm is beyond fp32's range have stats[0] = infinity and are clipped.)
- * max_norm >= 0; INFINITY only measures. */
+ * max_norm >= 0; INFINITY only measures.  A bounded device-side wait that gave
+ * up (never seen) sets stats to NaN; the outputs are then partly written. */
 typedef struct mg_grad_list mg_grad_list;
 mg_status mg_grad_list_create(int n, const void* const* grads, void* const* out,
                               const size_t* counts, const int* dtypes, mg_grad_list** list);

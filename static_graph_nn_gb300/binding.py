@@ -304,18 +304,30 @@ def ffma_peak(stream=None) -> tuple[float, float]:
 # Tensors are dense torch tensors on the current device; shapes and types are
 # checked here and refused with an MGError before the library is called.
 
-_DTYPES = {"torch.float32": 0, "torch.bfloat16": 1}
-_ID_KINDS = {"torch.int32": 0, "torch.int64": 1}
+_types = None
+
+
+def _type_tables():
+    """(dtype codes, id kinds, float32, int32), by torch's dtype objects; torch is
+    imported on first use."""
+    global _types
+    if _types is None:
+        import torch
+        _types = ({torch.float32: 0, torch.bfloat16: 1}, {torch.int32: 0, torch.int64: 1}, torch.float32,
+                  torch.int32)
+    return _types
 
 
 def _refuse(msg: str, status: int = MG_ERR_INVALID_ARG):
     raise MGError(status, msg)
 
 
-def _code(t, name: str, table: dict = _DTYPES) -> int:
-    k = table.get(str(t.dtype))
+def _code(t, name: str, table: dict | None = None) -> int:
+    if table is None:
+        table = _type_tables()[0]
+    k = table.get(t.dtype)
     if k is None:
-        _refuse(f"{name} must be one of {', '.join(sorted(table))}, not {t.dtype}")
+        _refuse(f"{name} must be one of {', '.join(sorted(map(str, table)))}, not {t.dtype}")
     return k
 
 
@@ -324,7 +336,7 @@ def _dense(t, name: str, shape: tuple | None = None):
         _refuse(f"{name} must be contiguous (strides {tuple(t.stride())})")
     if not t.is_cuda:
         _refuse(f"{name} must be a CUDA tensor")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         _refuse(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}", MG_ERR_SHAPE)
 
 
@@ -348,9 +360,9 @@ def embedding_forward(table, ids, out, scale: float = 1.0, stream=None):
     v, d = table.shape
     _dense(table, "table")
     _dense(ids, "ids")
-    _dense(out, "out", tuple(ids.shape) + (d,))
+    _dense(out, "out", ids.shape + (d,))
     _status(load().mg_embedding_forward(_code(table, "table"), _ptr(table), v, d,
-                                        _code(ids, "ids", _ID_KINDS), _ptr(ids), ids.numel(), scale,
+                                        _code(ids, "ids", _type_tables()[1]), _ptr(ids), ids.numel(), scale,
                                         _code(out, "out"), _ptr(out), _stream(stream)))
 
 
@@ -358,17 +370,17 @@ def embedding_backward(dout, ids, dtable, workspace, scale: float = 1.0, stream=
     """dtable[v] = scale * sum of dout[i] over ids[i] == v; every row of dtable is
     written.  dout [*ids.shape, dim] fp32 or bf16, dtable [vocab, dim] fp32,
     workspace a byte tensor of embedding_workspace_bytes."""
-    if dtable.dim() != 2 or str(dtable.dtype) != "torch.float32":
+    if dtable.dim() != 2 or dtable.dtype != _type_tables()[2]:
         _refuse("dtable must be [vocab, dim] float32", MG_ERR_SHAPE)
     v, d = dtable.shape
     _dense(dtable, "dtable")
     _dense(ids, "ids")
-    _dense(dout, "dout", tuple(ids.shape) + (d,))
+    _dense(dout, "dout", ids.shape + (d,))
     _dense(workspace, "workspace")
     _status(load().mg_embedding_backward(_code(dout, "dout"), _ptr(dout), v, d,
-                                         _code(ids, "ids", _ID_KINDS), _ptr(ids), ids.numel(), scale,
+                                         _code(ids, "ids", _type_tables()[1]), _ptr(ids), ids.numel(), scale,
                                          _ptr(dtable), _ptr(workspace),
-                                         workspace.numel() * workspace.element_size(),
+                                         workspace.nbytes,
                                          _stream(stream)))
 
 
@@ -381,11 +393,11 @@ def _grouped_args(rows_t, name, offsets, groups, workspace):
     if rows_t.dim() != 2:
         _refuse(f"{name} must be two-dimensional", MG_ERR_SHAPE)
     _dense(rows_t, name)
-    if str(offsets.dtype) != "torch.int32":
+    if offsets.dtype != _type_tables()[3]:
         _refuse("offsets must be int32")
     _dense(offsets, "offsets", (groups + 1,))
     _dense(workspace, "workspace")
-    return workspace.numel() * workspace.element_size()
+    return workspace.nbytes
 
 
 def _same_type(a, an, b, bn):
@@ -429,7 +441,7 @@ def grouped_linear_backward_input(dy, offsets, w, dx, workspace, stream=None):
 
 def grouped_linear_backward_weight(x, dy, offsets, dw, workspace, stream=None):
     """dw[e] = x_e.T @ dy_e (fp32; zeros for a group without rows)."""
-    if dw.dim() != 3 or str(dw.dtype) != "torch.float32":
+    if dw.dim() != 3 or dw.dtype != _type_tables()[2]:
         _refuse("dw must be [groups, d_in, d_out] float32", MG_ERR_SHAPE)
     e, k, n = dw.shape
     nb = _grouped_args(x, "x", offsets, e, workspace)
@@ -457,7 +469,7 @@ class GradList:
         for i, g in enumerate(grads):
             _dense(g, f"gradient {i}")
             if out is not None:
-                _dense(out[i], f"output {i}", tuple(g.shape))
+                _dense(out[i], f"output {i}", g.shape)
                 _same_type(g, f"gradient {i}", out[i], f"output {i}")
         n = len(grads)
         pg = (_P * max(1, n))(*[_ptr(g) for g in grads])
@@ -471,7 +483,7 @@ class GradList:
     def clip(self, max_norm: float, stats, stream=None):
         """stats[0] = the norm, stats[1] = the factor (fp32 [2] on the device);
         the gradients times the factor to their outputs."""
-        if str(stats.dtype) != "torch.float32":
+        if stats.dtype != _type_tables()[2]:
             _refuse("stats must be float32")
         _dense(stats, "stats", (2,))
         _status(self.lib.mg_grad_list_clip(self.h, max_norm, _ptr(stats), _stream(stream)))

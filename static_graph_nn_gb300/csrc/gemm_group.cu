@@ -10,7 +10,12 @@
 // for the router nor launches one product per expert.
 //
 // This file's kernel runs fp32 (FFMA only) and bf16 widths that TMA cannot
-// address (rows that are not multiples of 16 bytes).
+// address (rows that are not multiples of 16 bytes).  Bound by the FP32 units:
+// 64x64 tiles (a group's last tile is half empty on average, so small ones) of
+// 128 threads with 8x4 outputs each, which need 12 shared-memory floats per 32
+// FFMAs; fp32 operands come by 4-byte asynchronous copies (any width and
+// alignment, transposed on the way, zeros outside) three K steps ahead.  4096
+// rows x 16 experts x 1001x517, fp32: see kStages.
 #include <cstdio>
 
 #include "../../include/mg.h"
@@ -22,14 +27,46 @@
 namespace mg {
 namespace {
 
-constexpr int S_T = 64;    // output tile
+constexpr int S_T = 64;        // output tile
 constexpr int S_K = 16;
+constexpr int S_LD = S_T + 4;  // 16-byte aligned rows, transposed writes spread over the banks
+constexpr int S_STAGES = 3;
+constexpr int S_THREADS = 128;
 
-// One 64x64 output tile per step, 256 threads with 4x4 outputs each.
+struct SimtStage {
+  float a[S_K][S_LD], b[S_K][S_LD];
+};
+
+// Fetch a K step of one operand into s[k][i]: element (i, k) is src[i * ld + k]
+// (K_MAJOR) or src[k * ld + i]; zeros at i >= ni or k >= nk.
+template <bool K_MAJOR>
+__device__ __forceinline__ void simt_fetch(float (&s)[S_K][S_LD], const float* src, long long ld, int ni, int nk) {
+#pragma unroll
+  for (int q = 0; q < S_T * S_K / S_THREADS; ++q) {
+    const int j = threadIdx.x + q * S_THREADS;
+    const int k = K_MAJOR ? j % S_K : j / S_T, i = K_MAJOR ? j / S_K : j % S_T;
+    const bool ok = i < ni && k < nk;
+    const float* p = ok ? (K_MAJOR ? src + i * ld + k : src + k * ld + i) : src;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(&s[k][i]))),
+                 "l"(p), "r"(ok ? 4 : 0)
+                 : "memory");
+  }
+}
+template <bool K_MAJOR>
+__device__ __forceinline__ void simt_fetch(float (&s)[S_K][S_LD], const bf16* src, long long ld, int ni, int nk) {
+#pragma unroll
+  for (int q = 0; q < S_T * S_K / S_THREADS; ++q) {
+    const int j = threadIdx.x + q * S_THREADS;
+    const int k = K_MAJOR ? j % S_K : j / S_T, i = K_MAJOR ? j / S_K : j % S_T;
+    s[k][i] = i < ni && k < nk ? __bfloat162float(K_MAJOR ? src[i * ld + k] : src[k * ld + i]) : 0.0f;
+  }
+}
+
 template <typename T, int KIND>
-__global__ void __launch_bounds__(256) group_simt_kernel(const GroupArgs g) {
+__global__ void __launch_bounds__(S_THREADS, 5) group_simt_kernel(const GroupArgs g) {
   extern __shared__ int s_tab[];
-  __shared__ float As[S_K][S_T + 4], Bs[S_K][S_T + 4];
+  __shared__ __align__(16) SimtStage st[S_STAGES];
   GroupTable t;
   t.n = g.groups + (g.zero_rest ? 2 : 0);
   t.lo = s_tab;
@@ -64,51 +101,46 @@ __global__ void __launch_bounds__(256) group_simt_kernel(const GroupArgs g) {
       K = e < g.groups ? K0 : 0;
     }
     const T* W = KIND == GROUP_DW || e >= g.groups ? B : B + (size_t)e * g.d_in * g.d_out;
-    float acc[4][4] = {};
-    for (int k0 = 0; k0 < K; k0 += S_K) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int i = threadIdx.x + q * 256;
-        float a = 0.f, b = 0.f;
+    auto fetch = [&](int k0) {
+      SimtStage& q = st[k0 / S_K % S_STAGES];
+      if (k0 < K) {
         if (KIND == GROUP_DW) {
-          const int k = i / S_T, m = i % S_T;
-          if (k0 + k < K && m0 + m < m_end) a = ld_elem(A, (size_t)(krow0 + k0 + k) * g.d_in + m0 + m);
-          As[k][m] = a;
-          if (k0 + k < K && n0 + m < N) b = ld_elem(B, (size_t)(krow0 + k0 + k) * g.d_out + n0 + m);
-          Bs[k][m] = b;
+          simt_fetch<false>(q.a, A + (size_t)(krow0 + k0) * g.d_in + m0, g.d_in, m_end - m0, K - k0);
+          simt_fetch<false>(q.b, B + (size_t)(krow0 + k0) * g.d_out + n0, g.d_out, N - n0, K - k0);
         } else {
-          const int k = i % S_K, m = i / S_K;
-          if (k0 + k < K && m0 + m < m_end) a = ld_elem(A, (size_t)(m0 + m) * K0 + k0 + k);
-          As[k][m] = a;
-          if (KIND == GROUP_FWD) {
-            const int kb = i / S_T, n = i % S_T;
-            if (k0 + kb < K && n0 + n < N) b = ld_elem(W, (size_t)(k0 + kb) * g.d_out + n0 + n);
-            Bs[kb][n] = b;
-          } else {
-            if (k0 + k < K && n0 + m < N) b = ld_elem(W, (size_t)(n0 + m) * g.d_out + k0 + k);
-            Bs[k][m] = b;
-          }
+          simt_fetch<true>(q.a, A + (size_t)m0 * K0 + k0, K0, m_end - m0, K - k0);
+          if (KIND == GROUP_FWD) simt_fetch<false>(q.b, W + (size_t)k0 * g.d_out + n0, g.d_out, N - n0, K - k0);
+          else simt_fetch<true>(q.b, W + (size_t)n0 * g.d_out + k0, g.d_out, N - n0, K - k0);
         }
       }
-      __syncthreads();
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    float acc[8][4] = {};
+    __syncthreads();                       // the previous tile's last step has been read
+    fetch(0);
+    fetch(S_K);
+    for (int k0 = 0; k0 < K; k0 += S_K) {
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      __syncthreads();                     // this step is there for all, the one before is read
+      fetch(k0 + 2 * S_K);
+      const SimtStage& q = st[k0 / S_K % S_STAGES];
 #pragma unroll
       for (int k = 0; k < S_K; ++k) {
-        float a[4], b[4];
+        const float4 a0 = *reinterpret_cast<const float4*>(&q.a[k][ty * 8]);
+        const float4 a1 = *reinterpret_cast<const float4*>(&q.a[k][ty * 8 + 4]);
+        const float4 b4 = *reinterpret_cast<const float4*>(&q.b[k][tx * 4]);
+        const float a[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+        const float b[4] = {b4.x, b4.y, b4.z, b4.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          a[i] = As[k][ty * 4 + i];
-          b[i] = Bs[k][tx * 4 + i];
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 8; ++i)
 #pragma unroll
           for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
       }
-      __syncthreads();
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int m = m0 + ty * 4 + i;
+    for (int i = 0; i < 8; ++i) {
+      const int m = m0 + ty * 8 + i;
       if (m >= m_end) continue;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -139,10 +171,10 @@ cudaError_t simt_launch(const GroupArgs& g, cudaStream_t s) {
   const long long tiles_m = KIND == GROUP_DW ? (long long)g.groups * ((g.d_in + S_T - 1) / S_T)
                                              : (long long)g.rows / S_T + g.groups + 2;   // at most
   const long long items = tiles_m * tiles_n;
-  const int slots = 8 * device_sms();
+  const int slots = 5 * device_sms();
   const int grid = (int)(items < slots ? items : slots);
   const size_t smem = (size_t)kGroupTableInts(g.groups) * sizeof(int);
-  group_simt_kernel<T, KIND><<<grid, 256, smem, s>>>(g);
+  group_simt_kernel<T, KIND><<<grid, S_THREADS, smem, s>>>(g);
   return cudaGetLastError();
 }
 

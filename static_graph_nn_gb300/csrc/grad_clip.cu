@@ -4,18 +4,25 @@
 //   c    = max_norm / norm if norm > max_norm, else 1   (1 if norm is NaN or infinite)
 //   out  = c g
 //
-// Two passes over a table of chunks (runs of at most kClipChunk elements of
-// one tensor): the first sums squares, the second scales.  Both are bound by
-// memory; the second pass reads what the first read last, walking the table
-// backwards, so that the part of the gradients still in L2 is not read from
-// DRAM again.
+// The list is cut into chunks of at most 32 KB of one tensor; a block holds a
+// whole chunk in registers, eight 16-byte loads a thread.
 //
-// Sums: a thread squares and adds 32 elements at a time in fp32 and adds that
-// to an fp64 total, so that the error does not grow with the count; should an
-// fp32 sum leave the range in which squares neither overflow nor lose bits to
-// underflow, those 32 elements are summed again in fp64 from registers.  Every
-// block writes its total to its own slot and the block that finishes last adds
-// the slots in order: no atomic order enters the result.
+// Up to three chunks per SM (15 MB) all fit on chip at once: one cooperative
+// launch reads every gradient once, meets at a grid barrier for the norm, and
+// writes the scaled values from the registers.  This is bound by latency (one
+// launch, one DRAM round trip, the barrier).
+//
+// Larger lists take two launches, the sum of squares and the scaling, and are
+// bound by DRAM: 12 bytes per fp32 element (two reads and a write).  The second
+// pass walks the chunks backwards, so that what the first one read last is
+// still in L2.
+//
+// Sums: a thread squares and adds 32 elements at a time in fp32 (eight running
+// sums of four) and adds that to an fp64 total, so that the error does not
+// grow with the count; should an fp32 sum leave the range in which squares
+// neither overflow nor lose bits to underflow, those elements are summed again
+// in fp64 from registers.  Every block writes its total to its own slot and the
+// slots are added in order: no atomic order enters the result.
 #include <algorithm>
 #include <cmath>
 #include <cstdio>
@@ -31,14 +38,22 @@
 namespace mg {
 namespace {
 
-constexpr int kClipChunk = 16384;
 constexpr int kClipThreads = 256;
+constexpr int kClipVecs = 8;                                      // 16-byte loads a thread and chunk
+constexpr int kClipBytes = kClipThreads * kClipVecs * 16;         // 32 KB
+constexpr int kClipFusedPerSm = 3;   // resident blocks that hold a chunk each (84 registers a thread)
+constexpr unsigned kClipSpin = 1u << 22;                          // bounded barrier wait
 
 struct ClipChunk {
   const void* g;
   void* out;
   int len;
   int flags;   // bit 0: bf16, bit 1: g and out allow 16-byte accesses
+};
+
+struct ClipSync {
+  unsigned long long arrived;   // blocks that have reached the barrier, over all calls
+  unsigned last;                // blocks that have written their partial sum
 };
 
 __device__ __forceinline__ double block_sum_f64(double v, double* red /* 32 */) {
@@ -57,10 +72,10 @@ __device__ __forceinline__ double block_sum_f64(double v, double* red /* 32 */) 
 // Sum of the squares of N values held in registers.
 template <int N>
 __device__ __forceinline__ double squares(const float (&x)[N]) {
-  float s[4] = {0.f, 0.f, 0.f, 0.f};
+  float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int i = 0; i < N; ++i) s[i & 3] = fmaf(x[i], x[i], s[i & 3]);
-  const float t = (s[0] + s[1]) + (s[2] + s[3]);
+  for (int i = 0; i < N; ++i) s[i & 7] = fmaf(x[i], x[i], s[i & 7]);
+  const float t = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
   // inside this range the largest square neither overflows nor is a value
   // whose neighbours' squares underflow by more than 2^-24 of the sum
   if (t < 1e37f && t > 1e-25f) return (double)t;
@@ -76,144 +91,189 @@ __device__ __forceinline__ double squares(const float (&x)[N]) {
   return d;
 }
 
-template <typename T>
-__device__ __forceinline__ void load16(const T* p, float* f);
-template <>
-__device__ __forceinline__ void load16<float>(const float* p, float* f) {
+__device__ __forceinline__ void widen_bf16(const uint4& u, float* f) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const float4 v = reinterpret_cast<const float4*>(p)[q];
-    f[4 * q] = v.x; f[4 * q + 1] = v.y; f[4 * q + 2] = v.z; f[4 * q + 3] = v.w;
-  }
-}
-template <>
-__device__ __forceinline__ void load16<bf16>(const bf16* p, float* f) {
-#pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const uint4 u = reinterpret_cast<const uint4*>(p)[q];
-    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 t = __bfloat1622float2(h[i]);
-      f[8 * q + 2 * i] = t.x;
-      f[8 * q + 2 * i + 1] = t.y;
-    }
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
 }
 
-template <typename T>
-__device__ __forceinline__ double chunk_squares(const T* g, int len, bool vec) {
-  double total = 0.0;
-  const int step = kClipThreads * 16;
-  int done = 0;
-  if (vec) {
-    for (int b = threadIdx.x * 16; b + 16 <= len; b += step) {
-      float x[16];
-      load16<T>(g + b, x);
-      total += squares<16>(x);
+// A thread's part of a chunk: kClipVecs vectors of 16 bytes, a block's width
+// apart; zeros behind the chunk's last whole vector.
+struct ClipData {
+  uint4 u[kClipVecs];
+  __device__ __forceinline__ void load(const ClipChunk& c) {
+    const int nv = c.flags & 2 ? c.len / (c.flags & 1 ? 8 : 4) : 0;
+    const uint4* p = static_cast<const uint4*>(c.g);
+#pragma unroll
+    for (int q = 0; q < kClipVecs; ++q) {
+      const int i = threadIdx.x + q * kClipThreads;
+      u[q] = i < nv ? p[i] : make_uint4(0, 0, 0, 0);
     }
-    done = len & ~15;
   }
-  for (int i = done + threadIdx.x; i < len; i += kClipThreads) {
-    float x[1] = {ld_elem(g, i)};
-    total += squares<1>(x);
+  __device__ __forceinline__ double sum(const ClipChunk& c) const {
+    double t = 0.0;
+    if (c.flags & 1) {
+#pragma unroll
+      for (int q = 0; q < kClipVecs; q += 4) {
+        float x[32];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) widen_bf16(u[q + j], x + 8 * j);
+        t += squares<32>(x);
+      }
+    } else {
+      float x[32];
+#pragma unroll
+      for (int q = 0; q < kClipVecs; ++q) {
+        x[4 * q] = __uint_as_float(u[q].x);
+        x[4 * q + 1] = __uint_as_float(u[q].y);
+        x[4 * q + 2] = __uint_as_float(u[q].z);
+        x[4 * q + 3] = __uint_as_float(u[q].w);
+      }
+      t = squares<32>(x);
+    }
+    return t;
   }
-  return total;
+  // c = 1 stores the bits as they are (a NaN keeps its payload)
+  __device__ __forceinline__ void store(const ClipChunk& c, float f) const {
+    const int nv = c.flags & 2 ? c.len / (c.flags & 1 ? 8 : 4) : 0;
+    uint4* p = static_cast<uint4*>(c.out);
+#pragma unroll
+    for (int q = 0; q < kClipVecs; ++q) {
+      const int i = threadIdx.x + q * kClipThreads;
+      if (i >= nv) continue;
+      uint4 v = u[q];
+      if (f != 1.0f) {
+        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (c.flags & 1) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(w[j] << 16) * f,
+                                                           __uint_as_float(w[j] & 0xffff0000u) * f);
+            w[j] = *reinterpret_cast<const uint32_t*>(&h);
+          } else {
+            w[j] = __float_as_uint(__uint_as_float(w[j]) * f);
+          }
+        }
+        v = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      __stcs(p + i, v);
+    }
+  }
+};
+
+// Elements outside the whole vectors: a chunk's tail, or all of an unaligned one.
+template <typename F>
+__device__ __forceinline__ void clip_rest(const ClipChunk& c, F&& f) {
+  const int done = c.flags & 2 ? (c.flags & 1 ? c.len & ~7 : c.len & ~3) : 0;
+  for (int i = done + threadIdx.x; i < c.len; i += kClipThreads) f(i);
 }
 
-__global__ void __launch_bounds__(kClipThreads) clip_norm_kernel(const ClipChunk* chunks, int n_chunks,
-                                                                 double* partial, unsigned* arrivals,
-                                                                 float max_norm, float* stats) {
+__device__ __forceinline__ double chunk_squares(const ClipChunk& c, const ClipData& d) {
+  double t = d.sum(c);
+  clip_rest(c, [&](int i) {
+    const float x[1] = {c.flags & 1 ? ld_elem(static_cast<const bf16*>(c.g), i)
+                                    : ld_elem(static_cast<const float*>(c.g), i)};
+    t += squares<1>(x);
+  });
+  return t;
+}
+
+__device__ __forceinline__ void chunk_store(const ClipChunk& c, const ClipData& d, float f) {
+  d.store(c, f);
+  clip_rest(c, [&](int i) {
+    if (c.flags & 1) {
+      const bf16 x = static_cast<const bf16*>(c.g)[i];
+      static_cast<bf16*>(c.out)[i] = f == 1.0f ? x : __float2bfloat16_rn(__bfloat162float(x) * f);
+    } else {
+      const uint32_t x = static_cast<const uint32_t*>(c.g)[i];
+      static_cast<uint32_t*>(c.out)[i] = f == 1.0f ? x : __float_as_uint(__uint_as_float(x) * f);
+    }
+  });
+}
+
+// The norm and the factor from the blocks' sums, added in order by one block.
+__device__ __forceinline__ float2 clip_finish(const double* partial, int n, float max_norm, double* red) {
+  double s = 0.0;
+  for (int i = threadIdx.x; i < n; i += kClipThreads) s += __ldcg(partial + i);
+  s = block_sum_f64(s, red);
+  const double norm = sqrt(s);
+  const bool finite = norm - norm == 0.0;
+  return make_float2((float)norm, finite && norm > (double)max_norm ? (float)((double)max_norm / norm) : 1.0f);
+}
+
+// One chunk per block, all blocks resident (cooperative launch).
+__global__ void __launch_bounds__(kClipThreads, kClipFusedPerSm)
+    clip_fused_kernel(const ClipChunk* chunks, double* partial, ClipSync* sync, float max_norm, float* stats) {
+  __shared__ double red[32];
+  __shared__ int ok;
+  const ClipChunk c = chunks[blockIdx.x];
+  ClipData d;
+  d.load(c);
+  const double t = block_sum_f64(chunk_squares(c, d), red);
+  if (threadIdx.x == 0) {
+    partial[blockIdx.x] = t;
+    __threadfence();
+    const unsigned long long n = gridDim.x;
+    const unsigned long long want = (atomicAdd(&sync->arrived, 1ull) / n + 1) * n;
+    unsigned spin = 0;
+    while (*reinterpret_cast<volatile unsigned long long*>(&sync->arrived) < want && ++spin < kClipSpin) __nanosleep(20);
+    ok = spin < kClipSpin;
+    __threadfence();
+  }
+  __syncthreads();
+  if (!ok) {           // the results of this call are invalid: say so in the norm
+    if (threadIdx.x == 0) stats[0] = stats[1] = __int_as_float(0x7fffffff);
+    return;
+  }
+  const float2 r = clip_finish(partial, gridDim.x, max_norm, red);
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    stats[0] = r.x;
+    stats[1] = r.y;
+  }
+  if (r.y == 1.0f && c.out == c.g) return;
+  chunk_store(c, d, r.y);
+}
+
+__global__ void __launch_bounds__(kClipThreads, 4) clip_norm_kernel(const ClipChunk* chunks, int n_chunks,
+                                                                    double* partial, ClipSync* sync,
+                                                                    float max_norm, float* stats) {
   __shared__ double red[32];
   __shared__ bool last;
   double t = 0.0;
-  if ((int)blockIdx.x < n_chunks) {
-    const ClipChunk c = chunks[blockIdx.x];
-    t = c.flags & 1 ? chunk_squares(static_cast<const bf16*>(c.g), c.len, c.flags & 2)
-                    : chunk_squares(static_cast<const float*>(c.g), c.len, c.flags & 2);
+  for (int i = blockIdx.x; i < n_chunks; i += gridDim.x) {
+    const ClipChunk c = chunks[i];
+    ClipData d;
+    d.load(c);
+    t += chunk_squares(c, d);
   }
   t = block_sum_f64(t, red);
   if (threadIdx.x == 0) {
     partial[blockIdx.x] = t;
     __threadfence();
-    last = atomicAdd(arrivals, 1u) == gridDim.x - 1;
+    last = atomicAdd(&sync->last, 1u) == gridDim.x - 1;
   }
   __syncthreads();
   if (!last) return;
   __threadfence();
-  double s = 0.0;
-  for (int i = threadIdx.x; i < (int)gridDim.x; i += kClipThreads) s += __ldcg(partial + i);
-  s = block_sum_f64(s, red);
+  const float2 r = clip_finish(partial, gridDim.x, max_norm, red);
   if (threadIdx.x == 0) {
-    const double norm = sqrt(s);
-    const bool finite = norm - norm == 0.0;
-    stats[0] = (float)norm;
-    stats[1] = finite && norm > (double)max_norm ? (float)((double)max_norm / norm) : 1.0f;
-    *arrivals = 0;   // for the next call
+    stats[0] = r.x;
+    stats[1] = r.y;
+    sync->last = 0;   // for the next call
   }
 }
 
-template <typename T>
-__device__ __forceinline__ void chunk_scale(const T* g, T* out, int len, bool vec, float c) {
-  const int step = kClipThreads * 16;
-  int done = 0;
-  if (vec) {
-    for (int b = threadIdx.x * 16; b + 16 <= len; b += step) {
-      float x[16];
-      load16<T>(g + b, x);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] *= c;
-      if constexpr (sizeof(T) == 4) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          reinterpret_cast<float4*>(out + b)[q] = make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
-      } else {
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint32_t w[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(x[8 * q + 2 * i], x[8 * q + 2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t*>(&h);
-          }
-          reinterpret_cast<uint4*>(out + b)[q] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-      }
-    }
-    done = len & ~15;
-  }
-  for (int i = done + threadIdx.x; i < len; i += kClipThreads) st_elem(out, i, ld_elem(g, i) * c);
-}
-
-// c = 1: the bits as they are (a NaN keeps its payload).
-template <typename W>
-__device__ __forceinline__ void chunk_copy(const W* g, W* out, int len, bool vec) {
-  constexpr int N = 16 / sizeof(W);
-  int done = 0;
-  if (vec) {
-    for (int b = threadIdx.x; b < len / N; b += kClipThreads)
-      reinterpret_cast<uint4*>(out)[b] = reinterpret_cast<const uint4*>(g)[b];
-    done = len / N * N;
-  }
-  for (int i = done + threadIdx.x; i < len; i += kClipThreads) out[i] = g[i];
-}
-
-__global__ void __launch_bounds__(kClipThreads) clip_scale_kernel(const ClipChunk* chunks, int n_chunks,
-                                                                  const float* stats) {
-  const float c = stats[1];
-  const ClipChunk k = chunks[n_chunks - 1 - (int)blockIdx.x];
-  if (c == 1.0f) {
-    if (k.out == k.g) return;
-    if (k.flags & 1)
-      chunk_copy(static_cast<const uint16_t*>(k.g), static_cast<uint16_t*>(k.out), k.len, k.flags & 2);
-    else
-      chunk_copy(static_cast<const uint32_t*>(k.g), static_cast<uint32_t*>(k.out), k.len, k.flags & 2);
-    return;
-  }
-  if (k.flags & 1)
-    chunk_scale(static_cast<const bf16*>(k.g), static_cast<bf16*>(k.out), k.len, k.flags & 2, c);
-  else
-    chunk_scale(static_cast<const float*>(k.g), static_cast<float*>(k.out), k.len, k.flags & 2, c);
+__global__ void __launch_bounds__(kClipThreads, 4) clip_scale_kernel(const ClipChunk* chunks, int n_chunks,
+                                                                     const float* stats) {
+  const ClipChunk c = chunks[n_chunks - 1 - (int)blockIdx.x];
+  ClipData d;
+  d.load(c);           // in flight while the factor is fetched
+  const float f = stats[1];
+  if (f == 1.0f && c.out == c.g) return;
+  chunk_store(c, d, f);
 }
 
 }  // namespace
@@ -223,7 +283,9 @@ struct mg_grad_list {
   int device = 0;
   int n_chunks = 0;
   char* ws = nullptr;   // chunk table, partial sums, arrival counter
-  size_t partial_off = 0, arrivals_off = 0;
+  size_t partial_off = 0, sync_off = 0;
+  int sms = 0;
+  bool fused = false;   // all chunks resident at once: one launch
 };
 
 using mg::op_fail;
@@ -259,8 +321,9 @@ extern "C" mg_status mg_grad_list_create(int n, const void* const* grads, void* 
       if (gl != ol) spans.push_back({gl, gl + bytes, i, false});
       spans.push_back({ol, ol + bytes, i, true});
       const int flags = dtypes[i] | (gl % 16 == 0 && ol % 16 == 0 ? 2 : 0);
-      for (size_t a = 0; a < counts[i]; a += mg::kClipChunk)
-        table.push_back({g + a * es, o + a * es, (int)std::min<size_t>(mg::kClipChunk, counts[i] - a), flags});
+      const size_t step = mg::kClipBytes / es;
+      for (size_t a = 0; a < counts[i]; a += step)
+        table.push_back({g + a * es, o + a * es, (int)std::min<size_t>(step, counts[i] - a), flags});
     }
     if (table.size() > 0x7ffffff0u) return op_fail(MG_ERR_SHAPE, "%s: too many elements", fn);
     // a written range may meet no other range (the same tensor twice, or an
@@ -278,10 +341,16 @@ extern "C" mg_status mg_grad_list_create(int n, const void* const* grads, void* 
     std::unique_ptr<mg_grad_list> l(new mg_grad_list());
     l->n_chunks = (int)table.size();
     cudaError_t e = cudaGetDevice(&l->device);
-    const size_t blocks = std::max<size_t>(1, table.size());
+    int coop = 0, per_sm = 0;
+    l->sms = mg::device_sms();
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&coop, cudaDevAttrCooperativeLaunch, l->device);
+    if (e == cudaSuccess)
+      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, mg::clip_fused_kernel, mg::kClipThreads, 0);
+    l->fused = coop && l->n_chunks > 0 && l->n_chunks <= l->sms * std::min(per_sm, mg::kClipFusedPerSm);
+    const size_t blocks = std::max<size_t>(l->fused ? table.size() : 1, (size_t)l->sms * 4);
     l->partial_off = (table.size() * sizeof(mg::ClipChunk) + 255) / 256 * 256;
-    l->arrivals_off = l->partial_off + blocks * sizeof(double);
-    const size_t bytes = l->arrivals_off + 16;
+    l->sync_off = l->partial_off + blocks * sizeof(double);
+    const size_t bytes = l->sync_off + sizeof(mg::ClipSync);
     if (e == cudaSuccess) e = cudaMalloc((void**)&l->ws, bytes);
     if (e != cudaSuccess) {
       cudaGetLastError();
@@ -290,7 +359,7 @@ extern "C" mg_status mg_grad_list_create(int n, const void* const* grads, void* 
     }
     if (!table.empty())
       e = cudaMemcpy(l->ws, table.data(), table.size() * sizeof(mg::ClipChunk), cudaMemcpyHostToDevice);
-    if (e == cudaSuccess) e = cudaMemset(l->ws + l->arrivals_off, 0, 16);
+    if (e == cudaSuccess) e = cudaMemset(l->ws + l->sync_off, 0, sizeof(mg::ClipSync));
     if (e != cudaSuccess) {
       cudaFree(l->ws);
       return mg::op_end(fn, e);
@@ -323,11 +392,18 @@ extern "C" mg_status mg_grad_list_clip(mg_grad_list* l, float max_norm, float* s
   if (st != MG_OK) return st;
   cudaStream_t s = (cudaStream_t)stream;
   const auto* chunks = reinterpret_cast<const mg::ClipChunk*>(l->ws);
-  const int blocks = std::max(1, l->n_chunks);
-  mg::clip_norm_kernel<<<blocks, mg::kClipThreads, 0, s>>>(
-      chunks, l->n_chunks, reinterpret_cast<double*>(l->ws + l->partial_off),
-      reinterpret_cast<unsigned*>(l->ws + l->arrivals_off), max_norm, stats);
-  cudaError_t e = cudaGetLastError();
+  double* partial = reinterpret_cast<double*>(l->ws + l->partial_off);
+  mg::ClipSync* sync = reinterpret_cast<mg::ClipSync*>(l->ws + l->sync_off);
+  cudaError_t e;
+  if (l->fused) {
+    void* args[] = {&chunks, &partial, &sync, &max_norm, &stats};
+    e = cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(mg::clip_fused_kernel), dim3(l->n_chunks),
+                                    dim3(mg::kClipThreads), args, 0, s);
+    return mg::op_end(fn, e);
+  }
+  const int blocks = std::max(1, std::min(l->n_chunks, 4 * l->sms));
+  mg::clip_norm_kernel<<<blocks, mg::kClipThreads, 0, s>>>(chunks, l->n_chunks, partial, sync, max_norm, stats);
+  e = cudaGetLastError();
   if (e == cudaSuccess && l->n_chunks) {
     mg::clip_scale_kernel<<<l->n_chunks, mg::kClipThreads, 0, s>>>(chunks, l->n_chunks, stats);
     e = cudaGetLastError();
