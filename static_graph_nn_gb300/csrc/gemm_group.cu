@@ -12,10 +12,15 @@
 // This file's kernel runs fp32 (FFMA only) and bf16 widths that TMA cannot
 // address (rows that are not multiples of 16 bytes).  Bound by the FP32 units:
 // 64x64 tiles (a group's last tile is half empty on average, so small ones) of
-// 128 threads with 8x4 outputs each, which need 12 shared-memory floats per 32
-// FFMAs; fp32 operands come by 4-byte asynchronous copies (any width and
-// alignment, transposed on the way, zeros outside) three K steps ahead.  4096
-// rows x 16 experts x 1001x517, fp32: see kStages.
+// 128 threads with 8x4 outputs each, two products per instruction.  fp32
+// operands come by 4-byte asynchronous copies (any width and alignment,
+// transposed on the way, zeros outside) two K steps ahead.  Shared memory is
+// what limits it (three 16-byte reads per 32 products and thread): 4096 rows x
+// 16 experts x 1001x517 in fp32 took 273 us with 4x4 outputs a thread and
+// synchronous copies, 163 with 8x4 and the copies ahead, 140 with
+// conflict-free transposed writes and no bounds in the inner tiles (30
+// TFLOP/s); 8x8 outputs with 64 threads a tile read less but leave too few warps
+// (161).
 #include <cstdio>
 
 #include "../../include/mg.h"
@@ -39,19 +44,30 @@ struct SimtStage {
 
 // Fetch a K step of one operand into s[k][i]: element (i, k) is src[i * ld + k]
 // (K_MAJOR) or src[k * ld + i]; zeros at i >= ni or k >= nk.
-template <bool K_MAJOR>
-__device__ __forceinline__ void simt_fetch(float (&s)[S_K][S_LD], const float* src, long long ld, int ni, int nk) {
+template <bool K_MAJOR, bool FULL>
+__device__ __forceinline__ void simt_copy(float (&s)[S_K][S_LD], const float* src, long long ld, int ni, int nk) {
+  // K_MAJOR: 8 k x 4 i per warp, whose transposed writes meet 32 banks
+  const int k0 = K_MAJOR ? threadIdx.x % 8 : threadIdx.x / S_T;
+  const int i0 = K_MAJOR ? threadIdx.x / 8 : threadIdx.x % S_T;
+  constexpr int DI = S_THREADS / 8, DK = S_THREADS / S_T;   // steps of i (K_MAJOR) and of k
+  const float* p = src + (K_MAJOR ? i0 * ld + k0 : k0 * ld + i0);
+  const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(&s[k0][i0]));
 #pragma unroll
   for (int q = 0; q < S_T * S_K / S_THREADS; ++q) {
-    const int j = threadIdx.x + q * S_THREADS;
-    const int k = K_MAJOR ? j % S_K : j / S_T, i = K_MAJOR ? j / S_K : j % S_T;
-    const bool ok = i < ni && k < nk;
-    const float* p = ok ? (K_MAJOR ? src + i * ld + k : src + k * ld + i) : src;
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
-                     static_cast<uint32_t>(__cvta_generic_to_shared(&s[k][i]))),
-                 "l"(p), "r"(ok ? 4 : 0)
+    constexpr int HALF = S_T / DI;                          // K_MAJOR: copies per 8 k
+    const int dk = K_MAJOR ? q / HALF * 8 : q * DK, di = K_MAJOR ? q % HALF * DI : 0;
+    const bool ok = FULL || (i0 + di < ni && k0 + dk < nk);
+    const float* g = p + (K_MAJOR ? di * ld + dk : dk * ld);
+    if (!FULL && !ok) g = src;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + (dk * S_LD + di) * 4), "l"(g),
+                 "r"(ok ? 4 : 0)
                  : "memory");
   }
+}
+template <bool K_MAJOR>
+__device__ __forceinline__ void simt_fetch(float (&s)[S_K][S_LD], const float* src, long long ld, int ni, int nk) {
+  if (ni >= S_T && nk >= S_K) simt_copy<K_MAJOR, true>(s, src, ld, ni, nk);
+  else simt_copy<K_MAJOR, false>(s, src, ld, ni, nk);
 }
 template <bool K_MAJOR>
 __device__ __forceinline__ void simt_fetch(float (&s)[S_K][S_LD], const bf16* src, long long ld, int ni, int nk) {
@@ -63,8 +79,16 @@ __device__ __forceinline__ void simt_fetch(float (&s)[S_K][S_LD], const bf16* sr
   }
 }
 
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  return (uint64_t)__float_as_uint(hi) << 32 | __float_as_uint(lo);
+}
+// Two fp32 FMAs in one instruction, each rounded as fmaf.
+__device__ __forceinline__ void fma2(uint64_t& c, uint64_t a, uint64_t b) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(a), "l"(b));
+}
+
 template <typename T, int KIND>
-__global__ void __launch_bounds__(S_THREADS, 5) group_simt_kernel(const GroupArgs g) {
+__global__ void __launch_bounds__(S_THREADS, 4) group_simt_kernel(const GroupArgs g) {
   extern __shared__ int s_tab[];
   __shared__ __align__(16) SimtStage st[S_STAGES];
   GroupTable t;
@@ -82,7 +106,7 @@ __global__ void __launch_bounds__(S_THREADS, 5) group_simt_kernel(const GroupArg
                                            : (long long)t.cum[t.n - 1] * tiles_n;
   const T* A = static_cast<const T*>(g.A);
   const T* B = static_cast<const T*>(g.B);
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;   // rows ty*4.. and 32+ty*4.., columns tx*4..
   int e = 0;
   for (long long item = blockIdx.x; item < items; item += gridDim.x) {
     const int mt = (int)(item / tiles_n), n0 = (int)(item % tiles_n) * S_T;
@@ -115,7 +139,7 @@ __global__ void __launch_bounds__(S_THREADS, 5) group_simt_kernel(const GroupArg
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    float acc[8][4] = {};
+    uint64_t acc2[4][4] = {};              // the thread's rows 2i and 2i + 1, column j
     __syncthreads();                       // the previous tile's last step has been read
     fetch(0);
     fetch(S_K);
@@ -126,27 +150,29 @@ __global__ void __launch_bounds__(S_THREADS, 5) group_simt_kernel(const GroupArg
       const SimtStage& q = st[k0 / S_K % S_STAGES];
 #pragma unroll
       for (int k = 0; k < S_K; ++k) {
-        const float4 a0 = *reinterpret_cast<const float4*>(&q.a[k][ty * 8]);
-        const float4 a1 = *reinterpret_cast<const float4*>(&q.a[k][ty * 8 + 4]);
-        const float4 b4 = *reinterpret_cast<const float4*>(&q.b[k][tx * 4]);
-        const float a[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
-        const float b[4] = {b4.x, b4.y, b4.z, b4.w};
+        const float4 a0 = *reinterpret_cast<const float4*>(&q.a[k][ty * 4]);
+        const float4 a1 = *reinterpret_cast<const float4*>(&q.a[k][32 + ty * 4]);
+        const float4 b0 = *reinterpret_cast<const float4*>(&q.b[k][tx * 4]);
+        const uint64_t a[4] = {pack2(a0.x, a0.y), pack2(a0.z, a0.w), pack2(a1.x, a1.y), pack2(a1.z, a1.w)};
+        const float b[4] = {b0.x, b0.y, b0.z, b0.w};
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int j = 0; j < 4; ++j) {
+          const uint64_t bb = pack2(b[j], b[j]);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
+          for (int i = 0; i < 4; ++i) fma2(acc2[i][j], a[i], bb);
+        }
       }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int m = m0 + ty * 8 + i;
+      const int m = m0 + (i & 4) * 8 + ty * 4 + (i & 3);
       if (m >= m_end) continue;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int n = n0 + tx * 4 + j;
         if (n >= N) continue;
-        float x = acc[i][j];
+        float x = __uint_as_float((uint32_t)(acc2[i / 2][j] >> (i % 2 * 32)));
         if (KIND == GROUP_DW) {
           static_cast<float*>(g.out)[((size_t)e * g.d_in + m) * g.d_out + n] = x;
           continue;
@@ -171,7 +197,7 @@ cudaError_t simt_launch(const GroupArgs& g, cudaStream_t s) {
   const long long tiles_m = KIND == GROUP_DW ? (long long)g.groups * ((g.d_in + S_T - 1) / S_T)
                                              : (long long)g.rows / S_T + g.groups + 2;   // at most
   const long long items = tiles_m * tiles_n;
-  const int slots = 5 * device_sms();
+  const int slots = 4 * device_sms();
   const int grid = (int)(items < slots ? items : slots);
   const size_t smem = (size_t)kGroupTableInts(g.groups) * sizeof(int);
   group_simt_kernel<T, KIND><<<grid, S_THREADS, smem, s>>>(g);

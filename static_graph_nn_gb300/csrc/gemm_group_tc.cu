@@ -17,15 +17,16 @@
 // W is addressed as a three-dimensional tensor, so a K block past its last row
 // reads zeros, not the next expert's weights.  In dW the groups' rows are the
 // K dimension, and the last 64-row block of a group may hold rows of the next
-// one: the producer warp loads that block on a barrier of its own, overwrites
-// the foreign rows with zeros in shared memory (both operands: a NaN there
-// would survive a zero factor), fences them to the async proxy and only then
-// reports the stage full.  One such block per group and tile; the MMAs of the
-// blocks before it run meanwhile.
+// one: that block is loaded on a barrier of its own, and a warp of each CTA
+// overwrites the foreign rows with zeros in shared memory (both operands: a NaN
+// there would survive a zero factor), fences them to the async proxy and only
+// then reports the stage full.  The producer runs on meanwhile (with the
+// zeroing in the producer's own loop the ring ran dry once per tile: 404 us
+// against 352 for 16384 rows x 8 experts x 2048x8192).
 //
 // Warp roles and pipeline as in gemm_tc2.cu: warp 0 TMA producer, warp 1 MMA
-// issuer (leader CTA), warps 2-9 epilogue; six 32 KB stages per CTA; two
-// accumulators of 256 columns.  Every wait is bounded.
+// issuer (leader CTA), warps 2-9 epilogue, in dW warp 10 zeroing; six 32 KB
+// stages per CTA; two accumulators of 256 columns.  Every wait is bounded.
 #include <cuda.h>
 
 #include "common.cuh"
@@ -46,7 +47,9 @@ constexpr int G_BNH = 128;         // B columns per CTA (256 per pair)
 constexpr int G_BN = 256;
 constexpr int G_BK = 64;
 constexpr int G_STAGES = 6;
-constexpr int G_THREADS = 320;
+constexpr int G_THREADS = 320;      // one more warp in dW
+
+constexpr int group_threads(int kind) { return kind == GROUP_DW ? G_THREADS + 32 : G_THREADS; }
 constexpr uint32_t G_A_BYTES = G_BM * G_BK * 2;
 constexpr uint32_t G_B_BYTES = G_BNH * G_BK * 2;
 constexpr int G_PANEL = 64 * G_BK * 2;   // one 64-column panel of a stage
@@ -120,7 +123,7 @@ __device__ __forceinline__ void mbar_arrive_remote_release(uint32_t cluster_addr
 }
 
 template <int KIND, typename TO>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G_THREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(group_threads(KIND), 1)
     group_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                       const GroupTcParams P) {
   constexpr bool A_MN = KIND == GROUP_DW;
@@ -135,9 +138,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G_THREADS, 1)
   uint64_t* empty = full + G_STAGES;
   uint64_t* tfull = empty + G_STAGES;
   uint64_t* tempty = tfull + 2;
-  uint64_t* tailbar = tempty + 2;      // this CTA's loads of a block that needs zeroing
-  uint64_t* fixbar = tailbar + 1;      // leader: the peer's block is zeroed
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(fixbar + 1);
+  uint64_t* tailbar = tempty + 2;          // per stage: this CTA's loads of a block that needs zeroing
+  uint64_t* fixbar = tailbar + G_STAGES;   // per stage, leader: the peer's block is zeroed
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(fixbar + G_STAGES);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   GroupTable t;
   t.n = P.groups + (P.zero_rest ? 2 : 0);
@@ -154,13 +157,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G_THREADS, 1)
     for (int s = 0; s < G_STAGES; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
+      mbar_init(&tailbar[s], 1);
+      mbar_init(&fixbar[s], 1);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
       mbar_init(&tempty[a], 2 * 256);
     }
-    mbar_init(tailbar, 1);
-    mbar_init(fixbar, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -177,24 +180,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G_THREADS, 1)
   const int n_items = tile_count<KIND>(P, t);
 
   if (warp == 0) {
-    // ---------------- TMA producer (both CTAs; the whole warp, for the zeroing) ----------------
-    int stage = 0, e = 0;
-    uint32_t phase = 0, tail_phase = 0;
-    for (int item = pair; item < n_items; item += npairs) {
-      const GroupTile T = tile_at<KIND>(P, t, item, e);
-      const int plain = T.tail ? T.kb - 1 : T.kb;
-      const int m0 = T.m0 + (int)rank * G_BM, n0 = T.n0 + (int)rank * G_BNH;
-      int ok = 1;
-      if (lane == 0) {
-        int st = stage;
-        uint32_t ph = phase;
-        for (int kb = 0; kb < plain; ++kb) {
-          if (*abort_flag || !mbar_wait_cluster(&empty[st], ph ^ 1)) { ok = 0; break; }
-          if (leader) mbar_expect_tx(&full[st], 2 * (G_A_BYTES + G_B_BYTES));
-          const uint32_t fb = map_to(&full[st], 0);
+    // ---------------- TMA producer (both CTAs) ----------------
+    if (lane == 0) {
+      int stage = 0, e = 0;
+      uint32_t phase = 0;
+      for (int item = pair; item < n_items && !*abort_flag; item += npairs) {
+        const GroupTile T = tile_at<KIND>(P, t, item, e);
+        const int m0 = T.m0 + (int)rank * G_BM, n0 = T.n0 + (int)rank * G_BNH;
+        for (int kb = 0; kb < T.kb; ++kb) {
+          if (!mbar_wait_cluster(&empty[stage], phase ^ 1)) { *abort_flag = 1; atomicExch(P.err, 1); break; }
+          uint8_t* a = sA + stage * G_A_BYTES;
+          uint8_t* b = sB + stage * G_B_BYTES;
           const int k0 = kb * G_BK;
-          uint8_t* a = sA + st * G_A_BYTES;
-          uint8_t* b = sB + st * G_B_BYTES;
+          if (KIND == GROUP_DW && T.tail && kb == T.kb - 1) {
+            const int kr = T.krow0 + k0;
+            mbar_expect_tx(&tailbar[stage], G_A_BYTES + G_B_BYTES);
+            tma_load_2d(a, &tmA, &tailbar[stage], m0, kr);
+            tma_load_2d(a + G_PANEL, &tmA, &tailbar[stage], m0 + 64, kr);
+            tma_load_2d(b, &tmB, &tailbar[stage], n0, kr);
+            tma_load_2d(b + G_PANEL, &tmB, &tailbar[stage], n0 + 64, kr);
+            if (++stage == G_STAGES) { stage = 0; phase ^= 1; }
+            continue;
+          }
+          if (leader) mbar_expect_tx(&full[stage], 2 * (G_A_BYTES + G_B_BYTES));
+          const uint32_t fb = map_to(&full[stage], 0);
           if (A_MN) {
             tma_load_2d_to_leader(a, &tmA, fb, m0, T.krow0 + k0);
             tma_load_2d_to_leader(a + G_PANEL, &tmA, fb, m0 + 64, T.krow0 + k0);
@@ -210,52 +219,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G_THREADS, 1)
           } else {
             tma_load_3d_to_leader(b, &tmB, fb, k0, n0, T.e);
           }
-          if (++st == G_STAGES) { st = 0; ph ^= 1; }
+          if (++stage == G_STAGES) { stage = 0; phase ^= 1; }
         }
       }
-      const int adv = stage + plain;
-      stage = adv % G_STAGES;
-      phase ^= (uint32_t)(adv / G_STAGES) & 1u;
-      if (KIND == GROUP_DW && T.tail) {
+    }
+  } else if (KIND == GROUP_DW && warp == 10) {
+    // ---------------- zeroing of the blocks that end inside a group's rows ----------------
+    int blocks = 0, e = 0;          // K blocks of this pair's earlier tiles
+    uint32_t parity = 0;            // per stage: parity of its tailbar and fixbar
+    for (int item = pair; item < n_items; item += npairs) {
+      const GroupTile T = tile_at<KIND>(P, t, item, e);
+      const int stage = (blocks + T.kb - 1) % G_STAGES;
+      blocks = (blocks + T.kb) % G_STAGES;
+      if (!T.tail) continue;
+      const uint32_t ph = parity >> stage & 1u;
+      parity ^= 1u << stage;
+      int ok = __all_sync(0xffffffffu, mbar_wait(&tailbar[stage], ph));
+      if (ok) {
         uint8_t* a = sA + stage * G_A_BYTES;
         uint8_t* b = sB + stage * G_B_BYTES;
-        if (lane == 0 && ok) {
-          ok = !*abort_flag && mbar_wait_cluster(&empty[stage], phase ^ 1);
-          if (ok) {
-            const int kr = T.krow0 + plain * G_BK;
-            mbar_expect_tx(tailbar, G_A_BYTES + G_B_BYTES);
-            tma_load_2d(a, &tmA, tailbar, m0, kr);
-            tma_load_2d(a + G_PANEL, &tmA, tailbar, m0 + 64, kr);
-            tma_load_2d(b, &tmB, tailbar, n0, kr);
-            tma_load_2d(b + G_PANEL, &tmB, tailbar, n0 + 64, kr);
+        // a K row is one 128-byte line of each panel, whatever the swizzle inside it
+        const int n16 = (G_BK - T.tail) * 8;
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          uint4* q = reinterpret_cast<uint4*>((p < 2 ? a + p * G_PANEL : b + (p - 2) * G_PANEL) + T.tail * 128);
+          for (int i = lane; i < n16; i += 32) q[i] = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) {
+          if (leader) {
+            ok = mbar_wait_cluster(&fixbar[stage], ph);
+            if (ok) mbar_arrive(&full[stage]);
+          } else {
+            mbar_arrive_remote_release(map_to(&fixbar[stage], 0));
           }
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (ok) ok = mbar_wait(tailbar, tail_phase);
-        ok = __all_sync(0xffffffffu, ok);
-        if (ok) {
-          // a K row is one 128-byte line of each panel, whatever the swizzle inside it
-          const int n16 = (G_BK - T.tail) * 8;
-#pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            uint4* q = reinterpret_cast<uint4*>((p < 2 ? a + p * G_PANEL : b + (p - 2) * G_PANEL) + T.tail * 128);
-            for (int i = lane; i < n16; i += 32) q[i] = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async();
-          __syncwarp();
-          if (lane == 0) {
-            if (leader) {
-              ok = mbar_wait_cluster(fixbar, tail_phase);
-              if (ok) mbar_arrive(&full[stage]);
-            } else {
-              mbar_arrive_remote_release(map_to(fixbar, 0));
-            }
-          }
-        }
-        tail_phase ^= 1;
-        if (++stage == G_STAGES) { stage = 0; phase ^= 1; }
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
       if (!ok) {
         if (lane == 0) { *abort_flag = 1; atomicExch(P.err, 1); }
         break;
@@ -383,7 +384,7 @@ bool group_map(CUtensorMap* map, const void* base, long long outer, long long ro
 }
 
 size_t group_pair_smem(int groups) {
-  return 1024 + (size_t)G_STAGES * (G_A_BYTES + G_B_BYTES) + (2 * G_STAGES + 6) * 8 + 8 +
+  return 1024 + (size_t)G_STAGES * (G_A_BYTES + G_B_BYTES) + (4 * G_STAGES + 4) * 8 + 8 +
          (size_t)kGroupTableInts(groups) * 4;
 }
 
@@ -431,7 +432,7 @@ cudaError_t launch_group_pair(const GroupArgs& g, cudaStream_t s) {
   static const int slots = [&] {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * (device_sms() / 2));
-    cfg.blockDim = dim3(G_THREADS);
+    cfg.blockDim = dim3(group_threads(KIND));
     cfg.dynamicSmemBytes = group_pair_smem(kMaxGroups);
     cudaLaunchAttribute at;
     at.id = cudaLaunchAttributeClusterDimension;
@@ -453,7 +454,7 @@ cudaError_t launch_group_pair(const GroupArgs& g, cudaStream_t s) {
                               : ((long long)g.rows / (2 * G_BM) + g.groups + (g.zero_rest ? 2 : 0)) * P.tiles_n;
   if (items > 0x7fffffff) return cudaErrorInvalidValue;
   const int pairs = items < slots ? (int)items : slots;
-  kern<<<2 * pairs, G_THREADS, smem, s>>>(ma, mb, P);
+  kern<<<2 * pairs, group_threads(KIND), smem, s>>>(ma, mb, P);
   return cudaGetLastError();
 }
 
