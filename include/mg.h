@@ -57,7 +57,12 @@ typedef enum {
   MG_OP_RMSNORM = 3,          /* y = x / sqrt(mean(x^2) + eps) * gamma, gamma[d] */
   MG_OP_RESIDUAL_BEGIN = 4,   /* remember the current value as the skip input */
   MG_OP_RESIDUAL_END = 5,     /* value = skip + value */
-  MG_OP_CAUSAL_ATTENTION = 6  /* input [rows, 3d] = [Q|K|V], output [rows, d], d = n_heads*head_dim */
+  MG_OP_CAUSAL_ATTENTION = 6, /* input [rows, 3d] = [Q|K|V], output [rows, d], d = n_heads*head_dim */
+  MG_OP_EMBEDDING = 7,        /* first layer only: x is int32 ids [batch]; row = eps * W[id], W[d_in, d_out];
+                                 an id outside [0, d_in) (padding): a row of zeros and no gradient */
+  MG_OP_GROUPED_LINEAR = 8    /* Y[r] = X[r] W[e(r)], W[n_heads, d_in, d_out], the rows of group e given by
+                                 mg_set_row_groups; rows of no group: zeros.  Activations and residual ends
+                                 follow it as they follow LINEAR; no bias */
 } mg_op;
 
 typedef enum { MG_LOSS_CE_DENSE = 0, MG_LOSS_CE_INDEX = 1, MG_LOSS_MSE = 2 } mg_loss_kind;
@@ -76,11 +81,11 @@ typedef enum {
 
 typedef struct {
   int op;        /* mg_op */
-  int d_in;      /* LINEAR: input width; RMSNORM: width */
-  int d_out;     /* LINEAR: output width */
+  int d_in;      /* LINEAR, GROUPED_LINEAR: input width; RMSNORM: width; EMBEDDING: vocabulary */
+  int d_out;     /* LINEAR, GROUPED_LINEAR: output width; EMBEDDING: width */
   int has_bias;  /* LINEAR: 1 if a bias vector follows W in the parameters */
-  float eps;     /* RMSNORM: epsilon inside the square root */
-  int n_heads;   /* CAUSAL_ATTENTION */
+  float eps;     /* RMSNORM: epsilon inside the square root; EMBEDDING: the rows' factor */
+  int n_heads;   /* CAUSAL_ATTENTION; GROUPED_LINEAR: groups (at most 1024) */
   int head_dim;  /* CAUSAL_ATTENTION (64 supported) */
   int seq_len;   /* CAUSAL_ATTENTION: rows are [batch, seq_len] flattened */
 } mg_layer;
@@ -135,7 +140,7 @@ size_t mg_workspace_bytes(const mg_plan* plan);
  * Contents section: a trained model reloaded into a fresh inference session;
  * abstract: one graph and runtime for training and deployed inference).
  * params: flat fp32 [mg_param_count]; x: [batch, d_in], fp32 in strict mode,
- * bf16 in bf16 mode; out: fp32 [batch, d_out] (logits or the model output),
+ * bf16 in bf16 mode (int32 ids [batch] for an embedding); out: fp32 [batch, d_out] (logits or the model output),
  * written row-major; in bf16 mode each output value is the bf16 value the
  * graph stores, widened. */
 mg_status mg_forward(mg_plan* plan, const float* params, const void* x, float* out,
@@ -149,7 +154,8 @@ mg_status mg_forward(mg_plan* plan, const float* params, const void* x, float* o
  *  adam_m, adam_v fp32 [P]  optimizer state, updated in place: Adam and LaProp
  *          use both (first and second moment); SGD_MOMENTUM keeps its velocity
  *          in adam_m (adam_v may be NULL); plain SGD needs neither
- *  x       [batch, d_in], fp32 (strict) or bf16 (bf16)
+ *  x       [batch, d_in], fp32 (strict) or bf16 (bf16); int32 ids [batch] where
+ *          the first layer is an embedding
  *  labels  CE_DENSE: fp32 [batch, C]; CE_INDEX: int32 [batch], values in [0, C);
  *          MSE: target [batch, d_out] in the activation dtype (fp32 / bf16)
  *  lr      learning rate; step: Adam's / LaProp's t, 1-based (ignored by SGD)
@@ -173,6 +179,34 @@ mg_status mg_forward(mg_plan* plan, const float* params, const void* x, float* o
 mg_status mg_train_step(mg_plan* plan, float* params, float* grads, float* adam_m,
                         float* adam_v, const void* x, const void* labels, float lr, int step,
                         mg_stream_t stream);
+
+/* Row groups of a plan's GROUPED_LINEAR layers (all have the same number of
+ * groups): offsets [groups + 1] int32 in device memory, group e being the rows
+ * offsets[e] .. offsets[e+1]-1; nondecreasing within [0, batch], clamped to
+ * that where they are not.  The pointer is kept and its values are read on the
+ * device by every mg_forward and mg_train_step from now on (write new values
+ * to it, in stream order, as the batches change).  Required before either call
+ * of a plan with such layers; a plan without them answers MG_ERR_INVALID_ARG. */
+mg_status mg_set_row_groups(mg_plan* plan, const int* offsets);
+
+/* Clip the gradients of every later mg_train_step by their global norm: with
+ * norm = sqrt(sum of the squares of all gradients), the optimizer uses c * g, c
+ * = max_norm / norm if norm > max_norm, else 1 (also for a norm that is NaN or
+ * infinite).  `grads` still receives the gradients as they are, before the
+ * factor.  max_norm = INFINITY measures only; 0 turns it off again (the state
+ * after creation); anything else that is not positive is MG_ERR_INVALID_ARG.
+ * With clipping on, the updates run after the whole backward instead of under
+ * it (the sums of squares take their place there), and MG_FUSED_UPDATE has no
+ * effect.  The first call that turns it on allocates 8 bytes per 2048
+ * parameters.  Not while profiling. */
+mg_status mg_set_grad_clip(mg_plan* plan, float max_norm);
+
+/* Device address of {norm, c} (two fp32) of the last mg_train_step with
+ * clipping on; NULL if it was never on.  Valid until destroy. */
+const float* mg_grad_norm_device_ptr(const mg_plan* plan);
+
+/* Copy {norm, c} to the host; synchronises `stream`. */
+mg_status mg_grad_norm(mg_plan* plan, float* host_norm_and_factor, mg_stream_t stream);
 
 /* Copy the last step's loss (the batch mean the README's Example section
  * prints per step) to the host; synchronises `stream`. */

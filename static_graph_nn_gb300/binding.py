@@ -20,7 +20,7 @@ STATUS_NAMES = {0: "MG_OK", -1: "MG_ERR_INVALID_ARG", -2: "MG_ERR_UNSUPPORTED", 
                 -8: "MG_ERR_TIMEOUT", -9: "MG_ERR_INTERNAL"}
 
 OPS = {"linear": 0, "relu": 1, "gelu_tanh": 2, "rmsnorm": 3, "residual_begin": 4,
-       "residual_end": 5, "causal_attention": 6}
+       "residual_end": 5, "causal_attention": 6, "embedding": 7, "grouped_linear": 8}
 LOSSES = {"ce_dense": 0, "ce_index": 1, "mse": 2}
 PRECISIONS = {"strict": 0, "bf16": 1}
 OPTIMIZERS = {"sgd": 0, "adam": 1, "laprop": 2, "sgd_momentum": 3}
@@ -51,6 +51,10 @@ _SIGS = {
     "mg_forward": (ctypes.c_int, [_P, _P, _P, _P, _P]),
     "mg_train_step": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, ctypes.c_float, ctypes.c_int, _P]),
     "mg_loss": (ctypes.c_int, [_P, ctypes.POINTER(ctypes.c_float), _P]),
+    "mg_set_row_groups": (ctypes.c_int, [_P, _P]),
+    "mg_set_grad_clip": (ctypes.c_int, [_P, ctypes.c_float]),
+    "mg_grad_norm_device_ptr": (_P, [_P]),
+    "mg_grad_norm": (ctypes.c_int, [_P, ctypes.POINTER(ctypes.c_float), _P]),
     "mg_loss_device_ptr": (_P, [_P]),
     "mg_loss_async": (ctypes.c_int, [_P, ctypes.c_void_p, _P]),
     "mg_refresh_params": (ctypes.c_int, [_P, _P, _P]),
@@ -151,6 +155,10 @@ def layer_struct(l: dict) -> mg_layer:
         s.d_in, s.eps = l["d"], l["eps"]
     elif l["op"] == "causal_attention":
         s.n_heads, s.head_dim, s.seq_len = l["n_heads"], l["head_dim"], l["seq_len"]
+    elif l["op"] == "embedding":
+        s.d_in, s.d_out, s.eps = l["vocab"], l["dim"], l["scale"]
+    elif l["op"] == "grouped_linear":
+        s.d_in, s.d_out, s.n_heads = l["d_in"], l["d_out"], l["groups"]
     return s
 
 
@@ -172,6 +180,7 @@ class Plan:
             raise MGError(st, self.lib.mg_last_error(None).decode())
         self.h = h
         self.batch, self.precision, self.loss_kind = batch, precision, loss
+        self.layers = list(layers)
 
     @classmethod
     def for_workload(cls, w, precision: str):
@@ -218,6 +227,31 @@ class Plan:
         self._check(self.lib.mg_train_step(self.h, _ptr(params), _ptr(grads), _ptr(adam_m),
                                            _ptr(adam_v), _ptr(x), _ptr(labels), float(lr),
                                            int(step), _stream(stream)))
+
+    def set_row_groups(self, offsets):
+        """Row groups of the grouped_linear layers: int32 offsets [groups + 1] on the
+        device (kept; its values are read by every later forward and train_step)."""
+        if not isinstance(offsets, int):
+            groups = next((l["groups"] for l in self.layers if l["op"] == "grouped_linear"), 0)
+            if offsets.dtype != _type_tables()[3]:
+                _refuse("offsets must be int32")
+            _dense(offsets, "offsets", (groups + 1,))
+        self._check(self.lib.mg_set_row_groups(self.h, _ptr(offsets)))
+        self.row_groups = offsets
+
+    def set_grad_clip(self, max_norm: float):
+        """Clip every later step's gradients to this global norm (inf: measure only;
+        0: off)."""
+        self._check(self.lib.mg_set_grad_clip(self.h, max_norm))
+
+    def grad_norm(self, stream=None) -> tuple[float, float]:
+        """(norm, factor) of the last clipped step; waits for it."""
+        v = (ctypes.c_float * 2)()
+        self._check(self.lib.mg_grad_norm(self.h, v, _stream(stream)))
+        return v[0], v[1]
+
+    def grad_norm_device_ptr(self) -> int | None:
+        return self.lib.mg_grad_norm_device_ptr(self.h)
 
     def loss(self, stream=None) -> float:
         v = ctypes.c_float()

@@ -838,6 +838,11 @@ Ws ws_layout(long long n, int V, int d) {
 
 size_t embedding_ws_bytes(long long n, int V, int d) { return ws_layout(n, V, d).bytes; }
 
+int embedding_bwd_launches(long long n, int V, int d) {
+  if (n <= kSmallMax) return n > 0 ? 2 : 1;
+  return 3 * ws_layout(n, V, d).passes + 3;
+}
+
 cudaError_t embedding_fwd(DType tt, const void* table, int V, int d, int id64, const void* ids, long long n,
                           float scale, DType ot, void* out, cudaStream_t s) {
   if (n == 0) return cudaSuccess;

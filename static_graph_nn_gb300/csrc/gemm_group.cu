@@ -25,6 +25,7 @@
 
 #include "../../include/mg.h"
 #include "common.cuh"
+#include "group_epilogue.cuh"
 #include "group_table.cuh"
 #include "kernels.h"
 #include "op_checks.h"
@@ -177,14 +178,7 @@ __global__ void __launch_bounds__(S_THREADS, 4) group_simt_kernel(const GroupArg
           static_cast<float*>(g.out)[((size_t)e * g.d_in + m) * g.d_out + n] = x;
           continue;
         }
-        const size_t o = (size_t)m * N + n;
-        auto round_t = [](float v) { return sizeof(T) == 2 ? __bfloat162float(__float2bfloat16_rn(v)) : v; };
-        if (g.act || g.resid || g.out_z) x = round_t(x);
-        if (g.out_z) st_elem(static_cast<T*>(g.out_z), o, x);
-        if (g.act) x = apply_act(g.act, x);
-        if (g.dact) x = round_t(x) * act_grad_from_saved(g.dact, ld_elem(static_cast<const T*>(g.saved), o));
-        if (g.resid) x += ld_elem(static_cast<const T*>(g.resid), o);
-        st_elem(static_cast<T*>(g.out), o, x);
+        group_epilogue<T>(g, (size_t)m * N + n, x);
       }
     }
   }
@@ -207,8 +201,7 @@ cudaError_t simt_launch(const GroupArgs& g, cudaStream_t s) {
 }  // namespace
 
 size_t group_ws_bytes(int rows, int groups, int d_in, int d_out) {
-  (void)rows; (void)groups; (void)d_in; (void)d_out;
-  return 256;
+  return 256 + grouped_narrow_ws_bytes(rows, groups, d_in, d_out);
 }
 
 cudaError_t grouped_gemm(const GroupArgs& g, cudaStream_t s) {
@@ -260,7 +253,8 @@ mg_status grouped_call(const char* fn, mg::GroupKind kind, int dtype, const void
   g.A = a;
   g.B = b;
   g.out = out;
-  g.ws = static_cast<int*>(ws);
+  g.err = static_cast<int*>(ws);
+  g.ws = g.err + 64;
   return mg::op_end(fn, mg::grouped_gemm(g, (cudaStream_t)stream));
 }
 

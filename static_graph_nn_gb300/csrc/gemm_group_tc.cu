@@ -31,6 +31,7 @@
 
 #include "common.cuh"
 #include "group_table.cuh"
+#include "group_tma.h"
 #include "kernels.h"
 #include "op_checks.h"
 #include "tc_common.cuh"
@@ -368,21 +369,6 @@ EncodeTiledFn group_encode_fn() {
   return fn;
 }
 
-// bf16 [outer][rows][cols], dense; box box_cols x box_rows x 1, 128-byte
-// swizzle.  outer = 0: two-dimensional.
-bool group_map(CUtensorMap* map, const void* base, long long outer, long long rows, long long cols, int box_cols,
-               int box_rows) {
-  EncodeTiledFn fn = group_encode_fn();
-  if (!fn) return false;
-  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)outer};
-  cuuint64_t strides[2] = {(cuuint64_t)cols * 2, (cuuint64_t)cols * (cuuint64_t)rows * 2};
-  cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, outer ? 3 : 2, const_cast<void*>(base), dims, strides, box,
-            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 size_t group_pair_smem(int groups) {
   return 1024 + (size_t)G_STAGES * (G_A_BYTES + G_B_BYTES) + (4 * G_STAGES + 4) * 8 + 8 +
          (size_t)kGroupTableInts(groups) * 4;
@@ -420,7 +406,7 @@ cudaError_t launch_group_pair(const GroupArgs& g, cudaStream_t s) {
   P.tiles_n = (N + G_BN - 1) / G_BN;
   P.tiles_m = (g.d_in + 2 * G_BM - 1) / (2 * G_BM);
   P.k_blocks = ((KIND == GROUP_FWD ? g.d_in : g.d_out) + G_BK - 1) / G_BK;
-  P.err = g.ws;
+  P.err = g.err;
   auto al = [](const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; };
   P.vec = al(g.out, 16) && al(g.out_z, 16) && al(g.saved, 16) && al(g.resid, 16) && N % 8 == 0;
   P.vec32 = al(g.out, 32) && al(g.out_z, 32) && al(g.saved, 32) && al(g.resid, 32) && N % 16 == 0;
@@ -460,6 +446,21 @@ cudaError_t launch_group_pair(const GroupArgs& g, cudaStream_t s) {
 
 }  // namespace
 
+bool group_map(CUtensorMap* map, const void* base, long long outer, long long rows, long long cols, int box_cols,
+               int box_rows) {
+  EncodeTiledFn fn = group_encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)outer};
+  cuuint64_t strides[2] = {(cuuint64_t)cols * 2, (cuuint64_t)cols * (cuuint64_t)rows * 2};
+  cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, outer ? 3 : 2, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool group_map_available() { return group_encode_fn() != nullptr; }
+
 bool grouped_tc_eligible(const GroupArgs& g) {
   auto al = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
   // mo = e * d_in + m and the tile counts are 32-bit
@@ -473,6 +474,7 @@ bool grouped_tc_eligible(const GroupArgs& g) {
 }
 
 cudaError_t grouped_gemm_tc(const GroupArgs& g, cudaStream_t s) {
+  if (grouped_narrow(g)) return grouped_gemm_narrow(g, s);
   if (g.kind == GROUP_FWD) return launch_group_pair<GROUP_FWD, bf16>(g, s);
   if (g.kind == GROUP_DX) return launch_group_pair<GROUP_DX, bf16>(g, s);
   return launch_group_pair<GROUP_DW, float>(g, s);

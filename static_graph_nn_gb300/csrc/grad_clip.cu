@@ -276,7 +276,70 @@ __global__ void __launch_bounds__(kClipThreads, 4) clip_scale_kernel(const ClipC
   chunk_store(c, d, f);
 }
 
+// ---- inside a training step: the flat gradient buffer's chunk table
+__global__ void __launch_bounds__(kClipThreads) grad_squares_kernel(const Chunk* chunks, const float* g, double* sums) {
+  __shared__ double red[32];
+  const Chunk c = chunks[blockIdx.x];
+  const float4* g4 = reinterpret_cast<const float4*>(g + c.start);
+  double t = 0.0;
+  for (int b = 0; b < c.len / 4; b += 2 * kClipThreads) {
+    float4 v[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int i = b + q * kClipThreads + threadIdx.x;
+      v[q] = i < c.len / 4 ? g4[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    const float x[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+    t += squares<8>(x);
+  }
+  const int i = (c.len & ~3) + threadIdx.x;
+  if (i < c.len) {
+    const float x[1] = {g[c.start + i]};
+    t += squares<1>(x);
+  }
+  t = block_sum_f64(t, red);
+  if (threadIdx.x == 0) sums[blockIdx.x] = t;
+}
+
+__global__ void __launch_bounds__(kClipThreads) grad_norm_kernel(const double* sums, int n, double* parts,
+                                                                 unsigned* sync, float max_norm, float* stats) {
+  __shared__ double red[32];
+  __shared__ bool last;
+  double t = 0.0;
+  for (int i = blockIdx.x * kClipThreads + threadIdx.x; i < n; i += gridDim.x * kClipThreads) t += sums[i];
+  t = block_sum_f64(t, red);
+  if (threadIdx.x == 0) {
+    parts[blockIdx.x] = t;
+    __threadfence();
+    last = atomicAdd(sync, 1u) == gridDim.x - 1;
+  }
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  const float2 r = clip_finish(parts, gridDim.x, max_norm, red);
+  if (threadIdx.x == 0) {
+    stats[0] = r.x;
+    stats[1] = r.y;
+    *sync = 0;
+  }
+}
+
 }  // namespace
+
+cudaError_t grad_squares(const Chunk* chunks, int n_chunks, const float* g, double* sums, cudaStream_t s) {
+  if (n_chunks <= 0) return cudaSuccess;
+  grad_squares_kernel<<<n_chunks, kClipThreads, 0, s>>>(chunks, g, sums);
+  return cudaGetLastError();
+}
+
+cudaError_t grad_norm_finish(const double* sums, int n_chunks, double* parts, unsigned* sync, float max_norm,
+                             float* stats, cudaStream_t s) {
+  int grid = (n_chunks + kClipThreads - 1) / kClipThreads;
+  grid = grid < 1 ? 1 : grid > kNormParts ? kNormParts : grid;
+  grad_norm_kernel<<<grid, kClipThreads, 0, s>>>(sums, n_chunks, parts, sync, max_norm, stats);
+  return cudaGetLastError();
+}
+
 }  // namespace mg
 
 struct mg_grad_list {

@@ -142,7 +142,9 @@ struct Chunk {  // a run of one tensor's elements in the flat buffers
 };
 cudaError_t adam_update(const Chunk* chunks, int n_chunks, float* p, const float* g, float* m,
                         float* v, void* shadow, float lr_over_bc1, float inv_sqrt_bc2,
-                        float beta1, float beta2, float eps, cudaStream_t s);
+                        float beta1, float beta2, float eps, const float* gscale, cudaStream_t s);
+// (gscale in every update: NULL, or a factor in device memory that each
+// gradient is multiplied by first -- clipping by the global norm.)
 // The optimizer update kernels' (and write_step_scalars') argument layout, for replaying a captured
 // step with new step scalars: argument count and sizes, and the indices of
 // lr / (1 - b1^t), 1 / sqrt(1 - b2^t) (Adam, LaProp) or lr (SGD, momentum).
@@ -154,11 +156,20 @@ struct OptKernelInfo {
 bool optimizer_kernel_info(const void* func, OptKernelInfo* info);
 cudaError_t laprop_update(const Chunk* chunks, int n_chunks, float* p, const float* g, float* m,
                           float* v, void* shadow, float lr_over_bc1, float inv_sqrt_bc2,
-                          float beta1, float beta2, float eps, cudaStream_t s);
+                          float beta1, float beta2, float eps, const float* gscale,
+                          cudaStream_t s);
 cudaError_t momentum_update(const Chunk* chunks, int n_chunks, float* p, const float* g, float* b,
-                            void* shadow, float lr, float mu, cudaStream_t s);
+                            void* shadow, float lr, float mu, const float* gscale, cudaStream_t s);
 cudaError_t sgd_update(const Chunk* chunks, int n_chunks, float* p, const float* g, void* shadow,
-                       float lr, cudaStream_t s);
+                       float lr, const float* gscale, cudaStream_t s);
+// Sum of the squares of each chunk's gradients, one per chunk (a chunk of at
+// most 2048 elements); then, over all chunks, stats[0] = the norm and stats[1]
+// = max_norm / norm if that is below 1 and the norm is finite, else 1.  parts:
+// kNormParts doubles; sync: zeroed once.
+cudaError_t grad_squares(const Chunk* chunks, int n_chunks, const float* g, double* sums, cudaStream_t s);
+cudaError_t grad_norm_finish(const double* sums, int n_chunks, double* parts, unsigned* sync, float max_norm,
+                             float* stats, cudaStream_t s);
+constexpr int kNormParts = 128;
 // dst[0] = lr_bc1, dst[1] = inv_sqrt_bc2 (the step scalars a fused update
 // reads; a one-thread kernel, so that a replayed step graph can patch them).
 cudaError_t write_step_scalars(float* dst, float lr_bc1, float inv_sqrt_bc2, cudaStream_t s);
@@ -176,6 +187,7 @@ cudaError_t embedding_fwd(DType tt, const void* table, int V, int d, int id64, c
 size_t embedding_ws_bytes(long long n, int V, int d);
 cudaError_t embedding_bwd_sort(int id64, const void* ids, long long n, int V, int d, float* dtable,
                                void* workspace, cudaStream_t s);
+int embedding_bwd_launches(long long n, int V, int d);   // kernels of both parts
 cudaError_t embedding_bwd_sum(DType t, const void* dout, long long n, int V, int d, float scale,
                               float* dtable, void* workspace, cudaStream_t s);
 
@@ -199,11 +211,18 @@ struct GroupArgs {
   const void* saved = nullptr; int dact = 0;
   const void* resid = nullptr;
   int zero_rest = 0;           // rows of no group are computed as if A were 0 there
-  int* ws = nullptr;           // group_ws_bytes; ws[0] is set to 1 on a timed-out wait
+  int* err = nullptr;          // set to 1 on a timed-out wait
+  int* ws = nullptr;           // grouped_narrow_ws_bytes, counters zero between calls; NULL: none
 };
+// Workspace of an entry point: 256 bytes that begin with the error word, then ws.
 size_t group_ws_bytes(int rows, int groups, int d_in, int d_out);
 constexpr int kMaxGroups = 1024;
 cudaError_t grouped_gemm(const GroupArgs& g, cudaStream_t s);
+// The version for a few rows per group (forward and dX, where ws is given;
+// grouped_tc_eligible as well).
+bool grouped_narrow(const GroupArgs& g);
+size_t grouped_narrow_ws_bytes(int rows, int groups, int d_in, int d_out);
+cudaError_t grouped_gemm_narrow(const GroupArgs& g, cudaStream_t s);
 // The tensor-core version: bf16, widths that are multiples of 8.
 bool grouped_tc_eligible(const GroupArgs& g);
 cudaError_t grouped_gemm_tc(const GroupArgs& g, cudaStream_t s);

@@ -23,11 +23,18 @@ __global__ void step_scalars_kernel(float* dst, float lr_bc1, float inv_sqrt_bc2
   dst[1] = inv_sqrt_bc2;
 }
 
+// Gradients times the clipping factor (1 without clipping: the same bits); a
+// product of its own, so that it never merges into the update's FMAs.
+__device__ __forceinline__ float4 scaled4(const float4& g, float s) {
+  return make_float4(__fmul_rn(g.x, s), __fmul_rn(g.y, s), __fmul_rn(g.z, s), __fmul_rn(g.w, s));
+}
+
 __global__ void __launch_bounds__(256) adam_kernel(const Chunk* chunks, float* p, const float* g,
                                                    float* m, float* v, bf16* shadow, float lr_bc1,
                                                    float inv_sqrt_bc2, float b1, float b2,
-                                                   float eps) {
+                                                   float eps, const float* gscale) {
   const Chunk c = chunks[blockIdx.x];
+  const float gs = gscale ? *gscale : 1.0f;
   const long long base = c.start;
   const int n4 = c.len >> 2;
   float4* p4 = reinterpret_cast<float4*>(p + base);
@@ -35,7 +42,7 @@ __global__ void __launch_bounds__(256) adam_kernel(const Chunk* chunks, float* p
   float4* m4 = reinterpret_cast<float4*>(m + base);
   float4* v4 = reinterpret_cast<float4*>(v + base);
   for (int i = threadIdx.x; i < n4; i += blockDim.x) {
-    float4 pp = p4[i], gg = g4[i], mm = m4[i], vv = v4[i];
+    float4 pp = p4[i], gg = scaled4(g4[i], gs), mm = m4[i], vv = v4[i];
     adam_one(pp.x, gg.x, mm.x, vv.x, lr_bc1, inv_sqrt_bc2, b1, b2, eps);
     adam_one(pp.y, gg.y, mm.y, vv.y, lr_bc1, inv_sqrt_bc2, b1, b2, eps);
     adam_one(pp.z, gg.z, mm.z, vv.z, lr_bc1, inv_sqrt_bc2, b1, b2, eps);
@@ -55,7 +62,7 @@ __global__ void __launch_bounds__(256) adam_kernel(const Chunk* chunks, float* p
   for (int i = (n4 << 2) + threadIdx.x; i < c.len; i += blockDim.x) {
     long long k = base + i;
     float pp = p[k], mm = m[k], vv = v[k];
-    adam_one(pp, g[k], mm, vv, lr_bc1, inv_sqrt_bc2, b1, b2, eps);
+    adam_one(pp, __fmul_rn(g[k], gs), mm, vv, lr_bc1, inv_sqrt_bc2, b1, b2, eps);
     p[k] = pp;
     m[k] = mm;
     v[k] = vv;
@@ -82,8 +89,9 @@ __device__ __forceinline__ void shadow4(bf16* shadow, long long base, int i, con
 __global__ void __launch_bounds__(256) laprop_kernel(const Chunk* chunks, float* p, const float* g,
                                                      float* m, float* v, bf16* shadow, float lr_bc1,
                                                      float inv_sqrt_bc2, float b1, float b2,
-                                                     float eps) {
+                                                     float eps, const float* gscale) {
   const Chunk c = chunks[blockIdx.x];
+  const float gs = gscale ? *gscale : 1.0f;
   const long long base = c.start;
   const int n4 = c.len >> 2;
   float4* p4 = reinterpret_cast<float4*>(p + base);
@@ -91,7 +99,7 @@ __global__ void __launch_bounds__(256) laprop_kernel(const Chunk* chunks, float*
   float4* m4 = reinterpret_cast<float4*>(m + base);
   float4* v4 = reinterpret_cast<float4*>(v + base);
   for (int i = threadIdx.x; i < n4; i += blockDim.x) {
-    float4 pp = p4[i], gg = g4[i], mm = m4[i], vv = v4[i];
+    float4 pp = p4[i], gg = scaled4(g4[i], gs), mm = m4[i], vv = v4[i];
     laprop_one(pp.x, gg.x, mm.x, vv.x, lr_bc1, inv_sqrt_bc2, b1, b2, eps);
     laprop_one(pp.y, gg.y, mm.y, vv.y, lr_bc1, inv_sqrt_bc2, b1, b2, eps);
     laprop_one(pp.z, gg.z, mm.z, vv.z, lr_bc1, inv_sqrt_bc2, b1, b2, eps);
@@ -104,7 +112,7 @@ __global__ void __launch_bounds__(256) laprop_kernel(const Chunk* chunks, float*
   for (int i = (n4 << 2) + threadIdx.x; i < c.len; i += blockDim.x) {
     long long k = base + i;
     float pp = p[k], mm = m[k], vv = v[k];
-    laprop_one(pp, g[k], mm, vv, lr_bc1, inv_sqrt_bc2, b1, b2, eps);
+    laprop_one(pp, __fmul_rn(g[k], gs), mm, vv, lr_bc1, inv_sqrt_bc2, b1, b2, eps);
     p[k] = pp;
     m[k] = mm;
     v[k] = vv;
@@ -114,15 +122,16 @@ __global__ void __launch_bounds__(256) laprop_kernel(const Chunk* chunks, float*
 
 __global__ void __launch_bounds__(256) momentum_kernel(const Chunk* chunks, float* p,
                                                        const float* g, float* b, bf16* shadow,
-                                                       float lr, float mu) {
+                                                       float lr, float mu, const float* gscale) {
   const Chunk c = chunks[blockIdx.x];
+  const float gs = gscale ? *gscale : 1.0f;
   const long long base = c.start;
   const int n4 = c.len >> 2;
   float4* p4 = reinterpret_cast<float4*>(p + base);
   const float4* g4 = reinterpret_cast<const float4*>(g + base);
   float4* b4 = reinterpret_cast<float4*>(b + base);
   for (int i = threadIdx.x; i < n4; i += blockDim.x) {
-    float4 pp = p4[i], gg = g4[i], bb = b4[i];
+    float4 pp = p4[i], gg = scaled4(g4[i], gs), bb = b4[i];
     bb.x = mu * bb.x + gg.x; bb.y = mu * bb.y + gg.y; bb.z = mu * bb.z + gg.z; bb.w = mu * bb.w + gg.w;
     pp.x -= lr * bb.x; pp.y -= lr * bb.y; pp.z -= lr * bb.z; pp.w -= lr * bb.w;
     p4[i] = pp;
@@ -131,7 +140,7 @@ __global__ void __launch_bounds__(256) momentum_kernel(const Chunk* chunks, floa
   }
   for (int i = (n4 << 2) + threadIdx.x; i < c.len; i += blockDim.x) {
     long long k = base + i;
-    const float bb = mu * b[k] + g[k];
+    const float bb = mu * b[k] + __fmul_rn(g[k], gs);
     const float pp = p[k] - lr * bb;
     b[k] = bb;
     p[k] = pp;
@@ -140,11 +149,12 @@ __global__ void __launch_bounds__(256) momentum_kernel(const Chunk* chunks, floa
 }
 
 __global__ void __launch_bounds__(256) sgd_kernel(const Chunk* chunks, float* p, const float* g,
-                                                  bf16* shadow, float lr) {
+                                                  bf16* shadow, float lr, const float* gscale) {
   const Chunk c = chunks[blockIdx.x];
+  const float gs = gscale ? *gscale : 1.0f;
   for (int i = threadIdx.x; i < c.len; i += blockDim.x) {
     long long k = c.start + i;
-    float pp = p[k] - lr * g[k];
+    float pp = p[k] - lr * __fmul_rn(g[k], gs);
     p[k] = pp;
     if (shadow && c.shadow) shadow[k] = __float2bfloat16_rn(pp);
   }
@@ -182,15 +192,15 @@ cudaError_t write_step_scalars(float* dst, float lr_bc1, float inv_sqrt_bc2, cud
 
 bool optimizer_kernel_info(const void* func, OptKernelInfo* info) {
   // argument lists of the update kernels above: pointers are 8 bytes, scalars 4
-  static const int two_moment[11] = {8, 8, 8, 8, 8, 8, 4, 4, 4, 4, 4};
-  static const int momentum[7] = {8, 8, 8, 8, 8, 4, 4};
-  static const int sgd[5] = {8, 8, 8, 8, 4};
+  static const int two_moment[12] = {8, 8, 8, 8, 8, 8, 4, 4, 4, 4, 4, 8};
+  static const int momentum[8] = {8, 8, 8, 8, 8, 4, 4, 8};
+  static const int sgd[6] = {8, 8, 8, 8, 4, 8};
   static const int scalars[3] = {8, 4, 4};
   const int* sizes = nullptr;
   if (func == reinterpret_cast<const void*>(adam_kernel) ||
       func == reinterpret_cast<const void*>(laprop_kernel)) {
     sizes = two_moment;
-    info->nargs = 11;
+    info->nargs = 12;
     info->i_lr_bc1 = 6;
     info->i_inv_sqrt_bc2 = 7;
     info->i_lr = -1;
@@ -202,12 +212,12 @@ bool optimizer_kernel_info(const void* func, OptKernelInfo* info) {
     info->i_lr = -1;
   } else if (func == reinterpret_cast<const void*>(momentum_kernel)) {
     sizes = momentum;
-    info->nargs = 7;
+    info->nargs = 8;
     info->i_lr_bc1 = info->i_inv_sqrt_bc2 = -1;
     info->i_lr = 5;
   } else if (func == reinterpret_cast<const void*>(sgd_kernel)) {
     sizes = sgd;
-    info->nargs = 5;
+    info->nargs = 6;
     info->i_lr_bc1 = info->i_inv_sqrt_bc2 = -1;
     info->i_lr = 4;
   } else {
@@ -219,33 +229,33 @@ bool optimizer_kernel_info(const void* func, OptKernelInfo* info) {
 
 cudaError_t adam_update(const Chunk* chunks, int n_chunks, float* p, const float* g, float* m,
                         float* v, void* shadow, float lr_over_bc1, float inv_sqrt_bc2,
-                        float beta1, float beta2, float eps, cudaStream_t s) {
+                        float beta1, float beta2, float eps, const float* gscale, cudaStream_t s) {
   if (n_chunks <= 0) return cudaSuccess;
   adam_kernel<<<n_chunks, 256, 0, s>>>(chunks, p, g, m, v, (bf16*)shadow, lr_over_bc1,
-                                       inv_sqrt_bc2, beta1, beta2, eps);
+                                       inv_sqrt_bc2, beta1, beta2, eps, gscale);
   return cudaGetLastError();
 }
 
 cudaError_t laprop_update(const Chunk* chunks, int n_chunks, float* p, const float* g, float* m,
                           float* v, void* shadow, float lr_over_bc1, float inv_sqrt_bc2,
-                          float beta1, float beta2, float eps, cudaStream_t s) {
+                          float beta1, float beta2, float eps, const float* gscale, cudaStream_t s) {
   if (n_chunks <= 0) return cudaSuccess;
   laprop_kernel<<<n_chunks, 256, 0, s>>>(chunks, p, g, m, v, (bf16*)shadow, lr_over_bc1,
-                                         inv_sqrt_bc2, beta1, beta2, eps);
+                                         inv_sqrt_bc2, beta1, beta2, eps, gscale);
   return cudaGetLastError();
 }
 
 cudaError_t momentum_update(const Chunk* chunks, int n_chunks, float* p, const float* g, float* b,
-                            void* shadow, float lr, float mu, cudaStream_t s) {
+                            void* shadow, float lr, float mu, const float* gscale, cudaStream_t s) {
   if (n_chunks <= 0) return cudaSuccess;
-  momentum_kernel<<<n_chunks, 256, 0, s>>>(chunks, p, g, b, (bf16*)shadow, lr, mu);
+  momentum_kernel<<<n_chunks, 256, 0, s>>>(chunks, p, g, b, (bf16*)shadow, lr, mu, gscale);
   return cudaGetLastError();
 }
 
 cudaError_t sgd_update(const Chunk* chunks, int n_chunks, float* p, const float* g, void* shadow,
-                       float lr, cudaStream_t s) {
+                       float lr, const float* gscale, cudaStream_t s) {
   if (n_chunks <= 0) return cudaSuccess;
-  sgd_kernel<<<n_chunks, 256, 0, s>>>(chunks, p, g, (bf16*)shadow, lr);
+  sgd_kernel<<<n_chunks, 256, 0, s>>>(chunks, p, g, (bf16*)shadow, lr, gscale);
   return cudaGetLastError();
 }
 

@@ -8,7 +8,8 @@
 // own region of one workspace allocated at creation, and the backward pass is
 // derived by hand per fused node:
 //   Linear (+ bias, + ReLU/GELU, + residual add) -> one GEMM with a fused epilogue
-//   RMSNorm, causal attention                    -> their own kernels
+//   RMSNorm, causal attention, embedding         -> their own kernels
+//   grouped Linear (+ activation, + residual add) -> one ragged GEMM with the same epilogue
 //   cross-entropy / MSE                           -> a loss+gradient kernel
 //   SGD / Adam                                    -> one multi-tensor kernel
 #include <cuda_runtime.h>
@@ -45,7 +46,7 @@ constexpr int kNormChunks = 8 * 152;    // RMSNorm backward blocks (dgamma parti
 constexpr int kMsePartials = 1024;
 constexpr size_t kColsumFloats = (size_t)kColsumBlocks * 2048;   // column-sum partials capacity
 
-enum NodeKind { NK_LINEAR, NK_RMSNORM, NK_ATTN };
+enum NodeKind { NK_LINEAR, NK_RMSNORM, NK_ATTN, NK_EMBED, NK_GROUP };
 
 struct Value {
   int width = 0;
@@ -64,7 +65,8 @@ struct Node {
   NodeKind kind;
   int layer = 0;
   int in = -1, out = -1;
-  // linear
+  // linear, grouped linear (groups), embedding (d_in ids, factor in eps)
+  int groups = 0;
   int d_in = 0, d_out = 0, has_bias = 0, act = 0, skip = -1, z = -1;
   size_t w_off = 0, b_off = 0;
   // bf16 linear with a bias whose output feeds a linear: workspace offset of
@@ -118,6 +120,13 @@ struct mg_plan {
   size_t shadow_off = 0, chunks_off = 0, loss_off = 0, rowloss_off = 0, partial_off = 0,
          colsum_off = 0, flag_off = 0, lse_part_off = 0;
   size_t split_off = 0, split_floats = 0;   // strict weight gradients split over K
+  size_t embed_off = 0;      // embedding gradient's workspace
+  size_t group_bytes = 0, group_off = 0;      // grouped products' counters and partials (zero between calls)
+  int n_groups = 0;          // of the grouped layers; 0: there are none
+  const int* row_groups = nullptr;   // caller's offsets
+  // clipping by the global norm (mg_set_grad_clip): 0 off
+  float max_norm = 0.f;
+  char* clip_ws = nullptr;   // stats (2 floats), counter, kNormParts doubles, a double per chunk
   size_t scal_off = 0;       // Adam's step scalars for fused updates (2 floats)
   // MG_FUSED_UPDATE=1: Adam's weight updates in the weight-gradient GEMMs'
   // epilogues where they can be (measured slower on GB300 for the large
@@ -289,6 +298,11 @@ double gemm_bytes(const GemmArgs& g) {
   return b;
 }
 
+float* clip_stats(mg_plan* p) { return reinterpret_cast<float*>(p->clip_ws); }
+unsigned* clip_sync(mg_plan* p) { return reinterpret_cast<unsigned*>(p->clip_ws + 16); }
+double* clip_parts(mg_plan* p) { return reinterpret_cast<double*>(p->clip_ws + 64); }
+double* clip_sums(mg_plan* p) { return clip_parts(p) + kNormParts; }
+
 int norm_chunks(const mg_plan* p) { return p->batch < kNormChunks ? p->batch : kNormChunks; }
 
 bool tc_path(const mg_plan* p, const GemmArgs& g) { return p->use_tc && gemm_tc_eligible(g); }
@@ -314,6 +328,37 @@ std::string gemm_name(const mg_plan* p, const char* what, int layer, const GemmA
                      : gemm_simt_skinny(g) ? "bf16-skinny"
                                           : "bf16-simt";
   snprintf(b, sizeof b, "%s[l%d] %dx%dx%d %s", what, layer, g.M, g.N, g.K, kind);
+  return b;
+}
+
+// Grouped node n's product of this kind (pointers set by the caller).
+GroupArgs group_args(mg_plan* p, const Node& n, GroupKind kind) {
+  GroupArgs g;
+  g.kind = kind;
+  g.type = p->dt;
+  g.rows = p->batch;
+  g.groups = n.groups;
+  g.d_in = n.d_in;
+  g.d_out = n.d_out;
+  g.offsets = p->row_groups;
+  g.zero_rest = 1;
+  g.err = reinterpret_cast<int*>(p->ws + p->loss_off + 4);
+  if (p->group_off) g.ws = wsp<int>(p, p->group_off);
+  return g;
+}
+
+double group_bytes(const mg_plan* p, const Node& n, bool dw) {
+  const double es = (double)dtype_size(p->dt);
+  return es * p->batch * (n.d_in + n.d_out) + (dw ? 4.0 : es) * n.groups * (double)n.d_in * n.d_out;
+}
+
+std::string group_name(const mg_plan* p, const char* what, const Node& n) {
+  char b[160];
+  const char* kind = p->dt != DT_BF16                           ? "f32-ffma"
+                     : n.d_in % 8 == 0 && n.d_out % 8 == 0 ? "bf16-tcgen05"
+                                                                : "bf16-simt";
+  snprintf(b, sizeof b, "%s[l%d] %d rows x %d groups x %dx%d %s", what, n.layer, p->batch, n.groups, n.d_in, n.d_out,
+           kind);
   return b;
 }
 
@@ -346,6 +391,23 @@ void forward_pass(Exec& e, const float* params, const void* x) {
       }
       site(e, gemm_name(p, "fwd", n.layer, g), 2.0 * g.M * g.N * g.K, gemm_bytes(g), 1,
            [&] { return run_gemm(p, g, e.s); });
+    } else if (n.kind == NK_GROUP) {
+      GroupArgs g = group_args(p, n, GROUP_FWD);
+      g.A = val_ptr(p, n.in, x);
+      g.B = (const char*)wbase + n.w_off * dtype_size(dt);
+      g.act = n.act;
+      if (n.z >= 0) g.out_z = p->ws + p->values[n.z].off;
+      if (n.skip >= 0) g.resid = val_ptr(p, n.skip, x);
+      g.out = p->ws + p->values[n.out].off;
+      site(e, group_name(p, "grouped_fwd", n), 2.0 * p->batch * n.d_in * n.d_out, group_bytes(p, n, false), 1,
+           [&] { return grouped_gemm(g, e.s); });
+    } else if (n.kind == NK_EMBED) {
+      char nm[96];
+      snprintf(nm, sizeof nm, "embedding[l%d] %d of %dx%d", n.layer, p->batch, n.d_in, n.d_out);
+      site(e, nm, 0, 2.0 * dtype_size(dt) * p->batch * n.d_out + 4.0 * p->batch, 1, [&] {
+        return embedding_fwd(dt, (const char*)wbase + n.w_off * dtype_size(dt), n.d_in, n.d_out, 0, x, p->batch,
+                             n.eps, dt, p->ws + p->values[n.out].off, e.s);
+      });
     } else if (n.kind == NK_RMSNORM) {
       double bytes = 2.0 * dtype_size(dt) * p->batch * n.d + 4.0 * n.d + 4.0 * p->batch;
       char nm[96];
@@ -417,10 +479,42 @@ void step_scalars(const mg_plan* p, float lr, int step, float* lr_bc1, float* in
   *inv_sqrt_bc2 = (float)(1.0 / std::sqrt(bc2));
 }
 
+// Optimizer update of chunks [c0, c1) (np parameters) on stream st, with the
+// clipping factor where clipping is on.
+void update_chunks(Exec& e, cudaStream_t st, const char* where, int c0, int c1, double np) {
+  mg_plan* p = e.p;
+  const Chunk* chunks = wsp<Chunk>(p, p->chunks_off) + c0;
+  void* shadow = p->dt == DT_BF16 ? p->ws + p->shadow_off : nullptr;
+  const float* gs = p->max_norm != 0.f && p->clip_ws ? clip_stats(p) + 1 : nullptr;
+  char nm[96];
+  if (p->optimizer == MG_OPT_ADAM || p->optimizer == MG_OPT_LAPROP) {
+    float lr_bc1, inv_sqrt_bc2;
+    step_scalars(p, e.lr, e.step, &lr_bc1, &inv_sqrt_bc2);
+    const bool lap = p->optimizer == MG_OPT_LAPROP;
+    snprintf(nm, sizeof nm, "%s%s %.0f params", lap ? "laprop" : "adam", where, np);
+    site_on(e, st, nm, 0, np * (28.0 + (shadow ? 2.0 : 0.0)), 1, [&] {
+      return (lap ? laprop_update : adam_update)(chunks, c1 - c0, e.params, e.grads, e.m, e.v,
+                                                 shadow, lr_bc1, inv_sqrt_bc2, p->beta1,
+                                                 p->beta2, p->adam_eps, gs, st);
+    });
+  } else if (p->optimizer == MG_OPT_SGD_MOMENTUM) {
+    snprintf(nm, sizeof nm, "momentum%s %.0f params", where, np);
+    site_on(e, st, nm, 0, np * (20.0 + (shadow ? 2.0 : 0.0)), 1, [&] {
+      return momentum_update(chunks, c1 - c0, e.params, e.grads, e.m, shadow, e.lr, p->beta1, gs, st);
+    });
+  } else {
+    snprintf(nm, sizeof nm, "sgd%s %.0f params", where, np);
+    site_on(e, st, nm, 0, np * (12.0 + (shadow ? 2.0 : 0.0)), 1, [&] {
+      return sgd_update(chunks, c1 - c0, e.params, e.grads, shadow, e.lr, gs, st);
+    });
+  }
+}
+
 // Optimizer update of node ni's parameters, on the auxiliary stream once the
 // node's backward kernels (the last readers of its weights) have run; with
 // skip_weight, only its tensors after the weight (the weight's update was
-// fused into its gradient GEMM).
+// fused into its gradient GEMM).  With clipping on, the sums of squares of its
+// gradients instead: the updates wait for the norm (clipped_update).
 void node_update(Exec& e, int ni, bool skip_weight = false) {
   mg_plan* p = e.p;
   const Node& n = p->nodes[ni];
@@ -429,36 +523,41 @@ void node_update(Exec& e, int ni, bool skip_weight = false) {
   const int c0 = p->tensor_chunk[t_lo], c1 = p->tensor_chunk[t_hi];
   double np = 0;
   for (int t = t_lo; t < t_hi; ++t) np += (double)p->p_rows[t] * p->p_cols[t];
-  const Chunk* chunks = wsp<Chunk>(p, p->chunks_off) + c0;
-  void* shadow = p->dt == DT_BF16 ? p->ws + p->shadow_off : nullptr;
   if (!e.dry && e.err == cudaSuccess) {
     cudaError_t r = cudaEventRecord(p->node_ev[2 * ni], e.s);
     if (r == cudaSuccess) r = cudaStreamWaitEvent(p->aux, p->node_ev[2 * ni], 0);
     if (r != cudaSuccess) e.err = r;
   }
-  char nm[96];
-  if (p->optimizer == MG_OPT_ADAM || p->optimizer == MG_OPT_LAPROP) {
-    float lr_bc1, inv_sqrt_bc2;
-    step_scalars(p, e.lr, e.step, &lr_bc1, &inv_sqrt_bc2);
-    const bool lap = p->optimizer == MG_OPT_LAPROP;
-    snprintf(nm, sizeof nm, "%s[l%d] %.0f params", lap ? "laprop" : "adam", n.layer, np);
-    site_on(e, p->aux, nm, 0, np * (28.0 + (shadow ? 2.0 : 0.0)), 1, [&] {
-      return (lap ? laprop_update : adam_update)(chunks, c1 - c0, e.params, e.grads, e.m, e.v,
-                                                 shadow, lr_bc1, inv_sqrt_bc2, p->beta1,
-                                                 p->beta2, p->adam_eps, p->aux);
+  char where[24];
+  snprintf(where, sizeof where, "[l%d]", n.layer);
+  if (p->max_norm != 0.f) {
+    char nm[96];
+    snprintf(nm, sizeof nm, "grad_squares%s %.0f params", where, np);
+    site_on(e, p->aux, nm, 0, 4.0 * np, 1, [&] {
+      return grad_squares(wsp<Chunk>(p, p->chunks_off) + c0, c1 - c0, e.grads, clip_sums(p) + c0, p->aux);
     });
-  } else if (p->optimizer == MG_OPT_SGD_MOMENTUM) {
-    snprintf(nm, sizeof nm, "momentum[l%d] %.0f params", n.layer, np);
-    site_on(e, p->aux, nm, 0, np * (20.0 + (shadow ? 2.0 : 0.0)), 1, [&] {
-      return momentum_update(chunks, c1 - c0, e.params, e.grads, e.m, shadow, e.lr, p->beta1,
-                             p->aux);
-    });
-  } else {
-    snprintf(nm, sizeof nm, "sgd[l%d] %.0f params", n.layer, np);
-    site_on(e, p->aux, nm, 0, np * (12.0 + (shadow ? 2.0 : 0.0)), 1, [&] {
-      return sgd_update(chunks, c1 - c0, e.params, e.grads, shadow, e.lr, p->aux);
-    });
+    return;
   }
+  update_chunks(e, p->aux, where, c0, c1, np);
+}
+
+// The norm from every node's sums, then all updates, on the auxiliary stream
+// (behind the sums; the backward, the last reader of the weights, is waited
+// for).
+void clipped_update(Exec& e) {
+  mg_plan* p = e.p;
+  if (!e.dry && e.err == cudaSuccess) {
+    cudaError_t r = cudaEventRecord(p->join_ev, e.s);
+    if (r == cudaSuccess) r = cudaStreamWaitEvent(p->aux, p->join_ev, 0);
+    if (r != cudaSuccess) e.err = r;
+  }
+  site_on(e, p->aux, "grad_norm", 0, 8.0 * p->n_chunks, 1, [&] {
+    return grad_norm_finish(clip_sums(p), p->n_chunks, clip_parts(p), clip_sync(p), p->max_norm, clip_stats(p),
+                            p->aux);
+  });
+  double np = 0;
+  for (size_t t = 0; t < p->p_off.size(); ++t) np += (double)p->p_rows[t] * p->p_cols[t];
+  update_chunks(e, p->aux, "", 0, p->n_chunks, np);
 }
 
 // dW = X^T dZ of linear node n   (M = d_in, N = d_out, K = batch)
@@ -480,7 +579,7 @@ GemmArgs dw_args(mg_plan* p, const Node& n, float* grads, const void* x) {
 // can run in the GEMM's epilogue: Adam, bf16, a tensor-core kernel and no
 // split over K (a split's partial tiles are not the gradient).
 bool update_fusable(mg_plan* p, const GemmArgs& g) {
-  if (!p->fuse_update || p->dt != DT_BF16 || p->optimizer != MG_OPT_ADAM || !tc_path(p, g))
+  if (!p->fuse_update || p->max_norm != 0.f || p->dt != DT_BF16 || p->optimizer != MG_OPT_ADAM || !tc_path(p, g))
     return false;
   return (pair_path(p, g) ? gemm_pair_split_count(g) : gemm_tc_splits(g, nullptr)) == 1;
 }
@@ -502,6 +601,23 @@ void backward_pass(Exec& e, const float* params, float* grads, const void* x) {
   e.db_parts.assign(p->nodes.size(), 0);
   const DType dt = p->dt;
   const void* wbase = dt == DT_BF16 ? (const void*)(p->ws + p->shadow_off) : (const void*)params;
+  // Z of the Linear that produced v again (recompute_gelu), exactly as its
+  // forward GEMM formed it (same kernel, inputs and weights: the optimizer has
+  // not yet updated that node), into the shared Z buffer
+  auto recompute_z = [&](const Value& v) {
+    const Node& pn = p->nodes[v.producer];
+    if (!p->recompute_gelu || pn.kind != NK_LINEAR) return;
+    GemmArgs r;
+    r.M = p->batch; r.N = pn.d_out; r.K = pn.d_in;
+    r.A = val_ptr(p, pn.in, x); r.lda = pn.d_in; r.a_mn = 0;
+    r.B = (const char*)wbase + pn.w_off * dtype_size(dt); r.ldb = pn.d_out; r.b_k = 0;
+    r.in_type = dt;
+    r.bias = pn.has_bias ? params + pn.b_off : nullptr;
+    r.aux_type = dt;
+    r.out = p->ws + p->values[pn.z].off; r.ldo = pn.d_out; r.out_type = dt;
+    site(e, gemm_name(p, "recompute_z", pn.layer, r), 2.0 * r.M * r.N * r.K, gemm_bytes(r),
+         1, [&] { return run_gemm(p, r, e.s); });
+  };
   GemmArgs deferred;   // the deferred node's weight gradient
   bool deferred_fused = false;
   for (int ni = (int)p->nodes.size() - 1; ni >= 0; --ni) {
@@ -577,22 +693,7 @@ void backward_pass(Exec& e, const float* params, float* grads, const void* x) {
           int sv = vin.producer_act == ACT_GELU ? vin.z_value : n.in;
           h.saved = p->ws + p->values[sv].off;
           h.lds = n.d_in;
-          if (vin.producer_act == ACT_GELU && p->recompute_gelu) {
-            // Z of the producing Linear again, exactly as its forward GEMM
-            // formed it (same kernel, inputs and weights: the optimizer has
-            // not yet updated that node), into the shared Z buffer
-            const Node& pn = p->nodes[vin.producer];
-            GemmArgs r;
-            r.M = p->batch; r.N = pn.d_out; r.K = pn.d_in;
-            r.A = val_ptr(p, pn.in, x); r.lda = pn.d_in; r.a_mn = 0;
-            r.B = (const char*)wbase + pn.w_off * dtype_size(dt); r.ldb = pn.d_out; r.b_k = 0;
-            r.in_type = dt;
-            r.bias = pn.has_bias ? params + pn.b_off : nullptr;
-            r.aux_type = dt;
-            r.out = p->ws + p->values[pn.z].off; r.ldo = pn.d_out; r.out_type = dt;
-            site(e, gemm_name(p, "recompute_z", pn.layer, r), 2.0 * r.M * r.N * r.K, gemm_bytes(r),
-                 1, [&] { return run_gemm(p, r, e.s); });
-          }
+          if (vin.producer_act == ACT_GELU) recompute_z(vin);
         }
         if (dadd) { h.resid = dadd; h.ldr = n.d_in; }
         h.out = grad_ptr(p, n.in); h.ldo = n.d_in; h.out_type = dt;
@@ -607,6 +708,40 @@ void backward_pass(Exec& e, const float* params, float* grads, const void* x) {
       }
       if (n.fuse_upd) weight_grad();   // after dX, the last reader of the bf16 weights
       if (ni != p->defer_dw) node_update(e, ni, fused);
+    } else if (n.kind == NK_GROUP) {
+      GroupArgs g = group_args(p, n, GROUP_DW);
+      g.A = val_ptr(p, n.in, x);
+      g.B = gy;
+      g.out = grads + n.w_off;
+      site(e, group_name(p, "grouped_dW", n), 2.0 * p->batch * n.d_in * n.d_out, group_bytes(p, n, true), 1,
+           [&] { return grouped_gemm(g, e.s); });
+      if (vin.need_grad) {
+        GroupArgs h = group_args(p, n, GROUP_DX);
+        h.A = gy;
+        h.B = (const char*)wbase + n.w_off * dtype_size(dt);
+        if (vin.producer_act) {
+          h.dact = vin.producer_act;
+          const int sv = vin.producer_act == ACT_GELU ? vin.z_value : n.in;
+          h.saved = p->ws + p->values[sv].off;
+          if (vin.producer_act == ACT_GELU) recompute_z(vin);
+        }
+        h.resid = dadd;
+        h.out = grad_ptr(p, n.in);
+        site(e, group_name(p, "grouped_dX", n), 2.0 * p->batch * n.d_in * n.d_out, group_bytes(p, n, false), 1,
+             [&] { return grouped_gemm(h, e.s); });
+      }
+      node_update(e, ni);
+    } else if (n.kind == NK_EMBED) {
+      char nm[96];
+      snprintf(nm, sizeof nm, "embedding_bwd[l%d] %d into %dx%d", n.layer, p->batch, n.d_in, n.d_out);
+      site(e, nm, 0, (double)dtype_size(dt) * p->batch * n.d_out + 4.0 * n.d_in * n.d_out,
+           embedding_bwd_launches(p->batch, n.d_in, n.d_out), [&] {
+             char* ws = p->ws + p->embed_off;
+             cudaError_t r = embedding_bwd_sort(0, x, p->batch, n.d_in, n.d_out, grads + n.w_off, ws, e.s);
+             if (r != cudaSuccess) return r;
+             return embedding_bwd_sum(dt, gy, p->batch, n.d_in, n.d_out, n.eps, grads + n.w_off, ws, e.s);
+           });
+      node_update(e, ni);
     } else if (n.kind == NK_RMSNORM) {
       void* dx = vin.need_grad ? grad_ptr(p, n.in) : nullptr;
       double bytes = (double)dtype_size(dt) * p->batch * n.d * (dx ? (dadd ? 4 : 3) : 2);
@@ -683,6 +818,7 @@ void train_schedule(Exec& e, float* params, float* grads, float* m, float* v, co
   forward_pass(e, params, x);
   loss_pass(e, labels);
   backward_pass(e, params, grads, x);
+  if (p->max_norm != 0.f) clipped_update(e);
   join_updates(e);
 }
 
@@ -713,7 +849,8 @@ mg_status compile(mg_plan* p, const mg_graph_desc* d) {
   // input width
   int w0 = -1;
   for (auto& l : p->layers) {
-    if (l.op == MG_OP_LINEAR) { w0 = l.d_in; break; }
+    if (l.op == MG_OP_EMBEDDING) { w0 = 1; break; }
+    if (l.op == MG_OP_LINEAR || l.op == MG_OP_GROUPED_LINEAR) { w0 = l.d_in; break; }
     if (l.op == MG_OP_RMSNORM) { w0 = l.d_in; break; }
     if (l.op == MG_OP_CAUSAL_ATTENTION) { w0 = 3 * l.n_heads * l.head_dim; break; }
   }
@@ -748,19 +885,54 @@ mg_status compile(mg_plan* p, const mg_graph_desc* d) {
     const mg_layer& l = p->layers[i];
     Value& vc = p->values[cur];
     switch (l.op) {
+      case MG_OP_EMBEDDING: {
+        if (i != 0) return fail(p, MG_ERR_UNSUPPORTED, "layer %d: an embedding must be the first layer", i);
+        if (l.d_in <= 0 || l.d_in == 0x7fffffff || l.d_out <= 0)
+          return fail(p, MG_ERR_SHAPE, "layer %d: bad embedding sizes (%d ids of width %d)", i, l.d_in, l.d_out);
+        if (!std::isfinite(l.eps)) return fail(p, MG_ERR_INVALID_ARG, "layer %d: the embedding's factor is not finite", i);
+        Node n;
+        n.kind = NK_EMBED;
+        n.layer = i;
+        n.in = cur;
+        n.d_in = l.d_in;
+        n.d_out = l.d_out;
+        n.eps = l.eps;
+        n.t0 = (int)p->p_off.size();
+        n.w_off = add_param(l.d_in, l.d_out, 1);
+        n.nt = 1;
+        int ni = (int)p->nodes.size();
+        n.out = new_value(l.d_out, ni);
+        p->values[n.in].consumers++;
+        p->nodes.push_back(n);
+        cur = n.out;
+        break;
+      }
+      case MG_OP_GROUPED_LINEAR:
       case MG_OP_LINEAR: {
+        const bool grouped = l.op == MG_OP_GROUPED_LINEAR;
         if (l.d_in <= 0 || l.d_out <= 0) return fail(p, MG_ERR_SHAPE, "layer %d: bad Linear widths", i);
         if (l.d_in != vc.width)
           return fail(p, MG_ERR_SHAPE, "layer %d: Linear d_in %d != incoming width %d", i, l.d_in, vc.width);
+        if (grouped) {
+          if (l.n_heads < 1 || (long long)l.n_heads * l.d_in > 0x7fff0000ll)
+            return fail(p, MG_ERR_SHAPE, "layer %d: bad group count %d", i, l.n_heads);
+          if (l.n_heads > kMaxGroups)
+            return fail(p, MG_ERR_UNSUPPORTED, "layer %d: at most %d groups", i, kMaxGroups);
+          if (l.has_bias) return fail(p, MG_ERR_UNSUPPORTED, "layer %d: a grouped Linear has no bias", i);
+          if (p->n_groups && p->n_groups != l.n_heads)
+            return fail(p, MG_ERR_UNSUPPORTED, "layer %d: %d groups, an earlier layer has %d", i, l.n_heads, p->n_groups);
+          p->n_groups = l.n_heads;
+        }
         Node n;
-        n.kind = NK_LINEAR;
+        n.kind = grouped ? NK_GROUP : NK_LINEAR;
+        n.groups = grouped ? l.n_heads : 0;
         n.layer = i;
         n.in = cur;
         n.d_in = l.d_in;
         n.d_out = l.d_out;
         n.has_bias = l.has_bias ? 1 : 0;
         n.t0 = (int)p->p_off.size();
-        n.w_off = add_param(l.d_in, l.d_out, 1);
+        n.w_off = add_param(grouped ? l.n_heads * l.d_in : l.d_in, l.d_out, 1);
         if (n.has_bias) n.b_off = add_param(1, l.d_out, 0);
         n.nt = (int)p->p_off.size() - n.t0;
         if (i + 1 < nl && (p->layers[i + 1].op == MG_OP_RELU || p->layers[i + 1].op == MG_OP_GELU_TANH)) {
@@ -857,7 +1029,7 @@ mg_status compile(mg_plan* p, const mg_graph_desc* d) {
   p->final_value = cur;
   p->n_params = round_up(poff, kAlignElems);
   if (p->p_off.empty()) return fail(p, MG_ERR_INVALID_ARG, "graph has no parameters");
-  if (p->dt == DT_BF16 && p->values[0].width % 8)
+  if (p->dt == DT_BF16 && p->values[0].width % 8 && p->nodes[0].kind != NK_EMBED)
     return fail(p, MG_ERR_ALIGN, "bf16 input rows must be a multiple of 16 bytes");
 
   // which values need a gradient: anything downstream of a parameter
@@ -972,7 +1144,7 @@ void layout_workspace(mg_plan* p) {
   std::vector<char> is_z(p->values.size(), 0);
   size_t zmax = 0;
   for (const Node& n : p->nodes)
-    if (n.z >= 0) {
+    if (n.z >= 0 && n.kind == NK_LINEAR) {
       is_z[n.z] = 1;
       zmax = std::max(zmax, (size_t)p->values[n.z].width);
     }
@@ -1002,6 +1174,14 @@ void layout_workspace(mg_plan* p) {
     }
   }
   if (p->dt == DT_BF16) p->shadow_off = b.take(p->n_params * 2);
+  size_t group_ws = 0;
+  for (const Node& n : p->nodes) {
+    if (n.kind == NK_EMBED) p->embed_off = b.take(embedding_ws_bytes(p->batch, n.d_in, n.d_out));
+    if (n.kind == NK_GROUP && p->dt == DT_BF16)
+      group_ws = std::max(group_ws, grouped_narrow_ws_bytes(p->batch, n.groups, n.d_in, n.d_out));
+  }
+  p->group_bytes = group_ws;
+  if (group_ws) p->group_off = b.take(group_ws);
   // chunks
   p->n_chunks = 0;
   for (size_t t = 0; t < p->p_off.size(); ++t) {
@@ -1074,6 +1254,10 @@ void build_dump(mg_plan* p) {
   snprintf(b, sizeof b, "  gradient storage: %zu bytes (%zu without lifetime sharing%s)\n",
            p->grad_bytes, p->grad_bytes_unaliased, p->alias ? "" : "; MG_NO_ALIAS set");
   s += b;
+  if (p->max_norm != 0.f) {
+    snprintf(b, sizeof b, "  gradients clipped to a global norm of %g\n", p->max_norm);
+    s += b;
+  }
   if (p->recompute_gelu) s += "  GELU pre-activations: recomputed in the backward (MG_RECOMPUTE_GELU set)\n";
   for (const Node& n : p->nodes)
     if (n.fuse_upd) {
@@ -1269,6 +1453,7 @@ mg_status mg_step_plan_create(const mg_graph_desc* desc, mg_plan** out) {
   std::vector<Chunk> ch = chunk_table(p);
   e = cudaMemcpy(p->ws + p->chunks_off, ch.data(), ch.size() * sizeof(Chunk), cudaMemcpyHostToDevice);
   if (e == cudaSuccess) e = cudaMemset(p->ws + p->loss_off, 0, 16);
+  if (e == cudaSuccess && p->group_bytes) e = cudaMemset(p->ws + p->group_off, 0, p->group_bytes);
   // the optimizer stream gets the lowest priority: when a backward GEMM and
   // optimizer blocks wait for SMs together, the GEMM's CTAs go first
   int prio_lo = 0, prio_hi = 0;
@@ -1311,6 +1496,7 @@ void mg_step_plan_destroy(mg_plan* p) {
   if (p->join_ev) cudaEventDestroy(p->join_ev);
   if (p->aux) cudaStreamDestroy(p->aux);
   if (p->ws) cudaFree(p->ws);
+  if (p->clip_ws) cudaFree(p->clip_ws);
   if (prev >= 0) cudaSetDevice(prev);
   delete p;
 }
@@ -1336,6 +1522,8 @@ mg_status mg_forward(mg_plan* p, const float* params, const void* x, float* out,
   if (!params || !x || !out) return fail(p, MG_ERR_INVALID_ARG, "params, x and out must be non-NULL");
   if (!aligned16(params) || !aligned16(x) || !aligned16(out))
     return fail(p, MG_ERR_ALIGN, "params, x and out must be 16-byte aligned");
+  if (p->n_groups && !p->row_groups)
+    return fail(p, MG_ERR_INVALID_ARG, "the plan has grouped layers: call mg_set_row_groups first");
   mg_status st = check_device(p);
   if (st != MG_OK) return st;
   cudaStream_t s = (cudaStream_t)stream;
@@ -1375,6 +1563,8 @@ mg_status mg_train_step(mg_plan* p, float* params, float* grads, float* adam_m, 
   const size_t nb = p->n_params * sizeof(float);
   const char *pa = (const char*)params, *ga = (const char*)grads;
   if (pa < ga + nb && ga < pa + nb) return fail(p, MG_ERR_INVALID_ARG, "grads must not alias params");
+  if (p->n_groups && !p->row_groups)
+    return fail(p, MG_ERR_INVALID_ARG, "the plan has grouped layers: call mg_set_row_groups first");
   if (!(std::isfinite(lr))) return fail(p, MG_ERR_INVALID_ARG, "lr is not finite");
   mg_status st = check_device(p);
   if (st != MG_OK) return st;
@@ -1412,6 +1602,68 @@ mg_status mg_train_step(mg_plan* p, float* params, float* grads, float* adam_m, 
   if (p->profiling && p->prof_calls < p->prof_max) p->prof_calls++;
   p->last_launches = ex.launches;
   if (ex.err != cudaSuccess) return cuda_fail(p, ex.err, "mg_train_step launch");
+  return MG_OK;
+}
+
+mg_status mg_set_row_groups(mg_plan* p, const int* offsets) {
+  if (!p || !offsets) return fail(p, MG_ERR_INVALID_ARG, "plan and offsets must be non-NULL");
+  if (!p->n_groups) return fail(p, MG_ERR_INVALID_ARG, "the plan has no grouped layers");
+  if (reinterpret_cast<uintptr_t>(offsets) % 4) return fail(p, MG_ERR_ALIGN, "offsets must be 4-byte aligned");
+  if (offsets != p->row_groups)
+    for (auto& g : p->graphs) {      // captured steps hold the old pointer
+      drop_graph(g);
+      g.calls = 0;
+    }
+  p->row_groups = offsets;
+  return MG_OK;
+}
+
+mg_status mg_set_grad_clip(mg_plan* p, float max_norm) {
+  if (!p) return fail(nullptr, MG_ERR_INVALID_ARG, "plan is NULL");
+  if (!(max_norm >= 0.f)) return fail(p, MG_ERR_INVALID_ARG, "max_norm must be positive, or 0 for no clipping");
+  if (p->profiling) return fail(p, MG_ERR_INVALID_ARG, "mg_set_grad_clip while profiling");
+  mg_status st = check_device(p);
+  if (st != MG_OK) return st;
+  if (max_norm != 0.f && !p->clip_ws) {
+    const size_t bytes = 64 + ((size_t)kNormParts + p->n_chunks) * sizeof(double);
+    cudaError_t e = cudaMalloc((void**)&p->clip_ws, bytes);
+    if (e != cudaSuccess) {
+      cudaGetLastError();
+      p->clip_ws = nullptr;
+      return fail(p, MG_ERR_OOM, "clipping workspace of %zu bytes: %s", bytes, cudaGetErrorString(e));
+    }
+    e = cudaMemset(p->clip_ws, 0, bytes);
+    if (e != cudaSuccess) {
+      cudaFree(p->clip_ws);
+      p->clip_ws = nullptr;
+      return cuda_fail(p, e, "mg_set_grad_clip");
+    }
+  }
+  if (max_norm == p->max_norm) return MG_OK;
+  p->max_norm = max_norm;
+  for (auto& g : p->graphs) {        // captured steps are the old schedule
+    drop_graph(g);
+    g.calls = 0;
+  }
+  plan_fused_updates(p);
+  p->sites.clear();
+  Exec ex{p, nullptr, true, false};
+  train_schedule(ex, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, 0.f, 1);
+  build_dump(p);
+  return MG_OK;
+}
+
+const float* mg_grad_norm_device_ptr(const mg_plan* p) {
+  return p ? reinterpret_cast<const float*>(p->clip_ws) : nullptr;
+}
+
+mg_status mg_grad_norm(mg_plan* p, float* host_norm_and_factor, mg_stream_t stream) {
+  if (!p || !host_norm_and_factor) return fail(p, MG_ERR_INVALID_ARG, "plan and destination must be non-NULL");
+  if (!p->clip_ws) return fail(p, MG_ERR_INVALID_ARG, "clipping was never turned on (mg_set_grad_clip)");
+  cudaError_t e = cudaMemcpyAsync(host_norm_and_factor, clip_stats(p), 8, cudaMemcpyDeviceToHost,
+                                  (cudaStream_t)stream);
+  if (e == cudaSuccess) e = cudaStreamSynchronize((cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(p, e, "mg_grad_norm");
   return MG_OK;
 }
 

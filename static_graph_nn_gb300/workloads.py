@@ -71,8 +71,19 @@ def causal_attention(n_heads: int, head_dim: int, seq_len: int) -> dict:
             "seq_len": seq_len}
 
 
+def embedding(vocab: int, dim: int, scale: float = 1.0) -> dict:
+    """First layer only: rows scale * W[id] of int32 ids."""
+    return {"op": "embedding", "vocab": vocab, "dim": dim, "scale": float(scale)}
+
+
+def grouped_linear(groups: int, d_in: int, d_out: int) -> dict:
+    """One weight per row group (``Plan.set_row_groups``)."""
+    return {"op": "grouped_linear", "groups": groups, "d_in": d_in, "d_out": d_out}
+
+
 def param_shapes(layers: list[dict]) -> list[tuple[str, tuple[int, ...]]]:
-    """Trainable tensors in declaration order: W[in,out] then b[out]; gamma[d]."""
+    """Trainable tensors in declaration order: W[in,out] then b[out]; gamma[d];
+    table[vocab,dim]; grouped W[groups,in,out]."""
     out = []
     for i, l in enumerate(layers):
         if l["op"] == "linear":
@@ -81,12 +92,18 @@ def param_shapes(layers: list[dict]) -> list[tuple[str, tuple[int, ...]]]:
                 out.append((f"l{i}.b", (l["d_out"],)))
         elif l["op"] == "rmsnorm":
             out.append((f"l{i}.gamma", (l["d"],)))
+        elif l["op"] == "embedding":
+            out.append((f"l{i}.table", (l["vocab"], l["dim"])))
+        elif l["op"] == "grouped_linear":
+            out.append((f"l{i}.w", (l["groups"], l["d_in"], l["d_out"])))
     return out
 
 
 def input_width(layers: list[dict]) -> int:
     for l in layers:
-        if l["op"] == "linear":
+        if l["op"] == "embedding":
+            return 1                       # one id a row
+        if l["op"] in ("linear", "grouped_linear"):
             return l["d_in"]
         if l["op"] == "rmsnorm":
             return l["d"]
@@ -95,8 +112,10 @@ def input_width(layers: list[dict]) -> int:
 
 def output_width(layers: list[dict]) -> int:
     for l in reversed(layers):
-        if l["op"] == "linear":
+        if l["op"] in ("linear", "grouped_linear"):
             return l["d_out"]
+        if l["op"] == "embedding":
+            return l["dim"]
         if l["op"] == "rmsnorm":
             return l["d"]
     raise ValueError("graph has no layer that fixes the output width")
@@ -136,11 +155,11 @@ class Workload:
         f = 0.0
         upstream_param = False
         for l in self.layers:
-            if l["op"] == "linear":
+            if l["op"] in ("linear", "grouped_linear"):
                 g = 2.0 * self.batch * l["d_in"] * l["d_out"]
                 f += g * (3.0 if upstream_param else 2.0)
                 upstream_param = True
-            elif l["op"] == "rmsnorm":
+            elif l["op"] in ("rmsnorm", "embedding"):
                 upstream_param = True
             elif l["op"] == "causal_attention":
                 h, dh, s = l["n_heads"], l["head_dim"], l["seq_len"]
@@ -338,7 +357,7 @@ def init_params(w: Workload) -> list[np.ndarray]:
         elif name.endswith(".gamma"):
             out.append(np.ones(shape, dtype=np.float32))
         else:
-            fan_in, fan_out = shape
+            fan_in, fan_out = shape[-2:]
             if w.init == "he_normal":
                 a = normal(s, n, 0.0, math.sqrt(2.0 / fan_in))
             elif w.init == "xavier_uniform":
@@ -353,7 +372,11 @@ def init_params(w: Workload) -> list[np.ndarray]:
 
 
 def make_x(w: Workload) -> np.ndarray:
+    """float32 [batch, d_in]; int32 ids [batch] for a graph that begins with an
+    embedding."""
     s = stream_seed(base_seed(w), 1000)
+    if w.layers[0]["op"] == "embedding":
+        return class_ids(s, w.batch, w.layers[0]["vocab"])
     n = w.batch * w.d_in
     if w.x_dist == "uniform01":
         a = uniform01(s, n)

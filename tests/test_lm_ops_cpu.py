@@ -7,6 +7,7 @@ import pytest
 
 import __graft_entry__
 from static_graph_nn_gb300 import binding
+from static_graph_nn_gb300 import workloads as W
 
 torch = pytest.importorskip("torch")
 
@@ -25,7 +26,7 @@ def _fwd(lib, tt=0, table=P, v=10, d=8, kind=0, ids=P, n=4, scale=1.0, ot=0, out
     return lib.mg_embedding_forward(tt, table, v, d, kind, ids, n, scale, ot, out, None)
 
 
-def _bwd(lib, t=0, dout=P, v=10, d=8, kind=0, ids=P, n=4, scale=1.0, dtable=P, ws=P, nb=1 << 20):
+def _bwd(lib, t=0, dout=P, v=10, d=8, kind=0, ids=P, n=4, scale=1.0, dtable=P, ws=P, nb=1 << 30):
     return lib.mg_embedding_backward(t, dout, v, d, kind, ids, n, scale, dtable, ws, nb, None)
 
 
@@ -60,7 +61,7 @@ def test_workspace_sizes(lib):
     assert lib.mg_grouped_linear_workspace_bytes(0, 1, 8, 8) >= 4
 
 
-def _grouped(lib, which, dtype=1, a=P, b=P, off=P, rows=4, groups=2, k=8, n=8, out=P, ws=P, nb=1 << 20):
+def _grouped(lib, which, dtype=1, a=P, b=P, off=P, rows=4, groups=2, k=8, n=8, out=P, ws=P, nb=1 << 30):
     if which == "backward_weight":
         return lib.mg_grouped_linear_backward_weight(dtype, a, b, off, rows, groups, k, n, out, ws, nb, None)
     f = getattr(lib, "mg_grouped_linear_" + which)
@@ -128,3 +129,40 @@ def _z(*shape, dtype=None):
 def test_wrappers_refuse(lib, call):
     with pytest.raises(binding.MGError):
         call()
+
+
+def _create(lib, layers, batch=8, precision="strict"):
+    arr = (binding.mg_layer * len(layers))(*[binding.layer_struct(l) for l in layers])
+    d = binding.mg_graph_desc()
+    d.batch, d.n_layers, d.layers = batch, len(layers), arr
+    d.loss, d.precision, d.optimizer = 0, binding.PRECISIONS[precision], binding.OPTIMIZERS["sgd"]
+    h = ctypes.c_void_p()
+    st = lib.mg_step_plan_create(ctypes.byref(d), ctypes.byref(h))
+    if st == 0:
+        lib.mg_step_plan_destroy(h)
+    return st
+
+
+@pytest.mark.parametrize("layers,want", [
+    ([W.linear(4, 8, False), W.embedding(10, 8), W.linear(8, 4, False)], U),
+    ([W.embedding(0, 8), W.linear(8, 4, False)], S),
+    ([W.embedding(10, -8), W.linear(8, 4, False)], S),
+    ([W.embedding(10, 8, float("inf")), W.linear(8, 4, False)], E),
+    ([W.embedding(10, 8), W.linear(9, 4, False)], S),
+    ([W.embedding(10, 8), W.relu(), W.linear(8, 4, False)], U),
+    ([W.grouped_linear(0, 8, 4)], S),
+    ([W.grouped_linear(1025, 8, 4)], U),
+    ([W.grouped_linear(2, 8, 4), W.linear(5, 4, False)], S),
+    ([W.grouped_linear(2, 8, 8), W.grouped_linear(3, 8, 4)], U),
+    ([W.grouped_linear(2, 8, 8), W.relu()], U),
+])
+def test_layer_refusals(lib, layers, want):
+    assert _create(lib, layers) == want
+
+
+def test_null_plan_in_the_new_calls(lib):
+    f = (ctypes.c_float * 2)()
+    assert lib.mg_set_row_groups(None, P) == E
+    assert lib.mg_set_grad_clip(None, 1.0) == E
+    assert lib.mg_grad_norm_device_ptr(None) is None
+    assert lib.mg_grad_norm(None, f, None) == E
