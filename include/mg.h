@@ -393,9 +393,8 @@ mg_status mg_embedding_backward(int dtype, const void* dout, int vocab, int dim,
  * group is 0.  groups at most 1024.  bf16 widths that are multiples of 8 run
  * on the tensor cores, others and fp32 on the CUDA cores.
  * workspace: mg_grouped_linear_workspace_bytes; zero it once before its first
- * use (the calls leave its counters zero).  Its first int is set to 1 if a
- * bounded device-side wait gave up, in which case that call's results are
- * invalid. */
+ * use.  Its first int is set to 1 if a bounded device-side wait gave up, in
+ * which case that call's results are invalid. */
 size_t mg_grouped_linear_workspace_bytes(int rows, int groups, int d_in, int d_out);
 mg_status mg_grouped_linear_forward(int dtype, const void* x, const int* offsets, int rows, int groups,
                                     int d_in, int d_out, const void* w, void* y, void* workspace,

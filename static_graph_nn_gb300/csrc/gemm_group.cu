@@ -200,10 +200,6 @@ cudaError_t simt_launch(const GroupArgs& g, cudaStream_t s) {
 
 }  // namespace
 
-size_t group_ws_bytes(int rows, int groups, int d_in, int d_out) {
-  return 256 + grouped_narrow_ws_bytes(rows, groups, d_in, d_out);
-}
-
 cudaError_t grouped_gemm(const GroupArgs& g, cudaStream_t s) {
   if (g.rows == 0 && g.kind != GROUP_DW) return cudaSuccess;
   if (grouped_tc_eligible(g)) return grouped_gemm_tc(g, s);
@@ -224,6 +220,8 @@ namespace {
 
 using mg::op_fail;
 
+constexpr size_t kGroupedWorkspace = 256;   // begins with the error word
+
 mg_status grouped_call(const char* fn, mg::GroupKind kind, int dtype, const void* a, const void* b,
                        const int* offsets, int rows, int groups, int d_in, int d_out, void* out, void* ws,
                        size_t ws_bytes, mg_stream_t stream) {
@@ -237,7 +235,7 @@ mg_status grouped_call(const char* fn, mg::GroupKind kind, int dtype, const void
   const bool dw = kind == mg::GROUP_DW;
   if (!offsets || !ws || (rows_needed && !a) || (!b && (rows_needed || !dw)) || (!out && (rows_needed || dw)))
     return op_fail(MG_ERR_INVALID_ARG, "%s: a pointer is NULL", fn);
-  const size_t need = mg::group_ws_bytes(rows, groups, d_in, d_out);
+  const size_t need = kGroupedWorkspace;
   if (ws_bytes < need)
     return op_fail(MG_ERR_INVALID_ARG, "%s: the workspace needs %zu bytes, %zu given", fn, need, ws_bytes);
   mg_status st = mg::op_begin(fn, {{a, 16}, {b, 16}, {offsets, 4}, {out, 16}, {ws, 16}});
@@ -254,7 +252,6 @@ mg_status grouped_call(const char* fn, mg::GroupKind kind, int dtype, const void
   g.B = b;
   g.out = out;
   g.err = static_cast<int*>(ws);
-  g.ws = g.err + 64;
   return mg::op_end(fn, mg::grouped_gemm(g, (cudaStream_t)stream));
 }
 
@@ -262,7 +259,7 @@ mg_status grouped_call(const char* fn, mg::GroupKind kind, int dtype, const void
 
 extern "C" size_t mg_grouped_linear_workspace_bytes(int rows, int groups, int d_in, int d_out) {
   if (rows < 0 || groups < 1 || groups > mg::kMaxGroups || d_in < 1 || d_out < 1) return 0;
-  return mg::group_ws_bytes(rows, groups, d_in, d_out);
+  return kGroupedWorkspace;
 }
 
 extern "C" mg_status mg_grouped_linear_forward(int dtype, const void* x, const int* offsets, int rows, int groups,

@@ -118,11 +118,6 @@ __device__ __forceinline__ void tma_load_3d_to_leader(void* dst, const CUtensorM
       : "memory");
 }
 
-// Remote arrive that publishes this thread's earlier writes to the cluster.
-__device__ __forceinline__ void mbar_arrive_remote_release(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-
 template <int KIND, typename TO>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(group_threads(KIND), 1)
     group_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,

@@ -212,16 +212,12 @@ struct GroupArgs {
   const void* resid = nullptr;
   int zero_rest = 0;           // rows of no group are computed as if A were 0 there
   int* err = nullptr;          // set to 1 on a timed-out wait
-  int* ws = nullptr;           // grouped_narrow_ws_bytes, counters zero between calls; NULL: none
 };
-// Workspace of an entry point: 256 bytes that begin with the error word, then ws.
-size_t group_ws_bytes(int rows, int groups, int d_in, int d_out);
 constexpr int kMaxGroups = 1024;
 cudaError_t grouped_gemm(const GroupArgs& g, cudaStream_t s);
-// The version for a few rows per group (forward and dX, where ws is given;
-// grouped_tc_eligible as well).
+// The version for a few rows per group (forward and dX; grouped_tc_eligible as
+// well).
 bool grouped_narrow(const GroupArgs& g);
-size_t grouped_narrow_ws_bytes(int rows, int groups, int d_in, int d_out);
 cudaError_t grouped_gemm_narrow(const GroupArgs& g, cudaStream_t s);
 // The tensor-core version: bf16, widths that are multiples of 8.
 bool grouped_tc_eligible(const GroupArgs& g);

@@ -121,7 +121,6 @@ struct mg_plan {
          colsum_off = 0, flag_off = 0, lse_part_off = 0;
   size_t split_off = 0, split_floats = 0;   // strict weight gradients split over K
   size_t embed_off = 0;      // embedding gradient's workspace
-  size_t group_bytes = 0, group_off = 0;      // grouped products' counters and partials (zero between calls)
   int n_groups = 0;          // of the grouped layers; 0: there are none
   const int* row_groups = nullptr;   // caller's offsets
   // clipping by the global norm (mg_set_grad_clip): 0 off
@@ -343,7 +342,6 @@ GroupArgs group_args(mg_plan* p, const Node& n, GroupKind kind) {
   g.offsets = p->row_groups;
   g.zero_rest = 1;
   g.err = reinterpret_cast<int*>(p->ws + p->loss_off + 4);
-  if (p->group_off) g.ws = wsp<int>(p, p->group_off);
   return g;
 }
 
@@ -1174,14 +1172,8 @@ void layout_workspace(mg_plan* p) {
     }
   }
   if (p->dt == DT_BF16) p->shadow_off = b.take(p->n_params * 2);
-  size_t group_ws = 0;
-  for (const Node& n : p->nodes) {
+  for (const Node& n : p->nodes)
     if (n.kind == NK_EMBED) p->embed_off = b.take(embedding_ws_bytes(p->batch, n.d_in, n.d_out));
-    if (n.kind == NK_GROUP && p->dt == DT_BF16)
-      group_ws = std::max(group_ws, grouped_narrow_ws_bytes(p->batch, n.groups, n.d_in, n.d_out));
-  }
-  p->group_bytes = group_ws;
-  if (group_ws) p->group_off = b.take(group_ws);
   // chunks
   p->n_chunks = 0;
   for (size_t t = 0; t < p->p_off.size(); ++t) {
@@ -1453,7 +1445,6 @@ mg_status mg_step_plan_create(const mg_graph_desc* desc, mg_plan** out) {
   std::vector<Chunk> ch = chunk_table(p);
   e = cudaMemcpy(p->ws + p->chunks_off, ch.data(), ch.size() * sizeof(Chunk), cudaMemcpyHostToDevice);
   if (e == cudaSuccess) e = cudaMemset(p->ws + p->loss_off, 0, 16);
-  if (e == cudaSuccess && p->group_bytes) e = cudaMemset(p->ws + p->group_off, 0, p->group_bytes);
   // the optimizer stream gets the lowest priority: when a backward GEMM and
   // optimizer blocks wait for SMs together, the GEMM's CTAs go first
   int prio_lo = 0, prio_hi = 0;

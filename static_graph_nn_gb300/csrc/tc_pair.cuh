@@ -34,6 +34,11 @@ static __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr)
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
+// Remote arrive that publishes this thread's earlier writes to the cluster.
+static __device__ __forceinline__ void mbar_arrive_remote_release(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // TMA load into this CTA's shared memory whose completion is counted on the
 // leader CTA's barrier (cluster address bar_cluster).
 static __device__ __forceinline__ void tma_load_2d_to_leader(void* dst, const CUtensorMap* map,

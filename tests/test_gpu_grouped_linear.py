@@ -83,6 +83,8 @@ SHAPES = [
     # rows, groups, d_in, d_out
     (1, 1, 8, 8), (1, 3, 64, 256), (5, 4, 72, 136), (24, 8, 512, 1024), (63, 2, 8, 264), (64, 1, 64, 64),
     (300, 7, 200, 328), (1000, 16, 520, 1032), (129, 5, 256, 128), (2049, 3, 136, 264), (700, 64, 264, 72),
+    # few tiles and a long sum: two or four blocks share one
+    (20, 3, 2048, 200), (7, 1, 4104, 72), (30, 2, 200, 1160), (16, 1, 1088, 2304),
     # widths that rows of 16 bytes do not divide
     (77, 3, 33, 17), (300, 5, 1, 1), (50, 2, 100, 65),
 ]
