@@ -366,10 +366,9 @@ def _code(t, name: str, table: dict | None = None) -> int:
 
 
 def _dense(t, name: str, shape: tuple | None = None):
+    # (memory that is not this device's is refused by the library)
     if not t.is_contiguous():
         _refuse(f"{name} must be contiguous (strides {tuple(t.stride())})")
-    if not t.is_cuda:
-        _refuse(f"{name} must be a CUDA tensor")
     if shape is not None and t.shape != shape:
         _refuse(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}", MG_ERR_SHAPE)
 

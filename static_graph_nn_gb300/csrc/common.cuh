@@ -150,6 +150,13 @@ __device__ __forceinline__ void ld16bf(const bf16* p, float* f) {
   }
 }
 
+// Programmatic dependent launch.  A kernel launched as the dependent of the one
+// before it may start while that one still runs; everything it does before
+// dependency_wait must not touch what the earlier kernel writes.  The earlier
+// kernel calls dependents_start where its blocks no longer need the room.
+__device__ __forceinline__ void dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void dependents_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // Column sums over a warp's 32 rows: lane l holds row l's 32 consecutive
 // columns in x; returns the sum of column l over the 32 lanes.  A butterfly
 // reduce-scatter: at each of five steps every lane keeps one half of its

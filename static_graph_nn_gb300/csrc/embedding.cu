@@ -381,6 +381,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSmallThreads
     sort_small_kernel(const SmallArgs A) {
   extern __shared__ __align__(16) uint8_t raw[];
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  dependents_start();
   if (blockIdx.x >= kCluster) {
     // ---- zero rows of a contiguous range of the table
     uint32_t* bits = reinterpret_cast<uint32_t*>(raw);
@@ -665,6 +666,7 @@ __global__ void __launch_bounds__(256, 2) embed_sum_kernel(const SumArgs A) {
   __shared__ int last[2][256];
   const int lane = threadIdx.x % A.tpr, sub = threadIdx.x / A.tpr, rpb = 256 / A.tpr;
   const uint32_t items = A.n_windows * (uint32_t)A.col_tiles;
+  dependency_wait();
   for (uint32_t base = blockIdx.x * rpb; base < items; base += gridDim.x * rpb) {
     const uint32_t it = base + sub;
     const uint32_t win = it / A.col_tiles;
@@ -931,8 +933,7 @@ static cudaError_t sum_launch(const SumArgs& A, unsigned grid, cudaStream_t s) {
   static const cudaError_t attr = cudaFuncSetAttribute(embed_sum_kernel<T, VEC>,
                                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (attr != cudaSuccess) return attr;
-  embed_sum_kernel<T, VEC><<<grid, 256, smem, s>>>(A);
-  return cudaGetLastError();
+  return launch_dependent(embed_sum_kernel<T, VEC>, grid, 256, smem, s, A);
 }
 
 cudaError_t embedding_bwd_sum(DType t, const void* dout, long long n, int V, int d, float scale, float* dtable,

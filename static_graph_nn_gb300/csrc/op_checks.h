@@ -27,6 +27,24 @@ mg_status op_begin(const char* fn, std::initializer_list<OpPtr> ptrs);
 // The status of a call whose launches returned e.
 mg_status op_end(const char* fn, cudaError_t e);
 
+// Launch kern as a programmatic dependent of the kernel before it on s.
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kern)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t s,
+                             A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 // Multiprocessors of the current device.
 int device_sms();
 
