@@ -53,9 +53,31 @@ struct ClipChunk {
 };
 
 struct ClipSync {
-  unsigned long long arrived;   // blocks that have reached the barrier, over all calls
-  unsigned last;                // blocks that have written their partial sum
+  unsigned long long calls;     // fused calls finished
+  unsigned last;                // blocks that have written their partial sum (two-pass calls)
 };
+
+// A block's sum with the number of the call it belongs to, written and read as
+// one 16-byte word: a reader that finds its call's number has the sum.
+struct alignas(16) ClipSum {
+  double sum;
+  unsigned long long call;
+};
+__device__ __forceinline__ void put_sum(ClipSum* p, double sum, unsigned long long call) {
+  asm volatile("{\n.reg .b128 v;\nmov.b128 v, {%1, %2};\nst.relaxed.gpu.global.b128 [%0], v;\n}\n" ::"l"(p),
+               "l"(__double_as_longlong(sum)), "l"(call)
+               : "memory");
+}
+__device__ __forceinline__ bool get_sum(const ClipSum* p, unsigned long long call, double& sum) {
+  long long lo;
+  unsigned long long hi;
+  asm volatile("{\n.reg .b128 v;\nld.relaxed.gpu.global.b128 v, [%2];\nmov.b128 {%0, %1}, v;\n}\n"
+               : "=l"(lo), "=l"(hi)
+               : "l"(p)
+               : "memory");
+  sum = __longlong_as_double(lo);
+  return hi == call;
+}
 
 __device__ __forceinline__ double block_sum_f64(double v, double* red /* 32 */) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = blockDim.x >> 5;
@@ -195,44 +217,51 @@ __device__ __forceinline__ void chunk_store(const ClipChunk& c, const ClipData& 
   });
 }
 
-// The norm and the factor from the blocks' sums, added in order by one block.
-__device__ __forceinline__ float2 clip_finish(const double* partial, int n, float max_norm, double* red) {
-  double s = 0.0;
-  for (int i = threadIdx.x; i < n; i += kClipThreads) s += __ldcg(partial + i);
-  s = block_sum_f64(s, red);
-  const double norm = sqrt(s);
+// The norm and the factor.
+__device__ __forceinline__ float2 clip_factor(double sum, float max_norm) {
+  const double norm = sqrt(sum);
   const bool finite = norm - norm == 0.0;
   return make_float2((float)norm, finite && norm > (double)max_norm ? (float)((double)max_norm / norm) : 1.0f);
 }
 
-// One chunk per block, all blocks resident (cooperative launch).
+// The same from the blocks' sums, added in order by one block.
+__device__ __forceinline__ float2 clip_finish(const double* partial, int n, float max_norm, double* red) {
+  double s = 0.0;
+  for (int i = threadIdx.x; i < n; i += kClipThreads) s += __ldcg(partial + i);
+  return clip_factor(block_sum_f64(s, red), max_norm);
+}
+
+// One chunk per block, all blocks resident (cooperative launch).  The barrier is
+// the exchange of the sums itself: every block waits for every block's sum of
+// this call and adds them in the same order.
 __global__ void __launch_bounds__(kClipThreads, kClipFusedPerSm)
-    clip_fused_kernel(const ClipChunk* chunks, double* partial, ClipSync* sync, float max_norm, float* stats) {
+    clip_fused_kernel(const ClipChunk* chunks, ClipSum* sums, ClipSync* sync, float max_norm, float* stats) {
   __shared__ double red[32];
-  __shared__ int ok;
   const ClipChunk c = chunks[blockIdx.x];
+  const unsigned long long call = *reinterpret_cast<volatile unsigned long long*>(&sync->calls) + 1;
   ClipData d;
   d.load(c);
   const double t = block_sum_f64(chunk_squares(c, d), red);
-  if (threadIdx.x == 0) {
-    partial[blockIdx.x] = t;
-    __threadfence();
-    const unsigned long long n = gridDim.x;
-    const unsigned long long want = (atomicAdd(&sync->arrived, 1ull) / n + 1) * n;
+  if (threadIdx.x == 0) put_sum(sums + blockIdx.x, t, call);
+  double s = 0.0;
+  bool ok = true;
+  for (int i = threadIdx.x; i < (int)gridDim.x; i += kClipThreads) {
+    double v;
     unsigned spin = 0;
-    while (*reinterpret_cast<volatile unsigned long long*>(&sync->arrived) < want && ++spin < kClipSpin) __nanosleep(20);
-    ok = spin < kClipSpin;
-    __threadfence();
+    while (!get_sum(sums + i, call, v) && ++spin < kClipSpin) {}
+    ok = ok && spin < kClipSpin;
+    s += v;
   }
-  __syncthreads();
-  if (!ok) {           // the results of this call are invalid: say so in the norm
+  if (!__syncthreads_and(ok)) {      // the results of this call are invalid: say so in the norm
     if (threadIdx.x == 0) stats[0] = stats[1] = __int_as_float(0x7fffffff);
+    if (blockIdx.x == 0 && threadIdx.x == 0) sync->calls = call;
     return;
   }
-  const float2 r = clip_finish(partial, gridDim.x, max_norm, red);
+  const float2 r = clip_factor(block_sum_f64(s, red), max_norm);
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     stats[0] = r.x;
     stats[1] = r.y;
+    sync->calls = call;              // every block has read the old number: its sum is there
   }
   if (r.y == 1.0f && c.out == c.g) return;
   chunk_store(c, d, r.y);
@@ -418,7 +447,7 @@ extern "C" mg_status mg_grad_list_create(int n, const void* const* grads, void* 
     l->fused = coop && l->n_chunks > 0 && l->n_chunks <= l->sms * std::min(per_sm, mg::kClipFusedPerSm);
     const size_t blocks = std::max<size_t>(l->fused ? table.size() : 1, (size_t)l->sms * 4);
     l->partial_off = (table.size() * sizeof(mg::ClipChunk) + 255) / 256 * 256;
-    l->sync_off = l->partial_off + blocks * sizeof(double);
+    l->sync_off = l->partial_off + blocks * sizeof(mg::ClipSum);
     const size_t bytes = l->sync_off + sizeof(mg::ClipSync);
     if (e == cudaSuccess) e = cudaMalloc((void**)&l->ws, bytes);
     if (e != cudaSuccess) {
@@ -428,7 +457,7 @@ extern "C" mg_status mg_grad_list_create(int n, const void* const* grads, void* 
     }
     if (!table.empty())
       e = cudaMemcpy(l->ws, table.data(), table.size() * sizeof(mg::ClipChunk), cudaMemcpyHostToDevice);
-    if (e == cudaSuccess) e = cudaMemset(l->ws + l->sync_off, 0, sizeof(mg::ClipSync));
+    if (e == cudaSuccess) e = cudaMemset(l->ws + l->partial_off, 0, bytes - l->partial_off);
     if (e != cudaSuccess) {
       cudaFree(l->ws);
       return mg::op_end(fn, e);
@@ -461,15 +490,16 @@ extern "C" mg_status mg_grad_list_clip(mg_grad_list* l, float max_norm, float* s
   if (st != MG_OK) return st;
   cudaStream_t s = (cudaStream_t)stream;
   const auto* chunks = reinterpret_cast<const mg::ClipChunk*>(l->ws);
-  double* partial = reinterpret_cast<double*>(l->ws + l->partial_off);
   mg::ClipSync* sync = reinterpret_cast<mg::ClipSync*>(l->ws + l->sync_off);
   cudaError_t e;
   if (l->fused) {
-    void* args[] = {&chunks, &partial, &sync, &max_norm, &stats};
+    mg::ClipSum* sums = reinterpret_cast<mg::ClipSum*>(l->ws + l->partial_off);
+    void* args[] = {&chunks, &sums, &sync, &max_norm, &stats};
     e = cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(mg::clip_fused_kernel), dim3(l->n_chunks),
                                     dim3(mg::kClipThreads), args, 0, s);
     return mg::op_end(fn, e);
   }
+  double* partial = reinterpret_cast<double*>(l->ws + l->partial_off);
   const int blocks = std::max(1, std::min(l->n_chunks, 4 * l->sms));
   mg::clip_norm_kernel<<<blocks, mg::kClipThreads, 0, s>>>(chunks, l->n_chunks, partial, sync, max_norm, stats);
   e = cudaGetLastError();
