@@ -181,6 +181,7 @@ class Plan:
         self.h = h
         self.batch, self.precision, self.loss_kind = batch, precision, loss
         self.layers = list(layers)
+        self._takes_ids = bool(layers) and layers[0]["op"] == "embedding"
 
     @classmethod
     def for_workload(cls, w, precision: str):
@@ -219,11 +220,22 @@ class Plan:
             out.append((o.value, r.value, c.value))
         return out
 
+    def _check_ids(self, x):
+        # the library reads batch int32 ids; a tensor says whether it holds them
+        if self._takes_ids and x is not None and not isinstance(x, int):
+            if x.dtype != _type_tables()[3]:
+                _refuse(f"ids must be int32, not {x.dtype}")
+            if x.numel() != self.batch:
+                _refuse(f"{x.numel()} ids for a batch of {self.batch}", MG_ERR_SHAPE)
+            _dense(x, "ids")
+
     def forward(self, params, x, out, stream=None):
+        self._check_ids(x)
         self._check(self.lib.mg_forward(self.h, _ptr(params), _ptr(x), _ptr(out), _stream(stream)))
 
     def train_step(self, params, grads, adam_m, adam_v, x, labels, lr: float, step: int,
                    stream=None):
+        self._check_ids(x)
         self._check(self.lib.mg_train_step(self.h, _ptr(params), _ptr(grads), _ptr(adam_m),
                                            _ptr(adam_v), _ptr(x), _ptr(labels), float(lr),
                                            int(step), _stream(stream)))

@@ -220,7 +220,11 @@ namespace {
 
 using mg::op_fail;
 
-constexpr size_t kGroupedWorkspace = 256;   // begins with the error word
+constexpr size_t kErrorBytes = 256;   // of a workspace: begins with the error word; then the scratch
+
+size_t workspace_bytes(int rows, int groups, int d_in, int d_out) {
+  return kErrorBytes + mg::grouped_split_bytes(rows, groups, d_in, d_out);
+}
 
 mg_status grouped_call(const char* fn, mg::GroupKind kind, int dtype, const void* a, const void* b,
                        const int* offsets, int rows, int groups, int d_in, int d_out, void* out, void* ws,
@@ -235,7 +239,7 @@ mg_status grouped_call(const char* fn, mg::GroupKind kind, int dtype, const void
   const bool dw = kind == mg::GROUP_DW;
   if (!offsets || !ws || (rows_needed && !a) || (!b && (rows_needed || !dw)) || (!out && (rows_needed || dw)))
     return op_fail(MG_ERR_INVALID_ARG, "%s: a pointer is NULL", fn);
-  const size_t need = kGroupedWorkspace;
+  const size_t need = workspace_bytes(rows, groups, d_in, d_out);
   if (ws_bytes < need)
     return op_fail(MG_ERR_INVALID_ARG, "%s: the workspace needs %zu bytes, %zu given", fn, need, ws_bytes);
   mg_status st = mg::op_begin(fn, {{a, 16}, {b, 16}, {offsets, 4}, {out, 16}, {ws, 16}});
@@ -252,6 +256,7 @@ mg_status grouped_call(const char* fn, mg::GroupKind kind, int dtype, const void
   g.B = b;
   g.out = out;
   g.err = static_cast<int*>(ws);
+  g.ws = reinterpret_cast<float*>(static_cast<char*>(ws) + kErrorBytes);
   return mg::op_end(fn, mg::grouped_gemm(g, (cudaStream_t)stream));
 }
 
@@ -259,7 +264,7 @@ mg_status grouped_call(const char* fn, mg::GroupKind kind, int dtype, const void
 
 extern "C" size_t mg_grouped_linear_workspace_bytes(int rows, int groups, int d_in, int d_out) {
   if (rows < 0 || groups < 1 || groups > mg::kMaxGroups || d_in < 1 || d_out < 1) return 0;
-  return kGroupedWorkspace;
+  return workspace_bytes(rows, groups, d_in, d_out);
 }
 
 extern "C" mg_status mg_grouped_linear_forward(int dtype, const void* x, const int* offsets, int rows, int groups,

@@ -24,12 +24,29 @@
 // zeroing in the producer's own loop the ring ran dry once per tile: 404 us
 // against 352 for 16384 rows x 8 experts x 2048x8192).
 //
+// Long sums.  The tensor core truncates each addition to its fp32 accumulator,
+// an error that grows with the number of additions: 2.3e-6 of the result at
+// 2048 rows a group (in the 2-norm).  dW is stored in fp32, so there every G_SEG
+// K blocks start a new accumulator, and the epilogue adds them in registers,
+// rounding to nearest: segments of 8 and 12 blocks cost 8 and 4 % of the time
+// and leave 0.5e-6 and 0.7e-6, however long the group; plain fp32 products are at
+// 0.45e-6.  Outputs in bf16 round 1000 times as coarsely and keep one
+// accumulator.
+//
+// Few tiles.  Where they are fewer than half the pairs, each tile's K blocks
+// are split over several pairs, which write fp32 partial tiles into the
+// workspace; a second, dependent launch adds them in order and applies the
+// epilogue (the same bits in every run).  @@
+//
 // Warp roles and pipeline as in gemm_tc2.cu: warp 0 TMA producer, warp 1 MMA
 // issuer (leader CTA), warps 2-9 epilogue, in dW warp 10 zeroing; six 32 KB
 // stages per CTA; two accumulators of 256 columns.  Every wait is bounded.
 #include <cuda.h>
 
+#include <algorithm>
+
 #include "common.cuh"
+#include "group_epilogue.cuh"
 #include "group_table.cuh"
 #include "group_tma.h"
 #include "kernels.h"
@@ -53,6 +70,7 @@ constexpr int G_THREADS = 320;      // one more warp in dW
 constexpr int group_threads(int kind) { return kind == GROUP_DW ? G_THREADS + 32 : G_THREADS; }
 constexpr uint32_t G_A_BYTES = G_BM * G_BK * 2;
 constexpr uint32_t G_B_BYTES = G_BNH * G_BK * 2;
+constexpr int G_SEG = 12;          // K blocks (768 rows) per accumulator in dW
 constexpr int G_PANEL = 64 * G_BK * 2;   // one 64-column panel of a stage
 
 struct GroupTcParams {
@@ -64,6 +82,8 @@ struct GroupTcParams {
   int tiles_m;             // dW: 256-row tiles of one dW[e]
   int k_blocks;            // forward, dX
   int vec, vec32;
+  int splits;              // parts of every tile's K blocks; part s writes rows s * split_rows ..
+  int split_rows;
   int* err;
 };
 
@@ -71,19 +91,27 @@ struct GroupTcParams {
 struct GroupTile {
   int e, m0, m_end, n0;
   int kb;        // K blocks (0: the result is zero)
+  int k0;        // forward, dX: first of them
+  int part;      // split of the K blocks
   int krow0;     // dW: first row of the group
   int tail;      // dW: rows of the last K block that belong to the group, 0 if all 64 do
 };
 
 template <int KIND>
 __device__ __forceinline__ int tile_count(const GroupTcParams& P, const GroupTable& t) {
-  return KIND == GROUP_DW ? P.groups * P.tiles_m * P.tiles_n : t.cum[t.n - 1] * P.tiles_n;
+  return P.splits * (KIND == GROUP_DW ? P.groups * P.tiles_m * P.tiles_n : t.cum[t.n - 1] * P.tiles_n);
 }
 
 // e: cursor kept between calls (items ascend).
 template <int KIND>
 __device__ __forceinline__ GroupTile tile_at(const GroupTcParams& P, const GroupTable& t, int item, int& e) {
   GroupTile r;
+  r.part = 0;
+  if (P.splits > 1) {
+    r.part = item % P.splits;
+    item /= P.splits;
+  }
+  r.k0 = 0;
   if (KIND == GROUP_DW) {
     const int per = P.tiles_m * P.tiles_n;
     e = item / per;
@@ -95,6 +123,12 @@ __device__ __forceinline__ GroupTile tile_at(const GroupTcParams& P, const Group
     const int size = t.hi[e] - t.lo[e];
     r.kb = (size + G_BK - 1) / G_BK;
     r.tail = size % G_BK;
+    if (P.splits > 1) {
+      const int lo = r.kb * r.part / P.splits, hi = r.kb * (r.part + 1) / P.splits;
+      if (hi < r.kb || hi == lo) r.tail = 0;     // the group's last block is another part's
+      r.krow0 += lo * G_BK;
+      r.kb = hi - lo;
+    }
   } else {
     const int mt = item / P.tiles_n;
     r.n0 = (item - mt * P.tiles_n) * G_BN;
@@ -104,6 +138,10 @@ __device__ __forceinline__ GroupTile tile_at(const GroupTcParams& P, const Group
     r.kb = e < P.groups ? P.k_blocks : 0;
     r.krow0 = 0;
     r.tail = 0;
+    if (P.splits > 1) {
+      r.k0 = r.kb * r.part / P.splits;
+      r.kb = r.kb * (r.part + 1) / P.splits - r.k0;
+    }
   }
   r.e = e;
   return r;
@@ -187,7 +225,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(group_threads(KIND),
           if (!mbar_wait_cluster(&empty[stage], phase ^ 1)) { *abort_flag = 1; atomicExch(P.err, 1); break; }
           uint8_t* a = sA + stage * G_A_BYTES;
           uint8_t* b = sB + stage * G_B_BYTES;
-          const int k0 = kb * G_BK;
+          const int k0 = (T.k0 + kb) * G_BK;
           if (KIND == GROUP_DW && T.tail && kb == T.kb - 1) {
             const int kr = T.krow0 + k0;
             mbar_expect_tx(&tailbar[stage], G_A_BYTES + G_B_BYTES);
@@ -264,30 +302,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(group_threads(KIND),
       constexpr uint32_t idesc = instr_desc(2 * G_BM, G_BN, A_MN ? 1 : 0, B_MN ? 1 : 0);
       int stage = 0, e = 0, it = 0;
       uint32_t phase = 0;
-      for (int item = pair; item < n_items && !*abort_flag; item += npairs, ++it) {
+      for (int item = pair; item < n_items && !*abort_flag; item += npairs) {
         const GroupTile T = tile_at<KIND>(P, t, item, e);
-        const int acc = it & 1;
-        const uint32_t use = (uint32_t)(it >> 1) & 1u;
-        if (!mbar_wait_cluster(&tempty[acc], use ^ 1)) { *abort_flag = 1; atomicExch(P.err, 1); break; }
-        tc_fence_after();
-        const uint32_t d = tmem_base + (uint32_t)(acc * G_BN);
         bool ok = true;
-        for (int kb = 0; kb < T.kb; ++kb) {
-          if (!mbar_wait_cluster(&full[stage], phase)) { ok = false; break; }
+        for (int kb = 0; ok && (kb < T.kb || kb == 0);) {
+          // one accumulator: all K blocks, or a segment of them
+          const int k_end = KIND == GROUP_DW ? min(T.kb, kb + G_SEG) : T.kb;
+          const int k_begin = kb, acc = it & 1;
+          const uint32_t use = (uint32_t)(it >> 1) & 1u;
+          if (!mbar_wait_cluster(&tempty[acc], use ^ 1)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t a = smem_u32(sA + stage * G_A_BYTES);
-          const uint32_t b = smem_u32(sB + stage * G_B_BYTES);
+          const uint32_t d = tmem_base + (uint32_t)(acc * G_BN);
+          for (; kb < k_end; ++kb) {
+            if (!mbar_wait_cluster(&full[stage], phase)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t a = smem_u32(sA + stage * G_A_BYTES);
+            const uint32_t b = smem_u32(sB + stage * G_B_BYTES);
 #pragma unroll
-          for (int k = 0; k < G_BK / 16; ++k) {
-            const uint64_t ad = A_MN ? smem_desc(a + k * 2048, G_PANEL, 1024) : smem_desc(a + k * 32, 16, 1024);
-            const uint64_t bd = B_MN ? smem_desc(b + k * 2048, G_PANEL, 1024) : smem_desc(b + k * 32, 16, 1024);
-            mma_bf16_pair(d, ad, bd, idesc, (kb | k) ? 1u : 0u);
+            for (int k = 0; k < G_BK / 16; ++k) {
+              const uint64_t ad = A_MN ? smem_desc(a + k * 2048, G_PANEL, 1024) : smem_desc(a + k * 32, 16, 1024);
+              const uint64_t bd = B_MN ? smem_desc(b + k * 2048, G_PANEL, 1024) : smem_desc(b + k * 32, 16, 1024);
+              mma_bf16_pair(d, ad, bd, idesc, (kb > k_begin || k) ? 1u : 0u);
+            }
+            mma_commit_pair(&empty[stage]);
+            if (++stage == G_STAGES) { stage = 0; phase ^= 1; }
           }
-          mma_commit_pair(&empty[stage]);
-          if (++stage == G_STAGES) { stage = 0; phase ^= 1; }
+          if (!ok) break;
+          mma_commit_pair(&tfull[acc]);
+          ++it;
+          if (T.kb == 0) break;
         }
         if (!ok) { *abort_flag = 1; atomicExch(P.err, 1); break; }
-        mma_commit_pair(&tfull[acc]);
       }
     }
   } else {
@@ -297,40 +342,77 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(group_threads(KIND),
     const int row_in_tile = quarter * 32 + lane;
     const uint32_t leader_tempty[2] = {map_to(&tempty[0], 0), map_to(&tempty[1], 0)};
     int e = 0, it = 0;
-    for (int item = pair; item < n_items; item += npairs, ++it) {
-      const GroupTile T = tile_at<KIND>(P, t, item, e);
-      const int acc = it & 1;
-      const uint32_t use = (uint32_t)(it >> 1) & 1u;
-      if (!mbar_wait(&tfull[acc], use)) { *abort_flag = 1; atomicExch(P.err, 1); break; }
-      if (*abort_flag) break;
+    bool up = true;
+    // the next accumulator is full (false: a wait gave up)
+    auto wait_full = [&](int acc) {
+      if (!mbar_wait(&tfull[acc], (uint32_t)(it >> 1) & 1u)) { *abort_flag = 1; atomicExch(P.err, 1); }
+      up = !*abort_flag;
+      up = __all_sync(0xffffffffu, up);
       tc_fence_after();
+      return up;
+    };
+    for (int item = pair; item < n_items && up; item += npairs) {
+      const GroupTile T = tile_at<KIND>(P, t, item, e);
       const int m = T.m0 + (int)rank * G_BM + row_in_tile;
       const bool row_ok = m < T.m_end;
       // dW[e] is rows e*d_in .. of one [groups * d_in, d_out] matrix
-      const int mo = KIND == GROUP_DW ? T.e * P.d_in + m : m;
-      const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * G_BN);
+      const int mo = (KIND == GROUP_DW ? T.e * P.d_in + m : m) + T.part * P.split_rows;
+      const uint32_t lanes = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(half * (G_BN / 2));
+      const int n0 = T.n0 + half * (G_BN / 2);
+      if (KIND == GROUP_DW) {
+        float sum[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) sum[c][i] = 0.0f;
+        const int segs = T.kb ? (T.kb + G_SEG - 1) / G_SEG : 1;
+        for (int sg = 0; sg < segs; ++sg, ++it) {
+          const int acc = it & 1;
+          if (!wait_full(acc)) break;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t r[32];
+            tmem_ld32_async(lanes + acc * G_BN + c * 32, r);
+            tmem_wait_regs(r);
+            if (c == 3) {
+              tc_fence_before();
+              mbar_arrive_remote(leader_tempty[acc]);
+            }
+            if (T.kb) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) sum[c][i] += __uint_as_float(r[i]);
+            }
+          }
+        }
+        if (!up) break;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (row_ok && n0 + c * 32 < P.g.N) epi32<TO>(P.g, P.vec != 0, P.vec32 != 0, mo, n0 + c * 32, sum[c]);
+        continue;
+      }
+      const int acc = it & 1;
+      if (!wait_full(acc)) break;
+      ++it;
 #pragma unroll 1
       for (int cp = 0; cp < 2; ++cp) {
-        const int c0 = half * (G_BN / 64) + 2 * cp;
         uint32_t r0[32], r1[32];
-        tmem_ld32_async(taddr + c0 * 32, r0);
-        tmem_ld32_async(taddr + (c0 + 1) * 32, r1);
+        tmem_ld32_async(lanes + acc * G_BN + cp * 64, r0);
+        tmem_ld32_async(lanes + acc * G_BN + cp * 64 + 32, r1);
         tmem_wait_regs(r0);
         reg_fence(r1);
         if (cp == 1) {
           tc_fence_before();
           mbar_arrive_remote(leader_tempty[acc]);
         }
-        auto chunk = [&](int c, uint32_t (&r)[32]) {
-          const int n = T.n0 + c * 32;
+        auto chunk = [&](int n, uint32_t (&r)[32]) {
           if (!row_ok || n >= P.g.N) return;
           float v[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = T.kb ? __uint_as_float(r[i]) : 0.0f;
           epi32<TO>(P.g, P.vec != 0, P.vec32 != 0, mo, n, v);
         };
-        chunk(c0, r0);
-        chunk(c0 + 1, r1);
+        chunk(n0 + cp * 64, r0);
+        chunk(n0 + cp * 64 + 32, r1);
       }
     }
   }
@@ -369,8 +451,75 @@ size_t group_pair_smem(int groups) {
          (size_t)kGroupTableInts(groups) * 4;
 }
 
+// ---- joining of split tiles
+// out = the sum of the parts in order, through the epilogue (forward, dX: rows
+// of a group, and with zero_rest the others as zeros).
+template <int KIND>
+__global__ void __launch_bounds__(256) group_join_kernel(const GroupArgs g, const float* part, int splits, long long rows,
+                                                         int N) {
+  dependency_wait();
+  __shared__ int s_first, s_last;
+  if (KIND != GROUP_DW) {
+    if (threadIdx.x < 32) {
+      int hi = 0;
+      for (int e = threadIdx.x; e <= g.groups; e += 32) hi = max(hi, min(g.offsets[e], g.rows));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+      if (threadIdx.x == 0) {
+        s_first = min(max(g.offsets[0], 0), g.rows);
+        s_last = hi;
+      }
+    }
+    __syncthreads();
+  }
+  const long long total = rows * N / 4;              // N is a multiple of 8
+  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
+    bool inside = true;
+    if (KIND != GROUP_DW) {
+      const long long r = i * 4 / N;
+      inside = r >= s_first && r < s_last;
+      if (!inside && !g.zero_rest) continue;
+    }
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (inside)
+      for (int s = 0; s < splits; ++s) {
+        const float4 p = reinterpret_cast<const float4*>(part)[s * total + i];
+        v.x += p.x; v.y += p.y; v.z += p.z; v.w += p.w;
+      }
+    if (KIND == GROUP_DW) {
+      reinterpret_cast<float4*>(g.out)[i] = v;
+    } else {
+      const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) group_epilogue<bf16>(g, (size_t)i * 4 + q, f[q]);
+    }
+  }
+}
+
+// Parts of the K blocks for these sizes: as many as keep 76 pairs busy, with at
+// least eight blocks each (on average over the groups in dW).
+int group_splits(int kind, int rows, int groups, int d_in, int d_out) {
+  const int N = kind == GROUP_DX ? d_in : d_out, K = kind == GROUP_FWD ? d_in : d_out;
+  const long long tiles_n = (N + G_BN - 1) / G_BN;
+  const long long tiles = kind == GROUP_DW ? groups * ((d_in + 2ll * G_BM - 1) / (2 * G_BM)) * tiles_n
+                                           : ((long long)rows / (2 * G_BM) + groups) * tiles_n;
+  const long long kb = kind == GROUP_DW ? (long long)rows / groups / G_BK : (K + G_BK - 1) / G_BK;
+  const long long s = std::min(std::min(76 / tiles, kb / 8), 16ll);
+  return s < 2 ? 1 : (int)s;
+}
+
+long long group_out_rows(int kind, int rows, int groups, int d_in) {
+  return kind == GROUP_DW ? (long long)groups * d_in : rows;
+}
+
+size_t split_bytes(int kind, int rows, int groups, int d_in, int d_out) {
+  const int s = group_splits(kind, rows, groups, d_in, d_out);
+  const int N = kind == GROUP_DX ? d_in : d_out;
+  return s < 2 ? 0 : (size_t)s * group_out_rows(kind, rows, groups, d_in) * N * 4;
+}
+
 template <int KIND, typename TO>
-cudaError_t launch_group_pair(const GroupArgs& g, cudaStream_t s) {
+cudaError_t launch_group_pair(const GroupArgs& g, int splits, cudaStream_t s) {
   CUtensorMap ma, mb;
   bool ok;
   if (KIND == GROUP_DW) {
@@ -384,18 +533,23 @@ cudaError_t launch_group_pair(const GroupArgs& g, cudaStream_t s) {
   if (!ok) return cudaErrorInvalidValue;
   GroupTcParams P;
   const int N = KIND == GROUP_DX ? g.d_in : g.d_out;
+  P.splits = splits;
+  P.split_rows = (int)group_out_rows(g.kind, g.rows, g.groups, g.d_in);
   P.g.N = N;
-  P.g.act = g.act;
-  P.g.out_z = g.out_z; P.g.ldz = N;
-  P.g.saved = g.saved; P.g.lds = N; P.g.dact = g.dact;
-  P.g.resid = g.resid; P.g.ldr = N;
+  P.g.ldz = P.g.lds = P.g.ldr = P.g.ldo = N;
+  if (splits == 1) {
+    P.g.act = g.act;
+    P.g.out_z = g.out_z;
+    P.g.saved = g.saved; P.g.dact = g.dact;
+    P.g.resid = g.resid;
+  }
   P.g.aux_type = DT_BF16;
-  P.g.out = g.out; P.g.ldo = N;
+  P.g.out = splits > 1 ? g.ws : g.out;
   P.g.out_type = sizeof(TO) == 4 ? DT_F32 : DT_BF16;
   P.offsets = g.offsets;
   P.rows = g.rows;
   P.groups = g.groups;
-  P.zero_rest = g.zero_rest;
+  P.zero_rest = splits > 1 ? 0 : g.zero_rest;
   P.d_in = g.d_in;
   P.d_out = g.d_out;
   P.tiles_n = (N + G_BN - 1) / G_BN;
@@ -403,8 +557,8 @@ cudaError_t launch_group_pair(const GroupArgs& g, cudaStream_t s) {
   P.k_blocks = ((KIND == GROUP_FWD ? g.d_in : g.d_out) + G_BK - 1) / G_BK;
   P.err = g.err;
   auto al = [](const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; };
-  P.vec = al(g.out, 16) && al(g.out_z, 16) && al(g.saved, 16) && al(g.resid, 16) && N % 8 == 0;
-  P.vec32 = al(g.out, 32) && al(g.out_z, 32) && al(g.saved, 32) && al(g.resid, 32) && N % 16 == 0;
+  P.vec = al(P.g.out, 16) && al(P.g.out_z, 16) && al(P.g.saved, 16) && al(P.g.resid, 16) && N % 8 == 0;
+  P.vec32 = P.vec && al(P.g.out, 32) && al(P.g.out_z, 32) && al(P.g.saved, 32) && al(P.g.resid, 32) && N % 16 == 0;
   auto kern = group_pair_kernel<KIND, TO>;
   const size_t smem = group_pair_smem(g.groups);
   static const cudaError_t attr = cudaFuncSetAttribute(
@@ -430,13 +584,17 @@ cudaError_t launch_group_pair(const GroupArgs& g, cudaStream_t s) {
     return c;
   }();
   // tiles at most: every group may end inside one
-  const long long items = KIND == GROUP_DW
+  const long long items = splits * (KIND == GROUP_DW
                               ? (long long)g.groups * P.tiles_m * P.tiles_n
-                              : ((long long)g.rows / (2 * G_BM) + g.groups + (g.zero_rest ? 2 : 0)) * P.tiles_n;
+                              : ((long long)g.rows / (2 * G_BM) + g.groups + (P.zero_rest ? 2 : 0)) * P.tiles_n);
   if (items > 0x7fffffff) return cudaErrorInvalidValue;
   const int pairs = items < slots ? (int)items : slots;
   kern<<<2 * pairs, group_threads(KIND), smem, s>>>(ma, mb, P);
-  return cudaGetLastError();
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || splits == 1) return e;
+  const long long quads = (long long)P.split_rows * N / 4, blocks = (quads + 255) / 256;
+  return launch_dependent(group_join_kernel<KIND>, (unsigned)std::min(blocks, 152ll * 8), 256, 0, s, g,
+                          static_cast<const float*>(g.ws), splits, (long long)P.split_rows, N);
 }
 
 }  // namespace
@@ -468,11 +626,25 @@ bool grouped_tc_eligible(const GroupArgs& g) {
   return al(g.A) && al(g.B) && group_encode_fn() != nullptr;
 }
 
+size_t grouped_split_bytes(int rows, int groups, int d_in, int d_out) {
+  return std::max({split_bytes(GROUP_FWD, rows, groups, d_in, d_out), split_bytes(GROUP_DX, rows, groups, d_in, d_out),
+                   split_bytes(GROUP_DW, rows, groups, d_in, d_out)});
+}
+
+int grouped_launches(const GroupArgs& g) {
+  return g.ws && grouped_tc_eligible(g) && !grouped_narrow(g) &&
+                 group_splits(g.kind, g.rows, g.groups, g.d_in, g.d_out) > 1
+             ? 2
+             : 1;
+}
+
 cudaError_t grouped_gemm_tc(const GroupArgs& g, cudaStream_t s) {
   if (grouped_narrow(g)) return grouped_gemm_narrow(g, s);
-  if (g.kind == GROUP_FWD) return launch_group_pair<GROUP_FWD, bf16>(g, s);
-  if (g.kind == GROUP_DX) return launch_group_pair<GROUP_DX, bf16>(g, s);
-  return launch_group_pair<GROUP_DW, float>(g, s);
+  const int splits = g.ws ? group_splits(g.kind, g.rows, g.groups, g.d_in, g.d_out) : 1;
+  if (g.kind == GROUP_DW) return launch_group_pair<GROUP_DW, float>(g, splits, s);
+  if (g.kind == GROUP_FWD)
+    return splits > 1 ? launch_group_pair<GROUP_FWD, float>(g, splits, s) : launch_group_pair<GROUP_FWD, bf16>(g, 1, s);
+  return splits > 1 ? launch_group_pair<GROUP_DX, float>(g, splits, s) : launch_group_pair<GROUP_DX, bf16>(g, 1, s);
 }
 
 }  // namespace mg

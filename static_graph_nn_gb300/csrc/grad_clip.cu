@@ -27,6 +27,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdio>
+#include <exception>
 #include <memory>
 #include <new>
 #include <vector>
@@ -464,7 +465,7 @@ extern "C" mg_status mg_grad_list_create(int n, const void* const* grads, void* 
     }
     *list = l.release();
     return MG_OK;
-  } catch (const std::bad_alloc&) {
+  } catch (const std::exception&) {   // of the vectors: no exception leaves a C entry
     return op_fail(MG_ERR_OOM, "%s: host allocation failed", fn);
   }
 }

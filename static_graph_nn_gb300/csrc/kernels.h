@@ -212,7 +212,11 @@ struct GroupArgs {
   const void* resid = nullptr;
   int zero_rest = 0;           // rows of no group are computed as if A were 0 there
   int* err = nullptr;          // set to 1 on a timed-out wait
+  float* ws = nullptr;         // grouped_split_bytes of scratch; NULL: no split over K
 };
+// Scratch of the tensor-core products of these sizes (any kind), 32-byte aligned.
+size_t grouped_split_bytes(int rows, int groups, int d_in, int d_out);
+int grouped_launches(const GroupArgs& g);   // kernels of grouped_gemm(g)
 constexpr int kMaxGroups = 1024;
 cudaError_t grouped_gemm(const GroupArgs& g, cudaStream_t s);
 // The version for a few rows per group (forward and dX; grouped_tc_eligible as

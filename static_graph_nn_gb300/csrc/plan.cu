@@ -26,6 +26,7 @@
 
 #include "../../include/mg.h"
 #include "kernels.h"
+#include "op_checks.h"
 
 using namespace mg;
 
@@ -122,6 +123,7 @@ struct mg_plan {
   size_t split_off = 0, split_floats = 0;   // strict weight gradients split over K
   size_t embed_off = 0;      // embedding gradient's workspace
   int n_groups = 0;          // of the grouped layers; 0: there are none
+  size_t group_off = 0;      // scratch of the grouped products (0: none needed)
   const int* row_groups = nullptr;   // caller's offsets
   // clipping by the global norm (mg_set_grad_clip): 0 off
   float max_norm = 0.f;
@@ -342,6 +344,7 @@ GroupArgs group_args(mg_plan* p, const Node& n, GroupKind kind) {
   g.offsets = p->row_groups;
   g.zero_rest = 1;
   g.err = reinterpret_cast<int*>(p->ws + p->loss_off + 4);
+  if (p->group_off) g.ws = wsp<float>(p, p->group_off);
   return g;
 }
 
@@ -397,8 +400,8 @@ void forward_pass(Exec& e, const float* params, const void* x) {
       if (n.z >= 0) g.out_z = p->ws + p->values[n.z].off;
       if (n.skip >= 0) g.resid = val_ptr(p, n.skip, x);
       g.out = p->ws + p->values[n.out].off;
-      site(e, group_name(p, "grouped_fwd", n), 2.0 * p->batch * n.d_in * n.d_out, group_bytes(p, n, false), 1,
-           [&] { return grouped_gemm(g, e.s); });
+      site(e, group_name(p, "grouped_fwd", n), 2.0 * p->batch * n.d_in * n.d_out, group_bytes(p, n, false),
+           grouped_launches(g), [&] { return grouped_gemm(g, e.s); });
     } else if (n.kind == NK_EMBED) {
       char nm[96];
       snprintf(nm, sizeof nm, "embedding[l%d] %d of %dx%d", n.layer, p->batch, n.d_in, n.d_out);
@@ -711,8 +714,8 @@ void backward_pass(Exec& e, const float* params, float* grads, const void* x) {
       g.A = val_ptr(p, n.in, x);
       g.B = gy;
       g.out = grads + n.w_off;
-      site(e, group_name(p, "grouped_dW", n), 2.0 * p->batch * n.d_in * n.d_out, group_bytes(p, n, true), 1,
-           [&] { return grouped_gemm(g, e.s); });
+      site(e, group_name(p, "grouped_dW", n), 2.0 * p->batch * n.d_in * n.d_out, group_bytes(p, n, true),
+           grouped_launches(g), [&] { return grouped_gemm(g, e.s); });
       if (vin.need_grad) {
         GroupArgs h = group_args(p, n, GROUP_DX);
         h.A = gy;
@@ -725,8 +728,8 @@ void backward_pass(Exec& e, const float* params, float* grads, const void* x) {
         }
         h.resid = dadd;
         h.out = grad_ptr(p, n.in);
-        site(e, group_name(p, "grouped_dX", n), 2.0 * p->batch * n.d_in * n.d_out, group_bytes(p, n, false), 1,
-             [&] { return grouped_gemm(h, e.s); });
+        site(e, group_name(p, "grouped_dX", n), 2.0 * p->batch * n.d_in * n.d_out, group_bytes(p, n, false),
+             grouped_launches(h), [&] { return grouped_gemm(h, e.s); });
       }
       node_update(e, ni);
     } else if (n.kind == NK_EMBED) {
@@ -1172,8 +1175,13 @@ void layout_workspace(mg_plan* p) {
     }
   }
   if (p->dt == DT_BF16) p->shadow_off = b.take(p->n_params * 2);
-  for (const Node& n : p->nodes)
+  size_t group_ws = 0;
+  for (const Node& n : p->nodes) {
     if (n.kind == NK_EMBED) p->embed_off = b.take(embedding_ws_bytes(p->batch, n.d_in, n.d_out));
+    if (n.kind == NK_GROUP && p->dt == DT_BF16)
+      group_ws = std::max(group_ws, grouped_split_bytes(p->batch, n.groups, n.d_in, n.d_out));
+  }
+  if (group_ws) p->group_off = b.take(group_ws);
   // chunks
   p->n_chunks = 0;
   for (size_t t = 0; t < p->p_off.size(); ++t) {
@@ -1599,7 +1607,10 @@ mg_status mg_train_step(mg_plan* p, float* params, float* grads, float* adam_m, 
 mg_status mg_set_row_groups(mg_plan* p, const int* offsets) {
   if (!p || !offsets) return fail(p, MG_ERR_INVALID_ARG, "plan and offsets must be non-NULL");
   if (!p->n_groups) return fail(p, MG_ERR_INVALID_ARG, "the plan has no grouped layers");
-  if (reinterpret_cast<uintptr_t>(offsets) % 4) return fail(p, MG_ERR_ALIGN, "offsets must be 4-byte aligned");
+  mg_status st = check_device(p);
+  if (st != MG_OK) return st;
+  // 4-byte aligned memory of this device (the message is the process-wide one)
+  if ((st = op_begin("mg_set_row_groups", {{offsets, 4}})) != MG_OK) return fail(p, st, "%s", std::string(mg_last_error(nullptr)).c_str());
   if (offsets != p->row_groups)
     for (auto& g : p->graphs) {      // captured steps hold the old pointer
       drop_graph(g);

@@ -85,6 +85,8 @@ SHAPES = [
     (300, 7, 200, 328), (1000, 16, 520, 1032), (129, 5, 256, 128), (2049, 3, 136, 264), (700, 64, 264, 72),
     # few tiles and a long sum: two or four blocks share one
     (20, 3, 2048, 200), (7, 1, 4104, 72), (30, 2, 200, 1160), (16, 1, 1088, 2304),
+    # few tiles and long sums over d_in, d_out and the rows: split over blocks and joined
+    (300, 2, 1032, 136), (200, 3, 136, 2056), (5000, 2, 200, 72), (4000, 3, 72, 264), (700, 1, 2056, 1032),
     # widths that rows of 16 bytes do not divide
     (77, 3, 33, 17), (300, 5, 1, 1), (50, 2, 100, 65),
 ]
@@ -98,7 +100,8 @@ def test_products(rows, e, k, n, t):
 
 
 @pytest.mark.parametrize("t", ["bf16", "f32"])
-@pytest.mark.parametrize("rows,e,k,n", [(300, 4, 136, 264), (40, 6, 256, 512), (65, 2, 72, 40), (9, 3, 33, 17)])
+@pytest.mark.parametrize("rows,e,k,n", [(300, 4, 136, 264), (40, 6, 256, 512), (65, 2, 72, 40), (9, 3, 33, 17),
+                                          (300, 2, 1032, 136), (4000, 3, 72, 264)])
 def test_rows_of_no_group(rows, e, k, n, t):
     """Rows before the first and behind the last group hold NaN: neither read nor
     written, and the gradients stay finite."""

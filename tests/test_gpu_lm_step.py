@@ -92,7 +92,7 @@ def _reference(layers, params, ids, y, off):
             x = x + skip
     loss = torch.nn.functional.cross_entropy(x, y.long())
     loss.backward()
-    return float(loss), [p.grad.cpu().numpy() for p in ps]
+    return float(loss.detach()), [p.grad.cpu().numpy() for p in ps]
 
 
 class Run:
@@ -346,3 +346,43 @@ def test_operators_together_without_a_plan():
         assert (full.double() - want).abs().max() <= 1e-4 * want.abs().max()
         assert (got.double() - want / norm).abs().max() <= 1e-4 * want.abs().max() / norm
     lst.close()
+
+
+def test_plan_refuses_wrong_ids_and_offsets():
+    run = Run(LAYERS, "strict", "sgd", _params(LAYERS, 20))
+    ids, y = _batch(21)
+    with pytest.raises(binding.MGError):
+        run.plan.set_row_groups(torch.zeros(E, dtype=torch.int32, device="cuda"))
+    with pytest.raises(binding.MGError):
+        run.plan.set_row_groups(torch.zeros(E + 1, dtype=torch.int32))        # host memory
+    run.plan.set_row_groups(torch.tensor(OFFS["ragged"], dtype=torch.int32, device="cuda"))
+    for bad in (ids.long(), ids[:-1], ids.float()):
+        with pytest.raises(binding.MGError):
+            run.step(bad, y, 1)
+    linear = Run([W.linear(16, 4, False)], "strict", "sgd", _params([W.linear(16, 4, False)], 1), batch=8)
+    with pytest.raises(binding.MGError):
+        linear.plan.set_row_groups(torch.zeros(3, dtype=torch.int32, device="cuda"))
+
+
+def test_step_on_a_side_stream_inside_a_capture():
+    """A whole clipped step with embedding and grouped layers captured by the caller
+    gives what an eager one gives."""
+    params = _params(LAYERS, 22)
+    offs = torch.tensor(OFFS["gaps"], dtype=torch.int32, device="cuda")
+    ids, y = _batch(23)
+    a, b = (Run(LAYERS, "bf16", "sgd", params) for _ in range(2))
+    for r in (a, b):
+        r.plan.set_row_groups(offs)
+        r.plan.set_grad_clip(0.1)
+        r.step(ids, y, 1)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        b.step(ids, y, 2, stream=s)
+    for t in (2, 3):
+        a.step(ids, y, t)
+        g.replay()
+    torch.cuda.synchronize()
+    assert all(np.array_equal(u, v) for u, v in zip(a.tensors(a.params), b.tensors(b.params)))
+    assert a.plan.grad_norm() == b.plan.grad_norm()
