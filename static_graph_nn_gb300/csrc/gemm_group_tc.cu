@@ -81,7 +81,7 @@ struct GroupTcParams {
   int tiles_n;             // 256-column tiles of an output row
   int tiles_m;             // dW: 256-row tiles of one dW[e]
   int k_blocks;            // forward, dX
-  int vec, vec32;
+  int vec32;               // rows of the epilogue's matrices allow 32-byte accesses (16 always)
   int splits;              // parts of every tile's K blocks; part s writes rows s * split_rows ..
   int split_rows;
   int* err;
@@ -386,8 +386,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(group_threads(KIND),
         }
         if (!up) break;
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (row_ok && n0 + c * 32 < P.g.N) epi32<TO>(P.g, P.vec != 0, P.vec32 != 0, mo, n0 + c * 32, sum[c]);
+        for (int c = 0; c < 4; ++c) {
+          const int n = n0 + c * 32;
+          if (!row_ok || n >= P.g.N) continue;
+          if (n + 32 <= P.g.N) epi32<TO>(P.g, true, P.vec32 != 0, mo, n, sum[c]);
+          else epi_by8<TO>(P.g, mo, n, sum[c]);
+        }
         continue;
       }
       const int acc = it & 1;
@@ -409,7 +413,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(group_threads(KIND),
           float v[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = T.kb ? __uint_as_float(r[i]) : 0.0f;
-          epi32<TO>(P.g, P.vec != 0, P.vec32 != 0, mo, n, v);
+          if (n + 32 <= P.g.N) epi32<TO>(P.g, true, P.vec32 != 0, mo, n, v);
+          else epi_by8<TO>(P.g, mo, n, v);
         };
         chunk(n0 + cp * 64, r0);
         chunk(n0 + cp * 64 + 32, r1);
@@ -557,8 +562,8 @@ cudaError_t launch_group_pair(const GroupArgs& g, int splits, cudaStream_t s) {
   P.k_blocks = ((KIND == GROUP_FWD ? g.d_in : g.d_out) + G_BK - 1) / G_BK;
   P.err = g.err;
   auto al = [](const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; };
-  P.vec = al(P.g.out, 16) && al(P.g.out_z, 16) && al(P.g.saved, 16) && al(P.g.resid, 16) && N % 8 == 0;
-  P.vec32 = P.vec && al(P.g.out, 32) && al(P.g.out_z, 32) && al(P.g.saved, 32) && al(P.g.resid, 32) && N % 16 == 0;
+  if (!al(P.g.out, 16) || !al(P.g.out_z, 16) || !al(P.g.saved, 16) || !al(P.g.resid, 16)) return cudaErrorInvalidValue;
+  P.vec32 = al(P.g.out, 32) && al(P.g.out_z, 32) && al(P.g.saved, 32) && al(P.g.resid, 32) && N % 16 == 0;
   auto kern = group_pair_kernel<KIND, TO>;
   const size_t smem = group_pair_smem(g.groups);
   static const cudaError_t attr = cudaFuncSetAttribute(
