@@ -33,14 +33,22 @@
 // 0.45e-6.  Outputs in bf16 round 1000 times as coarsely and keep one
 // accumulator.
 //
+// dW's epilogue stores through shared memory: each warp puts 32 rows x 32
+// columns into a swizzled 4 KB buffer and one lane hands it to the TMA, which
+// also clips at d_in and d_out.  Stored row by row from the lanes' registers
+// (32-byte pieces of 32 rows an instruction), the 256 KB of a tile took longer
+// than the MMAs of the next two segments and held the tensor cores up: 429
+// against 417 us, and 46 against 37 for 8192 rows into one 1024x2048 gradient.
+//
 // Few tiles.  Where they are fewer than half the pairs, each tile's K blocks
 // are split over several pairs, which write fp32 partial tiles into the
 // workspace; a second, dependent launch adds them in order and applies the
-// epilogue (the same bits in every run).  @@
+// epilogue (the same bits in every run): 16384 rows into one 512x512 weight
+// gradient 30 us, 99 unsplit; 300 rows x 8192x256 23 us, 51 unsplit.
 //
 // Warp roles and pipeline as in gemm_tc2.cu: warp 0 TMA producer, warp 1 MMA
-// issuer (leader CTA), warps 2-9 epilogue, in dW warp 10 zeroing; six 32 KB
-// stages per CTA; two accumulators of 256 columns.  Every wait is bounded.
+// issuer (leader CTA), warps 2-9 epilogue, in dW warp 10 zeroing; five 32 KB
+// stages per CTA (a sixth gains nothing); two accumulators of 256 columns.  Every wait is bounded.
 #include <cuda.h>
 
 #include <algorithm>
@@ -64,13 +72,14 @@ constexpr int G_BM = 128;          // rows per CTA (256 per pair)
 constexpr int G_BNH = 128;         // B columns per CTA (256 per pair)
 constexpr int G_BN = 256;
 constexpr int G_BK = 64;
-constexpr int G_STAGES = 6;
+constexpr int G_STAGES = 5;
 constexpr int G_THREADS = 320;      // one more warp in dW
 
 constexpr int group_threads(int kind) { return kind == GROUP_DW ? G_THREADS + 32 : G_THREADS; }
 constexpr uint32_t G_A_BYTES = G_BM * G_BK * 2;
 constexpr uint32_t G_B_BYTES = G_BNH * G_BK * 2;
 constexpr int G_SEG = 12;          // K blocks (768 rows) per accumulator in dW
+constexpr uint32_t G_OUT_BYTES = 8 * 32 * 128;   // dW: a 32x32 fp32 buffer per epilogue warp
 constexpr int G_PANEL = 64 * G_BK * 2;   // one 64-column panel of a stage
 
 struct GroupTcParams {
@@ -156,10 +165,20 @@ __device__ __forceinline__ void tma_load_3d_to_leader(void* dst, const CUtensorM
       : "memory");
 }
 
+// A box of shared memory to global memory (clipped at the tensor's bounds), in a
+// bulk group of its own.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
 template <int KIND, typename TO>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(group_threads(KIND), 1)
     group_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                      const GroupTcParams P) {
+                      const __grid_constant__ CUtensorMap tmO, const GroupTcParams P) {
   constexpr bool A_MN = KIND == GROUP_DW;
   constexpr bool B_MN = KIND != GROUP_DX;
   constexpr uint32_t TMEM_COLS = 2 * G_BN;
@@ -168,7 +187,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(group_threads(KIND),
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* sA = smem;
   uint8_t* sB = smem + G_STAGES * G_A_BYTES;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sB + G_STAGES * G_B_BYTES);
+  uint8_t* sO = sB + G_STAGES * G_B_BYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sO + (KIND == GROUP_DW ? G_OUT_BYTES : 0));
   uint64_t* empty = full + G_STAGES;
   uint64_t* tfull = empty + G_STAGES;
   uint64_t* tempty = tfull + 2;
@@ -355,8 +375,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(group_threads(KIND),
       const GroupTile T = tile_at<KIND>(P, t, item, e);
       const int m = T.m0 + (int)rank * G_BM + row_in_tile;
       const bool row_ok = m < T.m_end;
-      // dW[e] is rows e*d_in .. of one [groups * d_in, d_out] matrix
-      const int mo = (KIND == GROUP_DW ? T.e * P.d_in + m : m) + T.part * P.split_rows;
+      const int mo = m + T.part * P.split_rows;
       const uint32_t lanes = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(half * (G_BN / 2));
       const int n0 = T.n0 + half * (G_BN / 2);
       if (KIND == GROUP_DW) {
@@ -385,12 +404,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(group_threads(KIND),
           }
         }
         if (!up) break;
+        const int row0 = T.m0 + (int)rank * G_BM + quarter * 32;     // the warp's rows
+        uint8_t* buf = sO + (warp - 2) * 4096;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const int n = n0 + c * 32;
-          if (!row_ok || n >= P.g.N) continue;
-          if (n + 32 <= P.g.N) epi32<TO>(P.g, true, P.vec32 != 0, mo, n, sum[c]);
-          else epi_by8<TO>(P.g, mo, n, sum[c]);
+          if (row0 >= T.m_end || n >= P.g.N) continue;               // warp-uniform
+          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          __syncwarp();
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            *reinterpret_cast<float4*>(buf + sw128(lane, q)) =
+                make_float4(sum[c][4 * q], sum[c][4 * q + 1], sum[c][4 * q + 2], sum[c][4 * q + 3]);
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) tma_store_3d(&tmO, buf, n, row0, T.part * P.groups + T.e);
         }
         continue;
       }
@@ -420,6 +448,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(group_threads(KIND),
         chunk(n0 + cp * 64 + 32, r1);
       }
     }
+    if (KIND == GROUP_DW && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
 
   tc_fence_before();
@@ -451,8 +480,21 @@ EncodeTiledFn group_encode_fn() {
   return fn;
 }
 
-size_t group_pair_smem(int groups) {
-  return 1024 + (size_t)G_STAGES * (G_A_BYTES + G_B_BYTES) + (4 * G_STAGES + 4) * 8 + 8 +
+// fp32 [outer][rows][cols], dense; 32x32 boxes, 128-byte swizzle.
+bool group_out_map(CUtensorMap* map, void* base, long long outer, long long rows, long long cols) {
+  EncodeTiledFn fn = group_encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)outer};
+  cuuint64_t strides[2] = {(cuuint64_t)cols * 4, (cuuint64_t)cols * (cuuint64_t)rows * 4};
+  cuuint32_t box[3] = {32, 32, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
+}
+
+size_t group_pair_smem(int kind, int groups) {
+  return 1024 + (size_t)G_STAGES * (G_A_BYTES + G_B_BYTES) + (kind == GROUP_DW ? G_OUT_BYTES : 0) + (4 * G_STAGES + 4) * 8 + 8 +
          (size_t)kGroupTableInts(groups) * 4;
 }
 
@@ -525,10 +567,11 @@ size_t split_bytes(int kind, int rows, int groups, int d_in, int d_out) {
 
 template <int KIND, typename TO>
 cudaError_t launch_group_pair(const GroupArgs& g, int splits, cudaStream_t s) {
-  CUtensorMap ma, mb;
+  CUtensorMap ma, mb, mo = {};
   bool ok;
   if (KIND == GROUP_DW) {
-    ok = group_map(&ma, g.A, 0, g.rows, g.d_in, 64, G_BK) && group_map(&mb, g.B, 0, g.rows, g.d_out, 64, G_BK);
+    ok = group_out_map(&mo, splits > 1 ? g.ws : g.out, (long long)splits * g.groups, g.d_in, g.d_out) &&
+         group_map(&ma, g.A, 0, g.rows, g.d_in, 64, G_BK) && group_map(&mb, g.B, 0, g.rows, g.d_out, 64, G_BK);
   } else {
     const int k = KIND == GROUP_FWD ? g.d_in : g.d_out;
     ok = group_map(&ma, g.A, 0, g.rows, k, G_BK, G_BM) &&
@@ -565,15 +608,15 @@ cudaError_t launch_group_pair(const GroupArgs& g, int splits, cudaStream_t s) {
   if (!al(P.g.out, 16) || !al(P.g.out_z, 16) || !al(P.g.saved, 16) || !al(P.g.resid, 16)) return cudaErrorInvalidValue;
   P.vec32 = al(P.g.out, 32) && al(P.g.out_z, 32) && al(P.g.saved, 32) && al(P.g.resid, 32) && N % 16 == 0;
   auto kern = group_pair_kernel<KIND, TO>;
-  const size_t smem = group_pair_smem(g.groups);
+  const size_t smem = group_pair_smem(KIND, g.groups);
   static const cudaError_t attr = cudaFuncSetAttribute(
-      kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)group_pair_smem(kMaxGroups));
+      kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)group_pair_smem(KIND, kMaxGroups));
   if (attr != cudaSuccess) return attr;
   static const int slots = [&] {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * (device_sms() / 2));
     cfg.blockDim = dim3(group_threads(KIND));
-    cfg.dynamicSmemBytes = group_pair_smem(kMaxGroups);
+    cfg.dynamicSmemBytes = group_pair_smem(KIND, kMaxGroups);
     cudaLaunchAttribute at;
     at.id = cudaLaunchAttributeClusterDimension;
     at.val.clusterDim.x = 2;
@@ -594,7 +637,7 @@ cudaError_t launch_group_pair(const GroupArgs& g, int splits, cudaStream_t s) {
                               : ((long long)g.rows / (2 * G_BM) + g.groups + (P.zero_rest ? 2 : 0)) * P.tiles_n);
   if (items > 0x7fffffff) return cudaErrorInvalidValue;
   const int pairs = items < slots ? (int)items : slots;
-  kern<<<2 * pairs, group_threads(KIND), smem, s>>>(ma, mb, P);
+  kern<<<2 * pairs, group_threads(KIND), smem, s>>>(ma, mb, mo, P);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || splits == 1) return e;
   const long long quads = (long long)P.split_rows * N / 4, blocks = (quads + 255) / 256;
