@@ -17,12 +17,14 @@
 // W is addressed as a three-dimensional tensor, so a K block past its last row
 // reads zeros, not the next expert's weights.  In dW the groups' rows are the
 // K dimension, and the last 64-row block of a group may hold rows of the next
-// one: that block is loaded on a barrier of its own, and a warp of each CTA
-// overwrites the foreign rows with zeros in shared memory (both operands: a NaN
-// there would survive a zero factor), fences them to the async proxy and only
-// then reports the stage full.  The producer runs on meanwhile (with the
-// zeroing in the producer's own loop the ring ran dry once per tile: 404 us
-// against 352 for 16384 rows x 8 experts x 2048x8192).
+// one: that block has a buffer and barriers of its own beside the ring, and a
+// warp of each CTA overwrites the foreign rows with zeros in shared memory (both
+// operands: a NaN there would survive a zero factor), fences them to the async
+// proxy and only then reports it full.  It is loaded while the tile's first
+// blocks are multiplied and comes last in the sum, so its extra steps take no
+// time.  (16384 rows x 8 experts x 2048x8192, ncu: in the producer's own loop 404
+// us, by a warp of its own but in the ring 377, so 352; groups of whole blocks
+// 350.)
 //
 // Long sums.  The tensor core truncates each addition to its fp32 accumulator,
 // an error that grows with the number of additions: 2.3e-6 of the result at
@@ -33,8 +35,8 @@
 // 0.45e-6.  Outputs in bf16 round 1000 times as coarsely and keep one
 // accumulator.
 //
-// dW's epilogue stores through shared memory: each warp puts 32 rows x 32
-// columns into a swizzled 4 KB buffer and one lane hands it to the TMA, which
+// dW's epilogue stores through shared memory: each warp puts 16 rows x 32
+// columns into a swizzled 2 KB buffer and one lane hands it to the TMA, which
 // also clips at d_in and d_out.  Stored row by row from the lanes' registers
 // (32-byte pieces of 32 rows an instruction), the 256 KB of a tile took longer
 // than the MMAs of the next two segments and held the tensor cores up: 429
@@ -79,7 +81,8 @@ constexpr int group_threads(int kind) { return kind == GROUP_DW ? G_THREADS + 32
 constexpr uint32_t G_A_BYTES = G_BM * G_BK * 2;
 constexpr uint32_t G_B_BYTES = G_BNH * G_BK * 2;
 constexpr int G_SEG = 12;          // K blocks (768 rows) per accumulator in dW
-constexpr uint32_t G_OUT_BYTES = 8 * 32 * 128;   // dW: a 32x32 fp32 buffer per epilogue warp
+constexpr uint32_t G_TAIL_BYTES = G_A_BYTES + G_B_BYTES;   // dW: the ragged K block
+constexpr uint32_t G_OUT_BYTES = 8 * 16 * 128;             // dW: a 16x32 fp32 buffer per epilogue warp
 constexpr int G_PANEL = 64 * G_BK * 2;   // one 64-column panel of a stage
 
 struct GroupTcParams {
@@ -187,14 +190,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(group_threads(KIND),
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* sA = smem;
   uint8_t* sB = smem + G_STAGES * G_A_BYTES;
-  uint8_t* sO = sB + G_STAGES * G_B_BYTES;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sO + (KIND == GROUP_DW ? G_OUT_BYTES : 0));
+  uint8_t* sT = sB + G_STAGES * G_B_BYTES;
+  uint8_t* sO = sT + G_TAIL_BYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sT + (KIND == GROUP_DW ? G_TAIL_BYTES + G_OUT_BYTES : 0));
   uint64_t* empty = full + G_STAGES;
   uint64_t* tfull = empty + G_STAGES;
   uint64_t* tempty = tfull + 2;
-  uint64_t* tailbar = tempty + 2;          // per stage: this CTA's loads of a block that needs zeroing
-  uint64_t* fixbar = tailbar + G_STAGES;   // per stage, leader: the peer's block is zeroed
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(fixbar + G_STAGES);
+  uint64_t* tail_loaded = tempty + 2;      // ragged block: this CTA's part has arrived,
+  uint64_t* tail_peer = tail_loaded + 1;   // leader: the peer's part is zeroed,
+  uint64_t* tail_full = tail_peer + 1;     // leader: both are,
+  uint64_t* tail_empty = tail_full + 1;    // it has been multiplied
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail_empty + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   GroupTable t;
   t.n = P.groups + (P.zero_rest ? 2 : 0);
@@ -211,9 +217,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(group_threads(KIND),
     for (int s = 0; s < G_STAGES; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
-      mbar_init(&tailbar[s], 1);
-      mbar_init(&fixbar[s], 1);
     }
+    for (int i = 0; i < 4; ++i) mbar_init(&tail_loaded[i], 1);
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
       mbar_init(&tempty[a], 2 * 256);
@@ -237,25 +242,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(group_threads(KIND),
     // ---------------- TMA producer (both CTAs) ----------------
     if (lane == 0) {
       int stage = 0, e = 0;
-      uint32_t phase = 0;
+      uint32_t phase = 0, tail_phase = 0;
       for (int item = pair; item < n_items && !*abort_flag; item += npairs) {
         const GroupTile T = tile_at<KIND>(P, t, item, e);
         const int m0 = T.m0 + (int)rank * G_BM, n0 = T.n0 + (int)rank * G_BNH;
-        for (int kb = 0; kb < T.kb; ++kb) {
+        const int plain = T.tail ? T.kb - 1 : T.kb;
+        for (int kb = 0; kb <= plain; ++kb) {
+          // the ragged block, once the ring has turned over: by then the one of
+          // the tile before has been multiplied
+          if (KIND == GROUP_DW && T.tail && kb == min(plain, G_STAGES)) {
+            if (!mbar_wait_cluster(tail_empty, tail_phase ^ 1)) { *abort_flag = 1; atomicExch(P.err, 1); break; }
+            tail_phase ^= 1;
+            const int kr = T.krow0 + plain * G_BK;
+            mbar_expect_tx(tail_loaded, G_TAIL_BYTES);
+            tma_load_2d(sT, &tmA, tail_loaded, m0, kr);
+            tma_load_2d(sT + G_PANEL, &tmA, tail_loaded, m0 + 64, kr);
+            tma_load_2d(sT + G_A_BYTES, &tmB, tail_loaded, n0, kr);
+            tma_load_2d(sT + G_A_BYTES + G_PANEL, &tmB, tail_loaded, n0 + 64, kr);
+          }
+          if (kb == plain) break;
           if (!mbar_wait_cluster(&empty[stage], phase ^ 1)) { *abort_flag = 1; atomicExch(P.err, 1); break; }
           uint8_t* a = sA + stage * G_A_BYTES;
           uint8_t* b = sB + stage * G_B_BYTES;
           const int k0 = (T.k0 + kb) * G_BK;
-          if (KIND == GROUP_DW && T.tail && kb == T.kb - 1) {
-            const int kr = T.krow0 + k0;
-            mbar_expect_tx(&tailbar[stage], G_A_BYTES + G_B_BYTES);
-            tma_load_2d(a, &tmA, &tailbar[stage], m0, kr);
-            tma_load_2d(a + G_PANEL, &tmA, &tailbar[stage], m0 + 64, kr);
-            tma_load_2d(b, &tmB, &tailbar[stage], n0, kr);
-            tma_load_2d(b + G_PANEL, &tmB, &tailbar[stage], n0 + 64, kr);
-            if (++stage == G_STAGES) { stage = 0; phase ^= 1; }
-            continue;
-          }
           if (leader) mbar_expect_tx(&full[stage], 2 * (G_A_BYTES + G_B_BYTES));
           const uint32_t fb = map_to(&full[stage], 0);
           if (A_MN) {
@@ -279,38 +288,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(group_threads(KIND),
     }
   } else if (KIND == GROUP_DW && warp == 10) {
     // ---------------- zeroing of the blocks that end inside a group's rows ----------------
-    int blocks = 0, e = 0;          // K blocks of this pair's earlier tiles
-    uint32_t parity = 0;            // per stage: parity of its tailbar and fixbar
+    int e = 0;
+    uint32_t ph = 0;
     for (int item = pair; item < n_items; item += npairs) {
       const GroupTile T = tile_at<KIND>(P, t, item, e);
-      const int stage = (blocks + T.kb - 1) % G_STAGES;
-      blocks = (blocks + T.kb) % G_STAGES;
       if (!T.tail) continue;
-      const uint32_t ph = parity >> stage & 1u;
-      parity ^= 1u << stage;
-      int ok = __all_sync(0xffffffffu, mbar_wait(&tailbar[stage], ph));
+      int ok = __all_sync(0xffffffffu, mbar_wait(tail_loaded, ph));
       if (ok) {
-        uint8_t* a = sA + stage * G_A_BYTES;
-        uint8_t* b = sB + stage * G_B_BYTES;
         // a K row is one 128-byte line of each panel, whatever the swizzle inside it
         const int n16 = (G_BK - T.tail) * 8;
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
-          uint4* q = reinterpret_cast<uint4*>((p < 2 ? a + p * G_PANEL : b + (p - 2) * G_PANEL) + T.tail * 128);
+          uint4* q = reinterpret_cast<uint4*>(sT + p * G_PANEL + T.tail * 128);
           for (int i = lane; i < n16; i += 32) q[i] = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) {
           if (leader) {
-            ok = mbar_wait_cluster(&fixbar[stage], ph);
-            if (ok) mbar_arrive(&full[stage]);
+            ok = mbar_wait_cluster(tail_peer, ph);
+            if (ok) mbar_arrive(tail_full);
           } else {
-            mbar_arrive_remote_release(map_to(&fixbar[stage], 0));
+            mbar_arrive_remote_release(map_to(tail_peer, 0));
           }
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
       }
+      ph ^= 1;
       if (!ok) {
         if (lane == 0) { *abort_flag = 1; atomicExch(P.err, 1); }
         break;
@@ -321,7 +325,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(group_threads(KIND),
       // ---------------- leader: MMA issuer for the pair ----------------
       constexpr uint32_t idesc = instr_desc(2 * G_BM, G_BN, A_MN ? 1 : 0, B_MN ? 1 : 0);
       int stage = 0, e = 0, it = 0;
-      uint32_t phase = 0;
+      uint32_t phase = 0, tail_phase = 0;
       for (int item = pair; item < n_items && !*abort_flag; item += npairs) {
         const GroupTile T = tile_at<KIND>(P, t, item, e);
         bool ok = true;
@@ -334,18 +338,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(group_threads(KIND),
           tc_fence_after();
           const uint32_t d = tmem_base + (uint32_t)(acc * G_BN);
           for (; kb < k_end; ++kb) {
-            if (!mbar_wait_cluster(&full[stage], phase)) { ok = false; break; }
+            const bool tail = KIND == GROUP_DW && T.tail && kb == T.kb - 1;
+            if (!(tail ? mbar_wait_cluster(tail_full, tail_phase) : mbar_wait_cluster(&full[stage], phase))) {
+              ok = false;
+              break;
+            }
             tc_fence_after();
-            const uint32_t a = smem_u32(sA + stage * G_A_BYTES);
-            const uint32_t b = smem_u32(sB + stage * G_B_BYTES);
+            const uint32_t a = smem_u32(tail ? sT : sA + stage * G_A_BYTES);
+            const uint32_t b = smem_u32(tail ? sT + G_A_BYTES : sB + stage * G_B_BYTES);
 #pragma unroll
             for (int k = 0; k < G_BK / 16; ++k) {
               const uint64_t ad = A_MN ? smem_desc(a + k * 2048, G_PANEL, 1024) : smem_desc(a + k * 32, 16, 1024);
               const uint64_t bd = B_MN ? smem_desc(b + k * 2048, G_PANEL, 1024) : smem_desc(b + k * 32, 16, 1024);
               mma_bf16_pair(d, ad, bd, idesc, (kb > k_begin || k) ? 1u : 0u);
             }
-            mma_commit_pair(&empty[stage]);
-            if (++stage == G_STAGES) { stage = 0; phase ^= 1; }
+            mma_commit_pair(tail ? tail_empty : &empty[stage]);
+            if (tail) tail_phase ^= 1;
+            else if (++stage == G_STAGES) { stage = 0; phase ^= 1; }
           }
           if (!ok) break;
           mma_commit_pair(&tfull[acc]);
@@ -405,20 +414,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(group_threads(KIND),
         }
         if (!up) break;
         const int row0 = T.m0 + (int)rank * G_BM + quarter * 32;     // the warp's rows
-        uint8_t* buf = sO + (warp - 2) * 4096;
+        uint8_t* buf = sO + (warp - 2) * 2048;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const int n = n0 + c * 32;
-          if (row0 >= T.m_end || n >= P.g.N) continue;               // warp-uniform
-          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-          __syncwarp();
+          if (n >= P.g.N) continue;                                  // warp-uniform, as below
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            if (row0 + 16 * h >= T.m_end) continue;
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            __syncwarp();
+            if (lane >> 4 == h) {
 #pragma unroll
-          for (int q = 0; q < 8; ++q)
-            *reinterpret_cast<float4*>(buf + sw128(lane, q)) =
-                make_float4(sum[c][4 * q], sum[c][4 * q + 1], sum[c][4 * q + 2], sum[c][4 * q + 3]);
-          fence_proxy_async();
-          __syncwarp();
-          if (lane == 0) tma_store_3d(&tmO, buf, n, row0, T.part * P.groups + T.e);
+              for (int q = 0; q < 8; ++q)
+                *reinterpret_cast<float4*>(buf + sw128(lane & 15, q)) =
+                    make_float4(sum[c][4 * q], sum[c][4 * q + 1], sum[c][4 * q + 2], sum[c][4 * q + 3]);
+              fence_proxy_async();
+            }
+            __syncwarp();
+            if (lane == 0) tma_store_3d(&tmO, buf, n, row0 + 16 * h, T.part * P.groups + T.e);
+          }
         }
         continue;
       }
@@ -480,13 +495,13 @@ EncodeTiledFn group_encode_fn() {
   return fn;
 }
 
-// fp32 [outer][rows][cols], dense; 32x32 boxes, 128-byte swizzle.
+// fp32 [outer][rows][cols], dense; 32x16 boxes, 128-byte swizzle.
 bool group_out_map(CUtensorMap* map, void* base, long long outer, long long rows, long long cols) {
   EncodeTiledFn fn = group_encode_fn();
   if (!fn) return false;
   cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)outer};
   cuuint64_t strides[2] = {(cuuint64_t)cols * 4, (cuuint64_t)cols * (cuuint64_t)rows * 4};
-  cuuint32_t box[3] = {32, 32, 1};
+  cuuint32_t box[3] = {32, 16, 1};
   cuuint32_t estr[3] = {1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
@@ -494,7 +509,7 @@ bool group_out_map(CUtensorMap* map, void* base, long long outer, long long rows
 }
 
 size_t group_pair_smem(int kind, int groups) {
-  return 1024 + (size_t)G_STAGES * (G_A_BYTES + G_B_BYTES) + (kind == GROUP_DW ? G_OUT_BYTES : 0) + (4 * G_STAGES + 4) * 8 + 8 +
+  return 1024 + (size_t)G_STAGES * (G_A_BYTES + G_B_BYTES) + (kind == GROUP_DW ? G_TAIL_BYTES + G_OUT_BYTES : 0) + (2 * G_STAGES + 8) * 8 + 8 +
          (size_t)kGroupTableInts(groups) * 4;
 }
 
