@@ -9,8 +9,8 @@
 // memory and walks the same list of output tiles, so the host neither waits
 // for the router nor launches one product per expert.
 //
-// This file's kernel runs fp32 (FFMA only) and bf16 widths that TMA cannot
-// address (rows that are not multiples of 16 bytes).  Bound by the FP32 units:
+// This file's kernel runs fp32 (FFMA only) and small bf16 products of widths
+// that TMA cannot address (rows that are not multiples of 16 bytes).  Bound by the FP32 units:
 // 64x64 tiles (a group's last tile is half empty on average, so small ones) of
 // 128 threads with 8x4 outputs each, two products per instruction.  fp32
 // operands come by 4-byte asynchronous copies (any width and alignment,
@@ -223,7 +223,7 @@ using mg::op_fail;
 constexpr size_t kErrorBytes = 256;   // of a workspace: begins with the error word; then the scratch
 
 size_t workspace_bytes(int rows, int groups, int d_in, int d_out) {
-  return kErrorBytes + mg::grouped_split_bytes(rows, groups, d_in, d_out);
+  return kErrorBytes + mg::grouped_scratch_bytes(rows, groups, d_in, d_out);
 }
 
 mg_status grouped_call(const char* fn, mg::GroupKind kind, int dtype, const void* a, const void* b,

@@ -266,9 +266,9 @@ cudaError_t launch_narrow(const GroupArgs& g, cudaStream_t s) {
   P.tiles_n = (P.N + N_M - 1) / N_M;
   P.k_blocks = (k + N_BK - 1) / N_BK;
   CUtensorMap mw, mx;
-  const bool ok = (KIND == GROUP_FWD ? group_map(&mw, g.B, g.groups, g.d_in, g.d_out, 64, N_BK)
-                                     : group_map(&mw, g.B, g.groups, g.d_in, g.d_out, N_BK, N_M)) &&
-                  group_map(&mx, g.A, 0, g.rows, k, N_BK, N_T);
+  const bool ok = (KIND == GROUP_FWD ? group_map(&mw, g.B, g.groups, g.d_in, g.d_out, g.ldb, 64, N_BK)
+                                     : group_map(&mw, g.B, g.groups, g.d_in, g.d_out, g.ldb, N_BK, N_M)) &&
+                  group_map(&mx, g.A, 0, g.rows, k, g.lda, N_BK, N_T);
   if (!ok) return cudaErrorInvalidValue;
   static const cudaError_t attr = cudaFuncSetAttribute(
       group_narrow_kernel<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)narrow_smem(kMaxGroups, N_SPLIT));

@@ -42,6 +42,12 @@
 // than the MMAs of the next two segments and held the tensor cores up: 429
 // against 417 us, and 46 against 37 for 8192 rows into one 1024x2048 gradient.
 //
+// Widths that are no multiples of 8 (rows that TMA cannot address) are repacked
+// into the workspace with padded rows first, and the outputs leave row by row
+// through the epilogue's buffers, a warp's lanes beside each other: 16384 rows x
+// 8 x 2047x8191 forward 518 us, dX 527, dW 591.  The CUDA-core kernel keeps what
+// that is not worth (group_repacks).
+//
 // Few tiles.  Where they are fewer than half the pairs, each tile's K blocks
 // are split over several pairs, which write fp32 partial tiles into the
 // workspace; a second, dependent launch adds them in order and applies the
@@ -83,10 +89,14 @@ constexpr uint32_t G_B_BYTES = G_BNH * G_BK * 2;
 constexpr int G_SEG = 12;          // K blocks (768 rows) per accumulator in dW
 constexpr uint32_t G_TAIL_BYTES = G_A_BYTES + G_B_BYTES;   // dW: the ragged K block
 constexpr uint32_t G_OUT_BYTES = 8 * 16 * 128;             // dW: a 16x32 fp32 buffer per epilogue warp
+constexpr uint32_t group_extra_bytes(int kind, bool any) {  // shared memory behind the ring
+  return (kind == GROUP_DW ? G_TAIL_BYTES : 0) + (kind == GROUP_DW || any ? G_OUT_BYTES : 0);
+}
 constexpr int G_PANEL = 64 * G_BK * 2;   // one 64-column panel of a stage
 
 struct GroupTcParams {
   GemmArgs g;              // the epilogue: N, leading dimensions, outputs
+  GroupArgs any;           // the same for widths that are no multiples of 8
   const int* offsets;
   int rows, groups, zero_rest;
   int d_in, d_out;
@@ -178,7 +188,35 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void*
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 
-template <int KIND, typename TO>
+// 32 columns of a warp's 32 rows (lane = row), stored row by row with the lanes
+// beside each other, through a buffer of 16 rows (rotated by the row: no bank
+// conflicts).  Rows below m_end; base: rows before the output's row 0.
+template <int KIND>
+__device__ __forceinline__ void store_any(const GroupTcParams& P, float* buf, const float (&v)[32], int row0, int m_end,
+                                          int base, int n0, int lane) {
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+    __syncwarp();
+    if (lane >> 4 == h) {
+      const int r = lane & 15;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) buf[r * 32 + ((j + r) & 31)] = v[j];
+    }
+    __syncwarp();
+    const int rows = min(16, m_end - row0 - 16 * h);
+#pragma unroll 1
+    for (int r = 0; r < rows; ++r) {
+      if (n0 + lane >= P.g.N) continue;
+      const float x = buf[r * 32 + ((lane + r) & 31)];
+      const size_t o = (size_t)(base + row0 + 16 * h + r) * P.g.N + n0 + lane;
+      if (KIND == GROUP_DW) static_cast<float*>(P.any.out)[o] = x;
+      else group_epilogue<bf16>(P.any, o, x);
+    }
+  }
+}
+
+// ANY: outputs of any width and alignment.
+template <int KIND, typename TO, bool ANY>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(group_threads(KIND), 1)
     group_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                       const __grid_constant__ CUtensorMap tmO, const GroupTcParams P) {
@@ -191,8 +229,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(group_threads(KIND),
   uint8_t* sA = smem;
   uint8_t* sB = smem + G_STAGES * G_A_BYTES;
   uint8_t* sT = sB + G_STAGES * G_B_BYTES;
-  uint8_t* sO = sT + G_TAIL_BYTES;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sT + (KIND == GROUP_DW ? G_TAIL_BYTES + G_OUT_BYTES : 0));
+  uint8_t* sO = sT + (KIND == GROUP_DW ? G_TAIL_BYTES : 0);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sT + group_extra_bytes(KIND, ANY));
   uint64_t* empty = full + G_STAGES;
   uint64_t* tfull = empty + G_STAGES;
   uint64_t* tempty = tfull + 2;
@@ -419,20 +457,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(group_threads(KIND),
         for (int c = 0; c < 4; ++c) {
           const int n = n0 + c * 32;
           if (n >= P.g.N) continue;                                  // warp-uniform, as below
+          if constexpr (ANY) {
+            store_any<KIND>(P, reinterpret_cast<float*>(buf), sum[c], row0, T.m_end, T.e * P.d_in, n, lane);
+          } else {
 #pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            if (row0 + 16 * h >= T.m_end) continue;
-            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-            __syncwarp();
-            if (lane >> 4 == h) {
+            for (int h = 0; h < 2; ++h) {
+              if (row0 + 16 * h >= T.m_end) continue;
+              if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+              __syncwarp();
+              if (lane >> 4 == h) {
 #pragma unroll
-              for (int q = 0; q < 8; ++q)
-                *reinterpret_cast<float4*>(buf + sw128(lane & 15, q)) =
-                    make_float4(sum[c][4 * q], sum[c][4 * q + 1], sum[c][4 * q + 2], sum[c][4 * q + 3]);
-              fence_proxy_async();
+                for (int q = 0; q < 8; ++q)
+                  *reinterpret_cast<float4*>(buf + sw128(lane & 15, q)) =
+                      make_float4(sum[c][4 * q], sum[c][4 * q + 1], sum[c][4 * q + 2], sum[c][4 * q + 3]);
+                fence_proxy_async();
+              }
+              __syncwarp();
+              if (lane == 0) tma_store_3d(&tmO, buf, n, row0 + 16 * h, T.part * P.groups + T.e);
             }
-            __syncwarp();
-            if (lane == 0) tma_store_3d(&tmO, buf, n, row0 + 16 * h, T.part * P.groups + T.e);
           }
         }
         continue;
@@ -452,18 +494,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(group_threads(KIND),
           mbar_arrive_remote(leader_tempty[acc]);
         }
         auto chunk = [&](int n, uint32_t (&r)[32]) {
-          if (!row_ok || n >= P.g.N) return;
+          if (n >= P.g.N || (!ANY && !row_ok)) return;
           float v[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = T.kb ? __uint_as_float(r[i]) : 0.0f;
-          if (n + 32 <= P.g.N) epi32<TO>(P.g, true, P.vec32 != 0, mo, n, v);
+          if (ANY)
+            store_any<KIND>(P, reinterpret_cast<float*>(sO + (warp - 2) * 2048), v, m - lane, T.m_end, 0, n, lane);
+          else if (n + 32 <= P.g.N) epi32<TO>(P.g, true, P.vec32 != 0, mo, n, v);
           else epi_by8<TO>(P.g, mo, n, v);
         };
         chunk(n0 + cp * 64, r0);
         chunk(n0 + cp * 64 + 32, r1);
       }
     }
-    if (KIND == GROUP_DW && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    if (KIND == GROUP_DW && !ANY && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
 
   tc_fence_before();
@@ -508,8 +552,8 @@ bool group_out_map(CUtensorMap* map, void* base, long long outer, long long rows
          CUDA_SUCCESS;
 }
 
-size_t group_pair_smem(int kind, int groups) {
-  return 1024 + (size_t)G_STAGES * (G_A_BYTES + G_B_BYTES) + (kind == GROUP_DW ? G_TAIL_BYTES + G_OUT_BYTES : 0) + (2 * G_STAGES + 8) * 8 + 8 +
+size_t group_pair_smem(int kind, bool any, int groups) {
+  return 1024 + (size_t)G_STAGES * (G_A_BYTES + G_B_BYTES) + group_extra_bytes(kind, any) + (2 * G_STAGES + 8) * 8 + 8 +
          (size_t)kGroupTableInts(groups) * 4;
 }
 
@@ -561,6 +605,7 @@ __global__ void __launch_bounds__(256) group_join_kernel(const GroupArgs g, cons
 // Parts of the K blocks for these sizes: as many as keep 76 pairs busy, with at
 // least eight blocks each (on average over the groups in dW).
 int group_splits(int kind, int rows, int groups, int d_in, int d_out) {
+  if (d_in % 8 || d_out % 8) return 1;
   const int N = kind == GROUP_DX ? d_in : d_out, K = kind == GROUP_FWD ? d_in : d_out;
   const long long tiles_n = (N + G_BN - 1) / G_BN;
   const long long tiles = kind == GROUP_DW ? groups * ((d_in + 2ll * G_BM - 1) / (2 * G_BM)) * tiles_n
@@ -580,22 +625,24 @@ size_t split_bytes(int kind, int rows, int groups, int d_in, int d_out) {
   return s < 2 ? 0 : (size_t)s * group_out_rows(kind, rows, groups, d_in) * N * 4;
 }
 
-template <int KIND, typename TO>
+template <int KIND, typename TO, bool ANY>
 cudaError_t launch_group_pair(const GroupArgs& g, int splits, cudaStream_t s) {
   CUtensorMap ma, mb, mo = {};
   bool ok;
   if (KIND == GROUP_DW) {
-    ok = group_out_map(&mo, splits > 1 ? g.ws : g.out, (long long)splits * g.groups, g.d_in, g.d_out) &&
-         group_map(&ma, g.A, 0, g.rows, g.d_in, 64, G_BK) && group_map(&mb, g.B, 0, g.rows, g.d_out, 64, G_BK);
+    ok = (ANY || group_out_map(&mo, splits > 1 ? g.ws : g.out, (long long)splits * g.groups, g.d_in, g.d_out)) &&
+         group_map(&ma, g.A, 0, g.rows, g.d_in, g.lda, 64, G_BK) &&
+         group_map(&mb, g.B, 0, g.rows, g.d_out, g.ldb, 64, G_BK);
   } else {
     const int k = KIND == GROUP_FWD ? g.d_in : g.d_out;
-    ok = group_map(&ma, g.A, 0, g.rows, k, G_BK, G_BM) &&
-         (KIND == GROUP_FWD ? group_map(&mb, g.B, g.groups, g.d_in, g.d_out, 64, G_BK)
-                            : group_map(&mb, g.B, g.groups, g.d_in, g.d_out, G_BK, G_BNH));
+    ok = group_map(&ma, g.A, 0, g.rows, k, g.lda, G_BK, G_BM) &&
+         (KIND == GROUP_FWD ? group_map(&mb, g.B, g.groups, g.d_in, g.d_out, g.ldb, 64, G_BK)
+                            : group_map(&mb, g.B, g.groups, g.d_in, g.d_out, g.ldb, G_BK, G_BNH));
   }
   if (!ok) return cudaErrorInvalidValue;
   GroupTcParams P;
   const int N = KIND == GROUP_DX ? g.d_in : g.d_out;
+  P.any = g;
   P.splits = splits;
   P.split_rows = (int)group_out_rows(g.kind, g.rows, g.groups, g.d_in);
   P.g.N = N;
@@ -620,18 +667,19 @@ cudaError_t launch_group_pair(const GroupArgs& g, int splits, cudaStream_t s) {
   P.k_blocks = ((KIND == GROUP_FWD ? g.d_in : g.d_out) + G_BK - 1) / G_BK;
   P.err = g.err;
   auto al = [](const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; };
-  if (!al(P.g.out, 16) || !al(P.g.out_z, 16) || !al(P.g.saved, 16) || !al(P.g.resid, 16)) return cudaErrorInvalidValue;
+  if (!ANY && !(al(P.g.out, 16) && al(P.g.out_z, 16) && al(P.g.saved, 16) && al(P.g.resid, 16)))
+    return cudaErrorInvalidValue;
   P.vec32 = al(P.g.out, 32) && al(P.g.out_z, 32) && al(P.g.saved, 32) && al(P.g.resid, 32) && N % 16 == 0;
-  auto kern = group_pair_kernel<KIND, TO>;
-  const size_t smem = group_pair_smem(KIND, g.groups);
+  auto kern = group_pair_kernel<KIND, TO, ANY>;
+  const size_t smem = group_pair_smem(KIND, ANY, g.groups);
   static const cudaError_t attr = cudaFuncSetAttribute(
-      kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)group_pair_smem(KIND, kMaxGroups));
+      kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)group_pair_smem(KIND, ANY, kMaxGroups));
   if (attr != cudaSuccess) return attr;
   static const int slots = [&] {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * (device_sms() / 2));
     cfg.blockDim = dim3(group_threads(KIND));
-    cfg.dynamicSmemBytes = group_pair_smem(KIND, kMaxGroups);
+    cfg.dynamicSmemBytes = group_pair_smem(KIND, ANY, kMaxGroups);
     cudaLaunchAttribute at;
     at.id = cudaLaunchAttributeClusterDimension;
     at.val.clusterDim.x = 2;
@@ -660,14 +708,68 @@ cudaError_t launch_group_pair(const GroupArgs& g, int splits, cudaStream_t s) {
                           static_cast<const float*>(g.ws), splits, (long long)P.split_rows, N);
 }
 
+// ---- operands of widths that are no multiples of 8
+// Rows of L elements to rows of Lp (a multiple of 8), zeros behind; a thread per
+// 16 bytes written.
+__global__ void __launch_bounds__(256) group_repack_kernel(const bf16* src, uint4* dst, unsigned L, unsigned Lp8,
+                                                           long long chunks) {
+  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < chunks; i += gridDim.x * 256ll) {
+    const long long r = i / Lp8;
+    const unsigned c = (unsigned)(i - r * Lp8) * 8;
+    const unsigned short* p = reinterpret_cast<const unsigned short*>(src) + r * L + c;
+    unsigned h[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) h[q] = c + q < L ? p[q] : 0;
+    dst[i] = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+  }
+}
+
+int pad8(int n) { return (n + 7) / 8 * 8; }
+
+// An operand's rows and width, and the scratch its repacked copy takes.
+struct Operand {
+  long long rows;
+  int width;
+  size_t bytes() const { return width % 8 ? ((size_t)rows * pad8(width) * 2 + 255) / 256 * 256 : 0; }
+};
+Operand operand_a(int kind, int rows, int d_in, int d_out) { return {rows, kind == GROUP_DX ? d_out : d_in}; }
+Operand operand_b(int kind, int rows, int groups, int d_in, int d_out) {
+  return {kind == GROUP_DW ? (long long)rows : (long long)groups * d_in, d_out};
+}
+
+// Whether a product of such widths is worth the repacking against the CUDA-core
+// kernel, whose time goes with the operations (64-row tiles) and with its steps
+// along the sum: forward 30 against 80 us for 300 rows x 4 x 601x1003, 29 against
+// 52 for 1000 x 8 x 333x333, 161 against 645 for 24 x 8 x 2047x8191.  A weight
+// gradient of few rows per group only writes, which the plain kernel does better
+// (24 rows: 193 against 334 us; 75 rows per group: 26 against 38).
+bool group_repacks(int kind, int rows, int groups, int d_in, int d_out) {
+  if (d_in % 8 == 0 && d_out % 8 == 0) return false;
+  if (kind == GROUP_DW) return rows >= 32ll * groups && 2.0 * rows * d_in * d_out >= 1e8;
+  const double tile_rows = std::max((double)rows, 64.0 * std::min(rows, groups));
+  return 2.0 * tile_rows * d_in * d_out >= 1e8 || (kind == GROUP_FWD ? d_in : d_out) >= 128;
+}
+
+cudaError_t repack(const void*& p, int& ld, const Operand& o, char*& ws, cudaStream_t s) {
+  if (o.width % 8 == 0) return cudaSuccess;
+  ld = pad8(o.width);
+  const long long chunks = o.rows * (ld / 8), blocks = (chunks + 255) / 256;
+  group_repack_kernel<<<(unsigned)std::min(blocks, 152ll * 32), 256, 0, s>>>(
+      static_cast<const bf16*>(p), reinterpret_cast<uint4*>(ws), (unsigned)o.width, (unsigned)(ld / 8), chunks);
+  p = ws;
+  ws += o.bytes();
+  return cudaGetLastError();
+}
+
 }  // namespace
 
-bool group_map(CUtensorMap* map, const void* base, long long outer, long long rows, long long cols, int box_cols,
-               int box_rows) {
+bool group_map(CUtensorMap* map, const void* base, long long outer, long long rows, long long cols, long long ld,
+               int box_cols, int box_rows) {
   EncodeTiledFn fn = group_encode_fn();
   if (!fn) return false;
   cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)outer};
-  cuuint64_t strides[2] = {(cuuint64_t)cols * 2, (cuuint64_t)cols * (cuuint64_t)rows * 2};
+  if (!ld) ld = cols;
+  cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)ld * (cuuint64_t)rows * 2};
   cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1};
   cuuint32_t estr[3] = {1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, outer ? 3 : 2, const_cast<void*>(base), dims, strides, box,
@@ -675,12 +777,11 @@ bool group_map(CUtensorMap* map, const void* base, long long outer, long long ro
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool group_map_available() { return group_encode_fn() != nullptr; }
-
 bool grouped_tc_eligible(const GroupArgs& g) {
   auto al = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
   // mo = e * d_in + m and the tile counts are 32-bit
-  if (g.type != DT_BF16 || g.rows == 0 || g.d_in % 8 || g.d_out % 8) return false;
+  if (g.type != DT_BF16 || g.rows == 0) return false;
+  if ((g.d_in % 8 || g.d_out % 8) && !(g.ws && group_repacks(g.kind, g.rows, g.groups, g.d_in, g.d_out))) return false;
   if ((long long)g.groups * g.d_in > 0x7fff0000ll) return false;
   const long long tiles_n = ((g.kind == GROUP_DX ? g.d_in : g.d_out) + G_BN - 1) / G_BN;
   const long long tiles_m = g.kind == GROUP_DW ? (long long)g.groups * ((g.d_in + 255) / 256)
@@ -689,25 +790,47 @@ bool grouped_tc_eligible(const GroupArgs& g) {
   return al(g.A) && al(g.B) && group_encode_fn() != nullptr;
 }
 
-size_t grouped_split_bytes(int rows, int groups, int d_in, int d_out) {
-  return std::max({split_bytes(GROUP_FWD, rows, groups, d_in, d_out), split_bytes(GROUP_DX, rows, groups, d_in, d_out),
-                   split_bytes(GROUP_DW, rows, groups, d_in, d_out)});
+size_t grouped_scratch_bytes(int rows, int groups, int d_in, int d_out) {
+  size_t most = 0;
+  for (int kind : {GROUP_FWD, GROUP_DX, GROUP_DW}) {
+    size_t n = split_bytes(kind, rows, groups, d_in, d_out);
+    if (group_repacks(kind, rows, groups, d_in, d_out))
+      n = operand_a(kind, rows, d_in, d_out).bytes() + operand_b(kind, rows, groups, d_in, d_out).bytes();
+    most = std::max(most, n);
+  }
+  return most;
 }
 
 int grouped_launches(const GroupArgs& g) {
-  return g.ws && grouped_tc_eligible(g) && !grouped_narrow(g) &&
-                 group_splits(g.kind, g.rows, g.groups, g.d_in, g.d_out) > 1
-             ? 2
-             : 1;
+  if (!grouped_tc_eligible(g)) return 1;
+  if (g.d_in % 8 || g.d_out % 8)
+    return 1 + (operand_a(g.kind, g.rows, g.d_in, g.d_out).width % 8 != 0) +
+           (operand_b(g.kind, g.rows, g.groups, g.d_in, g.d_out).width % 8 != 0);
+  return g.ws && !grouped_narrow(g) && group_splits(g.kind, g.rows, g.groups, g.d_in, g.d_out) > 1 ? 2 : 1;
 }
 
-cudaError_t grouped_gemm_tc(const GroupArgs& g, cudaStream_t s) {
+cudaError_t grouped_gemm_tc(const GroupArgs& given, cudaStream_t s) {
+  GroupArgs g = given;
+  const bool any = g.d_in % 8 || g.d_out % 8;
+  if (any) {
+    char* ws = reinterpret_cast<char*>(g.ws);
+    cudaError_t e = repack(g.A, g.lda, operand_a(g.kind, g.rows, g.d_in, g.d_out), ws, s);
+    if (e == cudaSuccess) e = repack(g.B, g.ldb, operand_b(g.kind, g.rows, g.groups, g.d_in, g.d_out), ws, s);
+    if (e != cudaSuccess) return e;
+  }
   if (grouped_narrow(g)) return grouped_gemm_narrow(g, s);
+  if (any) {
+    if (g.kind == GROUP_DW) return launch_group_pair<GROUP_DW, float, true>(g, 1, s);
+    return g.kind == GROUP_FWD ? launch_group_pair<GROUP_FWD, bf16, true>(g, 1, s)
+                               : launch_group_pair<GROUP_DX, bf16, true>(g, 1, s);
+  }
   const int splits = g.ws ? group_splits(g.kind, g.rows, g.groups, g.d_in, g.d_out) : 1;
-  if (g.kind == GROUP_DW) return launch_group_pair<GROUP_DW, float>(g, splits, s);
+  if (g.kind == GROUP_DW) return launch_group_pair<GROUP_DW, float, false>(g, splits, s);
   if (g.kind == GROUP_FWD)
-    return splits > 1 ? launch_group_pair<GROUP_FWD, float>(g, splits, s) : launch_group_pair<GROUP_FWD, bf16>(g, 1, s);
-  return splits > 1 ? launch_group_pair<GROUP_DX, float>(g, splits, s) : launch_group_pair<GROUP_DX, bf16>(g, 1, s);
+    return splits > 1 ? launch_group_pair<GROUP_FWD, float, false>(g, splits, s)
+                      : launch_group_pair<GROUP_FWD, bf16, false>(g, 1, s);
+  return splits > 1 ? launch_group_pair<GROUP_DX, float, false>(g, splits, s)
+                    : launch_group_pair<GROUP_DX, bf16, false>(g, 1, s);
 }
 
 }  // namespace mg

@@ -203,6 +203,7 @@ struct GroupArgs {
   const int* offsets = nullptr;
   const void* A = nullptr;     // x (FWD, DW) or dy (DX)
   const void* B = nullptr;     // W (FWD, DX) or dy (DW)
+  int lda = 0, ldb = 0;        // their row strides where the tensor-core version has repacked them; 0: dense
   void* out = nullptr;
   // epilogue of FWD and DX, as GemmArgs': v (rounded to the type when act,
   // resid or out_z is set); out_z = v; v = act(v); v *= act'(saved); v += resid
@@ -212,10 +213,10 @@ struct GroupArgs {
   const void* resid = nullptr;
   int zero_rest = 0;           // rows of no group are computed as if A were 0 there
   int* err = nullptr;          // set to 1 on a timed-out wait
-  float* ws = nullptr;         // grouped_split_bytes of scratch; NULL: no split over K
+  float* ws = nullptr;         // grouped_scratch_bytes; NULL: no split over K, no repacked operands
 };
-// Scratch of the tensor-core products of these sizes (any kind), 32-byte aligned.
-size_t grouped_split_bytes(int rows, int groups, int d_in, int d_out);
+// Scratch of the tensor-core products of these sizes (any kind), 16-byte aligned.
+size_t grouped_scratch_bytes(int rows, int groups, int d_in, int d_out);
 int grouped_launches(const GroupArgs& g);   // kernels of grouped_gemm(g)
 constexpr int kMaxGroups = 1024;
 cudaError_t grouped_gemm(const GroupArgs& g, cudaStream_t s);
@@ -223,7 +224,8 @@ cudaError_t grouped_gemm(const GroupArgs& g, cudaStream_t s);
 // well).
 bool grouped_narrow(const GroupArgs& g);
 cudaError_t grouped_gemm_narrow(const GroupArgs& g, cudaStream_t s);
-// The tensor-core version: bf16, widths that are multiples of 8.
+// The tensor-core version: bf16, of widths that are no multiples of 8 only large
+// products and with scratch.
 bool grouped_tc_eligible(const GroupArgs& g);
 cudaError_t grouped_gemm_tc(const GroupArgs& g, cudaStream_t s);
 

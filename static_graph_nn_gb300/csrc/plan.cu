@@ -356,8 +356,8 @@ double group_bytes(const mg_plan* p, const Node& n, bool dw) {
 std::string group_name(const mg_plan* p, const char* what, const Node& n) {
   char b[160];
   const char* kind = p->dt != DT_BF16                           ? "f32-ffma"
-                     : n.d_in % 8 == 0 && n.d_out % 8 == 0 ? "bf16-tcgen05"
-                                                                : "bf16-simt";
+                     : grouped_tc_eligible(group_args(const_cast<mg_plan*>(p), n, GROUP_FWD)) ? "bf16-tcgen05"
+                                                                                               : "bf16-simt";
   snprintf(b, sizeof b, "%s[l%d] %d rows x %d groups x %dx%d %s", what, n.layer, p->batch, n.groups, n.d_in, n.d_out,
            kind);
   return b;
@@ -1179,7 +1179,7 @@ void layout_workspace(mg_plan* p) {
   for (const Node& n : p->nodes) {
     if (n.kind == NK_EMBED) p->embed_off = b.take(embedding_ws_bytes(p->batch, n.d_in, n.d_out));
     if (n.kind == NK_GROUP && p->dt == DT_BF16)
-      group_ws = std::max(group_ws, grouped_split_bytes(p->batch, n.groups, n.d_in, n.d_out));
+      group_ws = std::max(group_ws, grouped_scratch_bytes(p->batch, n.groups, n.d_in, n.d_out));
   }
   if (group_ws) p->group_off = b.take(group_ws);
   // chunks

@@ -88,6 +88,7 @@ SHAPES = [
     # few tiles and long sums over d_in, d_out and the rows: split over blocks and joined
     (300, 2, 1032, 136), (200, 3, 136, 2056), (5000, 2, 200, 72), (4000, 3, 72, 264), (700, 1, 2056, 1032),
     # widths that rows of 16 bytes do not divide
+    (700, 3, 601, 1003), (640, 2, 1001, 520), (1500, 4, 520, 999), (20, 4, 1501, 999), (30, 3, 1000, 2003),
     (77, 3, 33, 17), (300, 5, 1, 1), (50, 2, 100, 65),
 ]
 
@@ -101,7 +102,8 @@ def test_products(rows, e, k, n, t):
 
 @pytest.mark.parametrize("t", ["bf16", "f32"])
 @pytest.mark.parametrize("rows,e,k,n", [(300, 4, 136, 264), (40, 6, 256, 512), (65, 2, 72, 40), (9, 3, 33, 17),
-                                          (300, 2, 1032, 136), (4000, 3, 72, 264)])
+                                          (300, 2, 1032, 136), (4000, 3, 72, 264), (900, 3, 601, 1003),
+                                          (25, 4, 1501, 999)])
 def test_rows_of_no_group(rows, e, k, n, t):
     """Rows before the first and behind the last group hold NaN: neither read nor
     written, and the gradients stay finite."""
