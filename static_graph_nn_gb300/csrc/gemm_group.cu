@@ -21,6 +21,11 @@
 // conflict-free transposed writes and no bounds in the inner tiles (30
 // TFLOP/s); 8x8 outputs with 64 threads a tile read less but leave too few warps
 // (161).
+//
+// Where the tiles are fewer than half the resident blocks, each one's sum is
+// split over several blocks through the workspace and joined in order by a
+// second launch: 111 rows x 3148x1224, one group, dX in fp32: 126 us whole, 39 so.
+#include <algorithm>
 #include <cstdio>
 
 #include "../../include/mg.h"
@@ -88,8 +93,10 @@ __device__ __forceinline__ void fma2(uint64_t& c, uint64_t a, uint64_t b) {
   asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(a), "l"(b));
 }
 
+// splits > 1: part s of every tile's sum goes, as it is, to rows s * out_rows ..
+// of g.ws.
 template <typename T, int KIND>
-__global__ void __launch_bounds__(S_THREADS, 4) group_simt_kernel(const GroupArgs g) {
+__global__ void __launch_bounds__(S_THREADS, 4) group_simt_kernel(const GroupArgs g, int splits, long long out_rows) {
   extern __shared__ int s_tab[];
   __shared__ __align__(16) SimtStage st[S_STAGES];
   GroupTable t;
@@ -103,14 +110,16 @@ __global__ void __launch_bounds__(S_THREADS, 4) group_simt_kernel(const GroupArg
   const int N = KIND == GROUP_DX ? g.d_in : g.d_out;
   const int tiles_n = (N + S_T - 1) / S_T;
   const int tiles_k = (g.d_in + S_T - 1) / S_T;          // DW: row tiles of each dW[e]
-  const long long items = KIND == GROUP_DW ? (long long)g.groups * tiles_k * tiles_n
-                                           : (long long)t.cum[t.n - 1] * tiles_n;
+  const long long items = splits * (KIND == GROUP_DW ? (long long)g.groups * tiles_k * tiles_n
+                                                     : (long long)t.cum[t.n - 1] * tiles_n);
   const T* A = static_cast<const T*>(g.A);
   const T* B = static_cast<const T*>(g.B);
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;   // rows ty*4.. and 32+ty*4.., columns tx*4..
   int e = 0;
   for (long long item = blockIdx.x; item < items; item += gridDim.x) {
-    const int mt = (int)(item / tiles_n), n0 = (int)(item % tiles_n) * S_T;
+    const int part = (int)(item % splits);
+    const long long tile = item / splits;
+    const int mt = (int)(tile / tiles_n), n0 = (int)(tile % tiles_n) * S_T;
     int m0, m_end, K;
     long long krow0 = 0;
     if (KIND == GROUP_DW) {
@@ -126,6 +135,9 @@ __global__ void __launch_bounds__(S_THREADS, 4) group_simt_kernel(const GroupArg
       K = e < g.groups ? K0 : 0;
     }
     const T* W = KIND == GROUP_DW || e >= g.groups ? B : B + (size_t)e * g.d_in * g.d_out;
+    const int steps = (K + S_K - 1) / S_K;
+    const int k_lo = (int)((long long)steps * part / splits) * S_K;
+    K = min(K, (int)((long long)steps * (part + 1) / splits) * S_K);       // this part: [k_lo, K)
     auto fetch = [&](int k0) {
       SimtStage& q = st[k0 / S_K % S_STAGES];
       if (k0 < K) {
@@ -142,9 +154,9 @@ __global__ void __launch_bounds__(S_THREADS, 4) group_simt_kernel(const GroupArg
     };
     uint64_t acc2[4][4] = {};              // the thread's rows 2i and 2i + 1, column j
     __syncthreads();                       // the previous tile's last step has been read
-    fetch(0);
-    fetch(S_K);
-    for (int k0 = 0; k0 < K; k0 += S_K) {
+    fetch(k_lo);
+    fetch(k_lo + S_K);
+    for (int k0 = k_lo; k0 < K; k0 += S_K) {
       asm volatile("cp.async.wait_group 1;" ::: "memory");
       __syncthreads();                     // this step is there for all, the one before is read
       fetch(k0 + 2 * S_K);
@@ -174,31 +186,113 @@ __global__ void __launch_bounds__(S_THREADS, 4) group_simt_kernel(const GroupArg
         const int n = n0 + tx * 4 + j;
         if (n >= N) continue;
         float x = __uint_as_float((uint32_t)(acc2[i / 2][j] >> (i % 2 * 32)));
-        if (KIND == GROUP_DW) {
-          static_cast<float*>(g.out)[((size_t)e * g.d_in + m) * g.d_out + n] = x;
-          continue;
-        }
-        group_epilogue<T>(g, (size_t)m * N + n, x);
+        const size_t o = (size_t)((KIND == GROUP_DW ? (long long)e * g.d_in : 0) + m) * N + n;
+        if (splits > 1) g.ws[(size_t)part * out_rows * N + o] = x;
+        else if (KIND == GROUP_DW) static_cast<float*>(g.out)[o] = x;
+        else group_epilogue<T>(g, o, x);
       }
     }
   }
 }
 
+// Tiles at most (every group may end inside one).
+long long simt_tiles(int kind, int rows, int groups, int d_in, int d_out) {
+  const long long tiles_n = ((kind == GROUP_DX ? d_in : d_out) + S_T - 1) / S_T;
+  return tiles_n * (kind == GROUP_DW ? (long long)groups * ((d_in + S_T - 1) / S_T)
+                                     : (long long)rows / S_T + std::min(groups, rows));
+}
+
+// Parts of every tile's sum: as many as fill 4 x 152 blocks, of twelve K steps at
+// least (on average over the groups in dW).
+int simt_splits(int kind, int rows, int groups, int d_in, int d_out) {
+  const long long tiles = simt_tiles(kind, rows, groups, d_in, d_out);
+  const long long steps = (kind == GROUP_FWD ? d_in : kind == GROUP_DX ? d_out : rows / groups) / S_K;
+  const long long s = std::min(std::min(4 * 152 / std::max(tiles, 1ll), steps / 12), 16ll);
+  return s < 2 ? 1 : (int)s;
+}
+
 template <typename T, int KIND>
-cudaError_t simt_launch(const GroupArgs& g, cudaStream_t s) {
-  const int N = KIND == GROUP_DX ? g.d_in : g.d_out;
-  const long long tiles_n = (N + S_T - 1) / S_T;
-  const long long tiles_m = KIND == GROUP_DW ? (long long)g.groups * ((g.d_in + S_T - 1) / S_T)
-                                             : (long long)g.rows / S_T + g.groups + 2;   // at most
-  const long long items = tiles_m * tiles_n;
+cudaError_t simt_launch(const GroupArgs& given, cudaStream_t s) {
+  GroupArgs g = given;
+  const int splits = g.ws ? simt_splits(KIND, g.rows, g.groups, g.d_in, g.d_out) : 1;
+  if (splits > 1) g.zero_rest = 0;       // those rows are the join's
+  const long long items = splits * (simt_tiles(KIND, g.rows, g.groups, g.d_in, g.d_out) +
+                                    (g.zero_rest ? 2 : 0) * ((KIND == GROUP_DX ? g.d_in : g.d_out) / S_T + 1));
   const int slots = 4 * device_sms();
   const int grid = (int)(items < slots ? items : slots);
   const size_t smem = (size_t)kGroupTableInts(g.groups) * sizeof(int);
-  group_simt_kernel<T, KIND><<<grid, S_THREADS, smem, s>>>(g);
-  return cudaGetLastError();
+  const long long out_rows = group_out_rows(KIND, g.rows, g.groups, g.d_in);
+  group_simt_kernel<T, KIND><<<grid, S_THREADS, smem, s>>>(g, splits, out_rows);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || splits == 1) return e;
+  return group_join(given, splits, out_rows, KIND == GROUP_DX ? g.d_in : g.d_out, s);
+}
+
+template <typename T, int KIND>
+__global__ void __launch_bounds__(256) group_join_kernel(const GroupArgs g, int splits, long long rows, int N) {
+  dependency_wait();
+  __shared__ int s_first, s_last;
+  if (KIND != GROUP_DW) {
+    if (threadIdx.x < 32) {
+      int hi = 0;
+      for (int e = threadIdx.x; e <= g.groups; e += 32) hi = max(hi, min(g.offsets[e], g.rows));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+      if (threadIdx.x == 0) {
+        s_first = min(max(g.offsets[0], 0), g.rows);
+        s_last = hi;
+      }
+    }
+    __syncthreads();
+  }
+  const long long total = rows * N;
+  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
+    bool inside = true;
+    if (KIND != GROUP_DW) {
+      const long long r = i / N;
+      inside = r >= s_first && r < s_last;
+      if (!inside && !g.zero_rest) continue;
+    }
+    float x = 0.0f;
+    if (inside)
+      for (int s = 0; s < splits; ++s) x += g.ws[s * total + i];
+    if (KIND == GROUP_DW) static_cast<float*>(g.out)[i] = x;
+    else group_epilogue<T>(g, (size_t)i, x);
+  }
+}
+
+template <typename T, int KIND>
+cudaError_t join_launch(const GroupArgs& g, int splits, long long rows, int N, cudaStream_t s) {
+  const long long blocks = (rows * N + 255) / 256;
+  return launch_dependent(group_join_kernel<T, KIND>, (unsigned)std::min(blocks, 152ll * 8), 256, 0, s, g, splits, rows, N);
 }
 
 }  // namespace
+
+size_t grouped_simt_split_bytes(int rows, int groups, int d_in, int d_out) {
+  size_t most = 0;
+  for (int kind : {GROUP_FWD, GROUP_DX, GROUP_DW}) {
+    const int s = simt_splits(kind, rows, groups, d_in, d_out);
+    const int N = kind == GROUP_DX ? d_in : d_out;
+    if (s > 1) most = std::max<size_t>(most, (size_t)s * group_out_rows(kind, rows, groups, d_in) * N * 4);
+  }
+  return most;
+}
+
+cudaError_t group_join(const GroupArgs& g, int splits, long long rows, int N, cudaStream_t s) {
+  if (g.kind == GROUP_DW) return join_launch<float, GROUP_DW>(g, splits, rows, N, s);
+  if (g.type == DT_F32)
+    return g.kind == GROUP_FWD ? join_launch<float, GROUP_FWD>(g, splits, rows, N, s)
+                               : join_launch<float, GROUP_DX>(g, splits, rows, N, s);
+  return g.kind == GROUP_FWD ? join_launch<bf16, GROUP_FWD>(g, splits, rows, N, s)
+                             : join_launch<bf16, GROUP_DX>(g, splits, rows, N, s);
+}
+
+int grouped_launches(const GroupArgs& g) {
+  if (g.rows == 0 && g.kind != GROUP_DW) return 0;
+  if (grouped_tc_eligible(g)) return grouped_tc_launches(g);
+  return g.ws && simt_splits(g.kind, g.rows, g.groups, g.d_in, g.d_out) > 1 ? 2 : 1;
+}
 
 cudaError_t grouped_gemm(const GroupArgs& g, cudaStream_t s) {
   if (g.rows == 0 && g.kind != GROUP_DW) return cudaSuccess;

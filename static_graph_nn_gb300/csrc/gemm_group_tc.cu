@@ -557,51 +557,7 @@ size_t group_pair_smem(int kind, bool any, int groups) {
          (size_t)kGroupTableInts(groups) * 4;
 }
 
-// ---- joining of split tiles
-// out = the sum of the parts in order, through the epilogue (forward, dX: rows
-// of a group, and with zero_rest the others as zeros).
-template <int KIND>
-__global__ void __launch_bounds__(256) group_join_kernel(const GroupArgs g, const float* part, int splits, long long rows,
-                                                         int N) {
-  dependency_wait();
-  __shared__ int s_first, s_last;
-  if (KIND != GROUP_DW) {
-    if (threadIdx.x < 32) {
-      int hi = 0;
-      for (int e = threadIdx.x; e <= g.groups; e += 32) hi = max(hi, min(g.offsets[e], g.rows));
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-      if (threadIdx.x == 0) {
-        s_first = min(max(g.offsets[0], 0), g.rows);
-        s_last = hi;
-      }
-    }
-    __syncthreads();
-  }
-  const long long total = rows * N / 4;              // N is a multiple of 8
-  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
-    bool inside = true;
-    if (KIND != GROUP_DW) {
-      const long long r = i * 4 / N;
-      inside = r >= s_first && r < s_last;
-      if (!inside && !g.zero_rest) continue;
-    }
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (inside)
-      for (int s = 0; s < splits; ++s) {
-        const float4 p = reinterpret_cast<const float4*>(part)[s * total + i];
-        v.x += p.x; v.y += p.y; v.z += p.z; v.w += p.w;
-      }
-    if (KIND == GROUP_DW) {
-      reinterpret_cast<float4*>(g.out)[i] = v;
-    } else {
-      const float f[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll 1
-      for (int q = 0; q < 4; ++q) group_epilogue<bf16>(g, (size_t)i * 4 + q, f[q]);
-    }
-  }
-}
-
+// ---- few tiles
 // Parts of the K blocks for these sizes: as many as keep 76 pairs busy, with at
 // least eight blocks each (on average over the groups in dW).
 int group_splits(int kind, int rows, int groups, int d_in, int d_out) {
@@ -613,10 +569,6 @@ int group_splits(int kind, int rows, int groups, int d_in, int d_out) {
   const long long kb = kind == GROUP_DW ? (long long)rows / groups / G_BK : (K + G_BK - 1) / G_BK;
   const long long s = std::min(std::min(76 / tiles, kb / 8), 16ll);
   return s < 2 ? 1 : (int)s;
-}
-
-long long group_out_rows(int kind, int rows, int groups, int d_in) {
-  return kind == GROUP_DW ? (long long)groups * d_in : rows;
 }
 
 size_t split_bytes(int kind, int rows, int groups, int d_in, int d_out) {
@@ -703,9 +655,7 @@ cudaError_t launch_group_pair(const GroupArgs& g, int splits, cudaStream_t s) {
   kern<<<2 * pairs, group_threads(KIND), smem, s>>>(ma, mb, mo, P);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || splits == 1) return e;
-  const long long quads = (long long)P.split_rows * N / 4, blocks = (quads + 255) / 256;
-  return launch_dependent(group_join_kernel<KIND>, (unsigned)std::min(blocks, 152ll * 8), 256, 0, s, g,
-                          static_cast<const float*>(g.ws), splits, (long long)P.split_rows, N);
+  return group_join(g, splits, P.split_rows, N, s);
 }
 
 // ---- operands of widths that are no multiples of 8
@@ -791,7 +741,7 @@ bool grouped_tc_eligible(const GroupArgs& g) {
 }
 
 size_t grouped_scratch_bytes(int rows, int groups, int d_in, int d_out) {
-  size_t most = 0;
+  size_t most = grouped_simt_split_bytes(rows, groups, d_in, d_out);
   for (int kind : {GROUP_FWD, GROUP_DX, GROUP_DW}) {
     size_t n = split_bytes(kind, rows, groups, d_in, d_out);
     if (group_repacks(kind, rows, groups, d_in, d_out))
@@ -801,8 +751,7 @@ size_t grouped_scratch_bytes(int rows, int groups, int d_in, int d_out) {
   return most;
 }
 
-int grouped_launches(const GroupArgs& g) {
-  if (!grouped_tc_eligible(g)) return 1;
+int grouped_tc_launches(const GroupArgs& g) {
   if (g.d_in % 8 || g.d_out % 8)
     return 1 + (operand_a(g.kind, g.rows, g.d_in, g.d_out).width % 8 != 0) +
            (operand_b(g.kind, g.rows, g.groups, g.d_in, g.d_out).width % 8 != 0);

@@ -215,8 +215,17 @@ struct GroupArgs {
   int* err = nullptr;          // set to 1 on a timed-out wait
   float* ws = nullptr;         // grouped_scratch_bytes; NULL: no split over K, no repacked operands
 };
-// Scratch of the tensor-core products of these sizes (any kind), 16-byte aligned.
+// Scratch of the products of these sizes (any kind and type), 16-byte aligned.
 size_t grouped_scratch_bytes(int rows, int groups, int d_in, int d_out);
+size_t grouped_simt_split_bytes(int rows, int groups, int d_in, int d_out);   // the CUDA-core part of it
+// Rows of the output matrix: g.rows, or groups * d_in in dW.
+inline long long group_out_rows(int kind, int rows, int groups, int d_in) {
+  return kind == GROUP_DW ? (long long)groups * d_in : rows;
+}
+// out = the sum of g.ws [splits][rows][N] in order, through the epilogue
+// (forward, dX: rows of a group, and with zero_rest the others as zeros); a
+// dependent launch.
+cudaError_t group_join(const GroupArgs& g, int splits, long long rows, int N, cudaStream_t s);
 int grouped_launches(const GroupArgs& g);   // kernels of grouped_gemm(g)
 constexpr int kMaxGroups = 1024;
 cudaError_t grouped_gemm(const GroupArgs& g, cudaStream_t s);
@@ -228,6 +237,7 @@ cudaError_t grouped_gemm_narrow(const GroupArgs& g, cudaStream_t s);
 // products and with scratch.
 bool grouped_tc_eligible(const GroupArgs& g);
 cudaError_t grouped_gemm_tc(const GroupArgs& g, cudaStream_t s);
+int grouped_tc_launches(const GroupArgs& g);
 
 // ---- misc --------------------------------------------------------------------
 cudaError_t cast_to_f32(DType t, const void* src, float* dst, size_t n, cudaStream_t s);

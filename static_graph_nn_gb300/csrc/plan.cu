@@ -1178,7 +1178,7 @@ void layout_workspace(mg_plan* p) {
   size_t group_ws = 0;
   for (const Node& n : p->nodes) {
     if (n.kind == NK_EMBED) p->embed_off = b.take(embedding_ws_bytes(p->batch, n.d_in, n.d_out));
-    if (n.kind == NK_GROUP && p->dt == DT_BF16)
+    if (n.kind == NK_GROUP)
       group_ws = std::max(group_ws, grouped_scratch_bytes(p->batch, n.groups, n.d_in, n.d_out));
   }
   if (group_ws) p->group_off = b.take(group_ws);

@@ -88,7 +88,7 @@ SHAPES = [
     # few tiles and long sums over d_in, d_out and the rows: split over blocks and joined
     (300, 2, 1032, 136), (200, 3, 136, 2056), (5000, 2, 200, 72), (4000, 3, 72, 264), (700, 1, 2056, 1032),
     # widths that rows of 16 bytes do not divide
-    (700, 3, 601, 1003), (640, 2, 1001, 520), (1500, 4, 520, 999), (20, 4, 1501, 999), (30, 3, 1000, 2003),
+    (111, 1, 404, 1003), (130, 2, 1003, 70), (3000, 2, 65, 33), (700, 3, 601, 1003), (640, 2, 1001, 520), (1500, 4, 520, 999), (20, 4, 1501, 999), (30, 3, 1000, 2003),
     (77, 3, 33, 17), (300, 5, 1, 1), (50, 2, 100, 65),
 ]
 
