@@ -42,7 +42,7 @@ constexpr int kSortThreads = 256;
 constexpr int kSortItems = 16;                            // per thread
 constexpr int kSortTile = kSortThreads * kSortItems;      // 4096 keys per block
 constexpr int kWarps = kSortThreads / 32;
-constexpr int kWindows = 512;       // windows a call is cut into (8 entries at least)
+constexpr int kSumThreads = 65536;  // threads that sum: windows of the sorted order times threads a row
 constexpr int kCluster = 4;         // CTAs that sort together
 constexpr int kSmallThreads = 1024;
 constexpr int kSmallItems = 16;     // ids per thread at most
@@ -809,7 +809,10 @@ struct Ws {
 Ws ws_layout(long long n, int V, int d) {
   Ws w = {};
   w.col_tiles = (d + 1023) / 1024;    // at most: 256 threads of 4 columns or more
-  long long win = ((n + kWindows - 1) / kWindows + 7) / 8 * 8;
+  // as many windows (of 8 entries at least) as give kSumThreads threads at 16
+  // columns each: 512 for rows of 2048, 8192 for rows of 128
+  const long long windows = kSumThreads / threads_per_row((d + 15) / 16);
+  long long win = ((n + windows - 1) / windows + 7) / 8 * 8;
   w.window = (uint32_t)(win > 8 ? win : 8);
   w.n_windows = (uint32_t)((n + w.window - 1) / w.window);
   w.sort_blocks = (uint32_t)((n + kSortTile - 1) / kSortTile);

@@ -202,12 +202,14 @@ long long simt_tiles(int kind, int rows, int groups, int d_in, int d_out) {
                                      : (long long)rows / S_T + std::min(groups, rows));
 }
 
-// Parts of every tile's sum: as many as fill 4 x 152 blocks, of twelve K steps at
+constexpr long long kSplitBlocks = 2 * 4 * 152;
+
+// Parts of every tile's sum: as many as fill 4 x 152 blocks twice, of twelve K steps at
 // least (on average over the groups in dW).
 int simt_splits(int kind, int rows, int groups, int d_in, int d_out) {
   const long long tiles = simt_tiles(kind, rows, groups, d_in, d_out);
   const long long steps = (kind == GROUP_FWD ? d_in : kind == GROUP_DX ? d_out : rows / groups) / S_K;
-  const long long s = std::min(std::min(4 * 152 / std::max(tiles, 1ll), steps / 12), 16ll);
+  const long long s = std::min(std::min(kSplitBlocks / std::max(tiles, 1ll), steps / 12), 16ll);
   return s < 2 ? 1 : (int)s;
 }
 

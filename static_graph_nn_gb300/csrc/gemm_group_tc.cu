@@ -97,6 +97,7 @@ constexpr int G_PANEL = 64 * G_BK * 2;   // one 64-column panel of a stage
 struct GroupTcParams {
   GemmArgs g;              // the epilogue: N, leading dimensions, outputs
   GroupArgs any;           // the same for widths that are no multiples of 8
+  int plain;               // nothing but the sum is stored
   const int* offsets;
   int rows, groups, zero_rest;
   int d_in, d_out;
@@ -204,13 +205,19 @@ __device__ __forceinline__ void store_any(const GroupTcParams& P, float* buf, co
     }
     __syncwarp();
     const int rows = min(16, m_end - row0 - 16 * h);
+    if (n0 + lane >= P.g.N) continue;
+    const size_t o = (size_t)(base + row0 + 16 * h) * P.g.N + n0 + lane;
+    if (KIND == GROUP_DW || P.splits > 1) {
+      float* out = static_cast<float*>(P.g.out) + o;
+#pragma unroll 4
+      for (int r = 0; r < rows; ++r) out[(size_t)r * P.g.N] = buf[r * 32 + ((lane + r) & 31)];
+    } else if (P.plain) {
+      bf16* out = static_cast<bf16*>(P.any.out) + o;
+#pragma unroll 4
+      for (int r = 0; r < rows; ++r) out[(size_t)r * P.g.N] = __float2bfloat16_rn(buf[r * 32 + ((lane + r) & 31)]);
+    } else {
 #pragma unroll 1
-    for (int r = 0; r < rows; ++r) {
-      if (n0 + lane >= P.g.N) continue;
-      const float x = buf[r * 32 + ((lane + r) & 31)];
-      const size_t o = (size_t)(base + row0 + 16 * h + r) * P.g.N + n0 + lane;
-      if (KIND == GROUP_DW) static_cast<float*>(P.any.out)[o] = x;
-      else group_epilogue<bf16>(P.any, o, x);
+      for (int r = 0; r < rows; ++r) group_epilogue<bf16>(P.any, o + (size_t)r * P.g.N, buf[r * 32 + ((lane + r) & 31)]);
     }
   }
 }
@@ -458,7 +465,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(group_threads(KIND),
           const int n = n0 + c * 32;
           if (n >= P.g.N) continue;                                  // warp-uniform, as below
           if constexpr (ANY) {
-            store_any<KIND>(P, reinterpret_cast<float*>(buf), sum[c], row0, T.m_end, T.e * P.d_in, n, lane);
+            store_any<KIND>(P, reinterpret_cast<float*>(buf), sum[c], row0, T.m_end,
+                            T.e * P.d_in + T.part * P.split_rows, n, lane);
           } else {
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
@@ -499,7 +507,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(group_threads(KIND),
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = T.kb ? __uint_as_float(r[i]) : 0.0f;
           if (ANY)
-            store_any<KIND>(P, reinterpret_cast<float*>(sO + (warp - 2) * 2048), v, m - lane, T.m_end, 0, n, lane);
+            store_any<KIND>(P, reinterpret_cast<float*>(sO + (warp - 2) * 2048), v, m - lane, T.m_end, T.part * P.split_rows, n,
+                            lane);
           else if (n + 32 <= P.g.N) epi32<TO>(P.g, true, P.vec32 != 0, mo, n, v);
           else epi_by8<TO>(P.g, mo, n, v);
         };
@@ -561,7 +570,6 @@ size_t group_pair_smem(int kind, bool any, int groups) {
 // Parts of the K blocks for these sizes: as many as keep 76 pairs busy, with at
 // least eight blocks each (on average over the groups in dW).
 int group_splits(int kind, int rows, int groups, int d_in, int d_out) {
-  if (d_in % 8 || d_out % 8) return 1;
   const int N = kind == GROUP_DX ? d_in : d_out, K = kind == GROUP_FWD ? d_in : d_out;
   const long long tiles_n = (N + G_BN - 1) / G_BN;
   const long long tiles = kind == GROUP_DW ? groups * ((d_in + 2ll * G_BM - 1) / (2 * G_BM)) * tiles_n
@@ -595,6 +603,7 @@ cudaError_t launch_group_pair(const GroupArgs& g, int splits, cudaStream_t s) {
   GroupTcParams P;
   const int N = KIND == GROUP_DX ? g.d_in : g.d_out;
   P.any = g;
+  P.plain = !g.act && !g.out_z && !g.dact && !g.resid;
   P.splits = splits;
   P.split_rows = (int)group_out_rows(g.kind, g.rows, g.groups, g.d_in);
   P.g.N = N;
@@ -745,17 +754,16 @@ size_t grouped_scratch_bytes(int rows, int groups, int d_in, int d_out) {
   for (int kind : {GROUP_FWD, GROUP_DX, GROUP_DW}) {
     size_t n = split_bytes(kind, rows, groups, d_in, d_out);
     if (group_repacks(kind, rows, groups, d_in, d_out))
-      n = operand_a(kind, rows, d_in, d_out).bytes() + operand_b(kind, rows, groups, d_in, d_out).bytes();
+      n += operand_a(kind, rows, d_in, d_out).bytes() + operand_b(kind, rows, groups, d_in, d_out).bytes();
     most = std::max(most, n);
   }
   return most;
 }
 
 int grouped_tc_launches(const GroupArgs& g) {
-  if (g.d_in % 8 || g.d_out % 8)
-    return 1 + (operand_a(g.kind, g.rows, g.d_in, g.d_out).width % 8 != 0) +
-           (operand_b(g.kind, g.rows, g.groups, g.d_in, g.d_out).width % 8 != 0);
-  return g.ws && !grouped_narrow(g) && group_splits(g.kind, g.rows, g.groups, g.d_in, g.d_out) > 1 ? 2 : 1;
+  return 1 + (operand_a(g.kind, g.rows, g.d_in, g.d_out).width % 8 != 0) +
+         (operand_b(g.kind, g.rows, g.groups, g.d_in, g.d_out).width % 8 != 0) +
+         (g.ws && !grouped_narrow(g) && group_splits(g.kind, g.rows, g.groups, g.d_in, g.d_out) > 1);
 }
 
 cudaError_t grouped_gemm_tc(const GroupArgs& given, cudaStream_t s) {
@@ -766,14 +774,15 @@ cudaError_t grouped_gemm_tc(const GroupArgs& given, cudaStream_t s) {
     cudaError_t e = repack(g.A, g.lda, operand_a(g.kind, g.rows, g.d_in, g.d_out), ws, s);
     if (e == cudaSuccess) e = repack(g.B, g.ldb, operand_b(g.kind, g.rows, g.groups, g.d_in, g.d_out), ws, s);
     if (e != cudaSuccess) return e;
+    g.ws = reinterpret_cast<float*>(ws);
   }
   if (grouped_narrow(g)) return grouped_gemm_narrow(g, s);
-  if (any) {
-    if (g.kind == GROUP_DW) return launch_group_pair<GROUP_DW, float, true>(g, 1, s);
-    return g.kind == GROUP_FWD ? launch_group_pair<GROUP_FWD, bf16, true>(g, 1, s)
-                               : launch_group_pair<GROUP_DX, bf16, true>(g, 1, s);
-  }
   const int splits = g.ws ? group_splits(g.kind, g.rows, g.groups, g.d_in, g.d_out) : 1;
+  if (any) {
+    if (g.kind == GROUP_DW) return launch_group_pair<GROUP_DW, float, true>(g, splits, s);
+    return g.kind == GROUP_FWD ? launch_group_pair<GROUP_FWD, bf16, true>(g, splits, s)
+                               : launch_group_pair<GROUP_DX, bf16, true>(g, splits, s);
+  }
   if (g.kind == GROUP_DW) return launch_group_pair<GROUP_DW, float, false>(g, splits, s);
   if (g.kind == GROUP_FWD)
     return splits > 1 ? launch_group_pair<GROUP_FWD, float, false>(g, splits, s)
