@@ -461,6 +461,9 @@ extern "C" mg_status mg_grad_list_create(int n, const void* const* grads, void* 
     if (e == cudaSuccess) e = cudaMemset(l->ws + l->partial_off, 0, bytes - l->partial_off);
     if (e != cudaSuccess) {
       cudaFree(l->ws);
+    // both may still be on their way, and a caller's stream need not wait for
+    // the default one
+    if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
       return mg::op_end(fn, e);
     }
     *list = l.release();

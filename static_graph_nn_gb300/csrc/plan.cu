@@ -1610,7 +1610,11 @@ mg_status mg_set_row_groups(mg_plan* p, const int* offsets) {
   mg_status st = check_device(p);
   if (st != MG_OK) return st;
   // 4-byte aligned memory of this device (the message is the process-wide one)
-  if ((st = op_begin("mg_set_row_groups", {{offsets, 4}})) != MG_OK) return fail(p, st, "%s", std::string(mg_last_error(nullptr)).c_str());
+  if ((st = op_begin("mg_set_row_groups", {{offsets, 4}})) != MG_OK) {
+    char msg[512];
+    snprintf(msg, sizeof msg, "%s", mg_last_error(nullptr));
+    return fail(p, st, "%s", msg);
+  }
   if (offsets != p->row_groups)
     for (auto& g : p->graphs) {      // captured steps hold the old pointer
       drop_graph(g);
@@ -1637,6 +1641,7 @@ mg_status mg_set_grad_clip(mg_plan* p, float max_norm) {
     e = cudaMemset(p->clip_ws, 0, bytes);
     if (e != cudaSuccess) {
       cudaFree(p->clip_ws);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);   // the steps' stream need not wait for the default one
       p->clip_ws = nullptr;
       return cuda_fail(p, e, "mg_set_grad_clip");
     }

@@ -1,7 +1,7 @@
 """Global gradient norm and clipping over lists of tensors, against the
 definitions in 64 bits.
 
-Tolerances.  Sixteen squares are added in fp32 (four running sums of four, two
+Tolerances.  32 squares are added in fp32 (eight running sums of four, three
 more additions: at most seven roundings a term, relative 7 * 2^-24 of a sum of
 nonnegative terms), the rest in fp64; the root halves that, and rounding the
 result adds 2^-24: 4.5 * 2^-24 for the norm.  The factor adds one rounding, the
@@ -185,3 +185,20 @@ def test_streams_and_graph_replay():
         torch.cuda.synchronize()
         _check(grads, outs, stats, 0.5)
     lst.close()
+
+
+def test_list_is_ready_for_any_stream():
+    """Clipping on a stream that does not wait for the default one, directly
+    after the list was made (its table and counters are complete by then)."""
+    s = torch.cuda.Stream()
+    for i in range(20):
+        grads = _make([70001] * 16, ["f32"], i)
+        norm, c = _want(grads, 1.0)
+        stats = torch.zeros(2, device="cuda")
+        torch.cuda.synchronize()
+        gl = mg.GradList(grads)
+        gl.clip(1.0, stats, stream=s)
+        s.synchronize()
+        gl.close()
+        assert abs(float(stats[0]) - norm) <= NORM_TOL * norm
+        assert abs(float(stats[1]) - c) <= (NORM_TOL + U32) * c
