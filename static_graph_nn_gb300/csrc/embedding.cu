@@ -878,7 +878,7 @@ cudaError_t embedding_fwd(DType tt, const void* table, int V, int d, int id64, c
 template <int IPT>
 static cudaError_t sort_small(const SmallArgs& A, cudaStream_t s) {
   constexpr size_t smem = sizeof(SmallSmem<IPT>) > kZeroRange / 8 ? sizeof(SmallSmem<IPT>) : kZeroRange / 8;
-  static const cudaError_t attr =
+  const cudaError_t attr =    // of this device's context: set in every call
       cudaFuncSetAttribute(sort_small_kernel<IPT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (attr != cudaSuccess) return attr;
   // clusters that run at once (a cluster's CTAs share a GPC, so some SMs may
@@ -947,8 +947,8 @@ cudaError_t embedding_bwd_sort(int id64, const void* ids, long long n, int V, in
 template <typename T, bool VEC>
 static cudaError_t sum_launch(const SumArgs& A, unsigned grid, cudaStream_t s) {
   constexpr int smem = Fetch<T, VEC>::SMEM;
-  static const cudaError_t attr = cudaFuncSetAttribute(embed_sum_kernel<T, VEC>,
-                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t attr =
+      cudaFuncSetAttribute(embed_sum_kernel<T, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (attr != cudaSuccess) return attr;
   return launch_dependent(embed_sum_kernel<T, VEC>, grid, 256, smem, s, A);
 }

@@ -270,7 +270,7 @@ cudaError_t launch_narrow(const GroupArgs& g, cudaStream_t s) {
                                      : group_map(&mw, g.B, g.groups, g.d_in, g.d_out, g.ldb, N_BK, N_M)) &&
                   group_map(&mx, g.A, 0, g.rows, k, g.lda, N_BK, N_T);
   if (!ok) return cudaErrorInvalidValue;
-  static const cudaError_t attr = cudaFuncSetAttribute(
+  const cudaError_t attr = cudaFuncSetAttribute(    // of this device's context: set in every call
       group_narrow_kernel<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)narrow_smem(kMaxGroups, N_SPLIT));
   if (attr != cudaSuccess) return attr;
   const int sms = device_sms();

@@ -633,7 +633,7 @@ cudaError_t launch_group_pair(const GroupArgs& g, int splits, cudaStream_t s) {
   P.vec32 = al(P.g.out, 32) && al(P.g.out_z, 32) && al(P.g.saved, 32) && al(P.g.resid, 32) && N % 16 == 0;
   auto kern = group_pair_kernel<KIND, TO, ANY>;
   const size_t smem = group_pair_smem(KIND, ANY, g.groups);
-  static const cudaError_t attr = cudaFuncSetAttribute(
+  const cudaError_t attr = cudaFuncSetAttribute(    // of this device's context: set in every call
       kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)group_pair_smem(KIND, ANY, kMaxGroups));
   if (attr != cudaSuccess) return attr;
   static const int slots = [&] {
