@@ -364,7 +364,7 @@ mg_status mg_softmax_ce_noalloc(int dtype, const void* logits, int rows, int col
  * Embedding: out[i, :] = scale * table[ids[i], :], rounded once to out's type.
  * id_kind 0 = int32, 1 = int64.  An id outside [0, vocab) -- padding -- reads
  * nothing: its row of out is 0.  table [vocab, dim], ids [n], out [n, dim];
- * n = 0 is allowed.
+ * n = 0 is allowed, dim is at most 2^30.
  *
  * Its gradient: dtable[v, :] = scale * sum over i with ids[i] == v of
  * dout[i, :], fp32 sums in ascending i order (long runs in a fixed order of
@@ -390,8 +390,10 @@ mg_status mg_embedding_backward(int dtype, const void* dout, int vocab, int dim,
  *   backward_weight  dw[e] = x_e^T dy_e              [groups, d_in, d_out], fp32
  * dtype is the type of x, w, y, dx, dy; sums are fp32.  Rows outside
  * [offsets[0], offsets[groups]) are neither read nor written; dw of an empty
- * group is 0.  groups at most 1024.  bf16 widths that are multiples of 8 run
- * on the tensor cores, others and fp32 on the CUDA cores.
+ * group is 0.  groups at most 1024, rows and widths at most 2^30.  bf16 runs on
+ * the tensor cores (rows of widths that are no multiples of 8 are copied to
+ * aligned ones in the workspace first; small products of such widths, and fp32,
+ * run on the CUDA cores).
  * workspace: mg_grouped_linear_workspace_bytes; zero it once before its first
  * use.  Its first int is set to 1 if a bounded device-side wait gave up, in
  * which case that call's results are invalid. */

@@ -997,8 +997,8 @@ constexpr long long kMaxIds = 0x7fffff00ll;   // positions and segment bounds ar
 mg_status check_embedding(const char* fn, int dtype, int id_kind, long long n, int vocab, int dim, float scale) {
   if ((dtype != 0 && dtype != 1) || (id_kind != 0 && id_kind != 1))
     return op_fail(MG_ERR_INVALID_ARG, "%s: dtypes and id_kind must be 0 or 1", fn);
-  if (vocab < 1 || vocab == 0x7fffffff || dim < 1)
-    return op_fail(MG_ERR_SHAPE, "%s: vocab and dim must be positive (got %d, %d)", fn, vocab, dim);
+  if (vocab < 1 || vocab == 0x7fffffff || dim < 1 || dim > mg::kMaxWidth)
+    return op_fail(MG_ERR_SHAPE, "%s: vocab and dim must be positive, dim at most 2^30 (got %d, %d)", fn, vocab, dim);
   if (n < 0 || n > kMaxIds)
     return op_fail(MG_ERR_SHAPE, "%s: n must be in [0, %lld] (got %lld)", fn, kMaxIds, n);
   if (!(scale - scale == 0.0f)) return op_fail(MG_ERR_INVALID_ARG, "%s: scale is not finite", fn);
@@ -1008,7 +1008,7 @@ mg_status check_embedding(const char* fn, int dtype, int id_kind, long long n, i
 }  // namespace
 
 extern "C" size_t mg_embedding_workspace_bytes(long long n, int vocab, int dim) {
-  if (n < 0 || n > kMaxIds || vocab < 1 || vocab == 0x7fffffff || dim < 1) return 0;
+  if (n < 0 || n > kMaxIds || vocab < 1 || vocab == 0x7fffffff || dim < 1 || dim > mg::kMaxWidth) return 0;
   return mg::embedding_ws_bytes(n, vocab, dim);
 }
 

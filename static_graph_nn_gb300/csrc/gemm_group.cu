@@ -329,6 +329,9 @@ mg_status grouped_call(const char* fn, mg::GroupKind kind, int dtype, const void
   if (rows < 0 || groups < 1 || d_in < 1 || d_out < 1)
     return op_fail(MG_ERR_SHAPE, "%s: bad sizes (rows %d, groups %d, d_in %d, d_out %d)", fn, rows, groups, d_in,
                    d_out);
+  if (rows > mg::kMaxWidth || d_in > mg::kMaxWidth || d_out > mg::kMaxWidth)
+    return op_fail(MG_ERR_SHAPE, "%s: rows, d_in and d_out must be at most 2^30 (got %d, %d, %d)", fn, rows, d_in,
+                   d_out);
   if (groups > mg::kMaxGroups)
     return op_fail(MG_ERR_UNSUPPORTED, "%s: at most %d groups (got %d)", fn, mg::kMaxGroups, groups);
   const bool rows_needed = rows > 0;
@@ -359,7 +362,9 @@ mg_status grouped_call(const char* fn, mg::GroupKind kind, int dtype, const void
 }  // namespace
 
 extern "C" size_t mg_grouped_linear_workspace_bytes(int rows, int groups, int d_in, int d_out) {
-  if (rows < 0 || groups < 1 || groups > mg::kMaxGroups || d_in < 1 || d_out < 1) return 0;
+  if (rows < 0 || groups < 1 || groups > mg::kMaxGroups || d_in < 1 || d_out < 1 || rows > mg::kMaxWidth ||
+      d_in > mg::kMaxWidth || d_out > mg::kMaxWidth)
+    return 0;
   return workspace_bytes(rows, groups, d_in, d_out);
 }
 

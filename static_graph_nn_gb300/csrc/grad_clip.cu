@@ -389,6 +389,8 @@ struct mg_grad_list {
 
 using mg::op_fail;
 
+static constexpr size_t kMaxChunks = 1u << 26;   // of a list: 2 TB of gradients, before the host allocates for them
+
 extern "C" mg_status mg_grad_list_create(int n, const void* const* grads, void* const* out, const size_t* counts,
                                          const int* dtypes, mg_grad_list** list) {
   const char* fn = "mg_grad_list_create";
@@ -412,7 +414,9 @@ extern "C" mg_status mg_grad_list_create(int n, const void* const* grads, void* 
       const char* g = static_cast<const char*>(grads[i]);
       char* o = out ? static_cast<char*>(out[i]) : const_cast<char*>(g);
       if (!g || !o) return op_fail(MG_ERR_INVALID_ARG, "%s: tensor %d is NULL", fn, i);
-      if (counts[i] > (size_t)1 << 46) return op_fail(MG_ERR_SHAPE, "%s: tensor %d has %zu elements", fn, i, counts[i]);
+      const size_t step = mg::kClipBytes / es;
+      if (counts[i] / step + table.size() > kMaxChunks)
+        return op_fail(MG_ERR_SHAPE, "%s: tensor %d has %zu elements, too many", fn, i, counts[i]);
       mg_status st = mg::op_begin(fn, {{g, (unsigned)es}, {o, (unsigned)es}});
       if (st != MG_OK) return st;
       const uintptr_t gl = reinterpret_cast<uintptr_t>(g), ol = reinterpret_cast<uintptr_t>(o);
@@ -420,11 +424,9 @@ extern "C" mg_status mg_grad_list_create(int n, const void* const* grads, void* 
       if (gl != ol) spans.push_back({gl, gl + bytes, i, false});
       spans.push_back({ol, ol + bytes, i, true});
       const int flags = dtypes[i] | (gl % 16 == 0 && ol % 16 == 0 ? 2 : 0);
-      const size_t step = mg::kClipBytes / es;
       for (size_t a = 0; a < counts[i]; a += step)
         table.push_back({g + a * es, o + a * es, (int)std::min<size_t>(step, counts[i] - a), flags});
     }
-    if (table.size() > 0x7ffffff0u) return op_fail(MG_ERR_SHAPE, "%s: too many elements", fn);
     // a written range may meet no other range (the same tensor twice, or an
     // output inside another tensor, would be scaled twice or read half scaled)
     std::sort(spans.begin(), spans.end(), [](const Span& a, const Span& b) { return a.lo < b.lo; });
@@ -459,11 +461,11 @@ extern "C" mg_status mg_grad_list_create(int n, const void* const* grads, void* 
     if (!table.empty())
       e = cudaMemcpy(l->ws, table.data(), table.size() * sizeof(mg::ClipChunk), cudaMemcpyHostToDevice);
     if (e == cudaSuccess) e = cudaMemset(l->ws + l->partial_off, 0, bytes - l->partial_off);
-    if (e != cudaSuccess) {
-      cudaFree(l->ws);
     // both may still be on their way, and a caller's stream need not wait for
     // the default one
     if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
+    if (e != cudaSuccess) {
+      cudaFree(l->ws);
       return mg::op_end(fn, e);
     }
     *list = l.release();

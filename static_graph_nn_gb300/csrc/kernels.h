@@ -228,6 +228,7 @@ inline long long group_out_rows(int kind, int rows, int groups, int d_in) {
 cudaError_t group_join(const GroupArgs& g, int splits, long long rows, int N, cudaStream_t s);
 int grouped_launches(const GroupArgs& g);   // kernels of grouped_gemm(g)
 constexpr int kMaxGroups = 1024;
+constexpr int kMaxWidth = 1 << 30;   // rows and widths: a tile past the end stays in an int
 cudaError_t grouped_gemm(const GroupArgs& g, cudaStream_t s);
 // The version for a few rows per group (forward and dX; grouped_tc_eligible as
 // well).

@@ -888,7 +888,7 @@ mg_status compile(mg_plan* p, const mg_graph_desc* d) {
     switch (l.op) {
       case MG_OP_EMBEDDING: {
         if (i != 0) return fail(p, MG_ERR_UNSUPPORTED, "layer %d: an embedding must be the first layer", i);
-        if (l.d_in <= 0 || l.d_in == 0x7fffffff || l.d_out <= 0)
+        if (l.d_in <= 0 || l.d_in == 0x7fffffff || l.d_out <= 0 || l.d_out > kMaxWidth)
           return fail(p, MG_ERR_SHAPE, "layer %d: bad embedding sizes (%d ids of width %d)", i, l.d_in, l.d_out);
         if (!std::isfinite(l.eps)) return fail(p, MG_ERR_INVALID_ARG, "layer %d: the embedding's factor is not finite", i);
         Node n;
@@ -915,6 +915,8 @@ mg_status compile(mg_plan* p, const mg_graph_desc* d) {
         if (l.d_in != vc.width)
           return fail(p, MG_ERR_SHAPE, "layer %d: Linear d_in %d != incoming width %d", i, l.d_in, vc.width);
         if (grouped) {
+          if (l.d_in > kMaxWidth || l.d_out > kMaxWidth || p->batch > kMaxWidth)
+            return fail(p, MG_ERR_SHAPE, "layer %d: rows and widths of a grouped Linear are at most 2^30", i);
           if (l.n_heads < 1 || (long long)l.n_heads * l.d_in > 0x7fff0000ll)
             return fail(p, MG_ERR_SHAPE, "layer %d: bad group count %d", i, l.n_heads);
           if (l.n_heads > kMaxGroups)
@@ -1639,9 +1641,9 @@ mg_status mg_set_grad_clip(mg_plan* p, float max_norm) {
       return fail(p, MG_ERR_OOM, "clipping workspace of %zu bytes: %s", bytes, cudaGetErrorString(e));
     }
     e = cudaMemset(p->clip_ws, 0, bytes);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);   // the steps' stream need not wait for the default one
     if (e != cudaSuccess) {
       cudaFree(p->clip_ws);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);   // the steps' stream need not wait for the default one
       p->clip_ws = nullptr;
       return cuda_fail(p, e, "mg_set_grad_clip");
     }

@@ -61,6 +61,19 @@ def test_workspace_sizes(lib):
     assert lib.mg_grouped_linear_workspace_bytes(0, 1, 8, 8) >= 4
 
 
+@pytest.mark.parametrize("sizes", [(2**30 + 1, 2, 8, 8), (4, 2, 2**30 + 1, 8), (4, 2, 8, 2**31 - 1)])
+def test_sizes_beyond_an_int_of_tiles_are_refused(lib, sizes):
+    rows, groups, k, n = sizes
+    assert lib.mg_grouped_linear_workspace_bytes(rows, groups, k, n) == 0
+    for which in ("forward", "backward_input", "backward_weight"):
+        assert _grouped(lib, which, rows=rows, groups=groups, k=k, n=n) == S
+    assert lib.mg_embedding_workspace_bytes(4, 10, 2**30 + 1) == 0
+    assert _fwd(lib, d=2**30 + 1) == S
+    assert _bwd(lib, d=2**31 - 1) == S
+    assert _create(lib, [W.embedding(10, 2**30 + 1), W.linear(2**30 + 1, 4, False)]) == S
+    assert _create(lib, [W.grouped_linear(1, 8, 2**30 + 1)]) == S
+
+
 def _grouped(lib, which, dtype=1, a=P, b=P, off=P, rows=4, groups=2, k=8, n=8, out=P, ws=P, nb=1 << 30):
     if which == "backward_weight":
         return lib.mg_grouped_linear_backward_weight(dtype, a, b, off, rows, groups, k, n, out, ws, nb, None)
@@ -92,7 +105,7 @@ def _list(lib, ptrs, counts, types, out=None):
 
 @pytest.mark.parametrize("args,want", [
     (([], [], []), E), (([P], [4], [2]), E), (([None], [4], [0]), E), (([P + 2], [4], [0]), A),
-    (([P + 1], [4], [1]), A), (([P], [2**60], [0]), S),
+    (([P + 1], [4], [1]), A), (([P], [2**60], [0]), S), (([P], [2**41], [1]), S),
     (([P], [4], [0], [None]), E), (([P], [4], [0], [P + 2]), A),
 ])
 def test_grad_list_refusals(lib, args, want):
