@@ -21,11 +21,13 @@
 //      that frequent ids cost no more than rare ones.  A group streams its
 //      window's rows of dout, eight in flight, and writes a row of the table
 //      whenever the id changes.  A sum that crosses windows leaves one partial
-//      per window; the group that arrives last adds them in window order.
+//      per window;
+//   3. a third launch joins those partials, a block per sum, in a fixed order.
 //
 // Every row of the table is written once, and the order of every addition is
 // fixed by the ids alone: the same bits in every run.  Bound by DRAM (V d fp32
 // written, n d read).
+#include <algorithm>
 #include <cstdio>
 
 #include "../../include/mg.h"
@@ -42,7 +44,7 @@ constexpr int kSortThreads = 256;
 constexpr int kSortItems = 16;                            // per thread
 constexpr int kSortTile = kSortThreads * kSortItems;      // 4096 keys per block
 constexpr int kWarps = kSortThreads / 32;
-constexpr int kSumThreads = 65536;  // threads that sum: windows of the sorted order times threads a row
+constexpr int kSumThreads = 152 * 2 * 256;  // threads that sum: windows of the sorted order times threads a row
 constexpr int kCluster = 4;         // CTAs that sort together
 constexpr int kSmallThreads = 1024;
 constexpr int kSmallItems = 16;     // ids per thread at most
@@ -318,12 +320,9 @@ __global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(KeysIn in, u
   }
 }
 
-// Segment bounds of every id that occurs, from the sorted keys; also clears the
-// arrival counters.
-__global__ void __launch_bounds__(256) sort_bounds_kernel(const uint32_t* key, uint32_t n, uint32_t V, uint2* seg,
-                                                          uint32_t* arrivals, uint32_t n_arrivals) {
+// Segment bounds of every id that occurs, from the sorted keys.
+__global__ void __launch_bounds__(256) sort_bounds_kernel(const uint32_t* key, uint32_t n, uint32_t V, uint2* seg) {
   const uint32_t i = blockIdx.x * 256u + threadIdx.x;
-  for (uint32_t a = i; a < n_arrivals; a += gridDim.x * 256u) arrivals[a] = 0;
   if (i >= n) return;
   const uint32_t k = key[i];
   if (k >= V) return;
@@ -357,8 +356,6 @@ struct SmallArgs {
   uint32_t* key;
   uint32_t* pos;
   uint2* seg;
-  uint32_t* arrivals;
-  uint32_t n_arrivals;
   float* dtable;
 };
 
@@ -429,7 +426,6 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSmallThreads
   constexpr uint32_t kChunk = kSmallThreads * IPT;
   const int bins = 1 << A.digit_bits;
   const uint32_t first = cta * kChunk + w * (32 * IPT) + lane;
-  for (uint32_t i = cta * kSmallThreads + tid; i < A.n_arrivals; i += kCluster * kSmallThreads) A.arrivals[i] = 0;
   uint32_t k[IPT], p[IPT], rank[IPT];
 #pragma unroll
   for (int j = 0; j < IPT; ++j) {
@@ -538,7 +534,6 @@ struct SumArgs {
   const uint32_t* key;
   const uint32_t* pos;
   float* part;            // [windows][2][d]
-  uint32_t* arrivals;     // [windows][column tiles]
   uint32_t n, V;
   int d;
   float scale;
@@ -675,9 +670,8 @@ struct Fetch<bf16, false> {
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256, 2) embed_sum_kernel(const SumArgs A) {
   using L = Fetch<T, VEC>;
-  constexpr int C = L::C, B = kBatch, kAhead = 2;
+  constexpr int C = L::C, B = kBatch;
   extern __shared__ __align__(16) uint4 ring[];
-  __shared__ int last[2][256];
   const int lane = threadIdx.x % A.tpr, sub = threadIdx.x / A.tpr, rpb = 256 / A.tpr;
   const uint32_t items = A.n_windows * (uint32_t)A.col_tiles;
   dependency_wait();
@@ -767,66 +761,110 @@ __global__ void __launch_bounds__(256, 2) embed_sum_kernel(const SumArgs A) {
         else flush();
       }
     }
-    // ---- sums that cross windows: slot 0 came from the left, slot 1 begins here
-    const bool has[2] = {left, right && !(left && klast == kfirst)};
-    if (!__syncthreads_or(has[0] || has[1])) continue;
-    __threadfence();
+  }
+}
+
+// The sums that cross windows, from their partials: slot 1 of the window in which
+// a segment begins, slot 0 of the later ones.  An id with a tenth of all
+// positions has a tenth of the windows' partials, so a block gives its 256
+// threads to one segment and 128 threads' columns at a time: each group of
+// threads adds a run of consecutive windows, and the runs are added in order.
+// (Joined by the last group to arrive in the kernel above, one by one, half of
+// 16384 positions under one id, 1024 columns, took 141 us for the whole
+// gradient, this way 60; of 1000003 in rows of 32, 2834 us and 244; frequencies
+// as in text, 16384 rows of 2048, 66 us and 69.)
+constexpr int kJoinCols = 128;  // threads a row at most
+constexpr int kJoinBlocks = 8;  // blocks per SM at most
+
+// Block (x, y): the windows x, x + gridDim.x, ...; the column tiles y, y + gridDim.y, ...
+template <int VEC>
+__global__ void __launch_bounds__(256) embed_join_kernel(const SumArgs A) {
+  constexpr int U = 8;                   // partials in flight a thread
+  __shared__ uint4 found[256];           // first window, windows, id
+  __shared__ uint32_t n_found;
+  __shared__ float red[256][VEC];
+  const int tid = threadIdx.x, lane = tid % A.tpr, grp = tid / A.tpr, groups = 256 / A.tpr;
+  dependency_wait();
+  for (uint32_t base = blockIdx.x; base < A.n_windows; base += 256 * gridDim.x) {
+    if (tid == 0) n_found = 0;
     __syncthreads();
-    if (lane == 0) {
-#pragma unroll
-      for (int slot = 0; slot < 2; ++slot) {
-        int l = 0;
-        if (has[slot]) {
-          const uint2 s = slot ? slast : sfirst;
-          const uint32_t w0 = s.x / A.window, w1 = (s.y - 1) / A.window;
-          l = atomicAdd(&A.arrivals[(size_t)w0 * A.col_tiles + tile], 1u) == w1 - w0;
-        }
-        last[slot][sub] = l;
+    const uint32_t win = base + tid * gridDim.x, we = (win + 1) * A.window;
+    if (win < A.n_windows && we < A.n) {
+      const uint32_t k = A.key[we - 1], next = A.key[we];
+      if (k < A.V && next == k) {
+        const uint2 s = A.seg[k];
+        if (s.y - s.x > A.window && s.x >= win * A.window)
+          found[atomicAdd(&n_found, 1u)] = make_uint4(win, (s.y - 1) / A.window - win + 1, k, 0);
       }
     }
     __syncthreads();
-    for (int slot = 0; slot < 2; ++slot) {
-      if (!last[slot][sub]) continue;
-      __threadfence();
-      const uint32_t k = slot ? klast : kfirst;
-      const uint2 s = slot ? slast : sfirst;
-      const uint32_t w0 = s.x / A.window, w1 = (s.y - 1) / A.window;
-      float acc[C];
+    const uint32_t n = n_found;
+    for (uint32_t j = 0; j < n; ++j) {
+      const uint32_t w0 = found[j].x, count = found[j].y;
+      const uint32_t run = (count + groups - 1) / groups, lo = grp * run, hi = min(count, lo + run);
+      for (int tile = blockIdx.y; tile < A.col_tiles; tile += gridDim.y) {
+        const int c = (tile * A.tpr + lane) * VEC;
+        float acc[VEC];
 #pragma unroll
-      for (int i = 0; i < C; ++i) acc[i] = 0.0f;
-      for (uint32_t w = w0; w <= w1; w += kAhead) {
-        float f[kAhead][C];
+        for (int i = 0; i < VEC; ++i) acc[i] = 0.0f;
+        if (c < A.d) {
+          const float* part = A.part + (size_t)w0 * 2 * A.d + c;
+#pragma unroll 1
+          for (uint32_t q = lo; q < hi; q += U) {
+            float f[U][VEC];
 #pragma unroll
-        for (int q = 0; q < kAhead; ++q)
-          if (w + q <= w1)
-            L::get(A.part + ((size_t)(w + q) * 2 + (w + q == w0 ? 1 : 0)) * A.d + c0, lane, d, A.tpr, f[q]);
+            for (int u = 0; u < U; ++u) {
+              if (q + u >= hi) continue;
+              const float* p = part + ((size_t)(q + u) * 2 + (q + u == 0)) * A.d;
+              if constexpr (VEC == 4) {
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(p));
+                f[u][0] = v.x; f[u][1] = v.y; f[u][2] = v.z; f[u][3] = v.w;
+              } else {
+                f[u][0] = __ldcg(p);
+              }
+            }
 #pragma unroll
-        for (int q = 0; q < kAhead; ++q) {
-          if (w + q > w1) continue;
+            for (int u = 0; u < U; ++u) {
+              if (q + u >= hi) continue;
 #pragma unroll
-          for (int i = 0; i < C; ++i) acc[i] += f[q][i];
+              for (int i = 0; i < VEC; ++i) acc[i] += f[u][i];
+            }
+          }
         }
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) red[tid][i] = acc[i];
+        __syncthreads();
+        if (grp == 0 && c < A.d) {
+          for (int q = 1; q < groups && q * run < count; ++q)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) acc[i] += red[q * A.tpr + lane][i];
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) acc[i] *= A.scale;
+          float* o = A.dtable + (size_t)found[j].z * A.d + c;
+          if constexpr (VEC == 4) store_vec<4>(o, acc);
+          else *o = acc[0];
+        }
+        __syncthreads();
       }
-      L::put(dtable + (size_t)k * A.d, lane, d, A.tpr, acc, A.scale, A.v32);
     }
-    __syncthreads();
+    __syncthreads();     // the list has been read
   }
 }
 
 // ---------------------------------------------------------------- workspace
 struct Ws {
-  size_t key[2], pos[2], seg, counts, arrivals, part, bytes;
+  size_t key[2], pos[2], seg, counts, part, bytes;
   uint32_t window, n_windows, sort_blocks;
-  int col_tiles, passes, digit_bits;
+  int passes, digit_bits;
 };
 
 Ws ws_layout(long long n, int V, int d) {
   Ws w = {};
-  w.col_tiles = (d + 1023) / 1024;    // at most: 256 threads of 4 columns or more
   // as many windows (of 8 entries at least) as give kSumThreads threads at 16
-  // columns each: 512 for rows of 2048, 8192 for rows of 128
+  // columns each: 608 for rows of 2048, 9728 for rows of 128.  Multiples of 4: a
+  // window's keys are read four at a time
   const long long windows = kSumThreads / threads_per_row((d + 15) / 16);
-  long long win = ((n + windows - 1) / windows + 7) / 8 * 8;
+  const long long win = ((n + windows - 1) / windows + 3) / 4 * 4;
   w.window = (uint32_t)(win > 8 ? win : 8);
   w.n_windows = (uint32_t)((n + w.window - 1) / w.window);
   w.sort_blocks = (uint32_t)((n + kSortTile - 1) / kSortTile);
@@ -847,7 +885,6 @@ Ws ws_layout(long long n, int V, int d) {
   }
   w.seg = take((size_t)V * 8);
   w.counts = take((size_t)kRadix * w.sort_blocks * 4);
-  w.arrivals = take((size_t)w.n_windows * w.col_tiles * 4);
   w.part = take((size_t)w.n_windows * 2 * d * 4);
   w.bytes = top;
   return w;
@@ -858,8 +895,9 @@ Ws ws_layout(long long n, int V, int d) {
 size_t embedding_ws_bytes(long long n, int V, int d) { return ws_layout(n, V, d).bytes; }
 
 int embedding_bwd_launches(long long n, int V, int d) {
-  if (n <= kSmallMax) return n > 0 ? 2 : 1;
-  return 3 * ws_layout(n, V, d).passes + 3;
+  if (n == 0) return 1;
+  const Ws w = ws_layout(n, V, d);
+  return (n <= kSmallMax ? 1 : 3 * w.passes + 2) + (w.n_windows > 1 ? 2 : 1);
 }
 
 cudaError_t embedding_fwd(DType tt, const void* table, int V, int d, int id64, const void* ids, long long n,
@@ -914,11 +952,10 @@ cudaError_t embedding_bwd_sort(int id64, const void* ids, long long n, int V, in
   char* base = static_cast<char*>(workspace);
   auto u32 = [&](size_t off) { return reinterpret_cast<uint32_t*>(base + off); };
   uint2* seg = reinterpret_cast<uint2*>(base + w.seg);
-  const uint32_t n_arrivals = w.n_windows * (uint32_t)w.col_tiles;
   KeysIn in{ids, id64, V, nullptr, nullptr};
   if (n <= kSmallMax) {
     SmallArgs A{in, (uint32_t)n, (uint32_t)V, d, w.digit_bits, w.passes, u32(w.key[0]), u32(w.pos[0]), seg,
-                u32(w.arrivals), n_arrivals, dtable};
+                dtable};
     const long long per_cluster = kCluster * kSmallThreads;
     if (n <= per_cluster) return sort_small<1>(A, s);
     if (n <= 2 * per_cluster) return sort_small<2>(A, s);
@@ -937,8 +974,7 @@ cudaError_t embedding_bwd_sort(int id64, const void* ids, long long n, int V, in
     in.key = u32(w.key[dst]);
     in.pos = u32(w.pos[dst]);
   }
-  sort_bounds_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(u32(w.key[0]), (uint32_t)n, (uint32_t)V, seg,
-                                                                 u32(w.arrivals), n_arrivals);
+  sort_bounds_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(u32(w.key[0]), (uint32_t)n, (uint32_t)V, seg);
   const long long zblocks = ((long long)V + 7) / 8;
   zero_rows_kernel<<<(unsigned)(zblocks < 152 * 8 ? zblocks : 152 * 8), 256, 0, s>>>(seg, (uint32_t)V, d, dtable);
   return cudaGetLastError();
@@ -965,7 +1001,6 @@ cudaError_t embedding_bwd_sum(DType t, const void* dout, long long n, int V, int
   A.key = reinterpret_cast<uint32_t*>(base + w.key[0]);
   A.pos = reinterpret_cast<uint32_t*>(base + w.pos[0]);
   A.part = reinterpret_cast<float*>(base + w.part);
-  A.arrivals = reinterpret_cast<uint32_t*>(base + w.arrivals);
   A.n = (uint32_t)n;
   A.V = (uint32_t)V;
   A.d = d;
@@ -981,8 +1016,17 @@ cudaError_t embedding_bwd_sum(DType t, const void* dout, long long n, int V, int
   const long long blocks = ((long long)w.n_windows * A.col_tiles + rpb - 1) / rpb;
   const unsigned grid = (unsigned)(blocks < 152 * 16 ? blocks : 152 * 16);
   const bool vec = d % 8 == 0;
-  if (t == DT_F32) return vec ? sum_launch<float, true>(A, grid, s) : sum_launch<float, false>(A, grid, s);
-  return vec ? sum_launch<bf16, true>(A, grid, s) : sum_launch<bf16, false>(A, grid, s);
+  cudaError_t e;
+  if (t == DT_F32) e = vec ? sum_launch<float, true>(A, grid, s) : sum_launch<float, false>(A, grid, s);
+  else e = vec ? sum_launch<bf16, true>(A, grid, s) : sum_launch<bf16, false>(A, grid, s);
+  if (e != cudaSuccess || w.n_windows == 1) return e;
+  const int cols = d % 4 == 0 ? d / 4 : d;
+  A.tpr = std::min(threads_per_row(cols), kJoinCols);
+  A.col_tiles = (cols + A.tpr - 1) / A.tpr;
+  const unsigned ty = (unsigned)std::min(A.col_tiles, 152);
+  const dim3 join_grid(std::min(w.n_windows, std::max(1u, 152 * kJoinBlocks / ty)), ty);
+  return d % 4 == 0 ? launch_dependent(embed_join_kernel<4>, join_grid, 256, 0, s, A)
+                    : launch_dependent(embed_join_kernel<1>, join_grid, 256, 0, s, A);
 }
 
 }  // namespace mg

@@ -29,10 +29,10 @@ mg_status op_end(const char* fn, cudaError_t e);
 
 // Launch kern as a programmatic dependent of the kernel before it on s.
 template <typename... P, typename... A>
-cudaError_t launch_dependent(void (*kern)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t s,
+cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, unsigned block, size_t smem, cudaStream_t s,
                              A... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;

@@ -112,7 +112,7 @@ def _bwd_check(dout, ids, v, scale, got):
 @pytest.mark.parametrize("n,v,d,hot", [
     (0, 5, 8, 0.0), (1, 1, 1, 0.0), (1, 70000, 16, 0.0), (33, 7, 24, 0.0), (257, 1000, 777, 0.0),
     (5000, 50, 33, 0.3), (4096, 3, 128, 0.0), (4097, 600, 2056, 0.4), (20000, 300000, 8, 0.2),
-    (129, 2, 64, 1.0), (128, 2, 64, 1.0), (70001, 513, 40, 0.5)])
+    (129, 2, 64, 1.0), (128, 2, 64, 1.0), (70001, 513, 40, 0.5), (30000, 40, 1030, 0.6)])
 @pytest.mark.parametrize("t,kind", [("f32", "i32"), ("bf16", "i64")])
 def test_backward(n, v, d, hot, t, kind):
     dout = _randn((n, d), t, 3)
