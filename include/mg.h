@@ -370,8 +370,8 @@ mg_status mg_softmax_ce_noalloc(int dtype, const void* logits, int rows, int col
  * dout[i, :], fp32 sums in ascending i order (long runs in a fixed order of
  * fixed windows), the same bits in every run.  All of dtable [vocab, dim]
  * fp32 is written, zeros for ids that do not occur; ids outside [0, vocab)
- * give nothing.  workspace: mg_embedding_workspace_bytes (0 for arguments the
- * call would refuse); its contents before the call do not matter. */
+ * give nothing.  workspace: mg_embedding_workspace_bytes (for n ids or fewer; 0 for
+ * arguments the call would refuse); its contents before the call do not matter. */
 size_t mg_embedding_workspace_bytes(long long n, int vocab, int dim);
 mg_status mg_embedding_forward(int table_dtype, const void* table, int vocab, int dim, int id_kind,
                                const void* ids, long long n, float scale, int out_dtype, void* out,
@@ -394,8 +394,8 @@ mg_status mg_embedding_backward(int dtype, const void* dout, int vocab, int dim,
  * the tensor cores (rows of widths that are no multiples of 8 are copied to
  * aligned ones in the workspace first; small products of such widths, and fp32,
  * run on the CUDA cores).
- * workspace: mg_grouped_linear_workspace_bytes; zero it once before its first
- * use.  Its first int is set to 1 if a bounded device-side wait gave up, in
+ * workspace: mg_grouped_linear_workspace_bytes (for these rows or fewer); zero it
+ * once before its first use.  Its first int is set to 1 if a bounded device-side wait gave up, in
  * which case that call's results are invalid. */
 size_t mg_grouped_linear_workspace_bytes(int rows, int groups, int d_in, int d_out);
 mg_status mg_grouped_linear_forward(int dtype, const void* x, const int* offsets, int rows, int groups,

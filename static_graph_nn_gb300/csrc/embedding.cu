@@ -885,7 +885,7 @@ Ws ws_layout(long long n, int V, int d) {
   }
   w.seg = take((size_t)V * 8);
   w.counts = take((size_t)kRadix * w.sort_blocks * 4);
-  w.part = take((size_t)w.n_windows * 2 * d * 4);
+  w.part = take((size_t)std::min(windows, (n + 7) / 8) * 2 * d * 4);   // at most, so that no smaller n needs more
   w.bytes = top;
   return w;
 }

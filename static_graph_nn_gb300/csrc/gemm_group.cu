@@ -271,12 +271,18 @@ cudaError_t join_launch(const GroupArgs& g, int splits, long long rows, int N, c
 
 }  // namespace
 
+// For these rows or fewer: in the forward and dX, s <= kSplitBlocks / tiles parts
+// of at most S_T tiles / tiles_n rows; dW's parts grow with the rows.
 size_t grouped_simt_split_bytes(int rows, int groups, int d_in, int d_out) {
   size_t most = 0;
   for (int kind : {GROUP_FWD, GROUP_DX, GROUP_DW}) {
-    const int s = simt_splits(kind, rows, groups, d_in, d_out);
+    const bool dw = kind == GROUP_DW;
+    const int s = simt_splits(kind, dw ? rows : std::min(rows, 1), groups, d_in, d_out);   // the most of any rows
     const int N = kind == GROUP_DX ? d_in : d_out;
-    if (s > 1) most = std::max<size_t>(most, (size_t)s * group_out_rows(kind, rows, groups, d_in) * N * 4);
+    if (s < 2) continue;
+    const long long part_rows = dw ? (long long)s * groups * d_in
+                                   : std::min((long long)s * rows, kSplitBlocks * S_T / ((N + S_T - 1) / S_T));
+    most = std::max<size_t>(most, (size_t)part_rows * N * 4);
   }
   return most;
 }

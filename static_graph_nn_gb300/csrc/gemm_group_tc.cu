@@ -579,10 +579,19 @@ int group_splits(int kind, int rows, int groups, int d_in, int d_out) {
   return s < 2 ? 1 : (int)s;
 }
 
+// Their bytes for these rows or fewer (forward, dX: s <= 76 / tiles parts of at
+// most 256 tiles / tiles_n rows; dW's parts grow with the rows).
 size_t split_bytes(int kind, int rows, int groups, int d_in, int d_out) {
-  const int s = group_splits(kind, rows, groups, d_in, d_out);
   const int N = kind == GROUP_DX ? d_in : d_out;
-  return s < 2 ? 0 : (size_t)s * group_out_rows(kind, rows, groups, d_in) * N * 4;
+  long long part_rows;
+  if (kind == GROUP_DW) {
+    const int s = group_splits(kind, rows, groups, d_in, d_out);
+    part_rows = s < 2 ? 0 : (long long)s * groups * d_in;
+  } else {
+    const int least = group_splits(kind, std::min(rows, 1), groups, d_in, d_out);   // the most parts of any rows
+    part_rows = least < 2 ? 0 : std::min((long long)least * rows, 76ll * 2 * G_BM / ((N + G_BN - 1) / G_BN));
+  }
+  return (size_t)part_rows * N * 4;
 }
 
 template <int KIND, typename TO, bool ANY>

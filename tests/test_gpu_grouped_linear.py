@@ -101,6 +101,17 @@ def test_products(rows, e, k, n, t):
 
 
 @pytest.mark.parametrize("t", ["bf16", "f32"])
+def test_one_workspace_for_fewer_rows(t):
+    """A workspace of the size for many rows, filled to its end by earlier calls,
+    serves calls of fewer (which split more)."""
+    e, k, n = 2, 1032, 1003
+    ws = torch.zeros(mg.grouped_linear_workspace_bytes(3001, e, k, n), dtype=torch.uint8, device="cuda")
+    for rows in (3001, 700, 130, 17, 1):
+        x, dy, w, _ = _data(rows, e, k, n, t)
+        _check_all(_offsets(rows, e, rows), rows, e, k, n, t, x, dy, w, ws)
+
+
+@pytest.mark.parametrize("t", ["bf16", "f32"])
 @pytest.mark.parametrize("rows,e,k,n", [(300, 4, 136, 264), (40, 6, 256, 512), (65, 2, 72, 40), (9, 3, 33, 17),
                                           (300, 2, 1032, 136), (4000, 3, 72, 264), (900, 3, 601, 1003),
                                           (25, 4, 1501, 999)])

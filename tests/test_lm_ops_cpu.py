@@ -61,6 +61,17 @@ def test_workspace_sizes(lib):
     assert lib.mg_grouped_linear_workspace_bytes(0, 1, 8, 8) >= 4
 
 
+@pytest.mark.parametrize("groups,k,n", [(1, 8, 8), (1, 1224, 3148), (8, 2048, 8192), (3, 601, 1003), (64, 4096, 64),
+                                        (2, 64, 16384)])
+def test_a_workspace_serves_fewer_rows(lib, groups, k, n):
+    sizes = [lib.mg_grouped_linear_workspace_bytes(r, groups, k, n)
+             for r in (0, 1, 2, 17, 64, 100, 111, 257, 300, 1000, 4099, 9000, 40000)]
+    assert sizes == sorted(sizes) and sizes[0] > 0
+    sizes = [lib.mg_embedding_workspace_bytes(r, n, k)
+             for r in (0, 1, 8, 100, 2432, 4863, 4864, 4865, 9000, 16384, 65536, 65537, 200000)]
+    assert sizes == sorted(sizes) and sizes[0] > 0
+
+
 @pytest.mark.parametrize("sizes", [(2**30 + 1, 2, 8, 8), (4, 2, 2**30 + 1, 8), (4, 2, 8, 2**31 - 1)])
 def test_sizes_beyond_an_int_of_tiles_are_refused(lib, sizes):
     rows, groups, k, n = sizes
