@@ -12,8 +12,8 @@
 // every touched row, and would change results from run to run.  Instead:
 //
 //   1. the positions are sorted by id with a stable counting sort (positions of
-//      one id stay ascending).  Up to 65536 ids one cluster of four CTAs sorts
-//      them in shared memory, exchanging counts and elements through DSMEM;
+//      one id stay ascending).  Up to 65536 ids one cluster of four or eight CTAs
+//      sorts them in shared memory, exchanging counts and elements through DSMEM;
 //      meanwhile the other CTAs of the launch write the zero rows, each
 //      finding the ids of its own range of rows with one scan of the ids, so
 //      the sort's latency hides under bandwidth-bound stores;
@@ -45,10 +45,8 @@ constexpr int kSortItems = 16;                            // per thread
 constexpr int kSortTile = kSortThreads * kSortItems;      // 4096 keys per block
 constexpr int kWarps = kSortThreads / 32;
 constexpr int kSumThreads = 152 * 2 * 256;  // threads that sum: windows of the sorted order times threads a row
-constexpr int kCluster = 4;         // CTAs that sort together
 constexpr int kSmallThreads = 1024;
-constexpr int kSmallItems = 16;     // ids per thread at most
-constexpr long long kSmallMax = (long long)kCluster * kSmallThreads * kSmallItems;
+constexpr long long kSmallMax = 64 * kSmallThreads;   // ids that a cluster sorts
 constexpr int kZeroRange = 65536;   // rows whose presence one block holds as bits
 
 // ---------------------------------------------------------------- forward
@@ -255,7 +253,7 @@ __global__ void __launch_bounds__(1024) sort_scan_kernel(uint32_t* counts, uint3
 }
 
 // The lanes with ok and this lane's digit, bit by bit: by __match_any_sync the
-// sort of 32768 ids took 58 us, this way 42; a whole gradient of 1000003 ids in
+// sort of 32768 ids by four CTAs took 58 us, this way 42; a whole gradient of 1000003 ids in
 // rows of 32 took 213 us and 208.
 __device__ __forceinline__ uint32_t same_digit(bool ok, uint32_t dg, int bits) {
   uint32_t same = __ballot_sync(0xffffffffu, ok);
@@ -387,16 +385,16 @@ struct SmallSmem {
   uint32_t wsum[32];
 };
 
-template <int IPT>
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSmallThreads, 1)
+template <int IPT, int CL>
+__global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kSmallThreads, 1)
     sort_small_kernel(const SmallArgs A) {
   extern __shared__ __align__(16) uint8_t raw[];
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   dependents_start();
-  if (blockIdx.x >= kCluster) {
+  if (blockIdx.x >= CL) {
     // ---- zero rows of a contiguous range of the table
     uint32_t* bits = reinterpret_cast<uint32_t*>(raw);
-    const uint32_t nz = gridDim.x - kCluster, z = blockIdx.x - kCluster;
+    const uint32_t nz = gridDim.x - CL, z = blockIdx.x - CL;
     const uint32_t lo = (uint32_t)((unsigned long long)A.V * z / nz);
     const uint32_t hi = (uint32_t)((unsigned long long)A.V * (z + 1) / nz);
     for (uint32_t r0 = lo; r0 < hi; r0 += kZeroRange) {
@@ -465,7 +463,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSmallThreads
     uint32_t all = 0, before = 0;
     if (tid < bins) {
 #pragma unroll
-      for (uint32_t c = 0; c < kCluster; ++c) {
+      for (uint32_t c = 0; c < CL; ++c) {
         const uint32_t t = ld_cluster(cluster_addr(&S.tot[tid], c));
         if (c < cta) before += t;
         all += t;
@@ -602,19 +600,6 @@ struct Fetch {   // VEC
       }
     }
   }
-  static __device__ __forceinline__ void get(const float* row, int lane, int d, int tpr, float* f) {
-#pragma unroll
-    for (int i = 0; i < NCH; ++i) {
-      const int c = (lane + i * tpr) * E;
-      if (c < d) {
-#pragma unroll
-        for (int q = 0; q < E / 4; ++q) {
-          const float4 v = __ldcg(reinterpret_cast<const float4*>(row + c) + q);
-          f[i * E + 4 * q] = v.x; f[i * E + 4 * q + 1] = v.y; f[i * E + 4 * q + 2] = v.z; f[i * E + 4 * q + 3] = v.w;
-        }
-      }
-    }
-  }
 };
 template <>
 struct Fetch<float, false> {   // 4-byte copies, 8 columns
@@ -637,11 +622,6 @@ struct Fetch<float, false> {   // 4-byte copies, 8 columns
     for (int i = 0; i < C; ++i)
       if (lane + i * tpr < d) row[lane + i * tpr] = f[i] * scale;
   }
-  static __device__ __forceinline__ void get(const float* row, int lane, int d, int tpr, float* f) {
-#pragma unroll
-    for (int i = 0; i < C; ++i)
-      if (lane + i * tpr < d) f[i] = __ldcg(row + lane + i * tpr);
-  }
 };
 template <>
 struct Fetch<bf16, false> {
@@ -659,11 +639,6 @@ struct Fetch<bf16, false> {
 #pragma unroll
     for (int i = 0; i < C; ++i)
       if (lane + i * tpr < d) row[lane + i * tpr] = f[i] * scale;
-  }
-  static __device__ __forceinline__ void get(const float* row, int lane, int d, int tpr, float* f) {
-#pragma unroll
-    for (int i = 0; i < C; ++i)
-      if (lane + i * tpr < d) f[i] = __ldcg(row + lane + i * tpr);
   }
 };
 
@@ -913,36 +888,36 @@ cudaError_t embedding_fwd(DType tt, const void* table, int V, int d, int id64, c
 #undef MG_EMBED_FWD
 }
 
-template <int IPT>
+template <int IPT, int CL>
 static cudaError_t sort_small(const SmallArgs& A, cudaStream_t s) {
   constexpr size_t smem = sizeof(SmallSmem<IPT>) > kZeroRange / 8 ? sizeof(SmallSmem<IPT>) : kZeroRange / 8;
   const cudaError_t attr =    // of this device's context: set in every call
-      cudaFuncSetAttribute(sort_small_kernel<IPT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      cudaFuncSetAttribute(sort_small_kernel<IPT, CL>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (attr != cudaSuccess) return attr;
   // clusters that run at once (a cluster's CTAs share a GPC, so some SMs may
   // stay out): a later one would start when the first zeroing ones end
   static const int slots = [&] {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(kCluster * (device_sms() / kCluster));
+    cfg.gridDim = dim3(CL * (device_sms() / CL));
     cfg.blockDim = dim3(kSmallThreads);
     cfg.dynamicSmemBytes = smem;
     cudaLaunchAttribute at;
     at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = kCluster;
+    at.val.clusterDim.x = CL;
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
     int c = 0;
-    if (cudaOccupancyMaxActiveClusters(&c, sort_small_kernel<IPT>, &cfg) != cudaSuccess || c < 2) {
+    if (cudaOccupancyMaxActiveClusters(&c, sort_small_kernel<IPT, CL>, &cfg) != cudaSuccess || c < 2) {
       cudaGetLastError();
       c = 2;
     }
     return c;
   }();
   // a block's rows are worth its scan of the ids only if they are many
-  const long long most = slots - 1, rows = (long long)A.V * A.d / (kCluster * 65536);
-  const unsigned grid = kCluster + kCluster * (unsigned)(rows < 1 ? 1 : rows < most ? rows : most);
-  sort_small_kernel<IPT><<<grid, kSmallThreads, smem, s>>>(A);
+  const long long most = slots - 1, rows = (long long)A.V * A.d / (CL * 65536);
+  const unsigned grid = CL + CL * (unsigned)(rows < 1 ? 1 : rows < most ? rows : most);
+  sort_small_kernel<IPT, CL><<<grid, kSmallThreads, smem, s>>>(A);
   return cudaGetLastError();
 }
 
@@ -956,11 +931,20 @@ cudaError_t embedding_bwd_sort(int id64, const void* ids, long long n, int V, in
   if (n <= kSmallMax) {
     SmallArgs A{in, (uint32_t)n, (uint32_t)V, d, w.digit_bits, w.passes, u32(w.key[0]), u32(w.pos[0]), seg,
                 dtable};
-    const long long per_cluster = kCluster * kSmallThreads;
-    if (n <= per_cluster) return sort_small<1>(A, s);
-    if (n <= 2 * per_cluster) return sort_small<2>(A, s);
-    if (n <= 4 * per_cluster) return sort_small<4>(A, s);
-    return sort_small<kSmallItems>(A, s);
+    // Eight CTAs sort faster than four, but fewer clusters of eight run at once (15
+    // of 19: 112 CTAs write the zero rows instead of 140), so up to 16384 ids four
+    // sort where the zeros take longer than the sort.  us, by eight and by four:
+    // 32768 ids x 2048, vocabulary 32000, 89 and 117; x 64, 37 and 71; 16384 ids x
+    // 2048, 73 and 70; x 768, 36 and 43; 5000 ids x 768, 33 and 31; x 256, 23 and 25.
+    if (n > 16 * kSmallThreads || (n > 4 * kSmallThreads && (long long)V * d <= 2048 * n)) {
+      if (n <= 8 * kSmallThreads) return sort_small<1, 8>(A, s);
+      if (n <= 16 * kSmallThreads) return sort_small<2, 8>(A, s);
+      if (n <= 32 * kSmallThreads) return sort_small<4, 8>(A, s);
+      return sort_small<8, 8>(A, s);
+    }
+    if (n <= 4 * kSmallThreads) return sort_small<1, 4>(A, s);
+    if (n <= 8 * kSmallThreads) return sort_small<2, 4>(A, s);
+    return sort_small<4, 4>(A, s);
   }
   cudaError_t e = cudaMemsetAsync(seg, 0, (size_t)V * sizeof(uint2), s);
   if (e != cudaSuccess) return e;
