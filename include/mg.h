@@ -62,7 +62,8 @@ typedef enum {
                                  an id outside [0, d_in) (padding): a row of zeros and no gradient */
   MG_OP_GROUPED_LINEAR = 8    /* Y[r] = X[r] W[e(r)], W[n_heads, d_in, d_out], the rows of group e given by
                                  mg_set_row_groups; rows of no group: zeros.  Activations and residual ends
-                                 follow it as they follow LINEAR; no bias */
+                                 follow it as they follow LINEAR; no bias.  Strict forward sums are
+                                 compensated, as LINEAR's */
 } mg_op;
 
 typedef enum { MG_LOSS_CE_DENSE = 0, MG_LOSS_CE_INDEX = 1, MG_LOSS_MSE = 2 } mg_loss_kind;

@@ -150,6 +150,17 @@ __device__ __forceinline__ void ld16bf(const bf16* p, float* f) {
   }
 }
 
+// s + c += a*b with the rounding errors of the product and the sum kept in c.
+__device__ __forceinline__ void dot2_step(float a, float b, float& s, float& c) {
+  float p = __fmul_rn(a, b);
+  float pe = __fmaf_rn(a, b, -p);            // a*b - p exactly
+  float t = __fadd_rn(s, p);
+  float z = __fsub_rn(t, s);
+  float se = __fadd_rn(__fsub_rn(s, __fsub_rn(t, z)), __fsub_rn(p, z));   // s + p - t exactly
+  s = t;
+  c = __fadd_rn(c, __fadd_rn(pe, se));
+}
+
 // Programmatic dependent launch.  A kernel launched as the dependent of the one
 // before it may start while that one still runs; everything it does before
 // dependency_wait must not touch what the earlier kernel writes.  The earlier

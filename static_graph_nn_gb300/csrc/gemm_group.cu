@@ -22,6 +22,11 @@
 // TFLOP/s); 8x8 outputs with 64 threads a tile read less but leave too few warps
 // (161).
 //
+// A strict plan's forward carries the rounding errors of its sums, as the dense
+// strict forward does (gemm_simt.cu): a ReLU behind it decides on the sign of
+// the exact pre-activation.  The same tiles with 256 threads of 4x4 outputs; ten
+// operations a product: 4096 rows x 16 x 1001x517 in 975 us, 123 plain.
+//
 // Where the tiles are fewer than half the resident blocks, each one's sum is
 // split over several blocks through the workspace and joined in order by a
 // second launch: 111 rows x 3148x1224, one group, dX in fp32: 126 us whole, 39 so.
@@ -42,7 +47,10 @@ constexpr int S_T = 64;        // output tile
 constexpr int S_K = 16;
 constexpr int S_LD = S_T + 4;  // 16-byte aligned rows, transposed writes spread over the banks
 constexpr int S_STAGES = 3;
-constexpr int S_THREADS = 128;
+// Threads of a block and resident blocks per SM: 8x4 outputs a thread, or 4x4
+// whose sums carry their errors (4096 rows x 16 x 1001x517: 975 us; 8x4 of those at 12 warps an SM 1370).
+constexpr int simt_threads(bool comp) { return comp ? 256 : 128; }
+constexpr int simt_per_sm(bool comp) { return comp ? 3 : 4; }
 
 struct SimtStage {
   float a[S_K][S_LD], b[S_K][S_LD];
@@ -50,16 +58,16 @@ struct SimtStage {
 
 // Fetch a K step of one operand into s[k][i]: element (i, k) is src[i * ld + k]
 // (K_MAJOR) or src[k * ld + i]; zeros at i >= ni or k >= nk.
-template <bool K_MAJOR, bool FULL>
+template <int NT, bool K_MAJOR, bool FULL>
 __device__ __forceinline__ void simt_copy(float (&s)[S_K][S_LD], const float* src, long long ld, int ni, int nk) {
   // K_MAJOR: 8 k x 4 i per warp, whose transposed writes meet 32 banks
   const int k0 = K_MAJOR ? threadIdx.x % 8 : threadIdx.x / S_T;
   const int i0 = K_MAJOR ? threadIdx.x / 8 : threadIdx.x % S_T;
-  constexpr int DI = S_THREADS / 8, DK = S_THREADS / S_T;   // steps of i (K_MAJOR) and of k
+  constexpr int DI = NT / 8, DK = NT / S_T;   // steps of i (K_MAJOR) and of k
   const float* p = src + (K_MAJOR ? i0 * ld + k0 : k0 * ld + i0);
   const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(&s[k0][i0]));
 #pragma unroll
-  for (int q = 0; q < S_T * S_K / S_THREADS; ++q) {
+  for (int q = 0; q < S_T * S_K / NT; ++q) {
     constexpr int HALF = S_T / DI;                          // K_MAJOR: copies per 8 k
     const int dk = K_MAJOR ? q / HALF * 8 : q * DK, di = K_MAJOR ? q % HALF * DI : 0;
     const bool ok = FULL || (i0 + di < ni && k0 + dk < nk);
@@ -70,16 +78,16 @@ __device__ __forceinline__ void simt_copy(float (&s)[S_K][S_LD], const float* sr
                  : "memory");
   }
 }
-template <bool K_MAJOR>
+template <int NT, bool K_MAJOR>
 __device__ __forceinline__ void simt_fetch(float (&s)[S_K][S_LD], const float* src, long long ld, int ni, int nk) {
-  if (ni >= S_T && nk >= S_K) simt_copy<K_MAJOR, true>(s, src, ld, ni, nk);
-  else simt_copy<K_MAJOR, false>(s, src, ld, ni, nk);
+  if (ni >= S_T && nk >= S_K) simt_copy<NT, K_MAJOR, true>(s, src, ld, ni, nk);
+  else simt_copy<NT, K_MAJOR, false>(s, src, ld, ni, nk);
 }
-template <bool K_MAJOR>
+template <int NT, bool K_MAJOR>
 __device__ __forceinline__ void simt_fetch(float (&s)[S_K][S_LD], const bf16* src, long long ld, int ni, int nk) {
 #pragma unroll
-  for (int q = 0; q < S_T * S_K / S_THREADS; ++q) {
-    const int j = threadIdx.x + q * S_THREADS;
+  for (int q = 0; q < S_T * S_K / NT; ++q) {
+    const int j = threadIdx.x + q * NT;
     const int k = K_MAJOR ? j % S_K : j / S_T, i = K_MAJOR ? j / S_K : j % S_T;
     s[k][i] = i < ni && k < nk ? __bfloat162float(K_MAJOR ? src[i * ld + k] : src[k * ld + i]) : 0.0f;
   }
@@ -93,10 +101,18 @@ __device__ __forceinline__ void fma2(uint64_t& c, uint64_t a, uint64_t b) {
   asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(a), "l"(b));
 }
 
+// The value of a compensated sum.  Where the sum itself has left the finite
+// range its error term is no number, and the sum is the answer.
+__device__ __forceinline__ float dot2_value(float s, float c) { return s - s == 0.0f ? __fadd_rn(s, c) : s; }
+
 // splits > 1: part s of every tile's sum goes, as it is, to rows s * out_rows ..
-// of g.ws.
-template <typename T, int KIND>
-__global__ void __launch_bounds__(S_THREADS, 4) group_simt_kernel(const GroupArgs g, int splits, long long out_rows) {
+// of g.ws.  COMP: sums that carry their rounding errors (dot2_step: ten
+// operations a product instead of one; two values a part in g.ws, the sums and
+// their errors).
+template <typename T, int KIND, bool COMP>
+__global__ void __launch_bounds__(simt_threads(COMP), simt_per_sm(COMP))
+    group_simt_kernel(const GroupArgs g, int splits, long long out_rows) {
+  constexpr int NT = simt_threads(COMP), RI = S_T * S_T / NT / 4;   // RI x 4 outputs a thread
   extern __shared__ int s_tab[];
   __shared__ __align__(16) SimtStage st[S_STAGES];
   GroupTable t;
@@ -114,7 +130,7 @@ __global__ void __launch_bounds__(S_THREADS, 4) group_simt_kernel(const GroupArg
                                                      : (long long)t.cum[t.n - 1] * tiles_n);
   const T* A = static_cast<const T*>(g.A);
   const T* B = static_cast<const T*>(g.B);
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;   // rows ty*4.. and 32+ty*4.., columns tx*4..
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;   // rows ty*4.. (and 32+ty*4..), columns tx*4..
   int e = 0;
   for (long long item = blockIdx.x; item < items; item += gridDim.x) {
     const int part = (int)(item % splits);
@@ -142,17 +158,18 @@ __global__ void __launch_bounds__(S_THREADS, 4) group_simt_kernel(const GroupArg
       SimtStage& q = st[k0 / S_K % S_STAGES];
       if (k0 < K) {
         if (KIND == GROUP_DW) {
-          simt_fetch<false>(q.a, A + (size_t)(krow0 + k0) * g.d_in + m0, g.d_in, m_end - m0, K - k0);
-          simt_fetch<false>(q.b, B + (size_t)(krow0 + k0) * g.d_out + n0, g.d_out, N - n0, K - k0);
+          simt_fetch<NT, false>(q.a, A + (size_t)(krow0 + k0) * g.d_in + m0, g.d_in, m_end - m0, K - k0);
+          simt_fetch<NT, false>(q.b, B + (size_t)(krow0 + k0) * g.d_out + n0, g.d_out, N - n0, K - k0);
         } else {
-          simt_fetch<true>(q.a, A + (size_t)m0 * K0 + k0, K0, m_end - m0, K - k0);
-          if (KIND == GROUP_FWD) simt_fetch<false>(q.b, W + (size_t)k0 * g.d_out + n0, g.d_out, N - n0, K - k0);
-          else simt_fetch<true>(q.b, W + (size_t)n0 * g.d_out + k0, g.d_out, N - n0, K - k0);
+          simt_fetch<NT, true>(q.a, A + (size_t)m0 * K0 + k0, K0, m_end - m0, K - k0);
+          if (KIND == GROUP_FWD) simt_fetch<NT, false>(q.b, W + (size_t)k0 * g.d_out + n0, g.d_out, N - n0, K - k0);
+          else simt_fetch<NT, true>(q.b, W + (size_t)n0 * g.d_out + k0, g.d_out, N - n0, K - k0);
         }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
     uint64_t acc2[4][4] = {};              // the thread's rows 2i and 2i + 1, column j
+    float hi[4][4] = {}, lo[4][4] = {};    // COMP: sums and their errors
     __syncthreads();                       // the previous tile's last step has been read
     fetch(k_lo);
     fetch(k_lo + S_K);
@@ -164,29 +181,43 @@ __global__ void __launch_bounds__(S_THREADS, 4) group_simt_kernel(const GroupArg
 #pragma unroll
       for (int k = 0; k < S_K; ++k) {
         const float4 a0 = *reinterpret_cast<const float4*>(&q.a[k][ty * 4]);
-        const float4 a1 = *reinterpret_cast<const float4*>(&q.a[k][32 + ty * 4]);
         const float4 b0 = *reinterpret_cast<const float4*>(&q.b[k][tx * 4]);
-        const uint64_t a[4] = {pack2(a0.x, a0.y), pack2(a0.z, a0.w), pack2(a1.x, a1.y), pack2(a1.z, a1.w)};
         const float b[4] = {b0.x, b0.y, b0.z, b0.w};
+        if constexpr (COMP) {
+          const float a[4] = {a0.x, a0.y, a0.z, a0.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint64_t bb = pack2(b[j], b[j]);
+          for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) fma2(acc2[i][j], a[i], bb);
+            for (int j = 0; j < 4; ++j) dot2_step(a[i], b[j], hi[i][j], lo[i][j]);
+        } else {
+          const float4 a1 = *reinterpret_cast<const float4*>(&q.a[k][32 + ty * 4]);
+          const uint64_t a[4] = {pack2(a0.x, a0.y), pack2(a0.z, a0.w), pack2(a1.x, a1.y), pack2(a1.z, a1.w)};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint64_t bb = pack2(b[j], b[j]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) fma2(acc2[i][j], a[i], bb);
+          }
         }
       }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < RI; ++i) {
       const int m = m0 + (i & 4) * 8 + ty * 4 + (i & 3);
       if (m >= m_end) continue;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int n = n0 + tx * 4 + j;
         if (n >= N) continue;
-        float x = __uint_as_float((uint32_t)(acc2[i / 2][j] >> (i % 2 * 32)));
         const size_t o = (size_t)((KIND == GROUP_DW ? (long long)e * g.d_in : 0) + m) * N + n;
+        float x;
+        if constexpr (COMP) {
+          if (splits > 1) g.ws[(size_t)(splits + part) * out_rows * N + o] = lo[i][j];
+          x = splits > 1 ? hi[i][j] : dot2_value(hi[i][j], lo[i][j]);
+        } else {
+          x = __uint_as_float((uint32_t)(acc2[i / 2][j] >> (i % 2 * 32)));
+        }
         if (splits > 1) g.ws[(size_t)part * out_rows * N + o] = x;
         else if (KIND == GROUP_DW) static_cast<float*>(g.out)[o] = x;
         else group_epilogue<T>(g, o, x);
@@ -213,18 +244,18 @@ int simt_splits(int kind, int rows, int groups, int d_in, int d_out) {
   return s < 2 ? 1 : (int)s;
 }
 
-template <typename T, int KIND>
+template <typename T, int KIND, bool COMP = false>
 cudaError_t simt_launch(const GroupArgs& given, cudaStream_t s) {
   GroupArgs g = given;
   const int splits = g.ws ? simt_splits(KIND, g.rows, g.groups, g.d_in, g.d_out) : 1;
   if (splits > 1) g.zero_rest = 0;       // those rows are the join's
   const long long items = splits * (simt_tiles(KIND, g.rows, g.groups, g.d_in, g.d_out) +
                                     (g.zero_rest ? 2 : 0) * ((KIND == GROUP_DX ? g.d_in : g.d_out) / S_T + 1));
-  const int slots = 4 * device_sms();
+  const int slots = simt_per_sm(COMP) * device_sms();
   const int grid = (int)(items < slots ? items : slots);
   const size_t smem = (size_t)kGroupTableInts(g.groups) * sizeof(int);
   const long long out_rows = group_out_rows(KIND, g.rows, g.groups, g.d_in);
-  group_simt_kernel<T, KIND><<<grid, S_THREADS, smem, s>>>(g, splits, out_rows);
+  group_simt_kernel<T, KIND, COMP><<<grid, simt_threads(COMP), smem, s>>>(g, splits, out_rows);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || splits == 1) return e;
   return group_join(given, splits, out_rows, KIND == GROUP_DX ? g.d_in : g.d_out, s);
@@ -256,8 +287,18 @@ __global__ void __launch_bounds__(256) group_join_kernel(const GroupArgs g, int 
       if (!inside && !g.zero_rest) continue;
     }
     float x = 0.0f;
-    if (inside)
+    if (inside && g.compensated) {
+      float err = 0.0f;
+      for (int s = 0; s < splits; ++s) {
+        const float h = g.ws[s * total + i], t = __fadd_rn(x, h), z = __fsub_rn(t, x);
+        err = __fadd_rn(err, __fadd_rn(g.ws[(splits + s) * total + i],
+                                       __fadd_rn(__fsub_rn(x, __fsub_rn(t, z)), __fsub_rn(h, z))));
+        x = t;
+      }
+      x = dot2_value(x, err);
+    } else if (inside) {
       for (int s = 0; s < splits; ++s) x += g.ws[s * total + i];
+    }
     if (KIND == GROUP_DW) static_cast<float*>(g.out)[i] = x;
     else group_epilogue<T>(g, (size_t)i, x);
   }
@@ -273,7 +314,7 @@ cudaError_t join_launch(const GroupArgs& g, int splits, long long rows, int N, c
 
 // For these rows or fewer: in the forward and dX, s <= kSplitBlocks / tiles parts
 // of at most S_T tiles / tiles_n rows; dW's parts grow with the rows.
-size_t grouped_simt_split_bytes(int rows, int groups, int d_in, int d_out) {
+size_t grouped_simt_split_bytes(int rows, int groups, int d_in, int d_out, bool compensated) {
   size_t most = 0;
   for (int kind : {GROUP_FWD, GROUP_DX, GROUP_DW}) {
     const bool dw = kind == GROUP_DW;
@@ -282,7 +323,7 @@ size_t grouped_simt_split_bytes(int rows, int groups, int d_in, int d_out) {
     if (s < 2) continue;
     const long long part_rows = dw ? (long long)s * groups * d_in
                                    : std::min((long long)s * rows, kSplitBlocks * S_T / ((N + S_T - 1) / S_T));
-    most = std::max<size_t>(most, (size_t)part_rows * N * 4);
+    most = std::max<size_t>(most, (size_t)part_rows * N * (kind == GROUP_FWD && compensated ? 8 : 4));
   }
   return most;
 }
@@ -306,7 +347,8 @@ cudaError_t grouped_gemm(const GroupArgs& g, cudaStream_t s) {
   if (g.rows == 0 && g.kind != GROUP_DW) return cudaSuccess;
   if (grouped_tc_eligible(g)) return grouped_gemm_tc(g, s);
   if (g.type == DT_F32) {
-    if (g.kind == GROUP_FWD) return simt_launch<float, GROUP_FWD>(g, s);
+    if (g.kind == GROUP_FWD)
+      return g.compensated ? simt_launch<float, GROUP_FWD, true>(g, s) : simt_launch<float, GROUP_FWD>(g, s);
     if (g.kind == GROUP_DX) return simt_launch<float, GROUP_DX>(g, s);
     return simt_launch<float, GROUP_DW>(g, s);
   }
@@ -325,7 +367,7 @@ using mg::op_fail;
 constexpr size_t kErrorBytes = 256;   // of a workspace: begins with the error word; then the scratch
 
 size_t workspace_bytes(int rows, int groups, int d_in, int d_out) {
-  return kErrorBytes + mg::grouped_scratch_bytes(rows, groups, d_in, d_out);
+  return kErrorBytes + mg::grouped_scratch_bytes(rows, groups, d_in, d_out, false);
 }
 
 mg_status grouped_call(const char* fn, mg::GroupKind kind, int dtype, const void* a, const void* b,

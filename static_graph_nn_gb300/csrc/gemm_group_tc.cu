@@ -758,8 +758,8 @@ bool grouped_tc_eligible(const GroupArgs& g) {
   return al(g.A) && al(g.B) && group_encode_fn() != nullptr;
 }
 
-size_t grouped_scratch_bytes(int rows, int groups, int d_in, int d_out) {
-  size_t most = grouped_simt_split_bytes(rows, groups, d_in, d_out);
+size_t grouped_scratch_bytes(int rows, int groups, int d_in, int d_out, bool compensated) {
+  size_t most = grouped_simt_split_bytes(rows, groups, d_in, d_out, compensated);
   for (int kind : {GROUP_FWD, GROUP_DX, GROUP_DW}) {
     size_t n = split_bytes(kind, rows, groups, d_in, d_out);
     if (group_repacks(kind, rows, groups, d_in, d_out))

@@ -150,17 +150,6 @@ __device__ __forceinline__ void epilogue_elem(const GemmArgs& g, const float* bi
   st_elem(static_cast<TO*>(g.out), (size_t)m * g.ldo + n, v);
 }
 
-// s + c += a*b with the rounding errors of the product and the sum kept in c.
-__device__ __forceinline__ void dot2_step(float a, float b, float& s, float& c) {
-  float p = __fmul_rn(a, b);
-  float pe = __fmaf_rn(a, b, -p);            // a*b - p exactly
-  float t = __fadd_rn(s, p);
-  float z = __fsub_rn(t, s);
-  float se = __fadd_rn(__fsub_rn(s, __fsub_rn(t, z)), __fsub_rn(p, z));   // s + p - t exactly
-  s = t;
-  c = __fadd_rn(c, __fadd_rn(pe, se));
-}
-
 // Two CTAs per SM (128 registers, four warps per SM sub-partition to hide
 // the FFMA latency chains).  A strict weight gradient split over K
 // (blockIdx.z = split, k_per > 0) writes its partial tile to its slice of

@@ -212,17 +212,19 @@ struct GroupArgs {
   const void* saved = nullptr; int dact = 0;
   const void* resid = nullptr;
   int zero_rest = 0;           // rows of no group are computed as if A were 0 there
+  int compensated = 0;         // fp32 FWD: sums carry their rounding errors (a strict plan's forward)
   int* err = nullptr;          // set to 1 on a timed-out wait
   float* ws = nullptr;         // grouped_scratch_bytes; NULL: no split over K, no repacked operands
 };
 // Scratch of the products of these sizes (any kind and type), 16-byte aligned.
-size_t grouped_scratch_bytes(int rows, int groups, int d_in, int d_out);
-size_t grouped_simt_split_bytes(int rows, int groups, int d_in, int d_out);   // the CUDA-core part of it
+// compensated: a FWD of that kind among them.
+size_t grouped_scratch_bytes(int rows, int groups, int d_in, int d_out, bool compensated);
+size_t grouped_simt_split_bytes(int rows, int groups, int d_in, int d_out, bool compensated);   // the CUDA cores' part
 // Rows of the output matrix: g.rows, or groups * d_in in dW.
 inline long long group_out_rows(int kind, int rows, int groups, int d_in) {
   return kind == GROUP_DW ? (long long)groups * d_in : rows;
 }
-// out = the sum of g.ws [splits][rows][N] in order, through the epilogue
+// out = the sum of g.ws [splits][rows][N] (compensated: then as many errors) in order, through the epilogue
 // (forward, dX: rows of a group, and with zero_rest the others as zeros); a
 // dependent launch.
 cudaError_t group_join(const GroupArgs& g, int splits, long long rows, int N, cudaStream_t s);

@@ -343,6 +343,7 @@ GroupArgs group_args(mg_plan* p, const Node& n, GroupKind kind) {
   g.d_out = n.d_out;
   g.offsets = p->row_groups;
   g.zero_rest = 1;
+  g.compensated = p->dt == DT_F32 && kind == GROUP_FWD;   // as the dense forward's
   g.err = reinterpret_cast<int*>(p->ws + p->loss_off + 4);
   if (p->group_off) g.ws = wsp<float>(p, p->group_off);
   return g;
@@ -1181,7 +1182,7 @@ void layout_workspace(mg_plan* p) {
   for (const Node& n : p->nodes) {
     if (n.kind == NK_EMBED) p->embed_off = b.take(embedding_ws_bytes(p->batch, n.d_in, n.d_out));
     if (n.kind == NK_GROUP)
-      group_ws = std::max(group_ws, grouped_scratch_bytes(p->batch, n.groups, n.d_in, n.d_out));
+      group_ws = std::max(group_ws, grouped_scratch_bytes(p->batch, n.groups, n.d_in, n.d_out, p->dt == DT_F32));
   }
   if (group_ws) p->group_off = b.take(group_ws);
   // chunks
