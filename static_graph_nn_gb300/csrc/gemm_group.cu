@@ -9,8 +9,9 @@
 // memory and walks the same list of output tiles, so the host neither waits
 // for the router nor launches one product per expert.
 //
-// This file's kernel runs fp32 (FFMA only) and small bf16 products of widths
-// that TMA cannot address (rows that are not multiples of 16 bytes).  Bound by the FP32 units:
+// This file's kernel runs fp32 (FFMA only), small bf16 products of widths that
+// TMA cannot address (rows that are not multiples of 16 bytes), and every bf16
+// product of a plan made with MG_GEMM=simt.  Bound by the FP32 units:
 // 64x64 tiles (a group's last tile is half empty on average, so small ones) of
 // 128 threads with 8x4 outputs each, two products per instruction.  fp32
 // operands come by 4-byte asynchronous copies (any width and alignment,

@@ -748,7 +748,7 @@ bool group_map(CUtensorMap* map, const void* base, long long outer, long long ro
 bool grouped_tc_eligible(const GroupArgs& g) {
   auto al = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
   // mo = e * d_in + m and the tile counts are 32-bit
-  if (g.type != DT_BF16 || g.rows == 0) return false;
+  if (!g.use_tc || g.type != DT_BF16 || g.rows == 0) return false;
   if ((g.d_in % 8 || g.d_out % 8) && !(g.ws && group_repacks(g.kind, g.rows, g.groups, g.d_in, g.d_out))) return false;
   if ((long long)g.groups * g.d_in > 0x7fff0000ll) return false;
   const long long tiles_n = ((g.kind == GROUP_DX ? g.d_in : g.d_out) + G_BN - 1) / G_BN;

@@ -212,6 +212,7 @@ struct GroupArgs {
   const void* saved = nullptr; int dact = 0;
   const void* resid = nullptr;
   int zero_rest = 0;           // rows of no group are computed as if A were 0 there
+  int use_tc = 1;              // 0: CUDA cores only
   int compensated = 0;         // fp32 FWD: sums carry their rounding errors (a strict plan's forward)
   int* err = nullptr;          // set to 1 on a timed-out wait
   float* ws = nullptr;         // grouped_scratch_bytes; NULL: no split over K, no repacked operands

@@ -343,6 +343,7 @@ GroupArgs group_args(mg_plan* p, const Node& n, GroupKind kind) {
   g.d_out = n.d_out;
   g.offsets = p->row_groups;
   g.zero_rest = 1;
+  g.use_tc = p->use_tc;
   g.compensated = p->dt == DT_F32 && kind == GROUP_FWD;   // as the dense forward's
   g.err = reinterpret_cast<int*>(p->ws + p->loss_off + 4);
   if (p->group_off) g.ws = wsp<float>(p, p->group_off);
