@@ -355,11 +355,9 @@ double group_bytes(const mg_plan* p, const Node& n, bool dw) {
   return es * p->batch * (n.d_in + n.d_out) + (dw ? 4.0 : es) * n.groups * (double)n.d_in * n.d_out;
 }
 
-std::string group_name(const mg_plan* p, const char* what, const Node& n) {
+std::string group_name(const mg_plan* p, const char* what, const Node& n, const GroupArgs& g) {
   char b[160];
-  const char* kind = p->dt != DT_BF16                           ? "f32-ffma"
-                     : grouped_tc_eligible(group_args(const_cast<mg_plan*>(p), n, GROUP_FWD)) ? "bf16-tcgen05"
-                                                                                               : "bf16-simt";
+  const char* kind = p->dt != DT_BF16 ? "f32-ffma" : grouped_tc_eligible(g) ? "bf16-tcgen05" : "bf16-simt";
   snprintf(b, sizeof b, "%s[l%d] %d rows x %d groups x %dx%d %s", what, n.layer, p->batch, n.groups, n.d_in, n.d_out,
            kind);
   return b;
@@ -402,7 +400,7 @@ void forward_pass(Exec& e, const float* params, const void* x) {
       if (n.z >= 0) g.out_z = p->ws + p->values[n.z].off;
       if (n.skip >= 0) g.resid = val_ptr(p, n.skip, x);
       g.out = p->ws + p->values[n.out].off;
-      site(e, group_name(p, "grouped_fwd", n), 2.0 * p->batch * n.d_in * n.d_out, group_bytes(p, n, false),
+      site(e, group_name(p, "grouped_fwd", n, g), 2.0 * p->batch * n.d_in * n.d_out, group_bytes(p, n, false),
            grouped_launches(g), [&] { return grouped_gemm(g, e.s); });
     } else if (n.kind == NK_EMBED) {
       char nm[96];
@@ -716,7 +714,7 @@ void backward_pass(Exec& e, const float* params, float* grads, const void* x) {
       g.A = val_ptr(p, n.in, x);
       g.B = gy;
       g.out = grads + n.w_off;
-      site(e, group_name(p, "grouped_dW", n), 2.0 * p->batch * n.d_in * n.d_out, group_bytes(p, n, true),
+      site(e, group_name(p, "grouped_dW", n, g), 2.0 * p->batch * n.d_in * n.d_out, group_bytes(p, n, true),
            grouped_launches(g), [&] { return grouped_gemm(g, e.s); });
       if (vin.need_grad) {
         GroupArgs h = group_args(p, n, GROUP_DX);
@@ -730,7 +728,7 @@ void backward_pass(Exec& e, const float* params, float* grads, const void* x) {
         }
         h.resid = dadd;
         h.out = grad_ptr(p, n.in);
-        site(e, group_name(p, "grouped_dX", n), 2.0 * p->batch * n.d_in * n.d_out, group_bytes(p, n, false),
+        site(e, group_name(p, "grouped_dX", n, h), 2.0 * p->batch * n.d_in * n.d_out, group_bytes(p, n, false),
              grouped_launches(h), [&] { return grouped_gemm(h, e.s); });
       }
       node_update(e, ni);

@@ -53,3 +53,16 @@ def test_simt_switch(rows, k, h, monkeypatch):
         assert float(a @ b) >= 0.999 * float(a.norm() * b.norm())
     tc.close()
     simt.close()
+
+
+def test_each_product_is_named_by_its_own_path():
+    """Odd widths, a few rows: the forward is worth the tensor cores, the weight
+    gradient is not, nor is an input gradient of a short sum."""
+    layers = [W.linear(128, 128, False), W.grouped_linear(8, 128, 65), W.linear(65, 16, False)]
+    plan, _ = _step(layers, 24, [0, 3, 3, 9, 12, 13, 20, 22, 24])
+    assert _sites(plan) == {"grouped_fwd": "bf16-tcgen05", "grouped_dW": "bf16-simt", "grouped_dX": "bf16-simt"}
+    plan.close()
+    layers = [W.linear(128, 128, False), W.grouped_linear(4, 128, 256), W.linear(256, 16, False)]
+    plan, _ = _step(layers, 600, [0, 100, 200, 200, 600])
+    assert set(_sites(plan).values()) == {"bf16-tcgen05"}
+    plan.close()
