@@ -689,8 +689,8 @@ __global__ void __launch_bounds__(256, 2) embed_sum_kernel(const SumArgs A) {
       // keys and fetches of the batch at j (a multiple of 4) into half h
       auto fetch = [&](uint32_t j, int h) {
         if (j < we) {
-          const uint4 k4 = __ldg(reinterpret_cast<const uint4*>(A.key + j));
-          const uint4 p4 = __ldg(reinterpret_cast<const uint4*>(A.pos + j));
+          const uint4 k4 = *reinterpret_cast<const uint4*>(A.key + j);
+          const uint4 p4 = *reinterpret_cast<const uint4*>(A.pos + j);
           const uint32_t kq[4] = {k4.x, k4.y, k4.z, k4.w}, pq[4] = {p4.x, p4.y, p4.z, p4.w};
 #pragma unroll
           for (int q = 0; q < B; ++q) {
