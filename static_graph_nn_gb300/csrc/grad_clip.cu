@@ -238,11 +238,15 @@ __device__ __forceinline__ float2 clip_finish(const double* partial, int n, floa
 __global__ void __launch_bounds__(kClipThreads, kClipFusedPerSm)
     clip_fused_kernel(const ClipChunk* chunks, ClipSum* sums, ClipSync* sync, float max_norm, float* stats) {
   __shared__ double red[32];
+  __shared__ unsigned long long s_call;
   const ClipChunk c = chunks[blockIdx.x];
-  const unsigned long long call = *reinterpret_cast<volatile unsigned long long*>(&sync->calls) + 1;
+  // one thread reads the number of calls and passes it on with the block's sum:
+  // block 0, which writes the next number, does so with every block's sum at hand
+  if (threadIdx.x == 0) s_call = *reinterpret_cast<volatile unsigned long long*>(&sync->calls) + 1;
   ClipData d;
   d.load(c);
   const double t = block_sum_f64(chunk_squares(c, d), red);
+  const unsigned long long call = s_call;
   if (threadIdx.x == 0) put_sum(sums + blockIdx.x, t, call);
   double s = 0.0;
   bool ok = true;
@@ -262,7 +266,7 @@ __global__ void __launch_bounds__(kClipThreads, kClipFusedPerSm)
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     stats[0] = r.x;
     stats[1] = r.y;
-    sync->calls = call;              // every block has read the old number: its sum is there
+    sync->calls = call;              // each sum carries the number that its block's one reader read
   }
   if (r.y == 1.0f && c.out == c.g) return;
   chunk_store(c, d, r.y);
