@@ -426,7 +426,9 @@ mg_status mg_grouped_linear_backward_weight(int dtype, const void* x, const void
  * gradients keep their bits for the caller to find.  (Finite gradients whose
  * norm is beyond fp32's range have stats[0] = infinity and are clipped.)
  * max_norm >= 0; INFINITY only measures.  A bounded device-side wait that gave
- * up (never seen) sets stats to NaN; the outputs are then partly written. */
+ * up (never seen) sets both stats to NaN, in that call and every later one of
+ * the list; the outputs are then partly written.
+ * (The wait of lists up to 15 MB: MG_CLIP_WAIT tries, read at creation.) */
 typedef struct mg_grad_list mg_grad_list;
 mg_status mg_grad_list_create(int n, const void* const* grads, void* const* out,
                               const size_t* counts, const int* dtypes, mg_grad_list** list);

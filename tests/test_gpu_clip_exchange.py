@@ -8,7 +8,7 @@ torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
 import static_graph_nn_gb300 as mg   # noqa: E402
-from test_gpu_grad_clip import NORM_TOL, U32, _make, _want   # noqa: E402
+from test_gpu_grad_clip import NORM_TOL, U32, _check, _make, _want   # noqa: E402
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -40,3 +40,38 @@ def test_calls_back_to_back(sizes):
         assert abs(float(got[i, 0]) - want) <= NORM_TOL * want
         assert abs(float(got[i, 1]) - c) <= (NORM_TOL + 2 * U32) * c      # the factor's rounding and max_norm's
     lst.close()
+
+
+def test_a_wait_that_gives_up_is_reported(monkeypatch):
+    """With one try a wait, blocks give up as they find sums missing.  Whatever each
+    of them met, statistics that are numbers mean that every chunk was written."""
+    grads = _make([8192] * 300, ["f32"], 2)
+    norm, c = _want(grads, 1.0)
+    lst = {}
+    for tries in ("1", ""):
+        monkeypatch.setenv("MG_CLIP_WAIT", tries)
+        outs = [torch.empty_like(x) for x in grads]
+        lst[tries] = (mg.GradList(grads, outs), outs)
+    stats = torch.empty(2, device="cuda")
+    gave_up = 0
+    for _ in range(60):
+        gl, outs = lst["1"]
+        for o in outs:
+            o.fill_(float("nan"))
+        gl.clip(1.0, stats)
+        nan = torch.isnan(stats)
+        assert bool(nan[0]) == bool(nan[1])
+        if bool(nan[0]):
+            gave_up += 1
+        elif gave_up:
+            raise AssertionError("numbers from a list whose exchange has failed before")
+        else:
+            assert abs(float(stats[0]) - norm) <= NORM_TOL * norm
+            assert not any(torch.isnan(o).any() for o in outs)
+        # another list is not touched
+        gl, outs = lst[""]
+        gl.clip(1.0, stats)
+        _check(grads, outs, stats, 1.0)
+    assert gave_up
+    for gl, _ in lst.values():
+        gl.close()
