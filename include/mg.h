@@ -396,8 +396,10 @@ mg_status mg_embedding_backward(int dtype, const void* dout, int vocab, int dim,
  * aligned ones in the workspace first; small products of such widths, and fp32,
  * run on the CUDA cores).
  * workspace: mg_grouped_linear_workspace_bytes (for these rows or fewer); zero it
- * once before its first use.  Its first int is set to 1 if a bounded device-side wait gave up, in
- * which case that call's results are invalid. */
+ * once before its first use.  Its first int is set to 1 if a bounded device-side wait gave up (never
+ * seen), in which case that call's results are invalid; it stays 1 until the workspace is zeroed again.
+ * mg_grouped_linear_status waits for `stream` and answers MG_ERR_TIMEOUT if it is set (not while
+ * `stream` is being captured). */
 size_t mg_grouped_linear_workspace_bytes(int rows, int groups, int d_in, int d_out);
 mg_status mg_grouped_linear_forward(int dtype, const void* x, const int* offsets, int rows, int groups,
                                     int d_in, int d_out, const void* w, void* y, void* workspace,
@@ -410,6 +412,8 @@ mg_status mg_grouped_linear_backward_weight(int dtype, const void* x, const void
                                             const int* offsets, int rows, int groups, int d_in,
                                             int d_out, float* dw, void* workspace,
                                             size_t workspace_bytes, mg_stream_t stream);
+
+mg_status mg_grouped_linear_status(const void* workspace, mg_stream_t stream);
 
 /* Global gradient norm and clipping over many tensors.  A list holds n device
  * tensors (counts[i] elements of dtypes[i] at grads[i]) and where their scaled

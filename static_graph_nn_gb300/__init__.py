@@ -5,4 +5,4 @@ holds the seeded synthetic workloads."""
 from .binding import (GradList, Plan, embedding_backward, embedding_forward,  # noqa: F401
                       embedding_workspace_bytes, grouped_linear_backward_input,
                       grouped_linear_backward_weight, grouped_linear_forward,
-                      grouped_linear_workspace_bytes, load)
+                      grouped_linear_status, grouped_linear_workspace_bytes, load)

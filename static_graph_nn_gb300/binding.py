@@ -94,6 +94,7 @@ _SIGS = {
                                          + [_P, _P, _P, ctypes.c_size_t, _P]),
     "mg_grouped_linear_backward_weight": (ctypes.c_int, [ctypes.c_int, _P, _P, _P] + [ctypes.c_int] * 4
                                           + [_P, _P, ctypes.c_size_t, _P]),
+    "mg_grouped_linear_status": (ctypes.c_int, [_P, _P]),
     "mg_grad_list_create": (ctypes.c_int, [ctypes.c_int, ctypes.POINTER(_P), ctypes.POINTER(_P),
                                            ctypes.POINTER(ctypes.c_size_t),
                                            ctypes.POINTER(ctypes.c_int), ctypes.POINTER(_P)]),
@@ -497,6 +498,13 @@ def grouped_linear_backward_weight(x, dy, offsets, dw, workspace, stream=None):
     _status(load().mg_grouped_linear_backward_weight(_code(x, "x"), _ptr(x), _ptr(dy), _ptr(offsets),
                                                      x.shape[0], e, k, n, _ptr(dw), _ptr(workspace), nb,
                                                      _stream(stream)))
+
+
+def grouped_linear_status(workspace, stream=None):
+    """Waits for the stream; raises an MGError (MG_ERR_TIMEOUT) if a device-side wait
+    gave up in an earlier call with this workspace, whose results are then invalid."""
+    _dense(workspace, "workspace")
+    _status(load().mg_grouped_linear_status(_ptr(workspace), _stream(stream)))
 
 
 class GradList:

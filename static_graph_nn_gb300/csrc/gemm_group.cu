@@ -437,3 +437,18 @@ extern "C" mg_status mg_grouped_linear_backward_weight(int dtype, const void* x,
   return grouped_call("mg_grouped_linear_backward_weight", mg::GROUP_DW, dtype, x, dy, offsets, rows, groups, d_in,
                       d_out, dw, ws, ws_bytes, stream);
 }
+
+extern "C" mg_status mg_grouped_linear_status(const void* ws, mg_stream_t stream) {
+  const char* fn = "mg_grouped_linear_status";
+  if (!ws) return op_fail(MG_ERR_INVALID_ARG, "%s: workspace is NULL", fn);
+  const mg_status st = mg::op_begin(fn, {{ws, 16}});
+  if (st != MG_OK) return st;
+  int gave_up = 0;
+  cudaError_t e = cudaMemcpyAsync(&gave_up, ws, sizeof gave_up, cudaMemcpyDeviceToHost, (cudaStream_t)stream);
+  if (e == cudaSuccess) e = cudaStreamSynchronize((cudaStream_t)stream);
+  if (e != cudaSuccess) return mg::op_end(fn, e);
+  if (gave_up)
+    return op_fail(MG_ERR_TIMEOUT, "%s: a device-side wait gave up in a call with this workspace: its results are invalid",
+                   fn);
+  return MG_OK;
+}
