@@ -147,7 +147,13 @@ def _stream(stream) -> int | None:
     return stream.cuda_stream
 
 
+_INT_MAX = 2 ** 31 - 1     # sizes in the C ABI; ctypes would keep a larger one's low bits
+
+
 def layer_struct(l: dict) -> mg_layer:
+    for name, v in l.items():
+        if isinstance(v, int) and abs(v) > _INT_MAX:
+            raise MGError(MG_ERR_SHAPE, f"{l['op']}: {name} = {v} is beyond 32 bits")
     s = mg_layer()
     s.op = OPS[l["op"]]
     if l["op"] == "linear":
@@ -386,13 +392,20 @@ def _dense(t, name: str, shape: tuple | None = None):
         _refuse(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}", MG_ERR_SHAPE)
 
 
+def _fits(*sizes: int):
+    if max(sizes) > _INT_MAX:
+        _refuse(f"a size is beyond 32 bits: {sizes}", MG_ERR_SHAPE)
+
+
 def _status(st: int):
     if st != MG_OK:
         raise MGError(st, load().mg_last_error(None).decode())
 
 
 def embedding_workspace_bytes(n: int, vocab: int, dim: int) -> int:
-    """Bytes of workspace that embedding_backward needs for n ids."""
+    """Bytes of workspace that embedding_backward needs for n ids (0: refused sizes)."""
+    if max(vocab, dim) > _INT_MAX or n >= 2 ** 63:
+        return 0
     return load().mg_embedding_workspace_bytes(n, vocab, dim)
 
 
@@ -404,6 +417,7 @@ def embedding_forward(table, ids, out, scale: float = 1.0, stream=None):
     if table.dim() != 2:
         _refuse("table must be [vocab, dim]", MG_ERR_SHAPE)
     v, d = table.shape
+    _fits(v, d)
     _dense(table, "table")
     _dense(ids, "ids")
     _dense(out, "out", ids.shape + (d,))
@@ -419,6 +433,7 @@ def embedding_backward(dout, ids, dtable, workspace, scale: float = 1.0, stream=
     if dtable.dim() != 2 or dtable.dtype != _type_tables()[2]:
         _refuse("dtable must be [vocab, dim] float32", MG_ERR_SHAPE)
     v, d = dtable.shape
+    _fits(v, d)
     _dense(dtable, "dtable")
     _dense(ids, "ids")
     _dense(dout, "dout", ids.shape + (d,))
@@ -431,17 +446,21 @@ def embedding_backward(dout, ids, dtable, workspace, scale: float = 1.0, stream=
 
 
 def grouped_linear_workspace_bytes(rows: int, groups: int, d_in: int, d_out: int) -> int:
-    """Bytes of workspace for the grouped products of these sizes (zero it once)."""
+    """Bytes of workspace for the grouped products of these sizes (zero it once; 0:
+    refused sizes)."""
+    if max(rows, groups, d_in, d_out) > _INT_MAX:
+        return 0
     return load().mg_grouped_linear_workspace_bytes(rows, groups, d_in, d_out)
 
 
-def _grouped_args(rows_t, name, offsets, groups, workspace):
+def _grouped_args(rows_t, name, offsets, weights, workspace):
     if rows_t.dim() != 2:
         _refuse(f"{name} must be two-dimensional", MG_ERR_SHAPE)
+    _fits(*rows_t.shape, *weights)
     _dense(rows_t, name)
     if offsets.dtype != _type_tables()[3]:
         _refuse("offsets must be int32")
-    _dense(offsets, "offsets", (groups + 1,))
+    _dense(offsets, "offsets", (weights[0] + 1,))
     _dense(workspace, "workspace")
     return workspace.nbytes
 
@@ -459,7 +478,7 @@ def grouped_linear_forward(x, offsets, w, y, workspace, stream=None):
     if w.dim() != 3:
         _refuse("w must be [groups, d_in, d_out]", MG_ERR_SHAPE)
     e, k, n = w.shape
-    nb = _grouped_args(x, "x", offsets, e, workspace)
+    nb = _grouped_args(x, "x", offsets, (e, k, n), workspace)
     _dense(x, "x", (x.shape[0], k))
     _dense(w, "w")
     _dense(y, "y", (x.shape[0], n))
@@ -474,7 +493,7 @@ def grouped_linear_backward_input(dy, offsets, w, dx, workspace, stream=None):
     if w.dim() != 3:
         _refuse("w must be [groups, d_in, d_out]", MG_ERR_SHAPE)
     e, k, n = w.shape
-    nb = _grouped_args(dy, "dy", offsets, e, workspace)
+    nb = _grouped_args(dy, "dy", offsets, (e, k, n), workspace)
     _dense(dy, "dy", (dy.shape[0], n))
     _dense(w, "w")
     _dense(dx, "dx", (dy.shape[0], k))
@@ -490,7 +509,7 @@ def grouped_linear_backward_weight(x, dy, offsets, dw, workspace, stream=None):
     if dw.dim() != 3 or dw.dtype != _type_tables()[2]:
         _refuse("dw must be [groups, d_in, d_out] float32", MG_ERR_SHAPE)
     e, k, n = dw.shape
-    nb = _grouped_args(x, "x", offsets, e, workspace)
+    nb = _grouped_args(x, "x", offsets, (e, k, n), workspace)
     _dense(x, "x", (x.shape[0], k))
     _dense(dy, "dy", (x.shape[0], n))
     _dense(dw, "dw")
