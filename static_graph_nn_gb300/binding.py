@@ -261,6 +261,8 @@ class Plan:
     def set_grad_clip(self, max_norm: float):
         """Clip every later step's gradients to this global norm (inf: measure only;
         0: off)."""
+        if max_norm > 0 and ctypes.c_float(max_norm).value == 0:
+            _refuse(f"max_norm = {max_norm} is 0 in fp32, which would turn clipping off")
         self._check(self.lib.mg_set_grad_clip(self.h, max_norm))
 
     def grad_norm(self, stream=None) -> tuple[float, float]:
