@@ -242,6 +242,8 @@ __global__ void __launch_bounds__(N_THREADS, 1)
     }
   }
 
+  if (*abort_flag) drain_in_flight();
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (P.split > 1) cluster_sync();     // no CTA leaves while another writes to it

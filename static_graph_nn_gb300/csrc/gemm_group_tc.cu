@@ -519,6 +519,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(group_threads(KIND),
     if (KIND == GROUP_DW && !ANY && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
 
+  if (*abort_flag) drain_in_flight();
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   cluster_sync();                      // no remote arrive or MMA still targets either CTA

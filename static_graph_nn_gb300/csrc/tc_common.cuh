@@ -77,6 +77,15 @@ static __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t
   return false;
 }
 
+// For a kernel that gives up after a wait ran out: copies and MMAs that it has
+// issued may still be on their way into its shared memory and TMEM, which the
+// next CTA of this SM is given once it leaves.  Each takes microseconds; two
+// milliseconds, by every thread, before the CTA's last barrier.
+static __device__ __forceinline__ void drain_in_flight() {
+#pragma unroll 1
+  for (int i = 0; i < 2000; ++i) __nanosleep(1000);
+}
+
 static __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar,
                                             int x, int y) {
   asm volatile(
