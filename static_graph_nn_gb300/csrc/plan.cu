@@ -20,8 +20,10 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <exception>
 #include <mutex>
 #include <string>
+#include <utility>
 #include <vector>
 
 #include "../../include/mg.h"
@@ -1284,7 +1286,7 @@ void build_dump(mg_plan* p) {
              p->sites[i].flops, p->sites[i].bytes);
     s += b;
   }
-  p->dump = s;
+  p->dump = std::move(s);
 }
 
 mg_status check_device(mg_plan* p) {
@@ -1300,7 +1302,11 @@ mg_status check_device(mg_plan* p) {
 
 void mg::set_global_error(const char* msg) {
   std::lock_guard<std::mutex> lk(g_err_mu);
-  g_err = msg;
+  try {
+    g_err = msg;
+  } catch (const std::exception&) {   // the status still says what happened
+    g_err.clear();
+  }
 }
 
 // ============================================================================
@@ -1649,16 +1655,25 @@ mg_status mg_set_grad_clip(mg_plan* p, float max_norm) {
     }
   }
   if (max_norm == p->max_norm) return MG_OK;
+  const float old_norm = p->max_norm;
+  std::vector<Site> old_sites;
+  old_sites.swap(p->sites);
   p->max_norm = max_norm;
   for (auto& g : p->graphs) {        // captured steps are the old schedule
     drop_graph(g);
     g.calls = 0;
   }
   plan_fused_updates(p);
-  p->sites.clear();
-  Exec ex{p, nullptr, true, false};
-  train_schedule(ex, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, 0.f, 1);
-  build_dump(p);
+  try {
+    Exec ex{p, nullptr, true, false};
+    train_schedule(ex, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, 0.f, 1);
+    build_dump(p);
+  } catch (const std::exception&) {   // of the site list's names: none leaves a C entry, and the plan stays as it was
+    p->sites.swap(old_sites);
+    p->max_norm = old_norm;
+    plan_fused_updates(p);
+    return MG_ERR_OOM;
+  }
   return MG_OK;
 }
 
