@@ -362,7 +362,8 @@ mg_status mg_softmax_ce_noalloc(int dtype, const void* logits, int rows, int col
  * scratch of one call at a time: calls that may overlap on the GPU (other
  * streams, other captured graphs) need one each.  Messages: mg_last_error(NULL).
  *
- * Embedding: out[i, :] = scale * table[ids[i], :], rounded once to out's type.
+ * Embedding: out[i, :] = scale * table[ids[i], :], a product in fp32 rounded to
+ * out's type.
  * id_kind 0 = int32, 1 = int64.  An id outside [0, vocab) -- padding -- reads
  * nothing: its row of out is 0.  table [vocab, dim], ids [n], out [n, dim];
  * n = 0 is allowed, dim is at most 2^30.
@@ -390,8 +391,8 @@ mg_status mg_embedding_backward(int dtype, const void* dout, int vocab, int dim,
  *   backward_input   dx[r] = dy[r] w[e(r)]^T         [rows, d_in]
  *   backward_weight  dw[e] = x_e^T dy_e              [groups, d_in, d_out], fp32
  * dtype is the type of x, w, y, dx, dy; sums are fp32.  Rows outside
- * [offsets[0], offsets[groups]) are neither read nor written; dw of an empty
- * group is 0.  groups at most 1024, rows and widths at most 2^30.  bf16 runs on
+ * [offsets[0], offsets[groups]) and the weights of empty groups enter no result,
+ * whatever they hold, and such rows are not written; dw of an empty group is 0.  groups at most 1024, rows and widths at most 2^30.  bf16 runs on
  * the tensor cores (rows of widths that are no multiples of 8 are copied to
  * aligned ones in the workspace first; small products of such widths, and fp32,
  * run on the CUDA cores).
@@ -425,7 +426,8 @@ mg_status mg_grouped_linear_status(const void* workspace, mg_stream_t stream);
  * time.
  * mg_grad_list_clip: stats[0] = norm = sqrt(sum of all squares), stats[1] =
  * c = max_norm / norm if norm > max_norm, else 1 (fp32, device memory, 8-byte
- * aligned), and out = c * grads.  With c = 1 an in-place list is left as it
+ * aligned; memory of no tensor of the list), and out = c * grads (c as rounded to
+ * fp32: 0 where it is below 2^-150).  With c = 1 an in-place list is left as it
  * is.  A gradient that holds NaN or infinity gives such a norm and c = 1: the
  * gradients keep their bits for the caller to find.  (Finite gradients whose
  * norm is beyond fp32's range have stats[0] = infinity and are clipped.)

@@ -3,9 +3,12 @@
 //   forward   out[i] = scale * table[id_i]               (0 for an id outside [0, V))
 //   backward  dtable[v] = scale * sum_{i: id_i = v} dout[i]   (dense, fp32)
 //
-// The forward is a gather: it reads n rows and writes n rows, nothing else, so
-// it is bound by DRAM (and, for a few tokens, by one launch).  A thread moves
-// 16 bytes of one row and has several rows' loads in flight.
+// The forward is a gather: it reads the rows that the ids name and writes n
+// rows, nothing else.  A thread moves 16 bytes of one row and has several rows'
+// loads in flight.  A few tokens are bound by one launch; many by the chain of
+// two loads (an id, then its row) of blocks that end after one round: 16384 bf16
+// rows of 2048, about 5800 of them distinct, take 21 us, and their bytes 13.4 at
+// the DRAM's rate.
 //
 // The backward must write all V rows, and sums the rows of dout that share an
 // id.  Adding with atomics would need a zeroed table, a read-modify-write of
@@ -25,8 +28,8 @@
 //   3. a third launch joins those partials, a block per sum, in a fixed order.
 //
 // Every row of the table is written once, and the order of every addition is
-// fixed by the ids alone: the same bits in every run.  Bound by DRAM (V d fp32
-// written, n d read).
+// fixed by the ids alone: the same bits in every run.  Wide rows are bound by
+// DRAM (V d fp32 written, n d read), narrow ones by the three launches in a row.
 #include <algorithm>
 #include <cstdio>
 
@@ -836,7 +839,9 @@ struct Ws {
 Ws ws_layout(long long n, int V, int d) {
   Ws w = {};
   // as many windows (of 8 entries at least) as give kSumThreads threads at 16
-  // columns each: 608 for rows of 2048, 9728 for rows of 128.  Multiples of 4: a
+  // columns each: 608 for rows of 2048, 9728 for rows of 128 (two blocks per SM; of
+  // fp32 rows in multiples of 8, which hold 128 KB of copies a block, one fits, and
+  // they run in two waves).  Multiples of 4: a
   // window's keys are read four at a time
   const long long windows = kSumThreads / threads_per_row((d + 15) / 16);
   const long long win = ((n + windows - 1) / windows + 3) / 4 * 4;

@@ -28,8 +28,8 @@
 // the exact pre-activation.  The same tiles with 256 threads of 4x4 outputs; ten
 // operations a product: 4096 rows x 16 x 1001x517 in 975 us, 123 plain.
 //
-// Where the tiles are fewer than half the resident blocks, each one's sum is
-// split over several blocks through the workspace and joined in order by a
+// Where the tiles do not outnumber the resident blocks, each one's sum is split
+// over several blocks through the workspace and joined in order by a
 // second launch: 111 rows x 3148x1224, one group, dX in fp32: 126 us whole, 39 so.
 #include <algorithm>
 #include <cstdio>

@@ -6,8 +6,8 @@
 // columns on the accumulator's lanes) and up to 32 rows of the group the N
 // side: D[n, t] = sum_k W[k, n] x[t, k], so that no tensor work is spent on
 // rows that do not exist and the stages hold weights, not padding (16 of 20
-// KB).  Seven stages, 112 KB of weights in flight per SM: more slowed it down
-// (24 rows x 8 experts x 2048x8192, weights in DRAM: 51 us with 7, 58 with 10).
+// KB).  Seven stages, 112 KB of weights in flight per SM (24 rows x 8 experts x
+// 2048x8192 with cold caches, a graph launch included: 52.0 us, and 52.3 with five).
 //
 // Where the tiles are fewer than half the SMs, a cluster of two or four CTAs
 // shares a tile, each with a part of K; the partial sums go to the first CTA's
@@ -16,8 +16,8 @@
 // memory, lost more in the joins than the evenness gave: 34 against 21 us for 16
 // experts x 2048x1024.)
 //
-// That call takes 42 us here (6.1 TB/s) and 59 on the 256-row tiles of the pair
-// kernel.
+// Called in a loop, where L2 keeps some of the weights, that product takes 42 us
+// (6.1 TB/s); with cold caches 52, and 73 on the 256-row tiles of the pair kernel.
 //
 // Warps: 0 TMA producer, 1 MMA issuer, 2-5 epilogue (one accumulator lane
 // quarter each).  Every wait is bounded.
@@ -302,10 +302,10 @@ cudaError_t launch_narrow(const GroupArgs& g, cudaStream_t s) {
 }  // namespace
 
 // Up to 16 rows per group on average: a tile then holds most groups whole.  Up
-// to there this kernel is 1.0 to 1.4 times as fast as the pair kernel (3, 8 and
-// 16 rows per group: 51, 51, 53 against 66, 57, 56 us for 8 x 2048x8192; 22, 25,
-// 26 against 25, 25, 25 for 64 x 1024x512); beyond, groups of several tiles read
-// their weights again.
+// to there this kernel is 1.0 to 1.4 times as fast as the pair kernel (cold
+// caches, 3, 8 and 16 rows per group: 52, 52, 53 against 73, 57, 58 us for 8 x
+// 2048x8192; 22, 24, 25 against 26, 26, 26 for 64 x 1024x512); beyond, groups of
+// several tiles read their weights again (32 rows: 66 against 59, 28 against 27).
 bool grouped_narrow(const GroupArgs& g) {
   const long long n = g.kind == GROUP_FWD ? g.d_out : g.d_in;
   const bool fits = ((long long)g.rows / N_T + g.groups) * ((n + N_M - 1) / N_M) <= 0x3fffffff;   // 32-bit tiles

@@ -48,7 +48,7 @@
 // 8 x 2047x8191 forward 518 us, dX 527, dW 591.  The CUDA-core kernel keeps what
 // that is not worth (group_repacks).
 //
-// Few tiles.  Where they are fewer than half the pairs, each tile's K blocks
+// Few tiles.  Where they are at most half the pairs, each tile's K blocks
 // are split over several pairs, which write fp32 partial tiles into the
 // workspace; a second, dependent launch adds them in order and applies the
 // epilogue (the same bits in every run): 16384 rows into one 512x512 weight
