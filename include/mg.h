@@ -426,7 +426,7 @@ mg_status mg_grouped_linear_status(const void* workspace, mg_stream_t stream);
  * time.
  * mg_grad_list_clip: stats[0] = norm = sqrt(sum of all squares), stats[1] =
  * c = max_norm / norm if norm > max_norm, else 1 (fp32, device memory, 8-byte
- * aligned; memory of no tensor of the list), and out = c * grads (c as rounded to
+ * aligned; within a tensor of the list: MG_ERR_INVALID_ARG), and out = c * grads (c as rounded to
  * fp32: 0 where it is below 2^-150).  With c = 1 an in-place list is left as it
  * is.  A gradient that holds NaN or infinity gives such a norm and c = 1: the
  * gradients keep their bits for the caller to find.  (Finite gradients whose

@@ -29,8 +29,10 @@
 #include <cstdio>
 #include <cstdlib>
 #include <exception>
+#include <iterator>
 #include <memory>
 #include <new>
+#include <utility>
 #include <vector>
 
 #include "../../include/mg.h"
@@ -401,6 +403,8 @@ struct mg_grad_list {
   size_t partial_off = 0, sync_off = 0;
   int sms = 0;
   bool fused = false;   // all chunks resident at once: one launch
+  // the tensors' memory: begins in ascending order, and the largest end up to each
+  std::vector<std::pair<uintptr_t, uintptr_t>> memory;
   unsigned spin = mg::kClipSpin;
 };
 
@@ -457,6 +461,8 @@ extern "C" mg_status mg_grad_list_create(int n, const void* const* grads, void* 
       if (s.written && s.hi > whi) { whi = s.hi; wt = s.tensor; }
     }
     std::unique_ptr<mg_grad_list> l(new mg_grad_list());
+    for (const Span& s : spans)
+      l->memory.emplace_back(s.lo, std::max(s.hi, l->memory.empty() ? 0 : l->memory.back().second));
     l->n_chunks = (int)table.size();
     cudaError_t e = cudaGetDevice(&l->device);
     int coop = 0, per_sm = 0;
@@ -513,6 +519,10 @@ extern "C" mg_status mg_grad_list_clip(mg_grad_list* l, float max_norm, float* s
     return op_fail(MG_ERR_INVALID_ARG, "%s: the list belongs to device %d but device %d is current", fn, l->device, dev);
   mg_status st = mg::op_begin(fn, {{stats, 8}});
   if (st != MG_OK) return st;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(stats);
+  const auto behind = std::lower_bound(l->memory.begin(), l->memory.end(), std::make_pair(at + 8, (uintptr_t)0));
+  if (behind != l->memory.begin() && std::prev(behind)->second > at)
+    return op_fail(MG_ERR_INVALID_ARG, "%s: stats lies in a tensor of the list", fn);
   cudaStream_t s = (cudaStream_t)stream;
   const auto* chunks = reinterpret_cast<const mg::ClipChunk*>(l->ws);
   mg::ClipSync* sync = reinterpret_cast<mg::ClipSync*>(l->ws + l->sync_off);
