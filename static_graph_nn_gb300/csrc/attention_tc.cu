@@ -495,6 +495,8 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
     }
     if (!ok) fail_wait(A.err, abort_flag);
   }
+  if (*abort_flag) drain_in_flight();
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (warp == 9) {
@@ -807,6 +809,8 @@ __global__ void __launch_bounds__(DKV_THREADS, 1)
     }
     if (!ok) fail_wait(A.err, abort_flag);
   }
+  if (*abort_flag) drain_in_flight();
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (warp == 16) {
@@ -1047,6 +1051,8 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
     }
     if (!ok) fail_wait(A.err, abort_flag);
   }
+  if (*abort_flag) drain_in_flight();
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (warp == 16) {

@@ -370,6 +370,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     }
   }
 
+  if (*abort_flag) drain_in_flight();
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {

@@ -246,6 +246,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1)
     }
   }
 
+  if (*abort_flag) drain_in_flight();
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   cluster_sync();                      // no remote arrive or MMA still targets either CTA
