@@ -441,6 +441,117 @@ mg_status mg_grad_list_create(int n, const void* const* grads, void* const* out,
 void mg_grad_list_destroy(mg_grad_list* list);
 mg_status mg_grad_list_clip(mg_grad_list* list, float max_norm, float* stats, mg_stream_t stream);
 
+/* ---- log probabilities of tokens --------------------------------------------
+ * Over each row x of logits [rows, vocab] (rows row_stride >= vocab elements
+ * apart; pointers aligned to their element), with p = softmax(x / temperature):
+ *   logp[r]     = log p[ids[r]]
+ *   entropy[r]  = -sum_v p_v log p_v
+ *   top_ids, top_logp [rows, k]: the k most likely tokens, most likely first, of
+ *     equal ones the lowest first, and their log probabilities
+ *   stats[r]    = {max x, log sum_v exp((x_v - max x) / temperature)}, for the
+ *     backward
+ * Each output may be NULL, but one (ids and logp are given together; k = 0: no
+ * top_ids and top_logp).  k is at most MG_MAX_TOP and vocab.  fp32 sums; outputs
+ * are fp32 and int32.
+ * A row whose id is outside [0, vocab) -- padding -- is not read: its outputs are
+ * 0, its top_ids -1.  Logits of -inf have probability 0; a row of nothing else
+ * has logp and top_logp -inf, entropy 0 and no gradient.  A row that holds a NaN
+ * or +inf has NaN in logp, entropy and top_logp (its top_ids are in order, NaN
+ * below -inf).
+ *
+ * backward: dlogits[r, v] = (dlogp[r] ([v = ids[r]] - p_v)
+ *                            - dentropy[r] p_v (log p_v + entropy[r])) / temperature
+ * with p from stats; dlogits has the logits' type and may be the logits
+ * themselves (same rows).  dlogp or dentropy may be NULL (no such gradient: ids,
+ * entropy are then not needed).  Rows of padding, and rows whose dlogp and
+ * dentropy are 0, are not read and get zeros.  Columns beyond vocab are neither
+ * read nor written. */
+#define MG_MAX_TOP 32
+mg_status mg_token_logprobs(int dtype, const void* logits, long long rows, int vocab,
+                            long long row_stride, int id_kind, const void* ids, float temperature,
+                            float* logp, float* stats, float* entropy, int k, int* top_ids,
+                            float* top_logp, mg_stream_t stream);
+mg_status mg_token_logprobs_backward(int dtype, const void* logits, long long rows, int vocab,
+                                     long long row_stride, int id_kind, const void* ids,
+                                     float temperature, const float* stats, const float* entropy,
+                                     const float* dlogp, const float* dentropy, void* dlogits,
+                                     long long dlogits_stride, mg_stream_t stream);
+
+/* ---- between two blocks of a residual network --------------------------------
+ * From a block's output y and the residual stream x [rows, dim]:
+ *   u     = y / sqrt(mean(y^2) + eps) * gamma_post     (u = y where gamma_post is NULL)
+ *   x_out = scale x + gate * u                         (x_out = scale x + u where gate is NULL)
+ *   h     = x_out / sqrt(mean(x_out^2) + eps) * gamma_pre   (not without h and gamma_pre)
+ * gate [gates, dim]: each row of it for rows / gates consecutive rows (1: one
+ * for all; rows: one each); gates = 0 without one.  dtype is the type of y, x,
+ * x_out, h and their gradients; gammas, gate, their gradients and rstd [rows, 2]
+ * (1 / sqrt of the two means, 1 where there is no norm; for the backward, may be
+ * NULL) are fp32.  h is computed from x_out before its rounding.  Sums of squares
+ * are fp32: finite within +-1e19 / sqrt(dim).
+ * x_out and h may each be y or x itself.
+ *
+ * backward, from dx_out and dh (either may be NULL, for none) and the forward's
+ * inputs: dy, dx, and, where not NULL, dgamma_post, dgamma_pre [dim] and dgate
+ * [gates, dim], fp32 sums in a fixed order (the same bits in every run).  dy and
+ * dx may each be dx_out, dh, y or x itself.  workspace:
+ * mg_norm_residual_workspace_bytes (0 for arguments the call would refuse); its
+ * contents before the call do not matter. */
+size_t mg_norm_residual_workspace_bytes(int rows, int dim, int gates);
+mg_status mg_norm_residual_forward(int dtype, const void* y, const void* x, int rows, int dim,
+                                   const float* gamma_post, const float* gate, int gates,
+                                   float scale, const float* gamma_pre, float eps, void* x_out,
+                                   void* h, float* rstd, mg_stream_t stream);
+mg_status mg_norm_residual_backward(int dtype, const void* dx_out, const void* dh, const void* y,
+                                    const void* x, const float* rstd, int rows, int dim,
+                                    const float* gamma_post, const float* gate, int gates,
+                                    float scale, const float* gamma_pre, void* dy, void* dx,
+                                    float* dgamma_post, float* dgate, float* dgamma_pre,
+                                    void* workspace, size_t workspace_bytes, mg_stream_t stream);
+
+/* ---- AdamW over many tensors ---------------------------------------------------
+ * One step of every tensor of a list, with decoupled weight decay:
+ *   g' = c grad;  m = beta1 m + (1 - beta1) g';  v = beta2 v + (1 - beta2) g'^2
+ *   param = param (1 - lr weight_decay)
+ *           - lr / (1 - beta1^step) m / (sqrt(v / (1 - beta2^step)) + eps)
+ * c = max_norm / norm[0] if norm[0] > max_norm, else 1; norm (device memory, may
+ * be NULL: c = 1) is what mg_grad_list_clip with max_norm = INFINITY measures.
+ * Where norm[0] is not finite the step changes nothing.
+ * state_bits 32: m and v are fp32 [count].  state_bits 8: m and v are bytes
+ * [count], the e4m3 codes of m and of sqrt(v), and m_scales, v_scales fp32
+ * [ceil(count / 256)] the power of two that every 256 of them are multiplied by:
+ * the least that keeps their largest magnitude at or below 446.72.  Zeros are
+ * valid states.  Codes are rounded up or down at random with the probability of
+ * the distance; the random bits depend on seed, step and the element's place in
+ * the list alone, so that runs repeat bit for bit.  A moment that is not finite
+ * becomes NaN.
+ * param is fp32 or bf16 (rounded to nearest), grad fp32 or bf16, copy (NULL, or
+ * bf16 [count]) receives the rounded new parameters.  Pointers are aligned to
+ * their element.  Memory that is written may not overlap any other of the list.
+ * Creation copies the table to the device (88 bytes per 8192 elements) and is
+ * bound to the current device; the list keeps no state of its own.
+ * lr_device, step_device (device memory, fp32 and int32; NULL: lr and step are
+ * taken) are read by the kernel, so that a captured step can be replayed with
+ * new values; a step_device below 1 counts as 1. */
+typedef struct {
+  void* param;
+  const void* grad;
+  void* m;
+  void* v;
+  float* m_scales;    /* state_bits 8 */
+  float* v_scales;
+  void* copy;
+  size_t count;       /* 0 is allowed */
+  int param_dtype, grad_dtype;
+  float weight_decay;
+} mg_adamw_tensor;
+typedef struct mg_adamw mg_adamw;
+mg_status mg_adamw_create(int n, const mg_adamw_tensor* tensors, int state_bits, double beta1,
+                          double beta2, double eps, unsigned long long seed, mg_adamw** opt);
+void mg_adamw_destroy(mg_adamw* opt);
+mg_status mg_adamw_step(mg_adamw* opt, double lr, long long step, const float* lr_device,
+                        const int* step_device, const float* norm, float max_norm,
+                        mg_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

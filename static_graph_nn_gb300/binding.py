@@ -39,6 +39,12 @@ class mg_graph_desc(ctypes.Structure):
                 ("beta1", ctypes.c_float), ("beta2", ctypes.c_float), ("adam_eps", ctypes.c_float)]
 
 
+class mg_adamw_tensor(ctypes.Structure):
+    _fields_ = ([(f, ctypes.c_void_p) for f in ("param", "grad", "m", "v", "m_scales", "v_scales", "copy")]
+                + [("count", ctypes.c_size_t), ("param_dtype", ctypes.c_int), ("grad_dtype", ctypes.c_int),
+                   ("weight_decay", ctypes.c_float)])
+
+
 _P = ctypes.c_void_p
 _SIGS = {
     "mg_step_plan_create": (ctypes.c_int, [ctypes.POINTER(mg_graph_desc), ctypes.POINTER(_P)]),
@@ -100,6 +106,21 @@ _SIGS = {
                                            ctypes.POINTER(ctypes.c_int), ctypes.POINTER(_P)]),
     "mg_grad_list_destroy": (None, [_P]),
     "mg_grad_list_clip": (ctypes.c_int, [_P, ctypes.c_float, _P, _P]),
+    "mg_token_logprobs": (ctypes.c_int, [ctypes.c_int, _P, ctypes.c_longlong, ctypes.c_int, ctypes.c_longlong,
+                                         ctypes.c_int, _P, ctypes.c_float, _P, _P, _P, ctypes.c_int, _P, _P, _P]),
+    "mg_token_logprobs_backward": (ctypes.c_int, [ctypes.c_int, _P, ctypes.c_longlong, ctypes.c_int,
+                                                  ctypes.c_longlong, ctypes.c_int, _P, ctypes.c_float, _P, _P, _P,
+                                                  _P, _P, ctypes.c_longlong, _P]),
+    "mg_norm_residual_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int] * 3),
+    "mg_norm_residual_forward": (ctypes.c_int, [ctypes.c_int, _P, _P, ctypes.c_int, ctypes.c_int, _P, _P,
+                                                ctypes.c_int, ctypes.c_float, _P, ctypes.c_float, _P, _P, _P, _P]),
+    "mg_norm_residual_backward": (ctypes.c_int, [ctypes.c_int] + [_P] * 5 + [ctypes.c_int] * 2
+                                  + [_P, _P, ctypes.c_int, ctypes.c_float] + [_P] * 7 + [ctypes.c_size_t, _P]),
+    "mg_adamw_create": (ctypes.c_int, [ctypes.c_int, ctypes.POINTER(mg_adamw_tensor), ctypes.c_int,
+                                       ctypes.c_double, ctypes.c_double, ctypes.c_double, ctypes.c_ulonglong,
+                                       ctypes.POINTER(_P)]),
+    "mg_adamw_destroy": (None, [_P]),
+    "mg_adamw_step": (ctypes.c_int, [_P, ctypes.c_double, ctypes.c_longlong, _P, _P, _P, ctypes.c_float, _P]),
 }
 
 _lib = None
@@ -565,6 +586,267 @@ class GradList:
     def close(self):
         if getattr(self, "h", None):
             self.lib.mg_grad_list_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+# ---- log probabilities of tokens ------------------------------------------------
+def _logit_rows(t, name: str) -> tuple[int, int, int]:
+    """(rows, vocab, row stride) of logits [..., vocab]: any row stride for two
+    dimensions, contiguous otherwise."""
+    if t.dim() < 1 or t.shape[-1] < 1:
+        _refuse(f"{name} must be [..., vocab]", MG_ERR_SHAPE)
+    v = t.shape[-1]
+    _fits(v)
+    if t.is_contiguous():
+        return t.numel() // v, v, v
+    if t.dim() != 2 or t.stride(1) != 1 or t.stride(0) < v:
+        _refuse(f"{name} must be contiguous or rows of contiguous logits (strides {tuple(t.stride())})")
+    return t.shape[0], v, t.stride(0)
+
+
+def _per_row(t, name: str, shape: tuple, dtype=None):
+    if t.dtype != (dtype or _type_tables()[2]):
+        _refuse(f"{name} must be {dtype or _type_tables()[2]}, not {t.dtype}")
+    _dense(t, name, shape)
+
+
+def token_logprobs(logits, ids=None, logp=None, stats=None, entropy=None, top_ids=None, top_logp=None,
+                   temperature: float = 1.0, stream=None):
+    """logp[r] = log softmax(logits[r] / temperature)[ids[r]], with the entropy of each
+    row and its most likely tokens (of equal ones the lowest first).
+
+    logits [..., vocab] fp32 or bf16 (of two dimensions with any row stride); for
+    rows [...]: ids int32 or int64, logp and entropy fp32 [...], stats fp32 [..., 2]
+    (for the backward), top_ids int32 and top_logp fp32 [..., k], k up to 32.  Any
+    of them may be left out, ids together with logp.  A row whose id is outside
+    [0, vocab) is not read: zeros, top_ids -1."""
+    rows, v, ld = _logit_rows(logits, "logits")
+    lead = logits.shape[:-1]
+    kind, k = 0, 0
+    if ids is not None:
+        kind = _code(ids, "ids", _type_tables()[1])
+        _dense(ids, "ids", lead)
+    if logp is not None:
+        _per_row(logp, "logp", lead)
+    if entropy is not None:
+        _per_row(entropy, "entropy", lead)
+    if stats is not None:
+        _per_row(stats, "stats", lead + (2,))
+    if (top_ids is None) != (top_logp is None):
+        _refuse("top_ids and top_logp are given together")
+    if top_ids is not None:
+        k = top_ids.shape[-1] if top_ids.dim() else 0
+        _fits(k)
+        _per_row(top_ids, "top_ids", lead + (k,), _type_tables()[3])
+        _per_row(top_logp, "top_logp", lead + (k,))
+    _status(load().mg_token_logprobs(_code(logits, "logits"), _ptr(logits), rows, v, ld, kind, _ptr(ids), temperature,
+                                     _ptr(logp), _ptr(stats), _ptr(entropy), k, _ptr(top_ids), _ptr(top_logp),
+                                     _stream(stream)))
+
+
+def token_logprobs_backward(logits, ids, stats, dlogp, dlogits, entropy=None, dentropy=None,
+                            temperature: float = 1.0, stream=None):
+    """dlogits from dlogp and dentropy (either may be None; dentropy needs the
+    forward's entropy), with the forward's stats and temperature.  dlogits has the
+    logits' shape and type, a row stride of its own, and may be the logits
+    themselves.  Rows of padding, and rows without a gradient, get zeros."""
+    rows, v, ld = _logit_rows(logits, "logits")
+    lead = logits.shape[:-1]
+    if dlogits.shape != logits.shape:
+        _refuse(f"dlogits has shape {tuple(dlogits.shape)}, expected {tuple(logits.shape)}", MG_ERR_SHAPE)
+    _same_type(logits, "logits", dlogits, "dlogits")
+    ldd = _logit_rows(dlogits, "dlogits")[2]
+    kind = 0
+    if ids is not None:
+        kind = _code(ids, "ids", _type_tables()[1])
+        _dense(ids, "ids", lead)
+    _per_row(stats, "stats", lead + (2,))
+    for t, name in ((entropy, "entropy"), (dlogp, "dlogp"), (dentropy, "dentropy")):
+        if t is not None:
+            _per_row(t, name, lead)
+    _status(load().mg_token_logprobs_backward(_code(logits, "logits"), _ptr(logits), rows, v, ld, kind, _ptr(ids),
+                                              temperature, _ptr(stats), _ptr(entropy), _ptr(dlogp), _ptr(dentropy),
+                                              _ptr(dlogits), ldd, _stream(stream)))
+
+
+# ---- between two blocks of a residual network ------------------------------------
+def norm_residual_workspace_bytes(rows: int, dim: int, gates: int = 0) -> int:
+    """Bytes of workspace that norm_residual_backward needs (0: refused sizes)."""
+    if max(rows, dim, gates) > _INT_MAX:
+        return 0
+    return load().mg_norm_residual_workspace_bytes(rows, dim, gates)
+
+
+def _residual_args(x, gate, vectors):
+    """(rows, dim, gates) of [..., dim] and its fp32 vectors."""
+    if x.dim() < 1 or x.shape[-1] < 1:
+        _refuse("x must be [..., dim]", MG_ERR_SHAPE)
+    d = x.shape[-1]
+    rows = x.numel() // d
+    _fits(rows, d)
+    for t, name in vectors:
+        if t is not None:
+            _per_row(t, name, (d,))
+    gates = 0
+    if gate is not None:
+        gates = 1 if gate.dim() == 1 else gate.shape[0]
+        _fits(gates)
+        _per_row(gate, "gate", (d,) if gate.dim() == 1 else (gates, d))
+    return rows, d, gates
+
+
+def _rows_like(x, tensors):
+    _dense(x, "x")
+    for t, name in tensors:
+        if t is not None:
+            _dense(t, name, x.shape)
+            _same_type(x, "x", t, name)
+
+
+def norm_residual_forward(y, x, x_out, h=None, gamma_post=None, gate=None, gamma_pre=None, scale: float = 1.0,
+                          eps: float = 1e-6, rstd=None, stream=None):
+    """x_out = scale * x + gate * rmsnorm(y) * gamma_post, h = rmsnorm(x_out) * gamma_pre.
+
+    y, x, x_out, h [..., dim], all fp32 or all bf16; gammas fp32 [dim]; gate fp32
+    [dim] or [gates, dim], each row of it for an equal run of rows.  Without
+    gamma_post y is added as it is, without gate it is not scaled, and without h
+    and gamma_pre there is no second norm.  rstd fp32 [..., 2] is for the backward.
+    x_out and h may each be y or x."""
+    rows, d, gates = _residual_args(x, gate, ((gamma_post, "gamma_post"), (gamma_pre, "gamma_pre")))
+    _rows_like(x, ((y, "y"), (x_out, "x_out"), (h, "h")))
+    if rstd is not None:
+        _per_row(rstd, "rstd", x.shape[:-1] + (2,))
+    _status(load().mg_norm_residual_forward(_code(x, "x"), _ptr(y), _ptr(x), rows, d, _ptr(gamma_post), _ptr(gate),
+                                            gates, scale, _ptr(gamma_pre), eps, _ptr(x_out), _ptr(h), _ptr(rstd),
+                                            _stream(stream)))
+
+
+def norm_residual_backward(dx_out, dh, y, x, rstd, dy, dx, workspace, gamma_post=None, gate=None, gamma_pre=None,
+                           dgamma_post=None, dgate=None, dgamma_pre=None, scale: float = 1.0, stream=None):
+    """Gradients of norm_residual_forward: dy, dx and, where given, dgamma_post,
+    dgamma_pre [dim] and dgate (fp32; of the gate's shape), from dx_out and dh (either
+    may be None), the forward's inputs and its rstd.  workspace: a byte tensor of
+    norm_residual_workspace_bytes.  dy and dx may each be dx_out, dh, y or x."""
+    rows, d, gates = _residual_args(x, gate, ((gamma_post, "gamma_post"), (gamma_pre, "gamma_pre"),
+                                              (dgamma_post, "dgamma_post"), (dgamma_pre, "dgamma_pre")))
+    _rows_like(x, ((dx_out, "dx_out"), (dh, "dh"), (y, "y"), (dy, "dy"), (dx, "dx")))
+    _per_row(rstd, "rstd", x.shape[:-1] + (2,))
+    if dgate is not None:
+        if gate is None:
+            _refuse("dgate without a gate")
+        _per_row(dgate, "dgate", tuple(gate.shape))
+    _dense(workspace, "workspace")
+    _status(load().mg_norm_residual_backward(_code(x, "x"), _ptr(dx_out), _ptr(dh), _ptr(y), _ptr(x), _ptr(rstd), rows,
+                                             d, _ptr(gamma_post), _ptr(gate), gates, scale, _ptr(gamma_pre), _ptr(dy),
+                                             _ptr(dx), _ptr(dgamma_post), _ptr(dgate), _ptr(dgamma_pre),
+                                             _ptr(workspace), workspace.nbytes, _stream(stream)))
+
+
+# ---- AdamW over many tensors -------------------------------------------------------
+ADAMW_BLOCK = 256     # elements of a tensor under one scale of its 8-bit moments
+
+
+def adamw_state(params, bits: int = 32):
+    """Zeroed moments of the parameters: (m, v, m_scales, v_scales), fp32 with None
+    for the scales, or float8_e4m3fn codes (of m and of sqrt(v)) with fp32 scales."""
+    import torch
+    if bits not in (8, 32):
+        _refuse(f"bits must be 8 or 32, not {bits}")
+    t = torch.float32 if bits == 32 else torch.float8_e4m3fn
+    m, v = ([torch.zeros(p.shape, dtype=t, device=p.device) for p in params] for _ in range(2))
+    if bits == 32:
+        return m, v, None, None
+    ms, vs = ([torch.zeros(-(-p.numel() // ADAMW_BLOCK), device=p.device) for p in params] for _ in range(2))
+    return m, v, ms, vs
+
+
+class AdamW:
+    """AdamW steps over many parameter tensors (fp32 or bf16, contiguous) in one
+    launch, in place.
+
+    grads: fp32 or bf16 tensors of the same shapes.  m, v: fp32 moments, or 8-bit
+    ones (float8_e4m3fn or uint8 codes of m and of sqrt(v)) with m_scales and
+    v_scales fp32 [ceil(n / 256)] (see adamw_state).  copies: bf16 tensors that
+    receive the new parameters (or None among them).  weight_decay: a number, or one
+    for each tensor.  Keeps the tensors alive; the table lives on the device until
+    close()."""
+
+    def __init__(self, params, grads, m, v, m_scales=None, v_scales=None, copies=None, betas=(0.9, 0.999),
+                 eps: float = 1e-8, weight_decay=0.01, seed: int = 0):
+        import torch
+        self.h = None
+        self.lib = load()
+        params = list(params)
+        n = len(params)
+        lists = {"grads": grads, "m": m, "v": v, "m_scales": m_scales, "v_scales": v_scales, "copies": copies}
+        lists = {k: [None] * n if t is None else list(t) for k, t in lists.items()}
+        for k, t in lists.items():
+            if len(t) != n:
+                _refuse(f"{n} parameters but {len(t)} {k}")
+        decay = [float(weight_decay)] * n if isinstance(weight_decay, (int, float)) else [float(w) for w in weight_decay]
+        if len(decay) != n:
+            _refuse(f"{n} parameters but {len(decay)} weight decays")
+        codes = (torch.float8_e4m3fn, torch.uint8)
+        bits = 8 if n and lists["m"][0] is not None and lists["m"][0].dtype in codes else 32
+        if not 0 <= seed < 2 ** 64:
+            _refuse("seed must lie in [0, 2^64)")
+        arr = (mg_adamw_tensor * max(1, n))()
+        for i, p in enumerate(params):
+            _dense(p, f"parameter {i}")
+            a = arr[i]
+            a.param, a.count, a.param_dtype, a.weight_decay = _ptr(p), p.numel(), _code(p, f"parameter {i}"), decay[i]
+            g = lists["grads"][i]
+            if g is None:
+                _refuse(f"gradient {i} is missing")
+            _dense(g, f"gradient {i}", p.shape)
+            a.grad, a.grad_dtype = _ptr(g), _code(g, f"gradient {i}")
+            for k in ("m", "v"):
+                t = lists[k][i]
+                if t is None or (t.dtype not in codes if bits == 8 else t.dtype != torch.float32):
+                    _refuse(f"{k} {i} must be {'8-bit codes' if bits == 8 else 'float32'}, as the first is")
+                _dense(t, f"{k} {i}", p.shape)
+                setattr(a, k, _ptr(t))
+                s = lists[k + "_scales"][i]
+                if (s is None) != (bits == 32):
+                    _refuse(f"{k}_scales belong to 8-bit moments")
+                if s is not None:
+                    _per_row(s, f"{k}_scales {i}", (-(-p.numel() // ADAMW_BLOCK),))
+                    setattr(a, k + "_scales", _ptr(s))
+            c = lists["copies"][i]
+            if c is not None:
+                _per_row(c, f"copy {i}", p.shape, torch.bfloat16)
+                a.copy = _ptr(c)
+        h = _P()
+        _status(self.lib.mg_adamw_create(n, arr, bits, betas[0], betas[1], eps, seed, ctypes.byref(h)))
+        self.h, self.tensors = h, (params, lists)
+
+    def step(self, lr, step, norm=None, max_norm: float = float("inf"), stream=None):
+        """One step.  lr: a number, or an fp32 tensor of one value on the device; step
+        (from 1): a number, or an int32 tensor of one value on the device.  norm: fp32 on
+        the device, its first value the gradients' global norm (GradList.clip(inf, stats)):
+        they are taken times max_norm / norm where that is below 1, and nothing changes
+        where it is not finite."""
+        lr_dev = step_dev = None
+        if not isinstance(lr, (int, float)):
+            lr_dev, lr = lr, 0.0
+            _per_row(lr_dev, "lr", lr_dev.shape if lr_dev.numel() == 1 else (1,))
+        if not isinstance(step, int):
+            step_dev, step = step, 1
+            _per_row(step_dev, "step", step_dev.shape if step_dev.numel() == 1 else (1,), _type_tables()[3])
+        if norm is not None and (norm.dtype != _type_tables()[2] or norm.numel() < 1):
+            _refuse("norm must be float32 with one value at least")
+        _status(self.lib.mg_adamw_step(self.h, lr, step, _ptr(lr_dev), _ptr(step_dev), _ptr(norm), max_norm,
+                                       _stream(stream)))
+
+    def close(self):
+        if getattr(self, "h", None):
+            self.lib.mg_adamw_destroy(self.h)
             self.h = None
 
     def __del__(self):

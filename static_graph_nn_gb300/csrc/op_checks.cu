@@ -50,6 +50,22 @@ mg_status op_begin(const char* fn, std::initializer_list<OpPtr> ptrs) {
   return MG_OK;
 }
 
+mg_status op_disjoint(const char* fn, std::initializer_list<OpRange> ranges) {
+  for (const OpRange* a = ranges.begin(); a != ranges.end(); ++a) {
+    if (!a->written || !a->p || !a->bytes) continue;
+    const uintptr_t al = reinterpret_cast<uintptr_t>(a->p), ah = al + a->bytes;
+    for (const OpRange* b = ranges.begin(); b != ranges.end(); ++b) {
+      if (b == a || !b->p || !b->bytes) continue;
+      const uintptr_t bl = reinterpret_cast<uintptr_t>(b->p), bh = bl + b->bytes;
+      if (ah <= bl || bh <= al) continue;
+      if (a->inplace && !b->written && al == bl && ah == bh) continue;
+      return op_fail(MG_ERR_INVALID_ARG, "%s: arguments %d and %d overlap in memory that is written", fn,
+                     (int)(a - ranges.begin()), (int)(b - ranges.begin()));
+    }
+  }
+  return MG_OK;
+}
+
 mg_status op_end(const char* fn, cudaError_t e) {
   if (e == cudaSuccess) return MG_OK;
   cudaGetLastError();

@@ -24,6 +24,18 @@ mg_status op_fail(mg_status st, const char* fmt, ...);
 // is pending on this thread.
 mg_status op_begin(const char* fn, std::initializer_list<OpPtr> ptrs);
 
+// A range of memory that a call reads or writes; NULL or no bytes: none.
+struct OpRange {
+  const void* p;
+  size_t bytes;
+  bool written;
+  bool inplace;   // an output that may be exactly one of the ranges it is computed from (begin and length)
+};
+
+// A written range may meet no other one, except that an in-place output may be
+// exactly one range that is only read.
+mg_status op_disjoint(const char* fn, std::initializer_list<OpRange> ranges);
+
 // The status of a call whose launches returned e.
 mg_status op_end(const char* fn, cudaError_t e);
 
