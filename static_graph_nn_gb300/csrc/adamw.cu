@@ -29,6 +29,8 @@
 #include <memory>
 #include <vector>
 
+#include <cuda_fp16.h>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "op_checks.h"
@@ -36,9 +38,10 @@
 namespace mg {
 namespace {
 
-constexpr int kAdamwBlock = 256;       // elements under a scale
+constexpr int kAdamwBlock = 256;       // elements under a scale: eight for each lane of a warp
 constexpr int kAdamwThreads = 256;
-constexpr int kAdamwChunk = 8192;      // elements of one tensor that a block updates
+constexpr int kAdamwPass = kAdamwThreads * 8;   // elements that a block updates at once
+constexpr int kAdamwChunk = 8 * kAdamwPass;     // of one tensor that it updates in all, in long lists
 
 struct AdamwChunk {
   void* p;
@@ -50,13 +53,14 @@ struct AdamwChunk {
   void* copy;
   unsigned long long place;   // of the chunk's first element in the list
   int len;
-  int flags;                  // bit 0: p bf16, bit 1: g bf16
+  int flags;                  // bit 0: p bf16, bit 1: g bf16, bit 2: eight elements of each allow one access
   float wd;
 };
 
 struct AdamwStep {
   const AdamwChunk* chunks;
   float b1, om1, b2, om2, ln_b1, ln_b2, eps;
+  float one;                           // 1, unknown to the compiler
   float lr, step_size, inv_root_bc2;   // from the host's lr and t
   const float* lr_dev;
   const int* step_dev;
@@ -71,9 +75,10 @@ __host__ __device__ __forceinline__ unsigned long long mix64(unsigned long long 
   return z ^ (z >> 31);
 }
 
-// Four elements' random bits; place a multiple of 4.
-__device__ __forceinline__ unsigned long long adamw_random(unsigned long long key, unsigned long long place) {
-  return mix64(key + (place / 4 + 1) * 0x9E3779B97F4A7C15ull);
+// Four elements' random bits are mix64 of this, place a multiple of 4.
+constexpr unsigned long long kWeyl = 0x9E3779B97F4A7C15ull;
+__device__ __forceinline__ unsigned long long random_state(unsigned long long key, unsigned long long place) {
+  return key + (place / 4 + 1) * kWeyl;
 }
 
 // The scale of a block whose largest magnitude has these bits, and its reciprocal.
@@ -85,15 +90,52 @@ __device__ __forceinline__ float reciprocal_of(float scale) {
   return __uint_as_float((254u << 23) - __float_as_uint(scale));
 }
 
-// e4m3 bits shifted to fp32's place are the value times 2^-120, subnormals too.
-__device__ __forceinline__ float e4m3_value(uint32_t code) {
-  if ((code & 0x7f) == 0x7f) return __int_as_float(0x7fffffff);
-  return __uint_as_float((code & 0x7f) << 20 | (code & 0x80) << 24) * 0x1p120f;
+// Two e4m3 codes' values (NaN for its code).
+__device__ __forceinline__ float2 e4m3_values(uint32_t two) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)two));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
-// |x| is at most 448; rnd: 16 random bits.  What is not finite becomes NaN.
-__device__ __forceinline__ uint32_t e4m3_code(float x, uint32_t rnd) {
-  const uint32_t b = __float_as_uint(x * 0x1p-120f);
-  return min(((b & 0x7fffffffu) + (rnd << 4)) >> 20, 0x7fu) | (b >> 31) << 7;
+
+// Two fp32 values in one register pair, an operation on both in one issue slot;
+// each rounds as the single operation does.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 both(float x, float y) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ f32x2 both(float x) { return both(x, x); }
+__device__ __forceinline__ float2 parts(f32x2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// The larger of three magnitudes; NaN if one is.
+__device__ __forceinline__ float max_abs3(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)), "f"(fabsf(c)));
+  return r;
+}
+__device__ __forceinline__ float rsqrt_near(float x) {
+  float r;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float reciprocal_near(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 
 struct AdamwScalars {
@@ -120,65 +162,404 @@ __device__ __forceinline__ AdamwScalars adamw_scalars(const AdamwStep& a) {
   return s;
 }
 
-__device__ __forceinline__ void adamw_moments(const AdamwStep& a, float g, float& m, float& v) {
-  m = __fadd_rn(__fmul_rn(m, a.b1), __fmul_rn(g, a.om1));
-  v = __fadd_rn(__fmul_rn(v, a.b2), __fmul_rn(__fmul_rn(g, g), a.om2));
+// Eight elements of a lane: neighbours in one access where the chunk allows it
+// (VEC), else 32 apart; n of them (VEC) or those below len exist.
+template <bool VEC>
+__device__ __forceinline__ int element(int i0, int j) {
+  return VEC ? i0 + j : i0 + 32 * j;
 }
-__device__ __forceinline__ float adamw_param(const AdamwScalars& s, float eps, float wd, float p, float m, float root) {
-  return p * (1.0f - s.lr * wd) - s.step_size * m / (root * s.inv_root_bc2 + eps);
+__device__ __forceinline__ void ld8f32(const float* p, float (&f)[8]) {
+  uint32_t w[8];
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p));
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(w[j]);
+}
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
+    w[j] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <bool VEC>
+__device__ __forceinline__ void load8(const void* p, bool narrow, int i0, int len, f32x2 (&o)[4]) {
+  float f[8];
+  if (VEC && i0 + 8 <= len) {
+    if (narrow) {
+      const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const bf16*>(p) + i0);
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        f[2 * j] = __uint_as_float(w[j] << 16);
+        f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+      }
+    } else {
+      ld8f32(static_cast<const float*>(p) + i0, f);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int i = element<VEC>(i0, j);
+      f[j] = i >= len ? 0.0f : narrow ? ld_elem(static_cast<const bf16*>(p), i) : ld_elem(static_cast<const float*>(p), i);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) o[j] = both(f[2 * j], f[2 * j + 1]);
+}
+template <bool VEC>
+__device__ __forceinline__ void store8(void* p, bool narrow, int i0, int len, const f32x2 (&o)[4]) {
+  float f[8];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 t = parts(o[j]);
+    f[2 * j] = t.x;
+    f[2 * j + 1] = t.y;
+  }
+  if (VEC && i0 + 8 <= len) {
+    if (narrow)
+      *reinterpret_cast<uint4*>(static_cast<bf16*>(p) + i0) = pack8(f);
+    else
+      st8f32(static_cast<float*>(p) + i0, f);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int i = element<VEC>(i0, j);
+    if (i >= len) continue;
+    if (narrow)
+      st_elem(static_cast<bf16*>(p), i, f[j]);
+    else
+      st_elem(static_cast<float*>(p), i, f[j]);
+  }
+}
+// Eight codes in two words.
+template <bool VEC>
+__device__ __forceinline__ uint2 load_codes(const uint8_t* p, int i0, int len) {
+  if (VEC && i0 + 8 <= len) return *reinterpret_cast<const uint2*>(p + i0);
+  uint32_t w[2] = {0, 0};
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int i = element<VEC>(i0, j);
+    if (i < len) w[j / 4] |= (uint32_t)p[i] << (8 * (j % 4));
+  }
+  return make_uint2(w[0], w[1]);
+}
+template <bool VEC>
+__device__ __forceinline__ void store_codes(uint8_t* p, int i0, int len, uint2 c) {
+  if (VEC && i0 + 8 <= len) {
+    *reinterpret_cast<uint2*>(p + i0) = c;
+    return;
+  }
+  const uint32_t w[2] = {c.x, c.y};
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int i = element<VEC>(i0, j);
+    if (i < len) p[i] = (uint8_t)(w[j / 4] >> (8 * (j % 4)));
+  }
+}
+// The moments and the root, eight elements of a lane.  Products with a scale, a
+// power of two, round nowhere, so a scale goes into the factor that follows it
+// (wide: not where that would leave the normal range).
+__device__ __forceinline__ void moments8(const AdamwStep& a, float c, const f32x2 (&g)[4], f32x2 (&m)[4], f32x2 (&v)[4]) {
+  // the sums as products with 1: the compiler makes one operation, with one
+  // rounding, of a product and a sum
+  const f32x2 cc = both(c), o1 = both(a.om1), o2 = both(a.om2), one = both(a.one);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const f32x2 t = mul2(g[j], cc);
+    m[j] = fma2(m[j], one, mul2(t, o1));
+    v[j] = fma2(v[j], one, mul2(mul2(t, t), o2));
+  }
+}
+__device__ __forceinline__ void scaled_moments(const AdamwStep& a, f32x2 (&m)[4], f32x2 (&v)[4]) {
+  const f32x2 b1 = both(a.b1), b2 = both(a.b2);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    m[j] = mul2(m[j], b1);
+    v[j] = mul2(v[j], b2);
+  }
+}
+// beta1 m and beta2 v from their codes.
+__device__ __forceinline__ void decode8(const AdamwStep& a, uint2 mc, uint2 vc, float ms, float vs, f32x2 (&m)[4], f32x2 (&v)[4]) {
+  const uint32_t mt[4] = {mc.x & 0xffffu, mc.x >> 16, mc.y & 0xffffu, mc.y >> 16};
+  const uint32_t vt[4] = {vc.x & 0xffffu, vc.x >> 16, vc.y & 0xffffu, vc.y >> 16};
+  const bool wide = (ms == 0.0f || (ms >= 0x1p-100f && ms <= 0x1p100f)) && (vs == 0.0f || (vs >= 0x1p-40f && vs <= 0x1p40f));
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 x = e4m3_values(mt[j]), y = e4m3_values(vt[j]);
+    m[j] = both(x.x, x.y);
+    v[j] = both(y.x, y.y);
+  }
+  if (wide) {
+    const f32x2 fm = both(ms * a.b1), fv = both(vs * vs * a.b2);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      m[j] = mul2(m[j], fm);
+      v[j] = mul2(mul2(v[j], v[j]), fv);   // (a code's square is exact)
+    }
+    return;
+  }
+  const f32x2 fm = both(ms), fv = both(vs);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    m[j] = mul2(m[j], fm);
+    v[j] = mul2(v[j], fv);
+    v[j] = mul2(v[j], v[j]);
+  }
+  scaled_moments(a, m, v);
+}
+// The largest magnitude's bits over the warp's 256 values (a NaN is larger than any number).
+__device__ __forceinline__ uint32_t block_top(const f32x2 (&f)[4]) {
+  const float2 p = parts(f[0]), q = parts(f[1]), r = parts(f[2]), t = parts(f[3]);
+  const float top = max_abs3(max_abs3(p.x, p.y, q.x), max_abs3(q.y, r.x, r.y), max_abs3(t.x, t.y, 0.0f));
+  return __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+}
+// Square roots, rounded: an estimate and one step of Newton's method on it, whose
+// residual is exact.  For values that are normal numbers or 0 (smaller ones: too small).
+__device__ __forceinline__ void roots8(f32x2 (&v)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 x = parts(v[j]);
+    const f32x2 y = both(rsqrt_near(fmaxf(x.x, 0x1p-126f)), rsqrt_near(fmaxf(x.y, 0x1p-126f)));
+    const f32x2 r = mul2(v[j], y), e = fma2(mul2(r, both(-1.0f)), r, v[j]);
+    v[j] = fma2(e, mul2(y, both(0.5f)), r);
+  }
+}
+__device__ __forceinline__ void update8(const AdamwStep& a, const AdamwScalars& s, float wd, const f32x2 (&m)[4],
+                                        const f32x2 (&root)[4], f32x2 (&p)[4]) {
+  const f32x2 keep = both(1.0f - s.lr * wd), rate = both(-s.step_size), inv = both(s.inv_root_bc2), eps = both(a.eps);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 d = parts(fma2(root[j], inv, eps));
+    p[j] = fma2(mul2(m[j], rate), both(reciprocal_near(d.x), reciprocal_near(d.y)), mul2(p[j], keep));
+  }
+}
+// Codes of eight values under the scale, top the largest's bits; rnd: two elements' 16
+// random bits in each word.  A value times 2^-120 over the scale has the bits of its
+// e4m3 code, subnormals too, at fp32's place; the random bits are added below the
+// code's last one, and the code is the top byte when all is shifted up by four (which
+// drops the sign).  What is not finite becomes NaN.
+__device__ __forceinline__ uint2 encode8(const f32x2 (&f)[4], float scale, uint32_t top, const uint32_t (&rnd)[4]) {
+  const f32x2 inv = both(reciprocal_of(scale)), place = both(0x1p-120f);
+  uint32_t w[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t t[4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float2 x = parts(mul2(mul2(f[2 * h + j], inv), place));
+      t[2 * j] = (__float_as_uint(x.x) << 4) + __byte_perm(rnd[2 * h + j], 0, 0x4104);
+      t[2 * j + 1] = (__float_as_uint(x.y) << 4) + __byte_perm(rnd[2 * h + j], 0, 0x4324);
+    }
+    w[h] = __byte_perm(__byte_perm(t[0], t[1], 0x0073), __byte_perm(t[2], t[3], 0x0073), 0x5410);
+  }
+  if (top >= 0x7f800000u) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 y = parts(f[j]);
+      if (!(fabsf(y.x) < INFINITY)) w[j / 2] |= 0x7fu << (16 * (j % 2));
+      if (!(fabsf(y.y) < INFINITY)) w[j / 2] |= 0x7fu << (16 * (j % 2) + 8);
+    }
+  }
+  return make_uint2(w[0], w[1]);
+}
+// The signs of eight values, in the codes' places.
+__device__ __forceinline__ uint2 signs8(const f32x2 (&f)[4]) {
+  uint32_t w[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const float2 x = parts(f[2 * h]), y = parts(f[2 * h + 1]);
+    w[h] = __byte_perm(__byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x0073),
+                       __byte_perm(__float_as_uint(y.x), __float_as_uint(y.y), 0x0073), 0x5410) & 0x80808080u;
+  }
+  return make_uint2(w[0], w[1]);
+}
+// Codes of 0 of values that are not 0 become 1.
+__device__ __forceinline__ void not_zero8(const f32x2 (&f)[4], uint2& c) {
+  uint32_t w[2] = {c.x, c.y};
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (((w[h] - 0x01010101u) & ~w[h] & 0x80808080u) == 0) continue;
+    const float2 x = parts(f[2 * h]), y = parts(f[2 * h + 1]);
+    const float e[4] = {x.x, x.y, y.x, y.y};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if ((w[h] >> (8 * j) & 0xffu) == 0 && e[j] != 0.0f) w[h] |= 1u << (8 * j);
+  }
+  c = make_uint2(w[0], w[1]);
+}
+// A warp's 256 elements of a chunk, from element b on, that are there: p and g, and
+// beta1 m and beta2 v.
+template <int BITS, bool VEC>
+__device__ __forceinline__ void adamw_finish(const AdamwStep& a, const AdamwScalars& s, const AdamwChunk& k, int b,
+                                             unsigned long long state, f32x2 (&p)[4], f32x2 (&g)[4], f32x2 (&m)[4],
+                                             f32x2 (&v)[4]) {
+  const int lane = threadIdx.x & 31, i0 = b + (VEC ? 8 * lane : lane), blk = b / kAdamwBlock;
+  moments8(a, s.c, g, m, v);
+  if (BITS == 32) {
+    store8<VEC>(k.m, false, i0, k.len, m);
+    store8<VEC>(k.v, false, i0, k.len, v);
+  }
+  const uint32_t tm = BITS == 8 ? block_top(m) : 0, tv = BITS == 8 ? block_top(v) : 0;
+  const float sm = scale_of(tm), sv = scale_of(__float_as_uint(sqrtf(__uint_as_float(tv))));
+  // (a root of a moment below the normal range is then far below eps, and its code the least)
+  if (BITS == 8 && sv >= 0x1p-30f && sv <= 0x1p60f && a.eps >= 1e-10f) {
+    roots8(v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 x = parts(v[j]);
+      v[j] = both(sqrtf(x.x), sqrtf(x.y));
+    }
+  }
+  update8(a, s, k.wd, m, v, p);
+  store8<VEC>(k.p, k.flags & 1, i0, k.len, p);
+  if (k.copy) store8<VEC>(k.copy, true, i0, k.len, p);
+  if (BITS == 8) {
+    uint32_t rnd[4];
+    if (VEC) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const unsigned long long w = mix64(state + h * kWeyl);
+        rnd[2 * h] = (uint32_t)w;
+        rnd[2 * h + 1] = (uint32_t)(w >> 32);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const unsigned long long at = k.place + i0 + 32 * j;
+        const uint32_t r = (uint32_t)(mix64(random_state(s.key, at)) >> (16 * (at & 3))) & 0xffffu;
+        rnd[j / 2] = j % 2 ? rnd[j / 2] | r << 16 : r;
+      }
+    }
+    const uint2 mc = encode8(m, sm, tm, rnd);
+    uint2 vc = encode8(v, sv, tv, rnd);
+    const uint2 signs = signs8(m);
+    not_zero8(v, vc);
+    store_codes<VEC>(static_cast<uint8_t*>(k.m), i0, k.len, make_uint2(mc.x | signs.x, mc.y | signs.y));
+    store_codes<VEC>(static_cast<uint8_t*>(k.v), i0, k.len, vc);
+    __syncwarp();   // every lane has read the scales
+    if (lane == 0) {
+      k.ms[blk] = sm;
+      k.vs[blk] = sv;
+    }
+  }
 }
 
-// A chunk per block, a thread per element of a scale's block.
+template <int BITS, bool VEC>
+__device__ __forceinline__ void adamw_block(const AdamwStep& a, const AdamwScalars& s, const AdamwChunk& k, int b,
+                                            unsigned long long state) {
+  const int lane = threadIdx.x & 31, i0 = b + (VEC ? 8 * lane : lane), blk = b / kAdamwBlock;
+  f32x2 p[4], g[4], m[4], v[4];
+  load8<VEC>(k.p, k.flags & 1, i0, k.len, p);
+  load8<VEC>(k.g, k.flags & 2, i0, k.len, g);
+  if (BITS == 32) {
+    load8<VEC>(k.m, false, i0, k.len, m);
+    load8<VEC>(k.v, false, i0, k.len, v);
+    scaled_moments(a, m, v);
+  } else {
+    const uint2 mc = load_codes<VEC>(static_cast<const uint8_t*>(k.m), i0, k.len);
+    const uint2 vc = load_codes<VEC>(static_cast<const uint8_t*>(k.v), i0, k.len);
+    decode8(a, mc, vc, k.ms[blk], k.vs[blk], m, v);
+  }
+  adamw_finish<BITS, VEC>(a, s, k, b, state, p, g, m, v);
+}
+
+// ---- 8-bit moments: whole blocks through shared memory, copied ahead
+constexpr int kAdamwStages = 3;
+constexpr int kAdamwStageBytes = 2560;   // p, g: 1024 each; m, v: 256 each
+constexpr int kAdamwSmem = kAdamwThreads / 32 * kAdamwStages * kAdamwStageBytes;
+
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t to, const void* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(from) : "memory");
+}
+// Every lane copies, and later reads, its own eight elements: nothing to wait for but its copies.
+__device__ __forceinline__ void copy_block(const AdamwChunk& k, int b, uint32_t stage) {
+  const int lane = threadIdx.x & 31, i0 = b + 8 * lane;
+  const auto wide = [&](uint32_t to, const void* p, bool narrow) {
+    if (narrow) {
+      copy16(to, static_cast<const bf16*>(p) + i0);
+    } else {
+      copy16(to, static_cast<const float*>(p) + i0);
+      copy16(to + 512, static_cast<const float*>(p) + i0 + 4);
+    }
+  };
+  wide(stage + 16 * lane, k.p, k.flags & 1);
+  wide(stage + 1024 + 16 * lane, k.g, k.flags & 2);
+  copy8(stage + 2048 + 8 * lane, static_cast<const uint8_t*>(k.m) + i0);
+  copy8(stage + 2304 + 8 * lane, static_cast<const uint8_t*>(k.v) + i0);
+}
+__device__ __forceinline__ void read_wide(const char* at, bool narrow, f32x2 (&o)[4]) {
+  const uint4 u = *reinterpret_cast<const uint4*>(at);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  if (narrow) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j] = both(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u));
+  } else {
+    const uint4 t = *reinterpret_cast<const uint4*>(at + 512);
+    o[0] = both(__uint_as_float(u.x), __uint_as_float(u.y));
+    o[1] = both(__uint_as_float(u.z), __uint_as_float(u.w));
+    o[2] = both(__uint_as_float(t.x), __uint_as_float(t.y));
+    o[3] = both(__uint_as_float(t.z), __uint_as_float(t.w));
+  }
+}
+__device__ __forceinline__ void adamw8_chunk(const AdamwStep& a, const AdamwScalars& s, const AdamwChunk& k) {
+  extern __shared__ __align__(16) char buffer[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, first = warp * kAdamwBlock;
+  char* mine = buffer + warp * kAdamwStages * kAdamwStageBytes;
+  const uint32_t at = (uint32_t)__cvta_generic_to_shared(mine);
+  const int whole = k.len < first + kAdamwBlock ? 0 : (k.len - first - kAdamwBlock) / kAdamwPass + 1;   // this warp's
+#pragma unroll
+  for (int i = 0; i < kAdamwStages - 1; ++i) {
+    if (i < whole) copy_block(k, first + i * kAdamwPass, at + i * kAdamwStageBytes);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  // lane i, and 16 + i, hold the scales of this warp's block i
+  float scales = 0.0f;
+  if ((lane & 15) < whole) scales = (lane < 16 ? k.ms : k.vs)[warp + (lane & 15) * (kAdamwPass / kAdamwBlock)];
+  unsigned long long state = random_state(s.key, k.place + first + 8 * lane);
+  int slot = 0;
+  for (int i = 0; i < whole; ++i) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAdamwStages - 2) : "memory");
+    const char* in = mine + slot * kAdamwStageBytes;
+    f32x2 p[4], g[4], m[4], v[4];
+    read_wide(in + 16 * lane, k.flags & 1, p);
+    read_wide(in + 1024 + 16 * lane, k.flags & 2, g);
+    const uint2 mc = *reinterpret_cast<const uint2*>(in + 2048 + 8 * lane);
+    const uint2 vc = *reinterpret_cast<const uint2*>(in + 2304 + 8 * lane);
+    const int next = i + kAdamwStages - 1;
+    if (next < whole)
+      copy_block(k, first + next * kAdamwPass, at + (slot == 0 ? kAdamwStages - 1 : slot - 1) * kAdamwStageBytes);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    decode8(a, mc, vc, __shfl_sync(0xffffffffu, scales, i), __shfl_sync(0xffffffffu, scales, 16 + i), m, v);
+    adamw_finish<8, true>(a, s, k, first + i * kAdamwPass, state, p, g, m, v);
+    state += kAdamwPass / 4 * kWeyl;
+    slot = slot == kAdamwStages - 1 ? 0 : slot + 1;
+  }
+  const int b = first + whole * kAdamwPass;
+  if (b < k.len) adamw_block<8, true>(a, s, k, b, state);   // the tensor's end
+}
+
+// A chunk per block, 256 elements at a time per warp.
 template <int BITS>
-__global__ void __launch_bounds__(kAdamwThreads) adamw_kernel(AdamwStep a) {
-  __shared__ float red[32];
+__global__ void __launch_bounds__(kAdamwThreads, 3) adamw_kernel(AdamwStep a) {
+  const AdamwChunk k = a.chunks[blockIdx.x];
   const AdamwScalars s = adamw_scalars(a);
   if (s.skip) return;
-  const AdamwChunk k = a.chunks[blockIdx.x];
-  for (int b = 0; b < k.len; b += kAdamwBlock) {
-    const int i = b + threadIdx.x;
-    const bool in = i < k.len;
-    float p = 0.0f, g = 0.0f, m = 0.0f, v = 0.0f;
-    if (in) {
-      p = k.flags & 1 ? ld_elem(static_cast<const bf16*>(k.p), i) : ld_elem(static_cast<const float*>(k.p), i);
-      g = k.flags & 2 ? ld_elem(static_cast<const bf16*>(k.g), i) : ld_elem(static_cast<const float*>(k.g), i);
-      if (BITS == 32) {
-        m = static_cast<const float*>(k.m)[i];
-        v = static_cast<const float*>(k.v)[i];
-      } else {
-        m = e4m3_value(static_cast<const uint8_t*>(k.m)[i]) * k.ms[b / kAdamwBlock];
-        v = e4m3_value(static_cast<const uint8_t*>(k.v)[i]) * k.vs[b / kAdamwBlock];
-        v = __fmul_rn(v, v);
-      }
-      g = __fmul_rn(g, s.c);
-      adamw_moments(a, g, m, v);
-    }
-    const float root = sqrtf(v);
-    if (BITS == 8) {
-      const uint32_t tm = __float_as_uint(block_max(fabsf(m), red)), tv = __float_as_uint(block_max(root, red));
-      const float sm = scale_of(tm), sv = scale_of(tv);
-      if (in) {
-        const uint32_t rnd = (uint32_t)(adamw_random(s.key, (k.place + i) & ~3ull) >> (16 * (i & 3))) & 0xffffu;
-        static_cast<uint8_t*>(k.m)[i] = e4m3_code(m * reciprocal_of(sm), rnd);
-        static_cast<uint8_t*>(k.v)[i] = max(e4m3_code(root * reciprocal_of(sv), rnd), root != 0.0f ? 1u : 0u);
-      }
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        k.ms[b / kAdamwBlock] = sm;
-        k.vs[b / kAdamwBlock] = sv;
-      }
-    } else if (in) {
-      static_cast<float*>(k.m)[i] = m;
-      static_cast<float*>(k.v)[i] = v;
-    }
-    if (in) {
-      p = adamw_param(s, a.eps, k.wd, p, m, root);
-      if (k.flags & 1)
-        st_elem(static_cast<bf16*>(k.p), i, p);
-      else
-        st_elem(static_cast<float*>(k.p), i, p);
-      if (k.copy) st_elem(static_cast<bf16*>(k.copy), i, p);
-    }
+  const int first = (threadIdx.x >> 5) * kAdamwBlock;
+  if (!(k.flags & 4)) {
+    for (int b = first; b < k.len; b += kAdamwPass) adamw_block<BITS, false>(a, s, k, b, 0);
+  } else if (BITS == 8) {
+    adamw8_chunk(a, s, k);
+  } else {
+    for (int b = first; b < k.len; b += kAdamwPass) adamw_block<BITS, true>(a, s, k, b, 0);
   }
 }
 
@@ -216,6 +597,10 @@ extern "C" mg_status mg_adamw_create(int n, const mg_adamw_tensor* tensors, int 
     std::vector<mg::AdamwChunk> table;
     unsigned long long place = 0;
     const size_t ss = state_bits == 8 ? 1 : 4;
+    // short lists in chunks of one pass, so that they spread over all multiprocessors
+    double total = 0.0;
+    for (int i = 0; i < n; ++i) total += (double)tensors[i].count;
+    const size_t chunk = total < 8.0 * mg::device_sms() * mg::kAdamwChunk ? mg::kAdamwPass : mg::kAdamwChunk;
     for (int i = 0; i < n; ++i) {
       const mg_adamw_tensor& t = tensors[i];
       if ((t.param_dtype != 0 && t.param_dtype != 1) || (t.grad_dtype != 0 && t.grad_dtype != 1))
@@ -225,7 +610,7 @@ extern "C" mg_status mg_adamw_create(int n, const mg_adamw_tensor* tensors, int 
       if (t.count == 0) continue;
       if (!t.param || !t.grad || !t.m || !t.v || (state_bits == 8 && (!t.m_scales || !t.v_scales)))
         return op_fail(MG_ERR_INVALID_ARG, "%s: a pointer of tensor %d is NULL", fn, i);
-      if (t.count / mg::kAdamwChunk + table.size() > kMaxAdamwChunks)
+      if (t.count / chunk + table.size() > kMaxAdamwChunks)
         return op_fail(MG_ERR_SHAPE, "%s: tensor %d has %zu elements, too many", fn, i, t.count);
       const size_t ps = t.param_dtype ? 2 : 4, gs = t.grad_dtype ? 2 : 4;
       const size_t blocks = (t.count + mg::kAdamwBlock - 1) / mg::kAdamwBlock;
@@ -244,7 +629,9 @@ extern "C" mg_status mg_adamw_create(int n, const mg_adamw_tensor* tensors, int 
       span(ms, blocks * 4, true);
       span(vs, blocks * 4, true);
       span(t.copy, t.count * 2, true);
-      for (size_t a = 0; a < t.count; a += mg::kAdamwChunk) {
+      const auto at = [](const void* p, size_t align) { return reinterpret_cast<uintptr_t>(p) % align == 0; };
+      const bool vec = at(t.param, 8 * ps) && at(t.grad, 8 * gs) && at(t.m, 8 * ss) && at(t.v, 8 * ss) && at(t.copy, 16);
+      for (size_t a = 0; a < t.count; a += chunk) {
         mg::AdamwChunk k;
         k.p = static_cast<char*>(t.param) + a * ps;
         k.g = static_cast<const char*>(t.grad) + a * gs;
@@ -254,8 +641,8 @@ extern "C" mg_status mg_adamw_create(int n, const mg_adamw_tensor* tensors, int 
         k.vs = vs ? vs + a / mg::kAdamwBlock : nullptr;
         k.copy = t.copy ? static_cast<char*>(t.copy) + a * 2 : nullptr;
         k.place = place + a;
-        k.len = (int)std::min<size_t>(mg::kAdamwChunk, t.count - a);
-        k.flags = t.param_dtype | t.grad_dtype << 1;
+        k.len = (int)std::min<size_t>(chunk, t.count - a);
+        k.flags = t.param_dtype | t.grad_dtype << 1 | (vec ? 4 : 0);
         k.wd = t.weight_decay;
         table.push_back(k);
       }
@@ -279,6 +666,8 @@ extern "C" mg_status mg_adamw_create(int n, const mg_adamw_tensor* tensors, int 
     o->seed = seed;
     o->n_chunks = (unsigned)table.size();
     cudaError_t e = cudaGetDevice(&o->device);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(mg::adamw_kernel<8>, cudaFuncAttributeMaxDynamicSharedMemorySize, mg::kAdamwSmem);
     if (e == cudaSuccess && o->n_chunks) {
       const size_t bytes = table.size() * sizeof(mg::AdamwChunk);
       e = cudaMalloc((void**)&o->chunks, bytes);
@@ -333,6 +722,7 @@ extern "C" mg_status mg_adamw_step(mg_adamw* o, double lr, long long step, const
   a.ln_b1 = (float)std::log(o->beta1);
   a.ln_b2 = (float)std::log(o->beta2);
   a.eps = (float)o->eps;
+  a.one = 1.0f;
   const double bc1 = step_device ? 1.0 : -std::expm1((double)step * std::log(o->beta1));
   const double bc2 = step_device ? 1.0 : -std::expm1((double)step * std::log(o->beta2));
   a.lr = (float)lr;
@@ -345,7 +735,7 @@ extern "C" mg_status mg_adamw_step(mg_adamw* o, double lr, long long step, const
   a.seed = o->seed;
   a.step = (unsigned long long)step;
   if (o->bits == 8)
-    mg::adamw_kernel<8><<<o->n_chunks, mg::kAdamwThreads, 0, (cudaStream_t)stream>>>(a);
+    mg::adamw_kernel<8><<<o->n_chunks, mg::kAdamwThreads, mg::kAdamwSmem, (cudaStream_t)stream>>>(a);
   else
     mg::adamw_kernel<32><<<o->n_chunks, mg::kAdamwThreads, 0, (cudaStream_t)stream>>>(a);
   return mg::op_end(fn, cudaGetLastError());
