@@ -41,7 +41,7 @@ namespace {
 constexpr int kAdamwBlock = 256;       // elements under a scale: eight for each lane of a warp
 constexpr int kAdamwThreads = 256;
 constexpr int kAdamwPass = kAdamwThreads * 8;   // elements that a block updates at once
-constexpr int kAdamwChunk = 8 * kAdamwPass;     // of one tensor that it updates in all, in long lists
+constexpr int kAdamwChunk = 4 * kAdamwPass;     // of one tensor that it updates in all, in long lists
 
 struct AdamwChunk {
   void* p;
@@ -162,11 +162,18 @@ __device__ __forceinline__ AdamwScalars adamw_scalars(const AdamwStep& a) {
   return s;
 }
 
-// Eight elements of a lane: neighbours in one access where the chunk allows it
-// (VEC), else 32 apart; n of them (VEC) or those below len exist.
-template <bool VEC>
+// The eight elements of a lane in a block of 256: neighbours, in one access
+// (RUN); twice four neighbours, 128 apart (PAIR; of whole blocks); 32 apart (APART;
+// for tensors at any address).
+enum Lay { APART, RUN, PAIR };
+template <Lay L>
 __device__ __forceinline__ int element(int i0, int j) {
-  return VEC ? i0 + j : i0 + 32 * j;
+  return L == RUN ? i0 + j : L == PAIR ? i0 + j + (j < 4 ? 0 : 124) : i0 + 32 * j;
+}
+template <Lay L>
+__device__ __forceinline__ int first_element(int b) {
+  const int lane = threadIdx.x & 31;
+  return b + (L == RUN ? 8 * lane : L == PAIR ? 4 * lane : lane);
 }
 __device__ __forceinline__ void ld8f32(const float* p, float (&f)[8]) {
   uint32_t w[8];
@@ -185,10 +192,10 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
-template <bool VEC>
+template <Lay L>
 __device__ __forceinline__ void load8(const void* p, bool narrow, int i0, int len, f32x2 (&o)[4]) {
   float f[8];
-  if (VEC && i0 + 8 <= len) {
+  if (L == RUN && i0 + 8 <= len) {
     if (narrow) {
       const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const bf16*>(p) + i0);
       const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -203,14 +210,14 @@ __device__ __forceinline__ void load8(const void* p, bool narrow, int i0, int le
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int i = element<VEC>(i0, j);
+      const int i = element<L>(i0, j);
       f[j] = i >= len ? 0.0f : narrow ? ld_elem(static_cast<const bf16*>(p), i) : ld_elem(static_cast<const float*>(p), i);
     }
   }
 #pragma unroll
   for (int j = 0; j < 4; ++j) o[j] = both(f[2 * j], f[2 * j + 1]);
 }
-template <bool VEC>
+template <Lay L>
 __device__ __forceinline__ void store8(void* p, bool narrow, int i0, int len, const f32x2 (&o)[4]) {
   float f[8];
 #pragma unroll
@@ -219,16 +226,27 @@ __device__ __forceinline__ void store8(void* p, bool narrow, int i0, int len, co
     f[2 * j] = t.x;
     f[2 * j + 1] = t.y;
   }
-  if (VEC && i0 + 8 <= len) {
+  if (L == RUN && i0 + 8 <= len) {
     if (narrow)
       *reinterpret_cast<uint4*>(static_cast<bf16*>(p) + i0) = pack8(f);
     else
       st8f32(static_cast<float*>(p) + i0, f);
     return;
   }
+  if (L == PAIR) {
+    if (narrow) {
+      const uint4 u = pack8(f);
+      *reinterpret_cast<uint2*>(static_cast<bf16*>(p) + i0) = make_uint2(u.x, u.y);
+      *reinterpret_cast<uint2*>(static_cast<bf16*>(p) + i0 + 128) = make_uint2(u.z, u.w);
+    } else {
+      *reinterpret_cast<float4*>(static_cast<float*>(p) + i0) = make_float4(f[0], f[1], f[2], f[3]);
+      *reinterpret_cast<float4*>(static_cast<float*>(p) + i0 + 128) = make_float4(f[4], f[5], f[6], f[7]);
+    }
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const int i = element<VEC>(i0, j);
+    const int i = element<L>(i0, j);
     if (i >= len) continue;
     if (narrow)
       st_elem(static_cast<bf16*>(p), i, f[j]);
@@ -237,27 +255,32 @@ __device__ __forceinline__ void store8(void* p, bool narrow, int i0, int len, co
   }
 }
 // Eight codes in two words.
-template <bool VEC>
+template <Lay L>
 __device__ __forceinline__ uint2 load_codes(const uint8_t* p, int i0, int len) {
-  if (VEC && i0 + 8 <= len) return *reinterpret_cast<const uint2*>(p + i0);
+  if (L == RUN && i0 + 8 <= len) return *reinterpret_cast<const uint2*>(p + i0);
   uint32_t w[2] = {0, 0};
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const int i = element<VEC>(i0, j);
+    const int i = element<L>(i0, j);
     if (i < len) w[j / 4] |= (uint32_t)p[i] << (8 * (j % 4));
   }
   return make_uint2(w[0], w[1]);
 }
-template <bool VEC>
+template <Lay L>
 __device__ __forceinline__ void store_codes(uint8_t* p, int i0, int len, uint2 c) {
-  if (VEC && i0 + 8 <= len) {
+  if (L == RUN && i0 + 8 <= len) {
     *reinterpret_cast<uint2*>(p + i0) = c;
+    return;
+  }
+  if (L == PAIR) {
+    *reinterpret_cast<uint32_t*>(p + i0) = c.x;
+    *reinterpret_cast<uint32_t*>(p + i0 + 128) = c.y;
     return;
   }
   const uint32_t w[2] = {c.x, c.y};
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const int i = element<VEC>(i0, j);
+    const int i = element<L>(i0, j);
     if (i < len) p[i] = (uint8_t)(w[j / 4] >> (8 * (j % 4)));
   }
 }
@@ -394,15 +417,15 @@ __device__ __forceinline__ void not_zero8(const f32x2 (&f)[4], uint2& c) {
 }
 // A warp's 256 elements of a chunk, from element b on, that are there: p and g, and
 // beta1 m and beta2 v.
-template <int BITS, bool VEC>
+template <int BITS, Lay L>
 __device__ __forceinline__ void adamw_finish(const AdamwStep& a, const AdamwScalars& s, const AdamwChunk& k, int b,
                                              unsigned long long state, f32x2 (&p)[4], f32x2 (&g)[4], f32x2 (&m)[4],
                                              f32x2 (&v)[4]) {
-  const int lane = threadIdx.x & 31, i0 = b + (VEC ? 8 * lane : lane), blk = b / kAdamwBlock;
+  const int i0 = first_element<L>(b), blk = b / kAdamwBlock;
   moments8(a, s.c, g, m, v);
   if (BITS == 32) {
-    store8<VEC>(k.m, false, i0, k.len, m);
-    store8<VEC>(k.v, false, i0, k.len, v);
+    store8<L>(k.m, false, i0, k.len, m);
+    store8<L>(k.v, false, i0, k.len, v);
   }
   const uint32_t tm = BITS == 8 ? block_top(m) : 0, tv = BITS == 8 ? block_top(v) : 0;
   const float sm = scale_of(tm), sv = scale_of(__float_as_uint(sqrtf(__uint_as_float(tv))));
@@ -417,14 +440,14 @@ __device__ __forceinline__ void adamw_finish(const AdamwStep& a, const AdamwScal
     }
   }
   update8(a, s, k.wd, m, v, p);
-  store8<VEC>(k.p, k.flags & 1, i0, k.len, p);
-  if (k.copy) store8<VEC>(k.copy, true, i0, k.len, p);
+  store8<L>(k.p, k.flags & 1, i0, k.len, p);
+  if (k.copy) store8<L>(k.copy, true, i0, k.len, p);
   if (BITS == 8) {
     uint32_t rnd[4];
-    if (VEC) {
+    if (L != APART) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const unsigned long long w = mix64(state + h * kWeyl);
+        const unsigned long long w = mix64(state + h * (element<L>(0, 4) / 4 * kWeyl));
         rnd[2 * h] = (uint32_t)w;
         rnd[2 * h + 1] = (uint32_t)(w >> 32);
       }
@@ -440,75 +463,85 @@ __device__ __forceinline__ void adamw_finish(const AdamwStep& a, const AdamwScal
     uint2 vc = encode8(v, sv, tv, rnd);
     const uint2 signs = signs8(m);
     not_zero8(v, vc);
-    store_codes<VEC>(static_cast<uint8_t*>(k.m), i0, k.len, make_uint2(mc.x | signs.x, mc.y | signs.y));
-    store_codes<VEC>(static_cast<uint8_t*>(k.v), i0, k.len, vc);
+    store_codes<L>(static_cast<uint8_t*>(k.m), i0, k.len, make_uint2(mc.x | signs.x, mc.y | signs.y));
+    store_codes<L>(static_cast<uint8_t*>(k.v), i0, k.len, vc);
     __syncwarp();   // every lane has read the scales
-    if (lane == 0) {
+    if ((threadIdx.x & 31) == 0) {
       k.ms[blk] = sm;
       k.vs[blk] = sv;
     }
   }
 }
 
-template <int BITS, bool VEC>
+template <int BITS, Lay L>
 __device__ __forceinline__ void adamw_block(const AdamwStep& a, const AdamwScalars& s, const AdamwChunk& k, int b,
                                             unsigned long long state) {
-  const int lane = threadIdx.x & 31, i0 = b + (VEC ? 8 * lane : lane), blk = b / kAdamwBlock;
+  const int i0 = first_element<L>(b), blk = b / kAdamwBlock;
   f32x2 p[4], g[4], m[4], v[4];
-  load8<VEC>(k.p, k.flags & 1, i0, k.len, p);
-  load8<VEC>(k.g, k.flags & 2, i0, k.len, g);
+  load8<L>(k.p, k.flags & 1, i0, k.len, p);
+  load8<L>(k.g, k.flags & 2, i0, k.len, g);
   if (BITS == 32) {
-    load8<VEC>(k.m, false, i0, k.len, m);
-    load8<VEC>(k.v, false, i0, k.len, v);
+    load8<L>(k.m, false, i0, k.len, m);
+    load8<L>(k.v, false, i0, k.len, v);
     scaled_moments(a, m, v);
   } else {
-    const uint2 mc = load_codes<VEC>(static_cast<const uint8_t*>(k.m), i0, k.len);
-    const uint2 vc = load_codes<VEC>(static_cast<const uint8_t*>(k.v), i0, k.len);
+    const uint2 mc = load_codes<L>(static_cast<const uint8_t*>(k.m), i0, k.len);
+    const uint2 vc = load_codes<L>(static_cast<const uint8_t*>(k.v), i0, k.len);
     decode8(a, mc, vc, k.ms[blk], k.vs[blk], m, v);
   }
-  adamw_finish<BITS, VEC>(a, s, k, b, state, p, g, m, v);
+  adamw_finish<BITS, L>(a, s, k, b, state, p, g, m, v);
 }
 
 // ---- 8-bit moments: whole blocks through shared memory, copied ahead
-constexpr int kAdamwStages = 3;
+constexpr int kAdamwStages = 2;
 constexpr int kAdamwStageBytes = 2560;   // p, g: 1024 each; m, v: 256 each
 constexpr int kAdamwSmem = kAdamwThreads / 32 * kAdamwStages * kAdamwStageBytes;
 
-__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+template <int N>
+__device__ __forceinline__ void copy_ahead(uint32_t to, const void* from) {
+  if (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(N) : "memory");
 }
-__device__ __forceinline__ void copy8(uint32_t to, const void* from) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(from) : "memory");
-}
-// Every lane copies, and later reads, its own eight elements: nothing to wait for but its copies.
+// Every lane copies, and later reads, its own elements (PAIR: a warp's accesses are
+// contiguous): nothing to wait for but its own copies.
 __device__ __forceinline__ void copy_block(const AdamwChunk& k, int b, uint32_t stage) {
-  const int lane = threadIdx.x & 31, i0 = b + 8 * lane;
+  const int lane = threadIdx.x & 31, i0 = first_element<PAIR>(b);
   const auto wide = [&](uint32_t to, const void* p, bool narrow) {
     if (narrow) {
-      copy16(to, static_cast<const bf16*>(p) + i0);
+      copy_ahead<8>(to + 8 * lane, static_cast<const bf16*>(p) + i0);
+      copy_ahead<8>(to + 512 + 8 * lane, static_cast<const bf16*>(p) + i0 + 128);
     } else {
-      copy16(to, static_cast<const float*>(p) + i0);
-      copy16(to + 512, static_cast<const float*>(p) + i0 + 4);
+      copy_ahead<16>(to + 16 * lane, static_cast<const float*>(p) + i0);
+      copy_ahead<16>(to + 512 + 16 * lane, static_cast<const float*>(p) + i0 + 128);
     }
   };
-  wide(stage + 16 * lane, k.p, k.flags & 1);
-  wide(stage + 1024 + 16 * lane, k.g, k.flags & 2);
-  copy8(stage + 2048 + 8 * lane, static_cast<const uint8_t*>(k.m) + i0);
-  copy8(stage + 2304 + 8 * lane, static_cast<const uint8_t*>(k.v) + i0);
+  wide(stage, k.p, k.flags & 1);
+  wide(stage + 1024, k.g, k.flags & 2);
+  copy_ahead<4>(stage + 2048 + 4 * lane, static_cast<const uint8_t*>(k.m) + i0);
+  copy_ahead<4>(stage + 2176 + 4 * lane, static_cast<const uint8_t*>(k.m) + i0 + 128);
+  copy_ahead<4>(stage + 2304 + 4 * lane, static_cast<const uint8_t*>(k.v) + i0);
+  copy_ahead<4>(stage + 2432 + 4 * lane, static_cast<const uint8_t*>(k.v) + i0 + 128);
 }
 __device__ __forceinline__ void read_wide(const char* at, bool narrow, f32x2 (&o)[4]) {
-  const uint4 u = *reinterpret_cast<const uint4*>(at);
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-  if (narrow) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) o[j] = both(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u));
-  } else {
-    const uint4 t = *reinterpret_cast<const uint4*>(at + 512);
-    o[0] = both(__uint_as_float(u.x), __uint_as_float(u.y));
-    o[1] = both(__uint_as_float(u.z), __uint_as_float(u.w));
-    o[2] = both(__uint_as_float(t.x), __uint_as_float(t.y));
-    o[3] = both(__uint_as_float(t.z), __uint_as_float(t.w));
+  for (int h = 0; h < 2; ++h) {
+    if (narrow) {
+      const uint2 u = *reinterpret_cast<const uint2*>(at + 512 * h + 8 * lane);
+      o[2 * h] = both(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u));
+      o[2 * h + 1] = both(__uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
+    } else {
+      const float4 u = *reinterpret_cast<const float4*>(at + 512 * h + 16 * lane);
+      o[2 * h] = both(u.x, u.y);
+      o[2 * h + 1] = both(u.z, u.w);
+    }
   }
+}
+__device__ __forceinline__ uint2 read_codes(const char* at) {
+  const int lane = threadIdx.x & 31;
+  return make_uint2(*reinterpret_cast<const uint32_t*>(at + 4 * lane), *reinterpret_cast<const uint32_t*>(at + 128 + 4 * lane));
 }
 __device__ __forceinline__ void adamw8_chunk(const AdamwStep& a, const AdamwScalars& s, const AdamwChunk& k) {
   extern __shared__ __align__(16) char buffer[];
@@ -524,42 +557,41 @@ __device__ __forceinline__ void adamw8_chunk(const AdamwStep& a, const AdamwScal
   // lane i, and 16 + i, hold the scales of this warp's block i
   float scales = 0.0f;
   if ((lane & 15) < whole) scales = (lane < 16 ? k.ms : k.vs)[warp + (lane & 15) * (kAdamwPass / kAdamwBlock)];
-  unsigned long long state = random_state(s.key, k.place + first + 8 * lane);
+  unsigned long long state = random_state(s.key, k.place + first_element<PAIR>(first));
   int slot = 0;
   for (int i = 0; i < whole; ++i) {
     asm volatile("cp.async.wait_group %0;" ::"n"(kAdamwStages - 2) : "memory");
     const char* in = mine + slot * kAdamwStageBytes;
     f32x2 p[4], g[4], m[4], v[4];
-    read_wide(in + 16 * lane, k.flags & 1, p);
-    read_wide(in + 1024 + 16 * lane, k.flags & 2, g);
-    const uint2 mc = *reinterpret_cast<const uint2*>(in + 2048 + 8 * lane);
-    const uint2 vc = *reinterpret_cast<const uint2*>(in + 2304 + 8 * lane);
+    read_wide(in, k.flags & 1, p);
+    read_wide(in + 1024, k.flags & 2, g);
+    const uint2 mc = read_codes(in + 2048), vc = read_codes(in + 2304);
     const int next = i + kAdamwStages - 1;
     if (next < whole)
       copy_block(k, first + next * kAdamwPass, at + (slot == 0 ? kAdamwStages - 1 : slot - 1) * kAdamwStageBytes);
     asm volatile("cp.async.commit_group;" ::: "memory");
     decode8(a, mc, vc, __shfl_sync(0xffffffffu, scales, i), __shfl_sync(0xffffffffu, scales, 16 + i), m, v);
-    adamw_finish<8, true>(a, s, k, first + i * kAdamwPass, state, p, g, m, v);
+    adamw_finish<8, PAIR>(a, s, k, first + i * kAdamwPass, state, p, g, m, v);
     state += kAdamwPass / 4 * kWeyl;
     slot = slot == kAdamwStages - 1 ? 0 : slot + 1;
   }
   const int b = first + whole * kAdamwPass;
-  if (b < k.len) adamw_block<8, true>(a, s, k, b, state);   // the tensor's end
+  if (b < k.len) adamw_block<8, RUN>(a, s, k, b, random_state(s.key, k.place + first_element<RUN>(b)));   // the tensor's end
 }
 
 // A chunk per block, 256 elements at a time per warp.
 template <int BITS>
-__global__ void __launch_bounds__(kAdamwThreads, 3) adamw_kernel(AdamwStep a) {
+__global__ void __launch_bounds__(kAdamwThreads, BITS == 8 ? 4 : 3) adamw_kernel(AdamwStep a) {
   const AdamwChunk k = a.chunks[blockIdx.x];
   const AdamwScalars s = adamw_scalars(a);
   if (s.skip) return;
   const int first = (threadIdx.x >> 5) * kAdamwBlock;
   if (!(k.flags & 4)) {
-    for (int b = first; b < k.len; b += kAdamwPass) adamw_block<BITS, false>(a, s, k, b, 0);
+    for (int b = first; b < k.len; b += kAdamwPass) adamw_block<BITS, APART>(a, s, k, b, 0);
   } else if (BITS == 8) {
     adamw8_chunk(a, s, k);
   } else {
-    for (int b = first; b < k.len; b += kAdamwPass) adamw_block<BITS, true>(a, s, k, b, 0);
+    for (int b = first; b < k.len; b += kAdamwPass) adamw_block<BITS, RUN>(a, s, k, b, 0);
   }
 }
 

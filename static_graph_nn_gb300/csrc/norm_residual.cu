@@ -18,7 +18,7 @@
 namespace mg {
 namespace {
 
-constexpr int kNrThreads = 256;
+constexpr int kNrThreads = 256;   // of the kernels for any width
 
 struct NormResArgs {
   const void* y;
@@ -31,6 +31,8 @@ struct NormResArgs {
   void* xo;
   void* h;
   float* rstd;
+  int block_rows;             // consecutive rows of a block
+  int stages;                 // rows in shared memory at once
 };
 
 struct NormResGradArgs {
@@ -42,18 +44,446 @@ struct NormResGradArgs {
   const float* g1;
   const float* gate;
   const float* g2;
-  int rows, dim, gate_rows;
+  int rows, dim, gate_rows, gates;
   float scale;
   void* dy;
   void* dx;
   float* dg1;
   float* dgate;
   float* dg2;
-  float* ws;
+  float* ws;                  // [blocks][2][dim]
+  // blocks: `parts` for each gate (block_rows rows each), or, where parts is 1, one for each block_gates gates
+  int parts, block_rows, block_gates;
+  int stages;
 };
 
+// ---- a row in a block's registers --------------------------------------------
+// A thread holds U units of 16 bytes of each row, a block's width apart, where rows
+// begin on 16 bytes (RING), else as many single elements.  In the ring the next rows
+// are copied ahead into shared memory, every thread its own units, so that a thread
+// waits for nothing but its own copies.
+template <typename T, int U>
+struct Cols {
+  static constexpr int kPer = 16 / (int)sizeof(T);   // elements of a unit
+  static constexpr int kE = U * kPer;
+};
+template <typename T, int U, bool RING>
+__device__ __forceinline__ int column(int e) {
+  constexpr int per = Cols<T, U>::kPer;
+  return RING ? ((int)threadIdx.x + e / per * (int)blockDim.x) * per + e % per : (int)threadIdx.x + e * (int)blockDim.x;
+}
+// The fp32 vector's values at this thread's columns, `other` where there is none.
+template <typename T, int U, bool RING>
+__device__ __forceinline__ void vector_at(const float* v, int dim, float other, float (&o)[Cols<T, U>::kE]) {
+  constexpr int E = Cols<T, U>::kE, per = Cols<T, U>::kPer;
+  if (RING) {
+#pragma unroll
+    for (int q = 0; q < E; q += 4) {
+      const int c = column<T, U, RING>(q);
+      const float4 f = v && c < dim ? *reinterpret_cast<const float4*>(v + c) : make_float4(other, other, other, other);
+      o[q] = f.x;
+      o[q + 1] = f.y;
+      o[q + 2] = f.z;
+      o[q + 3] = f.w;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int c = column<T, U, RING>(e);
+      o[e] = v && c < dim ? v[c] : other;
+    }
+  }
+  (void)per;
+}
+__device__ __forceinline__ void widen(const uint4& u, float (&f)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void widen(const uint4& u, float (&f)[4]) {
+  f[0] = __uint_as_float(u.x);
+  f[1] = __uint_as_float(u.y);
+  f[2] = __uint_as_float(u.z);
+  f[3] = __uint_as_float(u.w);
+}
+__device__ __forceinline__ uint4 narrow(const float (&f)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint4 narrow(const float (&f)[4]) {
+  return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+}
+// A row's values at this thread's columns (zeros beyond it), from memory.
+template <typename T, int U>
+__device__ __forceinline__ void row_direct(const T* p, int dim, float (&o)[Cols<T, U>::kE]) {
+#pragma unroll
+  for (int e = 0; e < Cols<T, U>::kE; ++e) {
+    const int c = column<T, U, false>(e);
+    o[e] = p && c < dim ? ld_elem(p, c) : 0.0f;
+  }
+}
+// One unit of a copied row.
 template <typename T>
-__global__ void __launch_bounds__(kNrThreads) norm_res_kernel(NormResArgs a) {
+__device__ __forceinline__ void unit_at(const uint4* at, float (&o)[Cols<T, 1>::kE]) {
+  widen(*at, o);
+}
+template <typename T, int U>
+__device__ __forceinline__ void copy_row(uint4* to, const T* p, int dim) {
+  constexpr int per = Cols<T, U>::kPer;
+#pragma unroll
+  for (int j = 0; j < U; ++j) {
+    const int u = threadIdx.x + j * blockDim.x;
+    if (u * per < dim)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                       (uint32_t)__cvta_generic_to_shared(to + j * blockDim.x + threadIdx.x)),
+                   "l"(p + (size_t)u * per)
+                   : "memory");
+  }
+}
+
+// Sums of N values over the block, the same in every thread; `turn` alternates.
+template <int N>
+__device__ __forceinline__ void block_sums(float (&v)[N], float* red /* [2][16][N] */, int turn) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+#pragma unroll
+  for (int n = 0; n < N; ++n) v[n] = warp_sum(v[n]);
+  if (warps == 1) return;
+  float* r = red + turn * 16 * N;
+  if (lane < N) {
+    float t = v[0];
+#pragma unroll
+    for (int n = 1; n < N; ++n) t = lane == n ? v[n] : t;
+    r[warp * N + lane] = t;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    float t = 0.0f;
+    for (int w = 0; w < warps; ++w) t += r[w * N + n];
+    v[n] = t;
+  }
+}
+
+constexpr int kNrStages = 3;   // rows in shared memory, one of them in use: fewer where they are wide
+// All but the youngest n groups of copies are there.
+__device__ __forceinline__ void copies_wait(int n) {
+  if (n == 2)
+    asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else if (n == 1)
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+template <typename T, int U, bool RING>
+__global__ void __launch_bounds__(512) norm_res_kernel(NormResArgs a) {
+  constexpr int E = Cols<T, U>::kE, per = Cols<T, U>::kPer;
+  extern __shared__ __align__(16) uint4 ring[];   // [stage][y, x][U][threads]
+  __shared__ float red[2 * 16 * 2];
+  const int stage = 2 * U * blockDim.x;
+  const int first = blockIdx.x * a.block_rows, end = min(first + a.block_rows, a.rows);
+  const T *ys = static_cast<const T*>(a.y), *xs = static_cast<const T*>(a.x);
+  const auto ahead = [&](int r) {
+    if (RING) {
+      if (r < end) {
+        uint4* to = ring + (r - first) % a.stages * stage;
+        copy_row<T, U>(to, ys + (size_t)r * a.dim, a.dim);
+        copy_row<T, U>(to + U * blockDim.x, xs + (size_t)r * a.dim, a.dim);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+  };
+  for (int i = 0; i < a.stages - 1; ++i) ahead(first + i);
+  float w[E], g2[E];
+  vector_at<T, U, RING>(a.g2, a.dim, 0.0f, g2);
+  int gate_end = first;
+  for (int r = first; r < end; ++r) {
+    if (r == gate_end) {   // the product of the post norm's factors and the gate, kept for the gate's rows
+      const int gi = r / a.gate_rows;
+      vector_at<T, U, RING>(a.g1, a.dim, 1.0f, w);
+      if (a.gate) {
+        float g[E];
+        vector_at<T, U, RING>(a.gate + (size_t)gi * a.dim, a.dim, 1.0f, g);
+#pragma unroll
+        for (int e = 0; e < E; ++e) w[e] *= g[e];
+      }
+      gate_end = (gi + 1) * a.gate_rows;
+    }
+    float y[E], x[E];
+    if (RING) {
+      ahead(r + a.stages - 1);
+      copies_wait(a.stages - 1);
+      const uint4* in = ring + (r - first) % a.stages * stage + threadIdx.x;
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        float f[per], t[per];
+        const bool there = column<T, U, RING>(j * per) < a.dim;
+        unit_at<T>(in + j * blockDim.x, f);
+        unit_at<T>(in + (U + j) * blockDim.x, t);
+#pragma unroll
+        for (int i = 0; i < per; ++i) {
+          y[j * per + i] = there ? f[i] : 0.0f;
+          x[j * per + i] = there ? t[i] : 0.0f;
+        }
+      }
+    } else {
+      row_direct<T, U>(ys + (size_t)r * a.dim, a.dim, y);
+      row_direct<T, U>(xs + (size_t)r * a.dim, a.dim, x);
+    }
+    float r1 = 1.0f, r2 = 1.0f;
+    if (a.g1) {
+      float s[1] = {0.0f};
+#pragma unroll
+      for (int e = 0; e < E; ++e) s[0] = fmaf(y[e], y[e], s[0]);
+      block_sums<1>(s, red, 0);
+      r1 = 1.0f / sqrtf(s[0] / a.dim + a.eps);
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = fmaf(a.scale, x[e], y[e] * w[e] * r1);
+    if (a.g2) {
+      float s[1] = {0.0f};
+#pragma unroll
+      for (int e = 0; e < E; ++e) s[0] = fmaf(x[e], x[e], s[0]);
+      block_sums<1>(s, red, 1);
+      r2 = 1.0f / sqrtf(s[0] / a.dim + a.eps);
+    } else if (a.g1) {
+      __syncthreads();   // the sums are read before they are written again
+    }
+    T* xo = static_cast<T*>(a.xo) + (size_t)r * a.dim;
+    T* h = a.h ? static_cast<T*>(a.h) + (size_t)r * a.dim : nullptr;
+    if (RING) {
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        const int c = column<T, U, RING>(j * per);
+        if (c >= a.dim) continue;
+        float f[per];
+#pragma unroll
+        for (int i = 0; i < per; ++i) f[i] = x[j * per + i];
+        *reinterpret_cast<uint4*>(xo + c) = narrow(f);
+        if (!h) continue;
+#pragma unroll
+        for (int i = 0; i < per; ++i) f[i] *= r2 * g2[j * per + i];
+        *reinterpret_cast<uint4*>(h + c) = narrow(f);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int c = column<T, U, RING>(e);
+        if (c >= a.dim) continue;
+        st_elem(xo, c, x[e]);
+        if (h) st_elem(h, c, x[e] * r2 * g2[e]);
+      }
+    }
+    if (a.rstd && threadIdx.x == 0) *reinterpret_cast<float2*>(a.rstd + 2 * (size_t)r) = make_float2(r1, r2);
+  }
+}
+
+// A block's rows, gate by gate: rows [first, end) of gate g.
+struct NormResSpan {
+  int g, first, end;
+};
+__device__ __forceinline__ bool next_span(const NormResGradArgs& a, NormResSpan& s) {
+  if (a.parts > 1) {
+    if (s.g >= 0) return false;
+    s.g = blockIdx.x / a.parts;
+    s.first = s.g * a.gate_rows + blockIdx.x % a.parts * a.block_rows;
+    s.end = min(s.first + a.block_rows, (s.g + 1) * a.gate_rows);
+    return s.first < s.end;
+  }
+  s.g = s.g < 0 ? (int)blockIdx.x * a.block_gates : s.g + 1;
+  s.first = s.g * a.gate_rows;
+  s.end = s.first + a.gate_rows;
+  return s.g < min(((int)blockIdx.x + 1) * a.block_gates, a.gates);
+}
+// A column's sums over a span.  P = sum t y r1 gives both the gate's gradient, g1 P,
+// and, times the gate, the post norm's.  Where a block has whole gates it writes
+// their gradients and keeps the post norm's; else it keeps P.
+__device__ __forceinline__ void span_sums(const NormResGradArgs& a, const NormResSpan& s, bool first, int c, float P) {
+  float* keep = a.ws + (size_t)blockIdx.x * 2 * a.dim + c;
+  if (a.parts > 1) {
+    *keep = P;
+    return;
+  }
+  if (a.dgate) a.dgate[(size_t)s.g * a.dim + c] = a.g1 ? a.g1[c] * P : P;
+  if (a.gate) P *= a.gate[(size_t)s.g * a.dim + c];
+  *keep = first ? P : *keep + P;
+}
+
+// The three sums of a row in one exchange.  With b = w y (w = gate g1) and q = dx' + r2 dh g2:
+// S1 = sum dh g2 x', and sum w t y = sum b q - r2^3 / dim S1 sum b x'.
+// (T0: threads at most; KEEP: the factors in registers)
+template <typename T, int U, bool RING, int T0, bool KEEP>
+__global__ void __launch_bounds__(T0, T0 == 512 ? 1 : RING ? 3 : 2) norm_res_grad_kernel(NormResGradArgs a) {
+  constexpr int E = Cols<T, U>::kE, per = Cols<T, U>::kPer;
+  extern __shared__ __align__(16) uint4 ring[];   // [stage][y, x, dx_out, dh][U][threads]
+  __shared__ float red[2 * 16 * 3];
+  const int stage = 4 * U * blockDim.x;
+  const T *ys = static_cast<const T*>(a.y), *xs = static_cast<const T*>(a.x);
+  const T *os = static_cast<const T*>(a.dxo), *hs = static_cast<const T*>(a.dh);
+  const float inv_dim = 1.0f / a.dim;
+  float sp[E], s2[E], w[KEEP ? E : 1], g2[KEEP ? E : 1];
+#pragma unroll
+  for (int e = 0; e < E; ++e) s2[e] = 0.0f;
+  if (KEEP) vector_at<T, U, RING>(a.dh ? a.g2 : nullptr, a.dim, 0.0f, reinterpret_cast<float(&)[E]>(g2));
+  NormResSpan s = {-1, 0, 0};
+  bool any = false;
+  int turn = 0;
+  while (next_span(a, s)) {
+    const float* gate = a.gate ? a.gate + (size_t)s.g * a.dim : nullptr;
+    const auto ahead = [&](int r) {
+      if (RING) {
+        if (r < s.end) {
+          uint4* to = ring + (r - s.first) % a.stages * stage;
+          const size_t at = (size_t)r * a.dim;
+          copy_row<T, U>(to, ys + at, a.dim);
+          copy_row<T, U>(to + U * blockDim.x, xs + at, a.dim);
+          if (os) copy_row<T, U>(to + 2 * U * blockDim.x, os + at, a.dim);
+          if (hs) copy_row<T, U>(to + 3 * U * blockDim.x, hs + at, a.dim);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      }
+    };
+    for (int i = 0; i < a.stages - 1; ++i) ahead(s.first + i);
+    if (KEEP) {
+      float(&ww)[E] = reinterpret_cast<float(&)[E]>(w);
+      vector_at<T, U, RING>(a.g1, a.dim, 1.0f, ww);
+      if (gate) {
+        float g[E];
+        vector_at<T, U, RING>(gate, a.dim, 1.0f, g);
+#pragma unroll
+        for (int e = 0; e < E; ++e) ww[e] *= g[e];
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) sp[e] = 0.0f;
+    const auto w_at = [&](int e) {
+      if (KEEP) return w[KEEP ? e : 0];
+      const int c = column<T, U, RING>(e);
+      return c < a.dim ? (a.g1 ? a.g1[c] : 1.0f) * (gate ? gate[c] : 1.0f) : 0.0f;
+    };
+    const auto g2_at = [&](int e) {
+      if (KEEP) return g2[KEEP ? e : 0];
+      const int c = column<T, U, RING>(e);
+      return hs && c < a.dim ? a.g2[c] : 0.0f;
+    };
+    for (int r = s.first; r < s.end; ++r) {
+      const size_t at = (size_t)r * a.dim;
+      const float2 rs = *reinterpret_cast<const float2*>(a.rstd + 2 * (size_t)r);
+      const float r1 = a.g1 ? rs.x : 1.0f, r2 = hs ? rs.y : 1.0f;
+      float dy_[RING ? 1 : E], dx_[RING ? 1 : E], do_[RING ? 1 : E], dh_[RING ? 1 : E];
+      const uint4* in = ring + (r - s.first) % a.stages * stage + threadIdx.x;
+      if (RING) {
+        ahead(r + a.stages - 1);
+        copies_wait(a.stages - 1);
+      } else {
+        row_direct<T, U>(ys + at, a.dim, reinterpret_cast<float(&)[E]>(dy_));
+        row_direct<T, U>(xs + at, a.dim, reinterpret_cast<float(&)[E]>(dx_));
+        row_direct<T, U>(os ? os + at : nullptr, a.dim, reinterpret_cast<float(&)[E]>(do_));
+        row_direct<T, U>(hs ? hs + at : nullptr, a.dim, reinterpret_cast<float(&)[E]>(dh_));
+      }
+      // unit j's values (RING: from shared memory, zeros beyond the row)
+      const auto unit = [&](int j, float (&y)[per], float (&x)[per], float (&o)[per], float (&h)[per]) {
+        if (RING) {
+          if (column<T, U, RING>(j * per) < a.dim) {
+            unit_at<T>(in + j * blockDim.x, y);
+            unit_at<T>(in + (U + j) * blockDim.x, x);
+            if (os) unit_at<T>(in + (2 * U + j) * blockDim.x, o);
+            if (hs) unit_at<T>(in + (3 * U + j) * blockDim.x, h);
+          } else {
+#pragma unroll
+            for (int i = 0; i < per; ++i) y[i] = x[i] = o[i] = h[i] = 0.0f;
+          }
+#pragma unroll
+          for (int i = 0; i < per; ++i) {
+            if (!os) o[i] = 0.0f;
+            if (!hs) h[i] = 0.0f;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < per; ++i) {
+            y[i] = dy_[RING ? 0 : j * per + i];
+            x[i] = dx_[RING ? 0 : j * per + i];
+            o[i] = do_[RING ? 0 : j * per + i];
+            h[i] = dh_[RING ? 0 : j * per + i];
+          }
+        }
+      };
+      float sum[3] = {0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        float y[per], x[per], o[per], h[per];
+        unit(j, y, x, o, h);
+#pragma unroll
+        for (int i = 0; i < per; ++i) {
+          const float b = w_at(j * per + i) * y[i], xo = fmaf(r1, b, a.scale * x[i]), p = h[i] * g2_at(j * per + i);
+          const float q = fmaf(r2, p, o[i]);
+          sum[0] = fmaf(p, xo, sum[0]);
+          sum[1] = fmaf(b, q, sum[1]);
+          sum[2] = fmaf(b, xo, sum[2]);
+        }
+      }
+      block_sums<3>(sum, red, turn);
+      turn ^= 1;
+      const float c1 = hs ? r2 * r2 * r2 * (sum[0] * inv_dim) : 0.0f;
+      const float c2 = a.g1 ? r1 * r1 * r1 * (fmaf(-c1, sum[2], sum[1]) * inv_dim) : 0.0f;
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        float y[per], x[per], o[per], h[per];
+        unit(j, y, x, o, h);
+#pragma unroll
+        for (int i = 0; i < per; ++i) {
+          const int e = j * per + i;
+          const float wy = w_at(e), xo = fmaf(r1, wy * y[i], a.scale * x[i]);
+          const float t = fmaf(-c1, xo, fmaf(r2, h[i] * g2_at(e), o[i])), yr = y[i] * r1;
+          sp[e] = fmaf(t, yr, sp[e]);
+          s2[e] = fmaf(h[i] * r2, xo, s2[e]);
+          x[i] = a.scale * t;
+          y[i] = fmaf(r1, wy * t, -y[i] * c2);
+        }
+        if (RING) {
+          const int c = column<T, U, RING>(j * per);
+          if (c >= a.dim) continue;
+          *reinterpret_cast<uint4*>(static_cast<T*>(a.dy) + at + c) = narrow(y);
+          *reinterpret_cast<uint4*>(static_cast<T*>(a.dx) + at + c) = narrow(x);
+        } else {
+#pragma unroll
+          for (int i = 0; i < per; ++i) {
+            const int c = column<T, U, RING>(j * per + i);
+            if (c >= a.dim) continue;
+            st_elem(static_cast<T*>(a.dy) + at, c, y[i]);
+            st_elem(static_cast<T*>(a.dx) + at, c, x[i]);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int c = column<T, U, RING>(e);
+      if (c < a.dim) span_sums(a, s, !any, c, sp[e]);
+    }
+    any = true;
+  }
+  float* keep = a.ws + (size_t)blockIdx.x * 2 * a.dim;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int c = column<T, U, RING>(e);
+    if (c >= a.dim) continue;
+    keep[a.dim + c] = s2[e];
+    if (!any) keep[c] = 0.0f;
+  }
+}
+
+// ---- rows of any width: read again for every sum -------------------------------
+template <typename T>
+__global__ void __launch_bounds__(kNrThreads) norm_res_wide_kernel(NormResArgs a) {
   __shared__ float red[32];
   const size_t row = (size_t)blockIdx.x * a.dim;
   const T *y = static_cast<const T*>(a.y) + row, *x = static_cast<const T*>(a.x) + row;
@@ -72,7 +502,10 @@ __global__ void __launch_bounds__(kNrThreads) norm_res_kernel(NormResArgs a) {
   };
   if (a.g2) {
     float s = 0.0f;
-    for (int c = threadIdx.x; c < a.dim; c += kNrThreads) s += out(c) * out(c);
+    for (int c = threadIdx.x; c < a.dim; c += kNrThreads) {
+      const float v = out(c);
+      s += v * v;
+    }
     r2 = 1.0f / sqrtf(block_sum(s, red) / a.dim + a.eps);
   }
   for (int c = threadIdx.x; c < a.dim; c += kNrThreads) {
@@ -86,76 +519,180 @@ __global__ void __launch_bounds__(kNrThreads) norm_res_kernel(NormResArgs a) {
   }
 }
 
-// One gate's rows, or a part of them, per block (blockIdx.y the part): the
-// gradients of the rows, and the columns' sums over them into the workspace.
 template <typename T>
-__global__ void __launch_bounds__(kNrThreads) norm_res_grad_kernel(NormResGradArgs a, int part_rows) {
+__global__ void __launch_bounds__(kNrThreads) norm_res_grad_wide_kernel(NormResGradArgs a) {
   __shared__ float red[32];
-  const size_t part = (size_t)blockIdx.x * gridDim.y + blockIdx.y;
-  const float* gate = a.gate ? a.gate + (size_t)blockIdx.x * a.dim : nullptr;
-  float* sums = a.ws + part * 3 * a.dim;
-  const int first = blockIdx.x * a.gate_rows;
-  const int end = min(first + a.gate_rows, first + ((int)blockIdx.y + 1) * part_rows);
-  for (int c = threadIdx.x; c < 3 * a.dim; c += kNrThreads) sums[c] = 0.0f;
+  float* sums = a.ws + (size_t)blockIdx.x * 2 * a.dim;   // the post norm's (or P), the pre norm's
+  for (int c = threadIdx.x; c < 2 * a.dim; c += kNrThreads) sums[c] = 0.0f;
   __syncthreads();
-  for (int r = first + blockIdx.y * part_rows; r < end; ++r) {
-    const size_t row = (size_t)r * a.dim;
-    const T *y = static_cast<const T*>(a.y) + row, *x = static_cast<const T*>(a.x) + row;
-    const T* dxo = a.dxo ? static_cast<const T*>(a.dxo) + row : nullptr;
-    const T* dh = a.dh ? static_cast<const T*>(a.dh) + row : nullptr;
-    const float r1 = a.g1 ? a.rstd[2 * (size_t)r] : 1.0f, r2 = dh ? a.rstd[2 * (size_t)r + 1] : 1.0f;
-    auto branch = [&](int c) { return a.g1 ? ld_elem(y, c) * r1 * a.g1[c] : ld_elem(y, c); };
-    auto sum = [&](int c) { return a.scale * ld_elem(x, c) + (gate ? gate[c] : 1.0f) * branch(c); };
-    float s1 = 0.0f;
-    if (dh) {
-      for (int c = threadIdx.x; c < a.dim; c += kNrThreads) s1 += ld_elem(dh, c) * a.g2[c] * sum(c);
-      s1 = block_sum(s1, red) / a.dim;
-    }
-    auto total = [&](int c) {
-      float t = dxo ? ld_elem(dxo, c) : 0.0f;
-      if (dh) t += r2 * (ld_elem(dh, c) * a.g2[c] - sum(c) * r2 * r2 * s1);
-      return t;
-    };
-    float s2 = 0.0f;
-    if (a.g1) {
-      for (int c = threadIdx.x; c < a.dim; c += kNrThreads)
-        s2 += (gate ? gate[c] : 1.0f) * total(c) * a.g1[c] * ld_elem(y, c);
-      s2 = block_sum(s2, red) / a.dim;
-    }
-    for (int c = threadIdx.x; c < a.dim; c += kNrThreads) {
-      const float t = total(c), w = (gate ? gate[c] : 1.0f) * t, yc = ld_elem(y, c);
-      sums[c] += a.g1 ? w * yc * r1 : 0.0f;
-      sums[a.dim + c] += t * branch(c);
-      sums[2 * a.dim + c] += dh ? ld_elem(dh, c) * sum(c) * r2 : 0.0f;
-      st_elem(static_cast<T*>(a.dy) + row, c, a.g1 ? r1 * (w * a.g1[c] - yc * r1 * r1 * s2) : w);
-      st_elem(static_cast<T*>(a.dx) + row, c, a.scale * t);
+  NormResSpan span = {-1, 0, 0};
+  while (next_span(a, span)) {
+    const float* gate = a.gate ? a.gate + (size_t)span.g * a.dim : nullptr;
+    for (int r = span.first; r < span.end; ++r) {
+      const size_t row = (size_t)r * a.dim;
+      const T *y = static_cast<const T*>(a.y) + row, *x = static_cast<const T*>(a.x) + row;
+      const T* dxo = a.dxo ? static_cast<const T*>(a.dxo) + row : nullptr;
+      const T* dh = a.dh ? static_cast<const T*>(a.dh) + row : nullptr;
+      const float r1 = a.g1 ? a.rstd[2 * (size_t)r] : 1.0f, r2 = dh ? a.rstd[2 * (size_t)r + 1] : 1.0f;
+      auto w = [&](int c) { return (a.g1 ? a.g1[c] : 1.0f) * (gate ? gate[c] : 1.0f); };
+      auto sum = [&](int c) { return a.scale * ld_elem(x, c) + r1 * (w(c) * ld_elem(y, c)); };
+      float s1 = 0.0f;
+      if (dh) {
+        for (int c = threadIdx.x; c < a.dim; c += kNrThreads) s1 += ld_elem(dh, c) * a.g2[c] * sum(c);
+        s1 = block_sum(s1, red) / a.dim;
+      }
+      auto total = [&](int c) {
+        float t = dxo ? ld_elem(dxo, c) : 0.0f;
+        if (dh) t += r2 * (ld_elem(dh, c) * a.g2[c] - sum(c) * r2 * r2 * s1);
+        return t;
+      };
+      float s2 = 0.0f;
+      if (a.g1) {
+        for (int c = threadIdx.x; c < a.dim; c += kNrThreads) s2 += w(c) * total(c) * ld_elem(y, c);
+        s2 = block_sum(s2, red) / a.dim;
+      }
+      for (int c = threadIdx.x; c < a.dim; c += kNrThreads) {
+        const float t = total(c), yc = ld_elem(y, c), g = a.parts == 1 && gate ? gate[c] : 1.0f;
+        const float P = t * yc * r1;
+        sums[c] += g * P;
+        if (a.parts == 1 && a.dgate) {
+          float* d = a.dgate + (size_t)span.g * a.dim + c;
+          *d = (r == span.first ? 0.0f : *d) + (a.g1 ? a.g1[c] * P : P);
+        }
+        if (dh) sums[a.dim + c] += ld_elem(dh, c) * sum(c) * r2;
+        const float d = r1 * w(c) * t - yc * r1 * r1 * r1 * s2;
+        st_elem(static_cast<T*>(a.dy) + row, c, d);
+        st_elem(static_cast<T*>(a.dx) + row, c, a.scale * t);
+      }
     }
   }
 }
 
-// The parts' sums in order: of all of them for the two norms, of a gate's for
-// its own (blockIdx.y; the norms' in the first).
-__global__ void __launch_bounds__(kNrThreads) norm_res_join_kernel(NormResGradArgs a, int gates, int parts) {
-  const int c = blockIdx.x * kNrThreads + threadIdx.x;
-  if (c >= a.dim) return;
-  auto add = [&](int which, size_t from, size_t n) {
+// The blocks' sums in order: 32 columns a block, 32 runs of blocks added side by side
+// and then in order.  blockIdx.y: 0 the two norms', beyond the gates' (a block has parts of one).
+__global__ void __launch_bounds__(1024) norm_res_join_kernel(NormResGradArgs a, int blocks) {
+  __shared__ float red[32][33];
+  const int lane = threadIdx.x & 31, run = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+  dependency_wait();
+  const auto add = [&](int which, int from, int n, bool gated) {
+    const int per = (n + 31) / 32, begin = min(n, run * per), end = min(n, begin + per);
     float s = 0.0f;
-    for (size_t i = from; i < from + n; ++i) s += a.ws[(i * 3 + which) * a.dim + c];
-    return s;
+    if (c < a.dim)
+      for (int i = from + begin; i < from + end; ++i) {
+        const float v = a.ws[((size_t)i * 2 + which) * a.dim + c];
+        s = gated ? fmaf(a.gate[(size_t)(i / a.parts) * a.dim + c], v, s) : s + v;
+      }
+    red[run][lane] = s;
+    __syncthreads();
+    float t = 0.0f;
+    if (run == 0)
+      for (int i = 0; i < 32; ++i) t += red[i][lane];
+    __syncthreads();
+    return t;
   };
-  if (a.dgate)
-    for (int g = blockIdx.y; g < gates; g += gridDim.y) a.dgate[(size_t)g * a.dim + c] = add(1, (size_t)g * parts, parts);
-  if (blockIdx.y) return;
-  if (a.dg1) a.dg1[c] = add(0, 0, (size_t)gates * parts);
-  if (a.dg2) a.dg2[c] = add(2, 0, (size_t)gates * parts);
+  if (blockIdx.y == 0) {
+    if (a.dg1) {
+      const float t = add(0, 0, blocks, a.parts > 1 && a.gate);
+      if (run == 0 && c < a.dim) a.dg1[c] = t;
+    }
+    if (a.dg2) {
+      const float t = a.dh ? add(1, 0, blocks, false) : 0.0f;
+      if (run == 0 && c < a.dim) a.dg2[c] = t;
+    }
+    return;
+  }
+  for (int g = blockIdx.y - 1; g < a.gates; g += gridDim.y - 1) {
+    const float t = add(0, g * a.parts, a.parts, false);
+    if (run == 0 && c < a.dim) a.dgate[(size_t)g * a.dim + c] = a.g1 ? a.g1[c] * t : t;
+  }
+}
+__global__ void __launch_bounds__(256) norm_res_zero_kernel(NormResGradArgs a) {
+  const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x, n = (size_t)a.gates * a.dim;
+  if (a.dgate && i < n) a.dgate[i] = 0.0f;
+  if (a.dg1 && i < (size_t)a.dim) a.dg1[i] = 0.0f;
+  if (a.dg2 && i < (size_t)a.dim) a.dg2[i] = 0.0f;
 }
 
-// Parts of each gate's rows.
-int norm_res_parts(int rows, int gates) {
+// ---- which kernel ----------------------------------------------------------------
+struct NormResShape {
+  int threads = 0;   // 0: the kernels for any width
+  int each = 0;      // elements a thread
+  bool ring = false;
+  int stages = 0;
+  size_t smem = 0;
+};
+constexpr size_t kNrSmem = 220 * 1024;
+// Eight elements a thread, more where 512 threads are not enough.
+NormResShape norm_res_shape(int dtype, int dim, bool grad) {
+  NormResShape s;
+  const int es = dtype ? 2 : 4;
+  s.ring = (size_t)dim * es % 16 == 0;
+  for (s.each = 8; s.each <= 32; s.each *= 2) {
+    const int threads = ((dim + s.each - 1) / s.each + 31) / 32 * 32;
+    if (threads > 512 || (grad && !s.ring && s.each == 32)) continue;
+    if (s.ring) {
+      const size_t row = (size_t)(grad ? 4 : 2) * s.each * es * threads;
+      s.stages = (int)std::min<size_t>(kNrStages, kNrSmem / row);
+      s.smem = s.stages * row;
+      if (!s.stages) break;
+    }
+    s.threads = threads;
+    break;
+  }
+  return s;
+}
+// Blocks that run at once: by registers (threads of an SM) and by shared memory.
+int norm_res_slots(const NormResShape& s, int threads_per_sm) {
+  if (!s.threads) return device_sms() * 4;
+  int n = std::max(1, std::min(threads_per_sm / s.threads, 32));
+  if (s.ring) n = std::min(n, std::max(1, (int)(kNrSmem / (s.smem + 2048))));
+  return device_sms() * n;
+}
+
+struct NormResSplit {
+  int parts, block_rows, block_gates;
+  long long blocks;
+};
+// Few gates: one round of blocks, whole parts of a gate each; more: four rounds, of
+// which the last may be partly empty, at eight rows or more to a part (a block also
+// writes two fp32 rows of sums).
+NormResSplit norm_res_split(int rows, int gates, int slots) {
+  NormResSplit p;
   const int per = rows / gates;
-  int parts = (2 * 152 + gates - 1) / gates;
-  if (parts > per) parts = per;
-  return parts < 1 ? 1 : parts;
+  int parts = slots / gates >= 4 ? slots / gates : std::min((4 * slots + gates - 1) / gates, (per + 7) / 8);
+  parts = std::max(1, std::min(parts, per));
+  p.block_rows = (per + parts - 1) / parts;
+  p.parts = (per + p.block_rows - 1) / p.block_rows;
+  p.block_gates = p.parts > 1 ? 1 : std::max(1, gates / (4 * slots));
+  p.blocks = p.parts > 1 ? (long long)gates * p.parts : (gates + p.block_gates - 1) / p.block_gates;
+  return p;
+}
+constexpr int kNrFwdThreads = 1024, kNrGradThreads = 768;   // of an SM
+
+template <typename K, typename A>
+cudaError_t norm_res_launch(K kernel, const A& a, long long blocks, int threads, size_t smem, cudaStream_t s) {
+  if (smem > 40 * 1024) {   // (the static part counts too)
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  kernel<<<(unsigned)blocks, threads, smem, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename T, bool RING>
+cudaError_t norm_res_forward(const NormResArgs& a, const NormResShape& s, long long blocks, cudaStream_t st) {
+  constexpr int W = sizeof(T) == 4 ? 2 : 1;   // units of eight elements
+  if (s.each == 8) return norm_res_launch(norm_res_kernel<T, W, RING>, a, blocks, s.threads, s.smem, st);
+  if (s.each == 16) return norm_res_launch(norm_res_kernel<T, 2 * W, RING>, a, blocks, s.threads, s.smem, st);
+  return norm_res_launch(norm_res_kernel<T, 4 * W, RING>, a, blocks, s.threads, s.smem, st);
+}
+template <typename T, bool RING>
+cudaError_t norm_res_backward(const NormResGradArgs& a, const NormResShape& s, long long blocks, cudaStream_t st) {
+  constexpr int W = sizeof(T) == 4 ? 2 : 1;
+  if (s.threads <= 256) return norm_res_launch(norm_res_grad_kernel<T, W, RING, 256, true>, a, blocks, s.threads, s.smem, st);
+  if (s.each == 8) return norm_res_launch(norm_res_grad_kernel<T, W, RING, 512, true>, a, blocks, s.threads, s.smem, st);
+  if (s.each == 16) return norm_res_launch(norm_res_grad_kernel<T, 2 * W, RING, 512, true>, a, blocks, s.threads, s.smem, st);
+  return norm_res_launch(norm_res_grad_kernel<T, 4 * W, true, 512, false>, a, blocks, s.threads, s.smem, st);
 }
 
 }  // namespace
@@ -175,8 +712,13 @@ static mg_status check_norm_res(const char* fn, int dtype, int rows, int dim, co
 
 extern "C" size_t mg_norm_residual_workspace_bytes(int rows, int dim, int gates) {
   if (rows < 0 || rows > mg::kMaxWidth || dim < 1 || dim > mg::kMaxWidth || gates < 0 || (gates && rows % gates)) return 0;
-  const int g = gates ? gates : 1;
-  return ((size_t)g * (rows ? mg::norm_res_parts(rows, g) : 1) * 3 * dim + 4) * sizeof(float);
+  // (of either type: the largest)
+  long long blocks = 1;
+  for (int dtype = 0; rows && dtype < 2; ++dtype) {
+    const mg::NormResShape s = mg::norm_res_shape(dtype, dim, true);
+    blocks = std::max(blocks, mg::norm_res_split(rows, gates ? gates : 1, mg::norm_res_slots(s, mg::kNrGradThreads)).blocks);
+  }
+  return ((size_t)blocks * 2 * dim + 4) * sizeof(float);
 }
 
 extern "C" mg_status mg_norm_residual_forward(int dtype, const void* y, const void* x, int rows, int dim,
@@ -196,12 +738,24 @@ extern "C" mg_status mg_norm_residual_forward(int dtype, const void* y, const vo
                             {gamma_pre, v, false, false}, {x_out, n, true, x_out == y || x_out == x},
                             {h, n, true, h == y || h == x}, {rstd, (size_t)rows * 8, true, false}});
   if (st != MG_OK || !rows) return st;
-  mg::NormResArgs a = {y, x, gamma_post, gate, gamma_pre, rows, dim, gates ? rows / gates : rows, scale, eps, x_out, h, rstd};
-  if (dtype)
-    mg::norm_res_kernel<mg::bf16><<<rows, mg::kNrThreads, 0, (cudaStream_t)stream>>>(a);
-  else
-    mg::norm_res_kernel<float><<<rows, mg::kNrThreads, 0, (cudaStream_t)stream>>>(a);
-  return mg::op_end(fn, cudaGetLastError());
+  mg::NormResArgs a = {y, x, gamma_post, gate, gamma_pre, rows, dim, gates ? rows / gates : rows, scale, eps, x_out, h, rstd, 1, 0};
+  cudaStream_t s = (cudaStream_t)stream;
+  const mg::NormResShape shape = mg::norm_res_shape(dtype, dim, false);
+  cudaError_t e;
+  if (!shape.threads) {
+    e = dtype ? mg::norm_res_launch(mg::norm_res_wide_kernel<mg::bf16>, a, rows, mg::kNrThreads, 0, s)
+              : mg::norm_res_launch(mg::norm_res_wide_kernel<float>, a, rows, mg::kNrThreads, 0, s);
+  } else {
+    a.stages = shape.stages;
+    const int slots = mg::norm_res_slots(shape, mg::kNrFwdThreads);
+    a.block_rows = (rows + slots - 1) / slots;
+    const long long blocks = (rows + a.block_rows - 1) / a.block_rows;
+    if (dtype)
+      e = shape.ring ? mg::norm_res_forward<mg::bf16, true>(a, shape, blocks, s) : mg::norm_res_forward<mg::bf16, false>(a, shape, blocks, s);
+    else
+      e = shape.ring ? mg::norm_res_forward<float, true>(a, shape, blocks, s) : mg::norm_res_forward<float, false>(a, shape, blocks, s);
+  }
+  return mg::op_end(fn, e);
 }
 
 extern "C" mg_status mg_norm_residual_backward(int dtype, const void* dx_out, const void* dh, const void* y,
@@ -231,26 +785,32 @@ extern "C" mg_status mg_norm_residual_backward(int dtype, const void* dx_out, co
                             {dgamma_post, v, true, false}, {dgate, gates * v, true, false}, {dgamma_pre, v, true, false},
                             {workspace, need, true, false}});
   if (st != MG_OK) return st;
-  mg::NormResGradArgs a = {dx_out, dh, y, x, rstd, gamma_post, gate, gamma_pre, rows, dim, 0, scale,
-                           dy, dx, dgamma_post, dgate, dgamma_pre, static_cast<float*>(workspace)};
+  mg::NormResGradArgs a = {dx_out, dh, y, x, rstd, gamma_post, gate, gamma_pre, rows, dim, 0, gates ? gates : 1, scale,
+                           dy, dx, dgamma_post, dgate, dgamma_pre, static_cast<float*>(workspace), 1, 1, 1, 0};
   cudaStream_t s = (cudaStream_t)stream;
-  const int g = gates ? gates : 1;
-  int parts = 0;
-  cudaError_t e = cudaSuccess;
-  if (rows) {
-    a.gate_rows = rows / g;
-    const int part_rows = (a.gate_rows + mg::norm_res_parts(rows, g) - 1) / mg::norm_res_parts(rows, g);
-    parts = (a.gate_rows + part_rows - 1) / part_rows;
-    if (dtype)
-      mg::norm_res_grad_kernel<mg::bf16><<<dim3(g, parts), mg::kNrThreads, 0, s>>>(a, part_rows);
-    else
-      mg::norm_res_grad_kernel<float><<<dim3(g, parts), mg::kNrThreads, 0, s>>>(a, part_rows);
-    e = cudaGetLastError();
+  if (!rows) {
+    const long long blocks = ((long long)a.gates * dim + 255) / 256;
+    return mg::op_end(fn, mg::norm_res_launch(mg::norm_res_zero_kernel, a, blocks, 256, 0, s));
   }
-  if (e == cudaSuccess && (dgamma_post || dgate || dgamma_pre)) {
-    mg::norm_res_join_kernel<<<dim3((dim + mg::kNrThreads - 1) / mg::kNrThreads, dgate ? std::min(g, 65535) : 1), mg::kNrThreads, 0,
-                               s>>>(a, g, parts);
-    e = cudaGetLastError();
-  }
+  a.gate_rows = rows / a.gates;
+  const mg::NormResShape shape = mg::norm_res_shape(dtype, dim, true);
+  const mg::NormResSplit split = mg::norm_res_split(rows, a.gates, mg::norm_res_slots(shape, mg::kNrGradThreads));
+  a.stages = shape.stages;
+  a.parts = split.parts;
+  a.block_rows = split.block_rows;
+  a.block_gates = split.block_gates;
+  cudaError_t e;
+  if (!shape.threads)
+    e = dtype ? mg::norm_res_launch(mg::norm_res_grad_wide_kernel<mg::bf16>, a, split.blocks, mg::kNrThreads, 0, s)
+              : mg::norm_res_launch(mg::norm_res_grad_wide_kernel<float>, a, split.blocks, mg::kNrThreads, 0, s);
+  else if (dtype)
+    e = shape.ring ? mg::norm_res_backward<mg::bf16, true>(a, shape, split.blocks, s)
+                   : mg::norm_res_backward<mg::bf16, false>(a, shape, split.blocks, s);
+  else
+    e = shape.ring ? mg::norm_res_backward<float, true>(a, shape, split.blocks, s)
+                   : mg::norm_res_backward<float, false>(a, shape, split.blocks, s);
+  const int gate_blocks = dgate && a.parts > 1 ? std::min(a.gates, 65534) : 0;
+  if (e == cudaSuccess && (dgamma_post || dgamma_pre || gate_blocks))
+    e = mg::launch_dependent(mg::norm_res_join_kernel, dim3((dim + 31) / 32, 1 + gate_blocks), 1024, 0, s, a, (int)split.blocks);
   return mg::op_end(fn, e);
 }
