@@ -32,6 +32,7 @@
 #include <cuda_fp16.h>
 
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "kernels.h"
 #include "op_checks.h"
 
@@ -97,30 +98,6 @@ __device__ __forceinline__ float2 e4m3_values(uint32_t two) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-// Two fp32 values in one register pair, an operation on both in one issue slot;
-// each rounds as the single operation does.
-typedef unsigned long long f32x2;
-__device__ __forceinline__ f32x2 both(float x, float y) {
-  f32x2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-  return r;
-}
-__device__ __forceinline__ f32x2 both(float x) { return both(x, x); }
-__device__ __forceinline__ float2 parts(f32x2 v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
-  f32x2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
 // The larger of three magnitudes; NaN if one is.
 __device__ __forceinline__ float max_abs3(float a, float b, float c) {
   float r;

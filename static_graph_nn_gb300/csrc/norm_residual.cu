@@ -12,6 +12,7 @@
 #include <cmath>
 
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "kernels.h"
 #include "op_checks.h"
 
@@ -59,117 +60,117 @@ struct NormResGradArgs {
 
 // ---- a row in a block's registers --------------------------------------------
 // A thread holds U units of 16 bytes of each row, a block's width apart, where rows
-// begin on 16 bytes (RING), else as many single elements.  In the ring the next rows
-// are copied ahead into shared memory, every thread its own units, so that a thread
-// waits for nothing but its own copies.
-template <typename T, int U>
-struct Cols {
-  static constexpr int kPer = 16 / (int)sizeof(T);   // elements of a unit
-  static constexpr int kE = U * kPer;
+// begin on 16 bytes (RING), else as many single elements; two at a time in the
+// arithmetic.  In the ring the next rows are copied ahead into shared memory, every
+// thread its own units, so that a thread waits for nothing but its own copies; units
+// beyond the row, and rows that are not given, are zeros there from the start.
+template <typename T>
+struct Unit {
+  static constexpr int kPer = 16 / (int)sizeof(T);   // elements
+  static constexpr int kPairs = kPer / 2;
 };
-template <typename T, int U, bool RING>
+template <typename T, bool RING>
 __device__ __forceinline__ int column(int e) {
-  constexpr int per = Cols<T, U>::kPer;
+  constexpr int per = Unit<T>::kPer;
   return RING ? ((int)threadIdx.x + e / per * (int)blockDim.x) * per + e % per : (int)threadIdx.x + e * (int)blockDim.x;
 }
-// The fp32 vector's values at this thread's columns, `other` where there is none.
-template <typename T, int U, bool RING>
-__device__ __forceinline__ void vector_at(const float* v, int dim, float other, float (&o)[Cols<T, U>::kE]) {
-  constexpr int E = Cols<T, U>::kE, per = Cols<T, U>::kPer;
+// The fp32 vector's values at columns e and e + 1 of this thread, `other` where there are none.
+template <typename T, bool RING>
+__device__ __forceinline__ f32x2 vector_at(const float* v, int dim, float other, int e) {
+  const int c = column<T, RING>(e), d = column<T, RING>(e + 1);
   if (RING) {
-#pragma unroll
-    for (int q = 0; q < E; q += 4) {
-      const int c = column<T, U, RING>(q);
-      const float4 f = v && c < dim ? *reinterpret_cast<const float4*>(v + c) : make_float4(other, other, other, other);
-      o[q] = f.x;
-      o[q + 1] = f.y;
-      o[q + 2] = f.z;
-      o[q + 3] = f.w;
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int c = column<T, U, RING>(e);
-      o[e] = v && c < dim ? v[c] : other;
-    }
+    if (!v || c >= dim) return both(other);
+    const float2 f = *reinterpret_cast<const float2*>(v + c);
+    return both(f.x, f.y);
   }
-  (void)per;
+  return both(v && c < dim ? v[c] : other, v && d < dim ? v[d] : other);
 }
-__device__ __forceinline__ void widen(const uint4& u, float (&f)[8]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
+__device__ __forceinline__ void widen(const uint4& u, f32x2 (&f)[4]) {
+  f[0] = widen2(u.x);
+  f[1] = widen2(u.y);
+  f[2] = widen2(u.z);
+  f[3] = widen2(u.w);
 }
-__device__ __forceinline__ void widen(const uint4& u, float (&f)[4]) {
-  f[0] = __uint_as_float(u.x);
-  f[1] = __uint_as_float(u.y);
-  f[2] = __uint_as_float(u.z);
-  f[3] = __uint_as_float(u.w);
+__device__ __forceinline__ void widen(const uint4& u, f32x2 (&f)[2]) {
+  f[0] = both(__uint_as_float(u.x), __uint_as_float(u.y));
+  f[1] = both(__uint_as_float(u.z), __uint_as_float(u.w));
 }
-__device__ __forceinline__ uint4 narrow(const float (&f)[8]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&h);
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+__device__ __forceinline__ uint4 narrow(const f32x2 (&f)[4]) {
+  return make_uint4(narrow2(f[0]), narrow2(f[1]), narrow2(f[2]), narrow2(f[3]));
 }
-__device__ __forceinline__ uint4 narrow(const float (&f)[4]) {
-  return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+__device__ __forceinline__ uint4 narrow(const f32x2 (&f)[2]) {
+  const float2 a = parts(f[0]), b = parts(f[1]);
+  return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
 }
-// A row's values at this thread's columns (zeros beyond it), from memory.
-template <typename T, int U>
-__device__ __forceinline__ void row_direct(const T* p, int dim, float (&o)[Cols<T, U>::kE]) {
-#pragma unroll
-  for (int e = 0; e < Cols<T, U>::kE; ++e) {
-    const int c = column<T, U, false>(e);
-    o[e] = p && c < dim ? ld_elem(p, c) : 0.0f;
-  }
-}
-// One unit of a copied row.
+// Columns e and e + 1 of a row in memory, zeros beyond it.
 template <typename T>
-__device__ __forceinline__ void unit_at(const uint4* at, float (&o)[Cols<T, 1>::kE]) {
-  widen(*at, o);
+__device__ __forceinline__ f32x2 pair_direct(const T* p, int dim, int e) {
+  const int c = column<T, false>(e), d = column<T, false>(e + 1);
+  return both(p && c < dim ? ld_elem(p, c) : 0.0f, p && d < dim ? ld_elem(p, d) : 0.0f);
+}
+template <typename T>
+__device__ __forceinline__ void store_pair(T* p, int dim, int e, f32x2 v) {
+  const int c = column<T, false>(e), d = column<T, false>(e + 1);
+  const float2 f = parts(v);
+  if (c < dim) st_elem(p, c, f.x);
+  if (d < dim) st_elem(p, d, f.y);
 }
 template <typename T, int U>
 __device__ __forceinline__ void copy_row(uint4* to, const T* p, int dim) {
-  constexpr int per = Cols<T, U>::kPer;
 #pragma unroll
   for (int j = 0; j < U; ++j) {
     const int u = threadIdx.x + j * blockDim.x;
-    if (u * per < dim)
+    if (u * Unit<T>::kPer < dim)
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
                        (uint32_t)__cvta_generic_to_shared(to + j * blockDim.x + threadIdx.x)),
-                   "l"(p + (size_t)u * per)
+                   "l"(p + (size_t)u * Unit<T>::kPer)
                    : "memory");
   }
 }
+// Zeros in the units that no copy writes: those beyond the row, and all of a row that is not given.
+template <typename T, int U>
+__device__ __forceinline__ void clear_row(uint4* to, bool given, int dim) {
+#pragma unroll
+  for (int j = 0; j < U; ++j)
+    if (!given || (int)(threadIdx.x + j * blockDim.x) * Unit<T>::kPer >= dim)
+      to[j * blockDim.x + threadIdx.x] = make_uint4(0, 0, 0, 0);
+}
 
-// Sums of N values over the block, the same in every thread; `turn` alternates.
+// Sums of N values over the block, the same in every thread.  `turn` alternates from
+// call to call: the barrier of one call lies between the reads of the call before it
+// and the writes of the call after it.
 template <int N>
-__device__ __forceinline__ void block_sums(float (&v)[N], float* red /* [2][16][N] */, int turn) {
+__device__ __forceinline__ void block_sums(float (&v)[N], float* red /* [2][N][16] */, int& turn) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
 #pragma unroll
   for (int n = 0; n < N; ++n) v[n] = warp_sum(v[n]);
   if (warps == 1) return;
   float* r = red + turn * 16 * N;
-  if (lane < N) {
-    float t = v[0];
+  turn ^= 1;
+  if (lane == 0) {
 #pragma unroll
-    for (int n = 1; n < N; ++n) t = lane == n ? v[n] : t;
-    r[warp * N + lane] = t;
+    for (int n = 0; n < N; ++n) r[n * 16 + warp] = v[n];
   }
   __syncthreads();
 #pragma unroll
-  for (int n = 0; n < N; ++n) {
-    float t = 0.0f;
-    for (int w = 0; w < warps; ++w) t += r[w * N + n];
-    v[n] = t;
+  for (int n = 0; n < N; ++n) v[n] = 0.0f;
+  for (int w = 0; w < warps; w += 4) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const float4 f = *reinterpret_cast<const float4*>(r + n * 16 + w);   // (zeros beyond the warps)
+      v[n] += (f.x + f.y) + (f.z + f.w);
+    }
   }
+}
+template <int N>
+__device__ __forceinline__ void clear_sums(float* red) {
+  for (int i = threadIdx.x; i < 2 * 16 * N; i += blockDim.x) red[i] = 0.0f;
+  __syncthreads();
+}
+// 1 / sqrt(x): an estimate and one step of Newton's method.
+__device__ __forceinline__ float inverse_root(float x) {
+  const float r = rsqrtf(x);
+  return r > 0.0f ? fmaf(r, 0.5f * fmaf(-x * r, r, 1.0f), r) : r;   // (0 of infinity, NaN of NaN)
 }
 
 constexpr int kNrStages = 3;   // rows in shared memory, one of them in use: fewer where they are wide
@@ -183,103 +184,101 @@ __device__ __forceinline__ void copies_wait(int n) {
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-template <typename T, int U, bool RING>
-__global__ void __launch_bounds__(512) norm_res_kernel(NormResArgs a) {
-  constexpr int E = Cols<T, U>::kE, per = Cols<T, U>::kPer;
+// (T0: threads at most)
+template <typename T, int U, bool RING, int T0>
+__global__ void __launch_bounds__(T0, T0 == 512 ? 1 : 5) norm_res_kernel(NormResArgs a) {
+  constexpr int per = Unit<T>::kPer, pairs = Unit<T>::kPairs, E = U * per, P = E / 2;
   extern __shared__ __align__(16) uint4 ring[];   // [stage][y, x][U][threads]
-  __shared__ float red[2 * 16 * 2];
-  const int stage = 2 * U * blockDim.x;
+  __shared__ __align__(16) float red[2 * 16];
+  clear_sums<1>(red);
+  const int array = U * blockDim.x, stage = 2 * array;
   const int first = blockIdx.x * a.block_rows, end = min(first + a.block_rows, a.rows);
   const T *ys = static_cast<const T*>(a.y), *xs = static_cast<const T*>(a.x);
+  int fill = 0;
   const auto ahead = [&](int r) {
     if (RING) {
       if (r < end) {
-        uint4* to = ring + (r - first) % a.stages * stage;
+        uint4* to = ring + fill * stage;
         copy_row<T, U>(to, ys + (size_t)r * a.dim, a.dim);
-        copy_row<T, U>(to + U * blockDim.x, xs + (size_t)r * a.dim, a.dim);
+        copy_row<T, U>(to + array, xs + (size_t)r * a.dim, a.dim);
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
+      fill = fill + 1 == a.stages ? 0 : fill + 1;
     }
   };
+  if (RING)
+    for (int i = 0; i < 2 * a.stages; ++i) clear_row<T, U>(ring + i * array, true, a.dim);
   for (int i = 0; i < a.stages - 1; ++i) ahead(first + i);
-  float w[E], g2[E];
-  vector_at<T, U, RING>(a.g2, a.dim, 0.0f, g2);
-  int gate_end = first;
+  f32x2 w[P], g2[P];
+#pragma unroll
+  for (int p = 0; p < P; ++p) g2[p] = vector_at<T, RING>(a.g2, a.dim, 0.0f, 2 * p);
+  const float inv_dim = 1.0f / a.dim;
+  const f32x2 scale = both(a.scale);
+  int gate_end = first, slot = 0, turn = 0;
   for (int r = first; r < end; ++r) {
     if (r == gate_end) {   // the product of the post norm's factors and the gate, kept for the gate's rows
       const int gi = r / a.gate_rows;
-      vector_at<T, U, RING>(a.g1, a.dim, 1.0f, w);
-      if (a.gate) {
-        float g[E];
-        vector_at<T, U, RING>(a.gate + (size_t)gi * a.dim, a.dim, 1.0f, g);
+      const float* gate = a.gate ? a.gate + (size_t)gi * a.dim : nullptr;
 #pragma unroll
-        for (int e = 0; e < E; ++e) w[e] *= g[e];
-      }
+      for (int p = 0; p < P; ++p)
+        w[p] = mul2(vector_at<T, RING>(a.g1, a.dim, 1.0f, 2 * p), vector_at<T, RING>(gate, a.dim, 1.0f, 2 * p));
       gate_end = (gi + 1) * a.gate_rows;
     }
-    float y[E], x[E];
+    f32x2 y[P], x[P];
     if (RING) {
       ahead(r + a.stages - 1);
       copies_wait(a.stages - 1);
-      const uint4* in = ring + (r - first) % a.stages * stage + threadIdx.x;
+      const uint4* in = ring + slot * stage + threadIdx.x;
+      slot = slot + 1 == a.stages ? 0 : slot + 1;
 #pragma unroll
       for (int j = 0; j < U; ++j) {
-        float f[per], t[per];
-        const bool there = column<T, U, RING>(j * per) < a.dim;
-        unit_at<T>(in + j * blockDim.x, f);
-        unit_at<T>(in + (U + j) * blockDim.x, t);
-#pragma unroll
-        for (int i = 0; i < per; ++i) {
-          y[j * per + i] = there ? f[i] : 0.0f;
-          x[j * per + i] = there ? t[i] : 0.0f;
-        }
+        widen(in[j * blockDim.x], reinterpret_cast<f32x2(&)[pairs]>(y[j * pairs]));
+        widen(in[array + j * blockDim.x], reinterpret_cast<f32x2(&)[pairs]>(x[j * pairs]));
       }
     } else {
-      row_direct<T, U>(ys + (size_t)r * a.dim, a.dim, y);
-      row_direct<T, U>(xs + (size_t)r * a.dim, a.dim, x);
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        y[p] = pair_direct(ys + (size_t)r * a.dim, a.dim, 2 * p);
+        x[p] = pair_direct(xs + (size_t)r * a.dim, a.dim, 2 * p);
+      }
     }
     float r1 = 1.0f, r2 = 1.0f;
-    if (a.g1) {
-      float s[1] = {0.0f};
+    const auto root_of = [&](const f32x2 (&v)[P]) {
+      f32x2 s = both(0.0f);
 #pragma unroll
-      for (int e = 0; e < E; ++e) s[0] = fmaf(y[e], y[e], s[0]);
-      block_sums<1>(s, red, 0);
-      r1 = 1.0f / sqrtf(s[0] / a.dim + a.eps);
-    }
+      for (int p = 0; p < P; ++p) s = fma2(v[p], v[p], s);
+      const float2 t = parts(s);
+      float q[1] = {t.x + t.y};
+      block_sums<1>(q, red, turn);
+      return inverse_root(fmaf(q[0], inv_dim, a.eps));
+    };
+    if (a.g1) r1 = root_of(y);
+    const f32x2 rr = both(r1);
 #pragma unroll
-    for (int e = 0; e < E; ++e) x[e] = fmaf(a.scale, x[e], y[e] * w[e] * r1);
-    if (a.g2) {
-      float s[1] = {0.0f};
-#pragma unroll
-      for (int e = 0; e < E; ++e) s[0] = fmaf(x[e], x[e], s[0]);
-      block_sums<1>(s, red, 1);
-      r2 = 1.0f / sqrtf(s[0] / a.dim + a.eps);
-    } else if (a.g1) {
-      __syncthreads();   // the sums are read before they are written again
-    }
+    for (int p = 0; p < P; ++p) x[p] = fma2(scale, x[p], mul2(mul2(y[p], w[p]), rr));
+    if (a.g2) r2 = root_of(x);
     T* xo = static_cast<T*>(a.xo) + (size_t)r * a.dim;
     T* h = a.h ? static_cast<T*>(a.h) + (size_t)r * a.dim : nullptr;
+    const f32x2 rq = both(r2);
     if (RING) {
 #pragma unroll
       for (int j = 0; j < U; ++j) {
-        const int c = column<T, U, RING>(j * per);
+        const int c = column<T, RING>(j * per);
         if (c >= a.dim) continue;
-        float f[per];
+        f32x2 f[pairs];
 #pragma unroll
-        for (int i = 0; i < per; ++i) f[i] = x[j * per + i];
+        for (int i = 0; i < pairs; ++i) f[i] = x[j * pairs + i];
         *reinterpret_cast<uint4*>(xo + c) = narrow(f);
         if (!h) continue;
 #pragma unroll
-        for (int i = 0; i < per; ++i) f[i] *= r2 * g2[j * per + i];
+        for (int i = 0; i < pairs; ++i) f[i] = mul2(f[i], mul2(rq, g2[j * pairs + i]));
         *reinterpret_cast<uint4*>(h + c) = narrow(f);
       }
     } else {
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const int c = column<T, U, RING>(e);
-        if (c >= a.dim) continue;
-        st_elem(xo, c, x[e]);
-        if (h) st_elem(h, c, x[e] * r2 * g2[e]);
+      for (int p = 0; p < P; ++p) {
+        store_pair(xo, a.dim, 2 * p, x[p]);
+        if (h) store_pair(h, a.dim, 2 * p, mul2(x[p], mul2(rq, g2[p])));
       }
     }
     if (a.rstd && threadIdx.x == 0) *reinterpret_cast<float2*>(a.rstd + 2 * (size_t)r) = make_float2(r1, r2);
@@ -321,163 +320,165 @@ __device__ __forceinline__ void span_sums(const NormResGradArgs& a, const NormRe
 // S1 = sum dh g2 x', and sum w t y = sum b q - r2^3 / dim S1 sum b x'.
 // (T0: threads at most; KEEP: the factors in registers)
 template <typename T, int U, bool RING, int T0, bool KEEP>
-__global__ void __launch_bounds__(T0, T0 == 512 ? 1 : RING ? 3 : 2) norm_res_grad_kernel(NormResGradArgs a) {
-  constexpr int E = Cols<T, U>::kE, per = Cols<T, U>::kPer;
+__global__ void __launch_bounds__(T0, T0 == 512 ? 1 : 3) norm_res_grad_kernel(NormResGradArgs a) {
+  constexpr int per = Unit<T>::kPer, pairs = Unit<T>::kPairs, E = U * per, P = E / 2;
   extern __shared__ __align__(16) uint4 ring[];   // [stage][y, x, dx_out, dh][U][threads]
-  __shared__ float red[2 * 16 * 3];
-  const int stage = 4 * U * blockDim.x;
+  __shared__ __align__(16) float red[2 * 16 * 3];
+  clear_sums<3>(red);
+  const int array = U * blockDim.x, stage = 4 * array;
   const T *ys = static_cast<const T*>(a.y), *xs = static_cast<const T*>(a.x);
   const T *os = static_cast<const T*>(a.dxo), *hs = static_cast<const T*>(a.dh);
   const float inv_dim = 1.0f / a.dim;
-  float sp[E], s2[E], w[KEEP ? E : 1], g2[KEEP ? E : 1];
+  const f32x2 scale = both(a.scale);
+  f32x2 sp[P], s2[P], w[KEEP ? P : 1], g2[KEEP ? P : 1];
 #pragma unroll
-  for (int e = 0; e < E; ++e) s2[e] = 0.0f;
-  if (KEEP) vector_at<T, U, RING>(a.dh ? a.g2 : nullptr, a.dim, 0.0f, reinterpret_cast<float(&)[E]>(g2));
+  for (int p = 0; p < P; ++p) {
+    s2[p] = both(0.0f);
+    if (KEEP) g2[KEEP ? p : 0] = vector_at<T, RING>(hs ? a.g2 : nullptr, a.dim, 0.0f, 2 * p);
+  }
+  if (RING)
+    for (int i = 0; i < a.stages; ++i) {
+      clear_row<T, U>(ring + i * stage, true, a.dim);
+      clear_row<T, U>(ring + i * stage + array, true, a.dim);
+      clear_row<T, U>(ring + i * stage + 2 * array, os != nullptr, a.dim);
+      clear_row<T, U>(ring + i * stage + 3 * array, hs != nullptr, a.dim);
+    }
   NormResSpan s = {-1, 0, 0};
   bool any = false;
   int turn = 0;
   while (next_span(a, s)) {
     const float* gate = a.gate ? a.gate + (size_t)s.g * a.dim : nullptr;
+    int fill = 0, slot = 0;
     const auto ahead = [&](int r) {
       if (RING) {
         if (r < s.end) {
-          uint4* to = ring + (r - s.first) % a.stages * stage;
+          uint4* to = ring + fill * stage;
           const size_t at = (size_t)r * a.dim;
           copy_row<T, U>(to, ys + at, a.dim);
-          copy_row<T, U>(to + U * blockDim.x, xs + at, a.dim);
-          if (os) copy_row<T, U>(to + 2 * U * blockDim.x, os + at, a.dim);
-          if (hs) copy_row<T, U>(to + 3 * U * blockDim.x, hs + at, a.dim);
+          copy_row<T, U>(to + array, xs + at, a.dim);
+          if (os) copy_row<T, U>(to + 2 * array, os + at, a.dim);
+          if (hs) copy_row<T, U>(to + 3 * array, hs + at, a.dim);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
+        fill = fill + 1 == a.stages ? 0 : fill + 1;
       }
     };
     for (int i = 0; i < a.stages - 1; ++i) ahead(s.first + i);
-    if (KEEP) {
-      float(&ww)[E] = reinterpret_cast<float(&)[E]>(w);
-      vector_at<T, U, RING>(a.g1, a.dim, 1.0f, ww);
-      if (gate) {
-        float g[E];
-        vector_at<T, U, RING>(gate, a.dim, 1.0f, g);
+    const auto w_here = [&](int p) {
+      return mul2(vector_at<T, RING>(a.g1, a.dim, 1.0f, 2 * p), vector_at<T, RING>(gate, a.dim, 1.0f, 2 * p));
+    };
 #pragma unroll
-        for (int e = 0; e < E; ++e) ww[e] *= g[e];
-      }
+    for (int p = 0; p < P; ++p) {
+      sp[p] = both(0.0f);
+      if (KEEP) w[KEEP ? p : 0] = w_here(p);
     }
-#pragma unroll
-    for (int e = 0; e < E; ++e) sp[e] = 0.0f;
-    const auto w_at = [&](int e) {
-      if (KEEP) return w[KEEP ? e : 0];
-      const int c = column<T, U, RING>(e);
-      return c < a.dim ? (a.g1 ? a.g1[c] : 1.0f) * (gate ? gate[c] : 1.0f) : 0.0f;
+    const auto w_at = [&](int p) { return KEEP ? w[KEEP ? p : 0] : w_here(p); };
+    const auto g2_at = [&](int p) {
+      return KEEP ? g2[KEEP ? p : 0] : vector_at<T, RING>(hs ? a.g2 : nullptr, a.dim, 0.0f, 2 * p);
     };
-    const auto g2_at = [&](int e) {
-      if (KEEP) return g2[KEEP ? e : 0];
-      const int c = column<T, U, RING>(e);
-      return hs && c < a.dim ? a.g2[c] : 0.0f;
-    };
+    const float2* roots = reinterpret_cast<const float2*>(a.rstd);
+    float2 root = roots[s.first];
     for (int r = s.first; r < s.end; ++r) {
       const size_t at = (size_t)r * a.dim;
-      const float2 rs = *reinterpret_cast<const float2*>(a.rstd + 2 * (size_t)r);
-      const float r1 = a.g1 ? rs.x : 1.0f, r2 = hs ? rs.y : 1.0f;
-      float dy_[RING ? 1 : E], dx_[RING ? 1 : E], do_[RING ? 1 : E], dh_[RING ? 1 : E];
-      const uint4* in = ring + (r - s.first) % a.stages * stage + threadIdx.x;
+      const float r1 = a.g1 ? root.x : 1.0f, r2 = hs ? root.y : 1.0f;
+      const f32x2 rr1 = both(r1), rr2 = both(r2);
+      f32x2 dy[RING ? 1 : P], dx[RING ? 1 : P], dq[RING ? 1 : P], dh[RING ? 1 : P];
+      const uint4* in = ring + slot * stage + threadIdx.x;
       if (RING) {
         ahead(r + a.stages - 1);
         copies_wait(a.stages - 1);
+        slot = slot + 1 == a.stages ? 0 : slot + 1;
       } else {
-        row_direct<T, U>(ys + at, a.dim, reinterpret_cast<float(&)[E]>(dy_));
-        row_direct<T, U>(xs + at, a.dim, reinterpret_cast<float(&)[E]>(dx_));
-        row_direct<T, U>(os ? os + at : nullptr, a.dim, reinterpret_cast<float(&)[E]>(do_));
-        row_direct<T, U>(hs ? hs + at : nullptr, a.dim, reinterpret_cast<float(&)[E]>(dh_));
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          dy[RING ? 0 : p] = pair_direct(ys + at, a.dim, 2 * p);
+          dx[RING ? 0 : p] = pair_direct(xs + at, a.dim, 2 * p);
+          dq[RING ? 0 : p] = pair_direct(os ? os + at : nullptr, a.dim, 2 * p);
+          dh[RING ? 0 : p] = pair_direct(hs ? hs + at : nullptr, a.dim, 2 * p);
+        }
       }
-      // unit j's values (RING: from shared memory, zeros beyond the row)
-      const auto unit = [&](int j, float (&y)[per], float (&x)[per], float (&o)[per], float (&h)[per]) {
+      if (r + 1 < s.end) root = roots[r + 1];
+      const auto unit = [&](int j, f32x2 (&y)[pairs], f32x2 (&x)[pairs], f32x2 (&o)[pairs], f32x2 (&h)[pairs]) {
         if (RING) {
-          if (column<T, U, RING>(j * per) < a.dim) {
-            unit_at<T>(in + j * blockDim.x, y);
-            unit_at<T>(in + (U + j) * blockDim.x, x);
-            if (os) unit_at<T>(in + (2 * U + j) * blockDim.x, o);
-            if (hs) unit_at<T>(in + (3 * U + j) * blockDim.x, h);
-          } else {
-#pragma unroll
-            for (int i = 0; i < per; ++i) y[i] = x[i] = o[i] = h[i] = 0.0f;
-          }
-#pragma unroll
-          for (int i = 0; i < per; ++i) {
-            if (!os) o[i] = 0.0f;
-            if (!hs) h[i] = 0.0f;
-          }
+          widen(in[j * blockDim.x], y);
+          widen(in[array + j * blockDim.x], x);
+          widen(in[2 * array + j * blockDim.x], o);
+          widen(in[3 * array + j * blockDim.x], h);
         } else {
 #pragma unroll
-          for (int i = 0; i < per; ++i) {
-            y[i] = dy_[RING ? 0 : j * per + i];
-            x[i] = dx_[RING ? 0 : j * per + i];
-            o[i] = do_[RING ? 0 : j * per + i];
-            h[i] = dh_[RING ? 0 : j * per + i];
+          for (int i = 0; i < pairs; ++i) {
+            const int p = RING ? 0 : j * pairs + i;
+            y[i] = dy[p];
+            x[i] = dx[p];
+            o[i] = dq[p];
+            h[i] = dh[p];
           }
         }
       };
-      float sum[3] = {0.0f, 0.0f, 0.0f};
+      f32x2 t1 = both(0.0f), t2 = t1, t3 = t1;
 #pragma unroll
       for (int j = 0; j < U; ++j) {
-        float y[per], x[per], o[per], h[per];
+        f32x2 y[pairs], x[pairs], o[pairs], h[pairs];
         unit(j, y, x, o, h);
 #pragma unroll
-        for (int i = 0; i < per; ++i) {
-          const float b = w_at(j * per + i) * y[i], xo = fmaf(r1, b, a.scale * x[i]), p = h[i] * g2_at(j * per + i);
-          const float q = fmaf(r2, p, o[i]);
-          sum[0] = fmaf(p, xo, sum[0]);
-          sum[1] = fmaf(b, q, sum[1]);
-          sum[2] = fmaf(b, xo, sum[2]);
+        for (int i = 0; i < pairs; ++i) {
+          const int p = j * pairs + i;
+          const f32x2 b = mul2(w_at(p), y[i]), xo = fma2(rr1, b, mul2(scale, x[i])), v = mul2(h[i], g2_at(p));
+          t1 = fma2(v, xo, t1);
+          t2 = fma2(b, fma2(rr2, v, o[i]), t2);
+          t3 = fma2(b, xo, t3);
         }
       }
+      const float2 u1 = parts(t1), u2 = parts(t2), u3 = parts(t3);
+      float sum[3] = {u1.x + u1.y, u2.x + u2.y, u3.x + u3.y};
       block_sums<3>(sum, red, turn);
-      turn ^= 1;
       const float c1 = hs ? r2 * r2 * r2 * (sum[0] * inv_dim) : 0.0f;
       const float c2 = a.g1 ? r1 * r1 * r1 * (fmaf(-c1, sum[2], sum[1]) * inv_dim) : 0.0f;
+      const f32x2 n1 = both(-c1), n2 = both(-c2);
 #pragma unroll
       for (int j = 0; j < U; ++j) {
-        float y[per], x[per], o[per], h[per];
+        f32x2 y[pairs], x[pairs], o[pairs], h[pairs];
         unit(j, y, x, o, h);
 #pragma unroll
-        for (int i = 0; i < per; ++i) {
-          const int e = j * per + i;
-          const float wy = w_at(e), xo = fmaf(r1, wy * y[i], a.scale * x[i]);
-          const float t = fmaf(-c1, xo, fmaf(r2, h[i] * g2_at(e), o[i])), yr = y[i] * r1;
-          sp[e] = fmaf(t, yr, sp[e]);
-          s2[e] = fmaf(h[i] * r2, xo, s2[e]);
-          x[i] = a.scale * t;
-          y[i] = fmaf(r1, wy * t, -y[i] * c2);
+        for (int i = 0; i < pairs; ++i) {
+          const int p = j * pairs + i;
+          const f32x2 wp = w_at(p), xo = fma2(rr1, mul2(wp, y[i]), mul2(scale, x[i]));
+          const f32x2 t = fma2(n1, xo, fma2(rr2, mul2(h[i], g2_at(p)), o[i]));
+          sp[p] = fma2(t, mul2(y[i], rr1), sp[p]);
+          s2[p] = fma2(mul2(h[i], rr2), xo, s2[p]);
+          x[i] = mul2(scale, t);
+          y[i] = fma2(rr1, mul2(wp, t), mul2(y[i], n2));
         }
         if (RING) {
-          const int c = column<T, U, RING>(j * per);
+          const int c = column<T, RING>(j * per);
           if (c >= a.dim) continue;
           *reinterpret_cast<uint4*>(static_cast<T*>(a.dy) + at + c) = narrow(y);
           *reinterpret_cast<uint4*>(static_cast<T*>(a.dx) + at + c) = narrow(x);
         } else {
 #pragma unroll
-          for (int i = 0; i < per; ++i) {
-            const int c = column<T, U, RING>(j * per + i);
-            if (c >= a.dim) continue;
-            st_elem(static_cast<T*>(a.dy) + at, c, y[i]);
-            st_elem(static_cast<T*>(a.dx) + at, c, x[i]);
+          for (int i = 0; i < pairs; ++i) {
+            store_pair(static_cast<T*>(a.dy) + at, a.dim, (j * pairs + i) * 2, y[i]);
+            store_pair(static_cast<T*>(a.dx) + at, a.dim, (j * pairs + i) * 2, x[i]);
           }
         }
       }
     }
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int c = column<T, U, RING>(e);
-      if (c < a.dim) span_sums(a, s, !any, c, sp[e]);
+    for (int p = 0; p < P; ++p) {
+      const float2 f = parts(sp[p]);
+      const int c = column<T, RING>(2 * p), d = column<T, RING>(2 * p + 1);
+      if (c < a.dim) span_sums(a, s, !any, c, f.x);
+      if (d < a.dim) span_sums(a, s, !any, d, f.y);
     }
     any = true;
   }
   float* keep = a.ws + (size_t)blockIdx.x * 2 * a.dim;
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const int c = column<T, U, RING>(e);
-    if (c >= a.dim) continue;
-    keep[a.dim + c] = s2[e];
-    if (!any) keep[c] = 0.0f;
+  for (int p = 0; p < P; ++p) {
+    const float2 f = parts(s2[p]);
+    const int c = column<T, RING>(2 * p), d = column<T, RING>(2 * p + 1);
+    if (c < a.dim) keep[a.dim + c] = f.x;
+    if (d < a.dim) keep[a.dim + d] = f.y;
   }
 }
 
@@ -569,19 +570,25 @@ __global__ void __launch_bounds__(kNrThreads) norm_res_grad_wide_kernel(NormResG
 }
 
 // The blocks' sums in order: 32 columns a block, 32 runs of blocks added side by side
-// and then in order.  blockIdx.y: 0 the two norms', beyond the gates' (a block has parts of one).
+// and then in order.  blockIdx.y: 0 the post norm's (and that of a gate for all rows,
+// which is made of the same sums), 1 the pre norm's, beyond the gates' (blocks have
+// parts of them).
 __global__ void __launch_bounds__(1024) norm_res_join_kernel(NormResGradArgs a, int blocks) {
   __shared__ float red[32][33];
   const int lane = threadIdx.x & 31, run = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+  const bool in = c < a.dim, gated = blockIdx.y == 0 && a.gate && a.parts > 1 && a.gates > 1;
   dependency_wait();
-  const auto add = [&](int which, int from, int n, bool gated) {
+  const auto add = [&](int which, size_t from, int n) {
     const int per = (n + 31) / 32, begin = min(n, run * per), end = min(n, begin + per);
+    const float* v = a.ws + (from * 2 + which) * a.dim + c;
     float s = 0.0f;
-    if (c < a.dim)
-      for (int i = from + begin; i < from + end; ++i) {
-        const float v = a.ws[((size_t)i * 2 + which) * a.dim + c];
-        s = gated ? fmaf(a.gate[(size_t)(i / a.parts) * a.dim + c], v, s) : s + v;
-      }
+    if (in) {
+      if (gated)
+        for (int i = begin; i < end; ++i) s = fmaf(a.gate[(size_t)(i / a.parts) * a.dim + c], v[(size_t)i * 2 * a.dim], s);
+      else
+#pragma unroll 8
+        for (int i = begin; i < end; ++i) s += v[(size_t)i * 2 * a.dim];
+    }
     red[run][lane] = s;
     __syncthreads();
     float t = 0.0f;
@@ -590,20 +597,22 @@ __global__ void __launch_bounds__(1024) norm_res_join_kernel(NormResGradArgs a, 
     __syncthreads();
     return t;
   };
+  const bool writes = run == 0 && in;
   if (blockIdx.y == 0) {
-    if (a.dg1) {
-      const float t = add(0, 0, blocks, a.parts > 1 && a.gate);
-      if (run == 0 && c < a.dim) a.dg1[c] = t;
+    if (!a.dg1 && !(a.dgate && a.gates == 1)) return;
+    const float t = add(0, 0, blocks);
+    const bool one = a.gates == 1 && a.parts > 1;   // then t is the sum of the P
+    if (writes && a.dg1) a.dg1[c] = one && a.gate ? a.gate[c] * t : t;
+    if (writes && a.dgate && one) a.dgate[c] = a.g1 ? a.g1[c] * t : t;
+  } else if (blockIdx.y == 1) {
+    if (!a.dg2) return;
+    const float t = a.dh ? add(1, 0, blocks) : 0.0f;
+    if (writes) a.dg2[c] = t;
+  } else {
+    for (int g = blockIdx.y - 2; g < a.gates; g += gridDim.y - 2) {
+      const float t = add(0, (size_t)g * a.parts, a.parts);
+      if (writes) a.dgate[(size_t)g * a.dim + c] = a.g1 ? a.g1[c] * t : t;
     }
-    if (a.dg2) {
-      const float t = a.dh ? add(1, 0, blocks, false) : 0.0f;
-      if (run == 0 && c < a.dim) a.dg2[c] = t;
-    }
-    return;
-  }
-  for (int g = blockIdx.y - 1; g < a.gates; g += gridDim.y - 1) {
-    const float t = add(0, g * a.parts, a.parts, false);
-    if (run == 0 && c < a.dim) a.dgate[(size_t)g * a.dim + c] = a.g1 ? a.g1[c] * t : t;
   }
 }
 __global__ void __launch_bounds__(256) norm_res_zero_kernel(NormResGradArgs a) {
@@ -622,12 +631,12 @@ struct NormResShape {
   size_t smem = 0;
 };
 constexpr size_t kNrSmem = 220 * 1024;
-// Eight elements a thread, more where 512 threads are not enough.
+// Sixteen elements a thread, more where 512 threads are not enough.
 NormResShape norm_res_shape(int dtype, int dim, bool grad) {
   NormResShape s;
   const int es = dtype ? 2 : 4;
   s.ring = (size_t)dim * es % 16 == 0;
-  for (s.each = 8; s.each <= 32; s.each *= 2) {
+  for (s.each = 16; s.each <= 32; s.each *= 2) {
     const int threads = ((dim + s.each - 1) / s.each + 31) / 32 * 32;
     if (threads > 512 || (grad && !s.ring && s.each == 32)) continue;
     if (s.ring) {
@@ -667,7 +676,7 @@ NormResSplit norm_res_split(int rows, int gates, int slots) {
   p.blocks = p.parts > 1 ? (long long)gates * p.parts : (gates + p.block_gates - 1) / p.block_gates;
   return p;
 }
-constexpr int kNrFwdThreads = 1024, kNrGradThreads = 768;   // of an SM
+constexpr int kNrFwdThreads = 640, kNrGradThreads = 384;   // of an SM
 
 template <typename K, typename A>
 cudaError_t norm_res_launch(K kernel, const A& a, long long blocks, int threads, size_t smem, cudaStream_t s) {
@@ -682,15 +691,14 @@ cudaError_t norm_res_launch(K kernel, const A& a, long long blocks, int threads,
 template <typename T, bool RING>
 cudaError_t norm_res_forward(const NormResArgs& a, const NormResShape& s, long long blocks, cudaStream_t st) {
   constexpr int W = sizeof(T) == 4 ? 2 : 1;   // units of eight elements
-  if (s.each == 8) return norm_res_launch(norm_res_kernel<T, W, RING>, a, blocks, s.threads, s.smem, st);
-  if (s.each == 16) return norm_res_launch(norm_res_kernel<T, 2 * W, RING>, a, blocks, s.threads, s.smem, st);
-  return norm_res_launch(norm_res_kernel<T, 4 * W, RING>, a, blocks, s.threads, s.smem, st);
+  if (s.threads <= 128) return norm_res_launch(norm_res_kernel<T, 2 * W, RING, 128>, a, blocks, s.threads, s.smem, st);
+  if (s.each == 16) return norm_res_launch(norm_res_kernel<T, 2 * W, RING, 512>, a, blocks, s.threads, s.smem, st);
+  return norm_res_launch(norm_res_kernel<T, 4 * W, RING, 512>, a, blocks, s.threads, s.smem, st);
 }
 template <typename T, bool RING>
 cudaError_t norm_res_backward(const NormResGradArgs& a, const NormResShape& s, long long blocks, cudaStream_t st) {
   constexpr int W = sizeof(T) == 4 ? 2 : 1;
-  if (s.threads <= 256) return norm_res_launch(norm_res_grad_kernel<T, W, RING, 256, true>, a, blocks, s.threads, s.smem, st);
-  if (s.each == 8) return norm_res_launch(norm_res_grad_kernel<T, W, RING, 512, true>, a, blocks, s.threads, s.smem, st);
+  if (s.threads <= 128) return norm_res_launch(norm_res_grad_kernel<T, 2 * W, RING, 128, true>, a, blocks, s.threads, s.smem, st);
   if (s.each == 16) return norm_res_launch(norm_res_grad_kernel<T, 2 * W, RING, 512, true>, a, blocks, s.threads, s.smem, st);
   return norm_res_launch(norm_res_grad_kernel<T, 4 * W, true, 512, false>, a, blocks, s.threads, s.smem, st);
 }
@@ -809,8 +817,8 @@ extern "C" mg_status mg_norm_residual_backward(int dtype, const void* dx_out, co
   else
     e = shape.ring ? mg::norm_res_backward<float, true>(a, shape, split.blocks, s)
                    : mg::norm_res_backward<float, false>(a, shape, split.blocks, s);
-  const int gate_blocks = dgate && a.parts > 1 ? std::min(a.gates, 65534) : 0;
-  if (e == cudaSuccess && (dgamma_post || dgamma_pre || gate_blocks))
-    e = mg::launch_dependent(mg::norm_res_join_kernel, dim3((dim + 31) / 32, 1 + gate_blocks), 1024, 0, s, a, (int)split.blocks);
+  const int gate_blocks = dgate && a.parts > 1 && a.gates > 1 ? std::min(a.gates, 65533) : 0;
+  if (e == cudaSuccess && (dgamma_post || dgamma_pre || (dgate && a.parts > 1)))
+    e = mg::launch_dependent(mg::norm_res_join_kernel, dim3((dim + 31) / 32, 2 + gate_blocks), 1024, 0, s, a, (int)split.blocks);
   return mg::op_end(fn, e);
 }
