@@ -34,6 +34,7 @@ struct NormResArgs {
   float* rstd;
   int block_rows;             // consecutive rows of a block
   int stages;                 // rows in shared memory at once
+  int row_units;              // 16-byte units of a row there, at any offset
 };
 
 struct NormResGradArgs {
@@ -55,30 +56,32 @@ struct NormResGradArgs {
   float* ws;                  // [blocks][2][dim]
   // blocks: `parts` for each gate (block_rows rows each), or, where parts is 1, one for each block_gates gates
   int parts, block_rows, block_gates;
-  int stages;
+  int stages, row_units;
 };
 
 // ---- a row in a block's registers --------------------------------------------
-// A thread holds U units of 16 bytes of each row, a block's width apart, where rows
-// begin on 16 bytes (RING), else as many single elements; two at a time in the
-// arithmetic.  In the ring the next rows are copied ahead into shared memory, every
-// thread its own units, so that a thread waits for nothing but its own copies; units
-// beyond the row, and rows that are not given, are zeros there from the start.
+// The next rows are copied ahead into a ring in shared memory, 16 bytes at a time.
+// Where rows begin on 16 bytes (OWN) a thread holds U such units of each row, a
+// block's width apart, and copies those itself, so that it waits for nothing but its
+// own copies; units beyond the row, and rows that are not given, are zeros from the
+// start.  Else it holds as many single elements, a block's width apart, of rows that
+// lie at any offset in what all threads copied together, and a barrier a row.  The
+// arithmetic takes two elements at a time.
 template <typename T>
 struct Unit {
   static constexpr int kPer = 16 / (int)sizeof(T);   // elements
   static constexpr int kPairs = kPer / 2;
 };
-template <typename T, bool RING>
+template <typename T, bool OWN>
 __device__ __forceinline__ int column(int e) {
   constexpr int per = Unit<T>::kPer;
-  return RING ? ((int)threadIdx.x + e / per * (int)blockDim.x) * per + e % per : (int)threadIdx.x + e * (int)blockDim.x;
+  return OWN ? ((int)threadIdx.x + e / per * (int)blockDim.x) * per + e % per : (int)threadIdx.x + e * (int)blockDim.x;
 }
 // The fp32 vector's values at columns e and e + 1 of this thread, `other` where there are none.
-template <typename T, bool RING>
+template <typename T, bool OWN>
 __device__ __forceinline__ f32x2 vector_at(const float* v, int dim, float other, int e) {
-  const int c = column<T, RING>(e), d = column<T, RING>(e + 1);
-  if (RING) {
+  const int c = column<T, OWN>(e), d = column<T, OWN>(e + 1);
+  if (OWN) {
     if (!v || c >= dim) return both(other);
     const float2 f = *reinterpret_cast<const float2*>(v + c);
     return both(f.x, f.y);
@@ -102,9 +105,9 @@ __device__ __forceinline__ uint4 narrow(const f32x2 (&f)[2]) {
   const float2 a = parts(f[0]), b = parts(f[1]);
   return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
 }
-// Columns e and e + 1 of a row in memory, zeros beyond it.
+// Columns e and e + 1 of a row in shared memory, zeros beyond it.
 template <typename T>
-__device__ __forceinline__ f32x2 pair_direct(const T* p, int dim, int e) {
+__device__ __forceinline__ f32x2 pair_at(const T* p, int dim, int e) {
   const int c = column<T, false>(e), d = column<T, false>(e + 1);
   return both(p && c < dim ? ld_elem(p, c) : 0.0f, p && d < dim ? ld_elem(p, d) : 0.0f);
 }
@@ -126,6 +129,22 @@ __device__ __forceinline__ void copy_row(uint4* to, const T* p, int dim) {
                    "l"(p + (size_t)u * Unit<T>::kPer)
                    : "memory");
   }
+}
+// All units of row r of a matrix of n rows, by all threads; the last one ends with the matrix.
+template <typename T>
+__device__ __forceinline__ void copy_whole_row(uint4* to, const T* m, int r, int n, int dim) {
+  const size_t bytes = (size_t)dim * sizeof(T), begin = r * bytes, first = begin / 16, last = (begin + bytes + 15) / 16;
+  for (size_t u = first + threadIdx.x; u < last; u += blockDim.x) {
+    const int size = (int)min((size_t)16, n * bytes - u * 16);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to + (u - first))),
+                 "l"(reinterpret_cast<const char*>(m) + u * 16), "r"(size)
+                 : "memory");
+  }
+}
+// Where row r begins in its copy.
+template <typename T>
+__device__ __forceinline__ const T* whole_row(const uint4* at, int r, int dim) {
+  return reinterpret_cast<const T*>(at) + (size_t)r * dim * sizeof(T) % 16 / sizeof(T);
 }
 // Zeros in the units that no copy writes: those beyond the row, and all of a row that is not given.
 template <typename T, int U>
@@ -173,7 +192,7 @@ __device__ __forceinline__ float inverse_root(float x) {
   return r > 0.0f ? fmaf(r, 0.5f * fmaf(-x * r, r, 1.0f), r) : r;   // (0 of infinity, NaN of NaN)
 }
 
-constexpr int kNrStages = 3;   // rows in shared memory, one of them in use: fewer where they are wide
+constexpr int kNrStages = 2;   // rows in shared memory, one of them in use: fewer where they are wide
 // All but the youngest n groups of copies are there.
 __device__ __forceinline__ void copies_wait(int n) {
   if (n == 2)
@@ -185,33 +204,34 @@ __device__ __forceinline__ void copies_wait(int n) {
 }
 
 // (T0: threads at most)
-template <typename T, int U, bool RING, int T0>
-__global__ void __launch_bounds__(T0, T0 == 512 ? 1 : 5) norm_res_kernel(NormResArgs a) {
+template <typename T, int U, bool OWN, int T0>
+__global__ void __launch_bounds__(T0, T0 == 512 ? 1 : 4) norm_res_kernel(NormResArgs a) {
   constexpr int per = Unit<T>::kPer, pairs = Unit<T>::kPairs, E = U * per, P = E / 2;
   extern __shared__ __align__(16) uint4 ring[];   // [stage][y, x][U][threads]
   __shared__ __align__(16) float red[2 * 16];
   clear_sums<1>(red);
-  const int array = U * blockDim.x, stage = 2 * array;
+  const int array = OWN ? U * blockDim.x : a.row_units, stage = 2 * array;
   const int first = blockIdx.x * a.block_rows, end = min(first + a.block_rows, a.rows);
   const T *ys = static_cast<const T*>(a.y), *xs = static_cast<const T*>(a.x);
   int fill = 0;
   const auto ahead = [&](int r) {
-    if (RING) {
-      if (r < end) {
-        uint4* to = ring + fill * stage;
-        copy_row<T, U>(to, ys + (size_t)r * a.dim, a.dim);
-        copy_row<T, U>(to + array, xs + (size_t)r * a.dim, a.dim);
-      }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-      fill = fill + 1 == a.stages ? 0 : fill + 1;
+    uint4* to = ring + fill * stage;
+    if (r < end && OWN) {
+      copy_row<T, U>(to, ys + (size_t)r * a.dim, a.dim);
+      copy_row<T, U>(to + array, xs + (size_t)r * a.dim, a.dim);
+    } else if (r < end) {
+      copy_whole_row(to, ys, r, a.rows, a.dim);
+      copy_whole_row(to + array, xs, r, a.rows, a.dim);
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    fill = fill + 1 == a.stages ? 0 : fill + 1;
   };
-  if (RING)
+  if (OWN)
     for (int i = 0; i < 2 * a.stages; ++i) clear_row<T, U>(ring + i * array, true, a.dim);
   for (int i = 0; i < a.stages - 1; ++i) ahead(first + i);
   f32x2 w[P], g2[P];
 #pragma unroll
-  for (int p = 0; p < P; ++p) g2[p] = vector_at<T, RING>(a.g2, a.dim, 0.0f, 2 * p);
+  for (int p = 0; p < P; ++p) g2[p] = vector_at<T, OWN>(a.g2, a.dim, 0.0f, 2 * p);
   const float inv_dim = 1.0f / a.dim;
   const f32x2 scale = both(a.scale);
   int gate_end = first, slot = 0, turn = 0;
@@ -221,25 +241,30 @@ __global__ void __launch_bounds__(T0, T0 == 512 ? 1 : 5) norm_res_kernel(NormRes
       const float* gate = a.gate ? a.gate + (size_t)gi * a.dim : nullptr;
 #pragma unroll
       for (int p = 0; p < P; ++p)
-        w[p] = mul2(vector_at<T, RING>(a.g1, a.dim, 1.0f, 2 * p), vector_at<T, RING>(gate, a.dim, 1.0f, 2 * p));
+        w[p] = mul2(vector_at<T, OWN>(a.g1, a.dim, 1.0f, 2 * p), vector_at<T, OWN>(gate, a.dim, 1.0f, 2 * p));
       gate_end = (gi + 1) * a.gate_rows;
     }
     f32x2 y[P], x[P];
-    if (RING) {
+    const uint4* in = ring + slot * stage;
+    slot = slot + 1 == a.stages ? 0 : slot + 1;
+    if (OWN) {
       ahead(r + a.stages - 1);
       copies_wait(a.stages - 1);
-      const uint4* in = ring + slot * stage + threadIdx.x;
-      slot = slot + 1 == a.stages ? 0 : slot + 1;
+      in += threadIdx.x;
 #pragma unroll
       for (int j = 0; j < U; ++j) {
         widen(in[j * blockDim.x], reinterpret_cast<f32x2(&)[pairs]>(y[j * pairs]));
         widen(in[array + j * blockDim.x], reinterpret_cast<f32x2(&)[pairs]>(x[j * pairs]));
       }
     } else {
+      copies_wait(a.stages - 2);
+      __syncthreads();             // row r is there, and the row before it has been read
+      ahead(r + a.stages - 1);
+      const T *yr = whole_row<T>(in, r, a.dim), *xr = whole_row<T>(in + array, r, a.dim);
 #pragma unroll
       for (int p = 0; p < P; ++p) {
-        y[p] = pair_direct(ys + (size_t)r * a.dim, a.dim, 2 * p);
-        x[p] = pair_direct(xs + (size_t)r * a.dim, a.dim, 2 * p);
+        y[p] = pair_at(yr, a.dim, 2 * p);
+        x[p] = pair_at(xr, a.dim, 2 * p);
       }
     }
     float r1 = 1.0f, r2 = 1.0f;
@@ -260,10 +285,10 @@ __global__ void __launch_bounds__(T0, T0 == 512 ? 1 : 5) norm_res_kernel(NormRes
     T* xo = static_cast<T*>(a.xo) + (size_t)r * a.dim;
     T* h = a.h ? static_cast<T*>(a.h) + (size_t)r * a.dim : nullptr;
     const f32x2 rq = both(r2);
-    if (RING) {
+    if (OWN) {
 #pragma unroll
       for (int j = 0; j < U; ++j) {
-        const int c = column<T, RING>(j * per);
+        const int c = column<T, OWN>(j * per);
         if (c >= a.dim) continue;
         f32x2 f[pairs];
 #pragma unroll
@@ -319,13 +344,13 @@ __device__ __forceinline__ void span_sums(const NormResGradArgs& a, const NormRe
 // The three sums of a row in one exchange.  With b = w y (w = gate g1) and q = dx' + r2 dh g2:
 // S1 = sum dh g2 x', and sum w t y = sum b q - r2^3 / dim S1 sum b x'.
 // (T0: threads at most; KEEP: the factors in registers)
-template <typename T, int U, bool RING, int T0, bool KEEP>
-__global__ void __launch_bounds__(T0, T0 == 512 ? 1 : 3) norm_res_grad_kernel(NormResGradArgs a) {
+template <typename T, int U, bool OWN, int T0, bool KEEP>
+__global__ void __launch_bounds__(T0, T0 == 512 ? 1 : OWN ? 4 : 3) norm_res_grad_kernel(NormResGradArgs a) {
   constexpr int per = Unit<T>::kPer, pairs = Unit<T>::kPairs, E = U * per, P = E / 2;
   extern __shared__ __align__(16) uint4 ring[];   // [stage][y, x, dx_out, dh][U][threads]
   __shared__ __align__(16) float red[2 * 16 * 3];
   clear_sums<3>(red);
-  const int array = U * blockDim.x, stage = 4 * array;
+  const int array = OWN ? U * blockDim.x : a.row_units, stage = 4 * array;
   const T *ys = static_cast<const T*>(a.y), *xs = static_cast<const T*>(a.x);
   const T *os = static_cast<const T*>(a.dxo), *hs = static_cast<const T*>(a.dh);
   const float inv_dim = 1.0f / a.dim;
@@ -334,9 +359,9 @@ __global__ void __launch_bounds__(T0, T0 == 512 ? 1 : 3) norm_res_grad_kernel(No
 #pragma unroll
   for (int p = 0; p < P; ++p) {
     s2[p] = both(0.0f);
-    if (KEEP) g2[KEEP ? p : 0] = vector_at<T, RING>(hs ? a.g2 : nullptr, a.dim, 0.0f, 2 * p);
+    if (KEEP) g2[KEEP ? p : 0] = vector_at<T, OWN>(hs ? a.g2 : nullptr, a.dim, 0.0f, 2 * p);
   }
-  if (RING)
+  if (OWN)
     for (int i = 0; i < a.stages; ++i) {
       clear_row<T, U>(ring + i * stage, true, a.dim);
       clear_row<T, U>(ring + i * stage + array, true, a.dim);
@@ -350,22 +375,26 @@ __global__ void __launch_bounds__(T0, T0 == 512 ? 1 : 3) norm_res_grad_kernel(No
     const float* gate = a.gate ? a.gate + (size_t)s.g * a.dim : nullptr;
     int fill = 0, slot = 0;
     const auto ahead = [&](int r) {
-      if (RING) {
-        if (r < s.end) {
-          uint4* to = ring + fill * stage;
-          const size_t at = (size_t)r * a.dim;
-          copy_row<T, U>(to, ys + at, a.dim);
-          copy_row<T, U>(to + array, xs + at, a.dim);
-          if (os) copy_row<T, U>(to + 2 * array, os + at, a.dim);
-          if (hs) copy_row<T, U>(to + 3 * array, hs + at, a.dim);
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        fill = fill + 1 == a.stages ? 0 : fill + 1;
+      uint4* to = ring + fill * stage;
+      if (r < s.end && OWN) {
+        const size_t at = (size_t)r * a.dim;
+        copy_row<T, U>(to, ys + at, a.dim);
+        copy_row<T, U>(to + array, xs + at, a.dim);
+        if (os) copy_row<T, U>(to + 2 * array, os + at, a.dim);
+        if (hs) copy_row<T, U>(to + 3 * array, hs + at, a.dim);
+      } else if (r < s.end) {
+        copy_whole_row(to, ys, r, a.rows, a.dim);
+        copy_whole_row(to + array, xs, r, a.rows, a.dim);
+        if (os) copy_whole_row(to + 2 * array, os, r, a.rows, a.dim);
+        if (hs) copy_whole_row(to + 3 * array, hs, r, a.rows, a.dim);
       }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      fill = fill + 1 == a.stages ? 0 : fill + 1;
     };
+    if (!OWN) __syncthreads();   // the last span's rows have been read
     for (int i = 0; i < a.stages - 1; ++i) ahead(s.first + i);
     const auto w_here = [&](int p) {
-      return mul2(vector_at<T, RING>(a.g1, a.dim, 1.0f, 2 * p), vector_at<T, RING>(gate, a.dim, 1.0f, 2 * p));
+      return mul2(vector_at<T, OWN>(a.g1, a.dim, 1.0f, 2 * p), vector_at<T, OWN>(gate, a.dim, 1.0f, 2 * p));
     };
 #pragma unroll
     for (int p = 0; p < P; ++p) {
@@ -374,7 +403,7 @@ __global__ void __launch_bounds__(T0, T0 == 512 ? 1 : 3) norm_res_grad_kernel(No
     }
     const auto w_at = [&](int p) { return KEEP ? w[KEEP ? p : 0] : w_here(p); };
     const auto g2_at = [&](int p) {
-      return KEEP ? g2[KEEP ? p : 0] : vector_at<T, RING>(hs ? a.g2 : nullptr, a.dim, 0.0f, 2 * p);
+      return KEEP ? g2[KEEP ? p : 0] : vector_at<T, OWN>(hs ? a.g2 : nullptr, a.dim, 0.0f, 2 * p);
     };
     const float2* roots = reinterpret_cast<const float2*>(a.rstd);
     float2 root = roots[s.first];
@@ -382,24 +411,31 @@ __global__ void __launch_bounds__(T0, T0 == 512 ? 1 : 3) norm_res_grad_kernel(No
       const size_t at = (size_t)r * a.dim;
       const float r1 = a.g1 ? root.x : 1.0f, r2 = hs ? root.y : 1.0f;
       const f32x2 rr1 = both(r1), rr2 = both(r2);
-      f32x2 dy[RING ? 1 : P], dx[RING ? 1 : P], dq[RING ? 1 : P], dh[RING ? 1 : P];
-      const uint4* in = ring + slot * stage + threadIdx.x;
-      if (RING) {
+      f32x2 dy[OWN ? 1 : P], dx[OWN ? 1 : P], dq[OWN ? 1 : P], dh[OWN ? 1 : P];
+      const uint4* in = ring + slot * stage;
+      slot = slot + 1 == a.stages ? 0 : slot + 1;
+      if (OWN) {
         ahead(r + a.stages - 1);
         copies_wait(a.stages - 1);
-        slot = slot + 1 == a.stages ? 0 : slot + 1;
+        in += threadIdx.x;
       } else {
+        copies_wait(a.stages - 2);
+        __syncthreads();             // row r is there, and the row before it has been read
+        ahead(r + a.stages - 1);
+        const T *yr = whole_row<T>(in, r, a.dim), *xr = whole_row<T>(in + array, r, a.dim);
+        const T* qr = os ? whole_row<T>(in + 2 * array, r, a.dim) : nullptr;
+        const T* hr = hs ? whole_row<T>(in + 3 * array, r, a.dim) : nullptr;
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-          dy[RING ? 0 : p] = pair_direct(ys + at, a.dim, 2 * p);
-          dx[RING ? 0 : p] = pair_direct(xs + at, a.dim, 2 * p);
-          dq[RING ? 0 : p] = pair_direct(os ? os + at : nullptr, a.dim, 2 * p);
-          dh[RING ? 0 : p] = pair_direct(hs ? hs + at : nullptr, a.dim, 2 * p);
+          dy[OWN ? 0 : p] = pair_at(yr, a.dim, 2 * p);
+          dx[OWN ? 0 : p] = pair_at(xr, a.dim, 2 * p);
+          dq[OWN ? 0 : p] = pair_at(qr, a.dim, 2 * p);
+          dh[OWN ? 0 : p] = pair_at(hr, a.dim, 2 * p);
         }
       }
       if (r + 1 < s.end) root = roots[r + 1];
       const auto unit = [&](int j, f32x2 (&y)[pairs], f32x2 (&x)[pairs], f32x2 (&o)[pairs], f32x2 (&h)[pairs]) {
-        if (RING) {
+        if (OWN) {
           widen(in[j * blockDim.x], y);
           widen(in[array + j * blockDim.x], x);
           widen(in[2 * array + j * blockDim.x], o);
@@ -407,7 +443,7 @@ __global__ void __launch_bounds__(T0, T0 == 512 ? 1 : 3) norm_res_grad_kernel(No
         } else {
 #pragma unroll
           for (int i = 0; i < pairs; ++i) {
-            const int p = RING ? 0 : j * pairs + i;
+            const int p = OWN ? 0 : j * pairs + i;
             y[i] = dy[p];
             x[i] = dx[p];
             o[i] = dq[p];
@@ -449,8 +485,8 @@ __global__ void __launch_bounds__(T0, T0 == 512 ? 1 : 3) norm_res_grad_kernel(No
           x[i] = mul2(scale, t);
           y[i] = fma2(rr1, mul2(wp, t), mul2(y[i], n2));
         }
-        if (RING) {
-          const int c = column<T, RING>(j * per);
+        if (OWN) {
+          const int c = column<T, OWN>(j * per);
           if (c >= a.dim) continue;
           *reinterpret_cast<uint4*>(static_cast<T*>(a.dy) + at + c) = narrow(y);
           *reinterpret_cast<uint4*>(static_cast<T*>(a.dx) + at + c) = narrow(x);
@@ -466,7 +502,7 @@ __global__ void __launch_bounds__(T0, T0 == 512 ? 1 : 3) norm_res_grad_kernel(No
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const float2 f = parts(sp[p]);
-      const int c = column<T, RING>(2 * p), d = column<T, RING>(2 * p + 1);
+      const int c = column<T, OWN>(2 * p), d = column<T, OWN>(2 * p + 1);
       if (c < a.dim) span_sums(a, s, !any, c, f.x);
       if (d < a.dim) span_sums(a, s, !any, d, f.y);
     }
@@ -476,7 +512,7 @@ __global__ void __launch_bounds__(T0, T0 == 512 ? 1 : 3) norm_res_grad_kernel(No
 #pragma unroll
   for (int p = 0; p < P; ++p) {
     const float2 f = parts(s2[p]);
-    const int c = column<T, RING>(2 * p), d = column<T, RING>(2 * p + 1);
+    const int c = column<T, OWN>(2 * p), d = column<T, OWN>(2 * p + 1);
     if (c < a.dim) keep[a.dim + c] = f.x;
     if (d < a.dim) keep[a.dim + d] = f.y;
   }
@@ -626,8 +662,8 @@ __global__ void __launch_bounds__(256) norm_res_zero_kernel(NormResGradArgs a) {
 struct NormResShape {
   int threads = 0;   // 0: the kernels for any width
   int each = 0;      // elements a thread
-  bool ring = false;
-  int stages = 0;
+  bool own = false;
+  int stages = 0, row_units = 0;
   size_t smem = 0;
 };
 constexpr size_t kNrSmem = 220 * 1024;
@@ -635,17 +671,15 @@ constexpr size_t kNrSmem = 220 * 1024;
 NormResShape norm_res_shape(int dtype, int dim, bool grad) {
   NormResShape s;
   const int es = dtype ? 2 : 4;
-  s.ring = (size_t)dim * es % 16 == 0;
+  s.own = (size_t)dim * es % 16 == 0;
   for (s.each = 16; s.each <= 32; s.each *= 2) {
     const int threads = ((dim + s.each - 1) / s.each + 31) / 32 * 32;
-    if (threads > 512 || (grad && !s.ring && s.each == 32)) continue;
-    if (s.ring) {
-      const size_t row = (size_t)(grad ? 4 : 2) * s.each * es * threads;
-      s.stages = (int)std::min<size_t>(kNrStages, kNrSmem / row);
-      s.smem = s.stages * row;
-      if (!s.stages) break;
-    }
-    s.threads = threads;
+    if (threads > 512 || (grad && !s.own && s.each == 32)) continue;
+    s.row_units = s.own ? s.each * es * threads / 16 : (dim * es + 15) / 16 + 1;
+    const size_t row = (size_t)(grad ? 4 : 2) * s.row_units * 16;
+    s.stages = (int)std::min<size_t>(kNrStages, kNrSmem / row);
+    s.smem = s.stages * row;
+    if (s.stages >= (s.own ? 1 : 2)) s.threads = threads;
     break;
   }
   return s;
@@ -653,8 +687,8 @@ NormResShape norm_res_shape(int dtype, int dim, bool grad) {
 // Blocks that run at once: by registers (threads of an SM) and by shared memory.
 int norm_res_slots(const NormResShape& s, int threads_per_sm) {
   if (!s.threads) return device_sms() * 4;
-  int n = std::max(1, std::min(threads_per_sm / s.threads, 32));
-  if (s.ring) n = std::min(n, std::max(1, (int)(kNrSmem / (s.smem + 2048))));
+  int n = std::max(1, std::min((s.own ? threads_per_sm : threads_per_sm * 3 / 4) / s.threads, 32));
+  n = std::min(n, std::max(1, (int)(kNrSmem / (s.smem + 2048))));
   return device_sms() * n;
 }
 
@@ -676,7 +710,7 @@ NormResSplit norm_res_split(int rows, int gates, int slots) {
   p.blocks = p.parts > 1 ? (long long)gates * p.parts : (gates + p.block_gates - 1) / p.block_gates;
   return p;
 }
-constexpr int kNrFwdThreads = 640, kNrGradThreads = 384;   // of an SM
+constexpr int kNrFwdThreads = 512, kNrGradThreads = 512;   // of an SM
 
 template <typename K, typename A>
 cudaError_t norm_res_launch(K kernel, const A& a, long long blocks, int threads, size_t smem, cudaStream_t s) {
@@ -688,18 +722,18 @@ cudaError_t norm_res_launch(K kernel, const A& a, long long blocks, int threads,
   return cudaGetLastError();
 }
 
-template <typename T, bool RING>
+template <typename T, bool OWN>
 cudaError_t norm_res_forward(const NormResArgs& a, const NormResShape& s, long long blocks, cudaStream_t st) {
   constexpr int W = sizeof(T) == 4 ? 2 : 1;   // units of eight elements
-  if (s.threads <= 128) return norm_res_launch(norm_res_kernel<T, 2 * W, RING, 128>, a, blocks, s.threads, s.smem, st);
-  if (s.each == 16) return norm_res_launch(norm_res_kernel<T, 2 * W, RING, 512>, a, blocks, s.threads, s.smem, st);
-  return norm_res_launch(norm_res_kernel<T, 4 * W, RING, 512>, a, blocks, s.threads, s.smem, st);
+  if (s.threads <= 128) return norm_res_launch(norm_res_kernel<T, 2 * W, OWN, 128>, a, blocks, s.threads, s.smem, st);
+  if (s.each == 16) return norm_res_launch(norm_res_kernel<T, 2 * W, OWN, 512>, a, blocks, s.threads, s.smem, st);
+  return norm_res_launch(norm_res_kernel<T, 4 * W, OWN, 512>, a, blocks, s.threads, s.smem, st);
 }
-template <typename T, bool RING>
+template <typename T, bool OWN>
 cudaError_t norm_res_backward(const NormResGradArgs& a, const NormResShape& s, long long blocks, cudaStream_t st) {
   constexpr int W = sizeof(T) == 4 ? 2 : 1;
-  if (s.threads <= 128) return norm_res_launch(norm_res_grad_kernel<T, 2 * W, RING, 128, true>, a, blocks, s.threads, s.smem, st);
-  if (s.each == 16) return norm_res_launch(norm_res_grad_kernel<T, 2 * W, RING, 512, true>, a, blocks, s.threads, s.smem, st);
+  if (s.threads <= 128) return norm_res_launch(norm_res_grad_kernel<T, 2 * W, OWN, 128, true>, a, blocks, s.threads, s.smem, st);
+  if (s.each == 16) return norm_res_launch(norm_res_grad_kernel<T, 2 * W, OWN, 512, true>, a, blocks, s.threads, s.smem, st);
   return norm_res_launch(norm_res_grad_kernel<T, 4 * W, true, 512, false>, a, blocks, s.threads, s.smem, st);
 }
 
@@ -746,22 +780,21 @@ extern "C" mg_status mg_norm_residual_forward(int dtype, const void* y, const vo
                             {gamma_pre, v, false, false}, {x_out, n, true, x_out == y || x_out == x},
                             {h, n, true, h == y || h == x}, {rstd, (size_t)rows * 8, true, false}});
   if (st != MG_OK || !rows) return st;
-  mg::NormResArgs a = {y, x, gamma_post, gate, gamma_pre, rows, dim, gates ? rows / gates : rows, scale, eps, x_out, h, rstd, 1, 0};
-  cudaStream_t s = (cudaStream_t)stream;
   const mg::NormResShape shape = mg::norm_res_shape(dtype, dim, false);
+  mg::NormResArgs a = {y, x, gamma_post, gate, gamma_pre, rows, dim, gates ? rows / gates : rows, scale, eps, x_out, h, rstd, 1, shape.stages, shape.row_units};
+  cudaStream_t s = (cudaStream_t)stream;
   cudaError_t e;
   if (!shape.threads) {
     e = dtype ? mg::norm_res_launch(mg::norm_res_wide_kernel<mg::bf16>, a, rows, mg::kNrThreads, 0, s)
               : mg::norm_res_launch(mg::norm_res_wide_kernel<float>, a, rows, mg::kNrThreads, 0, s);
   } else {
-    a.stages = shape.stages;
     const int slots = mg::norm_res_slots(shape, mg::kNrFwdThreads);
     a.block_rows = (rows + slots - 1) / slots;
     const long long blocks = (rows + a.block_rows - 1) / a.block_rows;
     if (dtype)
-      e = shape.ring ? mg::norm_res_forward<mg::bf16, true>(a, shape, blocks, s) : mg::norm_res_forward<mg::bf16, false>(a, shape, blocks, s);
+      e = shape.own ? mg::norm_res_forward<mg::bf16, true>(a, shape, blocks, s) : mg::norm_res_forward<mg::bf16, false>(a, shape, blocks, s);
     else
-      e = shape.ring ? mg::norm_res_forward<float, true>(a, shape, blocks, s) : mg::norm_res_forward<float, false>(a, shape, blocks, s);
+      e = shape.own ? mg::norm_res_forward<float, true>(a, shape, blocks, s) : mg::norm_res_forward<float, false>(a, shape, blocks, s);
   }
   return mg::op_end(fn, e);
 }
@@ -794,7 +827,7 @@ extern "C" mg_status mg_norm_residual_backward(int dtype, const void* dx_out, co
                             {workspace, need, true, false}});
   if (st != MG_OK) return st;
   mg::NormResGradArgs a = {dx_out, dh, y, x, rstd, gamma_post, gate, gamma_pre, rows, dim, 0, gates ? gates : 1, scale,
-                           dy, dx, dgamma_post, dgate, dgamma_pre, static_cast<float*>(workspace), 1, 1, 1, 0};
+                           dy, dx, dgamma_post, dgate, dgamma_pre, static_cast<float*>(workspace), 1, 1, 1, 0, 0};
   cudaStream_t s = (cudaStream_t)stream;
   if (!rows) {
     const long long blocks = ((long long)a.gates * dim + 255) / 256;
@@ -804,6 +837,7 @@ extern "C" mg_status mg_norm_residual_backward(int dtype, const void* dx_out, co
   const mg::NormResShape shape = mg::norm_res_shape(dtype, dim, true);
   const mg::NormResSplit split = mg::norm_res_split(rows, a.gates, mg::norm_res_slots(shape, mg::kNrGradThreads));
   a.stages = shape.stages;
+  a.row_units = shape.row_units;
   a.parts = split.parts;
   a.block_rows = split.block_rows;
   a.block_gates = split.block_gates;
@@ -812,10 +846,10 @@ extern "C" mg_status mg_norm_residual_backward(int dtype, const void* dx_out, co
     e = dtype ? mg::norm_res_launch(mg::norm_res_grad_wide_kernel<mg::bf16>, a, split.blocks, mg::kNrThreads, 0, s)
               : mg::norm_res_launch(mg::norm_res_grad_wide_kernel<float>, a, split.blocks, mg::kNrThreads, 0, s);
   else if (dtype)
-    e = shape.ring ? mg::norm_res_backward<mg::bf16, true>(a, shape, split.blocks, s)
+    e = shape.own ? mg::norm_res_backward<mg::bf16, true>(a, shape, split.blocks, s)
                    : mg::norm_res_backward<mg::bf16, false>(a, shape, split.blocks, s);
   else
-    e = shape.ring ? mg::norm_res_backward<float, true>(a, shape, split.blocks, s)
+    e = shape.own ? mg::norm_res_backward<float, true>(a, shape, split.blocks, s)
                    : mg::norm_res_backward<float, false>(a, shape, split.blocks, s);
   const int gate_blocks = dgate && a.parts > 1 && a.gates > 1 ? std::min(a.gates, 65533) : 0;
   if (e == cudaSuccess && (dgamma_post || dgamma_pre || (dgate && a.parts > 1)))

@@ -5,16 +5,32 @@
 //   logp    = (x[id] - m) / T - L
 //   entropy = L - sum_v p_v (x_v - m) / T        p_v = exp((x_v - m) / T - L)
 //   dx_v    = (g (1[v = id] - p_v) - h p_v (log p_v + entropy)) / T
+//
+// Forward: one read of the logits.  A thread keeps the maximum of its own elements
+// and, relative to it and in base 2, the sums of 2^t and of 2^t t; the block joins
+// them.  A block takes a row; few rows are split over a cluster of up to eight
+// blocks, whose results meet in the first one's shared memory.
+//
+// The k most likely: the k-th largest of the threads' maxima is at most the k-th
+// largest element, and few elements are as large.  The units of the threads that
+// hold any are read again (from L2) by all threads side by side, what is at least
+// that large is listed, and the list is ranked.  Where equal values make the list too
+// long, the smaller ones are left out and found in order of their places.
 #include <cmath>
 
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "kernels.h"
 #include "op_checks.h"
 
 namespace mg {
 namespace {
 
-constexpr int kLogpThreads = 256;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kNothing = -1000.0f;     // as an exponent of 2: 0, and finite
+constexpr int kLogpList = 512;           // candidates that are ranked
+constexpr int kLogpOwners = 64;          // threads whose elements are read again
+constexpr int kMaxCluster = 8;
 
 struct LogpArgs {
   const void* logits;
@@ -59,104 +75,503 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-__device__ __forceinline__ unsigned long long block_max_u64(unsigned long long v, unsigned long long* red) {
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = blockDim.x >> 5;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const unsigned long long t = __shfl_xor_sync(0xffffffffu, v, o);
-    v = t > v ? t : v;
-  }
-  __syncthreads();
-  if (lane == 0) red[w] = v;
-  __syncthreads();
-  v = lane < nw ? red[lane] : 0;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const unsigned long long t = __shfl_xor_sync(0xffffffffu, v, o);
-    v = t > v ? t : v;
-  }
-  return v;
+__device__ __forceinline__ float key_value(uint32_t key) {
+  return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);   // (of 0, which is NaN's: NaN)
+}
+// A value and its place in one integer: larger values first, of equal ones the lower place.
+__device__ __forceinline__ unsigned long long place_key(float x, int c) {
+  return (unsigned long long)order_key(x) << 32 | (uint32_t)~c;
 }
 
-// A row per block.
+__device__ __forceinline__ float exp2_near(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// The larger one, NaN if one is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// ---- a part of a row: whole 16-byte units, and single elements before and behind them
 template <typename T>
-__global__ void __launch_bounds__(kLogpThreads) logp_kernel(LogpArgs a) {
+struct Part {
+  static constexpr int kPer = 16 / (int)sizeof(T);
+  const T* x;        // its first element
+  int at;            // that element's place in the row
+  int head, units, tail;
+  __device__ __forceinline__ const uint4* unit(int u) const { return reinterpret_cast<const uint4*>(x + head) + u; }
+  __device__ __forceinline__ int unit_place(int u) const { return at + head + u * kPer; }
+  __device__ __forceinline__ const T* behind() const { return x + head + (size_t)units * kPer; }
+  __device__ __forceinline__ int count() const { return head + units * kPer + tail; }
+};
+// The part of rank `rank` of `ranks`: the units split evenly, the row's ends with the outer ones.
+template <typename T>
+__device__ __forceinline__ Part<T> part_of(const T* row, int n, int rank, int ranks) {
+  Part<T> p;
+  const int off = (int)((16 - reinterpret_cast<uintptr_t>(row) % 16) % 16 / sizeof(T));
+  const int head = min(off, n), units = (n - head) / Part<T>::kPer, tail = n - head - units * Part<T>::kPer;
+  const int begin = (int)((long long)units * rank / ranks), end = (int)((long long)units * (rank + 1) / ranks);
+  p.units = end - begin;
+  p.head = rank == 0 ? head : 0;
+  p.tail = rank == ranks - 1 ? tail : 0;
+  p.at = rank == 0 ? 0 : head + begin * Part<T>::kPer;
+  p.x = row + p.at;
+  return p;
+}
+__device__ __forceinline__ void widen(const uint4& u, f32x2 (&f)[4]) {
+  f[0] = widen2(u.x);
+  f[1] = widen2(u.y);
+  f[2] = widen2(u.z);
+  f[3] = widen2(u.w);
+}
+__device__ __forceinline__ void widen(const uint4& u, f32x2 (&f)[2]) {
+  f[0] = both(__uint_as_float(u.x), __uint_as_float(u.y));
+  f[1] = both(__uint_as_float(u.z), __uint_as_float(u.w));
+}
+__device__ __forceinline__ uint4 narrow(const f32x2 (&f)[4]) {
+  return make_uint4(narrow2(f[0]), narrow2(f[1]), narrow2(f[2]), narrow2(f[3]));
+}
+__device__ __forceinline__ uint4 narrow(const f32x2 (&f)[2]) {
+  const float2 a = parts(f[0]), b = parts(f[1]);
+  return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
+}
+// The largest of four units' values (a NaN only if all are).
+__device__ __forceinline__ float units_max(const uint4 (&u)[4], bf16) {
+  __nv_bfloat162 m = *reinterpret_cast<const __nv_bfloat162*>(&u[0].x);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const uint32_t w[4] = {u[q].x, u[q].y, u[q].z, u[q].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = __hmax2(m, *reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+  }
+  const float2 f = __bfloat1622float2(m);
+  return fmaxf(f.x, f.y);
+}
+__device__ __forceinline__ float units_max(const uint4 (&u)[4], float) {
+  float m = -INFINITY;
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    m = fmaxf(fmaxf(fmaxf(m, __uint_as_float(u[q].x)), fmaxf(__uint_as_float(u[q].y), __uint_as_float(u[q].z))),
+              __uint_as_float(u[q].w));
+  return m;
+}
+
+// The maximum m of some elements, and with t = (x - m) / T in base 2 the sums of 2^t and of 2^t t.
+struct RowSums {
+  float m, s, q;
+  // relative to a larger maximum
+  __device__ __forceinline__ void lift(float to, float c) {
+    const float d = max_nan((m - (to == -INFINITY ? 0.0f : to)) * c, kNothing), f = exp2_near(d);
+    q = f * fmaf(s, d, q);
+    s *= f;
+    m = to;
+  }
+  __device__ __forceinline__ void one(float x, float c) {
+    if (x > m) lift(x, c);
+    const float t = max_nan((x - (m == -INFINITY ? 0.0f : m)) * c, kNothing), e = exp2_near(t);
+    s += e;
+    q = fmaf(e, t, q);
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ RowSums row_sums(const Part<T>& p, float c) {
+  constexpr int pairs = Part<T>::kPer / 2;
+  constexpr uint32_t kNone = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;   // -inf
+  RowSums r = {-INFINITY, 0.0f, 0.0f};
+  const int step = blockDim.x;
+  const f32x2 cc = both(c);
+  for (int u0 = threadIdx.x; u0 < p.units; u0 += 4 * step) {
+    uint4 u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      u[i] = u0 + i * step < p.units ? *p.unit(u0 + i * step) : make_uint4(kNone, kNone, kNone, kNone);
+    const float top = units_max(u, T());
+    if (top > r.m) r.lift(top, c);
+    const f32x2 minus = both(r.m == -INFINITY ? 0.0f : -r.m);
+    f32x2 s = both(0.0f), q = both(0.0f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f32x2 f[pairs];
+      widen(u[i], f);
+#pragma unroll
+      for (int j = 0; j < pairs; ++j) {
+        const float2 d = parts(mul2(add2(f[j], minus), cc));
+        const float a = max_nan(d.x, kNothing), b = max_nan(d.y, kNothing);
+        const f32x2 e = both(exp2_near(a), exp2_near(b));
+        s = add2(s, e);
+        q = fma2(e, both(a, b), q);
+      }
+    }
+    const float2 ss = parts(s), qq = parts(q);
+    r.s += ss.x + ss.y;
+    r.q += qq.x + qq.y;
+  }
+  if ((int)threadIdx.x < p.head) r.one(ld_elem(p.x, threadIdx.x), c);
+  if ((int)threadIdx.x < p.tail) r.one(ld_elem(p.behind(), threadIdx.x), c);
+  return r;
+}
+
+// ---- the most likely ------------------------------------------------------------
+struct TopShared {
+  uint32_t maxima[512];                       // the threads', as keys
+  unsigned long long list[kLogpList];
+  int owner[kLogpOwners];
+  int n_owners, n_list, n_more;
+  uint32_t threshold;
+  unsigned long long best[MG_MAX_TOP];        // in order; 0 where there are fewer
+};
+
+// The k-th largest of the N threads' maxima, by the first warp.  (Keys of bf16 values
+// end in 16 equal bits: zeros, or ones below zero.)
+template <typename T, int N>
+__device__ __forceinline__ uint32_t kth_maximum(const TopShared& t, int k) {
+  const int lane = threadIdx.x & 31;
+  uint32_t v[N / 32];
+#pragma unroll
+  for (int i = 0; i < N / 32; ++i) v[i] = t.maxima[32 * i + lane];
+  uint32_t lo = 0;
+  for (int bit = 31; bit >= (sizeof(T) == 2 ? 16 : 0); --bit) {
+    const uint32_t mid = lo | 1u << bit;
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < N / 32; ++i) n += v[i] >= mid;
+    if ((int)__reduce_add_sync(0xffffffffu, n) >= k) lo = mid;
+  }
+  return sizeof(T) == 2 && lo && !(lo & 0x80000000u) ? lo | 0xffffu : lo;
+}
+
+// Every element of the part: f(value, place in the row).
+template <typename T, typename F>
+__device__ __forceinline__ void each_of_unit(const Part<T>& p, int u, F&& f) {
+  const uint4 w = *p.unit(u);
+  f32x2 v[Part<T>::kPer / 2];
+  widen(w, v);
+#pragma unroll
+  for (int j = 0; j < Part<T>::kPer / 2; ++j) {
+    const float2 d = parts(v[j]);
+    f(d.x, p.unit_place(u) + 2 * j);
+    f(d.y, p.unit_place(u) + 2 * j + 1);
+  }
+}
+template <typename T, typename F>
+__device__ __forceinline__ void each_element(const Part<T>& p, F&& f) {
+  for (int u = threadIdx.x; u < p.units; u += blockDim.x) each_of_unit(p, u, f);
+  if ((int)threadIdx.x < p.head) f(ld_elem(p.x, threadIdx.x), p.at + threadIdx.x);
+  if ((int)threadIdx.x < p.tail) f(ld_elem(p.behind(), threadIdx.x), p.at + p.count() - p.tail + threadIdx.x);
+}
+
+// Lists the elements whose keys are at least `least`, of the threads whose maxima
+// are; false if there are more than the list holds.
+template <typename T>
+__device__ bool list_from(const Part<T>& p, TopShared& t, uint32_t least) {
+  if (threadIdx.x == 0) t.n_owners = t.n_list = 0;
+  __syncthreads();
+  if (t.maxima[threadIdx.x] >= least) {
+    const int i = atomicAdd(&t.n_owners, 1);
+    if (i < kLogpOwners) t.owner[i] = threadIdx.x;
+  }
+  __syncthreads();
+  const int owners = t.n_owners;
+  if (owners > kLogpOwners) return false;
+  const auto add = [&](float x, int c) {
+    if (order_key(x) < least) return;
+    const int i = atomicAdd(&t.n_list, 1);
+    if (i < kLogpList) t.list[i] = place_key(x, c);
+  };
+  const int each = (p.units + blockDim.x - 1) / blockDim.x + 2;   // units of a thread, and its single elements
+  for (int i = threadIdx.x; i < owners * each; i += blockDim.x) {
+    const int who = t.owner[i / each], j = i % each, u = who + (j - 2) * (int)blockDim.x;
+    if (j >= 2) {
+      if (u < p.units) each_of_unit(p, u, add);
+    } else if (j == 0 && who < p.head) {
+      add(ld_elem(p.x, who), p.at + who);
+    } else if (j == 1 && who < p.tail) {
+      add(ld_elem(p.behind(), who), p.at + p.count() - p.tail + who);
+    }
+  }
+  __syncthreads();
+  return t.n_list <= kLogpList;
+}
+
+// The listed keys in order to t.best[0 .. k-1]; returns after a barrier.
+__device__ __forceinline__ void rank_list(TopShared& t, int n, int k) {
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    const unsigned long long v = t.list[i];
+    int above = 0;
+    for (int j = 0; j < n; ++j) above += t.list[j] > v;
+    if (above < k) t.best[above] = v;
+  }
+  __syncthreads();
+}
+
+// The part's k largest (fewer if it has fewer) in order in t.best.
+template <typename T, int N>
+__device__ void top_of_part(const Part<T>& p, TopShared& t, int k, float maximum) {
+  k = min(k, p.count());
+  const bool any = (int)threadIdx.x < p.units || (int)threadIdx.x < p.head || (int)threadIdx.x < p.tail;
+  t.maxima[threadIdx.x] = any ? order_key(maximum) : 0u;
+  if (threadIdx.x < MG_MAX_TOP) t.best[threadIdx.x] = 0;
+  __syncthreads();
+  if (k == 0) return;
+  if (threadIdx.x < 32) {
+    const uint32_t v = kth_maximum<T, N>(t, k);
+    if (threadIdx.x == 0) t.threshold = v;
+  }
+  __syncthreads();
+  uint32_t th = t.threshold;
+  if (list_from(p, t, th) && t.n_list >= k) {
+    rank_list(t, t.n_list, k);
+    return;
+  }
+  // Too many of the threshold itself, or (behind maxima of -inf that are NaN) too few
+  // of it: those above it, then equal ones in order of their places.
+  __syncthreads();
+  if (!list_from(p, t, th + 1)) {
+    // Many large values in few threads' hands: the exact k-th largest, bit by bit.
+    uint32_t lo = 0;
+    for (int bit = 31; bit >= 0; --bit) {
+      const uint32_t mid = lo | 1u << bit;
+      if (threadIdx.x == 0) t.n_more = 0;
+      __syncthreads();
+      int n = 0;
+      each_element(p, [&](float x, int) { n += order_key(x) >= mid; });
+      n = __reduce_add_sync(0xffffffffu, n);
+      if ((threadIdx.x & 31) == 0) atomicAdd(&t.n_more, n);
+      __syncthreads();
+      if (t.n_more >= k) lo = mid;
+      __syncthreads();
+    }
+    th = lo;
+    if (threadIdx.x == 0) t.n_list = 0;
+    __syncthreads();
+    each_element(p, [&](float x, int c) {
+      if (order_key(x) > th) t.list[atomicAdd(&t.n_list, 1)] = place_key(x, c);   // fewer than k
+    });
+    __syncthreads();
+  }
+  const int above = min(t.n_list, k);
+  rank_list(t, t.n_list, k);
+  // equal ones: of each step's elements in order, until there are enough
+  int have = above;
+  for (int round = 0; round < 2 && have < k; ++round, th = 0) {   // (the second: NaN)
+    for (int c0 = 0; c0 < p.count() && have < k; c0 += blockDim.x) {
+      const int i = c0 + threadIdx.x;
+      const bool is = i < p.count() && order_key(ld_elem(p.x, i)) == th;
+      const unsigned votes = __ballot_sync(0xffffffffu, is);
+      const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+      if (lane == 0) t.owner[warp] = __popc(votes);
+      __syncthreads();
+      int before = have, all = have;
+      for (int w = 0; w < (int)blockDim.x / 32; ++w) {
+        if (w < warp) before += t.owner[w];
+        all += t.owner[w];
+      }
+      before += __popc(votes & ((1u << lane) - 1));
+      if (is && before < k) t.best[before] = (unsigned long long)th << 32 | (uint32_t)~(p.at + i);
+      have = min(all, k);
+      __syncthreads();
+    }
+    if (th == 0) break;
+  }
+}
+
+// ---- clusters ---------------------------------------------------------------------
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Another block's shared memory at the place of p in this one's.
+template <typename V>
+__device__ __forceinline__ const V* of_rank(const V* p, int rank) {
+  uint64_t r;
+  asm("mapa.u64 %0, %1, %2;" : "=l"(r) : "l"((uint64_t)p), "r"(rank));
+  return reinterpret_cast<const V*>(r);
+}
+
+// A row per cluster of blocks of N threads.
+template <typename T, bool TOP, int N>
+__global__ void __launch_bounds__(N) logp_kernel(LogpArgs a, int ranks) {
   __shared__ float red[32];
-  __shared__ unsigned long long red64[32];
-  const size_t r = blockIdx.x;
+  __shared__ RowSums mine;
+  __shared__ TopShared top[1];   // (nothing refers to it without TOP)
+  const size_t r = blockIdx.x / ranks;
+  const int rank = blockIdx.x % ranks;
   const T* x = static_cast<const T*>(a.logits) + r * a.stride;
   const int id = a.ids ? token_of(a.ids, a.id64, a.vocab, r) : 0;
-  if (id < 0) {
+  if (id < 0) {   // (in all blocks of the cluster)
+    if (rank) return;
     if (threadIdx.x == 0) {
       a.logp[r] = 0.0f;
       if (a.stats) a.stats[2 * r] = a.stats[2 * r + 1] = 0.0f;
       if (a.entropy) a.entropy[r] = 0.0f;
     }
-    for (int i = threadIdx.x; i < a.k; i += kLogpThreads) {
+    for (int i = threadIdx.x; i < a.k; i += blockDim.x) {
       a.top_ids[r * a.k + i] = -1;
       a.top_logp[r * a.k + i] = 0.0f;
     }
     return;
   }
-  float m = -INFINITY;
-  for (int c = threadIdx.x; c < a.vocab; c += kLogpThreads) m = fmaxf(m, ld_elem(x, c));
-  m = block_max(m, red);
-  const float mm = m == -INFINITY ? 0.0f : m;
-  float s = 0.0f, q = 0.0f;
-  for (int c = threadIdx.x; c < a.vocab; c += kLogpThreads) {
-    const float t = (ld_elem(x, c) - mm) * a.inv_t, e = expf(t);
-    s += e;
-    if (e > 0.0f) q += e * t;
+  const float given = threadIdx.x == 0 && rank == 0 && a.logp ? ld_elem(x, id) : 0.0f;   // (ahead of the row)
+  const Part<T> p = part_of(x, a.vocab, rank, ranks);
+  const float c = a.inv_t * kLog2e;
+  RowSums t = row_sums(p, c);
+  const float maximum = t.m;
+  t.lift(block_max(t.m, red), c);
+  t.s = block_sum(t.s, red);
+  t.q = block_sum(t.q, red);
+  if (TOP) top_of_part<T, N>(p, top[0], a.k, maximum);
+  if (ranks > 1) {
+    if (threadIdx.x == 0) mine = t;
+    cluster_sync();
+    if (rank == 0) {
+      RowSums all[kMaxCluster];
+      float m = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < kMaxCluster; ++i) {
+        if (i < ranks) all[i] = *of_rank(&mine, i);
+        m = i < ranks ? fmaxf(m, all[i].m) : m;
+      }
+      t = {m, 0.0f, 0.0f};
+#pragma unroll
+      for (int i = 0; i < kMaxCluster; ++i) {
+        if (i >= ranks) continue;
+        all[i].lift(m, c);
+        t.s += all[i].s;
+        t.q += all[i].q;
+      }
+      if (TOP) {
+        for (int i = threadIdx.x; i < ranks * MG_MAX_TOP; i += blockDim.x)
+          top[0].list[i] = *of_rank(&top[0].best[i % MG_MAX_TOP], i / MG_MAX_TOP);
+        __syncthreads();
+        // (absent ones are 0, less than every element's key; they may share a rank that is not written)
+        rank_list(top[0], ranks * MG_MAX_TOP, a.k);
+      }
+    }
+    cluster_sync();
+    if (rank) return;
   }
-  s = block_sum(s, red);
-  q = block_sum(q, red);
-  const float ls = logf(s);
-  const bool none = s == 0.0f;   // every logit is -inf
+  const float m = t.m == -INFINITY ? 0.0f : t.m, ls = logf(t.s);
+  const bool none = t.s == 0.0f;   // every logit is -inf
   if (threadIdx.x == 0) {
-    if (a.logp) a.logp[r] = none ? -INFINITY : (ld_elem(x, id) - mm) * a.inv_t - ls;
-    if (a.stats) {
-      a.stats[2 * r] = m;
-      a.stats[2 * r + 1] = ls;
-    }
-    if (a.entropy) a.entropy[r] = none ? 0.0f : ls - q / s;
+    if (a.logp) a.logp[r] = none ? -INFINITY : (given - m) * a.inv_t - ls;
+    if (a.stats) *reinterpret_cast<float2*>(a.stats + 2 * r) = make_float2(t.m, ls);
+    if (a.entropy) a.entropy[r] = none ? 0.0f : ls - t.q / t.s * kLn2;
   }
-  unsigned long long last = ~0ull;
-  for (int i = 0; i < a.k; ++i) {
-    unsigned long long best = 0;
-    for (int c = threadIdx.x; c < a.vocab; c += kLogpThreads) {
-      const unsigned long long v = (unsigned long long)order_key(ld_elem(x, c)) << 32 | (uint32_t)~c;
-      if (v < last && v > best) best = v;
-    }
-    last = block_max_u64(best, red64);
-    if (threadIdx.x == 0) {
-      const int c = (int)~(uint32_t)last;
-      a.top_ids[r * a.k + i] = c;
-      a.top_logp[r * a.k + i] = none ? -INFINITY : (ld_elem(x, c) - mm) * a.inv_t - ls;
+  if (TOP) {
+    for (int i = threadIdx.x; i < a.k; i += blockDim.x) {
+      const unsigned long long v = top[0].best[i];
+      a.top_ids[r * a.k + i] = (int)~(uint32_t)v;
+      a.top_logp[r * a.k + i] = none ? -INFINITY : (key_value((uint32_t)(v >> 32)) - m) * a.inv_t - ls;
     }
   }
 }
 
+// ---- gradient -----------------------------------------------------------------------
+// A block takes a row, or one of `ranks` parts of it.
 template <typename T>
-__global__ void __launch_bounds__(kLogpThreads) logp_grad_kernel(LogpGradArgs a) {
-  const size_t r = blockIdx.x;
+__global__ void __launch_bounds__(256) logp_grad_kernel(LogpGradArgs a, int ranks) {
+  constexpr int per = Part<T>::kPer, pairs = per / 2;
+  const size_t r = blockIdx.x / ranks;
   const T* x = static_cast<const T*>(a.logits) + r * a.stride;
   T* dx = static_cast<T*>(a.dlogits) + r * a.dstride;
   const int id = a.ids ? token_of(a.ids, a.id64, a.vocab, r) : 0;
-  const float g = a.dlogp && id >= 0 ? a.dlogp[r] : 0.0f;
-  const float h = a.dentropy && id >= 0 ? a.dentropy[r] : 0.0f;
-  const float m = a.stats[2 * r], ls = a.stats[2 * r + 1];
-  if ((g == 0.0f && h == 0.0f) || m == -INFINITY) {
-    for (int c = threadIdx.x; c < a.vocab; c += kLogpThreads) st_elem(dx, c, 0.0f);
+  const float g = a.dlogp && id >= 0 ? a.dlogp[r] * a.inv_t : 0.0f;
+  const float h = a.dentropy && id >= 0 ? a.dentropy[r] * a.inv_t : 0.0f;
+  const float2 st = *reinterpret_cast<const float2*>(a.stats + 2 * r);
+  // by the places of the gradient's units; the logits' are the same, or they are taken one by one
+  const bool same = (reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(dx)) % 16 == 0;
+  const Part<T> p = part_of(static_cast<const T*>(dx), a.vocab, blockIdx.x % ranks, ranks);
+  T* const to = dx + p.at;
+  const T* const from = x + p.at;
+  const int step = blockDim.x, behind = p.head + p.units * per;
+  if ((g == 0.0f && h == 0.0f) || st.x == -INFINITY) {
+    for (int u = threadIdx.x; u < p.units; u += step) reinterpret_cast<uint4*>(to + p.head)[u] = make_uint4(0, 0, 0, 0);
+    if ((int)threadIdx.x < p.head) st_elem(to, threadIdx.x, 0.0f);
+    if ((int)threadIdx.x < p.tail) st_elem(to, behind + threadIdx.x, 0.0f);
     return;
   }
-  const float ent = a.dentropy ? a.entropy[r] : 0.0f;
-  for (int c = threadIdx.x; c < a.vocab; c += kLogpThreads) {
-    const float lp = (ld_elem(x, c) - m) * a.inv_t - ls, p = expf(lp);
-    float d = -g * p;
-    if (p != 0.0f) d -= h * p * (lp + ent);
-    if (c == id) d += g;
-    st_elem(dx, c, d * a.inv_t);
+  // in base 2: l = (x - m) c - L, p = 2^l, dx = p (k0 + k1 l) (+ g at the given token)
+  const float ent = a.dentropy ? a.entropy[r] : 0.0f, k0 = -fmaf(h, ent, g), k1 = -h * kLn2;
+  const f32x2 minus = both(-st.x), c = both(a.inv_t * kLog2e), l0 = both(-st.y * kLog2e), c0 = both(k0), c1 = both(k1);
+  const auto slope = [&](f32x2 v) {
+    const float2 d = parts(fma2(add2(v, minus), c, l0));
+    const float l = max_nan(d.x, kNothing), n = max_nan(d.y, kNothing);
+    return mul2(both(exp2_near(l), exp2_near(n)), fma2(c1, both(l, n), c0));
+  };
+  const int at_id = a.dlogp ? id - p.at : -1;   // the given token's place in the part
+  const auto single = [&](int i) {
+    const float d = parts(slope(both(ld_elem(from, i)))).x;
+    st_elem(to, i, i == at_id ? d + g : d);
+  };
+  if (same) {
+    const uint4* in = reinterpret_cast<const uint4*>(from + p.head);
+    uint4* out = reinterpret_cast<uint4*>(to + p.head);
+    const int id_unit = at_id >= p.head ? (at_id - p.head) / per : -1, id_in = (at_id - p.head) % per;
+    for (int u0 = threadIdx.x; u0 < p.units; u0 += 4 * step) {
+      uint4 w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = u0 + i * step < p.units ? in[u0 + i * step] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int u = u0 + i * step;
+        if (u >= p.units) continue;
+        f32x2 f[pairs];
+        widen(w[i], f);
+#pragma unroll
+        for (int j = 0; j < pairs; ++j) f[j] = slope(f[j]);
+        if (u == id_unit) {
+#pragma unroll
+          for (int j = 0; j < pairs; ++j) f[j] = add2(f[j], both(id_in == 2 * j ? g : 0.0f, id_in == 2 * j + 1 ? g : 0.0f));
+        }
+        out[u] = narrow(f);
+      }
+    }
+  } else {
+    for (int i = p.head + threadIdx.x; i < behind; i += step) single(i);
   }
+  if ((int)threadIdx.x < p.head) single(threadIdx.x);
+  if ((int)threadIdx.x < p.tail) single(behind + threadIdx.x);
+}
+
+// Many rows: 128 threads each, so that a row's sums are joined by few warps.  Few rows:
+// 512 threads, and as many blocks to a row, up to eight, as fill the multiprocessors
+// while a thread still has two units.
+template <typename T>
+cudaError_t logp_forward(const LogpArgs& a, int rows, cudaStream_t s) {
+  const int sms = device_sms();
+  int threads = 128, ranks = 1;
+  if (rows < 4 * sms) {
+    threads = 512;
+    while (ranks < kMaxCluster && 2 * ranks * rows <= 2 * sms && (long long)a.vocab * (int)sizeof(T) / 16 >= 4ll * ranks * threads)
+      ranks *= 2;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((long long)rows * ranks));
+  cfg.blockDim = dim3(threads);
+  cfg.stream = s;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = ranks;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  cudaError_t e;
+  if (threads == 128)
+    e = a.k ? cudaLaunchKernelEx(&cfg, logp_kernel<T, true, 128>, a, ranks) : cudaLaunchKernelEx(&cfg, logp_kernel<T, false, 128>, a, ranks);
+  else
+    e = a.k ? cudaLaunchKernelEx(&cfg, logp_kernel<T, true, 512>, a, ranks) : cudaLaunchKernelEx(&cfg, logp_kernel<T, false, 512>, a, ranks);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+template <typename T>
+cudaError_t logp_backward(const LogpGradArgs& a, int rows, cudaStream_t s) {
+  int ranks = 1;
+  const int sms = device_sms();
+  while (2ll * ranks * rows <= 8 * sms && (long long)a.vocab * (int)sizeof(T) / 16 >= 512ll * ranks) ranks *= 2;
+  logp_grad_kernel<T><<<(unsigned)((long long)rows * ranks), 256, 0, s>>>(a, ranks);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -201,11 +616,8 @@ extern "C" mg_status mg_token_logprobs(int dtype, const void* logits, long long 
                             {top_ids, nk, true, false}, {top_logp, nk, true, false}});
   if (st != MG_OK || !rows) return st;
   mg::LogpArgs a = {logits, row_stride, vocab, ids, id_kind, 1.0f / temperature, logp, stats, entropy, k, top_ids, top_logp};
-  if (dtype)
-    mg::logp_kernel<mg::bf16><<<(unsigned)rows, mg::kLogpThreads, 0, (cudaStream_t)stream>>>(a);
-  else
-    mg::logp_kernel<float><<<(unsigned)rows, mg::kLogpThreads, 0, (cudaStream_t)stream>>>(a);
-  return mg::op_end(fn, cudaGetLastError());
+  return mg::op_end(fn, dtype ? mg::logp_forward<mg::bf16>(a, (int)rows, (cudaStream_t)stream)
+                              : mg::logp_forward<float>(a, (int)rows, (cudaStream_t)stream));
 }
 
 extern "C" mg_status mg_token_logprobs_backward(int dtype, const void* logits, long long rows, int vocab,
@@ -232,9 +644,6 @@ extern "C" mg_status mg_token_logprobs_backward(int dtype, const void* logits, l
   if (st != MG_OK || !rows) return st;
   mg::LogpGradArgs a = {logits, row_stride, vocab, ids, id_kind, 1.0f / temperature, stats, entropy, dlogp, dentropy, dlogits,
                         dlogits_stride};
-  if (dtype)
-    mg::logp_grad_kernel<mg::bf16><<<(unsigned)rows, mg::kLogpThreads, 0, (cudaStream_t)stream>>>(a);
-  else
-    mg::logp_grad_kernel<float><<<(unsigned)rows, mg::kLogpThreads, 0, (cudaStream_t)stream>>>(a);
-  return mg::op_end(fn, cudaGetLastError());
+  return mg::op_end(fn, dtype ? mg::logp_backward<mg::bf16>(a, (int)rows, (cudaStream_t)stream)
+                              : mg::logp_backward<float>(a, (int)rows, (cudaStream_t)stream));
 }
