@@ -453,8 +453,8 @@ mg_status mg_grad_list_clip(mg_grad_list* list, float max_norm, float* stats, mg
  * Each output may be NULL, but one (ids and logp are given together; k = 0: no
  * top_ids and top_logp).  k is at most MG_MAX_TOP and vocab.  fp32 sums; outputs
  * are fp32 and int32.
- * A row whose id is outside [0, vocab) -- padding -- is not read: its outputs are
- * 0, its top_ids -1.  Logits of -inf have probability 0; a row of nothing else
+ * A row whose id is outside [0, vocab) -- padding -- enters nothing, whatever it holds:
+ * its outputs are 0, its top_ids -1.  Logits of -inf have probability 0; a row of nothing else
  * has logp and top_logp -inf, entropy 0 and no gradient.  A row that holds a NaN
  * or +inf has NaN in logp, entropy and top_logp (its top_ids are in order, NaN
  * below -inf).

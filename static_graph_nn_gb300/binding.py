@@ -595,6 +595,17 @@ class GradList:
             pass
 
 
+def _at(t, name: str, dtype, shape) -> int | None:
+    """The address of a contiguous tensor of this type and shape (None: none)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        if t.dtype is not dtype:
+            _refuse(f"{name} must be {dtype}, not {t.dtype}")
+        _dense(t, name, shape)
+    return t.data_ptr()
+
+
 # ---- log probabilities of tokens ------------------------------------------------
 def _logit_rows(t, name: str) -> tuple[int, int, int]:
     """(rows, vocab, row stride) of logits [..., vocab]: any row stride for two
@@ -625,29 +636,21 @@ def token_logprobs(logits, ids=None, logp=None, stats=None, entropy=None, top_id
     rows [...]: ids int32 or int64, logp and entropy fp32 [...], stats fp32 [..., 2]
     (for the backward), top_ids int32 and top_logp fp32 [..., k], k up to 32.  Any
     of them may be left out, ids together with logp.  A row whose id is outside
-    [0, vocab) is not read: zeros, top_ids -1."""
+    [0, vocab) enters nothing: zeros, top_ids -1."""
+    code, kinds, f32, i32 = _type_tables()
     rows, v, ld = _logit_rows(logits, "logits")
     lead = logits.shape[:-1]
-    kind, k = 0, 0
-    if ids is not None:
-        kind = _code(ids, "ids", _type_tables()[1])
-        _dense(ids, "ids", lead)
-    if logp is not None:
-        _per_row(logp, "logp", lead)
-    if entropy is not None:
-        _per_row(entropy, "entropy", lead)
-    if stats is not None:
-        _per_row(stats, "stats", lead + (2,))
-    if (top_ids is None) != (top_logp is None):
-        _refuse("top_ids and top_logp are given together")
-    if top_ids is not None:
+    kind = 0 if ids is None else _code(ids, "ids", kinds)
+    k = 0
+    if top_ids is not None or top_logp is not None:
+        if top_ids is None or top_logp is None:
+            _refuse("top_ids and top_logp are given together")
         k = top_ids.shape[-1] if top_ids.dim() else 0
         _fits(k)
-        _per_row(top_ids, "top_ids", lead + (k,), _type_tables()[3])
-        _per_row(top_logp, "top_logp", lead + (k,))
-    _status(load().mg_token_logprobs(_code(logits, "logits"), _ptr(logits), rows, v, ld, kind, _ptr(ids), temperature,
-                                     _ptr(logp), _ptr(stats), _ptr(entropy), k, _ptr(top_ids), _ptr(top_logp),
-                                     _stream(stream)))
+    _status((_lib or load()).mg_token_logprobs(
+        _code(logits, "logits", code), logits.data_ptr(), rows, v, ld, kind, None if ids is None else _at(ids, "ids", ids.dtype, lead),
+        temperature, _at(logp, "logp", f32, lead), _at(stats, "stats", f32, lead + (2,)), _at(entropy, "entropy", f32, lead), k,
+        _at(top_ids, "top_ids", i32, lead + (k,)), _at(top_logp, "top_logp", f32, lead + (k,)), _stream(stream)))
 
 
 def token_logprobs_backward(logits, ids, stats, dlogp, dlogits, entropy=None, dentropy=None,
@@ -662,17 +665,12 @@ def token_logprobs_backward(logits, ids, stats, dlogp, dlogits, entropy=None, de
         _refuse(f"dlogits has shape {tuple(dlogits.shape)}, expected {tuple(logits.shape)}", MG_ERR_SHAPE)
     _same_type(logits, "logits", dlogits, "dlogits")
     ldd = _logit_rows(dlogits, "dlogits")[2]
-    kind = 0
-    if ids is not None:
-        kind = _code(ids, "ids", _type_tables()[1])
-        _dense(ids, "ids", lead)
-    _per_row(stats, "stats", lead + (2,))
-    for t, name in ((entropy, "entropy"), (dlogp, "dlogp"), (dentropy, "dentropy")):
-        if t is not None:
-            _per_row(t, name, lead)
-    _status(load().mg_token_logprobs_backward(_code(logits, "logits"), _ptr(logits), rows, v, ld, kind, _ptr(ids),
-                                              temperature, _ptr(stats), _ptr(entropy), _ptr(dlogp), _ptr(dentropy),
-                                              _ptr(dlogits), ldd, _stream(stream)))
+    code, kinds, f32, _ = _type_tables()
+    kind = 0 if ids is None else _code(ids, "ids", kinds)
+    _status((_lib or load()).mg_token_logprobs_backward(
+        _code(logits, "logits", code), logits.data_ptr(), rows, v, ld, kind, None if ids is None else _at(ids, "ids", ids.dtype, lead),
+        temperature, _at(stats, "stats", f32, lead + (2,)), _at(entropy, "entropy", f32, lead), _at(dlogp, "dlogp", f32, lead),
+        _at(dentropy, "dentropy", f32, lead), dlogits.data_ptr(), ldd, _stream(stream)))
 
 
 # ---- between two blocks of a residual network ------------------------------------
@@ -683,30 +681,21 @@ def norm_residual_workspace_bytes(rows: int, dim: int, gates: int = 0) -> int:
     return load().mg_norm_residual_workspace_bytes(rows, dim, gates)
 
 
-def _residual_args(x, gate, vectors):
-    """(rows, dim, gates) of [..., dim] and its fp32 vectors."""
-    if x.dim() < 1 or x.shape[-1] < 1:
+def _residual_args(x, gate):
+    """(type code, rows, dim, gates) of contiguous x [..., dim] and its gate."""
+    shape = x.shape
+    if not shape or shape[-1] < 1:
         _refuse("x must be [..., dim]", MG_ERR_SHAPE)
-    d = x.shape[-1]
+    _dense(x, "x")
+    d = shape[-1]
     rows = x.numel() // d
-    _fits(rows, d)
-    for t, name in vectors:
-        if t is not None:
-            _per_row(t, name, (d,))
     gates = 0
     if gate is not None:
         gates = 1 if gate.dim() == 1 else gate.shape[0]
-        _fits(gates)
-        _per_row(gate, "gate", (d,) if gate.dim() == 1 else (gates, d))
-    return rows, d, gates
-
-
-def _rows_like(x, tensors):
-    _dense(x, "x")
-    for t, name in tensors:
-        if t is not None:
-            _dense(t, name, x.shape)
-            _same_type(x, "x", t, name)
+        if gate.shape != ((d,) if gate.dim() == 1 else (gates, d)):
+            _refuse(f"gate has shape {tuple(gate.shape)}, expected [{d}] or [gates, {d}]", MG_ERR_SHAPE)
+    _fits(rows, d, gates)
+    return _code(x, "x"), rows, d, gates
 
 
 def norm_residual_forward(y, x, x_out, h=None, gamma_post=None, gate=None, gamma_pre=None, scale: float = 1.0,
@@ -718,13 +707,12 @@ def norm_residual_forward(y, x, x_out, h=None, gamma_post=None, gate=None, gamma
     gamma_post y is added as it is, without gate it is not scaled, and without h
     and gamma_pre there is no second norm.  rstd fp32 [..., 2] is for the backward.
     x_out and h may each be y or x."""
-    rows, d, gates = _residual_args(x, gate, ((gamma_post, "gamma_post"), (gamma_pre, "gamma_pre")))
-    _rows_like(x, ((y, "y"), (x_out, "x_out"), (h, "h")))
-    if rstd is not None:
-        _per_row(rstd, "rstd", x.shape[:-1] + (2,))
-    _status(load().mg_norm_residual_forward(_code(x, "x"), _ptr(y), _ptr(x), rows, d, _ptr(gamma_post), _ptr(gate),
-                                            gates, scale, _ptr(gamma_pre), eps, _ptr(x_out), _ptr(h), _ptr(rstd),
-                                            _stream(stream)))
+    code, rows, d, gates = _residual_args(x, gate)
+    t, shape, v, f32 = x.dtype, x.shape, (d,), _type_tables()[2]
+    _status((_lib or load()).mg_norm_residual_forward(
+        code, _at(y, "y", t, shape), x.data_ptr(), rows, d, _at(gamma_post, "gamma_post", f32, v),
+        None if gate is None else _at(gate, "gate", f32, gate.shape), gates, scale, _at(gamma_pre, "gamma_pre", f32, v), eps,
+        _at(x_out, "x_out", t, shape), _at(h, "h", t, shape), _at(rstd, "rstd", f32, shape[:-1] + (2,)), _stream(stream)))
 
 
 def norm_residual_backward(dx_out, dh, y, x, rstd, dy, dx, workspace, gamma_post=None, gate=None, gamma_pre=None,
@@ -733,19 +721,18 @@ def norm_residual_backward(dx_out, dh, y, x, rstd, dy, dx, workspace, gamma_post
     dgamma_pre [dim] and dgate (fp32; of the gate's shape), from dx_out and dh (either
     may be None), the forward's inputs and its rstd.  workspace: a byte tensor of
     norm_residual_workspace_bytes.  dy and dx may each be dx_out, dh, y or x."""
-    rows, d, gates = _residual_args(x, gate, ((gamma_post, "gamma_post"), (gamma_pre, "gamma_pre"),
-                                              (dgamma_post, "dgamma_post"), (dgamma_pre, "dgamma_pre")))
-    _rows_like(x, ((dx_out, "dx_out"), (dh, "dh"), (y, "y"), (dy, "dy"), (dx, "dx")))
-    _per_row(rstd, "rstd", x.shape[:-1] + (2,))
-    if dgate is not None:
-        if gate is None:
-            _refuse("dgate without a gate")
-        _per_row(dgate, "dgate", tuple(gate.shape))
+    code, rows, d, gates = _residual_args(x, gate)
+    t, shape, v, f32 = x.dtype, x.shape, (d,), _type_tables()[2]
+    if dgate is not None and gate is None:
+        _refuse("dgate without a gate")
     _dense(workspace, "workspace")
-    _status(load().mg_norm_residual_backward(_code(x, "x"), _ptr(dx_out), _ptr(dh), _ptr(y), _ptr(x), _ptr(rstd), rows,
-                                             d, _ptr(gamma_post), _ptr(gate), gates, scale, _ptr(gamma_pre), _ptr(dy),
-                                             _ptr(dx), _ptr(dgamma_post), _ptr(dgate), _ptr(dgamma_pre),
-                                             _ptr(workspace), workspace.nbytes, _stream(stream)))
+    _status((_lib or load()).mg_norm_residual_backward(
+        code, _at(dx_out, "dx_out", t, shape), _at(dh, "dh", t, shape), _at(y, "y", t, shape), x.data_ptr(),
+        _at(rstd, "rstd", f32, shape[:-1] + (2,)), rows, d, _at(gamma_post, "gamma_post", f32, v),
+        None if gate is None else _at(gate, "gate", f32, gate.shape), gates, scale, _at(gamma_pre, "gamma_pre", f32, v),
+        _at(dy, "dy", t, shape), _at(dx, "dx", t, shape), _at(dgamma_post, "dgamma_post", f32, v),
+        None if dgate is None else _at(dgate, "dgate", f32, gate.shape), _at(dgamma_pre, "dgamma_pre", f32, v),
+        workspace.data_ptr(), workspace.nbytes, _stream(stream)))
 
 
 # ---- AdamW over many tensors -------------------------------------------------------

@@ -499,6 +499,7 @@ __global__ void __launch_bounds__(T0, T0 == 512 ? 1 : OWN ? 4 : 3) norm_res_grad
         }
       }
     }
+    if (a.parts > 1) dependents_start();   // (the join waits for the whole grid all the same)
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const float2 f = parts(sp[p]);
@@ -609,7 +610,7 @@ __global__ void __launch_bounds__(kNrThreads) norm_res_grad_wide_kernel(NormResG
 // and then in order.  blockIdx.y: 0 the post norm's (and that of a gate for all rows,
 // which is made of the same sums), 1 the pre norm's, beyond the gates' (blocks have
 // parts of them).
-__global__ void __launch_bounds__(1024) norm_res_join_kernel(NormResGradArgs a, int blocks) {
+__global__ void __launch_bounds__(1024, 2) norm_res_join_kernel(NormResGradArgs a, int blocks) {
   __shared__ float red[32][33];
   const int lane = threadIdx.x & 31, run = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
   const bool in = c < a.dim, gated = blockIdx.y == 0 && a.gate && a.parts > 1 && a.gates > 1;
@@ -618,12 +619,17 @@ __global__ void __launch_bounds__(1024) norm_res_join_kernel(NormResGradArgs a, 
     const int per = (n + 31) / 32, begin = min(n, run * per), end = min(n, begin + per);
     const float* v = a.ws + (from * 2 + which) * a.dim + c;
     float s = 0.0f;
-    if (in) {
-      if (gated)
-        for (int i = begin; i < end; ++i) s = fmaf(a.gate[(size_t)(i / a.parts) * a.dim + c], v[(size_t)i * 2 * a.dim], s);
-      else
+    if (in && gated) {   // each gate's blocks by themselves
+      for (int g = begin / a.parts, i = begin; i < end; ++g) {
+        const int stop = min(end, (g + 1) * a.parts);
+        float t = 0.0f;
 #pragma unroll 8
-        for (int i = begin; i < end; ++i) s += v[(size_t)i * 2 * a.dim];
+        for (; i < stop; ++i) t += v[(size_t)i * 2 * a.dim];
+        s = fmaf(a.gate[(size_t)g * a.dim + c], t, s);
+      }
+    } else if (in) {
+#pragma unroll 8
+      for (int i = begin; i < end; ++i) s += v[(size_t)i * 2 * a.dim];
     }
     red[run][lane] = s;
     __syncthreads();

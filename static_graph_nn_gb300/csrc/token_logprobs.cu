@@ -31,6 +31,7 @@ constexpr float kNothing = -1000.0f;     // as an exponent of 2: 0, and finite
 constexpr int kLogpList = 512;           // candidates that are ranked
 constexpr int kLogpOwners = 64;          // threads whose elements are read again
 constexpr int kMaxCluster = 8;
+constexpr int kLogpShort = 384;          // units of 16 bytes of a short row
 
 struct LogpArgs {
   const void* logits;
@@ -138,11 +139,12 @@ __device__ __forceinline__ uint4 narrow(const f32x2 (&f)[2]) {
   const float2 a = parts(f[0]), b = parts(f[1]);
   return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
 }
-// The largest of four units' values (a NaN only if all are).
-__device__ __forceinline__ float units_max(const uint4 (&u)[4], bf16) {
+// The largest of N units' values (a NaN only if all are).
+template <int N>
+__device__ __forceinline__ float units_max(const uint4 (&u)[N], bf16) {
   __nv_bfloat162 m = *reinterpret_cast<const __nv_bfloat162*>(&u[0].x);
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
+  for (int q = 0; q < N; ++q) {
     const uint32_t w[4] = {u[q].x, u[q].y, u[q].z, u[q].w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) m = __hmax2(m, *reinterpret_cast<const __nv_bfloat162*>(&w[i]));
@@ -150,10 +152,11 @@ __device__ __forceinline__ float units_max(const uint4 (&u)[4], bf16) {
   const float2 f = __bfloat1622float2(m);
   return fmaxf(f.x, f.y);
 }
-__device__ __forceinline__ float units_max(const uint4 (&u)[4], float) {
-  float m = -INFINITY;
+template <int N>
+__device__ __forceinline__ float units_max(const uint4 (&u)[N], float) {
+  float m = __uint_as_float(u[0].x);
 #pragma unroll
-  for (int q = 0; q < 4; ++q)
+  for (int q = 0; q < N; ++q)
     m = fmaxf(fmaxf(fmaxf(m, __uint_as_float(u[q].x)), fmaxf(__uint_as_float(u[q].y), __uint_as_float(u[q].z))),
               __uint_as_float(u[q].w));
   return m;
@@ -177,20 +180,53 @@ struct RowSums {
   }
 };
 
+// The block's sums of both, relative to one maximum.
+__device__ __forceinline__ void block_sums(RowSums& t, float (&red)[2][32]) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  t.s = warp_sum(t.s);
+  t.q = warp_sum(t.q);
+  if (lane == 0) {
+    red[0][w] = t.s;
+    red[1][w] = t.q;
+  }
+  __syncthreads();
+  t.s = warp_sum(lane < nw ? red[0][lane] : 0.0f);
+  t.q = warp_sum(lane < nw ? red[1][lane] : 0.0f);
+}
+
+// Where a thread's maximum is: in its chunk (of four units) of this number, -1 for one of the
+// row's single elements; and the largest of its other chunks' maxima.
+struct RowBest {
+  int chunk;
+  float others;
+};
+// Four units of the part from u0 on, a block's width apart; -inf behind the part.
 template <typename T>
-__device__ __forceinline__ RowSums row_sums(const Part<T>& p, float c) {
+__device__ __forceinline__ void fetch_chunk(const Part<T>& p, int u0, uint4 (&u)[4]) {
+  constexpr uint32_t kNone = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
+  const int step = blockDim.x;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    u[i] = u0 + i * step < p.units ? *p.unit(u0 + i * step) : make_uint4(kNone, kNone, kNone, kNone);
+}
+// A thread's sums; next: its first chunk.
+template <typename T>
+__device__ __forceinline__ RowSums row_sums(const Part<T>& p, float c, uint4 (&next)[4], RowBest& best) {
   constexpr int pairs = Part<T>::kPer / 2;
-  constexpr uint32_t kNone = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;   // -inf
   RowSums r = {-INFINITY, 0.0f, 0.0f};
+  best = {-1, -INFINITY};
   const int step = blockDim.x;
   const f32x2 cc = both(c);
-  for (int u0 = threadIdx.x; u0 < p.units; u0 += 4 * step) {
-    uint4 u[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      u[i] = u0 + i * step < p.units ? *p.unit(u0 + i * step) : make_uint4(kNone, kNone, kNone, kNone);
+  int chunk = 0;
+  for (int u0 = threadIdx.x; u0 < p.units; u0 += 4 * step, ++chunk) {
+    uint4 u[4] = {next[0], next[1], next[2], next[3]};
+    fetch_chunk(p, u0 + 4 * step, next);   // in flight while these are added
     const float top = units_max(u, T());
-    if (top > r.m) r.lift(top, c);
+    best.others = fmaxf(best.others, fminf(top, r.m));
+    if (top > r.m) {
+      best.chunk = chunk;
+      r.lift(top, c);
+    }
     const f32x2 minus = both(r.m == -INFINITY ? 0.0f : -r.m);
     f32x2 s = both(0.0f), q = both(0.0f);
 #pragma unroll
@@ -210,44 +246,56 @@ __device__ __forceinline__ RowSums row_sums(const Part<T>& p, float c) {
     r.s += ss.x + ss.y;
     r.q += qq.x + qq.y;
   }
-  if ((int)threadIdx.x < p.head) r.one(ld_elem(p.x, threadIdx.x), c);
-  if ((int)threadIdx.x < p.tail) r.one(ld_elem(p.behind(), threadIdx.x), c);
+  const auto single = [&](float x) {
+    if (x > r.m) {
+      best.others = fmaxf(best.others, r.m);
+      best.chunk = -1;
+    }
+    r.one(x, c);
+  };
+  if ((int)threadIdx.x < p.head) single(ld_elem(p.x, threadIdx.x));
+  if ((int)threadIdx.x < p.tail) single(ld_elem(p.behind(), threadIdx.x));
   return r;
 }
 
 // ---- the most likely ------------------------------------------------------------
+constexpr uint32_t kLeastKey = 0x007fffffu;   // of -inf
+
 struct TopShared {
+  alignas(16) uint32_t groups[64];            // maxima of groups of threads: keys, their last six bits the group's
   uint32_t maxima[512];                       // the threads', as keys
   unsigned long long list[kLogpList];
-  int owner[kLogpOwners];
-  int n_owners, n_list, n_more;
+  int owner[kLogpOwners];                     // of all of whose units may hold some
+  int2 chunk[kLogpOwners];                    // the only ones that may: a thread's
+  int n_owners, n_chunks, n_list, n_more;
   uint32_t threshold;
   unsigned long long best[MG_MAX_TOP];        // in order; 0 where there are fewer
 };
 
-// The k-th largest of the N threads' maxima, by the first warp.  (Keys of bf16 values
-// end in 16 equal bits: zeros, or ones below zero.)
-template <typename T, int N>
-__device__ __forceinline__ uint32_t kth_maximum(const TopShared& t, int k) {
-  const int lane = threadIdx.x & 31;
-  uint32_t v[N / 32];
+// A little below the k-th largest of the G groups' maxima: each of G threads counts those above its own.
+template <int G>
+__device__ __forceinline__ void kth_group(TopShared& t, int k) {
+  if (threadIdx.x >= G) return;
+  const uint32_t v = t.groups[threadIdx.x];
+  int above = 0;
 #pragma unroll
-  for (int i = 0; i < N / 32; ++i) v[i] = t.maxima[32 * i + lane];
-  uint32_t lo = 0;
-  for (int bit = 31; bit >= (sizeof(T) == 2 ? 16 : 0); --bit) {
-    const uint32_t mid = lo | 1u << bit;
-    int n = 0;
-#pragma unroll
-    for (int i = 0; i < N / 32; ++i) n += v[i] >= mid;
-    if ((int)__reduce_add_sync(0xffffffffu, n) >= k) lo = mid;
+  for (int j = 0; j < G; j += 4) {
+    const uint4 w = *reinterpret_cast<const uint4*>(t.groups + j);
+    above += (w.x > v) + (w.y > v) + (w.z > v) + (w.w > v);
   }
-  return sizeof(T) == 2 && lo && !(lo & 0x80000000u) ? lo | 0xffffu : lo;
+  if (above == k - 1) t.threshold = v & ~63u;
+}
+// Exactly the k-th largest of the threads' maxima.
+__device__ __forceinline__ void kth_maximum(TopShared& t, int k) {
+  const uint32_t v = t.maxima[threadIdx.x];
+  int before = 0;
+  for (int j = 0; j < (int)blockDim.x; ++j) before += t.maxima[j] > v || (t.maxima[j] == v && j < (int)threadIdx.x);
+  if (before == k - 1) t.threshold = v;
 }
 
 // Every element of the part: f(value, place in the row).
 template <typename T, typename F>
-__device__ __forceinline__ void each_of_unit(const Part<T>& p, int u, F&& f) {
-  const uint4 w = *p.unit(u);
+__device__ __forceinline__ void each_of_unit(const Part<T>& p, int u, const uint4& w, F&& f) {
   f32x2 v[Part<T>::kPer / 2];
   widen(w, v);
 #pragma unroll
@@ -259,39 +307,59 @@ __device__ __forceinline__ void each_of_unit(const Part<T>& p, int u, F&& f) {
 }
 template <typename T, typename F>
 __device__ __forceinline__ void each_element(const Part<T>& p, F&& f) {
-  for (int u = threadIdx.x; u < p.units; u += blockDim.x) each_of_unit(p, u, f);
+  for (int u = threadIdx.x; u < p.units; u += blockDim.x) each_of_unit(p, u, *p.unit(u), f);
   if ((int)threadIdx.x < p.head) f(ld_elem(p.x, threadIdx.x), p.at + threadIdx.x);
   if ((int)threadIdx.x < p.tail) f(ld_elem(p.behind(), threadIdx.x), p.at + p.count() - p.tail + threadIdx.x);
 }
 
-// Lists the elements whose keys are at least `least`, of the threads whose maxima
-// are; false if there are more than the list holds.
+// Lists the elements whose keys are at least `least` (that of -inf or more), of the
+// threads whose maxima are; false if there are more than the list holds.  The counts
+// are 0 before.
 template <typename T>
-__device__ bool list_from(const Part<T>& p, TopShared& t, uint32_t least) {
-  if (threadIdx.x == 0) t.n_owners = t.n_list = 0;
-  __syncthreads();
-  if (t.maxima[threadIdx.x] >= least) {
+__device__ bool list_from(const Part<T>& p, TopShared& t, const RowBest& best, uint32_t least) {
+  const bool mine = t.maxima[threadIdx.x] >= least;
+  if (mine && order_key(best.others) >= least) {
     const int i = atomicAdd(&t.n_owners, 1);
     if (i < kLogpOwners) t.owner[i] = threadIdx.x;
+  } else if (mine && best.chunk >= 0) {
+    const int i = atomicAdd(&t.n_chunks, 1);
+    if (i < kLogpOwners) t.chunk[i] = make_int2(threadIdx.x, best.chunk);
   }
   __syncthreads();
-  const int owners = t.n_owners;
-  if (owners > kLogpOwners) return false;
+  const int owners = t.n_owners, chunks = t.n_chunks;
+  if (owners > kLogpOwners || chunks > kLogpOwners) return false;
+  const float from = key_value(least);
   const auto add = [&](float x, int c) {
-    if (order_key(x) < least) return;
+    if (!(x >= from)) return;
     const int i = atomicAdd(&t.n_list, 1);
     if (i < kLogpList) t.list[i] = place_key(x, c);
   };
-  const int each = (p.units + blockDim.x - 1) / blockDim.x + 2;   // units of a thread, and its single elements
-  for (int i = threadIdx.x; i < owners * each; i += blockDim.x) {
-    const int who = t.owner[i / each], j = i % each, u = who + (j - 2) * (int)blockDim.x;
-    if (j >= 2) {
-      if (u < p.units) each_of_unit(p, u, add);
-    } else if (j == 0 && who < p.head) {
-      add(ld_elem(p.x, who), p.at + who);
-    } else if (j == 1 && who < p.tail) {
-      add(ld_elem(p.behind(), who), p.at + p.count() - p.tail + who);
+  const auto look = [&](int u) {
+    if (u >= p.units) return;
+    const uint4 w[1] = {*p.unit(u)};
+    if (units_max(w, T()) >= from) each_of_unit(p, u, w[0], add);
+  };
+  for (int i = threadIdx.x; i < 4 * chunks; i += blockDim.x) {
+    const int2 at = t.chunk[i / 4];
+    look(at.x + (4 * at.y + i % 4) * (int)blockDim.x);
+  }
+  const int rounds = (p.units + blockDim.x - 1) / blockDim.x;   // units of a thread at most
+  // a thread takes every blockDim.x-th of the owners' units, one owner after the other
+  if (rounds && owners) {
+    const int skip = blockDim.x / rounds, rest = blockDim.x % rounds;
+    for (int o = threadIdx.x / rounds, j = threadIdx.x % rounds; o < owners;) {
+      look(t.owner[o] + j * (int)blockDim.x);
+      o += skip;
+      j += rest;
+      if (j >= rounds) {
+        j -= rounds;
+        ++o;
+      }
     }
+  }
+  if (mine) {
+    if ((int)threadIdx.x < p.head) add(ld_elem(p.x, threadIdx.x), p.at + threadIdx.x);
+    if ((int)threadIdx.x < p.tail) add(ld_elem(p.behind(), threadIdx.x), p.at + p.count() - p.tail + threadIdx.x);
   }
   __syncthreads();
   return t.n_list <= kLogpList;
@@ -310,27 +378,34 @@ __device__ __forceinline__ void rank_list(TopShared& t, int n, int k) {
 
 // The part's k largest (fewer if it has fewer) in order in t.best.
 template <typename T, int N>
-__device__ void top_of_part(const Part<T>& p, TopShared& t, int k, float maximum) {
+__device__ void top_of_part(const Part<T>& p, TopShared& t, int k, float maximum, const RowBest& best) {
   k = min(k, p.count());
   const bool any = (int)threadIdx.x < p.units || (int)threadIdx.x < p.head || (int)threadIdx.x < p.tail;
-  t.maxima[threadIdx.x] = any ? order_key(maximum) : 0u;
+  constexpr int G = N < 64 ? N : 64;
+  uint32_t key = any ? order_key(maximum) : 0u;
+  t.maxima[threadIdx.x] = key;
+#pragma unroll
+  for (int o = 1; o < N / G; o *= 2) key = max(key, __shfl_xor_sync(0xffffffffu, key, o));
+  if (threadIdx.x % (N / G) == 0) t.groups[threadIdx.x / (N / G)] = (key & ~63u) | threadIdx.x / (N / G);
   if (threadIdx.x < MG_MAX_TOP) t.best[threadIdx.x] = 0;
+  if (threadIdx.x == 0) t.n_owners = t.n_chunks = t.n_list = 0;
   __syncthreads();
   if (k == 0) return;
-  if (threadIdx.x < 32) {
-    const uint32_t v = kth_maximum<T, N>(t, k);
-    if (threadIdx.x == 0) t.threshold = v;
-  }
+  kth_group<G>(t, k);
   __syncthreads();
   uint32_t th = t.threshold;
-  if (list_from(p, t, th) && t.n_list >= k) {
+  if (th > kLeastKey && list_from(p, t, best, th) && t.n_list >= k) {
     rank_list(t, t.n_list, k);
     return;
   }
-  // Too many of the threshold itself, or (behind maxima of -inf that are NaN) too few
-  // of it: those above it, then equal ones in order of their places.
+  // Too many equal ones, few that are not -inf, or (behind maxima of -inf that are NaN)
+  // too few: those above the exact threshold, then equal ones in order of their places.
   __syncthreads();
-  if (!list_from(p, t, th + 1)) {
+  kth_maximum(t, k);
+  if (threadIdx.x == 0) t.n_owners = t.n_chunks = t.n_list = 0;
+  __syncthreads();
+  th = t.threshold;
+  if (!list_from(p, t, best, max(th + 1, kLeastKey))) {
     // Many large values in few threads' hands: the exact k-th largest, bit by bit.
     uint32_t lo = 0;
     for (int bit = 31; bit >= 0; --bit) {
@@ -394,12 +469,15 @@ __device__ __forceinline__ const V* of_rank(const V* p, int rank) {
 // A row per cluster of blocks of N threads.
 template <typename T, bool TOP, int N>
 __global__ void __launch_bounds__(N) logp_kernel(LogpArgs a, int ranks) {
-  __shared__ float red[32];
+  __shared__ float red[32], red2[2][32];
   __shared__ RowSums mine;
   __shared__ TopShared top[1];   // (nothing refers to it without TOP)
   const size_t r = blockIdx.x / ranks;
   const int rank = blockIdx.x % ranks;
   const T* x = static_cast<const T*>(a.logits) + r * a.stride;
+  const Part<T> p = part_of(x, a.vocab, rank, ranks);
+  uint4 next[4];
+  fetch_chunk(p, threadIdx.x, next);   // under way before the id says whether the row counts
   const int id = a.ids ? token_of(a.ids, a.id64, a.vocab, r) : 0;
   if (id < 0) {   // (in all blocks of the cluster)
     if (rank) return;
@@ -415,14 +493,13 @@ __global__ void __launch_bounds__(N) logp_kernel(LogpArgs a, int ranks) {
     return;
   }
   const float given = threadIdx.x == 0 && rank == 0 && a.logp ? ld_elem(x, id) : 0.0f;   // (ahead of the row)
-  const Part<T> p = part_of(x, a.vocab, rank, ranks);
   const float c = a.inv_t * kLog2e;
-  RowSums t = row_sums(p, c);
+  RowBest best;
+  RowSums t = row_sums(p, c, next, best);
   const float maximum = t.m;
   t.lift(block_max(t.m, red), c);
-  t.s = block_sum(t.s, red);
-  t.q = block_sum(t.q, red);
-  if (TOP) top_of_part<T, N>(p, top[0], a.k, maximum);
+  block_sums(t, red2);
+  if (TOP) top_of_part<T, N>(p, top[0], a.k, maximum, best);
   if (ranks > 1) {
     if (threadIdx.x == 0) mine = t;
     cluster_sync();
@@ -443,11 +520,10 @@ __global__ void __launch_bounds__(N) logp_kernel(LogpArgs a, int ranks) {
         t.q += all[i].q;
       }
       if (TOP) {
-        for (int i = threadIdx.x; i < ranks * MG_MAX_TOP; i += blockDim.x)
-          top[0].list[i] = *of_rank(&top[0].best[i % MG_MAX_TOP], i / MG_MAX_TOP);
+        for (int i = threadIdx.x; i < ranks * a.k; i += blockDim.x) top[0].list[i] = *of_rank(&top[0].best[i % a.k], i / a.k);
         __syncthreads();
-        // (absent ones are 0, less than every element's key; they may share a rank that is not written)
-        rank_list(top[0], ranks * MG_MAX_TOP, a.k);
+        // (absent ones are 0, less than every element's key: their rank is not written)
+        rank_list(top[0], ranks * a.k, a.k);
       }
     }
     cluster_sync();
@@ -536,17 +612,17 @@ __global__ void __launch_bounds__(256) logp_grad_kernel(LogpGradArgs a, int rank
   if ((int)threadIdx.x < p.tail) single(behind + threadIdx.x);
 }
 
-// Many rows: 128 threads each, so that a row's sums are joined by few warps.  Few rows:
-// 512 threads, and as many blocks to a row, up to eight, as fill the multiprocessors
-// while a thread still has two units.
+// Many rows: 128 threads each, so that a row's sums are joined by few warps, or one
+// warp for the shortest without alternatives.  Few rows: 512 threads, and as many blocks to a row, up to
+// eight, as fill the multiprocessors while a thread still has two units.
 template <typename T>
 cudaError_t logp_forward(const LogpArgs& a, int rows, cudaStream_t s) {
   const int sms = device_sms();
-  int threads = 128, ranks = 1;
+  const int units = (int)((long long)a.vocab * (int)sizeof(T) / 16);
+  int threads = units < kLogpShort && !a.k ? 32 : 128, ranks = 1;
   if (rows < 4 * sms) {
-    threads = 512;
-    while (ranks < kMaxCluster && 2 * ranks * rows <= 2 * sms && (long long)a.vocab * (int)sizeof(T) / 16 >= 4ll * ranks * threads)
-      ranks *= 2;
+    threads = units < kLogpShort ? 128 : 512;
+    while (ranks < kMaxCluster && 2 * ranks * rows <= 2 * sms && units >= 4 * ranks * threads) ranks *= 2;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((long long)rows * ranks));
@@ -559,7 +635,9 @@ cudaError_t logp_forward(const LogpArgs& a, int rows, cudaStream_t s) {
   cfg.attrs = &at;
   cfg.numAttrs = 1;
   cudaError_t e;
-  if (threads == 128)
+  if (threads == 32)
+    e = cudaLaunchKernelEx(&cfg, logp_kernel<T, false, 32>, a, ranks);
+  else if (threads == 128)
     e = a.k ? cudaLaunchKernelEx(&cfg, logp_kernel<T, true, 128>, a, ranks) : cudaLaunchKernelEx(&cfg, logp_kernel<T, false, 128>, a, ranks);
   else
     e = a.k ? cudaLaunchKernelEx(&cfg, logp_kernel<T, true, 512>, a, ranks) : cudaLaunchKernelEx(&cfg, logp_kernel<T, false, 512>, a, ranks);
