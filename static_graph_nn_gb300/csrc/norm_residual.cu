@@ -35,6 +35,7 @@ struct NormResArgs {
   int block_rows;             // consecutive rows of a block
   int stages;                 // rows in shared memory at once
   int row_units;              // 16-byte units of a row there, at any offset
+  int ranks, part;            // blocks that share a row, columns of each
 };
 
 struct NormResGradArgs {
@@ -57,6 +58,7 @@ struct NormResGradArgs {
   // blocks: `parts` for each gate (block_rows rows each), or, where parts is 1, one for each block_gates gates
   int parts, block_rows, block_gates;
   int stages, row_units;
+  int ranks, part;            // blocks that share a row, columns of each
 };
 
 // ---- a row in a block's registers --------------------------------------------
@@ -130,21 +132,22 @@ __device__ __forceinline__ void copy_row(uint4* to, const T* p, int dim) {
                    : "memory");
   }
 }
-// All units of row r of a matrix of n rows, by all threads; the last one ends with the matrix.
+// The n elements of a matrix from element e on, with all of the 16-byte units that they
+// touch, by all threads; the last unit ends with the matrix (of `all` elements).
 template <typename T>
-__device__ __forceinline__ void copy_whole_row(uint4* to, const T* m, int r, int n, int dim) {
-  const size_t bytes = (size_t)dim * sizeof(T), begin = r * bytes, first = begin / 16, last = (begin + bytes + 15) / 16;
+__device__ __forceinline__ void copy_span(uint4* to, const T* m, size_t e, int n, size_t all) {
+  const size_t begin = e * sizeof(T), first = begin / 16, last = (begin + n * sizeof(T) + 15) / 16;
   for (size_t u = first + threadIdx.x; u < last; u += blockDim.x) {
-    const int size = (int)min((size_t)16, n * bytes - u * 16);
+    const int size = (int)min((size_t)16, all * sizeof(T) - u * 16);
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to + (u - first))),
                  "l"(reinterpret_cast<const char*>(m) + u * 16), "r"(size)
                  : "memory");
   }
 }
-// Where row r begins in its copy.
+// Where element e is in its copy.
 template <typename T>
-__device__ __forceinline__ const T* whole_row(const uint4* at, int r, int dim) {
-  return reinterpret_cast<const T*>(at) + (size_t)r * dim * sizeof(T) % 16 / sizeof(T);
+__device__ __forceinline__ const T* span_at(const uint4* at, size_t e) {
+  return reinterpret_cast<const T*>(at) + e * sizeof(T) % 16 / sizeof(T);
 }
 // Zeros in the units that no copy writes: those beyond the row, and all of a row that is not given.
 template <typename T, int U>
@@ -155,20 +158,40 @@ __device__ __forceinline__ void clear_row(uint4* to, bool given, int dim) {
       to[j * blockDim.x + threadIdx.x] = make_uint4(0, 0, 0, 0);
 }
 
-// Sums of N values over the block, the same in every thread.  `turn` alternates from
+constexpr int kNrRanks = 8;   // blocks that share wide rows, at most
+// A block's place in its cluster, and its columns.
+struct NormResPart {
+  int block, rank, c0, dim;
+};
+template <typename A>
+__device__ __forceinline__ NormResPart part_of(const A& a) {
+  NormResPart p;
+  p.block = blockIdx.x / a.ranks;
+  p.rank = blockIdx.x % a.ranks;
+  p.c0 = p.rank * a.part;
+  p.dim = min(a.part, a.dim - p.c0);
+  return p;
+}
+// Sums of N values over a row's blocks, the same in every thread.  `turn` alternates from
 // call to call: the barrier of one call lies between the reads of the call before it
-// and the writes of the call after it.
+// and the writes of the call after it.  A block writes its sums to every block of its
+// cluster; after the last call's barrier none is written to any more.
 template <int N>
-__device__ __forceinline__ void block_sums(float (&v)[N], float* red /* [2][N][16] */, int& turn) {
+struct RowSums {
+  alignas(16) float warp[2][N][16];
+  float block[2][kNrRanks][N];
+};
+template <int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], RowSums<N>& red, int& turn, int rank, int ranks) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
 #pragma unroll
   for (int n = 0; n < N; ++n) v[n] = warp_sum(v[n]);
   if (warps == 1) return;
-  float* r = red + turn * 16 * N;
+  const int now = turn;
   turn ^= 1;
   if (lane == 0) {
 #pragma unroll
-    for (int n = 0; n < N; ++n) r[n * 16 + warp] = v[n];
+    for (int n = 0; n < N; ++n) red.warp[now][n][warp] = v[n];
   }
   __syncthreads();
 #pragma unroll
@@ -176,15 +199,30 @@ __device__ __forceinline__ void block_sums(float (&v)[N], float* red /* [2][N][1
   for (int w = 0; w < warps; w += 4) {
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-      const float4 f = *reinterpret_cast<const float4*>(r + n * 16 + w);   // (zeros beyond the warps)
+      const float4 f = *reinterpret_cast<const float4*>(&red.warp[now][n][w]);   // (zeros beyond the warps)
       v[n] += (f.x + f.y) + (f.z + f.w);
     }
   }
+  if (ranks == 1) return;
+  if ((int)threadIdx.x < ranks) {
+    uint64_t to;
+    asm("mapa.u64 %0, %1, %2;" : "=l"(to) : "l"((uint64_t)&red.block[now][rank][0]), "r"(threadIdx.x));
+#pragma unroll
+    for (int n = 0; n < N; ++n) reinterpret_cast<float*>(to)[n] = v[n];
+  }
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    v[n] = 0.0f;
+    for (int i = 0; i < ranks; ++i) v[n] += *reinterpret_cast<volatile float*>(&red.block[now][i][n]);
+  }
 }
+// Zeros beyond the warps; in a cluster, every block is there before one writes to it.
 template <int N>
-__device__ __forceinline__ void clear_sums(float* red) {
-  for (int i = threadIdx.x; i < 2 * 16 * N; i += blockDim.x) red[i] = 0.0f;
+__device__ __forceinline__ void clear_sums(RowSums<N>& red, int ranks) {
+  for (int i = threadIdx.x; i < 2 * 16 * N; i += blockDim.x) (&red.warp[0][0][0])[i] = 0.0f;
   __syncthreads();
+  if (ranks > 1) asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // 1 / sqrt(x): an estimate and one step of Newton's method.
 __device__ __forceinline__ float inverse_root(float x) {
@@ -205,43 +243,46 @@ __device__ __forceinline__ void copies_wait(int n) {
 
 // (T0: threads at most)
 template <typename T, int U, bool OWN, int T0>
-__global__ void __launch_bounds__(T0, T0 == 512 ? 1 : 4) norm_res_kernel(NormResArgs a) {
+__global__ void __launch_bounds__(T0, T0 == 512 ? 1 : T0 == 128 ? 4 : 24) norm_res_kernel(NormResArgs a) {
   constexpr int per = Unit<T>::kPer, pairs = Unit<T>::kPairs, E = U * per, P = E / 2;
   extern __shared__ __align__(16) uint4 ring[];   // [stage][y, x][U][threads]
-  __shared__ __align__(16) float red[2 * 16];
-  clear_sums<1>(red);
+  __shared__ RowSums<1> red;
+  const NormResPart my = part_of(a);
+  const int dim = my.dim;
+  clear_sums<1>(red, a.ranks);
   const int array = OWN ? U * blockDim.x : a.row_units, stage = 2 * array;
-  const int first = blockIdx.x * a.block_rows, end = min(first + a.block_rows, a.rows);
+  const int first = my.block * a.block_rows, end = min(first + a.block_rows, a.rows);
   const T *ys = static_cast<const T*>(a.y), *xs = static_cast<const T*>(a.x);
+  const auto row_at = [&](int r) { return (size_t)r * a.dim + my.c0; };
   int fill = 0;
   const auto ahead = [&](int r) {
     uint4* to = ring + fill * stage;
     if (r < end && OWN) {
-      copy_row<T, U>(to, ys + (size_t)r * a.dim, a.dim);
-      copy_row<T, U>(to + array, xs + (size_t)r * a.dim, a.dim);
+      copy_row<T, U>(to, ys + row_at(r), dim);
+      copy_row<T, U>(to + array, xs + row_at(r), dim);
     } else if (r < end) {
-      copy_whole_row(to, ys, r, a.rows, a.dim);
-      copy_whole_row(to + array, xs, r, a.rows, a.dim);
+      copy_span(to, ys, row_at(r), dim, (size_t)a.rows * a.dim);
+      copy_span(to + array, xs, row_at(r), dim, (size_t)a.rows * a.dim);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
     fill = fill + 1 == a.stages ? 0 : fill + 1;
   };
   if (OWN)
-    for (int i = 0; i < 2 * a.stages; ++i) clear_row<T, U>(ring + i * array, true, a.dim);
+    for (int i = 0; i < 2 * a.stages; ++i) clear_row<T, U>(ring + i * array, true, dim);
   for (int i = 0; i < a.stages - 1; ++i) ahead(first + i);
   f32x2 w[P], g2[P];
 #pragma unroll
-  for (int p = 0; p < P; ++p) g2[p] = vector_at<T, OWN>(a.g2, a.dim, 0.0f, 2 * p);
+  for (int p = 0; p < P; ++p) g2[p] = vector_at<T, OWN>(a.g2 ? a.g2 + my.c0 : nullptr, dim, 0.0f, 2 * p);
   const float inv_dim = 1.0f / a.dim;
   const f32x2 scale = both(a.scale);
   int gate_end = first, slot = 0, turn = 0;
   for (int r = first; r < end; ++r) {
     if (r == gate_end) {   // the product of the post norm's factors and the gate, kept for the gate's rows
       const int gi = r / a.gate_rows;
-      const float* gate = a.gate ? a.gate + (size_t)gi * a.dim : nullptr;
+      const float* gate = a.gate ? a.gate + (size_t)gi * a.dim + my.c0 : nullptr;
 #pragma unroll
       for (int p = 0; p < P; ++p)
-        w[p] = mul2(vector_at<T, OWN>(a.g1, a.dim, 1.0f, 2 * p), vector_at<T, OWN>(gate, a.dim, 1.0f, 2 * p));
+        w[p] = mul2(vector_at<T, OWN>(a.g1 ? a.g1 + my.c0 : nullptr, dim, 1.0f, 2 * p), vector_at<T, OWN>(gate, dim, 1.0f, 2 * p));
       gate_end = (gi + 1) * a.gate_rows;
     }
     f32x2 y[P], x[P];
@@ -260,11 +301,11 @@ __global__ void __launch_bounds__(T0, T0 == 512 ? 1 : 4) norm_res_kernel(NormRes
       copies_wait(a.stages - 2);
       __syncthreads();             // row r is there, and the row before it has been read
       ahead(r + a.stages - 1);
-      const T *yr = whole_row<T>(in, r, a.dim), *xr = whole_row<T>(in + array, r, a.dim);
+      const T *yr = span_at<T>(in, row_at(r)), *xr = span_at<T>(in + array, row_at(r));
 #pragma unroll
       for (int p = 0; p < P; ++p) {
-        y[p] = pair_at(yr, a.dim, 2 * p);
-        x[p] = pair_at(xr, a.dim, 2 * p);
+        y[p] = pair_at(yr, dim, 2 * p);
+        x[p] = pair_at(xr, dim, 2 * p);
       }
     }
     float r1 = 1.0f, r2 = 1.0f;
@@ -274,7 +315,7 @@ __global__ void __launch_bounds__(T0, T0 == 512 ? 1 : 4) norm_res_kernel(NormRes
       for (int p = 0; p < P; ++p) s = fma2(v[p], v[p], s);
       const float2 t = parts(s);
       float q[1] = {t.x + t.y};
-      block_sums<1>(q, red, turn);
+      row_sums<1>(q, red, turn, my.rank, a.ranks);
       return inverse_root(fmaf(q[0], inv_dim, a.eps));
     };
     if (a.g1) r1 = root_of(y);
@@ -282,14 +323,14 @@ __global__ void __launch_bounds__(T0, T0 == 512 ? 1 : 4) norm_res_kernel(NormRes
 #pragma unroll
     for (int p = 0; p < P; ++p) x[p] = fma2(scale, x[p], mul2(mul2(y[p], w[p]), rr));
     if (a.g2) r2 = root_of(x);
-    T* xo = static_cast<T*>(a.xo) + (size_t)r * a.dim;
-    T* h = a.h ? static_cast<T*>(a.h) + (size_t)r * a.dim : nullptr;
+    T* xo = static_cast<T*>(a.xo) + row_at(r);
+    T* h = a.h ? static_cast<T*>(a.h) + row_at(r) : nullptr;
     const f32x2 rq = both(r2);
     if (OWN) {
 #pragma unroll
       for (int j = 0; j < U; ++j) {
         const int c = column<T, OWN>(j * per);
-        if (c >= a.dim) continue;
+        if (c >= dim) continue;
         f32x2 f[pairs];
 #pragma unroll
         for (int i = 0; i < pairs; ++i) f[i] = x[j * pairs + i];
@@ -302,11 +343,11 @@ __global__ void __launch_bounds__(T0, T0 == 512 ? 1 : 4) norm_res_kernel(NormRes
     } else {
 #pragma unroll
       for (int p = 0; p < P; ++p) {
-        store_pair(xo, a.dim, 2 * p, x[p]);
-        if (h) store_pair(h, a.dim, 2 * p, mul2(x[p], mul2(rq, g2[p])));
+        store_pair(xo, dim, 2 * p, x[p]);
+        if (h) store_pair(h, dim, 2 * p, mul2(x[p], mul2(rq, g2[p])));
       }
     }
-    if (a.rstd && threadIdx.x == 0) *reinterpret_cast<float2*>(a.rstd + 2 * (size_t)r) = make_float2(r1, r2);
+    if (a.rstd && my.rank == 0 && threadIdx.x == 0) *reinterpret_cast<float2*>(a.rstd + 2 * (size_t)r) = make_float2(r1, r2);
   }
 }
 
@@ -314,24 +355,24 @@ __global__ void __launch_bounds__(T0, T0 == 512 ? 1 : 4) norm_res_kernel(NormRes
 struct NormResSpan {
   int g, first, end;
 };
-__device__ __forceinline__ bool next_span(const NormResGradArgs& a, NormResSpan& s) {
+__device__ __forceinline__ bool next_span(const NormResGradArgs& a, int block, NormResSpan& s) {
   if (a.parts > 1) {
     if (s.g >= 0) return false;
-    s.g = blockIdx.x / a.parts;
-    s.first = s.g * a.gate_rows + blockIdx.x % a.parts * a.block_rows;
+    s.g = block / a.parts;
+    s.first = s.g * a.gate_rows + block % a.parts * a.block_rows;
     s.end = min(s.first + a.block_rows, (s.g + 1) * a.gate_rows);
     return s.first < s.end;
   }
-  s.g = s.g < 0 ? (int)blockIdx.x * a.block_gates : s.g + 1;
+  s.g = s.g < 0 ? block * a.block_gates : s.g + 1;
   s.first = s.g * a.gate_rows;
   s.end = s.first + a.gate_rows;
-  return s.g < min(((int)blockIdx.x + 1) * a.block_gates, a.gates);
+  return s.g < min((block + 1) * a.block_gates, a.gates);
 }
 // A column's sums over a span.  P = sum t y r1 gives both the gate's gradient, g1 P,
 // and, times the gate, the post norm's.  Where a block has whole gates it writes
 // their gradients and keeps the post norm's; else it keeps P.
-__device__ __forceinline__ void span_sums(const NormResGradArgs& a, const NormResSpan& s, bool first, int c, float P) {
-  float* keep = a.ws + (size_t)blockIdx.x * 2 * a.dim + c;
+__device__ __forceinline__ void span_sums(const NormResGradArgs& a, int block, const NormResSpan& s, bool first, int c, float P) {
+  float* keep = a.ws + (size_t)block * 2 * a.dim + c;
   if (a.parts > 1) {
     *keep = P;
     return;
@@ -343,72 +384,67 @@ __device__ __forceinline__ void span_sums(const NormResGradArgs& a, const NormRe
 
 // The three sums of a row in one exchange.  With b = w y (w = gate g1) and q = dx' + r2 dh g2:
 // S1 = sum dh g2 x', and sum w t y = sum b q - r2^3 / dim S1 sum b x'.
-// (T0: threads at most; KEEP: the factors in registers)
-template <typename T, int U, bool OWN, int T0, bool KEEP>
-__global__ void __launch_bounds__(T0, T0 == 512 ? 1 : OWN ? 4 : 3) norm_res_grad_kernel(NormResGradArgs a) {
+// (T0: threads at most)
+template <typename T, int U, bool OWN, int T0>
+__global__ void __launch_bounds__(T0, T0 == 512 ? 1 : T0 == 128 ? (OWN ? 4 : 3) : OWN ? 24 : 16) norm_res_grad_kernel(NormResGradArgs a) {
   constexpr int per = Unit<T>::kPer, pairs = Unit<T>::kPairs, E = U * per, P = E / 2;
   extern __shared__ __align__(16) uint4 ring[];   // [stage][y, x, dx_out, dh][U][threads]
-  __shared__ __align__(16) float red[2 * 16 * 3];
-  clear_sums<3>(red);
+  __shared__ RowSums<3> red;
+  const NormResPart my = part_of(a);
+  const int dim = my.dim;
+  clear_sums<3>(red, a.ranks);
   const int array = OWN ? U * blockDim.x : a.row_units, stage = 4 * array;
   const T *ys = static_cast<const T*>(a.y), *xs = static_cast<const T*>(a.x);
   const T *os = static_cast<const T*>(a.dxo), *hs = static_cast<const T*>(a.dh);
   const float inv_dim = 1.0f / a.dim;
   const f32x2 scale = both(a.scale);
-  f32x2 sp[P], s2[P], w[KEEP ? P : 1], g2[KEEP ? P : 1];
+  f32x2 sp[P], s2[P], w[P], g2[P];
 #pragma unroll
   for (int p = 0; p < P; ++p) {
     s2[p] = both(0.0f);
-    if (KEEP) g2[KEEP ? p : 0] = vector_at<T, OWN>(hs ? a.g2 : nullptr, a.dim, 0.0f, 2 * p);
+    g2[p] = vector_at<T, OWN>(hs ? a.g2 + my.c0 : nullptr, dim, 0.0f, 2 * p);
   }
   if (OWN)
     for (int i = 0; i < a.stages; ++i) {
-      clear_row<T, U>(ring + i * stage, true, a.dim);
-      clear_row<T, U>(ring + i * stage + array, true, a.dim);
-      clear_row<T, U>(ring + i * stage + 2 * array, os != nullptr, a.dim);
-      clear_row<T, U>(ring + i * stage + 3 * array, hs != nullptr, a.dim);
+      clear_row<T, U>(ring + i * stage, true, dim);
+      clear_row<T, U>(ring + i * stage + array, true, dim);
+      clear_row<T, U>(ring + i * stage + 2 * array, os != nullptr, dim);
+      clear_row<T, U>(ring + i * stage + 3 * array, hs != nullptr, dim);
     }
   NormResSpan s = {-1, 0, 0};
   bool any = false;
   int turn = 0;
-  while (next_span(a, s)) {
-    const float* gate = a.gate ? a.gate + (size_t)s.g * a.dim : nullptr;
+  while (next_span(a, my.block, s)) {
+    const float* gate = a.gate ? a.gate + (size_t)s.g * a.dim + my.c0 : nullptr;
     int fill = 0, slot = 0;
     const auto ahead = [&](int r) {
       uint4* to = ring + fill * stage;
+      const size_t at = (size_t)r * a.dim + my.c0, all = (size_t)a.rows * a.dim;
       if (r < s.end && OWN) {
-        const size_t at = (size_t)r * a.dim;
-        copy_row<T, U>(to, ys + at, a.dim);
-        copy_row<T, U>(to + array, xs + at, a.dim);
-        if (os) copy_row<T, U>(to + 2 * array, os + at, a.dim);
-        if (hs) copy_row<T, U>(to + 3 * array, hs + at, a.dim);
+        copy_row<T, U>(to, ys + at, dim);
+        copy_row<T, U>(to + array, xs + at, dim);
+        if (os) copy_row<T, U>(to + 2 * array, os + at, dim);
+        if (hs) copy_row<T, U>(to + 3 * array, hs + at, dim);
       } else if (r < s.end) {
-        copy_whole_row(to, ys, r, a.rows, a.dim);
-        copy_whole_row(to + array, xs, r, a.rows, a.dim);
-        if (os) copy_whole_row(to + 2 * array, os, r, a.rows, a.dim);
-        if (hs) copy_whole_row(to + 3 * array, hs, r, a.rows, a.dim);
+        copy_span(to, ys, at, dim, all);
+        copy_span(to + array, xs, at, dim, all);
+        if (os) copy_span(to + 2 * array, os, at, dim, all);
+        if (hs) copy_span(to + 3 * array, hs, at, dim, all);
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
       fill = fill + 1 == a.stages ? 0 : fill + 1;
     };
     if (!OWN) __syncthreads();   // the last span's rows have been read
     for (int i = 0; i < a.stages - 1; ++i) ahead(s.first + i);
-    const auto w_here = [&](int p) {
-      return mul2(vector_at<T, OWN>(a.g1, a.dim, 1.0f, 2 * p), vector_at<T, OWN>(gate, a.dim, 1.0f, 2 * p));
-    };
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       sp[p] = both(0.0f);
-      if (KEEP) w[KEEP ? p : 0] = w_here(p);
+      w[p] = mul2(vector_at<T, OWN>(a.g1 ? a.g1 + my.c0 : nullptr, dim, 1.0f, 2 * p), vector_at<T, OWN>(gate, dim, 1.0f, 2 * p));
     }
-    const auto w_at = [&](int p) { return KEEP ? w[KEEP ? p : 0] : w_here(p); };
-    const auto g2_at = [&](int p) {
-      return KEEP ? g2[KEEP ? p : 0] : vector_at<T, OWN>(hs ? a.g2 : nullptr, a.dim, 0.0f, 2 * p);
-    };
     const float2* roots = reinterpret_cast<const float2*>(a.rstd);
     float2 root = roots[s.first];
     for (int r = s.first; r < s.end; ++r) {
-      const size_t at = (size_t)r * a.dim;
+      const size_t at = (size_t)r * a.dim + my.c0;
       const float r1 = a.g1 ? root.x : 1.0f, r2 = hs ? root.y : 1.0f;
       const f32x2 rr1 = both(r1), rr2 = both(r2);
       f32x2 dy[OWN ? 1 : P], dx[OWN ? 1 : P], dq[OWN ? 1 : P], dh[OWN ? 1 : P];
@@ -422,15 +458,15 @@ __global__ void __launch_bounds__(T0, T0 == 512 ? 1 : OWN ? 4 : 3) norm_res_grad
         copies_wait(a.stages - 2);
         __syncthreads();             // row r is there, and the row before it has been read
         ahead(r + a.stages - 1);
-        const T *yr = whole_row<T>(in, r, a.dim), *xr = whole_row<T>(in + array, r, a.dim);
-        const T* qr = os ? whole_row<T>(in + 2 * array, r, a.dim) : nullptr;
-        const T* hr = hs ? whole_row<T>(in + 3 * array, r, a.dim) : nullptr;
+        const T *yr = span_at<T>(in, at), *xr = span_at<T>(in + array, at);
+        const T* qr = os ? span_at<T>(in + 2 * array, at) : nullptr;
+        const T* hr = hs ? span_at<T>(in + 3 * array, at) : nullptr;
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-          dy[OWN ? 0 : p] = pair_at(yr, a.dim, 2 * p);
-          dx[OWN ? 0 : p] = pair_at(xr, a.dim, 2 * p);
-          dq[OWN ? 0 : p] = pair_at(qr, a.dim, 2 * p);
-          dh[OWN ? 0 : p] = pair_at(hr, a.dim, 2 * p);
+          dy[OWN ? 0 : p] = pair_at(yr, dim, 2 * p);
+          dx[OWN ? 0 : p] = pair_at(xr, dim, 2 * p);
+          dq[OWN ? 0 : p] = pair_at(qr, dim, 2 * p);
+          dh[OWN ? 0 : p] = pair_at(hr, dim, 2 * p);
         }
       }
       if (r + 1 < s.end) root = roots[r + 1];
@@ -459,7 +495,7 @@ __global__ void __launch_bounds__(T0, T0 == 512 ? 1 : OWN ? 4 : 3) norm_res_grad
 #pragma unroll
         for (int i = 0; i < pairs; ++i) {
           const int p = j * pairs + i;
-          const f32x2 b = mul2(w_at(p), y[i]), xo = fma2(rr1, b, mul2(scale, x[i])), v = mul2(h[i], g2_at(p));
+          const f32x2 b = mul2(w[p], y[i]), xo = fma2(rr1, b, mul2(scale, x[i])), v = mul2(h[i], g2[p]);
           t1 = fma2(v, xo, t1);
           t2 = fma2(b, fma2(rr2, v, o[i]), t2);
           t3 = fma2(b, xo, t3);
@@ -467,7 +503,7 @@ __global__ void __launch_bounds__(T0, T0 == 512 ? 1 : OWN ? 4 : 3) norm_res_grad
       }
       const float2 u1 = parts(t1), u2 = parts(t2), u3 = parts(t3);
       float sum[3] = {u1.x + u1.y, u2.x + u2.y, u3.x + u3.y};
-      block_sums<3>(sum, red, turn);
+      row_sums<3>(sum, red, turn, my.rank, a.ranks);
       const float c1 = hs ? r2 * r2 * r2 * (sum[0] * inv_dim) : 0.0f;
       const float c2 = a.g1 ? r1 * r1 * r1 * (fmaf(-c1, sum[2], sum[1]) * inv_dim) : 0.0f;
       const f32x2 n1 = both(-c1), n2 = both(-c2);
@@ -478,8 +514,8 @@ __global__ void __launch_bounds__(T0, T0 == 512 ? 1 : OWN ? 4 : 3) norm_res_grad
 #pragma unroll
         for (int i = 0; i < pairs; ++i) {
           const int p = j * pairs + i;
-          const f32x2 wp = w_at(p), xo = fma2(rr1, mul2(wp, y[i]), mul2(scale, x[i]));
-          const f32x2 t = fma2(n1, xo, fma2(rr2, mul2(h[i], g2_at(p)), o[i]));
+          const f32x2 wp = w[p], xo = fma2(rr1, mul2(wp, y[i]), mul2(scale, x[i]));
+          const f32x2 t = fma2(n1, xo, fma2(rr2, mul2(h[i], g2[p]), o[i]));
           sp[p] = fma2(t, mul2(y[i], rr1), sp[p]);
           s2[p] = fma2(mul2(h[i], rr2), xo, s2[p]);
           x[i] = mul2(scale, t);
@@ -487,14 +523,14 @@ __global__ void __launch_bounds__(T0, T0 == 512 ? 1 : OWN ? 4 : 3) norm_res_grad
         }
         if (OWN) {
           const int c = column<T, OWN>(j * per);
-          if (c >= a.dim) continue;
+          if (c >= dim) continue;
           *reinterpret_cast<uint4*>(static_cast<T*>(a.dy) + at + c) = narrow(y);
           *reinterpret_cast<uint4*>(static_cast<T*>(a.dx) + at + c) = narrow(x);
         } else {
 #pragma unroll
           for (int i = 0; i < pairs; ++i) {
-            store_pair(static_cast<T*>(a.dy) + at, a.dim, (j * pairs + i) * 2, y[i]);
-            store_pair(static_cast<T*>(a.dx) + at, a.dim, (j * pairs + i) * 2, x[i]);
+            store_pair(static_cast<T*>(a.dy) + at, dim, (j * pairs + i) * 2, y[i]);
+            store_pair(static_cast<T*>(a.dx) + at, dim, (j * pairs + i) * 2, x[i]);
           }
         }
       }
@@ -504,18 +540,18 @@ __global__ void __launch_bounds__(T0, T0 == 512 ? 1 : OWN ? 4 : 3) norm_res_grad
     for (int p = 0; p < P; ++p) {
       const float2 f = parts(sp[p]);
       const int c = column<T, OWN>(2 * p), d = column<T, OWN>(2 * p + 1);
-      if (c < a.dim) span_sums(a, s, !any, c, f.x);
-      if (d < a.dim) span_sums(a, s, !any, d, f.y);
+      if (c < dim) span_sums(a, my.block, s, !any, my.c0 + c, f.x);
+      if (d < dim) span_sums(a, my.block, s, !any, my.c0 + d, f.y);
     }
     any = true;
   }
-  float* keep = a.ws + (size_t)blockIdx.x * 2 * a.dim;
+  float* keep = a.ws + (size_t)my.block * 2 * a.dim + my.c0;
 #pragma unroll
   for (int p = 0; p < P; ++p) {
     const float2 f = parts(s2[p]);
     const int c = column<T, OWN>(2 * p), d = column<T, OWN>(2 * p + 1);
-    if (c < a.dim) keep[a.dim + c] = f.x;
-    if (d < a.dim) keep[a.dim + d] = f.y;
+    if (c < dim) keep[a.dim + c] = f.x;
+    if (d < dim) keep[a.dim + d] = f.y;
   }
 }
 
@@ -564,7 +600,7 @@ __global__ void __launch_bounds__(kNrThreads) norm_res_grad_wide_kernel(NormResG
   for (int c = threadIdx.x; c < 2 * a.dim; c += kNrThreads) sums[c] = 0.0f;
   __syncthreads();
   NormResSpan span = {-1, 0, 0};
-  while (next_span(a, span)) {
+  while (next_span(a, blockIdx.x, span)) {
     const float* gate = a.gate ? a.gate + (size_t)span.g * a.dim : nullptr;
     for (int r = span.first; r < span.end; ++r) {
       const size_t row = (size_t)r * a.dim;
@@ -606,36 +642,40 @@ __global__ void __launch_bounds__(kNrThreads) norm_res_grad_wide_kernel(NormResG
   }
 }
 
-// The blocks' sums in order: 32 columns a block, 32 runs of blocks added side by side
-// and then in order.  blockIdx.y: 0 the post norm's (and that of a gate for all rows,
-// which is made of the same sums), 1 the pre norm's, beyond the gates' (blocks have
-// parts of them).
-__global__ void __launch_bounds__(1024, 2) norm_res_join_kernel(NormResGradArgs a, int blocks) {
-  __shared__ float red[32][33];
-  const int lane = threadIdx.x & 31, run = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+// The blocks' sums in order: `wide` columns a block, for each of them runs of blocks
+// added side by side and then in order.  blockIdx.y: 0 the post norm's (and that of a
+// gate for all rows, which is made of the same sums), 1 the pre norm's, beyond the gates'
+// (blocks have parts of them).
+__global__ void __launch_bounds__(1024) norm_res_join_kernel(NormResGradArgs a, int blocks, int wide) {
+  __shared__ float red[1024 + 128];
+  const int col = threadIdx.x % wide, run = threadIdx.x / wide, runs = blockDim.x / wide, c = blockIdx.x * wide + col;
   const bool in = c < a.dim, gated = blockIdx.y == 0 && a.gate && a.parts > 1 && a.gates > 1;
   dependency_wait();
   const auto add = [&](int which, size_t from, int n) {
-    const int per = (n + 31) / 32, begin = min(n, run * per), end = min(n, begin + per);
+    const int per = (n + runs - 1) / runs, begin = min(n, run * per), end = min(n, begin + per);
     const float* v = a.ws + (from * 2 + which) * a.dim + c;
     float s = 0.0f;
-    if (in && gated) {   // each gate's blocks by themselves
-      for (int g = begin / a.parts, i = begin; i < end; ++g) {
-        const int stop = min(end, (g + 1) * a.parts);
-        float t = 0.0f;
-#pragma unroll 8
-        for (; i < stop; ++i) t += v[(size_t)i * 2 * a.dim];
-        s = fmaf(a.gate[(size_t)g * a.dim + c], t, s);
+    const auto some = [&](int from_block, int to_block) {   // eight loads under way at once
+      float t = 0.0f;
+      for (int i0 = from_block; i0 < to_block; i0 += 8) {
+        float u[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) u[q] = i0 + q < to_block ? v[(size_t)(i0 + q) * 2 * a.dim] : 0.0f;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) t += u[q];
       }
-    } else if (in) {
-#pragma unroll 8
-      for (int i = begin; i < end; ++i) s += v[(size_t)i * 2 * a.dim];
-    }
-    red[run][lane] = s;
+      return t;
+    };
+    if (in && gated)   // gate by gate
+      for (int g = begin / a.parts, i = begin; i < end; i = (++g) * a.parts)
+        s = fmaf(a.gate[(size_t)g * a.dim + c], some(i, min(end, (g + 1) * a.parts)), s);
+    else if (in)
+      s = some(begin, end);
+    red[run * (wide + 1) + col] = s;
     __syncthreads();
     float t = 0.0f;
     if (run == 0)
-      for (int i = 0; i < 32; ++i) t += red[i][lane];
+      for (int i = 0; i < runs; ++i) t += red[i * (wide + 1) + col];
     __syncthreads();
     return t;
   };
@@ -669,33 +709,42 @@ struct NormResShape {
   int threads = 0;   // 0: the kernels for any width
   int each = 0;      // elements a thread
   bool own = false;
-  int stages = 0, row_units = 0;
+  int stages = 0, row_units = 0, ranks = 1, part = 0;
   size_t smem = 0;
 };
 constexpr size_t kNrSmem = 220 * 1024;
-// Sixteen elements a thread, more where 512 threads are not enough.
+constexpr int kNrMost = 512;
+// A warp of eight elements a lane for the narrowest rows, else sixteen elements a
+// thread; a cluster of blocks where a row is more than the threads of one hold, or two
+// rows of it more than shared memory does.
 NormResShape norm_res_shape(int dtype, int dim, bool grad) {
   NormResShape s;
-  const int es = dtype ? 2 : 4;
+  const int es = dtype ? 2 : 4, per = 16 / es;
   s.own = (size_t)dim * es % 16 == 0;
-  for (s.each = 16; s.each <= 32; s.each *= 2) {
-    const int threads = ((dim + s.each - 1) / s.each + 31) / 32 * 32;
-    if (threads > 512 || (grad && !s.own && s.each == 32)) continue;
-    s.row_units = s.own ? s.each * es * threads / 16 : (dim * es + 15) / 16 + 1;
+  for (s.ranks = 1; s.ranks <= kNrRanks; s.ranks *= 2) {
+    s.part = (dim + s.ranks - 1) / s.ranks;
+    if (s.own) s.part = (s.part + per - 1) / per * per;
+    // (forward: 32 elements a thread before two blocks, which cost a row two exchanges)
+    s.each = s.part <= 256 ? 8 : s.part <= 16 * 512 || grad ? 16 : 32;
+    const int threads = ((s.part + s.each - 1) / s.each + 31) / 32 * 32;
+    if (threads > kNrMost) continue;
+    s.row_units = s.own ? s.each * es * threads / 16 : (s.part * es + 15) / 16 + 1;
     const size_t row = (size_t)(grad ? 4 : 2) * s.row_units * 16;
     s.stages = (int)std::min<size_t>(kNrStages, kNrSmem / row);
     s.smem = s.stages * row;
-    if (s.stages >= (s.own ? 1 : 2)) s.threads = threads;
-    break;
+    if (s.stages < 2) continue;
+    s.threads = threads;
+    return s;
   }
+  s.ranks = 1;
   return s;
 }
-// Blocks that run at once: by registers (threads of an SM) and by shared memory.
-int norm_res_slots(const NormResShape& s, int threads_per_sm) {
+// Rows that are worked on at once: by registers (128 a thread; 80 in the narrowest) and by shared memory.
+int norm_res_slots(const NormResShape& s, bool grad) {
   if (!s.threads) return device_sms() * 4;
-  int n = std::max(1, std::min((s.own ? threads_per_sm : threads_per_sm * 3 / 4) / s.threads, 32));
-  n = std::min(n, std::max(1, (int)(kNrSmem / (s.smem + 2048))));
-  return device_sms() * n;
+  int n = s.threads == 32 && s.each == 8 ? (grad && !s.own ? 16 : 24) : 512 * (grad && !s.own ? 3 : 4) / 4 / s.threads;
+  n = std::max(1, std::min(n, (int)(kNrSmem / (s.smem + 2048))));
+  return std::max(1, device_sms() * n / s.ranks);
 }
 
 struct NormResSplit {
@@ -716,31 +765,42 @@ NormResSplit norm_res_split(int rows, int gates, int slots) {
   p.blocks = p.parts > 1 ? (long long)gates * p.parts : (gates + p.block_gates - 1) / p.block_gates;
   return p;
 }
-constexpr int kNrFwdThreads = 512, kNrGradThreads = 512;   // of an SM
 
 template <typename K, typename A>
-cudaError_t norm_res_launch(K kernel, const A& a, long long blocks, int threads, size_t smem, cudaStream_t s) {
+cudaError_t norm_res_launch(K kernel, const A& a, long long blocks, int threads, size_t smem, cudaStream_t s, int ranks = 1) {
   if (smem > 40 * 1024) {   // (the static part counts too)
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
-  kernel<<<(unsigned)blocks, threads, smem, s>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(blocks * ranks));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = ranks;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = ranks > 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <typename T, bool OWN>
 cudaError_t norm_res_forward(const NormResArgs& a, const NormResShape& s, long long blocks, cudaStream_t st) {
   constexpr int W = sizeof(T) == 4 ? 2 : 1;   // units of eight elements
-  if (s.threads <= 128) return norm_res_launch(norm_res_kernel<T, 2 * W, OWN, 128>, a, blocks, s.threads, s.smem, st);
-  if (s.each == 16) return norm_res_launch(norm_res_kernel<T, 2 * W, OWN, 512>, a, blocks, s.threads, s.smem, st);
-  return norm_res_launch(norm_res_kernel<T, 4 * W, OWN, 512>, a, blocks, s.threads, s.smem, st);
+  if (s.each == 8) return norm_res_launch(norm_res_kernel<T, W, OWN, 32>, a, blocks, s.threads, s.smem, st, s.ranks);
+  if (s.threads <= 128) return norm_res_launch(norm_res_kernel<T, 2 * W, OWN, 128>, a, blocks, s.threads, s.smem, st, s.ranks);
+  if (s.each == 16) return norm_res_launch(norm_res_kernel<T, 2 * W, OWN, 512>, a, blocks, s.threads, s.smem, st, s.ranks);
+  return norm_res_launch(norm_res_kernel<T, 4 * W, OWN, 512>, a, blocks, s.threads, s.smem, st, s.ranks);
 }
 template <typename T, bool OWN>
 cudaError_t norm_res_backward(const NormResGradArgs& a, const NormResShape& s, long long blocks, cudaStream_t st) {
   constexpr int W = sizeof(T) == 4 ? 2 : 1;
-  if (s.threads <= 128) return norm_res_launch(norm_res_grad_kernel<T, 2 * W, OWN, 128, true>, a, blocks, s.threads, s.smem, st);
-  if (s.each == 16) return norm_res_launch(norm_res_grad_kernel<T, 2 * W, OWN, 512, true>, a, blocks, s.threads, s.smem, st);
-  return norm_res_launch(norm_res_grad_kernel<T, 4 * W, true, 512, false>, a, blocks, s.threads, s.smem, st);
+  if (s.each == 8) return norm_res_launch(norm_res_grad_kernel<T, W, OWN, 32>, a, blocks, s.threads, s.smem, st, s.ranks);
+  if (s.threads <= 128) return norm_res_launch(norm_res_grad_kernel<T, 2 * W, OWN, 128>, a, blocks, s.threads, s.smem, st, s.ranks);
+  return norm_res_launch(norm_res_grad_kernel<T, 2 * W, OWN, 512>, a, blocks, s.threads, s.smem, st, s.ranks);
 }
 
 }  // namespace
@@ -764,7 +824,7 @@ extern "C" size_t mg_norm_residual_workspace_bytes(int rows, int dim, int gates)
   long long blocks = 1;
   for (int dtype = 0; rows && dtype < 2; ++dtype) {
     const mg::NormResShape s = mg::norm_res_shape(dtype, dim, true);
-    blocks = std::max(blocks, mg::norm_res_split(rows, gates ? gates : 1, mg::norm_res_slots(s, mg::kNrGradThreads)).blocks);
+    blocks = std::max(blocks, mg::norm_res_split(rows, gates ? gates : 1, mg::norm_res_slots(s, true)).blocks);
   }
   return ((size_t)blocks * 2 * dim + 4) * sizeof(float);
 }
@@ -787,14 +847,15 @@ extern "C" mg_status mg_norm_residual_forward(int dtype, const void* y, const vo
                             {h, n, true, h == y || h == x}, {rstd, (size_t)rows * 8, true, false}});
   if (st != MG_OK || !rows) return st;
   const mg::NormResShape shape = mg::norm_res_shape(dtype, dim, false);
-  mg::NormResArgs a = {y, x, gamma_post, gate, gamma_pre, rows, dim, gates ? rows / gates : rows, scale, eps, x_out, h, rstd, 1, shape.stages, shape.row_units};
+  mg::NormResArgs a = {y, x, gamma_post, gate, gamma_pre, rows, dim, gates ? rows / gates : rows, scale, eps, x_out, h, rstd, 1, shape.stages, shape.row_units,
+                       shape.ranks, shape.part};
   cudaStream_t s = (cudaStream_t)stream;
   cudaError_t e;
   if (!shape.threads) {
     e = dtype ? mg::norm_res_launch(mg::norm_res_wide_kernel<mg::bf16>, a, rows, mg::kNrThreads, 0, s)
               : mg::norm_res_launch(mg::norm_res_wide_kernel<float>, a, rows, mg::kNrThreads, 0, s);
   } else {
-    const int slots = mg::norm_res_slots(shape, mg::kNrFwdThreads);
+    const int slots = mg::norm_res_slots(shape, false);
     a.block_rows = (rows + slots - 1) / slots;
     const long long blocks = (rows + a.block_rows - 1) / a.block_rows;
     if (dtype)
@@ -833,7 +894,7 @@ extern "C" mg_status mg_norm_residual_backward(int dtype, const void* dx_out, co
                             {workspace, need, true, false}});
   if (st != MG_OK) return st;
   mg::NormResGradArgs a = {dx_out, dh, y, x, rstd, gamma_post, gate, gamma_pre, rows, dim, 0, gates ? gates : 1, scale,
-                           dy, dx, dgamma_post, dgate, dgamma_pre, static_cast<float*>(workspace), 1, 1, 1, 0, 0};
+                           dy, dx, dgamma_post, dgate, dgamma_pre, static_cast<float*>(workspace), 1, 1, 1, 0, 0, 1, dim};
   cudaStream_t s = (cudaStream_t)stream;
   if (!rows) {
     const long long blocks = ((long long)a.gates * dim + 255) / 256;
@@ -841,9 +902,11 @@ extern "C" mg_status mg_norm_residual_backward(int dtype, const void* dx_out, co
   }
   a.gate_rows = rows / a.gates;
   const mg::NormResShape shape = mg::norm_res_shape(dtype, dim, true);
-  const mg::NormResSplit split = mg::norm_res_split(rows, a.gates, mg::norm_res_slots(shape, mg::kNrGradThreads));
+  const mg::NormResSplit split = mg::norm_res_split(rows, a.gates, mg::norm_res_slots(shape, true));
   a.stages = shape.stages;
   a.row_units = shape.row_units;
+  a.ranks = shape.ranks;
+  a.part = shape.part;
   a.parts = split.parts;
   a.block_rows = split.block_rows;
   a.block_gates = split.block_gates;
@@ -859,6 +922,12 @@ extern "C" mg_status mg_norm_residual_backward(int dtype, const void* dx_out, co
                    : mg::norm_res_backward<float, false>(a, shape, split.blocks, s);
   const int gate_blocks = dgate && a.parts > 1 && a.gates > 1 ? std::min(a.gates, 65533) : 0;
   if (e == cudaSuccess && (dgamma_post || dgamma_pre || (dgate && a.parts > 1)))
-    e = mg::launch_dependent(mg::norm_res_join_kernel, dim3((dim + 31) / 32, 2 + gate_blocks), 1024, 0, s, a, (int)split.blocks);
+  {
+    // (many blocks: narrow rows; eight columns of a sector each, and four times the runs)
+    const int wide = split.blocks > 1024 ? 8 : 32;
+    const unsigned threads = 32 * (unsigned)std::max(4ll, std::min(32ll, split.blocks / 12));
+    e = mg::launch_dependent(mg::norm_res_join_kernel, dim3((dim + wide - 1) / wide, 2 + gate_blocks), threads, 0, s, a,
+                             (int)split.blocks, wide);
+  }
   return mg::op_end(fn, e);
 }

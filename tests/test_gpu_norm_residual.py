@@ -147,7 +147,8 @@ def _backward_check(i, rstd, scale, o, t):
 
 SHAPES = [(1, 1, 1), (3, 2, 0), (5, 8, 1), (4, 100, 2), (7, 777, 7), (33, 1024, 1), (64, 2048, 4), (130, 520, 0),
           (19, 4096, 1), (5, 4100, 1), (6, 8192, 2), (3, 16384, 1), (2, 16392, 1), (2, 40001, 2), (1000, 64, 1),
-          (2500, 264, 50), (300, 2056, 300), (9, 6000, 9)]
+          (2500, 264, 50), (300, 2056, 300), (9, 6000, 9), (400, 256, 1), (77, 250, 7), (40, 12288, 2), (30, 9001, 1),
+          (6, 32768, 3), (3, 65536, 1), (2, 70001, 1), (4, 70000, 2)]
 
 
 @pytest.mark.parametrize("t", ["f32", "bf16"])
