@@ -527,11 +527,13 @@ mg_status mg_norm_residual_backward(int dtype, const void* dx_out, const void* d
  * param is fp32 or bf16 (rounded to nearest), grad fp32 or bf16, copy (NULL, or
  * bf16 [count]) receives the rounded new parameters.  Pointers are aligned to
  * their element.  Memory that is written may not overlap any other of the list.
- * Creation copies the table to the device (88 bytes per 8192 elements) and is
+ * Creation copies the table to the device (88 bytes per 8192 elements, per 2048 of short
+ * lists) and is
  * bound to the current device; the list keeps no state of its own.
  * lr_device, step_device (device memory, fp32 and int32; NULL: lr and step are
  * taken) are read by the kernel, so that a captured step can be replayed with
- * new values; a step_device below 1 counts as 1. */
+ * new values; a step_device below 1 counts as 1.  Neither they nor norm may lie in
+ * memory that the step writes. */
 typedef struct {
   void* param;
   const void* grad;

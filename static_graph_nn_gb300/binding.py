@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmg.so")
@@ -737,6 +738,7 @@ def norm_residual_backward(dx_out, dh, y, x, rstd, dy, dx, workspace, gamma_post
 
 # ---- AdamW over many tensors -------------------------------------------------------
 ADAMW_BLOCK = 256     # elements of a tensor under one scale of its 8-bit moments
+_ADAMW_ROW = struct.Struct("@7QNiif4x")   # mg_adamw_tensor
 
 
 def adamw_state(params, bits: int = 32):
@@ -783,32 +785,24 @@ class AdamW:
         bits = 8 if n and lists["m"][0] is not None and lists["m"][0].dtype in codes else 32
         if not 0 <= seed < 2 ** 64:
             _refuse("seed must lie in [0, 2^64)")
-        arr = (mg_adamw_tensor * max(1, n))()
-        for i, p in enumerate(params):
-            _dense(p, f"parameter {i}")
-            a = arr[i]
-            a.param, a.count, a.param_dtype, a.weight_decay = _ptr(p), p.numel(), _code(p, f"parameter {i}"), decay[i]
-            g = lists["grads"][i]
-            if g is None:
-                _refuse(f"gradient {i} is missing")
-            _dense(g, f"gradient {i}", p.shape)
-            a.grad, a.grad_dtype = _ptr(g), _code(g, f"gradient {i}")
-            for k in ("m", "v"):
-                t = lists[k][i]
-                if t is None or (t.dtype not in codes if bits == 8 else t.dtype != torch.float32):
+        code, _, f32, _ = _type_tables()
+        rows = []
+        for i, (p, g, m, v, ms, vs, c) in enumerate(zip(params, *lists.values())):
+            if g is None or m is None or v is None:
+                _refuse(f"gradient or moment {i} is missing")
+            if (ms is None or vs is None) != (bits == 32) or (bits == 32 and (ms is not None or vs is not None)):
+                _refuse("m_scales and v_scales belong to 8-bit moments")
+            for t, k in ((m, "m"), (v, "v")):
+                if t.dtype not in codes if bits == 8 else t.dtype is not f32:
                     _refuse(f"{k} {i} must be {'8-bit codes' if bits == 8 else 'float32'}, as the first is")
-                _dense(t, f"{k} {i}", p.shape)
-                setattr(a, k, _ptr(t))
-                s = lists[k + "_scales"][i]
-                if (s is None) != (bits == 32):
-                    _refuse(f"{k}_scales belong to 8-bit moments")
-                if s is not None:
-                    _per_row(s, f"{k}_scales {i}", (-(-p.numel() // ADAMW_BLOCK),))
-                    setattr(a, k + "_scales", _ptr(s))
-            c = lists["copies"][i]
-            if c is not None:
-                _per_row(c, f"copy {i}", p.shape, torch.bfloat16)
-                a.copy = _ptr(c)
+            shape, count = p.shape, p.numel()
+            blocks = (-(-count // ADAMW_BLOCK),)
+            rows.append(_ADAMW_ROW.pack(
+                _at(p, "a parameter", p.dtype, shape), _at(g, "a gradient", g.dtype, shape), _at(m, "m", m.dtype, shape),
+                _at(v, "v", v.dtype, shape), _at(ms, "m_scales", f32, blocks) or 0, _at(vs, "v_scales", f32, blocks) or 0,
+                _at(c, "a copy", torch.bfloat16, shape) or 0, count, _code(p, f"parameter {i}", code),
+                _code(g, f"gradient {i}", code), decay[i]))
+        arr = (mg_adamw_tensor * max(1, n)).from_buffer_copy(b"".join(rows) or bytes(_ADAMW_ROW.size))
         h = _P()
         _status(self.lib.mg_adamw_create(n, arr, bits, betas[0], betas[1], eps, seed, ctypes.byref(h)))
         self.h, self.tensors = h, (params, lists)
@@ -820,12 +814,14 @@ class AdamW:
         they are taken times max_norm / norm where that is below 1, and nothing changes
         where it is not finite."""
         lr_dev = step_dev = None
-        if not isinstance(lr, (int, float)):
+        if hasattr(lr, "data_ptr"):
             lr_dev, lr = lr, 0.0
             _per_row(lr_dev, "lr", lr_dev.shape if lr_dev.numel() == 1 else (1,))
-        if not isinstance(step, int):
+        if hasattr(step, "data_ptr"):
             step_dev, step = step, 1
             _per_row(step_dev, "step", step_dev.shape if step_dev.numel() == 1 else (1,), _type_tables()[3])
+        elif not 0 < step < 2 ** 63:
+            _refuse(f"step must be at least 1 and below 2^63, not {step}")
         if norm is not None and (norm.dtype != _type_tables()[2] or norm.numel() < 1):
             _refuse("norm must be float32 with one value at least")
         _status(self.lib.mg_adamw_step(self.h, lr, step, _ptr(lr_dev), _ptr(step_dev), _ptr(norm), max_norm,

@@ -26,7 +26,9 @@
 #include <algorithm>
 #include <cmath>
 #include <exception>
+#include <iterator>
 #include <memory>
+#include <utility>
 #include <vector>
 
 #include <cuda_fp16.h>
@@ -581,6 +583,7 @@ struct mg_adamw {
   mg::AdamwChunk* chunks = nullptr;
   double beta1 = 0, beta2 = 0, eps = 0;
   unsigned long long seed = 0;
+  std::vector<std::pair<uintptr_t, uintptr_t>> written;   // the memory that a step writes: begins and ends, ascending
 };
 
 using mg::op_fail;
@@ -668,6 +671,8 @@ extern "C" mg_status mg_adamw_create(int n, const mg_adamw_tensor* tensors, int 
       if (s.written && s.hi > whi) { whi = s.hi; wt = s.tensor; }
     }
     std::unique_ptr<mg_adamw> o(new mg_adamw());
+    for (const Span& s : spans)
+      if (s.written) o->written.emplace_back(s.lo, s.hi);
     o->bits = state_bits;
     o->beta1 = beta1;
     o->beta2 = beta2;
@@ -722,6 +727,12 @@ extern "C" mg_status mg_adamw_step(mg_adamw* o, double lr, long long step, const
     return op_fail(MG_ERR_INVALID_ARG, "%s: the optimizer belongs to device %d but device %d is current", fn, o->device, dev);
   mg_status st = mg::op_begin(fn, {{lr_device, 4}, {step_device, 4}, {norm, 4}});
   if (st != MG_OK || !o->n_chunks) return st;
+  for (const void* p : {(const void*)lr_device, (const void*)step_device, (const void*)norm}) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    const auto behind = std::lower_bound(o->written.begin(), o->written.end(), std::make_pair(at + 4, (uintptr_t)0));
+    if (p && behind != o->written.begin() && std::prev(behind)->second > at)
+      return op_fail(MG_ERR_INVALID_ARG, "%s: lr_device, step_device or norm lies in memory that the step writes", fn);
+  }
   mg::AdamwStep a;
   a.chunks = o->chunks;
   a.b1 = (float)o->beta1;

@@ -387,7 +387,8 @@ def test_refused_steps():
     opt = mg.AdamW(d["p"], d["g"], d["m"], d["v"])
     for args, kw in (((-1.0, 1), {}), ((math.nan, 1), {}), ((0.1, 0), {}), ((0.1, 1), dict(norm=torch.zeros(1, device="cuda"), max_norm=-1.0)),
                      ((torch.zeros(2, device="cuda"), 1), {}), ((0.1, torch.ones(1, device="cuda")), {}),
-                     ((0.1, 1), dict(norm=torch.zeros(1)))):
+                     ((0.1, 1), dict(norm=torch.zeros(1))), ((0.1, 2 ** 63), {}), ((0.1, 1), dict(norm=d["v"][0][3:5])),
+                     ((d["p"][0][9:], 1), {})):
         with pytest.raises(binding.MGError):
             opt.step(*args, **kw)
     opt.close()
