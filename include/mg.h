@@ -494,8 +494,8 @@ mg_status mg_token_logprobs_backward(int dtype, const void* logits, long long ro
  * inputs: dy, dx, and, where not NULL, dgamma_post, dgamma_pre [dim] and dgate
  * [gates, dim], fp32 sums in a fixed order (the same bits in every run).  dy and
  * dx may each be dx_out, dh, y or x itself.  workspace:
- * mg_norm_residual_workspace_bytes (0 for arguments the call would refuse); its
- * contents before the call do not matter. */
+ * mg_norm_residual_workspace_bytes (for these rows or fewer, of either type; 0 for
+ * arguments the call would refuse); its contents before the call do not matter. */
 size_t mg_norm_residual_workspace_bytes(int rows, int dim, int gates);
 mg_status mg_norm_residual_forward(int dtype, const void* y, const void* x, int rows, int dim,
                                    const float* gamma_post, const float* gate, int gates,

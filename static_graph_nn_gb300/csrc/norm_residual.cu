@@ -74,15 +74,16 @@ struct Unit {
   static constexpr int kPer = 16 / (int)sizeof(T);   // elements
   static constexpr int kPairs = kPer / 2;
 };
-template <typename T, bool OWN>
+// (OWN: a block's threads may be any number of warps up to T0; else they are T0)
+template <typename T, bool OWN, int T0>
 __device__ __forceinline__ int column(int e) {
   constexpr int per = Unit<T>::kPer;
-  return OWN ? ((int)threadIdx.x + e / per * (int)blockDim.x) * per + e % per : (int)threadIdx.x + e * (int)blockDim.x;
+  return OWN ? ((int)threadIdx.x + e / per * (int)blockDim.x) * per + e % per : (int)threadIdx.x + e * T0;
 }
 // The fp32 vector's values at columns e and e + 1 of this thread, `other` where there are none.
-template <typename T, bool OWN>
+template <typename T, bool OWN, int T0>
 __device__ __forceinline__ f32x2 vector_at(const float* v, int dim, float other, int e) {
-  const int c = column<T, OWN>(e), d = column<T, OWN>(e + 1);
+  const int c = column<T, OWN, T0>(e), d = column<T, OWN, T0>(e + 1);
   if (OWN) {
     if (!v || c >= dim) return both(other);
     const float2 f = *reinterpret_cast<const float2*>(v + c);
@@ -108,14 +109,14 @@ __device__ __forceinline__ uint4 narrow(const f32x2 (&f)[2]) {
   return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
 }
 // Columns e and e + 1 of a row in shared memory, zeros beyond it.
-template <typename T>
+template <int T0, typename T>
 __device__ __forceinline__ f32x2 pair_at(const T* p, int dim, int e) {
-  const int c = column<T, false>(e), d = column<T, false>(e + 1);
+  const int c = column<T, false, T0>(e), d = column<T, false, T0>(e + 1);
   return both(p && c < dim ? ld_elem(p, c) : 0.0f, p && d < dim ? ld_elem(p, d) : 0.0f);
 }
-template <typename T>
+template <int T0, typename T>
 __device__ __forceinline__ void store_pair(T* p, int dim, int e, f32x2 v) {
-  const int c = column<T, false>(e), d = column<T, false>(e + 1);
+  const int c = column<T, false, T0>(e), d = column<T, false, T0>(e + 1);
   const float2 f = parts(v);
   if (c < dim) st_elem(p, c, f.x);
   if (d < dim) st_elem(p, d, f.y);
@@ -217,11 +218,13 @@ __device__ __forceinline__ void row_sums(float (&v)[N], RowSums<N>& red, int& tu
     for (int i = 0; i < ranks; ++i) v[n] += *reinterpret_cast<volatile float*>(&red.block[now][i][n]);
   }
 }
-// Zeros beyond the warps; in a cluster, every block is there before one writes to it.
+// Zeros beyond the warps (the first sums' barrier lies between them and their reads); in
+// a cluster, every block is there before one writes to it.
 template <int N>
 __device__ __forceinline__ void clear_sums(RowSums<N>& red, int ranks) {
-  for (int i = threadIdx.x; i < 2 * 16 * N; i += blockDim.x) (&red.warp[0][0][0])[i] = 0.0f;
-  __syncthreads();
+  const int warps = blockDim.x >> 5;
+  for (int i = threadIdx.x; i < 2 * 16 * N; i += blockDim.x)
+    if (i % 16 >= warps) (&red.warp[0][0][0])[i] = 0.0f;
   if (ranks > 1) asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // 1 / sqrt(x): an estimate and one step of Newton's method.
@@ -241,9 +244,8 @@ __device__ __forceinline__ void copies_wait(int n) {
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-// (T0: threads at most)
 template <typename T, int U, bool OWN, int T0>
-__global__ void __launch_bounds__(T0, T0 == 512 ? 1 : T0 == 128 ? 4 : 24) norm_res_kernel(NormResArgs a) {
+__global__ void __launch_bounds__(T0, T0 == 32 ? 24 : (U * Unit<T>::kPer == 8 ? 768 : 512) / T0) norm_res_kernel(NormResArgs a) {
   constexpr int per = Unit<T>::kPer, pairs = Unit<T>::kPairs, E = U * per, P = E / 2;
   extern __shared__ __align__(16) uint4 ring[];   // [stage][y, x][U][threads]
   __shared__ RowSums<1> red;
@@ -267,12 +269,13 @@ __global__ void __launch_bounds__(T0, T0 == 512 ? 1 : T0 == 128 ? 4 : 24) norm_r
     asm volatile("cp.async.commit_group;" ::: "memory");
     fill = fill + 1 == a.stages ? 0 : fill + 1;
   };
-  if (OWN)
-    for (int i = 0; i < 2 * a.stages; ++i) clear_row<T, U>(ring + i * array, true, dim);
-  for (int i = 0; i < a.stages - 1; ++i) ahead(first + i);
+  // (the vectors' loads and the first rows' copies are under way together)
   f32x2 w[P], g2[P];
 #pragma unroll
-  for (int p = 0; p < P; ++p) g2[p] = vector_at<T, OWN>(a.g2 ? a.g2 + my.c0 : nullptr, dim, 0.0f, 2 * p);
+  for (int p = 0; p < P; ++p) g2[p] = vector_at<T, OWN, T0>(a.g2 ? a.g2 + my.c0 : nullptr, dim, 0.0f, 2 * p);
+  for (int i = 0; i < a.stages - 1; ++i) ahead(first + i);
+  if (OWN)
+    for (int i = 0; i < 2 * a.stages; ++i) clear_row<T, U>(ring + i * array, true, dim);
   const float inv_dim = 1.0f / a.dim;
   const f32x2 scale = both(a.scale);
   int gate_end = first, slot = 0, turn = 0;
@@ -282,7 +285,7 @@ __global__ void __launch_bounds__(T0, T0 == 512 ? 1 : T0 == 128 ? 4 : 24) norm_r
       const float* gate = a.gate ? a.gate + (size_t)gi * a.dim + my.c0 : nullptr;
 #pragma unroll
       for (int p = 0; p < P; ++p)
-        w[p] = mul2(vector_at<T, OWN>(a.g1 ? a.g1 + my.c0 : nullptr, dim, 1.0f, 2 * p), vector_at<T, OWN>(gate, dim, 1.0f, 2 * p));
+        w[p] = mul2(vector_at<T, OWN, T0>(a.g1 ? a.g1 + my.c0 : nullptr, dim, 1.0f, 2 * p), vector_at<T, OWN, T0>(gate, dim, 1.0f, 2 * p));
       gate_end = (gi + 1) * a.gate_rows;
     }
     f32x2 y[P], x[P];
@@ -304,8 +307,8 @@ __global__ void __launch_bounds__(T0, T0 == 512 ? 1 : T0 == 128 ? 4 : 24) norm_r
       const T *yr = span_at<T>(in, row_at(r)), *xr = span_at<T>(in + array, row_at(r));
 #pragma unroll
       for (int p = 0; p < P; ++p) {
-        y[p] = pair_at(yr, dim, 2 * p);
-        x[p] = pair_at(xr, dim, 2 * p);
+        y[p] = pair_at<T0>(yr, dim, 2 * p);
+        x[p] = pair_at<T0>(xr, dim, 2 * p);
       }
     }
     float r1 = 1.0f, r2 = 1.0f;
@@ -329,7 +332,7 @@ __global__ void __launch_bounds__(T0, T0 == 512 ? 1 : T0 == 128 ? 4 : 24) norm_r
     if (OWN) {
 #pragma unroll
       for (int j = 0; j < U; ++j) {
-        const int c = column<T, OWN>(j * per);
+        const int c = column<T, OWN, T0>(j * per);
         if (c >= dim) continue;
         f32x2 f[pairs];
 #pragma unroll
@@ -343,8 +346,8 @@ __global__ void __launch_bounds__(T0, T0 == 512 ? 1 : T0 == 128 ? 4 : 24) norm_r
     } else {
 #pragma unroll
       for (int p = 0; p < P; ++p) {
-        store_pair(xo, dim, 2 * p, x[p]);
-        if (h) store_pair(h, dim, 2 * p, mul2(x[p], mul2(rq, g2[p])));
+        store_pair<T0>(xo, dim, 2 * p, x[p]);
+        if (h) store_pair<T0>(h, dim, 2 * p, mul2(x[p], mul2(rq, g2[p])));
       }
     }
     if (a.rstd && my.rank == 0 && threadIdx.x == 0) *reinterpret_cast<float2*>(a.rstd + 2 * (size_t)r) = make_float2(r1, r2);
@@ -384,9 +387,8 @@ __device__ __forceinline__ void span_sums(const NormResGradArgs& a, int block, c
 
 // The three sums of a row in one exchange.  With b = w y (w = gate g1) and q = dx' + r2 dh g2:
 // S1 = sum dh g2 x', and sum w t y = sum b q - r2^3 / dim S1 sum b x'.
-// (T0: threads at most)
 template <typename T, int U, bool OWN, int T0>
-__global__ void __launch_bounds__(T0, T0 == 512 ? 1 : T0 == 128 ? (OWN ? 4 : 3) : OWN ? 24 : 16) norm_res_grad_kernel(NormResGradArgs a) {
+__global__ void __launch_bounds__(T0, T0 == 32 ? (OWN ? 24 : 16) : (U * Unit<T>::kPer == 8 ? 768 : OWN || T0 >= 256 ? 512 : 384) / T0) norm_res_grad_kernel(NormResGradArgs a) {
   constexpr int per = Unit<T>::kPer, pairs = Unit<T>::kPairs, E = U * per, P = E / 2;
   extern __shared__ __align__(16) uint4 ring[];   // [stage][y, x, dx_out, dh][U][threads]
   __shared__ RowSums<3> red;
@@ -402,15 +404,17 @@ __global__ void __launch_bounds__(T0, T0 == 512 ? 1 : T0 == 128 ? (OWN ? 4 : 3) 
 #pragma unroll
   for (int p = 0; p < P; ++p) {
     s2[p] = both(0.0f);
-    g2[p] = vector_at<T, OWN>(hs ? a.g2 + my.c0 : nullptr, dim, 0.0f, 2 * p);
+    g2[p] = vector_at<T, OWN, T0>(hs ? a.g2 + my.c0 : nullptr, dim, 0.0f, 2 * p);
   }
-  if (OWN)
-    for (int i = 0; i < a.stages; ++i) {
-      clear_row<T, U>(ring + i * stage, true, dim);
-      clear_row<T, U>(ring + i * stage + array, true, dim);
-      clear_row<T, U>(ring + i * stage + 2 * array, os != nullptr, dim);
-      clear_row<T, U>(ring + i * stage + 3 * array, hs != nullptr, dim);
-    }
+  const auto clear = [&] {
+    if (OWN)
+      for (int i = 0; i < a.stages; ++i) {
+        clear_row<T, U>(ring + i * stage, true, dim);
+        clear_row<T, U>(ring + i * stage + array, true, dim);
+        clear_row<T, U>(ring + i * stage + 2 * array, os != nullptr, dim);
+        clear_row<T, U>(ring + i * stage + 3 * array, hs != nullptr, dim);
+      }
+  };
   NormResSpan s = {-1, 0, 0};
   bool any = false;
   int turn = 0;
@@ -435,14 +439,22 @@ __global__ void __launch_bounds__(T0, T0 == 512 ? 1 : T0 == 128 ? (OWN ? 4 : 3) 
       fill = fill + 1 == a.stages ? 0 : fill + 1;
     };
     if (!OWN) __syncthreads();   // the last span's rows have been read
+    // (the vectors' loads and the first rows' copies are under way together)
+    const float2* roots = reinterpret_cast<const float2*>(a.rstd);
+    float2 root = roots[s.first];
+    f32x2 g1[P], ga[P];
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      g1[p] = vector_at<T, OWN, T0>(a.g1 ? a.g1 + my.c0 : nullptr, dim, 1.0f, 2 * p);
+      ga[p] = vector_at<T, OWN, T0>(gate, dim, 1.0f, 2 * p);
+    }
     for (int i = 0; i < a.stages - 1; ++i) ahead(s.first + i);
+    if (!any) clear();
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       sp[p] = both(0.0f);
-      w[p] = mul2(vector_at<T, OWN>(a.g1 ? a.g1 + my.c0 : nullptr, dim, 1.0f, 2 * p), vector_at<T, OWN>(gate, dim, 1.0f, 2 * p));
+      w[p] = mul2(g1[p], ga[p]);
     }
-    const float2* roots = reinterpret_cast<const float2*>(a.rstd);
-    float2 root = roots[s.first];
     for (int r = s.first; r < s.end; ++r) {
       const size_t at = (size_t)r * a.dim + my.c0;
       const float r1 = a.g1 ? root.x : 1.0f, r2 = hs ? root.y : 1.0f;
@@ -463,10 +475,10 @@ __global__ void __launch_bounds__(T0, T0 == 512 ? 1 : T0 == 128 ? (OWN ? 4 : 3) 
         const T* hr = hs ? span_at<T>(in + 3 * array, at) : nullptr;
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-          dy[OWN ? 0 : p] = pair_at(yr, dim, 2 * p);
-          dx[OWN ? 0 : p] = pair_at(xr, dim, 2 * p);
-          dq[OWN ? 0 : p] = pair_at(qr, dim, 2 * p);
-          dh[OWN ? 0 : p] = pair_at(hr, dim, 2 * p);
+          dy[OWN ? 0 : p] = pair_at<T0>(yr, dim, 2 * p);
+          dx[OWN ? 0 : p] = pair_at<T0>(xr, dim, 2 * p);
+          dq[OWN ? 0 : p] = pair_at<T0>(qr, dim, 2 * p);
+          dh[OWN ? 0 : p] = pair_at<T0>(hr, dim, 2 * p);
         }
       }
       if (r + 1 < s.end) root = roots[r + 1];
@@ -522,15 +534,15 @@ __global__ void __launch_bounds__(T0, T0 == 512 ? 1 : T0 == 128 ? (OWN ? 4 : 3) 
           y[i] = fma2(rr1, mul2(wp, t), mul2(y[i], n2));
         }
         if (OWN) {
-          const int c = column<T, OWN>(j * per);
+          const int c = column<T, OWN, T0>(j * per);
           if (c >= dim) continue;
           *reinterpret_cast<uint4*>(static_cast<T*>(a.dy) + at + c) = narrow(y);
           *reinterpret_cast<uint4*>(static_cast<T*>(a.dx) + at + c) = narrow(x);
         } else {
 #pragma unroll
           for (int i = 0; i < pairs; ++i) {
-            store_pair(static_cast<T*>(a.dy) + at, dim, (j * pairs + i) * 2, y[i]);
-            store_pair(static_cast<T*>(a.dx) + at, dim, (j * pairs + i) * 2, x[i]);
+            store_pair<T0>(static_cast<T*>(a.dy) + at, dim, (j * pairs + i) * 2, y[i]);
+            store_pair<T0>(static_cast<T*>(a.dx) + at, dim, (j * pairs + i) * 2, x[i]);
           }
         }
       }
@@ -539,7 +551,7 @@ __global__ void __launch_bounds__(T0, T0 == 512 ? 1 : T0 == 128 ? (OWN ? 4 : 3) 
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const float2 f = parts(sp[p]);
-      const int c = column<T, OWN>(2 * p), d = column<T, OWN>(2 * p + 1);
+      const int c = column<T, OWN, T0>(2 * p), d = column<T, OWN, T0>(2 * p + 1);
       if (c < dim) span_sums(a, my.block, s, !any, my.c0 + c, f.x);
       if (d < dim) span_sums(a, my.block, s, !any, my.c0 + d, f.y);
     }
@@ -549,7 +561,7 @@ __global__ void __launch_bounds__(T0, T0 == 512 ? 1 : T0 == 128 ? (OWN ? 4 : 3) 
 #pragma unroll
   for (int p = 0; p < P; ++p) {
     const float2 f = parts(s2[p]);
-    const int c = column<T, OWN>(2 * p), d = column<T, OWN>(2 * p + 1);
+    const int c = column<T, OWN, T0>(2 * p), d = column<T, OWN, T0>(2 * p + 1);
     if (c < dim) keep[a.dim + c] = f.x;
     if (d < dim) keep[a.dim + d] = f.y;
   }
@@ -715,9 +727,12 @@ struct NormResShape {
 constexpr size_t kNrSmem = 220 * 1024;
 constexpr int kNrMost = 512;
 // A warp of eight elements a lane for the narrowest rows, else sixteen elements a
-// thread; a cluster of blocks where a row is more than the threads of one hold, or two
-// rows of it more than shared memory does.
-NormResShape norm_res_shape(int dtype, int dim, bool grad) {
+// thread, which take fewer exchanges (32768 x 1024 bf16 backward: 76 us against 80), but
+// eight up to 1024 where that leaves fewer threads without elements (16384 x 600 fp32:
+// 52 us against 57) or where blocks have few rows each and their start counts (2000 x 1000
+// bf16: 16.1 us against 18.6).  A cluster of blocks where a row is more than the threads
+// of one hold, or two rows of it more than shared memory does.
+NormResShape norm_res_shape(int dtype, int rows, int dim, bool grad) {
   NormResShape s;
   const int es = dtype ? 2 : 4, per = 16 / es;
   s.own = (size_t)dim * es % 16 == 0;
@@ -726,7 +741,16 @@ NormResShape norm_res_shape(int dtype, int dim, bool grad) {
     if (s.own) s.part = (s.part + per - 1) / per * per;
     // (forward: 32 elements a thread before two blocks, which cost a row two exchanges)
     s.each = s.part <= 256 ? 8 : s.part <= 16 * 512 || grad ? 16 : 32;
-    const int threads = ((s.part + s.each - 1) / s.each + 31) / 32 * 32;
+    int threads = ((s.part + s.each - 1) / s.each + 31) / 32 * 32;
+    if (s.own && s.each == 16 && s.part <= 1024) {
+      const int eight = ((s.part + 7) / 8 + 31) / 32 * 32;
+      if (20 * eight < 17 * 2 * threads || rows < 8 * device_sms() * 512 / threads) {
+        s.each = 8;
+        threads = eight;
+      }
+    }
+    if (!s.own && s.each > 8)   // (compiled for powers of two)
+      for (threads = 64; threads * s.each < s.part;) threads *= 2;
     if (threads > kNrMost) continue;
     s.row_units = s.own ? s.each * es * threads / 16 : (s.part * es + 15) / 16 + 1;
     const size_t row = (size_t)(grad ? 4 : 2) * s.row_units * 16;
@@ -742,7 +766,7 @@ NormResShape norm_res_shape(int dtype, int dim, bool grad) {
 // Rows that are worked on at once: by registers (128 a thread; 80 in the narrowest) and by shared memory.
 int norm_res_slots(const NormResShape& s, bool grad) {
   if (!s.threads) return device_sms() * 4;
-  int n = s.threads == 32 && s.each == 8 ? (grad && !s.own ? 16 : 24) : 512 * (grad && !s.own ? 3 : 4) / 4 / s.threads;
+  int n = s.each == 8 ? (grad && !s.own ? 512 : 768) / s.threads : (grad && !s.own && s.threads < 256 ? 384 : 512) / s.threads;
   n = std::max(1, std::min(n, (int)(kNrSmem / (s.smem + 2048))));
   return std::max(1, device_sms() * n / s.ranks);
 }
@@ -764,6 +788,18 @@ NormResSplit norm_res_split(int rows, int gates, int slots) {
   p.block_gates = p.parts > 1 ? 1 : std::max(1, gates / (4 * slots));
   p.blocks = p.parts > 1 ? (long long)gates * p.parts : (gates + p.block_gates - 1) / p.block_gates;
   return p;
+}
+
+// At least the blocks of any split of these rows or fewer: one round of them, or (the
+// split's four rounds, rounded up twice) eight.
+long long norm_res_most_blocks(int rows, int dim, int gates) {
+  long long most = 1;
+  for (int dtype = 0; dtype < 2; ++dtype)
+    for (int r : {1, rows}) {
+      const int slots = norm_res_slots(norm_res_shape(dtype, r, dim, true), true);
+      most = std::max(most, slots / gates >= 4 ? (long long)slots : 8ll * slots);
+    }
+  return std::min<long long>(most, std::max(rows, 1));
 }
 
 template <typename K, typename A>
@@ -790,17 +826,23 @@ cudaError_t norm_res_launch(K kernel, const A& a, long long blocks, int threads,
 template <typename T, bool OWN>
 cudaError_t norm_res_forward(const NormResArgs& a, const NormResShape& s, long long blocks, cudaStream_t st) {
   constexpr int W = sizeof(T) == 4 ? 2 : 1;   // units of eight elements
-  if (s.each == 8) return norm_res_launch(norm_res_kernel<T, W, OWN, 32>, a, blocks, s.threads, s.smem, st, s.ranks);
-  if (s.threads <= 128) return norm_res_launch(norm_res_kernel<T, 2 * W, OWN, 128>, a, blocks, s.threads, s.smem, st, s.ranks);
-  if (s.each == 16) return norm_res_launch(norm_res_kernel<T, 2 * W, OWN, 512>, a, blocks, s.threads, s.smem, st, s.ranks);
-  return norm_res_launch(norm_res_kernel<T, 4 * W, OWN, 512>, a, blocks, s.threads, s.smem, st, s.ranks);
+  const auto go = [&](auto kernel) { return norm_res_launch(kernel, a, blocks, s.threads, s.smem, st, s.ranks); };
+  if (s.each == 8) return s.threads == 32 ? go(norm_res_kernel<T, W, OWN, 32>) : go(norm_res_kernel<T, W, OWN, 128>);
+  if (s.each == 32) return go(norm_res_kernel<T, 4 * W, OWN, 512>);
+  if (!OWN && s.threads <= 64) return go(norm_res_kernel<T, 2 * W, OWN, OWN ? 128 : 64>);
+  if (s.threads <= 128) return go(norm_res_kernel<T, 2 * W, OWN, 128>);
+  if (!OWN && s.threads <= 256) return go(norm_res_kernel<T, 2 * W, OWN, OWN ? 512 : 256>);
+  return go(norm_res_kernel<T, 2 * W, OWN, 512>);
 }
 template <typename T, bool OWN>
 cudaError_t norm_res_backward(const NormResGradArgs& a, const NormResShape& s, long long blocks, cudaStream_t st) {
   constexpr int W = sizeof(T) == 4 ? 2 : 1;
-  if (s.each == 8) return norm_res_launch(norm_res_grad_kernel<T, W, OWN, 32>, a, blocks, s.threads, s.smem, st, s.ranks);
-  if (s.threads <= 128) return norm_res_launch(norm_res_grad_kernel<T, 2 * W, OWN, 128>, a, blocks, s.threads, s.smem, st, s.ranks);
-  return norm_res_launch(norm_res_grad_kernel<T, 2 * W, OWN, 512>, a, blocks, s.threads, s.smem, st, s.ranks);
+  const auto go = [&](auto kernel) { return norm_res_launch(kernel, a, blocks, s.threads, s.smem, st, s.ranks); };
+  if (s.each == 8) return s.threads == 32 ? go(norm_res_grad_kernel<T, W, OWN, 32>) : go(norm_res_grad_kernel<T, W, OWN, 128>);
+  if (!OWN && s.threads <= 64) return go(norm_res_grad_kernel<T, 2 * W, OWN, OWN ? 128 : 64>);
+  if (s.threads <= 128) return go(norm_res_grad_kernel<T, 2 * W, OWN, 128>);
+  if (!OWN && s.threads <= 256) return go(norm_res_grad_kernel<T, 2 * W, OWN, OWN ? 512 : 256>);
+  return go(norm_res_grad_kernel<T, 2 * W, OWN, 512>);
 }
 
 }  // namespace
@@ -820,13 +862,7 @@ static mg_status check_norm_res(const char* fn, int dtype, int rows, int dim, co
 
 extern "C" size_t mg_norm_residual_workspace_bytes(int rows, int dim, int gates) {
   if (rows < 0 || rows > mg::kMaxWidth || dim < 1 || dim > mg::kMaxWidth || gates < 0 || (gates && rows % gates)) return 0;
-  // (of either type: the largest)
-  long long blocks = 1;
-  for (int dtype = 0; rows && dtype < 2; ++dtype) {
-    const mg::NormResShape s = mg::norm_res_shape(dtype, dim, true);
-    blocks = std::max(blocks, mg::norm_res_split(rows, gates ? gates : 1, mg::norm_res_slots(s, true)).blocks);
-  }
-  return ((size_t)blocks * 2 * dim + 4) * sizeof(float);
+  return ((size_t)mg::norm_res_most_blocks(rows, dim, gates ? gates : 1) * 2 * dim + 4) * sizeof(float);
 }
 
 extern "C" mg_status mg_norm_residual_forward(int dtype, const void* y, const void* x, int rows, int dim,
@@ -846,7 +882,7 @@ extern "C" mg_status mg_norm_residual_forward(int dtype, const void* y, const vo
                             {gamma_pre, v, false, false}, {x_out, n, true, x_out == y || x_out == x},
                             {h, n, true, h == y || h == x}, {rstd, (size_t)rows * 8, true, false}});
   if (st != MG_OK || !rows) return st;
-  const mg::NormResShape shape = mg::norm_res_shape(dtype, dim, false);
+  const mg::NormResShape shape = mg::norm_res_shape(dtype, rows, dim, false);
   mg::NormResArgs a = {y, x, gamma_post, gate, gamma_pre, rows, dim, gates ? rows / gates : rows, scale, eps, x_out, h, rstd, 1, shape.stages, shape.row_units,
                        shape.ranks, shape.part};
   cudaStream_t s = (cudaStream_t)stream;
@@ -901,7 +937,7 @@ extern "C" mg_status mg_norm_residual_backward(int dtype, const void* dx_out, co
     return mg::op_end(fn, mg::norm_res_launch(mg::norm_res_zero_kernel, a, blocks, 256, 0, s));
   }
   a.gate_rows = rows / a.gates;
-  const mg::NormResShape shape = mg::norm_res_shape(dtype, dim, true);
+  const mg::NormResShape shape = mg::norm_res_shape(dtype, rows, dim, true);
   const mg::NormResSplit split = mg::norm_res_split(rows, a.gates, mg::norm_res_slots(shape, true));
   a.stages = shape.stages;
   a.row_units = shape.row_units;

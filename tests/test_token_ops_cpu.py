@@ -94,6 +94,13 @@ def test_norm_residual_workspace(lib):
     assert binding.norm_residual_workspace_bytes(16384, 2048, 1) == f(16384, 2048, 1) > 0
 
 
+@pytest.mark.parametrize("dim,gates", [(64, 1), (777, 7), (1000, 0), (2048, 1), (2048, 300), (8192, 4), (16384, 2), (70001, 1)])
+def test_a_workspace_serves_fewer_rows(lib, dim, gates):
+    g = max(1, gates)
+    sizes = [lib.mg_norm_residual_workspace_bytes(r * g, dim, gates) for r in (0, 1, 2, 7, 8, 9, 100, 431, 5000, 40000, 200000)]
+    assert sizes == sorted(sizes) and sizes[0] > 0
+
+
 def _tensor(**kw):
     t = dict(param=P, grad=2 * P, m=3 * P, v=4 * P, m_scales=None, v_scales=None, copy=None, count=4, param_dtype=0,
              grad_dtype=0, weight_decay=0.0) | kw
