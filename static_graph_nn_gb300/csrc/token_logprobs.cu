@@ -613,14 +613,18 @@ __global__ void __launch_bounds__(256) logp_grad_kernel(LogpGradArgs a, int rank
 }
 
 // Many rows: 128 threads each, so that a row's sums are joined by few warps, or one
-// warp for the shortest without alternatives.  Few rows: 512 threads, and as many blocks to a row, up to
-// eight, as fill the multiprocessors while a thread still has two units.
+// warp for the shortest without alternatives (4096 x 1000 bf16: 9.0 us against 11.6; with
+// 20 alternatives 26 against 22).  Four blocks to a multiprocessor keep the memory
+// busy, fewer are enough for rows of up to 64 KB (450 x 32000 bf16, 20 alternatives: 11.1
+// us against 14.1 with 512 threads; 450 x 131072 fp32: 61 against 49).  Few rows: 512
+// threads, and as many blocks to a row, up to eight, as fill the multiprocessors while a
+// thread still has two units (32 x 32000 bf16, 20 alternatives: four blocks 7.4 us, eight 11.5).
 template <typename T>
 cudaError_t logp_forward(const LogpArgs& a, int rows, cudaStream_t s) {
   const int sms = device_sms();
   const int units = (int)((long long)a.vocab * (int)sizeof(T) / 16);
   int threads = units < kLogpShort && !a.k ? 32 : 128, ranks = 1;
-  if (rows < 4 * sms) {
+  if (rows < sms || (rows < 4 * sms && units > 4096)) {
     threads = units < kLogpShort ? 128 : 512;
     while (ranks < kMaxCluster && 2 * ranks * rows <= 2 * sms && units >= 4 * ranks * threads) ranks *= 2;
   }
@@ -663,8 +667,8 @@ static mg_status check_logits(const char* fn, int dtype, int id_kind, long long 
     return op_fail(MG_ERR_INVALID_ARG, "%s: dtype and id_kind must be 0 or 1", fn);
   if (rows < 0 || rows > 0x7fffffff || vocab < 1 || vocab > mg::kMaxWidth || stride < vocab || stride > (1ll << 31))
     return op_fail(MG_ERR_SHAPE, "%s: rows %lld, vocab %d, row stride %lld", fn, rows, vocab, stride);
-  if (!(temperature > 0.0f) || !std::isfinite(temperature) || !std::isfinite(1.0f / temperature))
-    return op_fail(MG_ERR_INVALID_ARG, "%s: the temperature and its reciprocal must be positive and finite", fn);
+  if (!(temperature > 0.0f) || !std::isfinite(temperature) || !std::isfinite(mg::kLog2e * (1.0f / temperature)))
+    return op_fail(MG_ERR_INVALID_ARG, "%s: the temperature must be positive and finite, log2(e) over it finite", fn);
   return MG_OK;
 }
 

@@ -27,7 +27,7 @@ def _logp(lib, t=0, x=P, rows=4, v=10, ld=10, kind=0, ids=P, temp=1.0, logp=P, s
 @pytest.mark.parametrize("kw,want", [
     (dict(t=2), E), (dict(kind=2), E), (dict(rows=-1), S), (dict(rows=2**31), S), (dict(v=0), S), (dict(v=2**30 + 1, ld=2**31), S),
     (dict(ld=9), S), (dict(ld=2**31 + 1), S), (dict(temp=0.0), E), (dict(temp=-1.0), E), (dict(temp=NAN), E),
-    (dict(temp=INF), E), (dict(temp=1e-45), E), (dict(k=-1), S), (dict(k=11), S), (dict(v=100, ld=100, k=33), S),
+    (dict(temp=INF), E), (dict(temp=1e-45), E), (dict(temp=3.5e-39), E), (dict(k=-1), S), (dict(k=11), S), (dict(v=100, ld=100, k=33), S),
     (dict(x=None), E), (dict(ids=None), E), (dict(logp=None), E), (dict(ti=None), E), (dict(tl=None), E),
     (dict(ids=None, logp=None, stats=None, ent=None, k=0), E), (dict(x=P + 2), A), (dict(t=1, x=P + 1), A),
     (dict(ids=P + 2), A), (dict(ids=P + 4, kind=1), A), (dict(logp=P + 2), A), (dict(stats=P + 4), A),
