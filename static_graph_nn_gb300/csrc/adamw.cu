@@ -23,6 +23,15 @@
 // would be divided by eps).  The update itself uses the moments before they are
 // rounded.  Moments are computed one fp32 rounding an operation, so that a
 // host that does the same finds the same codes.
+//
+// Bound by DRAM: 28 bytes an fp32 element, 16 with 8-bit moments, 2 more for a bf16 copy.
+// 334M elements with a copy: 1435 us (7.0 TB/s), with 8-bit moments 861 us (7.0 TB/s).
+// With bf16 parameters and gradients, 10 bytes, by issue: 65 instructions an element (24M
+// in 400 tensors: 57 us, 4.2 TB/s); most arithmetic is done on two elements at once.
+// Blocks of 8-bit moments are copied ahead through shared memory: a warp's loads
+// are under way while it computes (861 us against 1201).  In them a lane takes
+// twice four neighbours, so that every access of a warp is contiguous; eight
+// neighbours are two half used accesses of each sector (1091 us).
 #include <algorithm>
 #include <cmath>
 #include <exception>
@@ -472,7 +481,7 @@ __device__ __forceinline__ void adamw_block(const AdamwStep& a, const AdamwScala
 }
 
 // ---- 8-bit moments: whole blocks through shared memory, copied ahead
-constexpr int kAdamwStages = 2;
+constexpr int kAdamwStages = 2;          // (three, with room for three blocks: 855 us, but 61 against 57 for the bf16 list)
 constexpr int kAdamwStageBytes = 2560;   // p, g: 1024 each; m, v: 256 each
 constexpr int kAdamwSmem = kAdamwThreads / 32 * kAdamwStages * kAdamwStageBytes;
 
