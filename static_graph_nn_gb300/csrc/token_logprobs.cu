@@ -18,10 +18,10 @@
 // listed, and the list is ranked.  Where equal values make the list too long, the
 // smaller ones are left out and found in order of their places.
 //
-// Bound by DRAM, with 70 % of the issue slots: nine instructions an element, five of
-// them the exponential and the sums.  16384 x 32000 bf16 with a tenth of padding: 152 us
-// (6.2 TB/s); its gradient 300 us (6.65 TB/s); without padding 164 us, with 5 alternatives
-// 195, with 32 230.  1037 x 50021 fp32, 5 alternatives: 39 us (5.1 TB/s; all rows at once, so their ends meet).
+// Bound by DRAM: 16384 x 32000 bf16 with a tenth of padding 144 us (6.5 TB/s; with one
+// chunk of four units on its way to a thread instead of two 152), its gradient 300 us
+// (6.65 TB/s); without padding 155 us, with 5 alternatives 186, with 32 226.  1037 x 50021
+// fp32, 5 alternatives: 37.5 us (5.3 TB/s; all rows at once, so their ends meet).
 #include <cmath>
 
 #include "common.cuh"
@@ -215,18 +215,16 @@ __device__ __forceinline__ void fetch_chunk(const Part<T>& p, int u0, uint4 (&u)
   for (int i = 0; i < 4; ++i)
     u[i] = u0 + i * step < p.units ? *p.unit(u0 + i * step) : make_uint4(kNone, kNone, kNone, kNone);
 }
-// A thread's sums; next: its first chunk.
+// A thread's sums; one: its first chunk.
 template <typename T>
-__device__ __forceinline__ RowSums row_sums(const Part<T>& p, float c, uint4 (&next)[4], RowBest& best) {
+__device__ __forceinline__ RowSums row_sums(const Part<T>& p, float c, uint4 (&one)[4], RowBest& best) {
   constexpr int pairs = Part<T>::kPer / 2;
   RowSums r = {-INFINITY, 0.0f, 0.0f};
   best = {-1, -INFINITY};
   const int step = blockDim.x;
   const f32x2 cc = both(c);
   int chunk = 0;
-  for (int u0 = threadIdx.x; u0 < p.units; u0 += 4 * step, ++chunk) {
-    uint4 u[4] = {next[0], next[1], next[2], next[3]};
-    fetch_chunk(p, u0 + 4 * step, next);   // in flight while these are added
+  const auto add = [&](const uint4 (&u)[4]) {
     const float top = units_max(u, T());
     best.others = fmaxf(best.others, fminf(top, r.m));
     if (top > r.m) {
@@ -251,6 +249,17 @@ __device__ __forceinline__ RowSums row_sums(const Part<T>& p, float c, uint4 (&n
     const float2 ss = parts(s), qq = parts(q);
     r.s += ss.x + ss.y;
     r.q += qq.x + qq.y;
+    ++chunk;
+  };
+  // two chunks on their way at any time
+  uint4 two[4];
+  fetch_chunk(p, threadIdx.x + 4 * step, two);
+  for (int u0 = threadIdx.x; u0 < p.units; u0 += 8 * step) {
+    add(one);
+    fetch_chunk(p, u0 + 8 * step, one);
+    if (u0 + 4 * step >= p.units) break;
+    add(two);
+    fetch_chunk(p, u0 + 12 * step, two);
   }
   const auto single = [&](float x) {
     if (x > r.m) {
