@@ -513,6 +513,7 @@ mg_status mg_norm_residual_backward(int dtype, const void* dx_out, const void* d
  *   g' = c grad;  m = beta1 m + (1 - beta1) g';  v = beta2 v + (1 - beta2) g'^2
  *   param = param (1 - lr weight_decay)
  *           - lr / (1 - beta1^step) m / (sqrt(v / (1 - beta2^step)) + eps)
+ * (betas in [0, 1), eps a normal fp32 number.)
  * c = max_norm / norm[0] if norm[0] > max_norm, else 1; norm (device memory, may
  * be NULL: c = 1) is what mg_grad_list_clip with max_norm = INFINITY measures.
  * Where norm[0] is not finite the step changes nothing.

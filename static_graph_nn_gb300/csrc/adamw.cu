@@ -330,7 +330,8 @@ __device__ __forceinline__ uint32_t block_top(const f32x2 (&f)[4]) {
   return __reduce_max_sync(0xffffffffu, __float_as_uint(top));
 }
 // Square roots, rounded: an estimate and one step of Newton's method on it, whose
-// residual is exact.  For values that are normal numbers or 0 (smaller ones: too small).
+// residual is exact.  For values that are normal numbers or 0 (of smaller ones the root
+// comes out too small).
 __device__ __forceinline__ void roots8(f32x2 (&v)[4]) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -418,7 +419,7 @@ __device__ __forceinline__ void adamw_finish(const AdamwStep& a, const AdamwScal
   const uint32_t tm = BITS == 8 ? block_top(m) : 0, tv = BITS == 8 ? block_top(v) : 0;
   const float sm = scale_of(tm), sv = scale_of(__float_as_uint(sqrtf(__uint_as_float(tv))));
   // (a root of a moment below the normal range is then far below eps, and its code the least)
-  if (BITS == 8 && sv >= 0x1p-30f && sv <= 0x1p60f && a.eps >= 1e-10f) {
+  if (BITS == 8 && sv >= 0x1p-30f && sv <= 0x1p60f && a.eps >= 1e-9f) {
     roots8(v);
   } else {
 #pragma unroll
@@ -606,8 +607,8 @@ extern "C" mg_status mg_adamw_create(int n, const mg_adamw_tensor* tensors, int 
   *out = nullptr;
   if (n < 1 || !tensors) return op_fail(MG_ERR_INVALID_ARG, "%s: n must be positive and tensors non-NULL", fn);
   if (state_bits != 8 && state_bits != 32) return op_fail(MG_ERR_INVALID_ARG, "%s: state_bits must be 8 or 32", fn);
-  if (!(beta1 >= 0.0 && (float)beta1 < 1.0f && beta2 >= 0.0 && (float)beta2 < 1.0f) || !((float)eps > 0.0f) || !std::isfinite(eps))
-    return op_fail(MG_ERR_INVALID_ARG, "%s: betas must lie in [0, 1) and eps be positive", fn);
+  if (!(beta1 >= 0.0 && (float)beta1 < 1.0f && beta2 >= 0.0 && (float)beta2 < 1.0f) || !((float)eps >= 0x1p-126f) || !std::isfinite((float)eps))
+    return op_fail(MG_ERR_INVALID_ARG, "%s: betas must lie in [0, 1) and eps be a positive normal fp32 number", fn);
   try {
     struct Span {
       uintptr_t lo, hi;

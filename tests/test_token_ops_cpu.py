@@ -133,7 +133,7 @@ def test_adamw_tensor_refusals(lib, kw, want):
 def test_adamw_refusals(lib):
     assert _adamw(lib, []) == E
     for kw in (dict(bits=16), dict(b1=1.0), dict(b1=-0.1), dict(b2=1.0), dict(b2=NAN), dict(b1=1.0 - 1e-9), dict(eps=0.0),
-               dict(eps=-1.0), dict(eps=1e-60), dict(eps=INF)):
+               dict(eps=-1.0), dict(eps=1e-60), dict(eps=1e-39), dict(eps=1e39), dict(eps=INF)):
         assert _adamw(lib, [_tensor()], **kw) == E
     assert _adamw(lib, [_tensor()], bits=8) == E            # no scales
     assert lib.mg_adamw_create(1, None, 32, 0.9, 0.999, 1e-8, 0, ctypes.byref(ctypes.c_void_p())) == E
