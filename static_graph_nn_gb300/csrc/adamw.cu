@@ -221,7 +221,7 @@ __device__ __forceinline__ void store8(void* p, bool narrow, int i0, int len, co
       st8f32(static_cast<float*>(p) + i0, f);
     return;
   }
-  if (L == PAIR) {
+  if constexpr (L == PAIR) {
     if (narrow) {
       const uint4 u = pack8(f);
       *reinterpret_cast<uint2*>(static_cast<bf16*>(p) + i0) = make_uint2(u.x, u.y);
@@ -230,16 +230,16 @@ __device__ __forceinline__ void store8(void* p, bool narrow, int i0, int len, co
       *reinterpret_cast<float4*>(static_cast<float*>(p) + i0) = make_float4(f[0], f[1], f[2], f[3]);
       *reinterpret_cast<float4*>(static_cast<float*>(p) + i0 + 128) = make_float4(f[4], f[5], f[6], f[7]);
     }
-    return;
-  }
+  } else {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int i = element<L>(i0, j);
-    if (i >= len) continue;
-    if (narrow)
-      st_elem(static_cast<bf16*>(p), i, f[j]);
-    else
-      st_elem(static_cast<float*>(p), i, f[j]);
+    for (int j = 0; j < 8; ++j) {
+      const int i = element<L>(i0, j);
+      if (i >= len) continue;
+      if (narrow)
+        st_elem(static_cast<bf16*>(p), i, f[j]);
+      else
+        st_elem(static_cast<float*>(p), i, f[j]);
+    }
   }
 }
 // Eight codes in two words.
@@ -260,16 +260,16 @@ __device__ __forceinline__ void store_codes(uint8_t* p, int i0, int len, uint2 c
     *reinterpret_cast<uint2*>(p + i0) = c;
     return;
   }
-  if (L == PAIR) {
+  if constexpr (L == PAIR) {
     *reinterpret_cast<uint32_t*>(p + i0) = c.x;
     *reinterpret_cast<uint32_t*>(p + i0 + 128) = c.y;
-    return;
-  }
-  const uint32_t w[2] = {c.x, c.y};
+  } else {
+    const uint32_t w[2] = {c.x, c.y};
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int i = element<L>(i0, j);
-    if (i < len) p[i] = (uint8_t)(w[j / 4] >> (8 * (j % 4)));
+    for (int j = 0; j < 8; ++j) {
+      const int i = element<L>(i0, j);
+      if (i < len) p[i] = (uint8_t)(w[j / 4] >> (8 * (j % 4)));
+    }
   }
 }
 // The moments and the root, eight elements of a lane.  Products with a scale, a
