@@ -187,6 +187,29 @@ def test_parts_left_out(dim, gates, pre, post, t):
     _backward_check(i, out[2], -1.25, _backward(i, out[2], -1.25), t)
 
 
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,dim,gates", [(60000, 64, 60000), (60000, 64, 30000), (50001, 50, 50001), (12000, 1024, 12000),
+                                            (9000, 777, 9000), (5000, 16384, 5000), (30000, 40, 15000)])
+def test_many_gates(rows, dim, gates, t):
+    """More gates than blocks: a block has several whole gates."""
+    i = _inputs(rows, dim, t, gates, True, True, gates)
+    out = _forward(i, 0.7)
+    _forward_check(i, 0.7, out, t)
+    o = _backward(i, out[2], 0.7)
+    _backward_check(i, out[2], 0.7, o, t)
+    again = _backward(i, out[2], 0.7)
+    assert all(torch.equal(o[k], again[k]) for k in o)
+
+
+def test_a_workspace_for_more_rows_serves_fewer():
+    ws = torch.full((mg.norm_residual_workspace_bytes(9000, 520, 3),), 255, dtype=torch.uint8, device="cuda")
+    for rows in (9000, 2001, 30, 3):
+        for t in ("f32", "bf16"):
+            i = _inputs(rows, 520, t, 3, True, True, rows)
+            out = _forward(i, 1.1)
+            _backward_check(i, out[2], 1.1, _backward(i, out[2], 1.1, ws=ws), t)
+
+
 def test_against_differences():
     """Central differences of the definition in 64 bits (step 1e-5: truncation below 1e-8 of third derivatives under
     100, rounding 1e-10) beside the kernel's own bound; rstd is the forward's, within its bound of the exact one, and

@@ -292,6 +292,49 @@ def test_alternatives_among_equals(vocab, k, t):
     _check(x, None, o, k)
 
 
+def test_large_vocabularies():
+    """Rows of millions of logits, by one cluster each and by one block each."""
+    for rows, vocab, t in ((3, 5_000_001, "bf16"), (2, 1 << 22, "f32"), (700, 300_007, "bf16")):
+        x = _logits(rows, vocab, t, vocab)
+        ids = _ids(rows, vocab, 4, torch.int64)
+        ids[0] = vocab - 1
+        o = _forward(x, ids, 32, 0.9)
+        at = [0, 1, rows - 1]
+        _check(x[at], ids[at], {n: v[at] for n, v in o.items()}, 32, 0.9)
+        if rows < 10:
+            _gradient(x, ids, o, t, 0.9)
+        del x, o
+
+
+def test_ids_beyond_32_bits_are_padding():
+    x = _logits(6, 100, "f32", 50)
+    ids = torch.tensor([2 ** 32 + 5, -2 ** 32 + 5, 2 ** 31, -1, 100, 5], device="cuda")
+    o = _forward(x, ids, 3)
+    assert (o["logp"][:5] == 0).all() and (o["top_ids"][:5] == -1).all() and float(o["logp"][5]) < 0
+    dx = torch.full_like(x, 7.0)
+    mg.token_logprobs_backward(x, ids, o["stats"], torch.ones(6, device="cuda"), dx)
+    assert (dx[:5] == 0).all() and (dx[5] != 0).any()
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+@pytest.mark.parametrize("temp", [1e-3, 1e3])
+def test_far_temperatures(temp, t):
+    x = _logits(40, 3001, t, 51)
+    x[::3, ::2] = -INF
+    ids = _ids(40, 3001, 52, pad=True)
+    o = _forward(x, ids, 10, temp)
+    _check(x, ids, o, 10, temp)
+    _gradient(x, ids, o, t, temp)
+
+
+def test_gradient_of_the_entropy_alone_keeps_the_padding():
+    x = _logits(9, 500, "bf16", 53)
+    ids = _ids(9, 500, 54)
+    ids[3] = -1
+    o = _forward(x, ids, 0)
+    _gradient(x, ids, o, "bf16", 1.0, which="entropy")
+
+
 def test_empty_and_outputs_left_out():
     x = _logits(6, 100, "f32", 20)
     ids = _ids(6, 100, 21)
