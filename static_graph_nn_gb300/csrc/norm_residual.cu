@@ -49,7 +49,7 @@ struct NormResArgs {
   float* rstd;
   int block_rows;             // consecutive rows of a block
   int stages;                 // rows in shared memory at once
-  int row_units;              // 16-byte units of a row there, at any offset
+  int row_units;              // 16-byte units of a row there
   int ranks, part;            // blocks that share a row, columns of each
 };
 
@@ -81,24 +81,28 @@ struct NormResGradArgs {
 // Where rows begin on 16 bytes (OWN) a thread holds U such units of each row, a
 // block's width apart, and copies those itself, so that it waits for nothing but its
 // own copies; units beyond the row, and rows that are not given, are zeros from the
-// start.  Else it holds as many single elements, a block's width apart, of rows that
-// lie at any offset in what all threads copied together, and a barrier a row.  The
-// arithmetic takes two elements at a time.
+// start.  Else all threads copy the 16-byte units that a row touches, with zeros for the
+// bytes behind it, and after a barrier a thread takes words of four bytes, a warp's
+// width apart.  bf16 rows that begin within a word have theirs shifted out of two, and
+// stored with the lane before's half.  (14124 x 2124 bf16: forward 61 us, backward 113; by
+// single elements 92 and 196; by units of 16 bytes, shifted out of two, 2.4 times the
+// aligned rows' instructions and 193.)  The arithmetic takes two elements at a time.
 template <typename T>
 struct Unit {
   static constexpr int kPer = 16 / (int)sizeof(T);   // elements
   static constexpr int kPairs = kPer / 2;
 };
-// (OWN: a block's threads may be any number of warps up to T0; else they are T0)
-template <typename T, bool OWN, int T0>
+// The column of a thread's element e.
+template <typename T, bool OWN, int U>
 __device__ __forceinline__ int column(int e) {
-  constexpr int per = Unit<T>::kPer;
-  return OWN ? ((int)threadIdx.x + e / per * (int)blockDim.x) * per + e % per : (int)threadIdx.x + e * T0;
+  constexpr int per = OWN ? Unit<T>::kPer : Unit<T>::kPer / 4;
+  if (OWN) return ((int)threadIdx.x + e / per * (int)blockDim.x) * per + e % per;
+  return ((int)threadIdx.x / 32 * U * 128 + (int)threadIdx.x % 32) * per + e / per * 32 * per + e % per;
 }
 // The fp32 vector's values at columns e and e + 1 of this thread, `other` where there are none.
-template <typename T, bool OWN, int T0>
+template <typename T, bool OWN, int U>
 __device__ __forceinline__ f32x2 vector_at(const float* v, int dim, float other, int e) {
-  const int c = column<T, OWN, T0>(e), d = column<T, OWN, T0>(e + 1);
+  const int c = column<T, OWN, U>(e), d = column<T, OWN, U>(e + 1);
   if (OWN) {
     if (!v || c >= dim) return both(other);
     const float2 f = *reinterpret_cast<const float2*>(v + c);
@@ -123,18 +127,61 @@ __device__ __forceinline__ uint4 narrow(const f32x2 (&f)[2]) {
   const float2 a = parts(f[0]), b = parts(f[1]);
   return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
 }
-// Columns e and e + 1 of a row in shared memory, zeros beyond it.
-template <int T0, typename T>
-__device__ __forceinline__ f32x2 pair_at(const T* p, int dim, int e) {
-  const int c = column<T, false, T0>(e), d = column<T, false, T0>(e + 1);
-  return both(p && c < dim ? ld_elem(p, c) : 0.0f, p && d < dim ? ld_elem(p, d) : 0.0f);
+// N pairs of elements from e on of a row, which begins `at` bytes into its copy.
+template <typename T, int U, int N>
+__device__ __forceinline__ void pairs_at(const uint4* copy, int at, int e, f32x2* v) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(copy) + at / 4 + threadIdx.x / 32 * U * 128 + threadIdx.x % 32;
+  if (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      v[i] = both(__uint_as_float(w[(e + 2 * i) * 32]), __uint_as_float(w[(e + 2 * i + 1) * 32]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      uint32_t u = w[(e / 2 + i) * 32];
+      if (at & 2) u = __funnelshift_r(u, w[(e / 2 + i) * 32 + 1], 16);
+      v[i] = widen2(u);
+    }
+  }
 }
-template <int T0, typename T>
-__device__ __forceinline__ void store_pair(T* p, int dim, int e, f32x2 v) {
-  const int c = column<T, false, T0>(e), d = column<T, false, T0>(e + 1);
-  const float2 f = parts(v);
-  if (c < dim) st_elem(p, c, f.x);
-  if (d < dim) st_elem(p, d, f.y);
+// Writes them to the row; by whole warps.
+template <int U, int N>
+__device__ __forceinline__ void store_pairs(float* row, int, int dim, int e, const f32x2* v) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int c = column<float, false, U>(e + 2 * i), d = column<float, false, U>(e + 2 * i + 1);
+    const float2 f = parts(v[i]);
+    if (c < dim) row[c] = f.x;
+    if (d < dim) row[d] = f.y;
+  }
+}
+template <int U, int N>
+__device__ __forceinline__ void store_pairs(bf16* row, int at, int dim, int e, const f32x2* v) {
+  const int lane = threadIdx.x & 31;
+  if (at & 2) {   // words are the last lane's second element and this one's first
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = column<bf16, false, U>(e + 2 * i);
+      uint16_t* half = reinterpret_cast<uint16_t*>(row) + c;
+      const uint32_t w = narrow2(v[i]), last = __shfl_up_sync(~0u, w, 1);
+      if (lane > 0 && c < dim)
+        *reinterpret_cast<uint32_t*>(half - 1) = __funnelshift_r(last, w, 16);
+      else if (c < dim)
+        half[0] = (uint16_t)w;
+      if (c + 1 < dim && (lane == 31 || c + 2 >= dim)) half[1] = (uint16_t)(w >> 16);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = column<bf16, false, U>(e + 2 * i);
+      uint16_t* half = reinterpret_cast<uint16_t*>(row) + c;
+      const uint32_t w = narrow2(v[i]);
+      if (c + 1 < dim)
+        *reinterpret_cast<uint32_t*>(half) = w;
+      else if (c < dim)
+        half[0] = (uint16_t)w;
+    }
+  }
 }
 template <typename T, int U>
 __device__ __forceinline__ void copy_row(uint4* to, const T* p, int dim) {
@@ -149,21 +196,17 @@ __device__ __forceinline__ void copy_row(uint4* to, const T* p, int dim) {
   }
 }
 // The n elements of a matrix from element e on, with all of the 16-byte units that they
-// touch, by all threads; the last unit ends with the matrix (of `all` elements).
+// touch, by all threads; zeros for the bytes behind them, up to the end of the next unit.
 template <typename T>
-__device__ __forceinline__ void copy_span(uint4* to, const T* m, size_t e, int n, size_t all) {
-  const size_t begin = e * sizeof(T), first = begin / 16, last = (begin + n * sizeof(T) + 15) / 16;
-  for (size_t u = first + threadIdx.x; u < last; u += blockDim.x) {
-    const int size = (int)min((size_t)16, all * sizeof(T) - u * 16);
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to + (u - first))),
-                 "l"(reinterpret_cast<const char*>(m) + u * 16), "r"(size)
+__device__ __forceinline__ void copy_span(uint4* to, const T* m, size_t e, int n) {
+  const int begin = (int)(e * sizeof(T) % 16), end = begin + n * (int)sizeof(T);
+  const char* from = reinterpret_cast<const char*>(m + e) - begin;
+  for (int b = threadIdx.x * 16; b < end + 16; b += blockDim.x * 16) {
+    const int size = max(0, min(16, end - b));
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to) + b),
+                 "l"(size ? from + b : from), "r"(size)
                  : "memory");
   }
-}
-// Where element e is in its copy.
-template <typename T>
-__device__ __forceinline__ const T* span_at(const uint4* at, size_t e) {
-  return reinterpret_cast<const T*>(at) + e * sizeof(T) % 16 / sizeof(T);
 }
 // Zeros in the units that no copy writes: those beyond the row, and all of a row that is not given.
 template <typename T, int U>
@@ -174,6 +217,13 @@ __device__ __forceinline__ void clear_row(uint4* to, bool given, int dim) {
       to[j * blockDim.x + threadIdx.x] = make_uint4(0, 0, 0, 0);
 }
 
+// Zeros in all units, before the first copy.
+__device__ __forceinline__ void clear_ring(uint4* ring, int units) {
+  for (int i = threadIdx.x; i < units; i += blockDim.x) ring[i] = make_uint4(0, 0, 0, 0);
+  __syncthreads();
+}
+
+constexpr int kNrWarps = 16;   // of a block, at most
 constexpr int kNrRanks = 8;   // blocks that share wide rows, at most
 // A block's place in its cluster, and its columns.
 struct NormResPart {
@@ -194,7 +244,7 @@ __device__ __forceinline__ NormResPart part_of(const A& a) {
 // cluster; after the last call's barrier none is written to any more.
 template <int N>
 struct RowSums {
-  alignas(16) float warp[2][N][16];
+  alignas(16) float warp[2][N][kNrWarps];
   float block[2][kNrRanks][N];
 };
 template <int N>
@@ -238,8 +288,8 @@ __device__ __forceinline__ void row_sums(float (&v)[N], RowSums<N>& red, int& tu
 template <int N>
 __device__ __forceinline__ void clear_sums(RowSums<N>& red, int ranks) {
   const int warps = blockDim.x >> 5;
-  for (int i = threadIdx.x; i < 2 * 16 * N; i += blockDim.x)
-    if (i % 16 >= warps) (&red.warp[0][0][0])[i] = 0.0f;
+  for (int i = threadIdx.x; i < 2 * kNrWarps * N; i += blockDim.x)
+    if (i % kNrWarps >= warps) (&red.warp[0][0][0])[i] = 0.0f;
   if (ranks > 1) asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // 1 / sqrt(x): an estimate and one step of Newton's method.
@@ -278,8 +328,8 @@ __global__ void __launch_bounds__(T0, T0 == 32 ? 24 : (U * Unit<T>::kPer == 8 ? 
       copy_row<T, U>(to, ys + row_at(r), dim);
       copy_row<T, U>(to + array, xs + row_at(r), dim);
     } else if (r < end) {
-      copy_span(to, ys, row_at(r), dim, (size_t)a.rows * a.dim);
-      copy_span(to + array, xs, row_at(r), dim, (size_t)a.rows * a.dim);
+      copy_span(to, ys, row_at(r), dim);
+      copy_span(to + array, xs, row_at(r), dim);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
     fill = fill + 1 == a.stages ? 0 : fill + 1;
@@ -287,7 +337,8 @@ __global__ void __launch_bounds__(T0, T0 == 32 ? 24 : (U * Unit<T>::kPer == 8 ? 
   // (the vectors' loads and the first rows' copies are under way together)
   f32x2 w[P], g2[P];
 #pragma unroll
-  for (int p = 0; p < P; ++p) g2[p] = vector_at<T, OWN, T0>(a.g2 ? a.g2 + my.c0 : nullptr, dim, 0.0f, 2 * p);
+  for (int p = 0; p < P; ++p) g2[p] = vector_at<T, OWN, U>(a.g2 ? a.g2 + my.c0 : nullptr, dim, 0.0f, 2 * p);
+  if (!OWN) clear_ring(ring, a.stages * stage);
   for (int i = 0; i < a.stages - 1; ++i) ahead(first + i);
   if (OWN)
     for (int i = 0; i < 2 * a.stages; ++i) clear_row<T, U>(ring + i * array, true, dim);
@@ -300,10 +351,11 @@ __global__ void __launch_bounds__(T0, T0 == 32 ? 24 : (U * Unit<T>::kPer == 8 ? 
       const float* gate = a.gate ? a.gate + (size_t)gi * a.dim + my.c0 : nullptr;
 #pragma unroll
       for (int p = 0; p < P; ++p)
-        w[p] = mul2(vector_at<T, OWN, T0>(a.g1 ? a.g1 + my.c0 : nullptr, dim, 1.0f, 2 * p), vector_at<T, OWN, T0>(gate, dim, 1.0f, 2 * p));
+        w[p] = mul2(vector_at<T, OWN, U>(a.g1 ? a.g1 + my.c0 : nullptr, dim, 1.0f, 2 * p), vector_at<T, OWN, U>(gate, dim, 1.0f, 2 * p));
       gate_end = (gi + 1) * a.gate_rows;
     }
     f32x2 y[P], x[P];
+    const int at = (int)(row_at(r) * sizeof(T) % 16);
     const uint4* in = ring + slot * stage;
     slot = slot + 1 == a.stages ? 0 : slot + 1;
     if (OWN) {
@@ -319,12 +371,8 @@ __global__ void __launch_bounds__(T0, T0 == 32 ? 24 : (U * Unit<T>::kPer == 8 ? 
       copies_wait(a.stages - 2);
       __syncthreads();             // row r is there, and the row before it has been read
       ahead(r + a.stages - 1);
-      const T *yr = span_at<T>(in, row_at(r)), *xr = span_at<T>(in + array, row_at(r));
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        y[p] = pair_at<T0>(yr, dim, 2 * p);
-        x[p] = pair_at<T0>(xr, dim, 2 * p);
-      }
+      pairs_at<T, U, P>(in, at, 0, y);
+      pairs_at<T, U, P>(in + array, at, 0, x);
     }
     float r1 = 1.0f, r2 = 1.0f;
     const auto root_of = [&](const f32x2 (&v)[P]) {
@@ -347,7 +395,7 @@ __global__ void __launch_bounds__(T0, T0 == 32 ? 24 : (U * Unit<T>::kPer == 8 ? 
     if (OWN) {
 #pragma unroll
       for (int j = 0; j < U; ++j) {
-        const int c = column<T, OWN, T0>(j * per);
+        const int c = column<T, OWN, U>(j * per);
         if (c >= dim) continue;
         f32x2 f[pairs];
 #pragma unroll
@@ -359,10 +407,11 @@ __global__ void __launch_bounds__(T0, T0 == 32 ? 24 : (U * Unit<T>::kPer == 8 ? 
         *reinterpret_cast<uint4*>(h + c) = narrow(f);
       }
     } else {
+      store_pairs<U, P>(xo, at, dim, 0, x);
+      if (h) {
 #pragma unroll
-      for (int p = 0; p < P; ++p) {
-        store_pair<T0>(xo, dim, 2 * p, x[p]);
-        if (h) store_pair<T0>(h, dim, 2 * p, mul2(x[p], mul2(rq, g2[p])));
+        for (int p = 0; p < P; ++p) x[p] = mul2(x[p], mul2(rq, g2[p]));
+        store_pairs<U, P>(h, at, dim, 0, x);
       }
     }
     if (a.rstd && my.rank == 0 && threadIdx.x == 0) *reinterpret_cast<float2*>(a.rstd + 2 * (size_t)r) = make_float2(r1, r2);
@@ -403,8 +452,9 @@ __device__ __forceinline__ void span_sums(const NormResGradArgs& a, int block, c
 // The three sums of a row in one exchange.  With b = w y (w = gate g1) and q = dx' + r2 dh g2:
 // S1 = sum dh g2 x', and sum w t y = sum b q - r2^3 / dim S1 sum b x'.
 template <typename T, int U, bool OWN, int T0>
-__global__ void __launch_bounds__(T0, T0 == 32 ? (OWN ? 24 : 16) : (U * Unit<T>::kPer == 8 ? 768 : OWN || T0 >= 256 ? 512 : 384) / T0) norm_res_grad_kernel(NormResGradArgs a) {
+__global__ void __launch_bounds__(T0, T0 == 32 ? 24 : (U * Unit<T>::kPer == 8 ? 768 : 512) / T0) norm_res_grad_kernel(NormResGradArgs a) {
   constexpr int per = Unit<T>::kPer, pairs = Unit<T>::kPairs, E = U * per, P = E / 2;
+  constexpr int N = sizeof(T) == 4 ? 1 : pairs;   // at any offset: pairs of a row at a time, as registers allow
   extern __shared__ __align__(16) uint4 ring[];   // [stage][y, x, dx_out, dh][U][threads]
   __shared__ RowSums<3> red;
   const NormResPart my = part_of(a);
@@ -419,7 +469,7 @@ __global__ void __launch_bounds__(T0, T0 == 32 ? (OWN ? 24 : 16) : (U * Unit<T>:
 #pragma unroll
   for (int p = 0; p < P; ++p) {
     s2[p] = both(0.0f);
-    g2[p] = vector_at<T, OWN, T0>(hs ? a.g2 + my.c0 : nullptr, dim, 0.0f, 2 * p);
+    g2[p] = vector_at<T, OWN, U>(hs ? a.g2 + my.c0 : nullptr, dim, 0.0f, 2 * p);
   }
   const auto clear = [&] {
     if (OWN)
@@ -438,30 +488,31 @@ __global__ void __launch_bounds__(T0, T0 == 32 ? (OWN ? 24 : 16) : (U * Unit<T>:
     int fill = 0, slot = 0;
     const auto ahead = [&](int r) {
       uint4* to = ring + fill * stage;
-      const size_t at = (size_t)r * a.dim + my.c0, all = (size_t)a.rows * a.dim;
+      const size_t at = (size_t)r * a.dim + my.c0;
       if (r < s.end && OWN) {
         copy_row<T, U>(to, ys + at, dim);
         copy_row<T, U>(to + array, xs + at, dim);
         if (os) copy_row<T, U>(to + 2 * array, os + at, dim);
         if (hs) copy_row<T, U>(to + 3 * array, hs + at, dim);
       } else if (r < s.end) {
-        copy_span(to, ys, at, dim, all);
-        copy_span(to + array, xs, at, dim, all);
-        if (os) copy_span(to + 2 * array, os, at, dim, all);
-        if (hs) copy_span(to + 3 * array, hs, at, dim, all);
+        copy_span(to, ys, at, dim);
+        copy_span(to + array, xs, at, dim);
+        if (os) copy_span(to + 2 * array, os, at, dim);
+        if (hs) copy_span(to + 3 * array, hs, at, dim);
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
       fill = fill + 1 == a.stages ? 0 : fill + 1;
     };
-    if (!OWN) __syncthreads();   // the last span's rows have been read
+    if (!OWN && any) __syncthreads();   // the last span's rows have been read
+    if (!OWN && !any) clear_ring(ring, a.stages * stage);
     // (the vectors' loads and the first rows' copies are under way together)
     const float2* roots = reinterpret_cast<const float2*>(a.rstd);
     float2 root = roots[s.first];
     f32x2 g1[P], ga[P];
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      g1[p] = vector_at<T, OWN, T0>(a.g1 ? a.g1 + my.c0 : nullptr, dim, 1.0f, 2 * p);
-      ga[p] = vector_at<T, OWN, T0>(gate, dim, 1.0f, 2 * p);
+      g1[p] = vector_at<T, OWN, U>(a.g1 ? a.g1 + my.c0 : nullptr, dim, 1.0f, 2 * p);
+      ga[p] = vector_at<T, OWN, U>(gate, dim, 1.0f, 2 * p);
     }
     for (int i = 0; i < a.stages - 1; ++i) ahead(s.first + i);
     if (!any) clear();
@@ -474,7 +525,7 @@ __global__ void __launch_bounds__(T0, T0 == 32 ? (OWN ? 24 : 16) : (U * Unit<T>:
       const size_t at = (size_t)r * a.dim + my.c0;
       const float r1 = a.g1 ? root.x : 1.0f, r2 = hs ? root.y : 1.0f;
       const f32x2 rr1 = both(r1), rr2 = both(r2);
-      f32x2 dy[OWN ? 1 : P], dx[OWN ? 1 : P], dq[OWN ? 1 : P], dh[OWN ? 1 : P];
+      const int off = (int)(at * sizeof(T) % 16);
       const uint4* in = ring + slot * stage;
       slot = slot + 1 == a.stages ? 0 : slot + 1;
       if (OWN) {
@@ -485,16 +536,6 @@ __global__ void __launch_bounds__(T0, T0 == 32 ? (OWN ? 24 : 16) : (U * Unit<T>:
         copies_wait(a.stages - 2);
         __syncthreads();             // row r is there, and the row before it has been read
         ahead(r + a.stages - 1);
-        const T *yr = span_at<T>(in, at), *xr = span_at<T>(in + array, at);
-        const T* qr = os ? span_at<T>(in + 2 * array, at) : nullptr;
-        const T* hr = hs ? span_at<T>(in + 3 * array, at) : nullptr;
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-          dy[OWN ? 0 : p] = pair_at<T0>(yr, dim, 2 * p);
-          dx[OWN ? 0 : p] = pair_at<T0>(xr, dim, 2 * p);
-          dq[OWN ? 0 : p] = pair_at<T0>(qr, dim, 2 * p);
-          dh[OWN ? 0 : p] = pair_at<T0>(hr, dim, 2 * p);
-        }
       }
       if (r + 1 < s.end) root = roots[r + 1];
       const auto unit = [&](int j, f32x2 (&y)[pairs], f32x2 (&x)[pairs], f32x2 (&o)[pairs], f32x2 (&h)[pairs]) {
@@ -505,12 +546,12 @@ __global__ void __launch_bounds__(T0, T0 == 32 ? (OWN ? 24 : 16) : (U * Unit<T>:
           widen(in[3 * array + j * blockDim.x], h);
         } else {
 #pragma unroll
-          for (int i = 0; i < pairs; ++i) {
-            const int p = OWN ? 0 : j * pairs + i;
-            y[i] = dy[p];
-            x[i] = dx[p];
-            o[i] = dq[p];
-            h[i] = dh[p];
+          for (int i = 0; i < pairs; i += N) {
+            const int e = j * per + 2 * i;
+            pairs_at<T, U, N>(in, off, e, y + i);
+            pairs_at<T, U, N>(in + array, off, e, x + i);
+            pairs_at<T, U, N>(in + 2 * array, off, e, o + i);
+            pairs_at<T, U, N>(in + 3 * array, off, e, h + i);
           }
         }
       };
@@ -549,15 +590,15 @@ __global__ void __launch_bounds__(T0, T0 == 32 ? (OWN ? 24 : 16) : (U * Unit<T>:
           y[i] = fma2(rr1, mul2(wp, t), mul2(y[i], n2));
         }
         if (OWN) {
-          const int c = column<T, OWN, T0>(j * per);
+          const int c = column<T, OWN, U>(j * per);
           if (c >= dim) continue;
           *reinterpret_cast<uint4*>(static_cast<T*>(a.dy) + at + c) = narrow(y);
           *reinterpret_cast<uint4*>(static_cast<T*>(a.dx) + at + c) = narrow(x);
         } else {
 #pragma unroll
-          for (int i = 0; i < pairs; ++i) {
-            store_pair<T0>(static_cast<T*>(a.dy) + at, dim, (j * pairs + i) * 2, y[i]);
-            store_pair<T0>(static_cast<T*>(a.dx) + at, dim, (j * pairs + i) * 2, x[i]);
+          for (int i = 0; i < pairs; i += N) {
+            store_pairs<U, N>(static_cast<T*>(a.dy) + at, off, dim, j * per + 2 * i, y + i);
+            store_pairs<U, N>(static_cast<T*>(a.dx) + at, off, dim, j * per + 2 * i, x + i);
           }
         }
       }
@@ -566,7 +607,7 @@ __global__ void __launch_bounds__(T0, T0 == 32 ? (OWN ? 24 : 16) : (U * Unit<T>:
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const float2 f = parts(sp[p]);
-      const int c = column<T, OWN, T0>(2 * p), d = column<T, OWN, T0>(2 * p + 1);
+      const int c = column<T, OWN, U>(2 * p), d = column<T, OWN, U>(2 * p + 1);
       if (c < dim) span_sums(a, my.block, s, !any, my.c0 + c, f.x);
       if (d < dim) span_sums(a, my.block, s, !any, my.c0 + d, f.y);
     }
@@ -576,7 +617,7 @@ __global__ void __launch_bounds__(T0, T0 == 32 ? (OWN ? 24 : 16) : (U * Unit<T>:
 #pragma unroll
   for (int p = 0; p < P; ++p) {
     const float2 f = parts(s2[p]);
-    const int c = column<T, OWN, T0>(2 * p), d = column<T, OWN, T0>(2 * p + 1);
+    const int c = column<T, OWN, U>(2 * p), d = column<T, OWN, U>(2 * p + 1);
     if (c < dim) keep[a.dim + c] = f.x;
     if (d < dim) keep[a.dim + d] = f.y;
   }
@@ -741,47 +782,56 @@ struct NormResShape {
 };
 constexpr size_t kNrSmem = 220 * 1024;
 constexpr int kNrMost = 512;
+constexpr int kNrFew = 192;
 // A warp of eight elements a lane for the narrowest rows, else sixteen elements a
 // thread, which take fewer exchanges (32768 x 1024 bf16 backward: 76 us against 80), but
 // eight up to 1024 where that leaves fewer threads without elements (16384 x 600 fp32:
 // 52 us against 57) or where blocks have few rows each and their start counts (2000 x 1000
 // bf16: 16.1 us against 18.6).  A cluster of blocks where a row is more than the threads
-// of one hold, or two rows of it more than shared memory does.
+// of one hold, or two rows of it more than shared memory does: backward, of blocks of up
+// to 192 threads, of which a multiprocessor has several (2142 x 14000 bf16 102 us, 1831 x
+// 8192 fp32 91; of up to 512 threads 124 and 119), forward, of up to 512 (1500 x 20000 bf16
+// 83 us against 94).  Rows that one block holds are faster so (6000 x 5000 bf16 backward 89
+// us, by clusters 103).
 NormResShape norm_res_shape(int dtype, int rows, int dim, bool grad) {
   NormResShape s;
   const int es = dtype ? 2 : 4, per = 16 / es;
   s.own = (size_t)dim * es % 16 == 0;
-  for (s.ranks = 1; s.ranks <= kNrRanks; s.ranks *= 2) {
-    s.part = (dim + s.ranks - 1) / s.ranks;
-    if (s.own) s.part = (s.part + per - 1) / per * per;
-    // (forward: 32 elements a thread before two blocks, which cost a row two exchanges)
-    s.each = s.part <= 256 ? 8 : s.part <= 16 * 512 || grad ? 16 : 32;
-    int threads = ((s.part + s.each - 1) / s.each + 31) / 32 * 32;
-    if (s.own && s.each == 16 && s.part <= 1024) {
-      const int eight = ((s.part + 7) / 8 + 31) / 32 * 32;
-      if (20 * eight < 17 * 2 * threads || rows < 8 * device_sms() * 512 / threads) {
-        s.each = 8;
-        threads = eight;
+  for (const int few : {kNrFew, kNrMost}) {
+    for (s.ranks = 1; s.ranks <= kNrRanks; s.ranks *= 2) {
+      const int most = grad && s.ranks > 1 ? few : kNrMost;
+      s.part = (dim + s.ranks - 1) / s.ranks;
+      if (s.own) s.part = (s.part + per - 1) / per * per;
+      // (forward: 32 elements a thread before two blocks, which cost a row two exchanges)
+      s.each = s.part <= 256 ? 8 : s.part <= 16 * 512 || grad ? 16 : 32;
+      int threads = ((s.part + s.each - 1) / s.each + 31) / 32 * 32;
+      if (s.each == 16 && s.part <= 1024) {
+        const int eight = ((s.part + 7) / 8 + 31) / 32 * 32;
+        if (20 * eight < 17 * 2 * threads || rows < 8 * device_sms() * 512 / threads) {
+          s.each = 8;
+          threads = eight;
+        }
       }
+      if (threads > most) continue;
+      s.row_units = s.each * es * threads / 16 + (s.own ? 0 : 2);
+      const size_t row = (size_t)(grad ? 4 : 2) * s.row_units * 16;
+      s.stages = (int)std::min<size_t>(kNrStages, kNrSmem / row);
+      s.smem = s.stages * row;
+      if (s.stages < 2) continue;
+      s.threads = threads;
+      return s;
     }
-    if (!s.own && s.each > 8)   // (compiled for powers of two)
-      for (threads = 64; threads * s.each < s.part;) threads *= 2;
-    if (threads > kNrMost) continue;
-    s.row_units = s.own ? s.each * es * threads / 16 : (s.part * es + 15) / 16 + 1;
-    const size_t row = (size_t)(grad ? 4 : 2) * s.row_units * 16;
-    s.stages = (int)std::min<size_t>(kNrStages, kNrSmem / row);
-    s.smem = s.stages * row;
-    if (s.stages < 2) continue;
-    s.threads = threads;
-    return s;
   }
   s.ranks = 1;
   return s;
 }
-// Rows that are worked on at once: by registers (128 a thread; 80 in the narrowest) and by shared memory.
-int norm_res_slots(const NormResShape& s, bool grad) {
+// Rows that are worked on at once: by registers (128 a thread; 80 in the narrowest) and by
+// shared memory.  Clusters may be fewer, as they do not fill all multiprocessors: the
+// launch asks how many run at once, or its last ones would wait for a second round (3125 x
+// 9600 bf16 backward, 112 clusters where 110 run: 151 us against 100).
+int norm_res_slots(const NormResShape& s) {
   if (!s.threads) return device_sms() * 4;
-  int n = s.each == 8 ? (grad && !s.own ? 512 : 768) / s.threads : (grad && !s.own && s.threads < 256 ? 384 : 512) / s.threads;
+  int n = (s.each == 8 ? 768 : 512) / s.threads;
   n = std::max(1, std::min(n, (int)(kNrSmem / (s.smem + 2048))));
   return std::max(1, device_sms() * n / s.ranks);
 }
@@ -811,14 +861,20 @@ long long norm_res_most_blocks(int rows, int dim, int gates) {
   long long most = 1;
   for (int dtype = 0; dtype < 2; ++dtype)
     for (int r : {1, rows}) {
-      const int slots = norm_res_slots(norm_res_shape(dtype, r, dim, true), true);
-      most = std::max(most, slots / gates >= 4 ? (long long)slots : 8ll * slots);
+      const NormResShape shape = norm_res_shape(dtype, r, dim, true);
+      const int slots = norm_res_slots(shape);
+      // (clusters: half the slots or more, see norm_res_clusters)
+      most = std::max(most, slots / gates >= (shape.ranks > 1 ? 8 : 4) ? (long long)slots : 8ll * slots);
     }
   return std::min<long long>(most, std::max(rows, 1));
 }
 
+// The slots of a cluster's shape, of which `active` run at once.
+int norm_res_clusters(int slots, int active) { return std::max((slots + 1) / 2, std::min(slots, active)); }
+
+// Launches, or, with `active`, tells how many clusters run at once.
 template <typename K, typename A>
-cudaError_t norm_res_launch(K kernel, const A& a, long long blocks, int threads, size_t smem, cudaStream_t s, int ranks = 1) {
+cudaError_t norm_res_launch(K kernel, const A& a, long long blocks, int threads, size_t smem, cudaStream_t s, int ranks = 1, int* active = nullptr) {
   if (smem > 40 * 1024) {   // (the static part counts too)
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
@@ -834,29 +890,26 @@ cudaError_t norm_res_launch(K kernel, const A& a, long long blocks, int threads,
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
   cfg.attrs = &at;
   cfg.numAttrs = ranks > 1;
+  if (active) return cudaOccupancyMaxActiveClusters(active, kernel, &cfg);
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <typename T, bool OWN>
-cudaError_t norm_res_forward(const NormResArgs& a, const NormResShape& s, long long blocks, cudaStream_t st) {
+cudaError_t norm_res_forward(const NormResArgs& a, const NormResShape& s, long long blocks, cudaStream_t st, int* active) {
   constexpr int W = sizeof(T) == 4 ? 2 : 1;   // units of eight elements
-  const auto go = [&](auto kernel) { return norm_res_launch(kernel, a, blocks, s.threads, s.smem, st, s.ranks); };
+  const auto go = [&](auto kernel) { return norm_res_launch(kernel, a, blocks, s.threads, s.smem, st, s.ranks, active); };
   if (s.each == 8) return s.threads == 32 ? go(norm_res_kernel<T, W, OWN, 32>) : go(norm_res_kernel<T, W, OWN, 128>);
   if (s.each == 32) return go(norm_res_kernel<T, 4 * W, OWN, 512>);
-  if (!OWN && s.threads <= 64) return go(norm_res_kernel<T, 2 * W, OWN, OWN ? 128 : 64>);
   if (s.threads <= 128) return go(norm_res_kernel<T, 2 * W, OWN, 128>);
-  if (!OWN && s.threads <= 256) return go(norm_res_kernel<T, 2 * W, OWN, OWN ? 512 : 256>);
   return go(norm_res_kernel<T, 2 * W, OWN, 512>);
 }
 template <typename T, bool OWN>
-cudaError_t norm_res_backward(const NormResGradArgs& a, const NormResShape& s, long long blocks, cudaStream_t st) {
+cudaError_t norm_res_backward(const NormResGradArgs& a, const NormResShape& s, long long blocks, cudaStream_t st, int* active) {
   constexpr int W = sizeof(T) == 4 ? 2 : 1;
-  const auto go = [&](auto kernel) { return norm_res_launch(kernel, a, blocks, s.threads, s.smem, st, s.ranks); };
+  const auto go = [&](auto kernel) { return norm_res_launch(kernel, a, blocks, s.threads, s.smem, st, s.ranks, active); };
   if (s.each == 8) return s.threads == 32 ? go(norm_res_grad_kernel<T, W, OWN, 32>) : go(norm_res_grad_kernel<T, W, OWN, 128>);
-  if (!OWN && s.threads <= 64) return go(norm_res_grad_kernel<T, 2 * W, OWN, OWN ? 128 : 64>);
   if (s.threads <= 128) return go(norm_res_grad_kernel<T, 2 * W, OWN, 128>);
-  if (!OWN && s.threads <= 256) return go(norm_res_grad_kernel<T, 2 * W, OWN, OWN ? 512 : 256>);
   return go(norm_res_grad_kernel<T, 2 * W, OWN, 512>);
 }
 
@@ -906,13 +959,18 @@ extern "C" mg_status mg_norm_residual_forward(int dtype, const void* y, const vo
     e = dtype ? mg::norm_res_launch(mg::norm_res_wide_kernel<mg::bf16>, a, rows, mg::kNrThreads, 0, s)
               : mg::norm_res_launch(mg::norm_res_wide_kernel<float>, a, rows, mg::kNrThreads, 0, s);
   } else {
-    const int slots = mg::norm_res_slots(shape, false);
+    const auto go = [&](long long blocks, int* active) {
+      if (dtype)
+        return shape.own ? mg::norm_res_forward<mg::bf16, true>(a, shape, blocks, s, active)
+                         : mg::norm_res_forward<mg::bf16, false>(a, shape, blocks, s, active);
+      return shape.own ? mg::norm_res_forward<float, true>(a, shape, blocks, s, active)
+                       : mg::norm_res_forward<float, false>(a, shape, blocks, s, active);
+    };
+    int slots = mg::norm_res_slots(shape), active = slots;
+    e = shape.ranks > 1 ? go(slots, &active) : cudaSuccess;
+    slots = mg::norm_res_clusters(slots, active);
     a.block_rows = (rows + slots - 1) / slots;
-    const long long blocks = (rows + a.block_rows - 1) / a.block_rows;
-    if (dtype)
-      e = shape.own ? mg::norm_res_forward<mg::bf16, true>(a, shape, blocks, s) : mg::norm_res_forward<mg::bf16, false>(a, shape, blocks, s);
-    else
-      e = shape.own ? mg::norm_res_forward<float, true>(a, shape, blocks, s) : mg::norm_res_forward<float, false>(a, shape, blocks, s);
+    if (e == cudaSuccess) e = go((rows + a.block_rows - 1) / a.block_rows, nullptr);
   }
   return mg::op_end(fn, e);
 }
@@ -953,7 +1011,18 @@ extern "C" mg_status mg_norm_residual_backward(int dtype, const void* dx_out, co
   }
   a.gate_rows = rows / a.gates;
   const mg::NormResShape shape = mg::norm_res_shape(dtype, rows, dim, true);
-  const mg::NormResSplit split = mg::norm_res_split(rows, a.gates, mg::norm_res_slots(shape, true));
+  const auto go = [&](long long blocks, int* active) {
+    if (dtype)
+      return shape.own ? mg::norm_res_backward<mg::bf16, true>(a, shape, blocks, s, active)
+                       : mg::norm_res_backward<mg::bf16, false>(a, shape, blocks, s, active);
+    return shape.own ? mg::norm_res_backward<float, true>(a, shape, blocks, s, active)
+                     : mg::norm_res_backward<float, false>(a, shape, blocks, s, active);
+  };
+  const int most = mg::norm_res_slots(shape);
+  int active = most;
+  cudaError_t e = shape.ranks > 1 ? go(most, &active) : cudaSuccess;
+  if (e != cudaSuccess) return mg::op_end(fn, e);
+  const mg::NormResSplit split = mg::norm_res_split(rows, a.gates, mg::norm_res_clusters(most, active));
   a.stages = shape.stages;
   a.row_units = shape.row_units;
   a.ranks = shape.ranks;
@@ -961,16 +1030,11 @@ extern "C" mg_status mg_norm_residual_backward(int dtype, const void* dx_out, co
   a.parts = split.parts;
   a.block_rows = split.block_rows;
   a.block_gates = split.block_gates;
-  cudaError_t e;
   if (!shape.threads)
     e = dtype ? mg::norm_res_launch(mg::norm_res_grad_wide_kernel<mg::bf16>, a, split.blocks, mg::kNrThreads, 0, s)
               : mg::norm_res_launch(mg::norm_res_grad_wide_kernel<float>, a, split.blocks, mg::kNrThreads, 0, s);
-  else if (dtype)
-    e = shape.own ? mg::norm_res_backward<mg::bf16, true>(a, shape, split.blocks, s)
-                   : mg::norm_res_backward<mg::bf16, false>(a, shape, split.blocks, s);
   else
-    e = shape.own ? mg::norm_res_backward<float, true>(a, shape, split.blocks, s)
-                   : mg::norm_res_backward<float, false>(a, shape, split.blocks, s);
+    e = go(split.blocks, nullptr);
   const int gate_blocks = dgate && a.parts > 1 && a.gates > 1 ? std::min(a.gates, 65533) : 0;
   if (e == cudaSuccess && (dgamma_post || dgamma_pre || (dgate && a.parts > 1)))
   {

@@ -210,6 +210,68 @@ def test_a_workspace_for_more_rows_serves_fewer():
             _backward_check(i, out[2], 1.1, _backward(i, out[2], 1.1, ws=ws), t)
 
 
+# around a warp's words, a unit, one block's rows, a cluster's parts; odd, even and aligned rows
+EDGES = [1, 2, 3, 7, 9, 63, 65, 127, 130, 255, 257, 258, 511, 513, 514, 1023, 1025, 1026, 1537, 2047, 2050, 4095, 4097, 6145,
+         8191, 8193, 8194, 9601, 12289, 16383, 16385]
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+@pytest.mark.parametrize("dim", EDGES)
+def test_any_offset(dim, t):
+    i = _inputs(13, dim, t, 1, True, True, dim)
+    out = _forward(i, 0.7)
+    _forward_check(i, 0.7, out, t)
+    _backward_check(i, out[2], 0.7, _backward(i, out[2], 0.7), t)
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+@pytest.mark.parametrize("dim", [50, 777, 778, 2045, 2124, 4097, 9011, 16385])
+def test_neighbours_of_other_kinds(dim, t):
+    """Rows and elements beside a matrix that are no numbers reach no other row; what lies around the outputs stays."""
+    rows, before, after = 9, 16, 64
+    n = rows * dim
+
+    def placed(v, fill):
+        big = torch.full((before + n + after,), fill, dtype=DT[t], device="cuda")
+        at = big[before:before + n].view(rows, dim)
+        at.copy_(v)
+        return big, at
+
+    i = _inputs(rows, dim, t, 1, True, True, dim + 1)
+    keep = [r for r in range(rows) if r not in (0, 4, 8)]
+    small = {k: v[keep].contiguous() if k in ("y", "x", "dxo", "dh") else v for k, v in i.items()}
+    for k in ("y", "x", "dxo", "dh"):
+        i[k][[0, 4, 8]] = float("nan")
+        i[k] = placed(i[k], float("inf"))[1]
+    rstd = torch.full((rows, 2), 77.0, device="cuda")
+    outs = [placed(torch.zeros(rows, dim, device="cuda"), 77.0) for _ in range(4)]
+    mg.norm_residual_forward(i["y"], i["x"], outs[0][1], outs[1][1], gamma_post=i["g1"], gate=i["gate"], gamma_pre=i["g2"],
+                             scale=0.7, eps=EPS, rstd=rstd)
+    ws = torch.full((mg.norm_residual_workspace_bytes(rows, dim, 1),), 255, dtype=torch.uint8, device="cuda")
+    mg.norm_residual_backward(i["dxo"], i["dh"], i["y"], i["x"], rstd, outs[2][1], outs[3][1], ws, gamma_post=i["g1"],
+                              gate=i["gate"], gamma_pre=i["g2"], scale=0.7)
+    for big, at in outs:
+        assert (big[:before] == 77).all() and (big[before + n:] == 77).all()
+        assert at[[0, 4, 8]].isnan().all()
+    _forward_check(small, 0.7, (outs[0][1][keep], outs[1][1][keep], rstd[keep]), t)
+    want, mag = _formula(small, rstd[keep], 0.7, -1), _formula(small, rstd[keep], 0.7, 1)
+    for k, o in (("dy", outs[2][1]), ("dx", outs[3][1])):
+        e = (30 + 2 * (dim / 32 + 10)) * U * mag[k]
+        assert ((o[keep].double() - want[k]).abs() <= e + HALF[t] * (want[k].abs() + e)).all(), k
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+@pytest.mark.parametrize("dim", [9600, 9011, 16384, 8192])
+@pytest.mark.parametrize("gates", [4, 9, 10, 13, 18, 19, 28, 38, 76, 150])
+def test_gates_of_wide_rows_stay_in_the_workspace(gates, dim, t):
+    need = mg.norm_residual_workspace_bytes(3 * gates, dim, gates)
+    ws = torch.full((need + 4096 * 64,), 255, dtype=torch.uint8, device="cuda")
+    i = _inputs(3 * gates, dim, t, gates, True, True, gates)
+    out = _forward(i, 0.7)
+    _backward_check(i, out[2], 0.7, _backward(i, out[2], 0.7, ws=ws[:need]), t)
+    assert (ws[need:] == 255).all()
+
+
 def test_against_differences():
     """Central differences of the definition in 64 bits (step 1e-5: truncation below 1e-8 of third derivatives under
     100, rounding 1e-10) beside the kernel's own bound; rstd is the forward's, within its bound of the exact one, and
@@ -341,3 +403,8 @@ def test_stream_and_graph(rows, dim, gates, t):
         torch.cuda.synchronize()
         _forward_check(i, 0.9, out, t)
         _backward_check(i, out[2], 0.9, o, t)
+
+
+@pytest.mark.parametrize("rows,dim,gates,t", [(40, 12288, 2, "bf16"), (40, 12291, 1, "bf16"), (20, 20000, 1, "f32"), (9, 16385, 3, "f32")])
+def test_stream_and_graph_of_wide_rows(rows, dim, gates, t):
+    test_stream_and_graph(rows, dim, gates, t)
