@@ -310,7 +310,7 @@ __device__ __forceinline__ void copies_wait(int n) {
 }
 
 template <typename T, int U, bool OWN, int T0>
-__global__ void __launch_bounds__(T0, T0 == 32 ? 24 : (U * Unit<T>::kPer == 8 ? 768 : 512) / T0) norm_res_kernel(NormResArgs a) {
+__global__ void __launch_bounds__(T0, T0 == 32 ? 24 : (U * Unit<T>::kPer == 8 ? 768 : T0 == 320 ? 640 : 512) / T0) norm_res_kernel(NormResArgs a) {
   constexpr int per = Unit<T>::kPer, pairs = Unit<T>::kPairs, E = U * per, P = E / 2;
   extern __shared__ __align__(16) uint4 ring[];   // [stage][y, x][U][threads]
   __shared__ RowSums<1> red;
@@ -777,6 +777,7 @@ struct NormResShape {
   int threads = 0;   // 0: the kernels for any width
   int each = 0;      // elements a thread
   bool own = false;
+  bool more = false;   // 640 threads on a multiprocessor instead of 512
   int stages = 0, row_units = 0, ranks = 1, part = 0;
   size_t smem = 0;
 };
@@ -792,7 +793,10 @@ constexpr int kNrFew = 192;
 // to 192 threads, of which a multiprocessor has several (2142 x 14000 bf16 102 us, 1831 x
 // 8192 fp32 91; of up to 512 threads 124 and 119), forward, of up to 512 (1500 x 20000 bf16
 // 83 us against 94).  Rows that one block holds are faster so (6000 x 5000 bf16 backward 89
-// us, by clusters 103).
+// us, by clusters 103).  Forward, 96 registers a thread are enough where they let one
+// more block onto a multiprocessor (bf16 7322 x 4097 72 us against 103, 5859 x 5120 44 against 56,
+// 10000 x 3000 45 against 50; fp32 3661 x 4097 46 against 55, but 5000 x 3000 44.6 against
+// 42.5: where it doubles the blocks); backward they are not (6000 x 5000 bf16 113 against 89).
 NormResShape norm_res_shape(int dtype, int rows, int dim, bool grad) {
   NormResShape s;
   const int es = dtype ? 2 : 4, per = 16 / es;
@@ -819,6 +823,7 @@ NormResShape norm_res_shape(int dtype, int rows, int dim, bool grad) {
       s.smem = s.stages * row;
       if (s.stages < 2) continue;
       s.threads = threads;
+    s.more = !grad && s.each == 16 && threads > (dtype ? 128 : 256) && 640 / threads > 512 / threads;
       return s;
     }
   }
@@ -831,7 +836,7 @@ NormResShape norm_res_shape(int dtype, int rows, int dim, bool grad) {
 // 9600 bf16 backward, 112 clusters where 110 run: 151 us against 100).
 int norm_res_slots(const NormResShape& s) {
   if (!s.threads) return device_sms() * 4;
-  int n = (s.each == 8 ? 768 : 512) / s.threads;
+  int n = (s.each == 8 ? 768 : s.more ? 640 : 512) / s.threads;
   n = std::max(1, std::min(n, (int)(kNrSmem / (s.smem + 2048))));
   return std::max(1, device_sms() * n / s.ranks);
 }
@@ -902,6 +907,7 @@ cudaError_t norm_res_forward(const NormResArgs& a, const NormResShape& s, long l
   if (s.each == 8) return s.threads == 32 ? go(norm_res_kernel<T, W, OWN, 32>) : go(norm_res_kernel<T, W, OWN, 128>);
   if (s.each == 32) return go(norm_res_kernel<T, 4 * W, OWN, 512>);
   if (s.threads <= 128) return go(norm_res_kernel<T, 2 * W, OWN, 128>);
+  if (s.more) return go(norm_res_kernel<T, 2 * W, OWN, 320>);
   return go(norm_res_kernel<T, 2 * W, OWN, 512>);
 }
 template <typename T, bool OWN>
