@@ -457,7 +457,7 @@ mg_status mg_grad_list_clip(mg_grad_list* list, float max_norm, float* stats, mg
  * its outputs are 0, its top_ids -1.  Logits of -inf have probability 0; a row of nothing else
  * has logp and top_logp -inf, entropy 0 and no gradient.  A row that holds a NaN
  * or +inf has NaN in logp, entropy and top_logp (its top_ids are in order, NaN
- * below -inf).
+ * below -inf), and its gradient is NaN.
  *
  * backward: dlogits[r, v] = (dlogp[r] ([v = ids[r]] - p_v)
  *                            - dentropy[r] p_v (log p_v + entropy[r])) / temperature

@@ -578,7 +578,8 @@ __global__ void __launch_bounds__(256) logp_grad_kernel(LogpGradArgs a, int rank
   T* const to = dx + p.at;
   const T* const from = x + p.at;
   const int step = blockDim.x, behind = p.head + p.units * per;
-  if ((g == 0.0f && h == 0.0f) || st.x == -INFINITY) {
+  // (every logit is -inf: the sum of none is 0; beside a NaN it is NaN, and the maximum may be -inf too)
+  if ((g == 0.0f && h == 0.0f) || (st.x == -INFINITY && st.y == -INFINITY)) {
     for (int u = threadIdx.x; u < p.units; u += step) reinterpret_cast<uint4*>(to + p.head)[u] = make_uint4(0, 0, 0, 0);
     if ((int)threadIdx.x < p.head) st_elem(to, threadIdx.x, 0.0f);
     if ((int)threadIdx.x < p.tail) st_elem(to, behind + threadIdx.x, 0.0f);

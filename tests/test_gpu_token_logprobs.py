@@ -408,3 +408,29 @@ def test_stream_and_graph(rows, vocab):
         _check(x, ids, o, 9)
         want, tol = _formula(x, ids, o["stats"], g, None, None, 1.0)
         assert ((dx.double() - want).abs() <= tol * 1.01 + HALF["bf16"] * want.abs() + 2.0 ** -140).all()
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,vocab", [(5, 31), (5, 32000), (700, 1003), (5, 200001)])
+def test_rows_of_nan_alone(rows, vocab, t):
+    """A row of NaN, or of NaN beside -inf, has NaN in its results and in all of its gradient; one of -inf alone has none."""
+    x = _logits(rows, vocab, t, 60)
+    x[0] = NAN
+    x[1] = -INF
+    x[1, vocab // 2] = NAN
+    x[2] = -INF
+    x[3, ::2] = NAN
+    x[3, 1::2] = -INF
+    ids = _ids(rows, vocab, 61)
+    o = _forward(x, ids, 4)
+    bad, rest = [0, 1, 3], [r for r in range(rows) if r not in (0, 1, 3)]
+    for n in ("logp", "entropy", "top_logp"):
+        assert torch.isnan(o[n][bad]).all() and not torch.isnan(o[n][rest]).any()
+    one = torch.ones(rows, device="cuda")
+    for g, h in ((one, None), (None, one), (one, one)):
+        out = torch.full_like(x, 3.0)
+        mg.token_logprobs_backward(x, ids, o["stats"], g, out, entropy=None if h is None else o["entropy"], dentropy=h)
+        assert torch.isnan(out[bad]).all()
+        assert (out[2] == 0).all() and torch.isfinite(out[rest]).all()
+    mg.token_logprobs_backward(x, ids, o["stats"], one, x)          # in place
+    assert torch.isnan(x[bad]).all() and torch.isfinite(x[rest]).all()
