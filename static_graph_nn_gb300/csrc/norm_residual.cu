@@ -881,7 +881,8 @@ int norm_res_clusters(int slots, int active) { return std::max((slots + 1) / 2, 
 template <typename K, typename A>
 cudaError_t norm_res_launch(K kernel, const A& a, long long blocks, int threads, size_t smem, cudaStream_t s, int ranks = 1, int* active = nullptr) {
   if (smem > 40 * 1024) {   // (the static part counts too)
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // the most of any call, not this call's: the limit is the kernel's, and another host thread may launch it
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kNrSmem);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};

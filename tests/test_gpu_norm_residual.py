@@ -8,6 +8,7 @@ term taken at its absolute value.  A row's sum goes through at most dim / 32 + 1
 additions (a warp's lanes or more, then a tree), a column's sum through at most as
 many as it has rows plus 10.  Then half a step of the stored type."""
 import math
+import threading
 
 import pytest
 
@@ -408,3 +409,61 @@ def test_stream_and_graph(rows, dim, gates, t):
 @pytest.mark.parametrize("rows,dim,gates,t", [(40, 12288, 2, "bf16"), (40, 12291, 1, "bf16"), (20, 20000, 1, "f32"), (9, 16385, 3, "f32")])
 def test_stream_and_graph_of_wide_rows(rows, dim, gates, t):
     test_stream_and_graph(rows, dim, gates, t)
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+def test_host_threads(t):
+    """Calls of six host threads at once, each with its own tensors, workspace and stream, of widths that take the same
+    kernel with different amounts of shared memory: none fails, and each computes its own."""
+    dims = (6144, 8192) if t == "bf16" else (2560, 4096)
+    lib, work = binding.load(), []
+    for n in range(6):
+        i = _inputs(1, dims[n % 2], t, 0, True, True, 90 + n)
+        rstd = _forward(i, 0.7)[2]
+        ws = torch.zeros(mg.norm_residual_workspace_bytes(1, dims[n % 2], 0), dtype=torch.uint8, device="cuda")
+        s, o = torch.cuda.Stream(), _backward(i, rstd, 0.7, ws=ws)
+        # (the C call: most of the thread's time passes inside of it, where threads run at once)
+        args = (int(t == "bf16"), *(i[k].data_ptr() for k in ("dxo", "dh", "y", "x")), rstd.data_ptr(), 1, dims[n % 2],
+                i["g1"].data_ptr(), None, 0, 0.7, i["g2"].data_ptr(), o["dy"].data_ptr(), o["dx"].data_ptr(), None, None, None,
+                ws.data_ptr(), ws.nbytes, s.cuda_stream)
+        work.append((i, rstd, o, args, s, ws))
+    torch.cuda.synchronize()
+    for _, _, o, *_ in work:
+        o["dy"].fill_(77.0)
+        o["dx"].fill_(77.0)
+    torch.cuda.synchronize()
+    start, failed = threading.Barrier(len(work)), []
+
+    def calls(args):
+        start.wait()
+        failed.append(sum(lib.mg_norm_residual_backward(*args) != 0 for _ in range(4000)))
+
+    threads = [threading.Thread(target=calls, args=(w[3],)) for w in work]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    torch.cuda.synchronize()
+    assert failed == [0] * len(work)
+    for i, rstd, o, *_ in work:
+        _backward_check(i, rstd, 0.7, o, t)
+
+
+def test_two_widths_of_a_kernel_in_one_graph():
+    work = []
+    for n, dim in enumerate((8192, 6144, 8192)):
+        i = _inputs(4, dim, "bf16", 1, True, True, 95 + n)
+        work.append((i, torch.zeros(mg.norm_residual_workspace_bytes(4, dim, 1), dtype=torch.uint8, device="cuda")))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph, outs = torch.cuda.CUDAGraph(), []
+    with torch.cuda.graph(graph, stream=s):
+        for i, ws in work:
+            out = _forward(i, 0.7, stream=s)
+            outs.append((out, _backward(i, out[2], 0.7, stream=s, ws=ws)))
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    for (i, _), (out, o) in zip(work, outs):
+        _forward_check(i, 0.7, out, "bf16")
+        _backward_check(i, out[2], 0.7, o, "bf16")
