@@ -665,7 +665,7 @@ template <typename T>
 __global__ void __launch_bounds__(kNrThreads) norm_res_grad_wide_kernel(NormResGradArgs a) {
   __shared__ float red[32];
   float* sums = a.ws + (size_t)blockIdx.x * 2 * a.dim;   // the post norm's (or P), the pre norm's
-  for (int c = threadIdx.x; c < 2 * a.dim; c += kNrThreads) sums[c] = 0.0f;
+  for (int c = threadIdx.x; c < a.dim; c += kNrThreads) sums[c] = sums[(size_t)a.dim + c] = 0.0f;   // (2 dim may pass 2^31)
   __syncthreads();
   NormResSpan span = {-1, 0, 0};
   while (next_span(a, blockIdx.x, span)) {

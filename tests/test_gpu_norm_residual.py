@@ -467,3 +467,21 @@ def test_two_widths_of_a_kernel_in_one_graph():
     for (i, _), (out, o) in zip(work, outs):
         _forward_check(i, 0.7, out, "bf16")
         _backward_check(i, out[2], 0.7, o, "bf16")
+
+
+def test_the_widest_row():
+    """A row of 2^30 columns: every column's sum is its own, whatever the workspace held.  Small whole numbers, so that
+    all sums are exact: y is 0, 1, 0, 1, ..., t = dx_out = 1, 1 / sqrt of the mean is given as 1."""
+    d = 1 << 30
+    y = torch.ones(1, d, dtype=torch.bfloat16, device="cuda")
+    y[:, ::2] = 0
+    dxo = torch.ones_like(y)
+    g1 = torch.ones(d, device="cuda")
+    rstd = torch.ones(1, 2, device="cuda")
+    dy, dx, dg1 = torch.full_like(y, 77.0), torch.full_like(y, 77.0), torch.full_like(g1, 77.0)
+    ws = torch.full((mg.norm_residual_workspace_bytes(1, d, 0),), 255, dtype=torch.uint8, device="cuda")
+    mg.norm_residual_backward(dxo, None, y, y, rstd, dy, dx, ws, gamma_post=g1, dgamma_post=dg1)
+    del ws
+    assert (dx == 1).all()
+    assert (dg1[::2] == 0).all() and (dg1[1::2] == 1).all()
+    assert (dy[0, ::2] == 1).all() and (dy[0, 1::2] == 0.5).all()        # t - y mean(t y)
