@@ -487,7 +487,8 @@ mg_status mg_token_logprobs_backward(int dtype, const void* logits, long long ro
  * x_out, h and their gradients; gammas, gate, their gradients and rstd [rows, 2]
  * (1 / sqrt of the two means, 1 where there is no norm; for the backward, may be
  * NULL) are fp32.  h is computed from x_out before its rounding.  Sums of squares
- * are fp32: finite within +-1e19 / sqrt(dim).
+ * are fp32: finite within +-1e19 / sqrt(dim) (backward: those of gate gamma_post y x_out
+ * too).
  * x_out and h may each be y or x itself.
  *
  * backward, from dx_out and dh (either may be NULL, for none) and the forward's

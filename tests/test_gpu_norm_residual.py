@@ -8,6 +8,7 @@ term taken at its absolute value.  A row's sum goes through at most dim / 32 + 1
 additions (a warp's lanes or more, then a tree), a column's sum through at most as
 many as it has rows plus 10.  Then half a step of the stored type."""
 import math
+import sys
 import threading
 
 import pytest
@@ -485,3 +486,26 @@ def test_the_widest_row():
     assert (dx == 1).all()
     assert (dg1[::2] == 0).all() and (dg1[1::2] == 1).all()
     assert (dy[0, ::2] == 1).all() and (dy[0, 1::2] == 0.5).all()        # t - y mean(t y)
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+@pytest.mark.parametrize("dim", [200, 777, 2048, 9011, 70001])
+@pytest.mark.parametrize("ymag,xmag,eps", [(1e14, 1.0, 1e-6), (1e15, 1e15, 1e-6), (1e16, 1e-3, 1e-6), (1.0, 1e15, 1e-6),
+                                           (1e-14, 1e-14, 1e-30), (1.0, 1.0, 1e-30)])
+@pytest.mark.parametrize("post", [True, False])
+def test_magnitudes(ymag, xmag, eps, dim, post, t, monkeypatch):
+    """Rows far from 1 and rows of zeros under a small eps: the cube of 1 / sqrt of the mean leaves fp32's range, the
+    gradients do not."""
+    monkeypatch.setattr(sys.modules[__name__], "EPS", eps)
+    i = _inputs(6, dim, t, 2, post, True, dim)
+    i["y"] *= ymag
+    i["x"] *= xmag
+    i["y"][2] = 0
+    i["x"][2] = 0
+    i["y"][4] = 0
+    out = _forward(i, 0.7)
+    _forward_check(i, 0.7, out, t)
+    assert torch.isfinite(out[2]).all()
+    _backward_check(i, out[2], 0.7, _backward(i, out[2], 0.7), t)
+    i["dxo"] = None
+    _backward_check(i, out[2], 0.7, _backward(i, out[2], 0.7), t)
