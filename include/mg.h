@@ -521,11 +521,11 @@ mg_status mg_norm_residual_backward(int dtype, const void* dx_out, const void* d
  * state_bits 32: m and v are fp32 [count].  state_bits 8: m and v are bytes
  * [count], the e4m3 codes of m and of sqrt(v), and m_scales, v_scales fp32
  * [ceil(count / 256)] the power of two that every 256 of them are multiplied by:
- * the least that keeps their largest magnitude at or below 446.72.  Zeros are
+ * the least that keeps their largest finite magnitude at or below 446.72.  Zeros are
  * valid states.  Codes are rounded up or down at random with the probability of
  * the distance; the random bits depend on seed, step and the element's place in
  * the list alone, so that runs repeat bit for bit.  A moment that is not finite
- * becomes NaN.
+ * becomes NaN, and leaves its neighbours as they are.
  * param is fp32 or bf16 (rounded to nearest), grad fp32 or bf16, copy (NULL, or
  * bf16 [count]) receives the rounded new parameters.  Pointers are aligned to
  * their element.  Memory that is written may not overlap any other of the list.

@@ -329,6 +329,17 @@ __device__ __forceinline__ uint32_t block_top(const f32x2 (&f)[4]) {
   const float top = max_abs3(max_abs3(p.x, p.y, q.x), max_abs3(q.y, r.x, r.y), max_abs3(t.x, t.y, 0.0f));
   return __reduce_max_sync(0xffffffffu, __float_as_uint(top));
 }
+// The same over those that are finite: what is not becomes NaN under any scale, and takes no part in it.
+__device__ __forceinline__ uint32_t finite_top(const f32x2 (&f)[4]) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 x = parts(f[j]);
+    const uint32_t a = __float_as_uint(fabsf(x.x)), b = __float_as_uint(fabsf(x.y));
+    top = max(top, max(a < 0x7f800000u ? a : 0u, b < 0x7f800000u ? b : 0u));
+  }
+  return __reduce_max_sync(0xffffffffu, top);
+}
 // Square roots, rounded: an estimate and one step of Newton's method on it, whose
 // residual is exact.  For values that are normal numbers or 0 (of smaller ones the root
 // comes out too small).
@@ -417,9 +428,11 @@ __device__ __forceinline__ void adamw_finish(const AdamwStep& a, const AdamwScal
     store8<L>(k.v, false, i0, k.len, v);
   }
   const uint32_t tm = BITS == 8 ? block_top(m) : 0, tv = BITS == 8 ? block_top(v) : 0;
-  const float sm = scale_of(tm), sv = scale_of(__float_as_uint(sqrtf(__uint_as_float(tv))));
+  const bool finite = max(tm, tv) < 0x7f800000u;
+  const float sm = scale_of(finite ? tm : finite_top(m));
+  const float sv = scale_of(__float_as_uint(sqrtf(__uint_as_float(finite ? tv : finite_top(v)))));
   // (a root of a moment below the normal range is then far below eps, and its code the least)
-  if (BITS == 8 && sv >= 0x1p-30f && sv <= 0x1p60f && a.eps >= 1e-9f) {
+  if (BITS == 8 && finite && sv >= 0x1p-30f && sv <= 0x1p60f && a.eps >= 1e-9f) {
     roots8(v);
   } else {
 #pragma unroll

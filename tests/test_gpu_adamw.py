@@ -408,3 +408,39 @@ def test_tensor_past_2_31_elements():
     assert int((p != 0).sum()) == len(at)
     assert int((m[0].view(torch.uint8) != 0).sum()) == len(at)
     opt.close()
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf, 1e30])
+@pytest.mark.parametrize("pt,gt,shift", [("f32", "f32", 0), ("bf16", "bf16", 0), ("f32", "bf16", 1)])
+def test_8_bit_neighbours_of_a_moment_that_is_not_finite(pt, gt, shift, bad):
+    """A gradient that is not finite, or whose square is not, reaches its own element alone: all others have the codes,
+    scales and parameters that they have when its element is 0, step after step.  (A first moment that is large and finite
+    decides its block's scale, and with it its neighbours' first moments.)"""
+    own = ("v", "vs") if abs(bad) < math.inf else ("m", "v", "ms", "vs", "p")
+    sizes = [5 * B + 100, 7]
+    at = [(0, 3), (0, 2 * B + 255), (0, 5 * B + 99), (1, 6)]     # in whole blocks, and at the tensors' ends
+    d, w = _make8(sizes, 21, pt, gt, shift), _make8(sizes, 21, pt, gt, shift)
+    opts = [mg.AdamW(q["p"], q["g"], q["m"], q["v"], q["ms"], q["vs"], weight_decay=0.1, seed=4, **HYPER) for q in (d, w)]
+    others = [torch.ones(n, dtype=torch.bool, device="cuda") for n in sizes]
+    for i, j in at:
+        others[i][j] = False
+    for t in range(1, 5):
+        for i, g in enumerate(_make(sizes, 40 + t, pt, gt, shift)["g"]):
+            for q in (d, w):
+                q["g"][i].copy_(g)
+        for i, j in at:
+            d["g"][i][j] = bad if t == 1 else 0.5
+            w["g"][i][j] = 0.0
+        for o in opts:
+            o.step(1e-2, t)
+        for i in range(len(sizes)):
+            for k in own:
+                a, b = (q[k][i] if k in ("ms", "vs", "p") else q[k][i].view(torch.uint8) for q in (d, w))
+                keep = others[i] if k in ("m", "v", "p") else slice(None)
+                assert torch.equal(a[keep], b[keep])
+        for i, j in at:
+            assert int(d["v"][i].view(torch.uint8)[j]) & 0x7F == 0x7F
+            if not abs(bad) < math.inf:
+                assert int(d["m"][i].view(torch.uint8)[j]) & 0x7F == 0x7F
+    for o in opts:
+        o.close()
