@@ -462,7 +462,7 @@ mg_status mg_grad_list_clip(mg_grad_list* list, float max_norm, float* stats, mg
  * backward: dlogits[r, v] = (dlogp[r] ([v = ids[r]] - p_v)
  *                            - dentropy[r] p_v (log p_v + entropy[r])) / temperature
  * with p from stats; dlogits has the logits' type and may be the logits
- * themselves (same rows).  dlogp or dentropy may be NULL (no such gradient: ids,
+ * themselves (same rows), or lie in other columns of their buffer (same stride).  dlogp or dentropy may be NULL (no such gradient: ids,
  * entropy are then not needed).  Rows of padding, and rows whose dlogp and
  * dentropy are 0, are not read and get zeros.  Columns beyond vocab are neither
  * read nor written. */

@@ -688,6 +688,15 @@ static mg_status check_logits(const char* fn, int dtype, int id_kind, long long 
   return MG_OK;
 }
 
+// Whether the rows of two matrices of one stride and width lie beside one another: between their starts are whole
+// strides, and a rest that leaves room for one row and, up to the next stride, for the other.
+static bool rows_beside(const void* a, const void* b, int vocab, long long stride, int dtype) {
+  const size_t es = dtype ? 2 : 4, line = stride * es, wide = vocab * es;
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+  const size_t rest = (p < q ? q - p : p - q) % line;
+  return rest >= wide && line - rest >= wide;
+}
+
 // Bytes from the first element to the last one's end.
 static size_t rows_bytes(long long rows, int vocab, long long stride, int dtype) {
   return rows ? ((size_t)(rows - 1) * stride + vocab) * (dtype ? 2 : 4) : 0;
@@ -734,7 +743,8 @@ extern "C" mg_status mg_token_logprobs_backward(int dtype, const void* logits, l
   st = mg::op_begin(fn, {{logits, es}, {ids, id_kind ? 8u : 4u}, {stats, 8}, {entropy, 4}, {dlogp, 4}, {dentropy, 4}, {dlogits, es}});
   if (st != MG_OK) return st;
   const size_t n = (size_t)rows;
-  st = mg::op_disjoint(fn, {{logits, rows_bytes(rows, vocab, row_stride, dtype), false, false},
+  const bool beside = row_stride == dlogits_stride && rows_beside(logits, dlogits, vocab, row_stride, dtype);
+  st = mg::op_disjoint(fn, {{beside ? nullptr : logits, rows_bytes(rows, vocab, row_stride, dtype), false, false},
                             {ids, n * (id_kind ? 8 : 4), false, false}, {stats, n * 8, false, false},
                             {entropy, n * 4, false, false}, {dlogp, n * 4, false, false}, {dentropy, n * 4, false, false},
                             {dlogits, rows_bytes(rows, vocab, dlogits_stride, dtype), true,

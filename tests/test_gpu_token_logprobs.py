@@ -434,3 +434,28 @@ def test_rows_of_nan_alone(rows, vocab, t):
         assert (out[2] == 0).all() and torch.isfinite(out[rest]).all()
     mg.token_logprobs_backward(x, ids, o["stats"], one, x)          # in place
     assert torch.isnan(x[bad]).all() and torch.isfinite(x[rest]).all()
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+def test_logits_and_their_gradient_as_columns_of_one_buffer(t):
+    rows, v = 9, 1003
+    x = _logits(rows, v, t, 70)
+    ids = _ids(rows, v, 71, pad=True)
+    o = _forward(x, ids)
+    g = torch.ones(rows, device="cuda")
+    for first, second, stride in ((0, v, 2 * v), (v, 0, 2 * v), (5, v + 9, 2 * v + 40), (v + 9, 5, 2 * v + 40)):
+        buf = torch.full((rows, stride), 5.0, dtype=DT[t], device="cuda")
+        a, b = buf[:, first:first + v], buf[:, second:second + v]
+        a.copy_(x)
+        _gradient(a, ids, o, t, 1.0, out=b)
+        assert torch.equal(a, x)
+        rest = torch.ones(stride, dtype=torch.bool, device="cuda")
+        rest[first:first + v] = rest[second:second + v] = False
+        assert (buf[:, rest] == 5).all()
+    # columns that meet: by one, across the end of a row, and in rows of another width
+    buf = torch.zeros(rows + 2, 2 * v, dtype=DT[t], device="cuda")
+    flat = buf.view(-1)
+    for b in (buf[:rows, v - 1:2 * v - 1], flat[v + 1:v + 1 + rows * 2 * v].view(rows, 2 * v)[:, :v],
+              flat[v:v + rows * (2 * v - 1)].view(rows, 2 * v - 1)[:, :v]):
+        with pytest.raises(binding.MGError):
+            mg.token_logprobs_backward(buf[:rows, :v], ids, o["stats"], g, b)
