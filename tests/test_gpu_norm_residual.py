@@ -509,3 +509,21 @@ def test_magnitudes(ymag, xmag, eps, dim, post, t, monkeypatch):
     _backward_check(i, out[2], 0.7, _backward(i, out[2], 0.7), t)
     i["dxo"] = None
     _backward_check(i, out[2], 0.7, _backward(i, out[2], 0.7), t)
+
+
+# Wider than eight blocks hold: 220 KB of shared memory for two rows of two arrays (fp32: 112640), 512 threads of 32
+# elements (131072); the gradients' rows leave the blocks at half of it.
+@pytest.mark.parametrize("rows,dim,gates,t", [(3, 112648, 1, "f32"), (2, 131073, 2, "f32"), (2, 131080, 2, "bf16"),
+                                              (3, 131073, 1, "bf16"), (2, 200003, 0, "bf16")])
+@pytest.mark.parametrize("post,pre", [(True, True), (False, True), (True, False), (False, False)])
+def test_rows_wider_than_a_cluster(rows, dim, gates, t, post, pre):
+    i = _inputs(rows, dim, t, gates, post, pre, dim)
+    out = _forward(i, -0.7)
+    _forward_check(i, -0.7, out, t)
+    o = _backward(i, out[2], -0.7)
+    _backward_check(i, out[2], -0.7, o, t)
+    o2 = _backward(i, out[2], -0.7, inplace=True)
+    assert all(torch.equal(o[k], o2[k]) for k in o)
+    i = _inputs(rows, dim, t, gates, post, pre, dim)
+    xo, h, rstd = _forward(i, -0.7, inplace=True)
+    assert torch.equal(xo, out[0]) and torch.equal(rstd, out[2]) and (h is None or torch.equal(h, out[1]))
