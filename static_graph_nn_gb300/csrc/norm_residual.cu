@@ -298,15 +298,14 @@ __device__ __forceinline__ float inverse_root(float x) {
   return r > 0.0f ? fmaf(r, 0.5f * fmaf(-x * r, r, 1.0f), r) : r;   // (0 of infinity, NaN of NaN)
 }
 
-constexpr int kNrStages = 2;   // rows in shared memory, one of them in use: fewer where they are wide
-// All but the youngest n groups of copies are there.
-__device__ __forceinline__ void copies_wait(int n) {
-  if (n == 2)
-    asm volatile("cp.async.wait_group 2;" ::: "memory");
-  else if (n == 1)
-    asm volatile("cp.async.wait_group 1;" ::: "memory");
-  else
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
+// Rows in shared memory, one of them in use.  The kernels get the number as an argument: as a constant it made the aligned
+// backward slower, whose registers the compiler then fills with addresses (fp32, 256 wide: 94 us against 81, 4096: 82
+// against 75).
+constexpr int kNrStages = 2;
+// All but the youngest N groups of copies are there.
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 template <typename T, int U, bool OWN, int T0>
@@ -360,7 +359,7 @@ __global__ void __launch_bounds__(T0, T0 == 32 ? 24 : (U * Unit<T>::kPer == 8 ? 
     slot = slot + 1 == a.stages ? 0 : slot + 1;
     if (OWN) {
       ahead(r + a.stages - 1);
-      copies_wait(a.stages - 1);
+      copies_wait<kNrStages - 1>();
       in += threadIdx.x;
 #pragma unroll
       for (int j = 0; j < U; ++j) {
@@ -368,7 +367,7 @@ __global__ void __launch_bounds__(T0, T0 == 32 ? 24 : (U * Unit<T>::kPer == 8 ? 
         widen(in[array + j * blockDim.x], reinterpret_cast<f32x2(&)[pairs]>(x[j * pairs]));
       }
     } else {
-      copies_wait(a.stages - 2);
+      copies_wait<kNrStages - 2>();
       __syncthreads();             // row r is there, and the row before it has been read
       ahead(r + a.stages - 1);
       pairs_at<T, U, P>(in, at, 0, y);
@@ -532,10 +531,10 @@ __global__ void __launch_bounds__(T0, T0 == 32 ? 24 : (U * Unit<T>::kPer == 8 ? 
       slot = slot + 1 == a.stages ? 0 : slot + 1;
       if (OWN) {
         ahead(r + a.stages - 1);
-        copies_wait(a.stages - 1);
+        copies_wait<kNrStages - 1>();
         in += threadIdx.x;
       } else {
-        copies_wait(a.stages - 2);
+        copies_wait<kNrStages - 2>();
         __syncthreads();             // row r is there, and the row before it has been read
         ahead(r + a.stages - 1);
       }
@@ -780,7 +779,7 @@ struct NormResShape {
   int each = 0;      // elements a thread
   bool own = false;
   bool more = false;   // 640 threads on a multiprocessor instead of 512
-  int stages = 0, row_units = 0, ranks = 1, part = 0;
+  int row_units = 0, ranks = 1, part = 0;
   size_t smem = 0;
 };
 constexpr size_t kNrSmem = 220 * 1024;
@@ -820,12 +819,10 @@ NormResShape norm_res_shape(int dtype, int rows, int dim, bool grad) {
       }
       if (threads > most) continue;
       s.row_units = s.each * es * threads / 16 + (s.own ? 0 : 2);
-      const size_t row = (size_t)(grad ? 4 : 2) * s.row_units * 16;
-      s.stages = (int)std::min<size_t>(kNrStages, kNrSmem / row);
-      s.smem = s.stages * row;
-      if (s.stages < 2) continue;
+      s.smem = (size_t)kNrStages * (grad ? 4 : 2) * s.row_units * 16;
+      if (s.smem > kNrSmem) continue;
       s.threads = threads;
-    s.more = !grad && s.each == 16 && threads > (dtype ? 128 : 256) && 640 / threads > 512 / threads;
+      s.more = !grad && s.each == 16 && threads > (dtype ? 128 : 256) && 640 / threads > 512 / threads;
       return s;
     }
   }
@@ -960,7 +957,7 @@ extern "C" mg_status mg_norm_residual_forward(int dtype, const void* y, const vo
                             {h, n, true, h == y || h == x}, {rstd, (size_t)rows * 8, true, false}});
   if (st != MG_OK || !rows) return st;
   const mg::NormResShape shape = mg::norm_res_shape(dtype, rows, dim, false);
-  mg::NormResArgs a = {y, x, gamma_post, gate, gamma_pre, rows, dim, gates ? rows / gates : rows, scale, eps, x_out, h, rstd, 1, shape.stages, shape.row_units,
+  mg::NormResArgs a = {y, x, gamma_post, gate, gamma_pre, rows, dim, gates ? rows / gates : rows, scale, eps, x_out, h, rstd, 1, mg::kNrStages, shape.row_units,
                        shape.ranks, shape.part};
   cudaStream_t s = (cudaStream_t)stream;
   cudaError_t e;
@@ -1032,7 +1029,7 @@ extern "C" mg_status mg_norm_residual_backward(int dtype, const void* dx_out, co
   cudaError_t e = shape.ranks > 1 ? go(most, &active) : cudaSuccess;
   if (e != cudaSuccess) return mg::op_end(fn, e);
   const mg::NormResSplit split = mg::norm_res_split(rows, a.gates, mg::norm_res_clusters(most, active));
-  a.stages = shape.stages;
+  a.stages = mg::kNrStages;
   a.row_units = shape.row_units;
   a.ranks = shape.ranks;
   a.part = shape.part;
@@ -1045,8 +1042,7 @@ extern "C" mg_status mg_norm_residual_backward(int dtype, const void* dx_out, co
   else
     e = go(split.blocks, nullptr);
   const int gate_blocks = dgate && a.parts > 1 && a.gates > 1 ? std::min(a.gates, 65533) : 0;
-  if (e == cudaSuccess && (dgamma_post || dgamma_pre || (dgate && a.parts > 1)))
-  {
+  if (e == cudaSuccess && (dgamma_post || dgamma_pre || (dgate && a.parts > 1))) {
     // (many blocks: narrow rows; eight columns of a sector each, and four times the runs)
     const int wide = split.blocks > 1024 ? 8 : 32;
     const unsigned threads = 32 * (unsigned)std::max(4ll, std::min(32ll, split.blocks / 12));
