@@ -448,10 +448,11 @@ __device__ __forceinline__ void span_sums(const NormResGradArgs& a, int block, c
   *keep = first ? P : *keep + P;
 }
 
-// The three sums of a row in one exchange.  With b = w y (w = gate g1) and q = dx' + r2 dh g2: n1 = r2 mean(dh g2 x'), and
-// sum w t y = sum b q - n1 r2^2 sum b x'.  The gradients are computed from x^ = x' r2 and y^ = y r1, which are near 1
-// whatever the rows' magnitude: t = dx' + r2 (dh g2 - x^ n1), dy = r1 (w t - y^ r1 mean(w t y)).  (The cube of r1 or r2
-// leaves fp32's range where rows are 1e13 or 1e-13, and where they are 0 under an eps below 1e-25.)
+// The three sums of a row in one exchange.  With b = w y (w = gate g1) and q = dx' + r2 dh g2: m1 = r2 mean(dh g2 x') and
+// sum w t y = sum b q - m1 r2^2 sum b x'.  With m2 = r1 mean(w t y), t = dx' + r2 (dh g2 - r2 m1 x') and dy = r1 (w t -
+// r1 m2 y): r1 y, r2 x', m1 and m2 stay near the gradients' and vectors' size whatever the rows' magnitude, and no power
+// of a root is formed.  (The cube of one leaves fp32's range where rows are 1e13 or 1e-13, and where they are 0 under an eps
+// below 1e-25.)
 template <typename T, int U, bool OWN, int T0>
 __global__ void __launch_bounds__(T0, T0 == 32 ? 24 : (U * Unit<T>::kPer == 8 ? 768 : 512) / T0) norm_res_grad_kernel(NormResGradArgs a) {
   constexpr int per = Unit<T>::kPer, pairs = Unit<T>::kPairs, E = U * per, P = E / 2;
@@ -575,7 +576,7 @@ __global__ void __launch_bounds__(T0, T0 == 32 ? 24 : (U * Unit<T>::kPer == 8 ? 
       row_sums<3>(sum, red, turn, my.rank, a.ranks);
       const float m1 = hs ? r2 * (sum[0] * inv_dim) : 0.0f;
       const float m2 = a.g1 ? r1 * ((hs ? fmaf(-m1, r2 * (r2 * sum[2]), sum[1]) : sum[1]) * inv_dim) : 0.0f;
-      const f32x2 n1 = both(-m1), n2 = both(-m2);
+      const f32x2 n1 = both(-r2 * m1), n2 = both(-r1 * m2);
 #pragma unroll
       for (int j = 0; j < U; ++j) {
         f32x2 y[pairs], x[pairs], o[pairs], h[pairs];
@@ -583,12 +584,12 @@ __global__ void __launch_bounds__(T0, T0 == 32 ? 24 : (U * Unit<T>::kPer == 8 ? 
 #pragma unroll
         for (int i = 0; i < pairs; ++i) {
           const int p = j * pairs + i;
-          const f32x2 wp = w[p], xh = mul2(rr2, fma2(rr1, mul2(wp, y[i]), mul2(scale, x[i]))), yh = mul2(y[i], rr1);
-          const f32x2 t = fma2(rr2, fma2(n1, xh, mul2(h[i], g2[p])), o[i]);
-          sp[p] = fma2(t, yh, sp[p]);
-          s2[p] = fma2(h[i], xh, s2[p]);
+          const f32x2 wp = w[p], xo = fma2(rr1, mul2(wp, y[i]), mul2(scale, x[i]));
+          const f32x2 t = fma2(rr2, fma2(n1, xo, mul2(h[i], g2[p])), o[i]);
+          sp[p] = fma2(t, mul2(y[i], rr1), sp[p]);
+          s2[p] = fma2(mul2(h[i], rr2), xo, s2[p]);
           x[i] = mul2(scale, t);
-          y[i] = mul2(rr1, fma2(n2, yh, mul2(wp, t)));
+          y[i] = mul2(rr1, fma2(n2, y[i], mul2(wp, t)));
         }
         if (OWN) {
           const int c = column<T, OWN, U>(j * per);
