@@ -462,10 +462,11 @@ mg_status mg_grad_list_clip(mg_grad_list* list, float max_norm, float* stats, mg
  * backward: dlogits[r, v] = (dlogp[r] ([v = ids[r]] - p_v)
  *                            - dentropy[r] p_v (log p_v + entropy[r])) / temperature
  * with p from stats; dlogits has the logits' type and may be the logits
- * themselves (same rows), or lie in other columns of their buffer (same stride).  dlogp or dentropy may be NULL (no such gradient: ids,
- * entropy are then not needed).  Rows of padding, and rows whose dlogp and
- * dentropy are 0, are not read and get zeros.  Columns beyond vocab are neither
- * read nor written. */
+ * themselves (same rows), or lie in other columns of their buffer (same stride).
+ * dlogp or dentropy may be NULL (no such gradient; entropy is not needed without
+ * dentropy, ids without dlogp, unless there is padding).  Rows of padding, and rows
+ * whose dlogp and dentropy are 0, are not read and get zeros.  Columns beyond vocab are
+ * neither read nor written. */
 #define MG_MAX_TOP 32
 mg_status mg_token_logprobs(int dtype, const void* logits, long long rows, int vocab,
                             long long row_stride, int id_kind, const void* ids, float temperature,
@@ -490,6 +491,8 @@ mg_status mg_token_logprobs_backward(int dtype, const void* logits, long long ro
  * are fp32: finite within +-1e19 / sqrt(dim) (backward: those of gate gamma_post y x_out
  * too).
  * x_out and h may each be y or x itself.
+ *
+ * All pointers are 16-byte aligned, the vectors' too.
  *
  * backward, from dx_out and dh (either may be NULL, for none) and the forward's
  * inputs: dy, dx, and, where not NULL, dgamma_post, dgamma_pre [dim] and dgate
@@ -529,9 +532,9 @@ mg_status mg_norm_residual_backward(int dtype, const void* dx_out, const void* d
  * param is fp32 or bf16 (rounded to nearest), grad fp32 or bf16, copy (NULL, or
  * bf16 [count]) receives the rounded new parameters.  Pointers are aligned to
  * their element.  Memory that is written may not overlap any other of the list.
- * Creation copies the table to the device (88 bytes per 8192 elements, per 2048 of short
- * lists) and is
- * bound to the current device; the list keeps no state of its own.
+ * Creation copies the table to the device (80 bytes per 8192 elements, per 2048 of short
+ * lists) and is bound to the current device; the list keeps no state of its own, but a captured step
+ * reads the table and needs the list alive.
  * lr_device, step_device (device memory, fp32 and int32; NULL: lr and step are
  * taken) are read by the kernel, so that a captured step can be replayed with
  * new values; a step_device below 1 counts as 1.  Neither they nor norm may lie in

@@ -7,8 +7,8 @@
 //
 // Moments in 8 bits: m and sqrt(v) are e4m3 codes under one scale for each 256
 // elements of a tensor.  A scale is the least power of two that keeps the
-// block's largest magnitude at or below 446.7: e4m3 keeps the same three bits
-// of mantissa under any scale, and a power of two leaves a value that does not
+// block's largest finite magnitude at or below 446.7 (what is not finite becomes
+// NaN under any scale): e4m3 keeps the same three bits of mantissa under any scale, and a power of two leaves a value that does not
 // change on its code, where a scale that follows the maximum would move all
 // values of the block against their codes in every step.  The border lies just
 // inside e4m3's 448, at a number that sums of short numbers do not hit, so that
@@ -27,7 +27,10 @@
 // Bound by DRAM: 28 bytes an fp32 element, 16 with 8-bit moments, 2 more for a bf16 copy.
 // 334M elements with a copy: 1435 us (7.0 TB/s), with 8-bit moments 861 us (7.0 TB/s).
 // With bf16 parameters and gradients, 10 bytes, by issue: 65 instructions an element (24M
-// in 400 tensors: 57 us, 4.2 TB/s); most arithmetic is done on two elements at once.
+// in 400 tensors: 57 us, 4.2 TB/s), about 45 of them the arithmetic of moments, roots and
+// codes (random bits about 5); most of it is done on two elements at once.  Tensors at any
+// address, one element an access: 100M fp32 in 429 us (aligned 404), with 8-bit moments 441
+// (234), bf16 with 8-bit moments 691 (203).
 // Blocks of 8-bit moments are copied ahead through shared memory: a warp's loads
 // are under way while it computes (861 us against 1201).  In them a lane takes
 // twice four neighbours, so that every access of a warp is contiguous; eight
@@ -68,6 +71,7 @@ struct AdamwChunk {
   int flags;                  // bit 0: p bf16, bit 1: g bf16, bit 2: eight elements of each allow one access
   float wd;
 };
+static_assert(sizeof(AdamwChunk) == 80, "the header states the table's bytes");
 
 struct AdamwStep {
   const AdamwChunk* chunks;

@@ -5,8 +5,8 @@
 //   x' = s x + a u                                      (a: one gate for all rows, or one for each run of rows)
 //   h = x' r2 g2, r2 = 1 / sqrt(mean(x'^2) + eps)
 // Backward, from the gradients dx' and dh:
-//   t = dx' + r2 (dh g2) - x' r2^3 mean(dh g2 x')       dx = s t
-//   w = a t,  dy = r1 (w g1) - y r1^3 mean(w g1 y)
+//   t = dx' + r2 (dh g2 - r2 x' mean(dh g2 r2 x'))      dx = s t
+//   w = a t,  dy = r1 (w g1 - r1 y mean(w g1 r1 y))
 //   dg2 = sum dh x' r2,  dg1 = sum w y r1,  da = sum t u (over the gate's rows)
 //
 // Bound by DRAM: four row vectors a row forward, six backward.  A block (a warp for
@@ -22,7 +22,8 @@
 // blocks of 128 threads on a multiprocessor x rows in shared memory: 4 x 2 46.2 us,
 // 3 x 2 49.6, 6 x 2 50.3, 4 x 3 49.6, 5 x 3 51.5; backward 4 x 2 78.7, 3 x 2 80.4, 3 x 3 81.9,
 // 4 x 3 84.4), and holding x' and q in registers between the sums and the
-// gradients, which leaves three blocks, is no faster (75 against 73).
+// gradients, which leaves three blocks, is no faster (in a loop of the backward alone 75
+// against 73).
 #include <algorithm>
 #include <cmath>
 
@@ -84,7 +85,7 @@ struct NormResGradArgs {
 // start.  Else all threads copy the 16-byte units that a row touches, with zeros for the
 // bytes behind it, and after a barrier a thread takes words of four bytes, a warp's
 // width apart.  bf16 rows that begin within a word have theirs shifted out of two, and
-// stored with the lane before's half.  (14124 x 2124 bf16: forward 61 us, backward 113; by
+// stored with the lane before's half.  (14124 x 2124 bf16: forward 56 us, backward 112; by
 // single elements 92 and 196; by units of 16 bytes, shifted out of two, 2.4 times the
 // aligned rows' instructions and 193.)  The arithmetic takes two elements at a time.
 template <typename T>
