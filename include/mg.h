@@ -497,7 +497,8 @@ mg_status mg_token_logprobs_backward(int dtype, const void* logits, long long ro
  * backward, from dx_out and dh (either may be NULL, for none) and the forward's
  * inputs: dy, dx, and, where not NULL, dgamma_post, dgamma_pre [dim] and dgate
  * [gates, dim], fp32 sums in a fixed order (the same bits in every run).  dy and
- * dx may each be dx_out, dh, y or x itself.  workspace:
+ * dx may each be dx_out, dh, y or x itself.  Where y or x is not finite, that
+ * element's dy and dx may be NaN without a norm too.  workspace:
  * mg_norm_residual_workspace_bytes (for these rows or fewer, of either type; 0 for
  * arguments the call would refuse); its contents before the call do not matter. */
 size_t mg_norm_residual_workspace_bytes(int rows, int dim, int gates);
@@ -533,8 +534,8 @@ mg_status mg_norm_residual_backward(int dtype, const void* dx_out, const void* d
  * bf16 [count]) receives the rounded new parameters.  Pointers are aligned to
  * their element.  Memory that is written may not overlap any other of the list.
  * Creation copies the table to the device (80 bytes per 8192 elements, per 2048 of short
- * lists) and is bound to the current device; the list keeps no state of its own, but a captured step
- * reads the table and needs the list alive.
+ * lists) and is bound to the current device; the list keeps no state of its own, but
+ * a captured step reads the table and needs the list alive.
  * lr_device, step_device (device memory, fp32 and int32; NULL: lr and step are
  * taken) are read by the kernel, so that a captured step can be replayed with
  * new values; a step_device below 1 counts as 1.  Neither they nor norm may lie in

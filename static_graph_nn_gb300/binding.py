@@ -659,7 +659,8 @@ def token_logprobs_backward(logits, ids, stats, dlogp, dlogits, entropy=None, de
     """dlogits from dlogp and dentropy (either may be None; dentropy needs the
     forward's entropy), with the forward's stats and temperature.  dlogits has the
     logits' shape and type, a row stride of its own, and may be the logits
-    themselves or other columns of one buffer with them.  Rows of padding, and rows without a gradient, get zeros."""
+    themselves or other columns of one buffer with them.  Rows of padding, and rows
+    without a gradient, get zeros."""
     rows, v, ld = _logit_rows(logits, "logits")
     lead = logits.shape[:-1]
     if dlogits.shape != logits.shape:

@@ -8,9 +8,10 @@
 // Moments in 8 bits: m and sqrt(v) are e4m3 codes under one scale for each 256
 // elements of a tensor.  A scale is the least power of two that keeps the
 // block's largest finite magnitude at or below 446.7 (what is not finite becomes
-// NaN under any scale): e4m3 keeps the same three bits of mantissa under any scale, and a power of two leaves a value that does not
-// change on its code, where a scale that follows the maximum would move all
-// values of the block against their codes in every step.  The border lies just
+// NaN under any scale): e4m3 keeps the same three bits of mantissa under any
+// scale, and a power of two leaves a value that does not change on its code,
+// where a scale that follows the maximum would move all values of the block
+// against their codes in every step.  The border lies just
 // inside e4m3's 448, at a number that sums of short numbers do not hit, so that
 // no rounding decides a scale.
 // A code is rounded up or down at random with the probability of its distance:
